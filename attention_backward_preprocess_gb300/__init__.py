@@ -29,7 +29,7 @@ EXPORTED = [
     "fa_device_status", "fa_set_wait_timeout_ns", "fa_status_string",
     "fa_selftest_umma", "fa_selftest_semaphore", "fa_selftest_tmem_layout", "fa_bwd_noalloc",
     "fa_bwd_noalloc_scratch_bytes", "fa_fwd_ext", "fa_bwd_ext", "fa_bwd_stages_ext", "fa_bwd_workspace_sync_layout",
-    "fa_bwd_noalloc_status",
+    "fa_bwd_noalloc_status", "fa_mask_ranges", "fa_mask_ranges_bytes",
 ]
 
 
@@ -59,7 +59,9 @@ class FaExt(ctypes.Structure):
                 ("dbias", ctypes.c_void_p), ("dropout_p", ctypes.c_float),
                 ("dropout_seed", ctypes.c_ulonglong), ("dropout_offset", ctypes.c_uint),
                 ("dropout_mask", ctypes.c_void_p), ("total_q", ctypes.c_longlong),
-                ("total_k", ctypes.c_longlong), ("head_dim_v", ctypes.c_int)]
+                ("total_k", ctypes.c_longlong), ("head_dim_v", ctypes.c_int),
+                ("softcap", ctypes.c_float), ("mask_ranges", ctypes.c_void_p),
+                ("mask_ranges_bytes", ctypes.c_size_t)]
 
 
 def dropout_mask_shape(q, k, cu_seqlens_q=None, max_seqlen_k=None):
@@ -73,7 +75,8 @@ def dropout_mask_shape(q, k, cu_seqlens_q=None, max_seqlen_k=None):
 
 
 def _ext(Hq, window=None, alibi_slopes=None, seqused_q=None, seqused_k=None, bias=None,
-         dbias=None, dropout=None, totals=None, head_dim_v=0):
+         dbias=None, dropout=None, totals=None, head_dim_v=0, softcap=0.0, mask_ranges=None,
+         sizes=None):
     """A pointer to an FaExt, or None when no extension is asked for.
 
     ``bias``: [B or 1, Hq or 1, Sq, >= Sk] in the input dtype, last axis
@@ -84,12 +87,19 @@ def _ext(Hq, window=None, alibi_slopes=None, seqused_q=None, seqused_k=None, bia
     flags and fa_bwd reads back; see fa_ext in include/fa.h.  ``totals``:
     (total_q, total_k), the packed row counts of a varlen call (cu_seqlens[B]),
     so that the library need not read them back (no stream synchronisation).
-    ``head_dim_v``: the value head dim when it differs from q's (else 0)."""
+    ``head_dim_v``: the value head dim when it differs from q's (else 0).
+    ``softcap``: scores become softcap * tanh(score / softcap) (0: none).
+    ``mask_ranges``: a MaskRanges of the call's ``sizes`` (B, Sq, Sk)."""
     if (window is None and alibi_slopes is None and seqused_q is None and seqused_k is None
             and bias is None and dbias is None and dropout is None and totals is None
-            and not head_dim_v):
+            and not head_dim_v and softcap == 0.0 and mask_ranges is None):
         return None
     e = FaExt(-1, -1, None, 0, None, None, None, 0, 0, 0, None, 0.0, 0, 0, None, 0, 0, 0)
+    e.softcap = float(softcap)
+    if mask_ranges is not None:
+        if not isinstance(mask_ranges, MaskRanges) or sizes != (mask_ranges.B, mask_ranges.S, mask_ranges.S):
+            raise ValueError("mask_ranges: what mask_ranges(B, S, ...) returned, for this call's B and S = Sq = Sk")
+        e.mask_ranges, e.mask_ranges_bytes = mask_ranges.buffer.data_ptr(), mask_ranges.buffer.numel()
     e.head_dim_v = int(head_dim_v)
     if totals is not None:
         e.total_q, e.total_k = int(totals[0]), int(totals[1])
@@ -125,6 +135,60 @@ def _ext(Hq, window=None, alibi_slopes=None, seqused_q=None, seqused_k=None, bia
             raise ValueError("dbias: a contiguous [B, Hq, Sq, Sk] tensor")
         e.dbias = dbias.data_ptr()
     return ctypes.pointer(e)
+
+
+def _same_device(device, t, name):
+    """Raises unless ``t`` is on ``device`` (None, or one without an index: any CUDA device)."""
+    d = None if device is None else torch.device(device)
+    if not t.is_cuda or (d is not None and (d.type != "cuda" or d.index not in (None, t.device.index))):
+        raise ValueError(name + ": on another device")
+
+
+class MaskRanges:
+    """Visible-key intervals of a batch (``mask_ranges``): ``buffer``, a uint8
+    CUDA tensor, for ``B`` sequences of ``S`` tokens."""
+
+    def __init__(self, buffer, B, S):
+        self.buffer, self.B, self.S = buffer, B, S
+
+
+def mask_ranges(B, S, doc_ids=None, prefix_len=None, causal=True, window=None, device=None, out=None,
+                stream=None):
+    """Visible keys of every query row of a dense self-attention batch, for the
+    ``mask_ranges`` keyword of fa_fwd and fa_bwd (see fa_mask_ranges in
+    include/fa.h); built once per batch, read by every layer.
+
+    ``doc_ids``: int32 [B, S], documents are runs of equal ids, a negative id
+    is padding.  ``prefix_len``: int32 [B] (one prefix length for every
+    document of a sequence) or [B, S] (read at a document's first token): the
+    leading tokens every row of the document sees; with ``causal`` and without
+    a window only.  ``window=(left, right)``, -1 = unbounded.  ``out``: a
+    MaskRanges of the same B and S to fill again (a captured graph's)."""
+    B, S = int(B), int(S)
+    for name, t in (("doc_ids", doc_ids), ("prefix_len", prefix_len)):
+        if t is not None:
+            if t.dtype != torch.int32 or not t.is_contiguous() or not t.is_cuda:
+                raise ValueError(name + ": a contiguous int32 CUDA tensor")
+            if tuple(t.shape) != (B, S) and not (name == "prefix_len" and tuple(t.shape) == (B,)):
+                raise ValueError(name + ": [B, S]" + (" or [B]" if name == "prefix_len" else ""))
+            _same_device(device, t, name)
+            device = t.device
+    if out is not None:
+        if not isinstance(out, MaskRanges) or (out.B, out.S) != (B, S):
+            raise ValueError("out: a MaskRanges of the same B and S")
+        _same_device(device, out.buffer, "out")
+        device = out.buffer.device
+    wl, wr = (-1, -1) if window is None else (int(window[0]), int(window[1]))
+    need = int(lib().fa_mask_ranges_bytes(B, S))
+    if need == 0:
+        raise FaError(FA_ERR_INVALID_ARG, "fa_mask_ranges")
+    with torch.cuda.device(device):   # None: the current device
+        if out is None:
+            out = MaskRanges(torch.empty(need, dtype=torch.uint8, device="cuda"), B, S)
+        per_token = prefix_len is not None and prefix_len.dim() == 2
+        _check(lib().fa_mask_ranges(_ptr(doc_ids), _ptr(prefix_len), int(per_token), B, S, int(bool(causal)), wl,
+                                    wr, _ptr(out.buffer), out.buffer.numel(), _stream(stream)), "fa_mask_ranges")
+    return out
 
 
 def lib():
@@ -167,12 +231,15 @@ def lib():
         L.fa_bwd_noalloc_status.restype = _i
         L.fa_bwd_workspace_sync_layout.argtypes = _SHAPE + [_i, _i] + [ctypes.POINTER(_sz)] * 3
         L.fa_bwd_workspace_sync_layout.restype = _i
+        L.fa_mask_ranges_bytes.argtypes = [_i, _i]
+        L.fa_mask_ranges_bytes.restype = _sz
+        L.fa_mask_ranges.argtypes = [_vp, _vp] + [_i] * 6 + [_vp, _sz, _vp]
         L.fa_selftest_umma.argtypes = [_i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]
         L.fa_selftest_semaphore.argtypes = [_vp, _i, ctypes.c_longlong, _vp, _vp]
         L.fa_selftest_tmem_layout.argtypes = [_i, _vp, _vp]
         for name in ("fa_bwd", "fa_bwd_with_workspace", "fa_bwd_preprocess", "fa_bwd_main",
                      "fa_bwd_postprocess", "fa_bwd_workspace_layout", "fa_fwd", "fa_fwd_ext",
-                     "fa_bwd_ext",
+                     "fa_bwd_ext", "fa_mask_ranges",
                      "fa_device_status", "fa_selftest_umma", "fa_selftest_semaphore",
                      "fa_selftest_tmem_layout"):
             getattr(L, name).restype = _i
@@ -225,13 +292,34 @@ def _value_dim(D, v) -> int:
     return 0 if v.shape[-1] == D else int(v.shape[-1])
 
 
+def _dense(stream, **tensors):
+    """The named tensors, each contiguous: the library reads them as they lie.
+    One that is not is copied on the current stream; with another ``stream``
+    the copy and the call would not be in order, so that is refused."""
+    out = []
+    for name, t in tensors.items():
+        if not t.is_contiguous():
+            if stream is not None:
+                raise ValueError(name + ": must be contiguous when a stream is given")
+            t = t.contiguous()
+        out.append(t)
+    return out
+
+
+def _outputs(**tensors):
+    for name, t in tensors.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError(name + ": a contiguous output tensor")
+
+
 def default_scale(D: int) -> float:
     return 1.0 / (D ** 0.5)
 
 
 def fa_fwd(q, k, v, causal=False, softmax_scale=None, cu_seqlens_q=None, cu_seqlens_k=None,
            max_seqlen_q=None, max_seqlen_k=None, stream=None, window=None, alibi_slopes=None,
-           seqused_q=None, seqused_k=None, bias=None, dropout=None, totals=None):
+           seqused_q=None, seqused_k=None, bias=None, dropout=None, totals=None, softcap=0.0,
+           mask_ranges=None):
     """Forward pass: returns (o, lse); lse fp32 [B,Hq,Sq] or [Hq,total_q].
 
     ``window=(left, right)`` (-1 = unbounded side), ``alibi_slopes`` (fp32
@@ -239,8 +327,11 @@ def fa_fwd(q, k, v, causal=False, softmax_scale=None, cu_seqlens_q=None, cu_seql
     (see ``_ext``) and ``dropout=(p, seed, offset)`` select fa_fwd_ext; rows
     past the used lengths are left as allocated.  ``totals=(total_q, total_k)``
     (varlen: cu_seqlens_q[B], cu_seqlens_k[B]) spares the read-back of the
-    packed totals, so the call does not synchronise the stream.
+    packed totals, so the call does not synchronise the stream.  ``softcap``
+    caps the scores, softcap * tanh(score / softcap); ``mask_ranges`` (from the
+    function of that name) takes the place of ``causal`` and ``window``.
     """
+    q, k, v = _dense(stream, q=q, k=k, v=v)
     B, Sq, Sk, Hq, Hkv, D = _shape(q, k, cu_seqlens_q, max_seqlen_q, max_seqlen_k)
     scale = default_scale(D) if softmax_scale is None else float(softmax_scale)
     o = torch.empty(q.shape[:-1] + (v.shape[-1],), dtype=q.dtype, device=q.device)
@@ -249,7 +340,8 @@ def fa_fwd(q, k, v, causal=False, softmax_scale=None, cu_seqlens_q=None, cu_seql
     else:
         lse = torch.empty((Hq, q.shape[0]), dtype=torch.float32, device=q.device)
     ext = _ext(Hq, window, alibi_slopes, seqused_q, seqused_k, bias, dropout=dropout,
-               totals=totals, head_dim_v=_value_dim(D, v))
+               totals=totals, head_dim_v=_value_dim(D, v), softcap=softcap, mask_ranges=mask_ranges,
+               sizes=(B, Sq, Sk))
     args = [_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Sq, Sk, Hq, Hkv, D, scale,
             int(bool(causal)), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k)]
     if ext is None:
@@ -263,7 +355,7 @@ def fa_bwd(q, k, v, o, dout, lse, causal=False, softmax_scale=None, cu_seqlens_q
            cu_seqlens_k=None, max_seqlen_q=None, max_seqlen_k=None, deterministic=False,
            dq=None, dk=None, dv=None, workspace=None, stream=None, window=None,
            alibi_slopes=None, seqused_q=None, seqused_k=None, bias=None, dbias=None,
-           dropout=None, totals=None):
+           dropout=None, totals=None, softcap=0.0, mask_ranges=None):
     """Backward pass through the C ABI; returns (dq, dk, dv).
 
     Outputs are allocated when not given.  ``workspace`` (a uint8 CUDA tensor
@@ -272,8 +364,10 @@ def fa_bwd(q, k, v, o, dout, lse, causal=False, softmax_scale=None, cu_seqlens_q
     (as for fa_fwd, plus ``dbias``, an output tensor filled with dBias = dS)
     select fa_bwd_ext, and so does ``totals=(total_q, total_k)`` (varlen: the
     packed row counts, which spare the stream synchronisation of reading them
-    back).
+    back).  ``softcap`` and ``mask_ranges`` as the forward had them.
     """
+    q, k, v, o, dout, lse = _dense(stream, q=q, k=k, v=v, o=o, dout=dout, lse=lse)
+    _outputs(dq=dq, dk=dk, dv=dv)
     B, Sq, Sk, Hq, Hkv, D = _shape(q, k, cu_seqlens_q, max_seqlen_q, max_seqlen_k)
     scale = default_scale(D) if softmax_scale is None else float(softmax_scale)
     dq = torch.empty_like(q) if dq is None else dq
@@ -283,7 +377,7 @@ def fa_bwd(q, k, v, o, dout, lse, causal=False, softmax_scale=None, cu_seqlens_q
             _ptr(dv), B, Sq, Sk, Hq, Hkv, D, scale, int(bool(causal)), _ptr(cu_seqlens_q),
             _ptr(cu_seqlens_k), int(bool(deterministic)), _dtype_code(q)]
     ext = _ext(Hq, window, alibi_slopes, seqused_q, seqused_k, bias, dbias, dropout, totals,
-               _value_dim(D, v))
+               _value_dim(D, v), softcap, mask_ranges, (B, Sq, Sk))
     if ext is not None:
         st = lib().fa_bwd_ext(*args[:19], ext, *args[19:], _ptr(workspace),
                               0 if workspace is None else workspace.numel(), _stream(stream))
@@ -352,21 +446,24 @@ def workspace_layout(B, Sq, Sk, Hq, Hkv, D, varlen=False, deterministic=False) -
 def fa_bwd_stages(q, k, v, o, dout, lse, workspace, causal=False, softmax_scale=None,
                   cu_seqlens_q=None, cu_seqlens_k=None, max_seqlen_q=None, max_seqlen_k=None,
                   deterministic=False, dq=None, dk=None, dv=None, stages=("pre", "main", "post"),
-                  stream=None, totals=None):
+                  stream=None, totals=None, window=None, softcap=0.0, mask_ranges=None):
     """Runs the chosen stages (preprocess / main / postprocess) on ``workspace``.
 
     ``totals=(total_q, total_k)`` (varlen) goes through fa_bwd_stages_ext with
-    the packed row counts, so that no stage synchronises the stream."""
+    the packed row counts, so that no stage synchronises the stream; so do
+    ``window``, ``softcap`` and ``mask_ranges`` (as for fa_bwd).  Stages in
+    separate calls share no copies, so every tensor must be contiguous."""
+    _outputs(q=q, k=k, v=v, o=o, dout=dout, lse=lse, dq=dq, dk=dk, dv=dv)
     B, Sq, Sk, Hq, Hkv, D = _shape(q, k, cu_seqlens_q, max_seqlen_q, max_seqlen_k)
     scale = default_scale(D) if softmax_scale is None else float(softmax_scale)
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
     shape = [B, Sq, Sk, Hq, Hkv, D]
-    if totals is not None:
+    ext = _ext(Hq, window, totals=totals, softcap=softcap, mask_ranges=mask_ranges, sizes=(B, Sq, Sk))
+    if ext is not None:
         mask = ((1 if "pre" in stages else 0) | (2 if "main" in stages else 0) |
                 (4 if "post" in stages else 0))
-        ext = _ext(Hq, totals=totals)
         _check(lib().fa_bwd_stages_ext(mask, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout),
                                        _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), *shape, scale,
                                        int(bool(causal)), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),

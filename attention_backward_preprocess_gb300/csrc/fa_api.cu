@@ -13,6 +13,7 @@
 
 #include "../../include/fa.h"
 #include "fa_params.h"
+#include "fa_ranges.h"
 
 namespace fa {
 cudaError_t launch_schedule(const BwdParams &p, cudaStream_t stream);
@@ -41,6 +42,11 @@ namespace {
 std::atomic<long long> g_budget_ns{2000000000LL};
 
 constexpr float kLog2e = 1.4426950408889634f;
+
+// Bounds of a soft cap.  The capped score's error is absolute, about softcap *
+// 2^-21 (fa_device.cuh): at 1000 that is the size of fp16's rounding of P.
+// Below 1 / 1000 every score is the same to the softmax.
+constexpr float kMinSoftcap = 1e-3f, kMaxSoftcap = 1000.f;
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -329,6 +335,30 @@ fa_status apply_ext(fa::BwdParams &p, int causal, const fa_ext *ext) {
             p.drop_mask = ext->dropout_mask;
             p.drop_mask_w = (p.Sk + 31) / 32;
         }
+    }
+    p.cap_log2 = p.cap_k = 0.f;
+    p.mr_row = nullptr;
+    if (ext && (ext->softcap != 0.f || ext->mask_ranges)) {
+        // the capped and interval instances carry no other score extension
+        if (ext->softcap != 0.f) {
+            if (!(ext->softcap >= kMinSoftcap && ext->softcap <= kMaxSoftcap)) return FA_ERR_INVALID_ARG;
+            p.cap_log2 = ext->softcap * kLog2e;
+            p.cap_k = 2.f * p.scale_log2 / ext->softcap;
+            if (!std::isfinite(p.cap_k)) return FA_ERR_INVALID_ARG;
+        }
+        if (ext->mask_ranges) {
+            if (p.varlen) return FA_ERR_UNSUPPORTED;
+            if (p.Sq != p.Sk || causal || wl != -1 || wr != -1) return FA_ERR_INVALID_ARG;
+            if (reinterpret_cast<uintptr_t>(ext->mask_ranges) & 255u) return FA_ERR_INVALID_ARG;
+            const fa::RangeTables t = fa::range_tables(const_cast<void *>(ext->mask_ranges), p.B, p.Sq);
+            if (ext->mask_ranges_bytes < t.bytes) return FA_ERR_INVALID_ARG;
+            p.mr_row = t.row;
+            p.mr_block = t.block;
+            p.mr_key = t.key;
+            p.mr_first = t.first;
+            p.mr_rows = t.rows;
+        }
+        if (p.alibi || p.bias || p.dbias || p.drop_t > 0 || wide_dims(p.Dh, p.Dhv)) return FA_ERR_UNSUPPORTED;
     }
     p.win_lo = (wl < 0 || wl >= fa::kNoWindow) ? fa::kNoWindow : wl;
     p.win_hi = (wr < 0 || wr >= fa::kNoWindow) ? fa::kNoWindow : wr;
@@ -686,6 +716,32 @@ fa_status fa_device_status(void *workspace, cudaStream_t stream) {
     }
     fa_status st2 = read_error_word(reinterpret_cast<int *>(ws), stream, true);
     return st2 != FA_OK ? st2 : st;
+}
+
+size_t fa_mask_ranges_bytes(int B, int S) {
+    if (B <= 0 || S <= 0 || (long long)B * S > (1LL << 31) - 1) return 0;
+    return fa::range_tables(nullptr, B, S).bytes;
+}
+
+fa_status fa_mask_ranges(const int *doc_ids, const int *prefix_len, int prefix_per_token, int B, int S,
+                         int causal, int window_left, int window_right, void *ranges, size_t ranges_bytes,
+                         cudaStream_t stream) {
+    const size_t need = fa_mask_ranges_bytes(B, S);
+    if (need == 0 || !ranges || (reinterpret_cast<uintptr_t>(ranges) & 255u) || ranges_bytes < need)
+        return FA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(doc_ids) & 3u) || (reinterpret_cast<uintptr_t>(prefix_len) & 3u))
+        return FA_ERR_INVALID_ARG;
+    if (window_left < -1 || window_right < -1) return FA_ERR_INVALID_ARG;
+    // a prefix joined to a window, or to rows that see all keys anyway, is not
+    // one interval / has no effect
+    if (prefix_len && (!causal || window_left != -1 || window_right != -1)) return FA_ERR_INVALID_ARG;
+    if (B > 65535) return FA_ERR_UNSUPPORTED;   // grid rows
+    fa_status st = check_device();
+    if (st != FA_OK) return st;
+    if (causal) window_right = 0;
+    const fa::RangeTables t = fa::range_tables(ranges, B, S);
+    return cuda_status(fa::launch_mask_ranges(doc_ids, prefix_len, prefix_per_token ? 1 : 0, B, S, window_left,
+                                              window_right, t, stream));
 }
 
 fa_status fa_fwd(const void *q, const void *k, const void *v, void *o, float *lse, int B, int Sq,

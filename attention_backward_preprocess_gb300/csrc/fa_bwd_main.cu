@@ -204,7 +204,9 @@ struct MainMaps {
 // visible key may lie right of the diagonal (a band with an upper edge above
 // it), which needs -slope |i + diag - j|; without it (e.g. causal) the bias is
 // linear in the key, slope (j - i - diag), and costs one add per pair.
-enum : int { kFBand = 1, kFAlibi = 2, kFBias = 4, kFDrop = 8, kFAbs = 16 };
+// kFCap: scores capped by a tanh.  kFRange: visible keys from fa_mask_ranges'
+// intervals in place of the band.
+enum : int { kFBand = 1, kFAlibi = 2, kFBias = 4, kFDrop = 8, kFAbs = 16, kFCap = 32, kFRange = 64 };
 // the instances built, each a superset of the flags before it in its chain
 constexpr int kMainFlagSets[] = {0,
                                  kFBand,
@@ -212,7 +214,10 @@ constexpr int kMainFlagSets[] = {0,
                                  kFBand | kFAlibi | kFAbs,
                                  kFBand | kFAlibi | kFAbs | kFBias,
                                  kFBand | kFDrop,
-                                 kFBand | kFAlibi | kFAbs | kFBias | kFDrop};
+                                 kFBand | kFAlibi | kFAbs | kFBias | kFDrop,
+                                 kFBand | kFCap,
+                                 kFRange,
+                                 kFRange | kFCap};
 
 // The elementwise bias of one 32-query chunk (from query qc) x a softmax
 // warp's 32 keys (from key kw), 8 queries (k) at a time: one 16-byte load per
@@ -289,14 +294,17 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
     using C = MainCfg<kD, T>;
     constexpr int D = C::D, BM = C::BM, BN = C::BN, S = C::kStages, HALF = C::HALF, NCH = C::NCH;
     constexpr bool kExt = (kFlags & kFBand) != 0, kAlibi = (kFlags & kFAlibi) != 0,
-                   kBias = (kFlags & kFBias) != 0, kDrop = (kFlags & kFDrop) != 0;
+                   kBias = (kFlags & kFBias) != 0, kDrop = (kFlags & kFDrop) != 0,
+                   kCap = (kFlags & kFCap) != 0, kRange = (kFlags & kFRange) != 0;
     // ALiBi with no visible key right of the diagonal: -slope |d| = slope d
     constexpr bool kAlibiLin = kAlibi && (kFlags & kFAbs) == 0;
     // D = 64, or an elementwise bias, without dropout: the dS pass reads P^T
     // back from tensor memory (the rounded operand of dV) instead of keeping
     // the step's fp32 values of P per thread in registers between the passes
     // (with a bias the registers hold the bias chunk meanwhile)
-    constexpr bool kPFromTmem = (NCH == 2 || kBias) && !kDrop;
+    // (capped scores keep P (1 - tanh^2) in those registers, P's place in dS =
+    // P (dP - Dv) (1 - tanh^2), so the cap adds nothing to the dS pass)
+    constexpr bool kPFromTmem = (NCH == 2 || kBias) && !kDrop && !kCap;
     // two 32-query chunks per softmax warp (D = 64) with P kept in registers:
     // the two 16-lane halves of a TMEM tile are loaded one after the other
     // (register pressure)
@@ -463,7 +471,7 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
                     mbar_arrive(ring.full0 + 8u * ring.k);
                     ring.advance(C::kRing);
                     if (t < 0) break;
-                    const Unit u = decode_unit<BM>(p, t);
+                    const Unit u = decode_unit<BM, kRange>(p, t);
                     if (u.iters == 0) continue;
                     const int nu = kn, ks = nu & 1;         // K slot; V goes to the other
                     // K into the slot that held the previous unit's V, once warp
@@ -504,7 +512,7 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
             while (ok) {
                 const int t = next_unit();
                 if (t < 0) break;
-                const Unit u = decode_unit<BM>(p, t);
+                const Unit u = decode_unit<BM, kRange>(p, t);
                 if (u.iters == 0) continue;
                 const int ks = nu & 1;
                 const uint32_t uph = (uint32_t)(nu >> 1) & 1u;
@@ -563,7 +571,7 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
             while (ok) {
                 const int t = next_unit();
                 if (t < 0) break;
-                const Unit u = decode_unit<BM>(p, t);
+                const Unit u = decode_unit<BM, kRange>(p, t);
                 if (u.iters == 0) continue;
                 const int ks = nu & 1;
                 const uint64_t dK_mn = sw128_desc(sbase + C::OFF_K + ks * C::KV_BYTES, BN * 128, 1024);
@@ -763,16 +771,18 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
             // from the last one down (the MMA warps' order)
             long long head0 = 0, hstride = 0;
             int g_it = 0, m_it = -1, m_first = 0, n_cur = 0, diag_cur = 0;
+            long long first0 = 0;   // kRange: the sequence's row in mr_first
             bool units_done = false;
             auto next_row = [&](long long &row0, int &nb) __attribute__((always_inline)) -> bool {
                 while (m_it < m_first) {
                     if (units_done) return false;
                     const int t = next_unit();
                     if (t < 0) { units_done = true; return false; }
-                    const Unit u = decode_unit<BM>(p, t);
+                    const Unit u = decode_unit<BM, kRange>(p, t);
                     if (u.nm == 0) continue;
                     n_cur = u.n_block;
                     diag_cur = u.lk - u.lq;
+                    if (kRange) first0 = (long long)u.b * (p.mr_rows / 64);
                     head0 = ws_row(p, u.b, u.hk * p.G, 0);
                     hstride = ws_row(p, u.b, u.hk * p.G + 1, 0) - head0;
                     m_first = u.m_begin;
@@ -783,6 +793,7 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
                 // deterministic order: contributions counted from the row block's
                 // first key block (block 0 unless the band has a lower edge)
                 nb = kExt ? n_cur - first_key_block(p, m_it * BM, diag_cur) : n_cur;
+                if (kRange && p.deterministic) nb = n_cur - p.mr_first[first0 + m_it * (BM / 64)];
                 if (++g_it == p.G) { g_it = 0; --m_it; }
                 return true;
             };
@@ -874,7 +885,7 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
             while (ok) {
                 const int t = next_unit();
                 if (t < 0) break;
-                const Unit u = decode_unit<BM>(p, t);
+                const Unit u = decode_unit<BM, kRange>(p, t);
                 for (int it = 0; it < u.iters; ++it) {
                     const int g = u.g_of(it, p.G), m = u.m_of(it, p.G);
                     const int h = u.hk * p.G + g;
@@ -896,8 +907,10 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
                         // contributions to this row block arrive in n-block order:
                         // wait until the 4 reducer warps of every earlier n block added
                         bool got = true;
-                        const int nb = kExt ? u.n_block - first_key_block(p, m * BM, u.lk - u.lq)
-                                            : u.n_block;
+                        const int nb = kExt     ? u.n_block - first_key_block(p, m * BM, u.lk - u.lq)
+                                       : kRange ? u.n_block - p.mr_first[(long long)u.b * (p.mr_rows / 64) +
+                                                                         m * (BM / 64)]
+                                                : u.n_block;
                         if (lane == 0) got = sem_wait_geq(sem, 4 * nb, w);
                         got = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
                         if (!got) { ok = false; break; }
@@ -972,7 +985,7 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
         Unit un;
         auto fetch = [&]() __attribute__((always_inline)) {
             t = next_unit();
-            if (t >= 0) un = decode_unit<BM>(p, t);
+            if (t >= 0) un = decode_unit<BM, kRange>(p, t);
         };
         if (kEarlyFetch) fetch();
         while (ok) {
@@ -991,7 +1004,18 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
                 const int m0 = m * BM;
                 // the tile crosses the upper / lower edge of the band: mask
                 // element by element (one compare per edge and element)
-                const bool masked_hi = n0 + BN - 1 - (m0 + diag) > whi;
+                const bool masked_hi = !kRange && n0 + BN - 1 - (m0 + diag) > whi;
+                // with intervals: some row of the step's block does not see the
+                // whole key block
+                bool masked_rng = false;
+                if (kRange) {
+                    const int4 *blk = p.mr_block + (long long)u.b * (p.mr_rows / 64) + m * (BM / 64);
+#pragma unroll
+                    for (int i = 0; i < BM / 64; ++i) {
+                        const int4 e = __ldg(blk + i);
+                        masked_rng |= e.z > n0 || e.w < n0 + BN;
+                    }
+                }
                 const bool masked_lo = kExt && n0 - (m0 + BM - 1 + diag) < -wlo;
                 // ALiBi slope of the step's query head, in log2 units (0: none)
                 float slope2 = 0.f;
@@ -1108,6 +1132,28 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
                             load_bias_chunk(bw, bias_h, p.bias_rs, m0 + c0, n0 + quarter * 32, u.lq, u.lk, lane);
                     }
                     const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
+                    const uint64_t capk2 = f2_pack(p.cap_k, p.cap_k);
+                    const uint64_t capm2 = f2_pack(-2.f * p.cap_log2, -2.f * p.cap_log2);
+                    if (kCap) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) nl2[k] = f2_add(nl2[k], f2_pack(p.cap_log2, p.cap_log2));
+                    }
+                    // intervals of the thread's query pairs, edge tiles only: key kb
+                    // + kr is visible iff (unsigned)(kr + rt) < rw
+                    int rt[kRange ? 8 : 1];
+                    uint32_t rw[kRange ? 8 : 1];
+                    if (kRange && masked_rng) {
+                        const int4 *rr = reinterpret_cast<const int4 *>(
+                            p.mr_row + (long long)u.b * p.mr_rows + m0 + c0 + 2 * q4);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int4 e = __ldg(rr + 4 * k);
+                            rt[kRange ? 2 * k : 0] = kb - e.x;
+                            rw[kRange ? 2 * k : 0] = (uint32_t)max(e.y - e.x, 0);
+                            rt[kRange ? 2 * k + 1 : 0] = kb - e.z;
+                            rw[kRange ? 2 * k + 1 : 0] = (uint32_t)max(e.w - e.z, 0);
+                        }
+                    }
                     tmem_wait_ld();
                     if constexpr (kBias) {
                         if (bias_h) bias_to_st_order(bw, lane);
@@ -1141,10 +1187,24 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
                                 uint64_t addend = nl2[k];
                                 if (kAlibiLin && kr > 0)
                                     addend = f2_add(addend, f2_pack(slope2 * (float)kr, slope2 * (float)kr));
-                                const float2 x = f2_unpack(f2_fma(
-                                    f2_pack(__uint_as_float(sr[h][4 * k + 2 * r]),
-                                            __uint_as_float(sr[h][4 * k + 2 * r + 1])),
-                                    sc2, addend));
+                                const uint64_t sraw = f2_pack(__uint_as_float(sr[h][4 * k + 2 * r]),
+                                                              __uint_as_float(sr[h][4 * k + 2 * r + 1]));
+                                float2 x;
+                                float g0 = 0.f, g1 = 0.f;   // kCap: 1 - tanh^2
+                                if (kCap) {
+                                    // cap_log2 tanh(.) - LSE2 = (cap_log2 - LSE2) - 2 cap_log2 r
+                                    const float2 z = f2_unpack(f2_mul(sraw, capk2));
+                                    float r0, r1;
+                                    cap_r2(z.x, z.y, r0, r1);
+                                    const uint64_t rr2 = f2_pack(r0, r1);
+                                    x = f2_unpack(f2_fma(rr2, capm2, addend));
+                                    const uint64_t r4 = f2_mul(rr2, f2_pack(4.f, 4.f));
+                                    const float2 g = f2_unpack(f2_sub(r4, f2_mul(r4, rr2)));
+                                    g0 = g.x;
+                                    g1 = g.y;
+                                } else {
+                                    x = f2_unpack(f2_fma(sraw, sc2, addend));
+                                }
                                 float x0 = x.x, x1 = x.y;
                                 if (kAlibi && !kAlibiLin) {
                                     // -slope * |qi + diag - kj|
@@ -1172,10 +1232,15 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
                                     if (lim_lo + kr < 8 * k) pv0 = 0.f;
                                     if (lim_lo + kr < 8 * k + 1) pv1 = 0.f;
                                 }
+                                if (kRange && masked_rng) {
+                                    if ((uint32_t)(rt[kRange ? 2 * k : 0] + kr) >= rw[kRange ? 2 * k : 0]) pv0 = 0.f;
+                                    if ((uint32_t)(rt[kRange ? 2 * k + 1 : 0] + kr) >= rw[kRange ? 2 * k + 1 : 0])
+                                        pv1 = 0.f;
+                                }
                                 if (kb + kr >= u.lk) { pv0 = 0.f; pv1 = 0.f; }
                                 if (!kPFromTmem) {
-                                    P[32 * ch + 16 * h + 4 * k + 2 * r] = pv0;
-                                    P[32 * ch + 16 * h + 4 * k + 2 * r + 1] = pv1;
+                                    P[32 * ch + 16 * h + 4 * k + 2 * r] = kCap ? pv0 * g0 : pv0;
+                                    P[32 * ch + 16 * h + 4 * k + 2 * r + 1] = kCap ? pv1 * g1 : pv1;
                                 }
                                 if (kDrop) {
                                     // dV takes the dropped-out, rescaled P
@@ -1453,7 +1518,8 @@ static cudaError_t launch_main_t(const BwdParams &p, const MainMaps &maps, int g
     using C = MainCfg<kD, T>;
     const int need = (p.win_lo < kNoWindow ? kFBand : 0) |
                      (p.alibi ? kFAlibi | (p.win_hi > 0 ? kFAbs : 0) : 0) |
-                     ((p.bias || p.dbias) ? kFBias : 0) | (p.drop_t > 0 ? kFDrop : 0);
+                     ((p.bias || p.dbias) ? kFBias : 0) | (p.drop_t > 0 ? kFDrop : 0) |
+                     (p.cap_log2 > 0.f ? kFCap : 0) | (p.mr_row ? kFRange : 0);
     auto kern = main_kernel_for<kD, T>(need);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          C::SMEM_BYTES);

@@ -43,7 +43,8 @@ struct Unit {
 // Work unit t: dense problems enumerate groups of (batch, kv head) pairs,
 // then n_block, then the pair inside the group; varlen problems read the list
 // the scheduler kernel wrote.
-template <int BM>
+// kRange: the row blocks come from fa_mask_ranges' table (dense problems).
+template <int BM, bool kRange = false>
 __device__ __forceinline__ Unit decode_unit(const BwdParams &p, int t) {
     Unit u;
     if (p.varlen) {
@@ -74,6 +75,16 @@ __device__ __forceinline__ Unit decode_unit(const BwdParams &p, int t) {
         u.lq = used_len_q(p, u.b);
         u.lk = used_len_k(p, u.b);
         u.bidx = u.b;
+    }
+    if constexpr (kRange) {
+        // 64-row blocks [r.x, r.y), inside the used rows
+        constexpr int F = BM / 64;
+        const int2 r = __ldg(p.mr_key + (long long)u.b * (p.mr_rows / kBlockN) + u.n_block);
+        const int lo = max(r.x, 0), hi = min(r.y, (u.lq + 63) / 64);
+        u.m_begin = lo / F;
+        u.nm = (lo < hi && u.n_block * kBlockN < u.lk) ? (hi + F - 1) / F - u.m_begin : 0;
+        u.iters = p.G * u.nm;
+        return u;
     }
     // queries that see a key of [n0, n0 + kBlockN): i >= n0 - diag - win_hi
     // (the first key against the upper edge of the band) and

@@ -578,4 +578,27 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Capped scores.  With e = exp(2 y), tanh(y) = 1 - 2 r and 1 - tanh(y)^2 =
+// 4 r (1 - r) for r = 1 / (1 + e): one exp2 per score and one reciprocal per
+// two, 1 / a = b / (a b).  z = 2 y log2(e) is held at 60, where r is below
+// 2^-59 and tanh rounds to 1, so that the product of two 1 + e stays finite;
+// NaN passes.  The error of 1 - 2 r is absolute, about 2^-22 (ex2 and rcp
+// each within 2^-22 of their result, r <= 1), which is what a capped score of
+// softcap * tanh needs: tanh.approx, one instruction, is off by 2^-11.
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float cap_exp(float z) {
+    asm("min.NaN.f32 %0, %0, 0f42700000;" : "+f"(z));   // 60
+    return ex2(z);
+}
+__device__ __forceinline__ void cap_r2(float z0, float z1, float &r0, float &r1) {
+    const float a = 1.f + cap_exp(z0), b = 1.f + cap_exp(z1);
+    const float r = rcp_approx(a * b);
+    r0 = r * b;
+    r1 = r * a;
+}
+
 }  // namespace fa

@@ -14,10 +14,12 @@ namespace fa {
 // (the band needs none: only edge blocks test it).  Each extension gets
 // compiled in only where asked for: its code slows the softmax even when
 // skipped at run time.
-enum : int { kFwdAlibi = 2, kFwdBias = 4, kFwdDrop = 8 };
+// kFwdCap: scores capped by a tanh; kFwdRange: visible keys from
+// fa_mask_ranges' intervals instead of the band.
+enum : int { kFwdAlibi = 2, kFwdBias = 4, kFwdDrop = 8, kFwdCap = 16, kFwdRange = 32 };
 // the instances built, each a superset of the flags before it in its chain
 constexpr int kFwdFlagSets[] = {0, kFwdAlibi, kFwdAlibi | kFwdBias, kFwdDrop,
-                                kFwdAlibi | kFwdBias | kFwdDrop};
+                                kFwdAlibi | kFwdBias | kFwdDrop, kFwdRange, kFwdCap | kFwdRange};
 constexpr int kNumFwdFlagSets = (int)(sizeof(kFwdFlagSets) / sizeof(int));
 
 // The first instance built that has every flag needed.
@@ -33,7 +35,7 @@ constexpr int fwd_instance_flags(int need) {
 // the 8k GQA workload, the plain and ALiBi instances at D = 128 run faster
 // with one warp per row (fa_fwd_tc.cu): there the per-block exchange of the
 // row maxima between the two warps costs more than the halved work saves.
-constexpr bool fwd_split(int d, int flags) { return (flags & (kFwdBias | kFwdDrop)) != 0 || d == 64; }
+constexpr bool fwd_split(int d, int flags) { return (flags & (kFwdBias | kFwdDrop | kFwdCap)) != 0 || d == 64; }
 
 // Launches the two-warps-per-row forward instance for (D, dtype, flags).
 cudaError_t launch_fwd_split(const BwdParams &p, const CUtensorMap &q, const CUtensorMap &k,

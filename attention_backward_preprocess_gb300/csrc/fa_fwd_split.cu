@@ -24,6 +24,7 @@
 
 #include "fa_device.cuh"
 #include "fa_fwd_common.h"
+#include "fa_fwd_ranges.cuh"
 #include "fa_params.h"
 
 namespace fa {
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(SplitCfg<kD, T>::kThreads, 1)
     using C = SplitCfg<kD, T>;
     constexpr int D = C::D, BM = C::BM, BN = C::BN, S = C::kStages;
     constexpr bool kAlibi = (kFlags & kFwdAlibi) != 0, kBias = (kFlags & kFwdBias) != 0,
-                   kDrop = (kFlags & kFwdDrop) != 0;
+                   kDrop = (kFlags & kFwdDrop) != 0, kCap = (kFlags & kFwdCap) != 0;
     constexpr bool kExt = kAlibi || kBias;   // scores other than the plain scaled ones
     // Without the bias or dropout the softmax holds a block's scores in
     // registers, and three S buffers fit tensor memory (with D = 128 exactly):
@@ -134,8 +135,10 @@ __global__ void __launch_bounds__(SplitCfg<kD, T>::kThreads, 1)
     if (m * BM >= lq) return;                       // uniform: the whole CTA leaves
     // key j is visible to query i iff -win_lo <= j - i - diag <= win_hi, j < lk
     const int diag = lk - lq;
-    const long long first_key = max(0LL, (long long)m * BM + diag - p.win_lo);
-    const long long last_key = min((long long)lk - 1, (long long)m * BM + BM - 1 + diag + p.win_hi);
+    long long first_key = max(0LL, (long long)m * BM + diag - p.win_lo);
+    long long last_key = min((long long)lk - 1, (long long)m * BM + BM - 1 + diag + p.win_hi);
+    const bool ranges = (kFlags & kFwdRange) != 0 && p.mr_row != nullptr;
+    if (ranges) tile_range(p, b, m, lk, &first_key, &last_key);
     // key blocks [n_begin, n_begin + nblk) hold every key some row of the tile sees
     const int n_begin = (int)(first_key / BN);
     const int nblk = last_key < first_key ? 0 : (int)(last_key / BN) + 1 - n_begin;
@@ -307,8 +310,9 @@ __global__ void __launch_bounds__(SplitCfg<kD, T>::kThreads, 1)
         const int qi = m * BM + r;                  // query index within the sequence
         const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
         // keys [kmin, kmax] are visible to this row (none if kmax < kmin)
-        const int kmin = (int)max(0LL, (long long)qi + diag - p.win_lo);
-        const int kmax = (int)min((long long)lk - 1, (long long)qi + diag + p.win_hi);
+        int kmin = (int)max(0LL, (long long)qi + diag - p.win_lo);
+        int kmax = (int)min((long long)lk - 1, (long long)qi + diag + p.win_hi);
+        if (ranges) row_range(p, b, qi, lq, lk, &kmin, &kmax);
         // ALiBi slope of this head, log2 units
         const float slope2 = (kAlibi && p.alibi)
                                  ? __ldg(p.alibi + (long long)b * p.alibi_bstride + h) * 1.4426950408889634f
@@ -479,6 +483,13 @@ __global__ void __launch_bounds__(SplitCfg<kD, T>::kThreads, 1)
                 }
                 const float mx = fmaxf(fmaxf(fmaxf(mxv[0], mxv[1]), fmaxf(mxv[2], mxv[3])),
                                        fmaxf(fmaxf(mxv[4], mxv[5]), fmaxf(mxv[6], mxv[7])));
+                if (kCap) {
+                    // tanh rises: the cap of the largest raw score is the largest
+                    // capped one (-inf, no visible key, stays -inf)
+                    float r0, r1;
+                    cap_r2(mx * p.cap_k, 0.f, r0, r1);
+                    return mx == -INFINITY ? mx : fmaf(-2.f * p.cap_log2, r0, p.cap_log2);
+                }
                 return kExt ? mx : mx * p.scale_log2;
             };
             float mx = edge ? half_max(std::true_type{}) : half_max(std::false_type{});
@@ -506,7 +517,13 @@ __global__ void __launch_bounds__(SplitCfg<kD, T>::kThreads, 1)
                     for (int i = 0; i < 16; ++i) {
                         const int e = 32 * c + 2 * i;
                         float p0, p1;
-                        if (kExt) {
+                        if (kCap) {
+                            float r0, r1;
+                            cap_r2(__uint_as_float(sr[2 * i]) * p.cap_k, __uint_as_float(sr[2 * i + 1]) * p.cap_k, r0,
+                                   r1);
+                            p0 = ex2(fmaf(-2.f * p.cap_log2, r0, p.cap_log2 - mref));
+                            p1 = ex2(fmaf(-2.f * p.cap_log2, r1, p.cap_log2 - mref));
+                        } else if (kExt) {
                             p0 = ex2(score2(sr[2 * i], e, bl[2 * i]) - mref);
                             p1 = ex2(score2(sr[2 * i + 1], e + 1, bl[2 * i + 1]) - mref);
                         } else {
@@ -574,6 +591,8 @@ __global__ void __launch_bounds__(SplitCfg<kD, T>::kThreads, 1)
                 float *lse_dst = p.varlen ? lse_out + (long long)h * p.cu_q[p.B] + q0 + qi
                                           : lse_out + ((long long)b * p.Hq + h) * p.Sq + qi;
                 *lse_dst = l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+                // a row of NaN scores: NaN (the other instances give -inf)
+                if ((kFlags & (kFwdCap | kFwdRange)) != 0 && l_run != l_run) *lse_dst = l_run;
             }
             const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
             // this warp's DW columns; Dh <= D columns are stored

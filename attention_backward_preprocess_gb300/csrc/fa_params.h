@@ -4,6 +4,8 @@
 
 #include <cstdint>
 
+#include <vector_types.h>
+
 namespace fa {
 
 constexpr int kRowTile = 128;   // workspace rows are padded per (sequence, head) to this
@@ -77,6 +79,17 @@ struct BwdParams {
     long long rows_per_head;  // varlen: rows of one head; dense: round_up(Sq, 128)
     int sq_round;       // round_up(Sq, 128)
     long long budget_ns;      // bound of every device-side wait
+    // Capped scores, softcap * tanh(c s / softcap) of the product s: cap_log2
+    // = softcap * log2(e) and cap_k = 2 log2(e) c / softcap (0: no cap)
+    float cap_log2, cap_k;
+    // Visible-key intervals of fa_mask_ranges (fa_ranges.h; null: the band
+    // above): per row, per 64-row block, per key block, and the first key
+    // block of a row block; mr_rows = Sq rounded up to 128
+    const int2 *mr_row;
+    const int4 *mr_block;
+    const int2 *mr_key;
+    const int *mr_first;
+    int mr_rows;
 };
 
 // Varlen: cu_seqlens agree with the packed totals and with the maximum

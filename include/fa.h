@@ -239,6 +239,22 @@ fa_status fa_fwd(const void *q, const void *k, const void *v, void *o, float *ls
  *   any row of the offending sequences.  The tensors must hold at least
  *   that many rows: a count larger than the rows allocated lets the tiled
  *   loads of the last rows run past the end of the tensors. */
+/* softcap (0 = none; else in [0.001, 1000]): the score of (i, j) becomes
+ *   softcap * tanh(scale * <q_i, k_j> / softcap), in natural-log units.  The
+ *   backward multiplies dS by 1 - tanh^2; fa_bwd_ext must get the forward's
+ *   softcap.  Computed with an absolute error of about softcap * 2^-21.  With
+ *   the causal mask, windows, used lengths, varlen, deterministic mode and
+ *   mask_ranges; not with ALiBi, the bias, dBias, dropout, or head dims above
+ *   128 or unequal ones (FA_ERR_UNSUPPORTED).
+ * mask_ranges (NULL = none): the buffer of at least mask_ranges_bytes bytes
+ *   that fa_mask_ranges filled for the same B and S = Sq = Sk; query i then
+ *   sees exactly the keys of its interval (inside the used lengths).  The
+ *   causal flag and the windows of the attention call itself must be off
+ *   (FA_ERR_INVALID_ARG): they are part of the intervals.  Dense problems
+ *   (FA_ERR_UNSUPPORTED with cu_seqlens), with softcap, used lengths and
+ *   deterministic mode; not with the extensions and head dims named above.
+ *   Keys and values of masked tokens must be finite, as for every mask of
+ *   this library: a masked entry has P = 0, and 0 times their value is added. */
 typedef struct {
     int window_left;
     int window_right;
@@ -258,7 +274,36 @@ typedef struct {
     long long total_q;
     long long total_k;
     int head_dim_v;
+    float softcap;
+    const void *mask_ranges;
+    size_t mask_ranges_bytes;
 } fa_ext;
+
+/* Visible keys of self-attention problems (Sq = Sk = S, dense) with documents
+ * and prefixes, as one interval per query row, for fa_ext.mask_ranges.  Built
+ * once per batch and read by every layer's forward and backward.  Within
+ * sequence b, row i sees the keys [lo, hi):
+ *   s, e  first and past-the-end position of i's document: a maximal run of
+ *         equal ids in doc_ids[b * S ...] (device int32 [B, S]; NULL: each
+ *         sequence is one document).  A negative id is padding: its rows see
+ *         no key (O = 0, LSE = -inf, dQ = 0) and no row sees its keys;
+ *   lo = s, with window_left >= 0 max(s, i - window_left);
+ *   hi = e, with window_right >= 0 min(e, i + window_right + 1); causal != 0:
+ *         min(e, i + 1);
+ *   prefix_len (device int32, NULL = none; causal only, without windows): hi =
+ *         max(hi, s + min(max(n, 0), e - s)), every row of a document also
+ *         sees its first n tokens.  n = prefix_len[b], or with
+ *         prefix_per_token != 0 prefix_len[b * S + s], the entry of the
+ *         document's first token in a [B, S] array.
+ * ranges: device buffer of fa_mask_ranges_bytes(B, S) bytes (0: bad sizes),
+ *   256-byte aligned, fully overwritten.  Two launches on `stream`, no other
+ *   call; can be captured into a CUDA graph.  Errors: FA_ERR_INVALID_ARG for
+ *   sizes, alignment, a window below -1, or a prefix without causal or with a
+ *   window; FA_ERR_UNSUPPORTED for B above 65535. */
+size_t fa_mask_ranges_bytes(int B, int S);
+fa_status fa_mask_ranges(const int *doc_ids, const int *prefix_len, int prefix_per_token, int B, int S,
+                         int causal, int window_left, int window_right, void *ranges,
+                         size_t ranges_bytes, cudaStream_t stream);
 
 /* fa_fwd with extensions.  Errors as fa_fwd, plus FA_ERR_INVALID_ARG for a
  * window side below -1, an ALiBi stride other than 0 / Hq, or a slope or
