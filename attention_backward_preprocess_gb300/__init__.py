@@ -30,6 +30,7 @@ EXPORTED = [
     "fa_selftest_umma", "fa_selftest_semaphore", "fa_selftest_tmem_layout", "fa_bwd_noalloc",
     "fa_bwd_noalloc_scratch_bytes", "fa_fwd_ext", "fa_bwd_ext", "fa_bwd_stages_ext", "fa_bwd_workspace_sync_layout",
     "fa_bwd_noalloc_status", "fa_mask_ranges", "fa_mask_ranges_bytes",
+    "fa_kvcache_append", "fa_fwd_kvcache", "fa_fwd_kvcache_workspace_bytes",
 ]
 
 
@@ -137,6 +138,110 @@ def _ext(Hq, window=None, alibi_slopes=None, seqused_q=None, seqused_k=None, bia
     return ctypes.pointer(e)
 
 
+class _KvCacheStruct(ctypes.Structure):
+    """fa_kv_cache of include/fa.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("Hkv", ctypes.c_int),
+                ("D", ctypes.c_int)]
+
+
+class KvCache:
+    """An 8-bit paged key / value cache over the caller's tensors: ``k``
+    float8_e4m3fn [pages, Hkv, page, D], ``v`` float8_e4m3fn [pages, Hkv, D,
+    page], ``k_scale`` / ``v_scale`` float32 [pages, Hkv], ``block_table``
+    int32 [B, max_pages]; see fa_kv_cache in include/fa.h.  Keeps the tensors,
+    copies nothing."""
+
+    def __init__(self, k, v, k_scale, v_scale, block_table):
+        if k.dim() != 4 or tuple(v.shape) != (k.shape[0], k.shape[1], k.shape[3], k.shape[2]):
+            raise ValueError("k: [pages, Hkv, page, D], v: [pages, Hkv, D, page]")
+        for name, t, dt, shape in (("k", k, torch.float8_e4m3fn, None), ("v", v, torch.float8_e4m3fn, None),
+                                   ("k_scale", k_scale, torch.float32, tuple(k.shape[:2])),
+                                   ("v_scale", v_scale, torch.float32, tuple(k.shape[:2])),
+                                   ("block_table", block_table, torch.int32, None)):
+            if t.dtype != dt or not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
+                raise ValueError("%s: contiguous %s%s" % (name, dt, "" if shape is None else " %r" % (shape,)))
+            _same_device(k.device, t, name)
+        if block_table.dim() != 2:
+            raise ValueError("block_table: [B, max_pages]")
+        self.k, self.v, self.k_scale, self.v_scale, self.block_table = k, v, k_scale, v_scale, block_table
+        self._c = _KvCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                 block_table.data_ptr(), k.shape[0], k.shape[2], block_table.shape[1], k.shape[1],
+                                 k.shape[3])
+
+    def _lengths(self, name, t, n):
+        if t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != (n,):
+            raise ValueError("%s: contiguous int32 [%d]" % (name, n))
+        _same_device(self.k.device, t, name)
+
+
+def kvcache_append(cache, cache_len, k_new, v_new, cu_new=None, max_new=None, stream=None):
+    """Quantises new keys and values into ``cache`` (a KvCache) behind the
+    ``cache_len`` (int32 [B]) tokens each sequence holds: fa_kvcache_append.
+
+    ``k_new`` / ``v_new``: [B, T, Hkv, D], or [total, Hkv, D] with ``cu_new``
+    (int32 [B + 1] prefix sums) and ``max_new``, the most tokens of one
+    sequence.  The cache's tensors are updated in place."""
+    B = cache.block_table.shape[0]
+    cache._lengths("cache_len", cache_len, B)
+    if cu_new is None:
+        if k_new.dim() != 4 or k_new.shape[0] != B:
+            raise ValueError("k_new: [B, T, Hkv, D]")
+        max_new = k_new.shape[1]
+    else:
+        cache._lengths("cu_new", cu_new, B + 1)
+        if k_new.dim() != 3 or max_new is None:
+            raise ValueError("k_new: [total, Hkv, D], with max_new")
+    if k_new.shape != v_new.shape or tuple(k_new.shape[-2:]) != (cache._c.Hkv, cache._c.D):
+        raise ValueError("k_new / v_new: the cache's heads and head dim")
+    if k_new.dtype != v_new.dtype:
+        raise ValueError("k_new / v_new: one dtype")
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        _same_device(cache.k.device, t, name)
+    k_new, v_new = _dense(stream, k_new=k_new, v_new=v_new)
+    with torch.cuda.device(cache.k.device):
+        _check(lib().fa_kvcache_append(ctypes.byref(cache._c), _ptr(cache_len), _ptr(k_new), _ptr(v_new),
+                                       _ptr(cu_new), B, int(max_new), _dtype_code(k_new), _stream(stream)),
+               "fa_kvcache_append")
+
+
+def fa_fwd_kvcache(q, cache, cache_len, softmax_scale=None, softcap=0.0, window_left=-1, workspace=None,
+                   out=None, stream=None):
+    """Attention of each sequence's last tokens over an 8-bit paged cache:
+    returns (o, lse).  ``q``: [B, Sq, Hq, D], the last Sq tokens of each
+    sequence, whose own keys and values are in the cache already; ``cache_len``
+    (int32 [B]) counts them.  ``workspace``: a uint8 CUDA tensor of
+    ``fa_fwd_kvcache_workspace_bytes(D)`` (allocated when not given); ``out``:
+    (o, lse) to write into.  See fa_fwd_kvcache in include/fa.h."""
+    if q.dim() != 4 or q.shape[0] != cache.block_table.shape[0] or q.shape[3] != cache._c.D:
+        raise ValueError("q: [B, Sq, Hq, D] of the cache's B and D")
+    B, Sq, Hq, D = q.shape
+    cache._lengths("cache_len", cache_len, B)
+    _same_device(cache.k.device, q, "q")
+    scale = default_scale(D) if softmax_scale is None else float(softmax_scale)
+    (q,) = _dense(stream, q=q)
+    with torch.cuda.device(cache.k.device):
+        if out is None:
+            out = torch.empty_like(q), torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
+        else:
+            _outputs(o=out[0], lse=out[1])
+            if out[0].shape != q.shape or out[0].dtype != q.dtype or tuple(out[1].shape) != (B, Hq, Sq) \
+                    or out[1].dtype != torch.float32:
+                raise ValueError("out: (o like q, float32 lse [B, Hq, Sq])")
+        if workspace is None:
+            workspace = torch.empty(fa_fwd_kvcache_workspace_bytes(D), dtype=torch.uint8, device=q.device)
+        _check(lib().fa_fwd_kvcache(_ptr(q), ctypes.byref(cache._c), _ptr(cache_len), _ptr(out[0]), _ptr(out[1]), B,
+                                    Sq, Hq, scale, float(softcap), int(window_left), _dtype_code(q),
+                                    _ptr(workspace), workspace.numel(), _stream(stream)), "fa_fwd_kvcache")
+    return out
+
+
+def fa_fwd_kvcache_workspace_bytes(D) -> int:
+    """Bytes of workspace fa_fwd_kvcache needs (0: a head dim it does not take)."""
+    return int(lib().fa_fwd_kvcache_workspace_bytes(int(D)))
+
+
 def _same_device(device, t, name):
     """Raises unless ``t`` is on ``device`` (None, or one without an index: any CUDA device)."""
     d = None if device is None else torch.device(device)
@@ -231,6 +336,11 @@ def lib():
         L.fa_bwd_noalloc_status.restype = _i
         L.fa_bwd_workspace_sync_layout.argtypes = _SHAPE + [_i, _i] + [ctypes.POINTER(_sz)] * 3
         L.fa_bwd_workspace_sync_layout.restype = _i
+        _kp = ctypes.POINTER(_KvCacheStruct)
+        L.fa_kvcache_append.argtypes = [_kp] + [_vp] * 4 + [_i] * 3 + [_vp]
+        L.fa_fwd_kvcache_workspace_bytes.argtypes = [_i]
+        L.fa_fwd_kvcache_workspace_bytes.restype = _sz
+        L.fa_fwd_kvcache.argtypes = [_vp, _kp, _vp, _vp, _vp] + [_i] * 3 + [_f, _f, _i, _i, _vp, _sz, _vp]
         L.fa_mask_ranges_bytes.argtypes = [_i, _i]
         L.fa_mask_ranges_bytes.restype = _sz
         L.fa_mask_ranges.argtypes = [_vp, _vp] + [_i] * 6 + [_vp, _sz, _vp]
@@ -239,7 +349,7 @@ def lib():
         L.fa_selftest_tmem_layout.argtypes = [_i, _vp, _vp]
         for name in ("fa_bwd", "fa_bwd_with_workspace", "fa_bwd_preprocess", "fa_bwd_main",
                      "fa_bwd_postprocess", "fa_bwd_workspace_layout", "fa_fwd", "fa_fwd_ext",
-                     "fa_bwd_ext", "fa_mask_ranges",
+                     "fa_bwd_ext", "fa_mask_ranges", "fa_kvcache_append", "fa_fwd_kvcache",
                      "fa_device_status", "fa_selftest_umma", "fa_selftest_semaphore",
                      "fa_selftest_tmem_layout"):
             getattr(L, name).restype = _i

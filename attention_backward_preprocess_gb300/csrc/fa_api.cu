@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/fa.h"
+#include "fa_kvcache.h"
 #include "fa_params.h"
 #include "fa_ranges.h"
 
@@ -519,7 +520,8 @@ fa_status read_error_word(int *err_dev, cudaStream_t stream, bool clear) {
     if (cudaMemcpy(&h, err_dev, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
         return FA_ERR_CUDA;
     if (clear && h != 0 && cudaMemset(err_dev, 0, sizeof(int)) != cudaSuccess) return FA_ERR_CUDA;
-    if (h & 4) return FA_ERR_INVALID_ARG;   // kErrBadLength: cu_seqlens against the sizes given
+    // kErrBadLength: cu_seqlens or cached lengths against the sizes given; kErrBadPage
+    if (h & 12) return FA_ERR_INVALID_ARG;
     return h ? FA_ERR_TIMEOUT : FA_OK;
 }
 
@@ -716,6 +718,108 @@ fa_status fa_device_status(void *workspace, cudaStream_t stream) {
     }
     fa_status st2 = read_error_word(reinterpret_cast<int *>(ws), stream, true);
     return st2 != FA_OK ? st2 : st;
+}
+
+namespace {
+
+// The cache's host-visible fields; fills the kernels' parameter block.
+fa_status check_kv_cache(const fa_kv_cache *c, int B, fa_dtype dtype, fa::KvCacheParams *p) {
+    if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || !c->block_table) return FA_ERR_INVALID_ARG;
+    if (B <= 0 || c->num_pages <= 0 || c->page_size <= 0 || c->max_pages <= 0 || c->Hkv <= 0)
+        return FA_ERR_INVALID_ARG;
+    if (!aligned16(c->k) || !aligned16(c->v) || (reinterpret_cast<uintptr_t>(c->k_scale) & 3u) ||
+        (reinterpret_cast<uintptr_t>(c->v_scale) & 3u) || (reinterpret_cast<uintptr_t>(c->block_table) & 3u))
+        return FA_ERR_INVALID_ARG;
+    if (c->page_size % 16 != 0 || c->page_size > 128) return FA_ERR_UNSUPPORTED;
+    if (c->D != 64 && c->D != 128) return FA_ERR_UNSUPPORTED;
+    if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
+    if ((long long)c->max_pages * c->page_size > 0x7fffffffLL - 128) return FA_ERR_INVALID_ARG;   // token indices
+    p->k = static_cast<uint8_t *>(c->k);
+    p->v = static_cast<uint8_t *>(c->v);
+    p->k_scale = c->k_scale;
+    p->v_scale = c->v_scale;
+    p->table = c->block_table;
+    p->num_pages = c->num_pages;
+    p->page = c->page_size;
+    p->max_pages = c->max_pages;
+    p->Hkv = c->Hkv;
+    return FA_OK;
+}
+
+}  // namespace
+
+fa_status fa_kvcache_append(const fa_kv_cache *cache, const int *cache_len, const void *k_new, const void *v_new,
+                            const int *cu_new, int B, int max_new, fa_dtype dtype, cudaStream_t stream) {
+    fa::KvAppendParams p;
+    std::memset(&p, 0, sizeof(p));
+    fa_status st = check_kv_cache(cache, B, dtype, &p.c);
+    if (st != FA_OK) return st;
+    if (!cache_len || !k_new || !v_new || max_new <= 0) return FA_ERR_INVALID_ARG;
+    if (!aligned16(k_new) || !aligned16(v_new) || (reinterpret_cast<uintptr_t>(cache_len) & 3u) ||
+        (reinterpret_cast<uintptr_t>(cu_new) & 3u))
+        return FA_ERR_INVALID_ARG;
+    if ((long long)B * max_new > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+    if (cache->Hkv > 65535) return FA_ERR_UNSUPPORTED;   // grid columns
+    if ((st = check_device()) != FA_OK) return st;
+    p.c.err = fa::fwd_error_word();
+    if (!p.c.err) return FA_ERR_CUDA;
+    p.len = cache_len;
+    p.cu = cu_new;
+    p.k = k_new;
+    p.v = v_new;
+    p.B = B;
+    p.max_new = max_new;
+    return cuda_status(fa::launch_kv_append(p, cache->D, dtype == FA_BF16, stream));
+}
+
+size_t fa_fwd_kvcache_workspace_bytes(int D) { return (D == 64 || D == 128) ? fa::kv_workspace_bytes(D) : 0; }
+
+fa_status fa_fwd_kvcache(const void *q, const fa_kv_cache *cache, const int *cache_len, void *o, float *lse, int B,
+                         int Sq, int Hq, float softmax_scale, float softcap, int window_left, fa_dtype dtype,
+                         void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    fa::KvAttnParams p;
+    std::memset(&p, 0, sizeof(p));
+    fa_status st = check_kv_cache(cache, B, dtype, &p.c);
+    if (st != FA_OK) return st;
+    if (!q || !o || !cache_len || !workspace || Sq <= 0 || Hq <= 0 || Hq % cache->Hkv != 0)
+        return FA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
+        (reinterpret_cast<uintptr_t>(cache_len) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return FA_ERR_INVALID_ARG;
+    if (!(std::isfinite(softmax_scale) && softmax_scale > 0.f) || window_left < -1) return FA_ERR_INVALID_ARG;
+    if (softcap != 0.f && !(softcap >= kMinSoftcap && softcap <= kMaxSoftcap)) return FA_ERR_INVALID_ARG;
+    if (B > fa::kKvMaxSeqs) return FA_ERR_UNSUPPORTED;
+    if ((long long)Sq * Hq > (1 << 24)) return FA_ERR_UNSUPPORTED;
+    p.scale_log2 = softmax_scale * kLog2e;
+    if (softcap != 0.f) {
+        p.cap_log2 = softcap * kLog2e;
+        p.cap_k = 2.f * p.scale_log2 / softcap;
+        if (!std::isfinite(p.cap_k)) return FA_ERR_INVALID_ARG;
+    }
+    const size_t need = fa_fwd_kvcache_workspace_bytes(cache->D);
+    if (workspace_bytes < need) return FA_ERR_INVALID_ARG;
+    p.len = cache_len;
+    p.q = q;
+    p.o = o;
+    p.lse = lse;
+    p.B = B;
+    p.Sq = Sq;
+    p.Hq = Hq;
+    p.G = Hq / cache->Hkv;
+    p.groups = (p.G * Sq + 15) / 16;
+    // tiles are counted in 32 bits per sequence sum
+    if ((long long)B * (cache->max_pages * (long long)cache->page_size / 64 + 1) > 0x7fffffffLL)
+        return FA_ERR_UNSUPPORTED;
+    p.window = std::min(window_left, 1 << 30);   // positions stay inside 32 bits
+    if ((st = check_device()) != FA_OK) return st;
+    p.c.err = fa::fwd_error_word();
+    if (!p.c.err) return FA_ERR_CUDA;
+    const size_t n = (size_t)fa::kKvSms * fa::kv_warps(cache->D);
+    uint8_t *w = static_cast<uint8_t *>(workspace);
+    p.acc = reinterpret_cast<float *>(w);
+    p.stat = reinterpret_cast<float4 *>(w + n * 2 * 16 * cache->D * sizeof(float));
+    p.meta = reinterpret_cast<int4 *>(w + n * 2 * 16 * cache->D * sizeof(float) + n * 2 * 16 * sizeof(float4));
+    return cuda_status(fa::launch_kv_attn(p, cache->D, dtype == FA_BF16, sm_count(), stream));
 }
 
 size_t fa_mask_ranges_bytes(int B, int S) {

@@ -1193,6 +1193,8 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
                                 float g0 = 0.f, g1 = 0.f;   // kCap: 1 - tanh^2
                                 if (kCap) {
                                     // cap_log2 tanh(.) - LSE2 = (cap_log2 - LSE2) - 2 cap_log2 r
+                                    // (the pair is two queries of one key: a NaN query takes
+                                    // its neighbour's dQ along; dK and dV are NaN then anyway)
                                     const float2 z = f2_unpack(f2_mul(sraw, capk2));
                                     float r0, r1;
                                     cap_r2(z.x, z.y, r0, r1);

@@ -13,13 +13,15 @@
 namespace fa {
 
 // ------------------------------------------------------------------ errors
-// Device error word bits (the host reports kErrBadLength as FA_ERR_INVALID_ARG,
+// Device error word bits (the host reports kErrBadLength and kErrBadPage as FA_ERR_INVALID_ARG,
 // any other non-zero value as FA_ERR_TIMEOUT).
 enum : int {
     kErrWaitTimeout = 1,       // an mbarrier wait ran out
     kErrSemaphoreTimeout = 2,  // a deterministic-order semaphore wait ran out
     kErrBadLength = 4,         // a varlen sequence longer than the maximum given, or
-                               // cu_seqlens[B] different from the packed total given
+                               // cu_seqlens[B] different from the packed total given;
+                               // a cached length outside the block table
+    kErrBadPage = 8,           // a block-table entry that is no page of the cache
 };
 
 __device__ __forceinline__ uint64_t globaltimer_ns() {
@@ -582,7 +584,9 @@ __device__ __forceinline__ float ex2(float x) {
 // 4 r (1 - r) for r = 1 / (1 + e): one exp2 per score and one reciprocal per
 // two, 1 / a = b / (a b).  z = 2 y log2(e) is held at 60, where r is below
 // 2^-59 and tanh rounds to 1, so that the product of two 1 + e stays finite;
-// NaN passes.  The error of 1 - 2 r is absolute, about 2^-22 (ex2 and rcp
+// NaN passes, to both scores of a pair: the forward passes pair keys of one
+// query and zero the hidden ones first, so that only a row that is NaN anyway
+// sees it.  The error of 1 - 2 r is absolute, about 2^-22 (ex2 and rcp
 // each within 2^-22 of their result, r <= 1), which is what a capped score of
 // softcap * tanh needs: tanh.approx, one instruction, is off by 2^-11.
 __device__ __forceinline__ float rcp_approx(float x) {

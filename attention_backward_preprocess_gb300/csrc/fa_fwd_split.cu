@@ -519,8 +519,12 @@ __global__ void __launch_bounds__(SplitCfg<kD, T>::kThreads, 1)
                         float p0, p1;
                         if (kCap) {
                             float r0, r1;
-                            cap_r2(__uint_as_float(sr[2 * i]) * p.cap_k, __uint_as_float(sr[2 * i + 1]) * p.cap_k, r0,
-                                   r1);
+                            float z0 = __uint_as_float(sr[2 * i]) * p.cap_k, z1 = __uint_as_float(sr[2 * i + 1]) * p.cap_k;
+                            if (kMask) {   // a hidden key's NaN stays out of the pair
+                                z0 = (e >= lo && e <= hi) ? z0 : 0.f;
+                                z1 = (e + 1 >= lo && e + 1 <= hi) ? z1 : 0.f;
+                            }
+                            cap_r2(z0, z1, r0, r1);
                             p0 = ex2(fmaf(-2.f * p.cap_log2, r0, p.cap_log2 - mref));
                             p1 = ex2(fmaf(-2.f * p.cap_log2, r1, p.cap_log2 - mref));
                         } else if (kExt) {

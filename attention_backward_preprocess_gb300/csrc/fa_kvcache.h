@@ -1,0 +1,57 @@
+// fa_kvcache.h -- parameter blocks of the 8-bit paged key / value cache.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+namespace fa {
+
+// The cache: e4m3 values, K as [page][kv head][token][d], V as [page][kv
+// head][d][token], one power-of-two scale per (page, kv head).
+struct KvCacheParams {
+    uint8_t *k, *v;
+    float *k_scale, *v_scale;
+    const int *table;      // [B, max_pages] page numbers
+    int num_pages, page, max_pages, Hkv;
+    int *err;              // device error word
+};
+
+struct KvAppendParams {
+    KvCacheParams c;
+    const int *len;        // [B] tokens held before the call
+    const int *cu;         // [B + 1] rows of the new tokens; null: max_new each
+    const void *k, *v;     // [rows, Hkv, D]
+    int B, max_new;
+};
+
+struct KvAttnParams {
+    KvCacheParams c;
+    const int *len;        // [B] tokens held, the queries' own among them
+    const void *q;         // [B, Sq, Hq, D]
+    void *o;
+    float *lse;            // [B, Hq, Sq]; null: not written
+    int B, Sq, Hq, G;
+    int groups;            // row groups of 16 (query, head) rows per kv head
+    int window;            // keys a query sees before its own; < 0: all
+    float scale_log2;      // c log2(e)
+    float cap_log2, cap_k; // softcap log2(e) and 2 log2(e) c / softcap; 0: no cap
+    // workspace: two pieces of up to 16 rows per worker
+    float *acc;            // [workers][2][16][D]
+    float4 *stat;          // [workers][2][16]  (m, l, R, -)
+    int4 *meta;            // [workers]  piece 0: segment, first worker, ends here, sequence
+    int workers;
+};
+
+// Workers of the attention kernel at most: warps of kKvSms CTAs.  The grid is
+// the device's SM count (152 on GB300), held at kKvSms.
+constexpr int kKvSms = 160;
+constexpr int kKvMaxSeqs = 4096;   // sequences whose tile counts fit shared memory
+int kv_warps(int D);               // warps per CTA
+size_t kv_workspace_bytes(int D);
+
+cudaError_t launch_kv_append(const KvAppendParams &p, int D, int bf16, cudaStream_t stream);
+cudaError_t launch_kv_attn(const KvAttnParams &p, int D, int bf16, int sms, cudaStream_t stream);
+
+}  // namespace fa

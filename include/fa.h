@@ -253,8 +253,9 @@ fa_status fa_fwd(const void *q, const void *k, const void *v, void *o, float *ls
  *   (FA_ERR_INVALID_ARG): they are part of the intervals.  Dense problems
  *   (FA_ERR_UNSUPPORTED with cu_seqlens), with softcap, used lengths and
  *   deterministic mode; not with the extensions and head dims named above.
- *   Keys and values of masked tokens must be finite, as for every mask of
- *   this library: a masked entry has P = 0, and 0 times their value is added. */
+ *   Values (forward), and queries, keys, values and dout (backward) of masked
+ *   tokens must be finite, as for every mask of this library: a masked entry
+ *   has P = dS = 0, and 0 times their value is added. */
 typedef struct {
     int window_left;
     int window_right;
@@ -322,6 +323,67 @@ fa_status fa_bwd_ext(const void *q, const void *k, const void *v, const void *o,
                      const int *cu_seqlens_q, const int *cu_seqlens_k, const fa_ext *ext,
                      int deterministic, fa_dtype dtype, void *workspace, size_t workspace_bytes,
                      cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The 8-bit paged key / value cache: what a model answers from.  Tokens live
+ * in pages of page_size (a multiple of 16, at most 128); block_table[b *
+ * max_pages + i] is the page that holds tokens [i page_size, (i + 1)
+ * page_size) of sequence b.  Values are e4m3 (4-bit exponent, 3-bit fraction,
+ * largest magnitude 448) times one scale per (page, kv head):
+ *   k        [num_pages, Hkv, page_size, D]   16-byte aligned
+ *   v        [num_pages, Hkv, D, page_size]   16-byte aligned
+ *   k_scale, v_scale   fp32 [num_pages, Hkv]
+ * D is 64 or 128.  The caller owns everything; both calls read block_table and
+ * the lengths on the device, need no host copy, and can be captured into a
+ * CUDA graph.  Table entries past a sequence's tokens are not read.
+ *
+ * fa_kvcache_append writes the new tokens of B sequences behind the
+ * cache_len[b] tokens (device int32 [B]) they hold.  k_new / v_new: [rows,
+ * Hkv, D], 16-bit; sequence b's are rows cu_new[b] .. cu_new[b + 1] (device
+ * int32 [B + 1]), at most max_new, or with cu_new NULL rows b * max_new ..
+ * (b + 1) * max_new.  Per (page, head) the scale becomes 2^e, the smallest e
+ * in [-120, 120] with max |new value| <= 448 * 2^e, or stays the larger one a
+ * page that already held tokens of the sequence has; if it grows, those are
+ * moved to it (rounded again to nearest even).  What a page held before its
+ * first token is ignored.  NaN is stored as NaN, an infinity as +-448 scale.
+ * A page written by the call must belong to one sequence.
+ *
+ * fa_fwd_kvcache: attention of the last Sq tokens of each sequence (their own
+ * keys and values already appended) over the cache.  q, o: [B, Sq, Hq, D],
+ * lse (NULL: not written): fp32 [B, Hq, Sq]; cache_len[b] counts the Sq tokens
+ * too.  Query i sits at position p = cache_len[b] - Sq + i and sees the keys
+ * j <= p, with window_left >= 0 also j >= p - window_left; a query that sees
+ * none gives O = 0, LSE = -inf.  softcap as in fa_ext.  Pages wholly before
+ * every query's window are not read.  workspace:
+ * fa_fwd_kvcache_workspace_bytes(D) bytes, 256-byte aligned, no
+ * initialisation; calls that overlap need one each.  Results do not depend on
+ * anything but the arguments and the GPU (no atomics).
+ *
+ * Errors: FA_ERR_INVALID_ARG for null or misaligned pointers, sizes, scale,
+ * softcap or window; FA_ERR_UNSUPPORTED for D, page_size, dtype, more than
+ * 4096 sequences (fa_fwd_kvcache) or heads times tokens beyond 2^24.  A length
+ * outside [0, max_pages page_size], more new tokens than max_new, or a table
+ * entry that is no page is found on the device: such a sequence (or page) is
+ * neither read nor written, its attention output is 0 / -inf (a bad page's
+ * tokens count as zero keys and values), and fa_device_status(NULL, ...)
+ * returns FA_ERR_INVALID_ARG.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    const int *block_table;
+    int num_pages, page_size, max_pages, Hkv, D;
+} fa_kv_cache;
+
+fa_status fa_kvcache_append(const fa_kv_cache *cache, const int *cache_len, const void *k_new,
+                            const void *v_new, const int *cu_new, int B, int max_new,
+                            fa_dtype dtype, cudaStream_t stream);
+
+size_t fa_fwd_kvcache_workspace_bytes(int D);
+fa_status fa_fwd_kvcache(const void *q, const fa_kv_cache *cache, const int *cache_len, void *o,
+                         float *lse, int B, int Sq, int Hq, float softmax_scale, float softcap,
+                         int window_left, fa_dtype dtype, void *workspace, size_t workspace_bytes,
+                         cudaStream_t stream);
 
 /* CUDA graphs.  A backward call that issues only launches and memsets on
  * `stream` can be captured into a CUDA graph and replayed: fa_bwd_ext /

@@ -364,20 +364,31 @@ def test_training_step_in_a_graph(fa, cuda_device):
 
 
 @pytest.mark.gpu
-def test_nan_scores_stay_nan(fa, cuda_device):
-    """A NaN query row gives a NaN output row under a cap; its neighbours and a
-    masked NaN key's readers do not change."""
-    q, k, v, _ = (t.cuda() for t in _inputs(1, 200, 200, 2, 2, 128, BF, 51))
-    want, _ = fa.fa_fwd(q, k, v, causal=True, softcap=30.0)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [149, 150])
+def test_nan_scores_stay_nan(fa, cuda_device, D, bad):
+    """A NaN query row gives NaN output and gradient rows under a cap; other
+    rows, and rows that do not see a NaN key (next to their last one, an
+    even and an odd one), give what they gave."""
+    q, k, v, g = (t.cuda() for t in _inputs(1, 200, 200, 2, 2, D, BF, 51))
+    kw = dict(causal=True, softcap=30.0)
+    want, wl = fa.fa_fwd(q, k, v, **kw)
+    dq, _, _ = fa.fa_bwd(q, k, v, want, g, wl, deterministic=True, **kw)
     q2, k2 = q.clone(), k.clone()
     q2[0, 77, 1] = float("nan")
-    k2[0, 150, 0] = float("nan")
-    got, lse = fa.fa_fwd(q2, k2, v, causal=True, softcap=30.0)
+    k2[0, bad, 0] = float("nan")
+    got, lse = fa.fa_fwd(q2, k2, v, **kw)
     assert torch.isnan(got[0, 77, 1]).all() and torch.isnan(lse[0, 1, 77])
-    assert torch.isnan(got[0, 150:, 0]).all()
-    assert torch.equal(got[0, :150, 0], want[0, :150, 0])
+    assert torch.isnan(got[0, bad:, 0]).all()
+    assert torch.equal(got[0, :bad, 0], want[0, :bad, 0])
     rest = [i for i in range(200) if i != 77]
     assert torch.equal(got[0, rest, 1], want[0, rest, 1])
+    # in the backward dK and dV of the head are NaN then; dQ of the row, and of
+    # the one it shares a reciprocal with
+    dq2, _, _ = fa.fa_bwd(q2, k, v, want, g, wl, deterministic=True, **kw)
+    assert torch.isnan(dq2[0, 77, 1]).all()
+    rest = [i for i in rest if i != 76]
+    assert torch.equal(dq2[0, :, 0], dq[0, :, 0]) and torch.equal(dq2[0, rest, 1], dq[0, rest, 1])
 
 
 @pytest.mark.gpu
