@@ -62,7 +62,8 @@ class FaExt(ctypes.Structure):
                 ("dropout_mask", ctypes.c_void_p), ("total_q", ctypes.c_longlong),
                 ("total_k", ctypes.c_longlong), ("head_dim_v", ctypes.c_int),
                 ("softcap", ctypes.c_float), ("mask_ranges", ctypes.c_void_p),
-                ("mask_ranges_bytes", ctypes.c_size_t)]
+                ("mask_ranges_bytes", ctypes.c_size_t)] + [
+                    (n + "_stride", ctypes.c_longlong * 3) for n in ("q", "k", "v", "o", "dout")]
 
 
 def dropout_mask_shape(q, k, cu_seqlens_q=None, max_seqlen_k=None):
@@ -77,7 +78,7 @@ def dropout_mask_shape(q, k, cu_seqlens_q=None, max_seqlen_k=None):
 
 def _ext(Hq, window=None, alibi_slopes=None, seqused_q=None, seqused_k=None, bias=None,
          dbias=None, dropout=None, totals=None, head_dim_v=0, softcap=0.0, mask_ranges=None,
-         sizes=None):
+         sizes=None, strides=None):
     """A pointer to an FaExt, or None when no extension is asked for.
 
     ``bias``: [B or 1, Hq or 1, Sq, >= Sk] in the input dtype, last axis
@@ -90,12 +91,16 @@ def _ext(Hq, window=None, alibi_slopes=None, seqused_q=None, seqused_k=None, bia
     so that the library need not read them back (no stream synchronisation).
     ``head_dim_v``: the value head dim when it differs from q's (else 0).
     ``softcap``: scores become softcap * tanh(score / softcap) (0: none).
-    ``mask_ranges``: a MaskRanges of the call's ``sizes`` (B, Sq, Sk)."""
+    ``mask_ranges``: a MaskRanges of the call's ``sizes`` (B, Sq, Sk).
+    ``strides``: what ``_inputs`` said of inputs that are not contiguous."""
     if (window is None and alibi_slopes is None and seqused_q is None and seqused_k is None
             and bias is None and dbias is None and dropout is None and totals is None
-            and not head_dim_v and softcap == 0.0 and mask_ranges is None):
+            and not head_dim_v and softcap == 0.0 and mask_ranges is None and not strides):
         return None
-    e = FaExt(-1, -1, None, 0, None, None, None, 0, 0, 0, None, 0.0, 0, 0, None, 0, 0, 0)
+    e = FaExt(-1, -1)   # the rest 0
+    if strides:
+        for name, s in strides.items():
+            setattr(e, name + "_stride", s)
     e.softcap = float(softcap)
     if mask_ranges is not None:
         if not isinstance(mask_ranges, MaskRanges) or sizes != (mask_ranges.B, mask_ranges.S, mask_ranges.S):
@@ -154,26 +159,25 @@ class KvCache:
     copies nothing."""
 
     def __init__(self, k, v, k_scale, v_scale, block_table):
-        if k.dim() != 4 or tuple(v.shape) != (k.shape[0], k.shape[1], k.shape[3], k.shape[2]):
-            raise ValueError("k: [pages, Hkv, page, D], v: [pages, Hkv, D, page]")
-        for name, t, dt, shape in (("k", k, torch.float8_e4m3fn, None), ("v", v, torch.float8_e4m3fn, None),
-                                   ("k_scale", k_scale, torch.float32, tuple(k.shape[:2])),
-                                   ("v_scale", v_scale, torch.float32, tuple(k.shape[:2])),
-                                   ("block_table", block_table, torch.int32, None)):
-            if t.dtype != dt or not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
-                raise ValueError("%s: contiguous %s%s" % (name, dt, "" if shape is None else " %r" % (shape,)))
-            _same_device(k.device, t, name)
-        if block_table.dim() != 2:
-            raise ValueError("block_table: [B, max_pages]")
+        if k.dim() != 4 or block_table.dim() != 2:
+            raise ValueError("k: [pages, Hkv, page, D], block_table: [B, max_pages]")
+        P, H, ps, D = k.shape
+        self.B = block_table.shape[0]
+        self.device = k.get_device()   # index, -1: not on a GPU
+        for name, t, dt, shape in (("k", k, torch.float8_e4m3fn, (P, H, ps, D)),
+                                   ("v", v, torch.float8_e4m3fn, (P, H, D, ps)),
+                                   ("k_scale", k_scale, torch.float32, (P, H)),
+                                   ("v_scale", v_scale, torch.float32, (P, H)),
+                                   ("block_table", block_table, torch.int32, block_table.shape)):
+            self._check(name, t, dt, shape)
         self.k, self.v, self.k_scale, self.v_scale, self.block_table = k, v, k_scale, v_scale, block_table
         self._c = _KvCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                                 block_table.data_ptr(), k.shape[0], k.shape[2], block_table.shape[1], k.shape[1],
-                                 k.shape[3])
+                                 block_table.data_ptr(), P, ps, block_table.shape[1], H, D)
 
-    def _lengths(self, name, t, n):
-        if t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != (n,):
-            raise ValueError("%s: contiguous int32 [%d]" % (name, n))
-        _same_device(self.k.device, t, name)
+    def _check(self, name, t, dtype, shape):
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != self.device \
+                or self.device < 0:
+            raise ValueError("%s: contiguous %s %r on the cache's GPU" % (name, dtype, tuple(shape)))
 
 
 def kvcache_append(cache, cache_len, k_new, v_new, cu_new=None, max_new=None, stream=None):
@@ -183,27 +187,26 @@ def kvcache_append(cache, cache_len, k_new, v_new, cu_new=None, max_new=None, st
     ``k_new`` / ``v_new``: [B, T, Hkv, D], or [total, Hkv, D] with ``cu_new``
     (int32 [B + 1] prefix sums) and ``max_new``, the most tokens of one
     sequence.  The cache's tensors are updated in place."""
-    B = cache.block_table.shape[0]
-    cache._lengths("cache_len", cache_len, B)
+    B, c = cache.B, cache._c
+    cache._check("cache_len", cache_len, torch.int32, (B,))
     if cu_new is None:
-        if k_new.dim() != 4 or k_new.shape[0] != B:
+        if k_new.dim() != 4:
             raise ValueError("k_new: [B, T, Hkv, D]")
         max_new = k_new.shape[1]
+        shape = (B, max_new, c.Hkv, c.D)
     else:
-        cache._lengths("cu_new", cu_new, B + 1)
-        if k_new.dim() != 3 or max_new is None:
-            raise ValueError("k_new: [total, Hkv, D], with max_new")
-    if k_new.shape != v_new.shape or tuple(k_new.shape[-2:]) != (cache._c.Hkv, cache._c.D):
-        raise ValueError("k_new / v_new: the cache's heads and head dim")
-    if k_new.dtype != v_new.dtype:
-        raise ValueError("k_new / v_new: one dtype")
-    for name, t in (("k_new", k_new), ("v_new", v_new)):
-        _same_device(cache.k.device, t, name)
-    k_new, v_new = _dense(stream, k_new=k_new, v_new=v_new)
-    with torch.cuda.device(cache.k.device):
-        _check(lib().fa_kvcache_append(ctypes.byref(cache._c), _ptr(cache_len), _ptr(k_new), _ptr(v_new),
-                                       _ptr(cu_new), B, int(max_new), _dtype_code(k_new), _stream(stream)),
-               "fa_kvcache_append")
+        cache._check("cu_new", cu_new, torch.int32, (B + 1,))
+        if max_new is None:
+            raise ValueError("max_new: the most new tokens of one sequence")
+        shape = (k_new.shape[0], c.Hkv, c.D)
+    code = _dtype_code(k_new)
+    if not (k_new.is_contiguous() and v_new.is_contiguous()):
+        k_new, v_new = _dense(stream, k_new=k_new, v_new=v_new)
+    cache._check("k_new", k_new, k_new.dtype, shape)
+    cache._check("v_new", v_new, k_new.dtype, shape)
+    with _on(cache.device):
+        _check(lib().fa_kvcache_append(ctypes.byref(c), cache_len.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+                                       _ptr(cu_new), B, int(max_new), code, _stream(stream)), "fa_kvcache_append")
 
 
 def fa_fwd_kvcache(q, cache, cache_len, softmax_scale=None, softcap=0.0, window_left=-1, workspace=None,
@@ -214,26 +217,27 @@ def fa_fwd_kvcache(q, cache, cache_len, softmax_scale=None, softcap=0.0, window_
     (int32 [B]) counts them.  ``workspace``: a uint8 CUDA tensor of
     ``fa_fwd_kvcache_workspace_bytes(D)`` (allocated when not given); ``out``:
     (o, lse) to write into.  See fa_fwd_kvcache in include/fa.h."""
-    if q.dim() != 4 or q.shape[0] != cache.block_table.shape[0] or q.shape[3] != cache._c.D:
-        raise ValueError("q: [B, Sq, Hq, D] of the cache's B and D")
+    c = cache._c
+    if q.dim() != 4:
+        raise ValueError("q: [B, Sq, Hq, D]")
     B, Sq, Hq, D = q.shape
-    cache._lengths("cache_len", cache_len, B)
-    _same_device(cache.k.device, q, "q")
+    if not q.is_contiguous():
+        (q,) = _dense(stream, q=q)
+    code = _dtype_code(q)
+    cache._check("q", q, q.dtype, (cache.B, Sq, Hq, c.D))
+    cache._check("cache_len", cache_len, torch.int32, (B,))
     scale = default_scale(D) if softmax_scale is None else float(softmax_scale)
-    (q,) = _dense(stream, q=q)
-    with torch.cuda.device(cache.k.device):
+    with _on(cache.device):
         if out is None:
-            out = torch.empty_like(q), torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
+            out = torch.empty_like(q), q.new_empty((B, Hq, Sq), dtype=torch.float32)
         else:
-            _outputs(o=out[0], lse=out[1])
-            if out[0].shape != q.shape or out[0].dtype != q.dtype or tuple(out[1].shape) != (B, Hq, Sq) \
-                    or out[1].dtype != torch.float32:
-                raise ValueError("out: (o like q, float32 lse [B, Hq, Sq])")
+            cache._check("out[0]", out[0], q.dtype, q.shape)
+            cache._check("out[1]", out[1], torch.float32, (B, Hq, Sq))
         if workspace is None:
-            workspace = torch.empty(fa_fwd_kvcache_workspace_bytes(D), dtype=torch.uint8, device=q.device)
-        _check(lib().fa_fwd_kvcache(_ptr(q), ctypes.byref(cache._c), _ptr(cache_len), _ptr(out[0]), _ptr(out[1]), B,
-                                    Sq, Hq, scale, float(softcap), int(window_left), _dtype_code(q),
-                                    _ptr(workspace), workspace.numel(), _stream(stream)), "fa_fwd_kvcache")
+            workspace = q.new_empty(fa_fwd_kvcache_workspace_bytes(D), dtype=torch.uint8)
+        _check(lib().fa_fwd_kvcache(q.data_ptr(), ctypes.byref(c), cache_len.data_ptr(), out[0].data_ptr(),
+                                    out[1].data_ptr(), B, Sq, Hq, scale, softcap, window_left, code,
+                                    workspace.data_ptr(), workspace.numel(), _stream(stream)), "fa_fwd_kvcache")
     return out
 
 
@@ -242,11 +246,20 @@ def fa_fwd_kvcache_workspace_bytes(D) -> int:
     return int(lib().fa_fwd_kvcache_workspace_bytes(int(D)))
 
 
-def _same_device(device, t, name):
-    """Raises unless ``t`` is on ``device`` (None, or one without an index: any CUDA device)."""
-    d = None if device is None else torch.device(device)
-    if not t.is_cuda or (d is not None and (d.type != "cuda" or d.index not in (None, t.device.index))):
-        raise ValueError(name + ": on another device")
+class _Here:
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def _on(index):
+    """A context in which GPU ``index`` (None: the current one) is current."""
+    return _HERE if index is None or index == torch._C._cuda_getDevice() else torch.cuda.device(index)
 
 
 class MaskRanges:
@@ -269,36 +282,46 @@ def mask_ranges(B, S, doc_ids=None, prefix_len=None, causal=True, window=None, d
     leading tokens every row of the document sees; with ``causal`` and without
     a window only.  ``window=(left, right)``, -1 = unbounded.  ``out``: a
     MaskRanges of the same B and S to fill again (a captured graph's)."""
-    B, S = int(B), int(S)
-    for name, t in (("doc_ids", doc_ids), ("prefix_len", prefix_len)):
-        if t is not None:
-            if t.dtype != torch.int32 or not t.is_contiguous() or not t.is_cuda:
-                raise ValueError(name + ": a contiguous int32 CUDA tensor")
-            if tuple(t.shape) != (B, S) and not (name == "prefix_len" and tuple(t.shape) == (B,)):
-                raise ValueError(name + ": [B, S]" + (" or [B]" if name == "prefix_len" else ""))
-            _same_device(device, t, name)
-            device = t.device
+    at = None if device is None else torch.device(device).index   # None: the current GPU
     if out is not None:
         if not isinstance(out, MaskRanges) or (out.B, out.S) != (B, S):
             raise ValueError("out: a MaskRanges of the same B and S")
-        _same_device(device, out.buffer, "out")
-        device = out.buffer.device
+        at = _ranges_device(at, "out", out.buffer)
+    if doc_ids is not None:
+        at = _ranges_device(at, "doc_ids", doc_ids)
+        if doc_ids.dtype != torch.int32 or doc_ids.shape != (B, S):
+            raise ValueError("doc_ids: int32 [B, S]")
+    if prefix_len is not None:
+        at = _ranges_device(at, "prefix_len", prefix_len)
+        if prefix_len.dtype != torch.int32 or (prefix_len.shape != (B, S) and prefix_len.shape != (B,)):
+            raise ValueError("prefix_len: int32 [B] or [B, S]")
     wl, wr = (-1, -1) if window is None else (int(window[0]), int(window[1]))
-    need = int(lib().fa_mask_ranges_bytes(B, S))
+    L = lib()
+    need = L.fa_mask_ranges_bytes(B, S)
     if need == 0:
         raise FaError(FA_ERR_INVALID_ARG, "fa_mask_ranges")
-    with torch.cuda.device(device):   # None: the current device
+    with _on(at):
         if out is None:
             out = MaskRanges(torch.empty(need, dtype=torch.uint8, device="cuda"), B, S)
-        per_token = prefix_len is not None and prefix_len.dim() == 2
-        _check(lib().fa_mask_ranges(_ptr(doc_ids), _ptr(prefix_len), int(per_token), B, S, int(bool(causal)), wl,
-                                    wr, _ptr(out.buffer), out.buffer.numel(), _stream(stream)), "fa_mask_ranges")
+        per_token = 1 if prefix_len is not None and prefix_len.dim() == 2 else 0
+        _check(L.fa_mask_ranges(_ptr(doc_ids), _ptr(prefix_len), per_token, B, S, 1 if causal else 0, wl, wr,
+                                out.buffer.data_ptr(), out.buffer.numel(), _stream(stream)), "fa_mask_ranges")
     return out
+
+
+def _ranges_device(at, name, t):
+    """The GPU of one of mask_ranges' tensors, which is ``at`` when that is known."""
+    d = t.get_device()
+    if d < 0 or not t.is_contiguous() or (at is not None and at != d):
+        raise ValueError(name + ": a contiguous CUDA tensor, all on one GPU")
+    return d
 
 
 def lib():
     """The loaded library; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -367,12 +390,14 @@ def _check(status: int, what: str):
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current stream's handle itself: building torch's stream object
+        # took 2.8 of a decoding step's 27 us on the host
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -402,10 +427,32 @@ def _value_dim(D, v) -> int:
     return 0 if v.shape[-1] == D else int(v.shape[-1])
 
 
+def _inputs(stream, **tensors):
+    """The named inputs as the library can read them, and {name: (batch, row,
+    head) element strides} of those that are not contiguous.  The tensor loads
+    take any strides that are multiples of 16 bytes; a tensor that lies
+    otherwise is copied on the current stream -- with another ``stream`` the
+    copy and the call would not be in order, so that is refused."""
+    out, strides = [], {}
+    for name, t in tensors.items():
+        if not t.is_contiguous():
+            st = t.stride()
+            st = ((0,) if t.dim() == 3 else ()) + st
+            # an axis of one entry may carry any stride: a step of 8 serves
+            size = ((1,) if t.dim() == 3 else ()) + tuple(t.shape)
+            use = [8 if n == 1 else x for n, x in zip(size[:3], st[:3])]
+            if t.dim() in (3, 4) and st[3] == 1 and all(0 < x < 1 << 39 and x % 8 == 0 for x in use) \
+                    and t.data_ptr() % 16 == 0:
+                strides[name] = tuple(use)
+            else:
+                t = _dense(stream, **{name: t})[0]
+        out.append(t)
+    return out, strides
+
+
 def _dense(stream, **tensors):
-    """The named tensors, each contiguous: the library reads them as they lie.
-    One that is not is copied on the current stream; with another ``stream``
-    the copy and the call would not be in order, so that is refused."""
+    """The named tensors, each contiguous: copied on the current stream where
+    they are not, refused where the call goes to another ``stream``."""
     out = []
     for name, t in tensors.items():
         if not t.is_contiguous():
@@ -414,6 +461,11 @@ def _dense(stream, **tensors):
             t = t.contiguous()
         out.append(t)
     return out
+
+
+def _like(t):
+    """A new contiguous tensor of t's shape, dtype and device."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _outputs(**tensors):
@@ -441,7 +493,7 @@ def fa_fwd(q, k, v, causal=False, softmax_scale=None, cu_seqlens_q=None, cu_seql
     caps the scores, softcap * tanh(score / softcap); ``mask_ranges`` (from the
     function of that name) takes the place of ``causal`` and ``window``.
     """
-    q, k, v = _dense(stream, q=q, k=k, v=v)
+    (q, k, v), strides = _inputs(stream, q=q, k=k, v=v)
     B, Sq, Sk, Hq, Hkv, D = _shape(q, k, cu_seqlens_q, max_seqlen_q, max_seqlen_k)
     scale = default_scale(D) if softmax_scale is None else float(softmax_scale)
     o = torch.empty(q.shape[:-1] + (v.shape[-1],), dtype=q.dtype, device=q.device)
@@ -451,7 +503,7 @@ def fa_fwd(q, k, v, causal=False, softmax_scale=None, cu_seqlens_q=None, cu_seql
         lse = torch.empty((Hq, q.shape[0]), dtype=torch.float32, device=q.device)
     ext = _ext(Hq, window, alibi_slopes, seqused_q, seqused_k, bias, dropout=dropout,
                totals=totals, head_dim_v=_value_dim(D, v), softcap=softcap, mask_ranges=mask_ranges,
-               sizes=(B, Sq, Sk))
+               sizes=(B, Sq, Sk), strides=strides)
     args = [_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Sq, Sk, Hq, Hkv, D, scale,
             int(bool(causal)), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k)]
     if ext is None:
@@ -476,18 +528,17 @@ def fa_bwd(q, k, v, o, dout, lse, causal=False, softmax_scale=None, cu_seqlens_q
     packed row counts, which spare the stream synchronisation of reading them
     back).  ``softcap`` and ``mask_ranges`` as the forward had them.
     """
-    q, k, v, o, dout, lse = _dense(stream, q=q, k=k, v=v, o=o, dout=dout, lse=lse)
+    (q, k, v, o, dout), strides = _inputs(stream, q=q, k=k, v=v, o=o, dout=dout)
+    (lse,) = _dense(stream, lse=lse)
     _outputs(dq=dq, dk=dk, dv=dv)
     B, Sq, Sk, Hq, Hkv, D = _shape(q, k, cu_seqlens_q, max_seqlen_q, max_seqlen_k)
     scale = default_scale(D) if softmax_scale is None else float(softmax_scale)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq, dk, dv = (_like(t) if g is None else g for t, g in ((q, dq), (k, dk), (v, dv)))
     args = [_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk),
             _ptr(dv), B, Sq, Sk, Hq, Hkv, D, scale, int(bool(causal)), _ptr(cu_seqlens_q),
             _ptr(cu_seqlens_k), int(bool(deterministic)), _dtype_code(q)]
     ext = _ext(Hq, window, alibi_slopes, seqused_q, seqused_k, bias, dbias, dropout, totals,
-               _value_dim(D, v), softcap, mask_ranges, (B, Sq, Sk))
+               _value_dim(D, v), softcap, mask_ranges, (B, Sq, Sk), strides)
     if ext is not None:
         st = lib().fa_bwd_ext(*args[:19], ext, *args[19:], _ptr(workspace),
                               0 if workspace is None else workspace.numel(), _stream(stream))
@@ -566,9 +617,7 @@ def fa_bwd_stages(q, k, v, o, dout, lse, workspace, causal=False, softmax_scale=
     _outputs(q=q, k=k, v=v, o=o, dout=dout, lse=lse, dq=dq, dk=dk, dv=dv)
     B, Sq, Sk, Hq, Hkv, D = _shape(q, k, cu_seqlens_q, max_seqlen_q, max_seqlen_k)
     scale = default_scale(D) if softmax_scale is None else float(softmax_scale)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq, dk, dv = (_like(t) if g is None else g for t, g in ((q, dq), (k, dk), (v, dv)))
     shape = [B, Sq, Sk, Hq, Hkv, D]
     ext = _ext(Hq, window, totals=totals, softcap=softcap, mask_ranges=mask_ranges, sizes=(B, Sq, Sk))
     if ext is not None:

@@ -161,15 +161,15 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// 4-D map over a [batch, rows, heads, D] 16-bit tensor (d innermost), box of
-// 64 d x 1 head x box_rows rows, 128-byte swizzle, zero fill out of bounds.
+// 4-D map over a [batch, rows, heads, D] 16-bit tensor (d innermost; strides
+// st in elements: batch, row, head), box of 64 d x 1 head x box_rows rows,
+// 128-byte swizzle, zero fill out of bounds.
 bool encode_rows_map(CUtensorMap *m, const void *base, int D, int H, long long rows, int batch,
-                     int box_rows, int bf16) {
+                     int box_rows, int bf16, const long long (&st)[3]) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)rows, (cuuint64_t)batch};
-    const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2,
-                                   (cuuint64_t)rows * H * D * 2};
+    const cuuint64_t strides[3] = {(cuuint64_t)st[2] * 2, (cuuint64_t)st[1] * 2, (cuuint64_t)st[0] * 2};
     const cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
@@ -256,6 +256,32 @@ fa_status check_ext_totals(const fa_ext *ext, bool varlen, int B, int Sq, int Sk
     if (!varlen || ext->total_q <= 0 || ext->total_k <= 0) return FA_ERR_INVALID_ARG;
     if (ext->total_q > (long long)B * Sq || ext->total_k > (long long)B * Sk) return FA_ERR_INVALID_ARG;
     return FA_OK;
+}
+
+// Strides of a [batch, rows, H, D] tensor: the caller's (all zero: contiguous),
+// else contiguous.  A packed varlen tensor has no batch stride.
+fa_status set_strides(long long (&dst)[3], const long long *given, int varlen, long long rows, int H, int D) {
+    dst[2] = D;
+    dst[1] = (long long)H * D;
+    dst[0] = rows * H * D;
+    if (!given || (given[0] == 0 && given[1] == 0 && given[2] == 0)) return FA_OK;
+    for (int i = varlen ? 1 : 0; i < 3; ++i) {
+        // the tensor maps' terms: multiples of 16 bytes below 2^40 bytes
+        if (given[i] <= 0 || (given[i] & 7) || given[i] >= (1LL << 39)) return FA_ERR_INVALID_ARG;
+        dst[i] = given[i];
+    }
+    return FA_OK;
+}
+
+// The strides of q, k, v, o and dout, once the head dims and lengths are known
+// (rq / rk: rows of the query and key side of one batch entry).
+fa_status apply_strides(fa::BwdParams &p, const fa_ext *ext, long long rq, long long rk) {
+    fa_status st;
+    if ((st = set_strides(p.sq, ext ? ext->q_stride : nullptr, p.varlen, rq, p.Hq, p.Dh)) != FA_OK) return st;
+    if ((st = set_strides(p.sk, ext ? ext->k_stride : nullptr, p.varlen, rk, p.Hkv, p.Dh)) != FA_OK) return st;
+    if ((st = set_strides(p.sv, ext ? ext->v_stride : nullptr, p.varlen, rk, p.Hkv, p.Dhv)) != FA_OK) return st;
+    if ((st = set_strides(p.so, ext ? ext->o_stride : nullptr, p.varlen, rq, p.Hq, p.Dhv)) != FA_OK) return st;
+    return set_strides(p.sdo, ext ? ext->dout_stride : nullptr, p.varlen, rq, p.Hq, p.Dhv);
 }
 
 struct Prepared {
@@ -406,6 +432,7 @@ fa_status prepare(const void *q, const void *k, const void *v, const void *o, co
     // the extensions are host arguments too: checked before the device is
     if ((st = apply_ext(p, causal, ext)) != FA_OK) return st;
     if ((st = check_ext_totals(ext, cu_q != nullptr, B, Sq, Sk)) != FA_OK) return st;
+    if ((st = apply_strides(p, ext, Sq, Sk)) != FA_OK) return st;   // (before any launch)
     // the wide kernel adds dQ without the deterministic order
     if (deterministic && wide_dims(p.Dh, p.Dhv)) return FA_ERR_UNSUPPORTED;
     st = check_device();
@@ -415,6 +442,7 @@ fa_status prepare(const void *q, const void *k, const void *v, const void *o, co
         if ((st = packed_totals(ext, cu_q, cu_k, B, Sq, Sk, stream, &tq, &tk)) != FA_OK) return st;
         p.total_q = tq;
         p.total_k = tk;
+        if ((st = apply_strides(p, ext, tq, tk)) != FA_OK) return st;
     }
     p.err = reinterpret_cast<int *>(w + L.err);
     p.ntiles = reinterpret_cast<int *>(w + L.ntiles);
@@ -485,10 +513,10 @@ fa_status run_main(const Prepared &P, fa_dtype dtype, cudaStream_t stream) {
     const int nb = p.varlen ? 1 : p.B;
     if (rq <= 0 || rk <= 0) return FA_ERR_INVALID_ARG;
     if (!p.q || !p.k || !p.v || !p.dout || !p.dk || !p.dv) return FA_ERR_INVALID_ARG;
-    if (!encode_rows_map(&mq, p.q, p.Dh, p.Hq, rq, nb, bm, bf16) ||
-        !encode_rows_map(&mdo, p.dout, p.Dhv, p.Hq, rq, nb, bm, bf16) ||
-        !encode_rows_map(&mk, p.k, p.Dh, p.Hkv, rk, nb, fa::kBlockN, bf16) ||
-        !encode_rows_map(&mv, p.v, p.Dhv, p.Hkv, rk, nb, fa::kBlockN, bf16))
+    if (!encode_rows_map(&mq, p.q, p.Dh, p.Hq, rq, nb, bm, bf16, p.sq) ||
+        !encode_rows_map(&mdo, p.dout, p.Dhv, p.Hq, rq, nb, bm, bf16, p.sdo) ||
+        !encode_rows_map(&mk, p.k, p.Dh, p.Hkv, rk, nb, fa::kBlockN, bf16, p.sk) ||
+        !encode_rows_map(&mv, p.v, p.Dhv, p.Hkv, rk, nb, fa::kBlockN, bf16, p.sv))
         return FA_ERR_CUDA;
     if (p.varlen) {
         // the unit list depends on the device-resident cu_seqlens
@@ -502,8 +530,11 @@ fa_status run_main(const Prepared &P, fa_dtype dtype, cudaStream_t stream) {
     }
     // dK / dV leave the main kernel through tensor stores of the same geometry as K / V
     CUtensorMap mdk, mdv;
-    if (!encode_rows_map(&mdk, p.dk, p.Dh, p.Hkv, rk, nb, fa::kBlockN, bf16) ||
-        !encode_rows_map(&mdv, p.dv, p.Dhv, p.Hkv, rk, nb, fa::kBlockN, bf16))
+    long long sdk[3], sdv[3];   // the outputs are contiguous
+    set_strides(sdk, nullptr, p.varlen, rk, p.Hkv, p.Dh);
+    set_strides(sdv, nullptr, p.varlen, rk, p.Hkv, p.Dhv);
+    if (!encode_rows_map(&mdk, p.dk, p.Dh, p.Hkv, rk, nb, fa::kBlockN, bf16, sdk) ||
+        !encode_rows_map(&mdv, p.dv, p.Dhv, p.Hkv, rk, nb, fa::kBlockN, bf16, sdv))
         return FA_ERR_CUDA;
     const int grid = (int)std::min<long long>(p.max_tiles, sm_count());
     return cuda_status(fa::launch_bwd_main(p, mq, mk, mv, mdo, mdk, mdv, bf16, grid, stream));
@@ -880,6 +911,7 @@ fa_status fa_fwd_ext(const void *q, const void *k, const void *v, void *o, float
     p.cu_k = cu_seqlens_k;
     if ((st = apply_ext(p, causal, ext)) != FA_OK) return st;
     if ((st = check_ext_totals(ext, p.varlen, B, Sq, Sk)) != FA_OK) return st;
+    if ((st = apply_strides(p, ext, Sq, Sk)) != FA_OK) return st;
     if ((st = check_device()) != FA_OK) return st;
     p.err = fa::fwd_error_word();
     if (!p.err) return FA_ERR_CUDA;
@@ -894,13 +926,14 @@ fa_status fa_fwd_ext(const void *q, const void *k, const void *v, void *o, float
     }
     // a map needs at least one row; with no keys at all no K/V tile is loaded
     rk = std::max<long long>(rk, 1);
+    if (p.varlen && (st = apply_strides(p, ext, rq, rk)) != FA_OK) return st;
     const int bf16 = dtype == FA_BF16;
     const int nb = p.varlen ? 1 : B;
     CUtensorMap mq, mk, mv;
     const int bn = fa::fwd_block_n(p.D, p.Dv);
-    if (!encode_rows_map(&mq, q, D, Hq, rq, nb, fa::fwd_block_m(), bf16) ||
-        !encode_rows_map(&mk, k, D, Hkv, rk, nb, bn, bf16) ||
-        !encode_rows_map(&mv, v, p.Dhv, Hkv, rk, nb, bn, bf16))
+    if (!encode_rows_map(&mq, q, D, Hq, rq, nb, fa::fwd_block_m(), bf16, p.sq) ||
+        !encode_rows_map(&mk, k, D, Hkv, rk, nb, bn, bf16, p.sk) ||
+        !encode_rows_map(&mv, v, p.Dhv, Hkv, rk, nb, bn, bf16, p.sv))
         return FA_ERR_CUDA;
     return cuda_status(fa::launch_fwd_tc(p, mq, mk, mv, o, lse, Sq, bf16, stream));
 }

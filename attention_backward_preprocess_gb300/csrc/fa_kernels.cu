@@ -172,6 +172,9 @@ __global__ void __launch_bounds__(256) preprocess_kernel(BwdParams p) {
     const int part = (int)(gid % TPR);
     const long long qbase = p.varlen ? (long long)p.cu_q[b] : (long long)b * p.Sq;
     const long long ltot = p.varlen ? (long long)p.cu_q[p.B] : 0;   // varlen LSE row length
+    // first elements of the sequence in o and dout
+    const long long obase = p.varlen ? qbase * p.so[1] : b * p.so[0];
+    const long long dbase = p.varlen ? qbase * p.sdo[1] : b * p.sdo[0];
     float acc[RPT];
 #pragma unroll
     for (int k = 0; k < RPT; ++k) {
@@ -180,9 +183,10 @@ __global__ void __launch_bounds__(256) preprocess_kernel(BwdParams p) {
         const int s = (int)(row / p.Hq), h = (int)(row % p.Hq);
         // O / dO rows hold Dhv <= DV columns (a multiple of 8): parts past Dhv add 0
         if (row < nrows && s < lq && part * 8 < p.Dhv) {
-            const long long off = ((qbase + s) * p.Hq + h) * p.Dhv + part * 8;
-            const uint4 ov = *reinterpret_cast<const uint4 *>(reinterpret_cast<const T *>(p.o) + off);
-            const uint4 dv = *reinterpret_cast<const uint4 *>(reinterpret_cast<const T *>(p.dout) + off);
+            const long long oo = obase + s * p.so[1] + h * p.so[2] + part * 8;
+            const long long od = dbase + s * p.sdo[1] + h * p.sdo[2] + part * 8;
+            const uint4 ov = *reinterpret_cast<const uint4 *>(reinterpret_cast<const T *>(p.o) + oo);
+            const uint4 dv = *reinterpret_cast<const uint4 *>(reinterpret_cast<const T *>(p.dout) + od);
             const uint32_t oa[4] = {ov.x, ov.y, ov.z, ov.w}, da[4] = {dv.x, dv.y, dv.z, dv.w};
 #pragma unroll
             for (int t = 0; t < 4; ++t) {

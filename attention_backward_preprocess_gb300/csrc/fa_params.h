@@ -90,6 +90,8 @@ struct BwdParams {
     const int2 *mr_key;
     const int *mr_first;
     int mr_rows;
+    // strides in elements (batch, row, head) of q, k, v, o and dout
+    long long sq[3], sk[3], sv[3], so[3], sdo[3];
 };
 
 // Varlen: cu_seqlens agree with the packed totals and with the maximum

@@ -65,6 +65,18 @@ __device__ __forceinline__ int block_scan_max_excl(int v, int *sh, int first) {
     return lane > 0 ? max(r, up) : r;
 }
 
+// The keys [x, y) row i of the document [start, end) sees.
+__device__ __forceinline__ int2 row_interval(const MaskArgs &a, int b, int i, int start, int end) {
+    int lo = start, hi = end;
+    if (a.wl >= 0) lo = max(lo, i - min(a.wl, i));
+    if (a.wr >= 0) hi = min(hi, i + 1 + min(a.wr, a.S - 1 - i));
+    if (a.prefix) {
+        const int n = __ldg(a.prefix + (long long)b * a.prefix_row + (long long)start * a.prefix_tok);
+        hi = max(hi, start + min(max(n, 0), end - start));
+    }
+    return make_int2(lo, hi);
+}
+
 __global__ void __launch_bounds__(kThreads) row_ranges_kernel(MaskArgs a, RangeTables t) {
     __shared__ int sh[kThreads / 32];
     const int b = blockIdx.y, base = blockIdx.x * kTile, S = a.S;
@@ -158,14 +170,8 @@ __global__ void __launch_bounds__(kThreads) row_ranges_kernel(MaskArgs a, RangeT
         const int i = i0 + k;
         r[k] = make_int2(0, 0);
         if (live[k]) {
-            int lo = start[k], hi = end[k];
-            if (a.wl >= 0) lo = max(lo, i - min(a.wl, i));
-            if (a.wr >= 0) hi = min(hi, i + 1 + min(a.wr, S - 1 - i));
-            if (a.prefix) {
-                const int n = __ldg(a.prefix + (long long)b * a.prefix_row + (long long)start[k] * a.prefix_tok);
-                hi = max(hi, start[k] + min(max(n, 0), end[k] - start[k]));
-            }
-            r[k] = make_int2(lo, hi);
+            r[k] = row_interval(a, b, i, start[k], end[k]);
+            const int lo = r[k].x, hi = r[k].y;
             min_lo = min(min_lo, lo);
             max_hi = max(max_hi, hi);
         }
@@ -227,6 +233,25 @@ __device__ __forceinline__ int block_scan_incl(int v, bool mx, int carry, int *s
     return scan_op(r, x, mx);
 }
 
+// The row blocks [x, y) a unit of key block n works on, from the suffix minimum
+// `first` and the prefix maximum `last`.
+__device__ __forceinline__ int2 key_blocks(const int *first, const int *last, int nm, int n) {
+    int lo = 0, hi = nm;                    // number of m with first[m] <= n
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] <= n) lo = mid + 1;
+        else hi = mid;
+    }
+    const int end = lo;
+    lo = 0, hi = nm;                        // first m with last[m] >= n
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (last[mid] >= n) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo < end ? make_int2(lo, end) : make_int2(0, 0);
+}
+
 __global__ void __launch_bounds__(kTabThreads) range_tables_kernel(RangeTables t) {
     __shared__ int sh[kTabThreads / 32];
     const int b = blockIdx.x, nm = t.rows / 64, nn = t.rows / kBlockN, tid = threadIdx.x;
@@ -256,20 +281,128 @@ __global__ void __launch_bounds__(kTabThreads) range_tables_kernel(RangeTables t
     }
     __syncthreads();   // the block's own writes, read back below
     for (int n = tid; n < nn; n += kTabThreads) {
-        int lo = 0, hi = nm;                    // number of m with first[m] <= n
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (first[mid] <= n) lo = mid + 1;
-            else hi = mid;
+        t.key[(long long)b * nn + n] = key_blocks(first, last, nm, n);
+    }
+}
+
+// ------------------------------------------------------- short sequences
+// Up to kShort rows: one CTA per sequence holds everything, eight rows per
+// thread, so one launch does both steps and no document end is searched for.
+// Measured (2 launches -> this): @SHORT@
+constexpr int kShortThreads = 1024, kShortPer = 8, kShort = kShortThreads * kShortPer;
+constexpr int kShortBlocks = kShort / 64;
+
+__global__ void __launch_bounds__(kShortThreads) short_ranges_kernel(MaskArgs a, RangeTables t) {
+    __shared__ int sh[kShortThreads / 32];
+    __shared__ int rev[kShortThreads];
+    __shared__ int s_first[kShortBlocks], s_last[kShortBlocks];
+    const int b = blockIdx.x, S = a.S, tid = threadIdx.x, i0 = tid * kShortPer;
+    const int *doc = a.doc ? a.doc + (long long)b * S : nullptr;
+    int start[kShortPer], end[kShortPer];
+    bool live[kShortPer];
+    if (doc) {
+        int id[kShortPer + 2];
+#pragma unroll
+        for (int k = 0; k < kShortPer + 2; ++k) {
+            const int i = i0 - 1 + k;
+            id[k] = (i >= 0 && i < S) ? __ldg(doc + i) : 0;
         }
-        const int end = lo;
-        lo = 0, hi = nm;                        // first m with last[m] >= n
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (last[mid] >= n) hi = mid;
-            else lo = mid + 1;
+        int last = -1, next = -1, all;   // as in row_ranges_kernel
+#pragma unroll
+        for (int k = 0; k < kShortPer; ++k) {
+            const int i = i0 + k;
+            if (i < S && (i == 0 || id[k + 1] != id[k])) last = i;
+            start[k] = last;
         }
-        t.key[(long long)b * nn + n] = lo < end ? make_int2(lo, end) : make_int2(0, 0);
+#pragma unroll
+        for (int k = kShortPer - 1; k >= 0; --k) {
+            const int i = i0 + k + 1;
+            if (i < S && id[k + 2] != id[k + 1]) next = S - i;
+            else if (i == S) next = 0;
+            end[k] = next;
+        }
+        // inclusive scans; a thread takes its neighbour's value
+        rev[tid] = block_scan_incl(last, true, 0, sh, &all);
+        __syncthreads();
+        const int carry = tid > 0 ? rev[tid - 1] : 0;
+        __syncthreads();
+        rev[kShortThreads - 1 - tid] = next;
+        __syncthreads();
+        const int mirrored = rev[tid];
+        const int scan = block_scan_incl(mirrored, true, 0, sh, &all);
+        rev[tid] = scan;   // every thread has read its mirrored value (the scan's barriers)
+        __syncthreads();
+        const int carry_end = tid < kShortThreads - 1 ? rev[kShortThreads - 2 - tid] : 0;
+#pragma unroll
+        for (int k = 0; k < kShortPer; ++k) {
+            start[k] = start[k] >= 0 ? start[k] : carry;
+            end[k] = S - (end[k] >= 0 ? end[k] : carry_end);
+            live[k] = i0 + k < S && id[k + 1] >= 0;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kShortPer; ++k) {
+            start[k] = 0;
+            end[k] = S;
+            live[k] = i0 + k < S;
+        }
+    }
+    int2 r[kShortPer];
+    int min_lo = 0x7fffffff, max_hi = 0, max_lo = 0, min_hi = 0x7fffffff;
+#pragma unroll
+    for (int k = 0; k < kShortPer; ++k) {
+        const int i = i0 + k;
+        r[k] = make_int2(0, 0);
+        if (live[k]) {
+            r[k] = row_interval(a, b, i, start[k], end[k]);
+            min_lo = min(min_lo, r[k].x);
+            max_hi = max(max_hi, r[k].y);
+        }
+        if (i < S) {
+            max_lo = max(max_lo, r[k].x);
+            min_hi = min(min_hi, r[k].y);
+        }
+    }
+    if (i0 < t.rows) {
+        int4 *dst = reinterpret_cast<int4 *>(t.row + (long long)b * t.rows + i0);
+#pragma unroll
+        for (int k = 0; k < kShortPer / 2; ++k)
+            dst[k] = make_int4(r[2 * k].x, r[2 * k].y, r[2 * k + 1].x, r[2 * k + 1].y);
+    }
+    const int nm = t.rows / 64, nn = t.rows / kBlockN;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) {   // 64 rows: eight threads
+        min_lo = min(min_lo, __shfl_xor_sync(0xffffffffu, min_lo, o));
+        max_hi = max(max_hi, __shfl_xor_sync(0xffffffffu, max_hi, o));
+        max_lo = max(max_lo, __shfl_xor_sync(0xffffffffu, max_lo, o));
+        min_hi = min(min_hi, __shfl_xor_sync(0xffffffffu, min_hi, o));
+    }
+    if ((tid & 7) == 0) {
+        const int m = tid / 8;   // of kShortBlocks
+        if (m < nm) t.block[(long long)b * nm + m] = make_int4(min_lo, max_hi, max_lo, min_hi);
+        const bool some = m < nm && max_hi > min_lo;
+        s_first[m] = some ? min_lo / kBlockN : 0x7fffffff;
+        s_last[m] = some ? (max_hi - 1) / kBlockN : -1;
+    }
+    // suffix minimum of first, prefix maximum of last, in log steps
+    for (int o = 1; o < kShortBlocks; o <<= 1) {
+        __syncthreads();
+        int f = 0, l = 0;
+        if (tid < kShortBlocks) {
+            f = tid + o < kShortBlocks ? min(s_first[tid], s_first[tid + o]) : s_first[tid];
+            l = tid >= o ? max(s_last[tid], s_last[tid - o]) : s_last[tid];
+        }
+        __syncthreads();
+        if (tid < kShortBlocks) {
+            s_first[tid] = f;
+            s_last[tid] = l;
+        }
+    }
+    __syncthreads();
+    if (tid < nm) t.first[(long long)b * nm + tid] = s_first[tid];
+    if (tid < nn) {
+        const int2 r2 = key_blocks(s_first, s_last, nm, tid);
+        t.key[(long long)b * nn + tid] = r2;
     }
 }
 
@@ -278,6 +411,10 @@ __global__ void __launch_bounds__(kTabThreads) range_tables_kernel(RangeTables t
 cudaError_t launch_mask_ranges(const int *doc, const int *prefix, int prefix_per_token, int B, int S, int wl,
                                int wr, const RangeTables &t, cudaStream_t stream) {
     MaskArgs a{doc, prefix, prefix_per_token ? S : 1, prefix_per_token ? 1 : 0, B, S, wl, wr};
+    if (S <= kShort) {
+        short_ranges_kernel<<<(unsigned)B, kShortThreads, 0, stream>>>(a, t);
+        return cudaGetLastError();
+    }
     const dim3 grid((unsigned)((t.rows + kTile - 1) / kTile), (unsigned)B);
     row_ranges_kernel<<<grid, kThreads, 0, stream>>>(a, t);
     const cudaError_t e = cudaGetLastError();

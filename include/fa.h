@@ -255,7 +255,13 @@ fa_status fa_fwd(const void *q, const void *k, const void *v, void *o, float *ls
  *   deterministic mode; not with the extensions and head dims named above.
  *   Values (forward), and queries, keys, values and dout (backward) of masked
  *   tokens must be finite, as for every mask of this library: a masked entry
- *   has P = dS = 0, and 0 times their value is added. */
+ *   has P = dS = 0, and 0 times their value is added.
+ * q_stride, k_stride, v_stride, o_stride, dout_stride: element strides
+ *   (batch, row, head) of an input that is not contiguous, e.g. a slice of a
+ *   joint projection; all zero: contiguous.  Multiples of 8 in (0, 2^39); the
+ *   head dim itself is contiguous.  Packed varlen tensors have no batch
+ *   stride (the first is not looked at).  o_stride: fa_bwd_ext only.  Outputs
+ *   and lse are contiguous. */
 typedef struct {
     int window_left;
     int window_right;
@@ -278,6 +284,7 @@ typedef struct {
     float softcap;
     const void *mask_ranges;
     size_t mask_ranges_bytes;
+    long long q_stride[3], k_stride[3], v_stride[3], o_stride[3], dout_stride[3];
 } fa_ext;
 
 /* Visible keys of self-attention problems (Sq = Sk = S, dense) with documents
@@ -297,7 +304,7 @@ typedef struct {
  *         prefix_per_token != 0 prefix_len[b * S + s], the entry of the
  *         document's first token in a [B, S] array.
  * ranges: device buffer of fa_mask_ranges_bytes(B, S) bytes (0: bad sizes),
- *   256-byte aligned, fully overwritten.  Two launches on `stream`, no other
+ *   256-byte aligned, fully overwritten.  Launches on `stream` and no other
  *   call; can be captured into a CUDA graph.  Errors: FA_ERR_INVALID_ARG for
  *   sizes, alignment, a window below -1, or a prefix without causal or with a
  *   window; FA_ERR_UNSUPPORTED for B above 65535. */

@@ -70,7 +70,8 @@ RANGES = [
     dict(B=1, S=1500, doc="mixed", prefix="doc"), dict(B=3, S=700, prefix="seq"),
     dict(B=2, S=700, doc="pad", prefix="seq"), dict(B=1, S=1025, doc="mixed", window=(40, -1)),
     dict(B=1, S=400, window=(0, 0), causal=False), dict(B=1, S=400, window=(2 ** 31 - 1, 2 ** 31 - 1), causal=False),
-    dict(B=2, S=300, doc="ones"),
+    dict(B=2, S=300, doc="ones"), dict(B=2, S=8192, doc="mixed"), dict(B=2, S=8193, doc="pad", prefix="seq"),
+    dict(B=1, S=9000, window=(700, 5), causal=False),
 ]
 
 
@@ -409,8 +410,22 @@ def test_other_strides(fa, cuda_device):
         assert a.is_contiguous() and torch.equal(a, b)
     with pytest.raises(ValueError):
         fa.fa_bwd(*x[:3], o, x[3], lse, dq=y[0])
+    # lying off the 16-byte steps of the tensor loads: copied, on the current stream only
+    odd = [torch.cat([t, t], dim=3)[..., 1:65].copy_(t) for t in x[:3]]
+    o3, _ = fa.fa_fwd(*odd, causal=True, softcap=30.0)
+    assert torch.equal(o, o3)
+    o4, _ = fa.fa_fwd(*y, causal=True, softcap=30.0, stream=torch.cuda.current_stream())
+    assert torch.equal(o, o4)
     with pytest.raises(ValueError):
-        fa.fa_fwd(*y, stream=torch.cuda.current_stream())
+        fa.fa_fwd(*odd, stream=torch.cuda.current_stream())
+    # packed varlen slices of a joint projection
+    cu = torch.tensor([0, 60, 150], dtype=torch.int32).cuda()
+    kw = dict(cu_seqlens_q=cu, cu_seqlens_k=cu, max_seqlen_q=90, max_seqlen_k=90, causal=True, totals=(150, 150))
+    joint = torch.cat([x[0][0, :, :2], x[1][0], x[2][0]], dim=1)
+    parts = [joint[:, :2], joint[:, 2:4], joint[:, 4:]]
+    a = fa.fa_fwd(*parts, **kw)
+    b = fa.fa_fwd(*(t.contiguous() for t in parts), **kw)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 # ------------------------------------------------------- refusals (no GPU)
@@ -447,6 +462,8 @@ REFUSED = [
     (dict(mask_ranges=0x10000, mask_ranges_bytes=1 << 30), dict(cu=0xA000), 2),
     (dict(mask_ranges=0x10000, mask_ranges_bytes=1 << 30), dict(D=192), 2),
     (dict(mask_ranges=0x10000, mask_ranges_bytes=1 << 30, alibi_slopes=0x7000), {}, 2),
+    (dict(q_stride=(8192, 100, 64)), {}, 1), (dict(k_stride=(0, 128, 64)), {}, 1),
+    (dict(v_stride=(8192, 128, -64)), {}, 1), (dict(q_stride=(8192, 1 << 39, 64)), {}, 1),
 ]
 
 
