@@ -837,7 +837,6 @@ fa_status fa_fwd_kvcache(const void *q, const fa_kv_cache *cache, const int *cac
     p.Sq = Sq;
     p.Hq = Hq;
     p.G = Hq / cache->Hkv;
-    p.groups = (p.G * Sq + 15) / 16;
     // tiles are counted in 32 bits per sequence sum
     if ((long long)B * (cache->max_pages * (long long)cache->page_size / 64 + 1) > 0x7fffffffLL)
         return FA_ERR_UNSUPPORTED;
@@ -845,11 +844,15 @@ fa_status fa_fwd_kvcache(const void *q, const fa_kv_cache *cache, const int *cac
     if ((st = check_device()) != FA_OK) return st;
     p.c.err = fa::fwd_error_word();
     if (!p.c.err) return FA_ERR_CUDA;
-    const size_t n = (size_t)fa::kKvSms * fa::kv_warps(cache->D);
+    const size_t n = (size_t)fa::kKvSms * fa::kKvMaxWarps;
     uint8_t *w = static_cast<uint8_t *>(workspace);
     p.acc = reinterpret_cast<float *>(w);
     p.stat = reinterpret_cast<float4 *>(w + n * 2 * 16 * cache->D * sizeof(float));
-    p.meta = reinterpret_cast<int4 *>(w + n * 2 * 16 * cache->D * sizeof(float) + n * 2 * 16 * sizeof(float4));
+    w += fa::kv_pieces_bytes(n, cache->D);
+    p.cta_acc = reinterpret_cast<float *>(w);
+    p.cta_stat = reinterpret_cast<float4 *>(w + (size_t)fa::kKvSms * 2 * 16 * cache->D * sizeof(float));
+    w += fa::kv_pieces_bytes(fa::kKvSms, cache->D);
+    p.meta = reinterpret_cast<int4 *>(w);
     return cuda_status(fa::launch_kv_attn(p, cache->D, dtype == FA_BF16, sm_count(), stream));
 }
 

@@ -9,7 +9,7 @@
 //
 // K lies token by token, V dim by dim, so that in both products the 16-byte
 // pieces a lane reads are contiguous along the axis the tensor core contracts.
-#include <cuda_fp8.h>
+#include <type_traits>
 
 #include "fa_device.cuh"
 #include "fa_kvcache.h"
@@ -177,15 +177,16 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
 
 // --------------------------------------------------------------- attention
 // For one kv head the G query heads of a group times Sq tokens are the rows of
-// one tile: S = Q K^T and O = P V run as m16n8k16 products over 64 keys at a
-// time.  Bytes bound it (2 D bytes per key against 4 D flops per row and key),
-// so the design keeps reads in flight: every warp is a worker of its own with
-// a contiguous share of all (sequence, kv head, row group, 64-key tile) work,
-// each lane copies the pieces of K and V it needs itself into a ring in shared
-// memory (cp.async, no barrier: a lane reads only what it copied), and e4m3
-// becomes f16 in registers on the way into the tensor core.  Equal shares
-// whatever the lengths; a (sequence, kv head) cut between workers leaves
-// pieces that a second kernel joins in a fixed order.
+// one product: S^T = K Q^T and O^T = V^T P^T run as m16n8k16 products over 64
+// keys at a time, keys (then dims) along M and the rows along N, so a decoding
+// step's few rows pad to 8 and not to 16.  Bytes bound it (2 D bytes per key
+// against 4 D flops per row and key), so the design keeps reads in flight:
+// every warp is a worker of its own with a contiguous share of all (sequence,
+// kv head, row group, 64-key tile) work, each lane copies the pieces of K and
+// V it needs itself into shared memory (cp.async, no barrier: a lane reads
+// only what it copied), and e4m3 becomes f16 in registers on the way into the
+// tensor core.  Equal shares whatever the lengths; a (sequence, kv head) cut
+// between workers leaves pieces that a second kernel joins in a fixed order.
 //
 // e4m3 fits f16 exactly.  Q (bf16 or f16) enters as f16 under a power of two
 // per row that brings its largest magnitude to [2^14, 2^15): exact but for
@@ -195,19 +196,23 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
 //
 // Fragments.  The contracted axis may be permuted at will if both operands
 // agree: a lane holds 16 consecutive bytes of a key's row (K) or of a dim's
-// row of tokens (V), i.e. four k-steps of four values.  Column n of S tile (u,
-// h) is key 16 (n / 2) + 4 u + 2 h + n % 2, which puts a lane's P where the
-// product with V wants it, and all a lane's keys into one 16-key group, hence
-// one page and one scale.
+// row of tokens (V), i.e. four k-steps of four values.  Row 8 h + r of S^T
+// tile t is key 16 (r / 2) + r % 2 + 4 t + 2 h: all keys of lanes r = 4 r / 4
+// are then of one 16-key group (one page, one scale), and the 8x8 blocks of
+// P, transposed across the lanes (movmatrix), are where the product with V
+// wants them.
 constexpr int kTile = 64;   // keys per step
 constexpr float kLazy = 8.f;
 
-template <int D>
+// NR: 8-row blocks of a worker's rows (1 or 2).  The warps per CTA fill shared
+// memory (K and V of one tile each: @WARPS@).
+template <int D, int NR>
 struct KvCfg {
-    static constexpr int kWarps = (D == 128) ? 6 : 8;
-    static constexpr int kStages = (D == 128) ? 2 : 3;
+    static constexpr int kWarps = (D == 128) ? (NR == 1 ? 12 : 8) : (NR == 1 ? 16 : 12);
     static constexpr int KB = kTile * D;                 // bytes of a K (or V) tile
-    static constexpr int SMEM = kWarps * kStages * 2 * KB;
+    static constexpr int SMEM = kWarps * 2 * KB;
+    static constexpr int PIECE = NR * 8 * D;             // floats of a piece
+    static_assert(kWarps <= kKvMaxWarps, "the workspace holds kKvMaxWarps workers per SM");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool on) {
@@ -228,13 +233,22 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float quad_max(float v) {
-    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+// an 8x8 block of 16-bit values transposed across the warp
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
-__device__ __forceinline__ float quad_sum(float v) {
-    v += __shfl_xor_sync(0xffffffffu, v, 1);
-    return v + __shfl_xor_sync(0xffffffffu, v, 2);
+// over the lanes of equal lane % 4 (the keys of a row pair)
+__device__ __forceinline__ float keys_max(float v) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float keys_sum(float v) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
 
 // Tokens of sequence b, 0 where the length is outside the table.
@@ -276,17 +290,150 @@ struct Cursor {
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : l == 0.f ? -INFINITY : l;
 }
+// What turns a row's accumulator into its output: 2^(R - m) / l (0 for a row
+// that saw nothing).
+__device__ __forceinline__ float out_factor(float R, float m, float l) { return l == 0.f ? 0.f : ex2(R - m) / l; }
 
-template <int D, typename T, bool kCap>
-__global__ void __launch_bounds__(KvCfg<D>::kWarps * 32, 1) kv_attn_kernel(const __grid_constant__ KvAttnParams p) {
-    using C = KvCfg<D>;
-    constexpr int W = C::kWarps, ST = C::kStages, KS = D / 16;
+// Output rows of a piece in fragment order: acc[dm] holds dims 16 dm + r8 (and
+// + 8) of rows row0 + 2 q4, + 1, already scaled.
+template <int D, typename T>
+__device__ __forceinline__ void store_rows(const KvAttnParams &p, int b, int hk, int row0, int lane,
+                                           float (&acc)[4], int dm) {
+    const int r8 = lane >> 2, q4 = lane & 3;
+    // two 8x8 blocks (dims x rows), transposed: lane gets row r8, dims 2 q4, + 1
+    const uint32_t lo = transpose8(Cvt<T>::pack(acc[0], acc[1]));
+    const uint32_t hi = transpose8(Cvt<T>::pack(acc[2], acc[3]));
+    const int row = row0 + r8;
+    if (row < p.Sq * p.G) {
+        const int i = row / p.G, hq = hk * p.G + row % p.G;
+        T *dst = reinterpret_cast<T *>(p.o) + (((long long)b * p.Sq + i) * p.Hq + hq) * D + 16 * dm + 2 * q4;
+        *reinterpret_cast<uint32_t *>(dst) = lo;
+        *reinterpret_cast<uint32_t *>(dst + 8) = hi;
+    }
+}
+
+// Adds a piece (fragments and statistics number `at` of a list) to a worker's
+// state of one row block.  The row sums stay with the lanes of the first key.
+template <int NR, int DM>
+__device__ __forceinline__ void add_piece(const KvAttnParams &p, const float *list, const float4 *stats, long long at,
+                                          int nr, int row0, int lane, float (&m)[2], float (&l)[2], float (&R)[2],
+                                          float (&acc)[DM][4]) {
+    const int q4 = lane & 3;
+    const float4 *src = reinterpret_cast<const float4 *>(list + (at * NR + nr) * DM * 128) + lane;
+    float4 v[DM], st[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)   // rows past the last carry no statistics
+        st[e] = row0 + 2 * q4 + e < p.Sq * p.G ? __ldcg(stats + (at * NR + nr) * 8 + 2 * q4 + e)
+                                               : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+#pragma unroll
+    for (int dm = 0; dm < DM; ++dm) v[dm] = __ldcg(src + 32 * dm);
+    float g[2], h[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const float mn = fmaxf(m[e], st[e].x), rn = fmaxf(R[e], st[e].z);
+        const float m0 = mn == -INFINITY ? 0.f : mn, r0 = rn == -INFINITY ? 0.f : rn;
+        l[e] = l[e] * ex2(m[e] - m0) + (lane < 4 ? st[e].y * ex2(st[e].x - m0) : 0.f);
+        g[e] = ex2(R[e] - r0);
+        h[e] = ex2(st[e].z - r0);
+        m[e] = mn;
+        R[e] = rn;
+    }
+#pragma unroll
+    for (int dm = 0; dm < DM; ++dm) {
+        acc[dm][0] = fmaf(v[dm].x, h[0], acc[dm][0] * g[0]);
+        acc[dm][1] = fmaf(v[dm].y, h[1], acc[dm][1] * g[1]);
+        acc[dm][2] = fmaf(v[dm].z, h[0], acc[dm][2] * g[0]);
+        acc[dm][3] = fmaf(v[dm].w, h[1], acc[dm][3] * g[1]);
+    }
+}
+
+// Rows 2 q4 + e of one row block, one 16-dim part, over several pieces.
+struct Joined {
+    float4 v;
+    float m[2], l[2], r[2];
+};
+
+// The pieces of holders from .. to (piece 1 of holder `first`, piece 0 of the
+// others) summed in order against their common maxima: statistics in a first
+// pass, values in a second, whose loads do not wait for one another.
+template <int NR, int DM>
+__device__ __forceinline__ void join_pieces(const KvAttnParams &p, const float *acc, const float4 *stat, int from,
+                                            int to, int first, int nr, int dm, int row0, int lane, Joined &x) {
+    constexpr int PIECE = NR * DM * 128;
+    const int q4 = lane & 3;
+    // rows past the last carry no statistics
+    const bool live[2] = {row0 + 2 * q4 < p.Sq * p.G, row0 + 2 * q4 + 1 < p.Sq * p.G};
+    auto stat_of = [&](int w, int e) -> float4 {
+        const long long at = ((long long)w * 2 + (w == first ? 1 : 0)) * (NR * 8) + nr * 8 + 2 * q4 + e;
+        return live[e] ? __ldcg(stat + at) : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    };
+#pragma unroll
+    for (int e = 0; e < 2; ++e) x.m[e] = x.r[e] = -INFINITY, x.l[e] = 0.f;
+#pragma unroll 4
+    for (int w = from; w <= to; ++w)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float4 st = stat_of(w, e);
+            x.m[e] = fmaxf(x.m[e], st.x);
+            x.r[e] = fmaxf(x.r[e], st.z);
+        }
+    const float m0[2] = {x.m[0] == -INFINITY ? 0.f : x.m[0], x.m[1] == -INFINITY ? 0.f : x.m[1]};
+    const float r0[2] = {x.r[0] == -INFINITY ? 0.f : x.r[0], x.r[1] == -INFINITY ? 0.f : x.r[1]};
+    x.v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int w = from; w <= to; ++w) {
+        const long long at = (long long)w * 2 + (w == first ? 1 : 0);
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(acc + at * PIECE + nr * DM * 128) + 32 * dm + lane);
+        float h[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float4 st = stat_of(w, e);
+            x.l[e] = fmaf(st.y, ex2(st.x - m0[e]), x.l[e]);
+            h[e] = ex2(st.z - r0[e]);
+        }
+        x.v.x = fmaf(v.x, h[0], x.v.x);
+        x.v.y = fmaf(v.y, h[1], x.v.y);
+        x.v.z = fmaf(v.z, h[0], x.v.z);
+        x.v.w = fmaf(v.w, h[1], x.v.w);
+    }
+}
+
+template <int D, typename T>
+__device__ __forceinline__ void finish_rows(const KvAttnParams &p, const Joined &x, int b, int hk, int row0, int dm,
+                                            int lane) {
+    const float f0 = out_factor(x.r[0], x.m[0], x.l[0]), f1 = out_factor(x.r[1], x.m[1], x.l[1]);
+    float o[4] = {x.v.x * f0, x.v.y * f1, x.v.z * f0, x.v.w * f1};
+    store_rows<D, T>(p, b, hk, row0, lane, o, dm);
+    if (p.lse && dm == 0 && lane < 4) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int row = row0 + 2 * lane + e;
+            if (row < p.Sq * p.G)
+                p.lse[((long long)b * p.Hq + hk * p.G + row % p.G) * p.Sq + row / p.G] = lse_of(x.m[e], x.l[e]);
+        }
+    }
+}
+
+// Programmatic dependent launch: the second kernel's CTAs may be set up while
+// the first still runs, and wait here for its results.
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <int D, int NR, typename T, bool kCap>
+__global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1) kv_attn_kernel(const __grid_constant__ KvAttnParams p) {
+    using C = KvCfg<D, NR>;
+    constexpr int W = C::kWarps, HH = D / 64, KS = D / 16, DM = D / 16;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ int s_pre[kKvMaxSeqs];   // tiles of sequences 0 .. b, inclusive
     __shared__ int s_warp[W];
+    // pieces written of the segment whose last holder in this CTA is worker w
+    // and which ends there (0) or goes on (1)
+    __shared__ int s_done[W][2];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int r8 = lane >> 2, q4 = lane & 3;
 
+    if (threadIdx.x == 0) p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (lane < 2) s_done[warp][lane] = 0;
     // ---- the work: tiles per sequence, summed
     const int per_tile = p.c.Hkv * p.groups;
     int carry = 0;
@@ -309,9 +456,11 @@ __global__ void __launch_bounds__(KvCfg<D>::kWarps * 32, 1) kv_attn_kernel(const
         if (lane == 31) s_warp[warp] = x;
         __syncthreads();
         int add = carry, all = carry;
+#pragma unroll
         for (int i = 0; i < W; ++i) {
-            if (i < warp) add += s_warp[i];
-            all += s_warp[i];
+            const int v = s_warp[i];
+            if (i < warp) add += v;
+            all += v;
         }
         if (b < p.B) s_pre[b] = x + add;
         carry = all;
@@ -327,9 +476,9 @@ __global__ void __launch_bounds__(KvCfg<D>::kWarps * 32, 1) kv_attn_kernel(const
     }
     const long long total = (long long)carry * per_tile;
     // shares of the workers: worker c takes tiles [c total / N, (c + 1) total / N)
-    const int wid = blockIdx.x * W + warp;
+    const int cta0 = blockIdx.x * W, wid = cta0 + warp;
     const long long N = min((long long)p.workers, total);
-    if (lane == 0 && wid < p.workers) p.meta[wid] = make_int4(-1, 0, 0, 0);
+    pdl_launch();
     if (wid >= N) return;
     const long long w0 = total * wid / N, w1 = total * (wid + 1) / N;
     auto worker_of = [&](long long w) -> int { return (int)(((w + 1) * N - 1) / total); };
@@ -353,8 +502,8 @@ __global__ void __launch_bounds__(KvCfg<D>::kWarps * 32, 1) kv_attn_kernel(const
     Cursor cc = pc;   // what is computed next
     int left = (int)(w1 - w0), to_load = left;
 
-    const uint32_t ring = smem_u32(smem_raw) + warp * (ST * 2 * C::KB) + 16 * lane;
-    // page of 16-key group (lane % 4) of the tile at pc, and the lookup of the next
+    const uint32_t kt = smem_u32(smem_raw) + warp * (2 * C::KB) + 16 * lane, vt = kt + C::KB;
+    // page of 16-key group (lane % 4) of a tile
     auto lookup = [&](const Cursor &c) -> int {
         const int tok = kTile * c.t + 16 * q4;
         if (tok >= c.n || tok + 16 <= c.lo) return -1;    // a group nobody sees: not read
@@ -366,37 +515,35 @@ __global__ void __launch_bounds__(KvCfg<D>::kWarps * 32, 1) kv_attn_kernel(const
         return page;
     };
     int pg = lookup(pc);
-    float ksc[ST], vsc[ST];   // scales of the lane's group, tiles in the ring
-    // K of the tile at pc into slot st (and its scales), then V of the same tile
-    auto load_k = [&](int st) __attribute__((always_inline)) {
+    float ksc = 0.f, vsc = 0.f;   // scales of group r8 / 2 (a lane's keys) of the loaded tile
+    // K of the tile at pc (and its scales), then V of the same tile
+    auto load_k = [&]() __attribute__((always_inline)) {
         if (to_load > 0) {
-            const int hk = pc.s / p.groups;
-            ksc[st] = 0.f;
-            vsc[st] = 0.f;
-            if (pg >= 0) {
-                ksc[st] = __ldg(p.c.k_scale + (long long)pg * p.c.Hkv + hk);
-                vsc[st] = __ldg(p.c.v_scale + (long long)pg * p.c.Hkv + hk);
-            }
-            const int grp = r8 >> 1;
+            const int hk = pc.s / p.groups, grp = r8 >> 1;
             const int page = __shfl_sync(0xffffffffu, pg, grp);
+            const long long ph = (long long)max(page, 0) * p.c.Hkv + hk;
+            ksc = page >= 0 ? __ldg(p.c.k_scale + ph) : 0.f;
+            vsc = page >= 0 ? __ldg(p.c.v_scale + ph) : 0.f;
             const int in_page = (kTile * pc.t + 16 * grp) % p.c.page + (r8 & 1);
-            const uint8_t *src = p.c.k + (((long long)max(page, 0) * p.c.Hkv + hk) * p.c.page + in_page) * D + 16 * q4;
+            const uint8_t *src = p.c.k + (ph * p.c.page + in_page) * D + 16 * q4;
 #pragma unroll
-            for (int ut = 0; ut < 8; ++ut)
+            for (int u = 0; u < 8; ++u)   // u = 2 t + h: key + 2 u
 #pragma unroll
-                for (int hh = 0; hh < D / 64; ++hh)
-                    cp_async16(ring + st * 2 * C::KB + 512 * (ut * (D / 64) + hh), src + 2 * ut * D + 64 * hh, page >= 0);
+                for (int hh = 0; hh < HH; ++hh) cp_async16(kt + 512 * (u * HH + hh), src + 2 * u * D + 64 * hh, page >= 0);
         }
         cp_commit();
     };
-    auto load_v = [&](int st) __attribute__((always_inline)) {
+    auto load_v = [&]() __attribute__((always_inline)) {
         if (to_load > 0) {
             const int hk = pc.s / p.groups;
             const int in_page = (kTile * pc.t + 16 * q4) % p.c.page;
             const uint8_t *src = p.c.v + (((long long)max(pg, 0) * p.c.Hkv + hk) * D + r8) * p.c.page + in_page;
+            const long long step = 8 * p.c.page;
 #pragma unroll
-            for (int dt = 0; dt < D / 8; ++dt)
-                cp_async16(ring + st * 2 * C::KB + C::KB + 512 * dt, src + (long long)8 * dt * p.c.page, pg >= 0);
+            for (int dt = 0; dt < D / 8; ++dt) {
+                cp_async16(vt + 512 * dt, src, pg >= 0);
+                src += step;
+            }
             if (--to_load > 0) {
                 pc.next(p);
                 pg = lookup(pc);
@@ -404,304 +551,357 @@ __global__ void __launch_bounds__(KvCfg<D>::kWarps * 32, 1) kv_attn_kernel(const
         }
         cp_commit();
     };
-    // (the slots are compile-time constants: the scales stay in registers)
-#pragma unroll
-    for (int st = 0; st < ST; ++st) {
-        load_k(st);
-        load_v(st);
-    }
+    load_k();
+    load_v();
 
-    // ---- state of the segment being computed
-    uint32_t qa[KS][4];          // Q fragments (f16)
-    float fr[2];                 // per row r8, r8 + 8: undoes Q's power of two, times c log2(e) (or the cap's factor)
-    int lo_r[2], hi_r[2];        // visible keys of the two rows
-    float acc[D / 8][4];
-    float m_run[2], l_run[2], R[2];
+    // ---- state of the segment being computed: row block nr, row 2 q4 + e of it
+    uint32_t qb[NR][KS][2];      // Q fragments (f16): row r8 of the block
+    float fr[NR][2];             // undoes Q's power of two, times c log2(e) (or the cap's factor)
+    int lo_r[NR][2], hi_r[NR][2];   // visible keys
+    float acc[NR][DM][4];
+    float m_run[NR][2], l_run[NR][2], R[NR][2];
     bool fresh = true, begins = false;
-    auto open_segment = [&]() __attribute__((always_inline)) {
-        const int hk = cc.s / p.groups, rg = cc.s % p.groups;
+    while (true) {
+        if (fresh) {
+            const int hk = cc.s / p.groups, rg = cc.s % p.groups;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int row = rg * 16 + r8 + 8 * j;
-            const bool live = row < p.Sq * p.G;
-            const int i = live ? row / p.G : p.Sq - 1, g = live ? row % p.G : 0;
-            const T *src = reinterpret_cast<const T *>(p.q) + (((long long)cc.b * p.Sq + i) * p.Hq + hk * p.G + g) * D + 16 * q4;
-            uint32_t raw[D / 64][8];
-            float amax = 0.f;
+            for (int nr = 0; nr < NR; ++nr) {
+                const int row = (rg * NR + nr) * 8 + r8;
+                const bool live = row < p.Sq * p.G;
+                const int i = live ? row / p.G : p.Sq - 1, g = live ? row % p.G : 0;
+                const T *src = reinterpret_cast<const T *>(p.q) + (((long long)cc.b * p.Sq + i) * p.Hq + hk * p.G + g) * D + 16 * q4;
+                uint32_t raw[HH][8];
+                float amax = 0.f;
 #pragma unroll
-            for (int hh = 0; hh < D / 64; ++hh) {
-                const uint4 a = live ? __ldg(reinterpret_cast<const uint4 *>(src + 64 * hh)) : make_uint4(0, 0, 0, 0);
-                const uint4 c = live ? __ldg(reinterpret_cast<const uint4 *>(src + 64 * hh) + 1) : make_uint4(0, 0, 0, 0);
-                raw[hh][0] = a.x, raw[hh][1] = a.y, raw[hh][2] = a.z, raw[hh][3] = a.w;
-                raw[hh][4] = c.x, raw[hh][5] = c.y, raw[hh][6] = c.z, raw[hh][7] = c.w;
+                for (int hh = 0; hh < HH; ++hh) {
+                    const uint4 a = live ? __ldg(reinterpret_cast<const uint4 *>(src + 64 * hh)) : make_uint4(0, 0, 0, 0);
+                    const uint4 c = live ? __ldg(reinterpret_cast<const uint4 *>(src + 64 * hh) + 1) : make_uint4(0, 0, 0, 0);
+                    raw[hh][0] = a.x, raw[hh][1] = a.y, raw[hh][2] = a.z, raw[hh][3] = a.w;
+                    raw[hh][4] = c.x, raw[hh][5] = c.y, raw[hh][6] = c.z, raw[hh][7] = c.w;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float2 f = Cvt<T>::unpack(raw[hh][k]);
-                    amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    for (int k = 0; k < 8; ++k) {
+                        const float2 f = Cvt<T>::unpack(raw[hh][k]);
+                        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
                 }
-            }
-            amax = quad_max(amax);
-            const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -100);
-            const float up = pow2(14 - min(e, 126)), down = pow2(min(e, 126) - 14);
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 126);
+                const float up = pow2(14 - e), down = pow2(e - 14) * (kCap ? p.cap_k : p.scale_log2);
 #pragma unroll
-            for (int hh = 0; hh < D / 64; ++hh)
+                for (int hh = 0; hh < HH; ++hh)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {   // piece k of the row: k-step 4 hh + k / 2, register j + 2 (k % 2)
-                    const float2 f = Cvt<T>::unpack(raw[hh][k]);
-                    qa[4 * hh + k / 2][j + 2 * (k & 1)] = Cvt<__half>::pack(f.x * up, f.y * up);
+                    for (int k = 0; k < 8; ++k) {   // word k of the row: k-step 4 hh + k / 2
+                        const float2 f = Cvt<T>::unpack(raw[hh][k]);
+                        qb[nr][4 * hh + k / 2][k & 1] = Cvt<__half>::pack(f.x * up, f.y * up);
+                    }
+                const int hi = cc.n - p.Sq + i;
+#pragma unroll
+                for (int e2 = 0; e2 < 2; ++e2) {   // the rows a lane's scores belong to
+                    fr[nr][e2] = __shfl_sync(0xffffffffu, down, 4 * (2 * q4 + e2));
+                    hi_r[nr][e2] = __shfl_sync(0xffffffffu, hi, 4 * (2 * q4 + e2));
+                    lo_r[nr][e2] = p.window < 0 ? 0 : max(0, hi_r[nr][e2] - p.window);
+                    m_run[nr][e2] = R[nr][e2] = -INFINITY;
+                    l_run[nr][e2] = 0.f;
                 }
-            fr[j] = down * (kCap ? p.cap_k : p.scale_log2);
-            hi_r[j] = cc.n - p.Sq + i;
-            lo_r[j] = p.window < 0 ? 0 : max(0, hi_r[j] - p.window);
-            m_run[j] = R[j] = -INFINITY;
-            l_run[j] = 0.f;
-        }
 #pragma unroll
-        for (int dt = 0; dt < D / 8; ++dt)
+                for (int dm = 0; dm < DM; ++dm)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[dt][i] = 0.f;
-        begins = cc.t == cc.t0;
-        fresh = false;
-    };
-    // the rows' results, or the piece's for the join
-    auto close_segment = [&](bool ends) __attribute__((always_inline)) {
-        const int hk = cc.s / p.groups, rg = cc.s % p.groups;
-        const bool whole = begins && ends;
-        const int piece = begins ? 1 : 0;
-        if (!whole && !begins && lane == 0) {
-            // the segment's first tile in the order of all work
-            const long long first = (long long)(cc.b > 0 ? s_pre[cc.b - 1] : 0) * per_tile + (long long)cc.s * (cc.t1 - cc.t0);
-            p.meta[wid] = make_int4(cc.s, worker_of(first), ends ? 1 : 0, cc.b);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float l = quad_sum(l_run[j]);
-            const int row = rg * 16 + r8 + 8 * j;
-            if (row >= p.Sq * p.G) continue;
-            if (whole) {
-                const int i = row / p.G, hq = hk * p.G + row % p.G;
-                const float f = l == 0.f ? 0.f : ex2(R[j] - m_run[j]) / l;
-                T *dst = reinterpret_cast<T *>(p.o) + (((long long)cc.b * p.Sq + i) * p.Hq + hq) * D + 2 * q4;
-#pragma unroll
-                for (int dt = 0; dt < D / 8; ++dt)
-                    *reinterpret_cast<uint32_t *>(dst + 8 * dt) =
-                        l == 0.f ? 0u : Cvt<T>::pack(acc[dt][2 * j] * f, acc[dt][2 * j + 1] * f);
-                if (p.lse && q4 == 0) p.lse[((long long)cc.b * p.Hq + hq) * p.Sq + i] = lse_of(m_run[j], l);
-            } else {
-                const long long at = ((long long)wid * 2 + piece) * 16 + r8 + 8 * j;
-                float *dst = p.acc + at * D + 2 * q4;
-#pragma unroll
-                for (int dt = 0; dt < D / 8; ++dt)
-                    *reinterpret_cast<float2 *>(dst + 8 * dt) = make_float2(acc[dt][2 * j], acc[dt][2 * j + 1]);
-                if (q4 == 0) p.stat[at] = make_float4(m_run[j], l, R[j], 0.f);
+                    for (int k = 0; k < 4; ++k) acc[nr][dm][k] = 0.f;
             }
+            begins = cc.t == cc.t0;
+            fresh = false;
         }
-        fresh = true;
-    };
-
-    auto step = [&](int st) __attribute__((always_inline)) {
-        if (fresh) open_segment();
-        const uint32_t kt = ring + st * 2 * C::KB, vt = kt + C::KB;
-        // S = Q K^T
-        cp_wait<2 * ST - 1>();
-        float s[8][4];
+        // ---- S^T = K Q^T
+        cp_wait<1>();
+        float s[NR][4][4];
 #pragma unroll
-        for (int ut = 0; ut < 8; ++ut) {
+        for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[ut][i] = 0.f;
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int hh = 0; hh < D / 64; ++hh) {
-                const uint4 v = ld_shared_v4(kt + 512 * (ut * (D / 64) + hh));
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                for (int i = 0; i < 4; ++i) s[nr][t][i] = 0.f;
+#pragma unroll
+        for (int hh = 0; hh < HH; ++hh) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const uint4 v = ld_shared_v4(kt + 512 * (2 * t * HH + hh)), u = ld_shared_v4(kt + 512 * ((2 * t + 1) * HH + hh));
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w}, x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    uint32_t b0, b1;
-                    e4m3x4_to_f16(w[k], b0, b1);
-                    mma_f16(s[ut], qa[4 * hh + k], b0, b1);
+                    uint32_t a[4];
+                    e4m3x4_to_f16(w[k], a[0], a[2]);
+                    e4m3x4_to_f16(x[k], a[1], a[3]);
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr) mma_f16(s[nr][t], a, qb[nr][4 * hh + k][0], qb[nr][4 * hh + k][1]);
                 }
             }
         }
-        const float ks = ksc[st], vs = vsc[st];
-        const int key0 = kTile * cc.t + 16 * q4;   // first key of the lane's group
-        const int n = cc.n;
+        const float ks = ksc, vs = vsc;
+        const int key0 = kTile * cc.t + 16 * (r8 >> 1) + (r8 & 1);   // the lane's keys: key0 + 2 u
         const bool ends = cc.t + 1 == cc.t1;
-        load_k(st);   // the slot's K has been read
+        load_k();   // this tile's K has been read
         const float ev = vs > 0.f ? log2f(vs) : -INFINITY;   // exact for a power of two
-        // scores in log2 units; a tile inside every row's keys takes no compare
-        const bool edge = __any_sync(0xffffffffu, kTile * cc.t < max(lo_r[0], lo_r[1]) ||
-                                                      kTile * cc.t + kTile - 1 > min(hi_r[0], hi_r[1]));
-        float mx[2] = {-INFINITY, -INFINITY};
+        // a tile inside every row's keys, all its pages read, takes no compare
+        bool edge = ks == 0.f;
 #pragma unroll
-        for (int ut = 0; ut < 8; ++ut)
+        for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float x0 = s[ut][2 * j] * (fr[j] * ks), x1 = s[ut][2 * j + 1] * (fr[j] * ks);
-                const int key = key0 + 2 * ut;
-                const bool off0 = key < lo_r[j] || key > hi_r[j], off1 = key + 1 < lo_r[j] || key + 1 > hi_r[j];
+            for (int e = 0; e < 2; ++e) edge |= kTile * cc.t < lo_r[nr][e] || kTile * cc.t + kTile - 1 > hi_r[nr][e];
+        edge = __any_sync(0xffffffffu, edge);
+        uint32_t pt[NR][4][2];   // P^T blocks, transposed: the B operand of O^T
+        // scores in log2 units, masked; per block of rows
+        auto scores = [&](auto edge_tag, int nr, float (&mx)[2]) __attribute__((always_inline)) {
+            constexpr bool kEdge = decltype(edge_tag)::value;
+            const uint64_t f2 = f2_pack(fr[nr][0] * ks, fr[nr][1] * ks);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                float2 x = f2_unpack(f2_mul(f2_pack(s[nr][u >> 1][2 * (u & 1)], s[nr][u >> 1][2 * (u & 1) + 1]), f2));
+                const int key = key0 + 2 * u;
+                const bool off0 = kEdge && (ks == 0.f || key < lo_r[nr][0] || key > hi_r[nr][0]);
+                const bool off1 = kEdge && (ks == 0.f || key < lo_r[nr][1] || key > hi_r[nr][1]);
                 if (kCap) {
+                    // what lies behind the last token may be NaN: not into the pair
+                    if (off0) x.x = 0.f;
+                    if (off1) x.y = 0.f;
                     float r0, r1;
-                    if (edge) {   // what lies behind the last token may be NaN: not into the pair
-                        x0 = off0 ? 0.f : x0;
-                        x1 = off1 ? 0.f : x1;
+                    cap_r2(x.x, x.y, r0, r1);
+                    x.x = fmaf(-2.f * p.cap_log2, r0, p.cap_log2);
+                    x.y = fmaf(-2.f * p.cap_log2, r1, p.cap_log2);
+                }
+                if (off0) x.x = -INFINITY;
+                if (off1) x.y = -INFINITY;
+                s[nr][u >> 1][2 * (u & 1)] = x.x;
+                s[nr][u >> 1][2 * (u & 1) + 1] = x.y;
+                mx[0] = fmaxf(mx[0], x.x);
+                mx[1] = fmaxf(mx[1], x.y);
+            }
+        };
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+            float mx[2] = {-INFINITY, -INFINITY};
+            if (edge) scores(std::true_type{}, nr, mx);
+            else scores(std::false_type{}, nr, mx);
+            // p = 2^(x - m) for the row sum; P = 2^(x + ev - R) = p 2^(ev + m - R)
+            // for the product, one exp2 for both unless that factor leaves 32
+            // bits (V scales more than 2^100 apart)
+            float mref[2], rref[2], fv[2], grow[2];
+            bool any_grow = false, wide = false;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float y = keys_max(mx[e] + ev);
+                const float m = fmaxf(m_run[nr][e], keys_max(mx[e]));
+                mref[e] = m == -INFINITY ? 0.f : m;
+                l_run[nr][e] *= ex2(m_run[nr][e] - mref[e]);   // -inf before the first key: 0
+                m_run[nr][e] = m;
+                grow[e] = 1.f;
+                if (y > R[nr][e] + kLazy || (R[nr][e] == -INFINITY && y > R[nr][e])) {
+                    grow[e] = ex2(R[nr][e] - y);
+                    R[nr][e] = y;
+                    any_grow = true;
+                }
+                rref[e] = R[nr][e] == -INFINITY ? INFINITY : R[nr][e] - ev;   // no weight yet: P = 0
+                wide |= mref[e] - rref[e] > 100.f;
+                fv[e] = ex2(mref[e] - rref[e]);
+            }
+            if (__any_sync(0xffffffffu, any_grow)) {
+                const uint64_t g2 = f2_pack(grow[0], grow[1]);
+#pragma unroll
+                for (int dm = 0; dm < DM; ++dm)
+#pragma unroll
+                    for (int k = 0; k < 4; k += 2) {
+                        const float2 v = f2_unpack(f2_mul(f2_pack(acc[nr][dm][k], acc[nr][dm][k + 1]), g2));
+                        acc[nr][dm][k] = v.x;
+                        acc[nr][dm][k + 1] = v.y;
                     }
-                    cap_r2(x0, x1, r0, r1);
-                    x0 = fmaf(-2.f * p.cap_log2, r0, p.cap_log2);
-                    x1 = fmaf(-2.f * p.cap_log2, r1, p.cap_log2);
-                }
-                if (edge) {
-                    if (off0) x0 = -INFINITY;
-                    if (off1) x1 = -INFINITY;
-                }
-                s[ut][2 * j] = x0;
-                s[ut][2 * j + 1] = x1;
-                mx[j] = fmaxf(mx[j], fmaxf(x0, x1));
             }
-        uint32_t pa[4][4];
-        float mref[2], rref[2];
-        bool grow = false;
-        float ry[2];
+            wide = __any_sync(0xffffffffu, wide);
+            const uint64_t nm = f2_pack(-mref[0], -mref[1]), f2 = f2_pack(fv[0], fv[1]);
+            uint64_t sum = 0ull;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float y = quad_max(mx[j] + ev);
-            const float m = fmaxf(m_run[j], quad_max(mx[j]));
-            mref[j] = m == -INFINITY ? 0.f : m;
-            l_run[j] *= ex2(m_run[j] - mref[j]);   // -inf before the first key: 0
-            m_run[j] = m;
-            ry[j] = R[j];
-            if (y > R[j] + kLazy || R[j] == -INFINITY) {
-                ry[j] = fmaxf(R[j], y);
-                grow |= ry[j] != R[j];
+            for (int u = 0; u < 8; ++u) {
+                const float2 x = f2_unpack(f2_add(f2_pack(s[nr][u >> 1][2 * (u & 1)], s[nr][u >> 1][2 * (u & 1) + 1]), nm));
+                const uint64_t p2 = f2_pack(ex2(x.x), ex2(x.y));
+                sum = f2_add(sum, p2);
+                const float2 w = f2_unpack(f2_mul(p2, f2));
+                pt[nr][u >> 1][u & 1] = Cvt<__half>::pack(w.x, w.y);
             }
+            if (wide) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    pt[nr][u >> 1][u & 1] = Cvt<__half>::pack(ex2(s[nr][u >> 1][2 * (u & 1)] - rref[0]),
+                                                              ex2(s[nr][u >> 1][2 * (u & 1) + 1] - rref[1]));
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) pt[nr][u >> 1][u & 1] = transpose8(pt[nr][u >> 1][u & 1]);
+            const float2 t = f2_unpack(sum);
+            l_run[nr][0] += t.x;
+            l_run[nr][1] += t.y;
         }
-        if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float a = ry[j] == R[j] ? 1.f : ex2(R[j] - ry[j]);
-#pragma unroll
-                for (int dt = 0; dt < D / 8; ++dt) {
-                    acc[dt][2 * j] *= a;
-                    acc[dt][2 * j + 1] *= a;
-                }
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            R[j] = ry[j];
-            rref[j] = R[j] == -INFINITY ? INFINITY : R[j] - ev;   // no weight yet: P = 0
-            float sum = 0.f;
-#pragma unroll
-            for (int ut = 0; ut < 8; ++ut) {
-                const float x0 = s[ut][2 * j], x1 = s[ut][2 * j + 1];
-                sum += ex2(x0 - mref[j]) + ex2(x1 - mref[j]);
-                // k-step ut / 2: register j (first eight columns) or 2 + j
-                pa[ut >> 1][j + 2 * (ut & 1)] = Cvt<__half>::pack(ex2(x0 - rref[j]), ex2(x1 - rref[j]));
-            }
-            l_run[j] += sum;
-        }
-        // O += P V
-        cp_wait<2 * ST - 1>();
-        const int nv = n - key0;   // tokens of the group that exist: bytes behind them hold anything
+        // ---- O^T += V^T P^T
+        cp_wait<1>();
+        // tokens of the V group that exist: bytes behind them hold anything
+        const int nv = cc.n - (kTile * cc.t + 16 * q4);
         const bool tail = __any_sync(0xffffffffu, nv < 16);
 #pragma unroll
-        for (int dt = 0; dt < D / 8; ++dt) {
-            const uint4 v = ld_shared_v4(vt + 512 * dt);
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int dm = 0; dm < DM; ++dm) {
+            const uint4 v = ld_shared_v4(vt + 512 * (2 * dm)), u = ld_shared_v4(vt + 512 * (2 * dm + 1));
+            uint32_t w[4] = {v.x, v.y, v.z, v.w}, x[4] = {u.x, u.y, u.z, u.w};
             if (tail) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int c = min(max(nv - 4 * k, 0), 4);
-                    w[k] = c >= 4 ? w[k] : w[k] & ((1u << (8 * c)) - 1u);
+                    const uint32_t keep = c >= 4 ? 0xffffffffu : (1u << (8 * c)) - 1u;
+                    w[k] &= keep;
+                    x[k] &= keep;
                 }
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                uint32_t b0, b1;
-                e4m3x4_to_f16(w[k], b0, b1);
-                mma_f16(acc[dt], pa[k], b0, b1);
-            }
-        }
-        load_v(st);
-        --left;
-        if (ends || left == 0) close_segment(ends);
-        if (left > 0) cc.next(p);
-    };
-    while (true) {
+                uint32_t a[4];
+                e4m3x4_to_f16(w[k], a[0], a[2]);
+                e4m3x4_to_f16(x[k], a[1], a[3]);
 #pragma unroll
-        for (int st = 0; st < ST; ++st) {
-            step(st);
-            if (left == 0) {
-                cp_wait<0>();
-                return;
+                for (int nr = 0; nr < NR; ++nr) mma_f16(acc[nr][dm], a, pt[nr][k][0], pt[nr][k][1]);
             }
         }
+        load_v();
+        --left;
+        if (ends || left == 0) {
+            // the rows' results, or the piece's for the join
+            const int hk = cc.s / p.groups, rg = cc.s % p.groups;
+            const bool whole = begins && ends;
+            // The holders of the segment: workers z0 .. z1, of them lo .. hi in
+            // this CTA.  One that is the CTA's only holder writes the CTA's
+            // piece, else its own; the last to write joins them.
+            const int nt = cc.t1 - cc.t0;
+            const long long tile0 = (long long)(cc.b > 0 ? s_pre[cc.b - 1] : 0) * per_tile + (long long)cc.s * nt;
+            const int z0 = worker_of(tile0), z1 = worker_of(tile0 + nt - 1);
+            const int lo = max(z0, cta0), hi = min(z1, cta0 + W - 1);
+            const bool here = z0 >= cta0, over = z1 == hi, alone = lo == hi;
+            bool out = whole, mine = !whole && !alone;   // what is written next: rows, this worker's piece, the CTA's
+            while (true) {
+                const long long at = mine ? (long long)wid * 2 + (begins ? 1 : 0) : (long long)blockIdx.x * 2 + (here ? 1 : 0);
+                float *dst_acc = (mine ? p.acc : p.cta_acc) + at * C::PIECE;
+                float4 *dst_stat = (mine ? p.stat : p.cta_stat) + at * (NR * 8);
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) {
+                    const int row0 = (rg * NR + nr) * 8;
+                    float f[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float l = keys_sum(l_run[nr][e]);
+                        f[e] = out_factor(R[nr][e], m_run[nr][e], l);
+                        const int row = row0 + 2 * q4 + e;
+                        if (r8 == 0 && row < p.Sq * p.G) {
+                            if (!out)
+                                dst_stat[nr * 8 + 2 * q4 + e] = make_float4(m_run[nr][e], l, R[nr][e], 0.f);
+                            else if (p.lse)
+                                p.lse[((long long)cc.b * p.Hq + hk * p.G + row % p.G) * p.Sq + row / p.G] =
+                                    lse_of(m_run[nr][e], l);
+                        }
+                    }
+                    if (out) {
+#pragma unroll
+                        for (int dm = 0; dm < DM; ++dm) {
+                            // (a row without keys: its sums are 0, and so is the factor)
+                            float o[4] = {acc[nr][dm][0] * f[0], acc[nr][dm][1] * f[1], acc[nr][dm][2] * f[0],
+                                          acc[nr][dm][3] * f[1]};
+                            store_rows<D, T>(p, cc.b, hk, row0, lane, o, dm);
+                        }
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(dst_acc + nr * 8 * D) + lane;
+#pragma unroll
+                        for (int dm = 0; dm < DM; ++dm)
+                            dst[32 * dm] = make_float4(acc[nr][dm][0], acc[nr][dm][1], acc[nr][dm][2], acc[nr][dm][3]);
+                    }
+                }
+                if (!mine) {
+                    if (!out && !here && lane == 0) p.meta[blockIdx.x] = make_int4(cc.s, cc.b, z0 / W, over ? 1 : 0);
+                    break;
+                }
+                __threadfence_block();
+                __syncwarp();
+                int n = 0;
+                if (lane == 0) n = atomicAdd(&s_done[hi - cta0][over ? 0 : 1], 1);
+                n = __shfl_sync(0xffffffffu, n, 0);
+                __threadfence_block();
+                if (n != hi - lo) break;
+                // the last of the segment's holders here: their pieces in order,
+                // each one's loads in flight together
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) m_run[nr][e] = R[nr][e] = -INFINITY, l_run[nr][e] = 0.f;
+#pragma unroll
+                    for (int dm = 0; dm < DM; ++dm)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) acc[nr][dm][k] = 0.f;
+#pragma unroll 1
+                    for (int w = lo; w <= hi; ++w)
+                        add_piece<NR, DM>(p, p.acc, p.stat, (long long)w * 2 + (w == z0 ? 1 : 0), nr,
+                                          (rg * NR + nr) * 8, lane, m_run[nr], l_run[nr], R[nr], acc[nr]);
+                }
+                mine = false;
+                out = here && over;
+            }
+            fresh = true;
+        }
+        if (left == 0) break;
+        cc.next(p);
     }
+    cp_wait<0>();
 }
 
 // ------------------------------------------------------------------- join
-// One CTA per worker whose share begins inside a segment that ends in it: the
-// pieces of that segment (piece 1 of its first worker, piece 0 of the others)
-// joined in worker order, one warp per row at a time.
-template <int D, typename T>
-__global__ void __launch_bounds__(128) kv_join_kernel(const __grid_constant__ KvAttnParams p) {
-    const int wid = blockIdx.x;
-    const int4 me = p.meta[wid];
-    if (me.x < 0 || me.z == 0) return;
-    const int hk = me.x / p.groups, rg = me.x % p.groups, first = me.y, b = me.w;
-    constexpr int V = D / 32;   // dims per lane
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    for (int r = warp; r < 16; r += 4) {
-        const int row = rg * 16 + r;
-        if (row >= p.Sq * p.G) break;
-        auto slot = [&](int w) -> long long { return ((long long)w * 2 + (w == first ? 1 : 0)) * 16 + r; };
-        float M = -INFINITY, RM = -INFINITY;
-        for (int w = first + lane; w <= wid; w += 32) {
-            const float4 st = p.stat[slot(w)];
-            M = fmaxf(M, st.x);
-            RM = fmaxf(RM, st.z);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            RM = fmaxf(RM, __shfl_xor_sync(0xffffffffu, RM, o));
-        }
-        const float m0 = M == -INFINITY ? 0.f : M, r0 = RM == -INFINITY ? 0.f : RM;
-        float l = 0.f, x[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = 0.f;
-#pragma unroll 4
-        for (int w = first; w <= wid; ++w) {
-            const float4 st = p.stat[slot(w)];
-            l += st.y * ex2(st.x - m0);
-            const float f = ex2(st.z - r0);
-            const float *src = p.acc + slot(w) * D + V * lane;
-#pragma unroll
-            for (int i = 0; i < V; i += 2) {
-                const float2 v = *reinterpret_cast<const float2 *>(src + i);
-                x[i] = fmaf(v.x, f, x[i]);
-                x[i + 1] = fmaf(v.y, f, x[i + 1]);
-            }
-        }
-        const int i = row / p.G, hq = hk * p.G + row % p.G;
-        const float f = l == 0.f ? 0.f : ex2(r0 - m0) / l;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(reinterpret_cast<T *>(p.o) + (((long long)b * p.Sq + i) * p.Hq + hq) * D + V * lane);
-#pragma unroll
-        for (int k = 0; k < V / 2; ++k) dst[k] = l == 0.f ? 0u : Cvt<T>::pack(x[2 * k] * f, x[2 * k + 1] * f);
-        if (p.lse && lane == 0) p.lse[((long long)b * p.Hq + hq) * p.Sq + i] = lse_of(M, l);
+// One CTA per CTA of the attention kernel: if a segment begun in an earlier one
+// ends in it, the pieces of the CTAs between (piece 1 of the first, piece 0 of
+// the others) are joined and finished.  A warp per 16 dims.
+template <int D, int NR, typename T>
+__global__ void __launch_bounds__(D * 2) kv_join_kernel(const __grid_constant__ KvAttnParams p) {
+    constexpr int DM = D / 16;
+    pdl_wait();
+    const int4 me = p.meta[blockIdx.x];
+    if (me.x < 0 || me.w == 0) return;
+    const int dm = threadIdx.x / 32, lane = threadIdx.x % 32;
+#pragma unroll 1
+    for (int nr = 0; nr < NR; ++nr) {
+        const int row0 = ((me.x % p.groups) * NR + nr) * 8;
+        Joined x;
+        join_pieces<NR, DM>(p, p.cta_acc, p.cta_stat, me.z, blockIdx.x, me.z, nr, dm, row0, lane, x);
+        finish_rows<D, T>(p, x, me.y, me.x / p.groups, row0, dm, lane);
     }
 }
 
-template <int D, typename T, bool kCap>
+template <int D, int NR, typename T, bool kCap>
 cudaError_t launch_attn_t(KvAttnParams p, int sms, cudaStream_t stream) {
-    using C = KvCfg<D>;
-    auto kern = kv_attn_kernel<D, T, kCap>;
+    using C = KvCfg<D, NR>;
+    auto kern = kv_attn_kernel<D, NR, T, kCap>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     const int grid = sms < kKvSms ? sms : kKvSms;
     p.workers = grid * C::kWarps;
+    p.groups = (p.G * p.Sq + 8 * NR - 1) / (8 * NR);
     kern<<<grid, C::kWarps * 32, C::SMEM, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    kv_join_kernel<D, T><<<p.workers, 128, 0, stream>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(D * 2);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NR, T>, p);
+}
+
+template <int D, typename T>
+cudaError_t launch_attn_dt(const KvAttnParams &p, int sms, cudaStream_t stream) {
+    const bool cap = p.cap_log2 > 0.f;
+    if (p.G * p.Sq <= 8)
+        return cap ? launch_attn_t<D, 1, T, true>(p, sms, stream) : launch_attn_t<D, 1, T, false>(p, sms, stream);
+    return cap ? launch_attn_t<D, 2, T, true>(p, sms, stream) : launch_attn_t<D, 2, T, false>(p, sms, stream);
 }
 
 template <int D, typename T>
@@ -717,11 +917,10 @@ cudaError_t launch_append_t(const KvAppendParams &p, cudaStream_t stream) {
 
 }  // namespace
 
-int kv_warps(int D) { return D == 128 ? KvCfg<128>::kWarps : KvCfg<64>::kWarps; }
-
 size_t kv_workspace_bytes(int D) {
-    const size_t n = (size_t)kKvSms * kv_warps(D);
-    return n * 2 * 16 * D * sizeof(float) + n * 2 * 16 * sizeof(float4) + n * sizeof(int4);
+    // two pieces per worker and two per CTA: fragments and row statistics; what a CTA's piece 0 is
+    const size_t n = (size_t)kKvSms * kKvMaxWarps;
+    return kv_pieces_bytes(n, D) + kv_pieces_bytes(kKvSms, D) + (size_t)kKvSms * sizeof(int4);
 }
 
 cudaError_t launch_kv_append(const KvAppendParams &p, int D, int bf16, cudaStream_t stream) {
@@ -731,17 +930,9 @@ cudaError_t launch_kv_append(const KvAppendParams &p, int D, int bf16, cudaStrea
 }
 
 cudaError_t launch_kv_attn(const KvAttnParams &p, int D, int bf16, int sms, cudaStream_t stream) {
-    const bool cap = p.cap_log2 > 0.f;
-    if (D == 128) {
-        if (bf16)
-            return cap ? launch_attn_t<128, __nv_bfloat16, true>(p, sms, stream)
-                       : launch_attn_t<128, __nv_bfloat16, false>(p, sms, stream);
-        return cap ? launch_attn_t<128, __half, true>(p, sms, stream) : launch_attn_t<128, __half, false>(p, sms, stream);
-    }
-    if (bf16)
-        return cap ? launch_attn_t<64, __nv_bfloat16, true>(p, sms, stream)
-                   : launch_attn_t<64, __nv_bfloat16, false>(p, sms, stream);
-    return cap ? launch_attn_t<64, __half, true>(p, sms, stream) : launch_attn_t<64, __half, false>(p, sms, stream);
+    if (D == 128)
+        return bf16 ? launch_attn_dt<128, __nv_bfloat16>(p, sms, stream) : launch_attn_dt<128, __half>(p, sms, stream);
+    return bf16 ? launch_attn_dt<64, __nv_bfloat16>(p, sms, stream) : launch_attn_dt<64, __half>(p, sms, stream);
 }
 
 }  // namespace fa

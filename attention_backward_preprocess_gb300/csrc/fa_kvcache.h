@@ -33,22 +33,23 @@ struct KvAttnParams {
     void *o;
     float *lse;            // [B, Hq, Sq]; null: not written
     int B, Sq, Hq, G;
-    int groups;            // row groups of 16 (query, head) rows per kv head
+    int groups;            // row groups (8 or 16 (query, head) rows) per kv head
     int window;            // keys a query sees before its own; < 0: all
     float scale_log2;      // c log2(e)
     float cap_log2, cap_k; // softcap log2(e) and 2 log2(e) c / softcap; 0: no cap
-    // workspace: two pieces of up to 16 rows per worker
-    float *acc;            // [workers][2][16][D]
-    float4 *stat;          // [workers][2][16]  (m, l, R, -)
-    int4 *meta;            // [workers]  piece 0: segment, first worker, ends here, sequence
+    // workspace: two pieces of up to 16 rows per worker, and per CTA
+    float *acc, *cta_acc;        // [workers | CTAs][2] pieces in fragment order
+    float4 *stat, *cta_stat;     // [workers | CTAs][2][rows]  (m, l, R, -)
+    int4 *meta;                  // [CTAs]  piece 0: segment, sequence, first CTA, ends here
     int workers;
 };
 
-// Workers of the attention kernel at most: warps of kKvSms CTAs.  The grid is
-// the device's SM count (152 on GB300), held at kKvSms.
-constexpr int kKvSms = 160;
+// Workers of the attention kernel at most: kKvMaxWarps warps of kKvSms CTAs.
+// The grid is the device's SM count (152 on GB300), held at kKvSms.
+constexpr int kKvSms = 160, kKvMaxWarps = 16;
 constexpr int kKvMaxSeqs = 4096;   // sequences whose tile counts fit shared memory
-int kv_warps(int D);               // warps per CTA
+// bytes of two pieces of 16 rows for n holders: fragments, then statistics
+inline size_t kv_pieces_bytes(size_t n, int D) { return n * 2 * 16 * (D * sizeof(float) + sizeof(float4)); }
 size_t kv_workspace_bytes(int D);
 
 cudaError_t launch_kv_append(const KvAppendParams &p, int D, int bf16, cudaStream_t stream);

@@ -371,9 +371,9 @@ fa_status fa_bwd_ext(const void *q, const void *k, const void *v, const void *o,
  * 4096 sequences (fa_fwd_kvcache) or heads times tokens beyond 2^24.  A length
  * outside [0, max_pages page_size], more new tokens than max_new, or a table
  * entry that is no page is found on the device: such a sequence (or page) is
- * neither read nor written, its attention output is 0 / -inf (a bad page's
- * tokens count as zero keys and values), and fa_device_status(NULL, ...)
- * returns FA_ERR_INVALID_ARG.
+ * neither read nor written, its attention output is 0 / -inf (with a bad page,
+ * that over the other pages' tokens), and fa_device_status(NULL, ...) returns
+ * FA_ERR_INVALID_ARG.
  * ------------------------------------------------------------------------- */
 typedef struct {
     void *k, *v;
