@@ -179,6 +179,19 @@ bool encode_rows_map(CUtensorMap *m, const void *base, int D, int H, long long r
     return r == CUDA_SUCCESS;
 }
 
+// 2-D map over the cache's V as rows of page bytes, box of block tokens x D dims.
+bool encode_v_map(CUtensorMap *m, const void *base, int page, long long rows, int block, int D) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)page, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)page};
+    const cuuint32_t box[2] = {(cuuint32_t)block, (cuuint32_t)D};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // ------------------------------------------------- library-owned workspace
 struct DeviceWs {
     void *ptr = nullptr;
@@ -837,9 +850,12 @@ fa_status fa_fwd_kvcache(const void *q, const fa_kv_cache *cache, const int *cac
     p.Sq = Sq;
     p.Hq = Hq;
     p.G = Hq / cache->Hkv;
-    // tiles are counted in 32 bits per sequence sum
-    if ((long long)B * (cache->max_pages * (long long)cache->page_size / 64 + 1) > 0x7fffffffLL)
-        return FA_ERR_UNSUPPORTED;
+    // tiles of all sequences, heads and row groups are counted in 32 bits
+    const long long groups = ((long long)p.G * Sq + 7) / 8;
+    const long long tiles = 2 * ((long long)cache->max_pages * cache->page_size / 64 + 3);   // in halves
+    if (tiles * B > 0x7fffffffLL / ((long long)cache->Hkv * groups)) return FA_ERR_UNSUPPORTED;
+    // rows of V as the tensor loads see it
+    if ((long long)cache->num_pages * cache->Hkv * cache->D > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
     p.window = std::min(window_left, 1 << 30);   // positions stay inside 32 bits
     if ((st = check_device()) != FA_OK) return st;
     p.c.err = fa::fwd_error_word();
@@ -853,7 +869,16 @@ fa_status fa_fwd_kvcache(const void *q, const fa_kv_cache *cache, const int *cac
     p.cta_stat = reinterpret_cast<float4 *>(w + (size_t)fa::kKvSms * 2 * 16 * cache->D * sizeof(float));
     w += fa::kv_pieces_bytes(fa::kKvSms, cache->D);
     p.meta = reinterpret_cast<int4 *>(w);
-    return cuda_status(fa::launch_kv_attn(p, cache->D, dtype == FA_BF16, sm_count(), stream));
+    p.budget_ns = g_budget_ns.load();
+    const int ps = cache->page_size;
+    p.v_block = ps % 64 == 0 ? 64 : ps % 32 == 0 ? 32 : 16;
+    // pads that spread the blocks of a lane's four rows over the banks; tensor
+    // loads (a block narrower than its page) need 128-byte destinations
+    p.v_pad = p.v_block != ps || ps == 64 ? 0 : ps == 32 ? 64 : 32;
+    CUtensorMap mv;
+    if (!encode_v_map(&mv, cache->v, ps, (long long)cache->num_pages * cache->Hkv * cache->D, p.v_block, cache->D))
+        return FA_ERR_CUDA;
+    return cuda_status(fa::launch_kv_attn(p, mv, cache->D, dtype == FA_BF16, sm_count(), stream));
 }
 
 size_t fa_mask_ranges_bytes(int B, int S) {

@@ -182,46 +182,55 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
 // step's few rows pad to 8 and not to 16.  Bytes bound it (2 D bytes per key
 // against 4 D flops per row and key), so the design keeps reads in flight:
 // every warp is a worker of its own with a contiguous share of all (sequence,
-// kv head, row group, 64-key tile) work, each lane copies the pieces of K and
-// V it needs itself into shared memory (cp.async, no barrier: a lane reads
-// only what it copied), and e4m3 becomes f16 in registers on the way into the
-// tensor core.  Equal shares whatever the lengths; a (sequence, kv head) cut
+// kv head, row group, 64-key tile) work and its own K and V slot in shared
+// memory, filled by bulk copies (one per 16 keys of K, one per page of V) that
+// go out as soon as the slot has been read.  (With a 16-byte cp.async per lane
+// instead, 3600 of a tile's 8200 cycles went by issuing the 32 copies.)  Equal shares whatever the lengths; a (sequence, kv head) cut
 // between workers leaves pieces that a second kernel joins in a fixed order.
 //
-// e4m3 fits f16 exactly.  Q (bf16 or f16) enters as f16 under a power of two
-// per row that brings its largest magnitude to [2^14, 2^15): exact but for
-// values 2^-29 below that.  P enters as f16 <= 2^8 against a running maximum R
-// of score + log2(V scale), so the V scales cost no range; the row sums keep
-// the running maximum of the scores alone.
+// K goes to the tensor core as it lies.  Q is split into e4m3 parts, each what
+// the one before left, times 16: a bf16 value (8 significant bits) is two
+// parts of four bits, an f16 value (11) three, under a power of two per row
+// that brings its largest magnitude to [2^7, 2^8).  The parts are exact but for
+// values more than 2^13 below that (the last part's smallest step, 2^-13 or
+// 2^-17 of the row's units); their products run in accumulators of their own,
+// the e4m3 product adds in full 32 bits (measured: within 2^-22 of the sum of
+// magnitudes), and it is four times as fast per key as the f16 one behind two
+// conversions per value.  For V, e4m3 fits f16 exactly; P enters as f16 <= 2^8
+// against a running maximum R of score + log2(V scale), so the V scales cost no
+// range; the row sums keep the running maximum of the scores alone.
 //
 // Fragments.  The contracted axis may be permuted at will if both operands
 // agree: a lane holds 16 consecutive bytes of a key's row (K) or of a dim's
-// row of tokens (V), i.e. four k-steps of four values.  Row 8 h + r of S^T
-// tile t is key 16 (r / 2) + r % 2 + 4 t + 2 h: all keys of lanes r = 4 r / 4
-// are then of one 16-key group (one page, one scale), and the 8x8 blocks of
-// P, transposed across the lanes (movmatrix), are where the product with V
-// wants them.
+// row of tokens (V).  Row 8 h + r of S^T tile t is key 16 (r / 2) + r % 2 + 4 t
+// + 2 h: all keys of a lane are then of one 16-key group (one page, one scale),
+// and the 8x8 blocks of P, transposed across the lanes (movmatrix), are where
+// the product with V wants them.
 constexpr int kTile = 64;   // keys per step
 constexpr float kLazy = 8.f;
+template <typename T> constexpr int kQParts = Cvt<T>::is_bf16 ? 2 : 3;
 
-// NR: 8-row blocks of a worker's rows (1 or 2).  The warps per CTA fill shared
-// memory (K and V of one tile each: @WARPS@).
+// NR: 8-row blocks of a worker's rows (1 or 2).  Warps per CTA: at D = 128, 8
+// with up to 255 registers each stream at 21 bytes per cycle and SM; 12 with
+// 168 spill, and every part of a step took 1.6 to 3 times as long (75 against
+// 66 us on 64 requests of 256 to 8192 tokens).
 template <int D, int NR>
 struct KvCfg {
-    static constexpr int kWarps = (D == 128) ? (NR == 1 ? 12 : 8) : (NR == 1 ? 16 : 12);
+    static constexpr int kWarps = (D == 128 || NR == 2) ? 8 : 12;
     static constexpr int KB = kTile * D;                 // bytes of a K (or V) tile
-    static constexpr int SMEM = kWarps * 2 * KB;
+    static constexpr int VB = KB + 128;                  // V's blocks lie apart (kv_block_pad)
+    static constexpr int SMEM = kWarps * (KB + VB);
     static constexpr int PIECE = NR * 8 * D;             // floats of a piece
     static_assert(kWarps <= kKvMaxWarps, "the workspace holds kKvMaxWarps workers per SM");
+    static_assert(SMEM + 8 * kKvMaxSeqs + 2048 <= 232448, "shared memory overflow");
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool on) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// 2-D tiled load (bytes along a row, row) completing on an mbarrier.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(m), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
 }
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     uint4 v;
@@ -232,6 +241,16 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float lg2_approx(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 // an 8x8 block of 16-bit values transposed across the warp
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
@@ -251,11 +270,6 @@ __device__ __forceinline__ float keys_sum(float v) {
     return v;
 }
 
-// Tokens of sequence b, 0 where the length is outside the table.
-__device__ __forceinline__ int kv_len(const KvAttnParams &p, int b) {
-    const int n = __ldg(p.len + b);
-    return (n < 0 || (long long)n > (long long)p.c.max_pages * p.c.page) ? 0 : n;
-}
 // First key any of the sequence's queries sees.
 __device__ __forceinline__ int kv_first(const KvAttnParams &p, int n) {
     return p.window < 0 ? 0 : max(0, n - p.Sq - min(p.window, n));
@@ -263,25 +277,36 @@ __device__ __forceinline__ int kv_first(const KvAttnParams &p, int n) {
 __device__ __forceinline__ int kv_tiles(const KvAttnParams &p, int n) {
     return (n + kTile - 1) / kTile - kv_first(p, n) / kTile;
 }
+// Work is shared out in half tiles: a segment of nt tiles counts 2 nt + 2, for
+// opening and closing it takes about as long as a tile.  A border x half tiles
+// into a segment lies before tile kv_border(x); tile t belongs to the worker
+// that holds half tile 2 t + 2.  (Shared out by tiles alone, workers with short
+// sequences took 145 k cycles where the mean was 118 k.)
+__device__ __forceinline__ int kv_units(int nt) { return nt > 0 ? 2 * nt + 2 : 0; }
+__device__ __forceinline__ int kv_border(int x) { return max(x - 1, 0) / 2; }
 
-// A worker's place in the work: tile t of [t0, t1) of (sequence b, head and row
-// group s).
+// A worker's place in the work: tile t of [t0, t1) of sequence b, kv head hk and
+// row group rg.
 struct Cursor {
-    int b, s, t, t0, t1, n, lo;
-    __device__ __forceinline__ void open(const KvAttnParams &p) {   // sequence b
-        n = kv_len(p, b);
+    int b, hk, rg, t, t0, t1, n, lo;
+    __device__ __forceinline__ void open(const KvAttnParams &p, const int *lens) {   // sequence b
+        n = lens[b];
         lo = kv_first(p, n);
         t0 = lo / kTile;
         t1 = (n + kTile - 1) / kTile;
     }
-    __device__ __forceinline__ void next(const KvAttnParams &p) {
+    __device__ __forceinline__ void next(const KvAttnParams &p, const int *lens) {
         if (++t < t1) return;
-        if (++s == p.c.Hkv * p.groups) {
-            s = 0;
-            do {
-                if (++b >= p.B) return;   // the end of all work
-                open(p);
-            } while (t1 <= t0);
+        t = 0;   // (the end of all work: 0)
+        if (++rg == p.groups) {
+            rg = 0;
+            if (++hk == p.c.Hkv) {
+                hk = 0;
+                do {
+                    if (++b >= p.B) return;   // the end of all work
+                    open(p, lens);
+                } while (t1 <= t0);
+            }
         }
         t = t0;
     }
@@ -420,20 +445,29 @@ __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.laun
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <int D, int NR, typename T, bool kCap>
-__global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1) kv_attn_kernel(const __grid_constant__ KvAttnParams p) {
+__global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1)
+    kv_attn_kernel(const __grid_constant__ KvAttnParams p, const __grid_constant__ CUtensorMap map_v) {
     using C = KvCfg<D, NR>;
-    constexpr int W = C::kWarps, HH = D / 64, KS = D / 16, DM = D / 16;
+    constexpr int W = C::kWarps, HH = D / 64, K32 = D / 32, DM = D / 16, QP = kQParts<T>;
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    __shared__ int s_pre[kKvMaxSeqs];   // tiles of sequences 0 .. b, inclusive
+    __shared__ int s_pre[kKvMaxSeqs];   // half tiles of one head and row group of sequences 0 .. b, inclusive
+    __shared__ int s_len[kKvMaxSeqs];   // their tokens, 0 where the length is outside the table
     __shared__ int s_warp[W];
     // pieces written of the segment whose last holder in this CTA is worker w
     // and which ends there (0) or goes on (1)
     __shared__ int s_done[W][2];
+    __shared__ __align__(8) uint64_t s_bar[W][2];   // K, V of the worker's tile landed
+    __shared__ int s_abort;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int r8 = lane >> 2, q4 = lane & 3;
 
     if (threadIdx.x == 0) p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    if (lane < 2) s_done[warp][lane] = 0;
+    if (threadIdx.x == 0) s_abort = 0;
+    if (lane < 2) {
+        s_done[warp][lane] = 0;
+        mbar_init(smem_u32(&s_bar[warp][lane]), 1);
+        fence_mbar_init();
+    }
     // ---- the work: tiles per sequence, summed
     const int per_tile = p.c.Hkv * p.groups;
     int carry = 0;
@@ -441,12 +475,13 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1) kv_attn_kernel(c
         const int b = b0 + threadIdx.x;
         int x = 0;
         if (b < p.B) {
-            const int n = __ldg(p.len + b);
+            int n = __ldg(p.len + b);
             if (n < 0 || (long long)n > (long long)p.c.max_pages * p.c.page) {
                 if (blockIdx.x == 0) atomicOr(p.c.err, kErrBadLength);
-            } else {
-                x = kv_tiles(p, n);
+                n = 0;
             }
+            x = kv_units(kv_tiles(p, n));
+            s_len[b] = n;
         }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -474,40 +509,75 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1) kv_attn_kernel(c
         if (p.lse)
             for (int i = threadIdx.x; i < p.Sq * p.Hq; i += W * 32) p.lse[(long long)b * p.Sq * p.Hq + i] = -INFINITY;
     }
-    const long long total = (long long)carry * per_tile;
-    // shares of the workers: worker c takes tiles [c total / N, (c + 1) total / N)
-    const int cta0 = blockIdx.x * W, wid = cta0 + warp;
-    const long long N = min((long long)p.workers, total);
+    const int total = carry * per_tile;   // (the host keeps it below 2^31)
+    // shares of the workers: total / N half tiles each, one more for the first
+    // total % N; a worker holds at least two tiles' worth, so that few pieces
+    // are made of little work
+    const int cta0 = blockIdx.x * W, wid = cta0 + warp, N = min(p.workers, max(total / 4, 1));
     pdl_launch();
-    if (wid >= N) return;
-    const long long w0 = total * wid / N, w1 = total * (wid + 1) / N;
-    auto worker_of = [&](long long w) -> int { return (int)(((w + 1) * N - 1) / total); };
-
-    Cursor pc;   // what is loaded next
-    {
-        const int u = (int)(w0 / per_tile);   // tile over the sequences, if every tile came once
-        int lo = 0, hi = p.B - 1;
+    if (wid >= N || total == 0) return;
+    const int share = total / N, more = total - share * N;
+    const int w0 = wid * share + min(wid, more), w1 = w0 + share + (wid < more ? 1 : 0);
+    auto worker_of = [&](int w) -> int {
+        const int head = (share + 1) * more;
+        return w < head ? w / (share + 1) : more + (w - head) / share;
+    };
+    // the tile behind a border (past the last one: b == B)
+    auto place = [&](int w, Cursor &c) {
+        const int u = w / per_tile;   // the border over the sequences, if every half tile came once
+        int lo = 0, hi = p.B;
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (s_pre[mid] > u) hi = mid;
             else lo = mid + 1;
         }
-        pc.b = lo;
-        pc.open(p);
-        const long long in = w0 - (long long)(lo > 0 ? s_pre[lo - 1] : 0) * per_tile;
-        const int nt = pc.t1 - pc.t0;
-        pc.s = (int)(in / nt);
-        pc.t = pc.t0 + (int)(in - (long long)pc.s * nt);
-    }
+        c.b = lo;
+        c.hk = c.rg = c.t = 0;
+        if (lo == p.B) return;
+        c.open(p, s_len);
+        const int in = w - (lo > 0 ? s_pre[lo - 1] : 0) * per_tile, units = kv_units(c.t1 - c.t0);
+        const int seg = in / units;
+        c.hk = seg / p.groups;
+        c.rg = seg - c.hk * p.groups;
+        c.t = c.t0 + kv_border(in - seg * units) - 1;
+        c.next(p, s_len);   // (a border behind a segment's last tile: the next one's first)
+    };
+    Cursor pc, end;   // what is loaded next, and where the worker stops
+    place(w0, pc);
+    place(w1, end);
+    auto at_end = [&](const Cursor &c) -> bool {
+        return c.b == end.b && c.hk == end.hk && c.rg == end.rg && c.t == end.t;
+    };
+    if (at_end(pc)) return;
     Cursor cc = pc;   // what is computed next
-    int left = (int)(w1 - w0), to_load = left;
+    {   // the first rows of Q on their way while the block table is read
+        const int row = cc.rg * NR * 8 + r8;
+        if (row < p.Sq * p.G) {
+            const T *src = reinterpret_cast<const T *>(p.q) +
+                           (((long long)cc.b * p.Sq + row / p.G) * p.Hq + cc.hk * p.G + row % p.G) * D + q4 * (D / 4);
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+        }
+    }
+    bool loads = true;   // pc is a tile of this worker's
 
-    const uint32_t kt = smem_u32(smem_raw) + warp * (2 * C::KB) + 16 * lane, vt = kt + C::KB;
-    // page of 16-key group (lane % 4) of a tile
+    const uint32_t kt = smem_u32(smem_raw) + warp * (C::KB + C::VB), vt = kt + C::KB;
+    const uint32_t k_bar = smem_u32(&s_bar[warp][0]), v_bar = smem_u32(&s_bar[warp][1]);
+    const WaitCtl wctl{&s_abort, p.c.err, p.budget_ns};
+    uint32_t phase = 0;   // of both barriers: the tile being computed
+    bool ahead = false;   // gave up with the next tile's K on its way
+    // V in shared memory: 64 / bw blocks of bw tokens, D rows each, a pad apart
+    const int bw = p.v_block, v_step = D * bw + p.v_pad;
+    // this lane's 16 tokens of dim r8, and its keys' rows
+    const uint32_t v_at = vt + (16 * q4 / bw) * v_step + (16 * q4) % bw + r8 * bw;
+    const uint32_t k_at = kt + (16 * (r8 >> 1) + (r8 & 1)) * D + 16 * q4;
+    // 16-key group x of a sequence: its page, and its place in the page
+    auto page_of = [&](int x) -> int { return p.page_magic ? __umulhi((uint32_t)x, p.page_magic) : x; };
+    const int page16 = p.c.page / 16;
+    // page of group (lane % 4) of a tile
     auto lookup = [&](const Cursor &c) -> int {
-        const int tok = kTile * c.t + 16 * q4;
-        if (tok >= c.n || tok + 16 <= c.lo) return -1;    // a group nobody sees: not read
-        const int page = __ldg(p.c.table + (long long)c.b * p.c.max_pages + tok / p.c.page);
+        const int x = 4 * c.t + q4;
+        if (16 * x >= c.n || 16 * x + 16 <= c.lo) return -1;    // a group nobody sees: not read
+        const int page = __ldg(p.c.table + (long long)c.b * p.c.max_pages + page_of(x));
         if (page < 0 || page >= p.c.num_pages) {
             atomicOr(p.c.err, kErrBadPage);
             return -1;
@@ -516,60 +586,76 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1) kv_attn_kernel(c
     };
     int pg = lookup(pc);
     float ksc = 0.f, vsc = 0.f;   // scales of group r8 / 2 (a lane's keys) of the loaded tile
-    // K of the tile at pc (and its scales), then V of the same tile
+    bool v_ok = false;            // the lane's 16 tokens (group q4) of it are there
+    // K of the tile at pc (and its scales), then V of the same tile.  Lanes 0-3
+    // copy a group of 16 keys each; groups not read are masked.
     auto load_k = [&]() __attribute__((always_inline)) {
-        if (to_load > 0) {
-            const int hk = pc.s / p.groups, grp = r8 >> 1;
-            const int page = __shfl_sync(0xffffffffu, pg, grp);
-            const long long ph = (long long)max(page, 0) * p.c.Hkv + hk;
-            ksc = page >= 0 ? __ldg(p.c.k_scale + ph) : 0.f;
-            vsc = page >= 0 ? __ldg(p.c.v_scale + ph) : 0.f;
-            const int in_page = (kTile * pc.t + 16 * grp) % p.c.page + (r8 & 1);
-            const uint8_t *src = p.c.k + (ph * p.c.page + in_page) * D + 16 * q4;
-#pragma unroll
-            for (int u = 0; u < 8; ++u)   // u = 2 t + h: key + 2 u
-#pragma unroll
-                for (int hh = 0; hh < HH; ++hh) cp_async16(kt + 512 * (u * HH + hh), src + 2 * u * D + 64 * hh, page >= 0);
+        if (!loads) return;
+        const int page = __shfl_sync(0xffffffffu, pg, r8 >> 1);   // (also: every lane has read the slot)
+        const long long ph = (long long)max(page, 0) * p.c.Hkv + pc.hk;
+        ksc = page >= 0 ? __ldg(p.c.k_scale + ph) : 0.f;
+        vsc = page >= 0 ? __ldg(p.c.v_scale + ph) : 0.f;
+        const bool mine = lane < 4 && pg >= 0;
+        const int n = __popc(__ballot_sync(0xffffffffu, mine));
+        if (lane == 0) mbar_arrive_expect_tx(k_bar, n * 16 * D);
+        __syncwarp();
+        if (mine) {
+            const int x = 4 * pc.t + lane;
+            const long long row = ((long long)pg * p.c.Hkv + pc.hk) * p.c.page + 16 * (x - page_of(x) * page16);
+            bulk_load(kt + lane * 16 * D, p.c.k + row * D, 16 * D, k_bar);
         }
-        cp_commit();
     };
     auto load_v = [&]() __attribute__((always_inline)) {
-        if (to_load > 0) {
-            const int hk = pc.s / p.groups;
-            const int in_page = (kTile * pc.t + 16 * q4) % p.c.page;
-            const uint8_t *src = p.c.v + (((long long)max(pg, 0) * p.c.Hkv + hk) * D + r8) * p.c.page + in_page;
-            const long long step = 8 * p.c.page;
+        if (!loads) return;
+        // lanes 0 .. 64 / bw - 1 copy a block of bw tokens each, if one of its
+        // groups is read (the groups of a block share a page)
+        v_ok = pg >= 0;
+        const uint32_t ok = __ballot_sync(0xffffffffu, pg >= 0) & 15u;
+        const int per = bw / 16, first = lane * per;          // the block's groups
+        int page = -1;
 #pragma unroll
-            for (int dt = 0; dt < D / 8; ++dt) {
-                cp_async16(vt + 512 * dt, src, pg >= 0);
-                src += step;
-            }
-            if (--to_load > 0) {
-                pc.next(p);
-                pg = lookup(pc);
+        for (int g = 0; g < 4; ++g) {
+            const int pgg = __shfl_sync(0xffffffffu, pg, g);
+            if (g >= first && g < first + per) page = max(page, pgg);
+        }
+        const bool mine = lane < 64 / bw && (ok >> first & ((1u << per) - 1u)) != 0u;
+        const int n = __popc(__ballot_sync(0xffffffffu, mine));
+        if (lane == 0) mbar_arrive_expect_tx(v_bar, n * bw * D);
+        __syncwarp();
+        if (mine) {
+            const long long ph = (long long)page * p.c.Hkv + pc.hk;
+            const uint32_t dst = vt + lane * v_step;
+            if (bw == p.c.page) {
+                bulk_load(dst, p.c.v + ph * D * bw, bw * D, v_bar);
+            } else {
+                const int x = 4 * pc.t + first;
+                tma_load_2d(dst, &map_v, v_bar, 16 * (x - page_of(x) * page16), (int)(ph * D));
             }
         }
-        cp_commit();
+        pc.next(p, s_len);
+        loads = !at_end(pc);
+        if (loads) pg = lookup(pc);
     };
     load_k();
     load_v();
 
     // ---- state of the segment being computed: row block nr, row 2 q4 + e of it
-    uint32_t qb[NR][KS][2];      // Q fragments (f16): row r8 of the block
+    uint32_t qb[NR][QP][K32][2];   // parts of Q (e4m3): row r8 of the block
     float fr[NR][2];             // undoes Q's power of two, times c log2(e) (or the cap's factor)
     int lo_r[NR][2], hi_r[NR][2];   // visible keys
+    int lo_all = 0, hi_all = 0;     // keys every row of the worker sees
     float acc[NR][DM][4];
     float m_run[NR][2], l_run[NR][2], R[NR][2];
     bool fresh = true, begins = false;
     while (true) {
         if (fresh) {
-            const int hk = cc.s / p.groups, rg = cc.s % p.groups;
+            lo_all = 0, hi_all = 0x7fffffff;
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr) {
-                const int row = (rg * NR + nr) * 8 + r8;
+                const int row = (cc.rg * NR + nr) * 8 + r8;
                 const bool live = row < p.Sq * p.G;
                 const int i = live ? row / p.G : p.Sq - 1, g = live ? row % p.G : 0;
-                const T *src = reinterpret_cast<const T *>(p.q) + (((long long)cc.b * p.Sq + i) * p.Hq + hk * p.G + g) * D + 16 * q4;
+                const T *src = reinterpret_cast<const T *>(p.q) + (((long long)cc.b * p.Sq + i) * p.Hq + cc.hk * p.G + g) * D + 16 * q4;
                 uint32_t raw[HH][8];
                 float amax = 0.f;
 #pragma unroll
@@ -587,20 +673,34 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1) kv_attn_kernel(c
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                 const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 126);
-                const float up = pow2(14 - e), down = pow2(e - 14) * (kCap ? p.cap_k : p.scale_log2);
+                const float up = pow2(7 - e), down = pow2(e - 7) * (kCap ? p.cap_k : p.scale_log2);
 #pragma unroll
                 for (int hh = 0; hh < HH; ++hh)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {   // word k of the row: k-step 4 hh + k / 2
-                        const float2 f = Cvt<T>::unpack(raw[hh][k]);
-                        qb[nr][4 * hh + k / 2][k & 1] = Cvt<__half>::pack(f.x * up, f.y * up);
+                    for (int k = 0; k < 8; k += 2) {   // words k, k + 1: four dims, register (k / 2) % 2 of k-step 2 hh + k / 4
+                        const float2 a = Cvt<T>::unpack(raw[hh][k]), c = Cvt<T>::unpack(raw[hh][k + 1]);
+                        float x[4] = {a.x * up, a.y * up, c.x * up, c.y * up};
+#pragma unroll
+                        for (int part = 0; part < QP; ++part) {
+                            const uint32_t w = f32_to_e4m3x2(x[0], x[1]) | f32_to_e4m3x2(x[2], x[3]) << 16;
+                            qb[nr][part][2 * hh + k / 4][(k / 2) & 1] = w;
+                            uint32_t lo, hi;
+                            e4m3x4_to_f16(w, lo, hi);
+                            const float2 y = Cvt<__half>::unpack(lo), z = Cvt<__half>::unpack(hi);
+                            x[0] = (x[0] - y.x) * 16.f, x[1] = (x[1] - y.y) * 16.f;
+                            x[2] = (x[2] - z.x) * 16.f, x[3] = (x[3] - z.y) * 16.f;
+                        }
                     }
+                // a NaN or infinite query: what is left of it is NaN, for its own row only
+                const float dn = amax < INFINITY ? down : NAN;
                 const int hi = cc.n - p.Sq + i;
 #pragma unroll
                 for (int e2 = 0; e2 < 2; ++e2) {   // the rows a lane's scores belong to
-                    fr[nr][e2] = __shfl_sync(0xffffffffu, down, 4 * (2 * q4 + e2));
+                    fr[nr][e2] = __shfl_sync(0xffffffffu, dn, 4 * (2 * q4 + e2));
                     hi_r[nr][e2] = __shfl_sync(0xffffffffu, hi, 4 * (2 * q4 + e2));
                     lo_r[nr][e2] = p.window < 0 ? 0 : max(0, hi_r[nr][e2] - p.window);
+                    lo_all = max(lo_all, lo_r[nr][e2]);
+                    hi_all = min(hi_all, hi_r[nr][e2]);
                     m_run[nr][e2] = R[nr][e2] = -INFINITY;
                     l_run[nr][e2] = 0.f;
                 }
@@ -609,46 +709,45 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1) kv_attn_kernel(c
 #pragma unroll
                     for (int k = 0; k < 4; ++k) acc[nr][dm][k] = 0.f;
             }
+            lo_all = __reduce_max_sync(0xffffffffu, lo_all);
+            hi_all = __reduce_min_sync(0xffffffffu, hi_all);
             begins = cc.t == cc.t0;
             fresh = false;
         }
         // ---- S^T = K Q^T
-        cp_wait<1>();
+        if (!mbar_wait_warp(k_bar, phase, wctl)) break;
         float s[NR][4][4];
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
+        for (int t = 0; t < 4; ++t) {
+            uint32_t a[K32][4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int hh = 0; hh < HH; ++hh) {
+                const uint4 v = ld_shared_v4(k_at + 4 * t * D + 64 * hh), u = ld_shared_v4(k_at + (4 * t + 2) * D + 64 * hh);
+                a[2 * hh][0] = v.x, a[2 * hh][1] = u.x, a[2 * hh][2] = v.y, a[2 * hh][3] = u.y;
+                a[2 * hh + 1][0] = v.z, a[2 * hh + 1][1] = u.z, a[2 * hh + 1][2] = v.w, a[2 * hh + 1][3] = u.w;
+            }
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) {
+                // the last part first, a sixteenth of its sum under the next
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s[nr][t][i] = 0.f;
 #pragma unroll
-        for (int hh = 0; hh < HH; ++hh) {
+                for (int q = QP - 1; q >= 0; --q) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const uint4 v = ld_shared_v4(kt + 512 * (2 * t * HH + hh)), u = ld_shared_v4(kt + 512 * ((2 * t + 1) * HH + hh));
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w}, x[4] = {u.x, u.y, u.z, u.w};
+                    for (int i = 0; i < 4; ++i) s[nr][t][i] = q < QP - 1 ? s[nr][t][i] * 0.0625f : s[nr][t][i];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t a[4];
-                    e4m3x4_to_f16(w[k], a[0], a[2]);
-                    e4m3x4_to_f16(x[k], a[1], a[3]);
-#pragma unroll
-                    for (int nr = 0; nr < NR; ++nr) mma_f16(s[nr][t], a, qb[nr][4 * hh + k][0], qb[nr][4 * hh + k][1]);
+                    for (int k = 0; k < K32; ++k) mma_e4m3(s[nr][t], a[k], qb[nr][q][k][0], qb[nr][q][k][1]);
                 }
             }
         }
         const float ks = ksc, vs = vsc;
         const int key0 = kTile * cc.t + 16 * (r8 >> 1) + (r8 & 1);   // the lane's keys: key0 + 2 u
         const bool ends = cc.t + 1 == cc.t1;
+        const bool v_here = v_ok;
         load_k();   // this tile's K has been read
-        const float ev = vs > 0.f ? log2f(vs) : -INFINITY;   // exact for a power of two
+        const float ev = vs > 0.f ? lg2_approx(vs) : -INFINITY;
         // a tile inside every row's keys, all its pages read, takes no compare
-        bool edge = ks == 0.f;
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) edge |= kTile * cc.t < lo_r[nr][e] || kTile * cc.t + kTile - 1 > hi_r[nr][e];
-        edge = __any_sync(0xffffffffu, edge);
+        const bool edge = __any_sync(0xffffffffu, ks == 0.f) || kTile * cc.t < lo_all || kTile * cc.t + kTile - 1 > hi_all;
         uint32_t pt[NR][4][2];   // P^T blocks, transposed: the B operand of O^T
         // scores in log2 units, masked; per block of rows
         auto scores = [&](auto edge_tag, int nr, float (&mx)[2]) __attribute__((always_inline)) {
@@ -704,7 +803,7 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1) kv_attn_kernel(c
                 wide |= mref[e] - rref[e] > 100.f;
                 fv[e] = ex2(mref[e] - rref[e]);
             }
-            if (__any_sync(0xffffffffu, any_grow)) {
+            if (__any_sync(0xffffffffu, any_grow || wide)) {
                 const uint64_t g2 = f2_pack(grow[0], grow[1]);
 #pragma unroll
                 for (int dm = 0; dm < DM; ++dm)
@@ -714,8 +813,8 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1) kv_attn_kernel(c
                         acc[nr][dm][k] = v.x;
                         acc[nr][dm][k + 1] = v.y;
                     }
+                wide = __any_sync(0xffffffffu, wide);
             }
-            wide = __any_sync(0xffffffffu, wide);
             const uint64_t nm = f2_pack(-mref[0], -mref[1]), f2 = f2_pack(fv[0], fv[1]);
             uint64_t sum = 0ull;
 #pragma unroll
@@ -739,15 +838,19 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1) kv_attn_kernel(c
             l_run[nr][1] += t.y;
         }
         // ---- O^T += V^T P^T
-        cp_wait<1>();
-        // tokens of the V group that exist: bytes behind them hold anything
-        const int nv = cc.n - (kTile * cc.t + 16 * q4);
-        const bool tail = __any_sync(0xffffffffu, nv < 16);
+        if (!mbar_wait_warp(v_bar, phase, wctl)) {
+            ahead = loads;
+            break;
+        }
+        phase ^= 1u;
+        // tokens of the V group that exist: bytes behind them hold anything (such
+        // a tile has keys no row sees)
+        const int nv = v_here ? cc.n - (kTile * cc.t + 16 * q4) : 0;
 #pragma unroll
         for (int dm = 0; dm < DM; ++dm) {
-            const uint4 v = ld_shared_v4(vt + 512 * (2 * dm)), u = ld_shared_v4(vt + 512 * (2 * dm + 1));
+            const uint4 v = ld_shared_v4(v_at + 16 * dm * bw), u = ld_shared_v4(v_at + (16 * dm + 8) * bw);
             uint32_t w[4] = {v.x, v.y, v.z, v.w}, x[4] = {u.x, u.y, u.z, u.w};
-            if (tail) {
+            if (edge) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int c = min(max(nv - 4 * k, 0), 4);
@@ -766,17 +869,19 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1) kv_attn_kernel(c
             }
         }
         load_v();
-        --left;
-        if (ends || left == 0) {
+        Cursor nx = cc;
+        nx.next(p, s_len);
+        const bool done = at_end(nx);
+        if (ends || done) {
             // the rows' results, or the piece's for the join
-            const int hk = cc.s / p.groups, rg = cc.s % p.groups;
+            const int hk = cc.hk, rg = cc.rg, seg = hk * p.groups + rg;
             const bool whole = begins && ends;
             // The holders of the segment: workers z0 .. z1, of them lo .. hi in
             // this CTA.  One that is the CTA's only holder writes the CTA's
             // piece, else its own; the last to write joins them.
             const int nt = cc.t1 - cc.t0;
-            const long long tile0 = (long long)(cc.b > 0 ? s_pre[cc.b - 1] : 0) * per_tile + (long long)cc.s * nt;
-            const int z0 = worker_of(tile0), z1 = worker_of(tile0 + nt - 1);
+            const int unit0 = (cc.b > 0 ? s_pre[cc.b - 1] : 0) * per_tile + seg * kv_units(nt);
+            const int z0 = worker_of(unit0 + 2), z1 = worker_of(unit0 + 2 * nt);
             const int lo = max(z0, cta0), hi = min(z1, cta0 + W - 1);
             const bool here = z0 >= cta0, over = z1 == hi, alone = lo == hi;
             bool out = whole, mine = !whole && !alone;   // what is written next: rows, this worker's piece, the CTA's
@@ -817,7 +922,7 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1) kv_attn_kernel(c
                     }
                 }
                 if (!mine) {
-                    if (!out && !here && lane == 0) p.meta[blockIdx.x] = make_int4(cc.s, cc.b, z0 / W, over ? 1 : 0);
+                    if (!out && !here && lane == 0) p.meta[blockIdx.x] = make_int4(seg, cc.b, z0 / W, over ? 1 : 0);
                     break;
                 }
                 __threadfence_block();
@@ -847,10 +952,15 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1) kv_attn_kernel(c
             }
             fresh = true;
         }
-        if (left == 0) break;
-        cc.next(p);
+        if (done) return;
+        cc = nx;
     }
-    cp_wait<0>();
+    {
+        // a wait ran out: the copies in flight land before the CTA's memory goes
+        mbar_wait_drain_warp(k_bar, phase, p.c.err, p.budget_ns);
+        mbar_wait_drain_warp(v_bar, phase, p.c.err, p.budget_ns);
+        if (ahead) mbar_wait_drain_warp(k_bar, phase ^ 1u, p.c.err, p.budget_ns);
+    }
 }
 
 // ------------------------------------------------------------------- join
@@ -874,7 +984,7 @@ __global__ void __launch_bounds__(D * 2) kv_join_kernel(const __grid_constant__ 
 }
 
 template <int D, int NR, typename T, bool kCap>
-cudaError_t launch_attn_t(KvAttnParams p, int sms, cudaStream_t stream) {
+cudaError_t launch_attn_t(KvAttnParams p, const CUtensorMap &map_v, int sms, cudaStream_t stream) {
     using C = KvCfg<D, NR>;
     auto kern = kv_attn_kernel<D, NR, T, kCap>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
@@ -882,7 +992,10 @@ cudaError_t launch_attn_t(KvAttnParams p, int sms, cudaStream_t stream) {
     const int grid = sms < kKvSms ? sms : kKvSms;
     p.workers = grid * C::kWarps;
     p.groups = (p.G * p.Sq + 8 * NR - 1) / (8 * NR);
-    kern<<<grid, C::kWarps * 32, C::SMEM, stream>>>(p);
+    // x / (page / 16) as a product: exact for x below 2^29 and divisors up to 8
+    const uint32_t d = (uint32_t)p.c.page / 16;
+    p.page_magic = d > 1 ? (uint32_t)((1ull << 32) / d + 1) : 0u;
+    kern<<<grid, C::kWarps * 32, C::SMEM, stream>>>(p, map_v);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
@@ -897,11 +1010,11 @@ cudaError_t launch_attn_t(KvAttnParams p, int sms, cudaStream_t stream) {
 }
 
 template <int D, typename T>
-cudaError_t launch_attn_dt(const KvAttnParams &p, int sms, cudaStream_t stream) {
+cudaError_t launch_attn_dt(const KvAttnParams &p, const CUtensorMap &mv, int sms, cudaStream_t stream) {
     const bool cap = p.cap_log2 > 0.f;
     if (p.G * p.Sq <= 8)
-        return cap ? launch_attn_t<D, 1, T, true>(p, sms, stream) : launch_attn_t<D, 1, T, false>(p, sms, stream);
-    return cap ? launch_attn_t<D, 2, T, true>(p, sms, stream) : launch_attn_t<D, 2, T, false>(p, sms, stream);
+        return cap ? launch_attn_t<D, 1, T, true>(p, mv, sms, stream) : launch_attn_t<D, 1, T, false>(p, mv, sms, stream);
+    return cap ? launch_attn_t<D, 2, T, true>(p, mv, sms, stream) : launch_attn_t<D, 2, T, false>(p, mv, sms, stream);
 }
 
 template <int D, typename T>
@@ -929,10 +1042,13 @@ cudaError_t launch_kv_append(const KvAppendParams &p, int D, int bf16, cudaStrea
     return bf16 ? launch_append_t<64, __nv_bfloat16>(p, stream) : launch_append_t<64, __half>(p, stream);
 }
 
-cudaError_t launch_kv_attn(const KvAttnParams &p, int D, int bf16, int sms, cudaStream_t stream) {
+cudaError_t launch_kv_attn(const KvAttnParams &p, const CUtensorMap &mv, int D, int bf16, int sms,
+                           cudaStream_t stream) {
     if (D == 128)
-        return bf16 ? launch_attn_dt<128, __nv_bfloat16>(p, sms, stream) : launch_attn_dt<128, __half>(p, sms, stream);
-    return bf16 ? launch_attn_dt<64, __nv_bfloat16>(p, sms, stream) : launch_attn_dt<64, __half>(p, sms, stream);
+        return bf16 ? launch_attn_dt<128, __nv_bfloat16>(p, mv, sms, stream)
+                    : launch_attn_dt<128, __half>(p, mv, sms, stream);
+    return bf16 ? launch_attn_dt<64, __nv_bfloat16>(p, mv, sms, stream)
+                : launch_attn_dt<64, __half>(p, mv, sms, stream);
 }
 
 }  // namespace fa

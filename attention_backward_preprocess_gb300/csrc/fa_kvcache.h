@@ -4,6 +4,7 @@
 #include <cstddef>
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace fa {
@@ -42,6 +43,11 @@ struct KvAttnParams {
     float4 *stat, *cta_stat;     // [workers | CTAs][2][rows]  (m, l, R, -)
     int4 *meta;                  // [CTAs]  piece 0: segment, sequence, first CTA, ends here
     int workers;
+    uint32_t page_magic;         // divides by page / 16 (0: by 1)
+    // V reaches shared memory in blocks of v_block tokens (64, 32 or 16: the
+    // widest that divides a page's tokens), v_pad bytes apart
+    int v_block, v_pad;
+    long long budget_ns;         // bound of every device-side wait
 };
 
 // Workers of the attention kernel at most: kKvMaxWarps warps of kKvSms CTAs.
@@ -53,6 +59,7 @@ inline size_t kv_pieces_bytes(size_t n, int D) { return n * 2 * 16 * (D * sizeof
 size_t kv_workspace_bytes(int D);
 
 cudaError_t launch_kv_append(const KvAppendParams &p, int D, int bf16, cudaStream_t stream);
-cudaError_t launch_kv_attn(const KvAttnParams &p, int D, int bf16, int sms, cudaStream_t stream);
+cudaError_t launch_kv_attn(const KvAttnParams &p, const CUtensorMap &map_v, int D, int bf16, int sms,
+                           cudaStream_t stream);
 
 }  // namespace fa

@@ -367,8 +367,10 @@ fa_status fa_bwd_ext(const void *q, const void *k, const void *v, const void *o,
  * anything but the arguments and the GPU (no atomics).
  *
  * Errors: FA_ERR_INVALID_ARG for null or misaligned pointers, sizes, scale,
- * softcap or window; FA_ERR_UNSUPPORTED for D, page_size, dtype, more than
- * 4096 sequences (fa_fwd_kvcache) or heads times tokens beyond 2^24.  A length
+ * softcap or window; FA_ERR_UNSUPPORTED for D, page_size, dtype, and in
+ * fa_fwd_kvcache more than 4096 sequences, Sq times Hq above 2^24, a cache of
+ * 2^31 or more (page, head, dim) rows, or a table so wide that 64-key tiles
+ * times heads times sequences reach 2^31.  A length
  * outside [0, max_pages page_size], more new tokens than max_new, or a table
  * entry that is no page is found on the device: such a sequence (or page) is
  * neither read nor written, its attention output is 0 / -inf (with a bad page,
