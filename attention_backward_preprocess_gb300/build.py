@@ -18,6 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfa_gb300.so")
 SOURCES = ["fa_api.cu", "fa_bwd_main.cu", "fa_bwd_wide.cu", "fa_fwd_tc.cu", "fa_fwd_split.cu",
+           "fa_fwd_duo.cu",
            "fa_kernels.cu", "fa_ranges.cu", "fa_kvcache.cu",
            "fa_selftest.cu", "fa_noalloc.cu"]
 HEADERS = ["fa_device.cuh", "fa_params.h", "fa_fwd_common.h", "fa_bwd_units.cuh", "fa_ranges.h",

@@ -22,10 +22,10 @@ cudaError_t launch_preprocess(const BwdParams &p, int bf16, cudaStream_t stream)
 cudaError_t launch_postprocess(const BwdParams &p, int bf16, cudaStream_t stream);
 cudaError_t launch_dbias_zero(const BwdParams &p, int bm, cudaStream_t stream);
 cudaError_t launch_fwd_tc(const BwdParams &p, const CUtensorMap &q, const CUtensorMap &k,
-                          const CUtensorMap &v, void *o, float *lse, int max_lq, int bf16,
+                          const CUtensorMap &v, void *o, float *lse, int max_lq, int bf16, int sms,
                           cudaStream_t stream);
 int fwd_block_m();
-int fwd_block_n(int Dq_tile, int Dv_tile);
+int fwd_block_n(const BwdParams &p, int sms);
 int *fwd_error_word();
 cudaError_t launch_bwd_main(const BwdParams &p, const CUtensorMap &q, const CUtensorMap &k,
                             const CUtensorMap &v, const CUtensorMap &dout, const CUtensorMap &dk,
@@ -958,12 +958,12 @@ fa_status fa_fwd_ext(const void *q, const void *k, const void *v, void *o, float
     const int bf16 = dtype == FA_BF16;
     const int nb = p.varlen ? 1 : B;
     CUtensorMap mq, mk, mv;
-    const int bn = fa::fwd_block_n(p.D, p.Dv);
+    const int bn = fa::fwd_block_n(p, sm_count());
     if (!encode_rows_map(&mq, q, D, Hq, rq, nb, fa::fwd_block_m(), bf16, p.sq) ||
         !encode_rows_map(&mk, k, D, Hkv, rk, nb, bn, bf16, p.sk) ||
         !encode_rows_map(&mv, v, p.Dhv, Hkv, rk, nb, bn, bf16, p.sv))
         return FA_ERR_CUDA;
-    return cuda_status(fa::launch_fwd_tc(p, mq, mk, mv, o, lse, Sq, bf16, stream));
+    return cuda_status(fa::launch_fwd_tc(p, mq, mk, mv, o, lse, Sq, bf16, sm_count(), stream));
 }
 
 }  // extern "C"

@@ -35,11 +35,22 @@ constexpr int fwd_instance_flags(int need) {
 // the 8k GQA workload, the plain and ALiBi instances at D = 128 run faster
 // with one warp per row (fa_fwd_tc.cu): there the per-block exchange of the
 // row maxima between the two warps costs more than the halved work saves.
-constexpr bool fwd_split(int d, int flags) { return (flags & (kFwdBias | kFwdDrop | kFwdCap)) != 0 || d == 64; }
+// Capped scores and interval masks run in fa_fwd_duo.cu, or with at most one
+// tile per SM, where only a tile's own latency counts, here too.
+constexpr bool fwd_split(int d, int flags) {
+    return (flags & (kFwdBias | kFwdDrop | kFwdCap | kFwdRange)) != 0 || d == 64;
+}
 
 // Launches the two-warps-per-row forward instance for (D, dtype, flags).
 cudaError_t launch_fwd_split(const BwdParams &p, const CUtensorMap &q, const CUtensorMap &k,
                              const CUtensorMap &v, void *o, float *lse, int max_lq, int bf16,
                              int flags, cudaStream_t stream);
+
+// Key rows of the K / V boxes of the two-CTAs-per-SM instances.
+int fwd_duo_block_n();
+// Launches the two-CTAs-per-SM instance for (D, dtype, flags with kFwdRange).
+cudaError_t launch_fwd_duo(const BwdParams &p, const CUtensorMap &q, const CUtensorMap &k,
+                           const CUtensorMap &v, void *o, float *lse, int max_lq, int bf16,
+                           int flags, cudaStream_t stream);
 
 }  // namespace fa

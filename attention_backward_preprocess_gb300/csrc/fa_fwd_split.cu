@@ -1,6 +1,7 @@
 // fa_fwd_split.cu -- the forward pass (O and LSE, as in fa_fwd_tc.cu) with
 // two softmax warps per query row, for the instances fwd_split() selects: the
-// bias and dropout instances and every instance at D = 64.
+// bias and dropout instances, every plain and ALiBi instance at D = 64, and
+// capped scores and interval masks of problems with few tiles.
 //
 // One CTA per (128-query tile, sequence, query head); per block of 128 keys
 //   S = Q K^T           tcgen05 SS, M = 128 queries, N = 128 keys, fp32 in TMEM
@@ -595,6 +596,8 @@ __global__ void __launch_bounds__(SplitCfg<kD, T>::kThreads, 1)
                 float *lse_dst = p.varlen ? lse_out + (long long)h * p.cu_q[p.B] + q0 + qi
                                           : lse_out + ((long long)b * p.Hq + h) * p.Sq + qi;
                 *lse_dst = l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+                // a row of NaN scores: NaN (the other instances give -inf)
+                if ((kFlags & (kFwdCap | kFwdRange)) != 0 && l_run != l_run) *lse_dst = l_run;
                 // a row of NaN scores: NaN (the other instances give -inf)
                 if ((kFlags & (kFwdCap | kFwdRange)) != 0 && l_run != l_run) *lse_dst = l_run;
             }

@@ -24,7 +24,6 @@
 
 #include "fa_device.cuh"
 #include "fa_fwd_common.h"
-#include "fa_fwd_ranges.cuh"
 #include "fa_params.h"
 
 namespace fa {
@@ -91,8 +90,8 @@ __global__ void __launch_bounds__(FwdCfg<kDQ, kDV, kBN, T>::kThreads, 1)
                   void *o_out, float *lse_out, int nmb) {
     using C = FwdCfg<kDQ, kDV, kBN, T>;
     constexpr int DQ = C::DQ, DV = C::DV, BM = C::BM, BN = C::BN, S = C::kStages;
-    static_assert((kFlags & (kFwdBias | kFwdDrop | kFwdCap)) == 0,
-                  "the bias, dropout and capped instances run in fa_fwd_split.cu");
+    static_assert((kFlags & (kFwdBias | kFwdDrop)) == 0,
+                  "the bias and dropout instances run in fa_fwd_split.cu");
     constexpr bool kAlibi = (kFlags & kFwdAlibi) != 0;
     constexpr bool kExt = kAlibi;   // scores other than the plain scaled ones
     // ---- tile of this CTA: longest causal rows first
@@ -110,10 +109,8 @@ __global__ void __launch_bounds__(FwdCfg<kDQ, kDV, kBN, T>::kThreads, 1)
     if (m * BM >= lq) return;                       // uniform: the whole CTA leaves
     // key j is visible to query i iff -win_lo <= j - i - diag <= win_hi, j < lk
     const int diag = lk - lq;
-    long long first_key = max(0LL, (long long)m * BM + diag - p.win_lo);
-    long long last_key = min((long long)lk - 1, (long long)m * BM + BM - 1 + diag + p.win_hi);
-    const bool ranges = (kFlags & kFwdRange) != 0 && p.mr_row != nullptr;
-    if (ranges) tile_range(p, b, m, lk, &first_key, &last_key);
+    const long long first_key = max(0LL, (long long)m * BM + diag - p.win_lo);
+    const long long last_key = min((long long)lk - 1, (long long)m * BM + BM - 1 + diag + p.win_hi);
     // key blocks [n_begin, n_begin + nblk) hold every key some row of the tile sees
     const int n_begin = (int)(first_key / BN);
     const int nblk = last_key < first_key ? 0 : (int)(last_key / BN) + 1 - n_begin;
@@ -250,9 +247,8 @@ __global__ void __launch_bounds__(FwdCfg<kDQ, kDV, kBN, T>::kThreads, 1)
         const int qi = m * BM + r;                  // query index within the sequence
         const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
         // keys [kmin, kmax] are visible to this row (none if kmax < kmin)
-        int kmin = (int)max(0LL, (long long)qi + diag - p.win_lo);
-        int kmax = (int)min((long long)lk - 1, (long long)qi + diag + p.win_hi);
-        if (ranges) row_range(p, b, qi, lq, lk, &kmin, &kmax);
+        const int kmin = (int)max(0LL, (long long)qi + diag - p.win_lo);
+        const int kmax = (int)min((long long)lk - 1, (long long)qi + diag + p.win_hi);
         // ALiBi slope of this head, log2 units
         const float slope2 = (kAlibi && p.alibi)
                                  ? __ldg(p.alibi + (long long)b * p.alibi_bstride + h) * 1.4426950408889634f
@@ -417,8 +413,6 @@ __global__ void __launch_bounds__(FwdCfg<kDQ, kDV, kBN, T>::kThreads, 1)
                 float *lse_dst = p.varlen ? lse_out + (long long)h * p.cu_q[p.B] + q0 + qi
                                           : lse_out + ((long long)b * p.Hq + h) * p.Sq + qi;
                 *lse_dst = l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
-                // a row of NaN scores: NaN (the other instances give -inf)
-                if ((kFlags & (kFwdCap | kFwdRange)) != 0 && l_run != l_run) *lse_dst = l_run;
             }
             const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
             T *dst = reinterpret_cast<T *>(o_out) + (row * p.Hq + h) * p.Dhv;   // Dhv <= DV columns
@@ -516,6 +510,15 @@ cudaError_t launch_fwd_wide_t(const BwdParams &p, const CUtensorMap &mq, const C
     return cudaErrorInvalidValue;
 }
 
+// Capped scores and interval masks: two CTAs to an SM (fa_fwd_duo.cu), unless the
+// problem has at most a tile per SM.  Then only a tile's own
+// latency counts, and two warps per row (fa_fwd_split.cu) finish it sooner (36
+// tiles of 333 tokens, D = 64, cap and prefix: 8 against 15 us).
+bool fwd_duo(const BwdParams &p, int sms) {
+    if (p.cap_log2 <= 0.f && !p.mr_row) return false;
+    return (long long)p.B * p.Hq * ((p.Sq + 127) / 128) > sms;
+}
+
 // Error word of the forward pass (its bounded waits record timeouts here).
 __device__ int g_fwd_err;
 
@@ -529,17 +532,21 @@ int *fwd_error_word() {
 // Query rows of one TMA box for Q in the forward pass, and key rows of one box
 // for K / V (tile widths of the two sides).
 int fwd_block_m() { return FwdCfg<128, 128, 128, __nv_bfloat16>::BM; }
-int fwd_block_n(int Dq_tile, int Dv_tile) { return (Dq_tile > 128 || Dv_tile > 128) ? 64 : 128; }
+int fwd_block_n(const BwdParams &p, int sms) {
+    if (fwd_duo(p, sms)) return fwd_duo_block_n();
+    return (p.D > 128 || p.Dv > 128) ? 64 : 128;
+}
 
 cudaError_t launch_fwd_tc(const BwdParams &p, const CUtensorMap &q, const CUtensorMap &k,
                           const CUtensorMap &v, void *o, float *lse, int max_lq, int bf16,
-                          cudaStream_t stream) {
+                          int sms, cudaStream_t stream) {
     if (p.D != p.Dv || p.D > 128 || p.Dh != p.Dhv)   // wide or unequal head dims
         return bf16 ? launch_fwd_wide_t<__nv_bfloat16>(p, q, k, v, o, lse, max_lq, stream)
                     : launch_fwd_wide_t<__half>(p, q, k, v, o, lse, max_lq, stream);
     const int need = (p.alibi ? kFwdAlibi : 0) | (p.bias ? kFwdBias : 0) | (p.drop_t > 0 ? kFwdDrop : 0) |
                      (p.cap_log2 > 0.f ? kFwdCap : 0) | (p.mr_row ? kFwdRange : 0);
     const int f = fwd_instance_flags(need);
+    if (fwd_duo(p, sms)) return launch_fwd_duo(p, q, k, v, o, lse, max_lq, bf16, f, stream);
     if (fwd_split(p.D, f)) return launch_fwd_split(p, q, k, v, o, lse, max_lq, bf16, f, stream);
     if (p.D != 128) return cudaErrorInvalidValue;
     return bf16 ? launch_fwd_tc_t<128, __nv_bfloat16>(p, q, k, v, o, lse, max_lq, need, stream)
