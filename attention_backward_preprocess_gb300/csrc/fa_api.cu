@@ -396,6 +396,7 @@ fa_status apply_ext(fa::BwdParams &p, int causal, const fa_ext *ext) {
             p.mr_block = t.block;
             p.mr_key = t.key;
             p.mr_first = t.first;
+            p.mr_order = t.order;
             p.mr_rows = t.rows;
         }
         if (p.alibi || p.bias || p.dbias || p.drop_t > 0 || wide_dims(p.Dh, p.Dhv)) return FA_ERR_UNSUPPORTED;
@@ -474,7 +475,9 @@ fa_status prepare(const void *q, const void *k, const void *v, const void *o, co
     // sequences of at least 1.5 grids of units each, the same idea; in
     // deterministic mode none (0: the plain order).
     p.unit_group = B * Hkv;
-    if (!cu_q && !deterministic) {
+    // With intervals all pairs are one group: its units go out longest first
+    // (fa_ranges.cu), and a second group's long ones would begin half way.
+    if (!cu_q && !deterministic && !p.mr_row) {
         const int nblk = (Sk + fa::kBlockN - 1) / fa::kBlockN;
         const long long grid = std::min<long long>(L.max_tiles, sm_count());
         for (int g = 1; g <= B * Hkv; ++g)

@@ -1005,17 +1005,9 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
                 // the tile crosses the upper / lower edge of the band: mask
                 // element by element (one compare per edge and element)
                 const bool masked_hi = !kRange && n0 + BN - 1 - (m0 + diag) > whi;
-                // with intervals: some row of the step's block does not see the
+                // with intervals: some row of the step's block may not see the
                 // whole key block
-                bool masked_rng = false;
-                if (kRange) {
-                    const int4 *blk = p.mr_block + (long long)u.b * (p.mr_rows / 64) + m * (BM / 64);
-#pragma unroll
-                    for (int i = 0; i < BM / 64; ++i) {
-                        const int4 e = __ldg(blk + i);
-                        masked_rng |= e.z > n0 || e.w < n0 + BN;
-                    }
-                }
+                const bool masked_rng = kRange && (m < u.m_open || m >= u.m_shut || n0 + BN > u.lk);
                 const bool masked_lo = kExt && n0 - (m0 + BM - 1 + diag) < -wlo;
                 // ALiBi slope of the step's query head, in log2 units (0: none)
                 float slope2 = 0.f;
@@ -1138,20 +1130,24 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) nl2[k] = f2_add(nl2[k], f2_pack(p.cap_log2, p.cap_log2));
                     }
-                    // intervals of the thread's query pairs, edge tiles only: key kb
-                    // + kr is visible iff (unsigned)(kr + rt) < rw
-                    int rt[kRange ? 8 : 1];
-                    uint32_t rw[kRange ? 8 : 1];
+                    // edge tiles of intervals: bit 4 (2k + e) + 2h + r of `seen` is set
+                    // iff query 8k + 2 q4 + e sees key kb + 16h + 8r (the used length
+                    // among it); one word instead of the sixteen ends
+                    uint32_t seen = 0u;
                     if (kRange && masked_rng) {
                         const int4 *rr = reinterpret_cast<const int4 *>(
                             p.mr_row + (long long)u.b * p.mr_rows + m0 + c0 + 2 * q4);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int4 e = __ldg(rr + 4 * k);
-                            rt[kRange ? 2 * k : 0] = kb - e.x;
-                            rw[kRange ? 2 * k : 0] = (uint32_t)max(e.y - e.x, 0);
-                            rt[kRange ? 2 * k + 1 : 0] = kb - e.z;
-                            rw[kRange ? 2 * k + 1 : 0] = (uint32_t)max(e.w - e.z, 0);
+                            const int t0 = kb - e.x, t1 = kb - e.z;
+                            const uint32_t w0 = (uint32_t)max(min(e.y, u.lk) - e.x, 0);
+                            const uint32_t w1 = (uint32_t)max(min(e.w, u.lk) - e.z, 0);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                seen |= (uint32_t)(t0 + 8 * i) < w0 ? 1u << (8 * k + i) : 0u;
+                                seen |= (uint32_t)(t1 + 8 * i) < w1 ? 1u << (8 * k + 4 + i) : 0u;
+                            }
                         }
                     }
                     tmem_wait_ld();
@@ -1234,12 +1230,15 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
                                     if (lim_lo + kr < 8 * k) pv0 = 0.f;
                                     if (lim_lo + kr < 8 * k + 1) pv1 = 0.f;
                                 }
-                                if (kRange && masked_rng) {
-                                    if ((uint32_t)(rt[kRange ? 2 * k : 0] + kr) >= rw[kRange ? 2 * k : 0]) pv0 = 0.f;
-                                    if ((uint32_t)(rt[kRange ? 2 * k + 1 : 0] + kr) >= rw[kRange ? 2 * k + 1 : 0])
-                                        pv1 = 0.f;
+                                if (kRange) {
+                                    if (masked_rng) {
+                                        if (!(seen >> (8 * k + 2 * h + r) & 1u)) pv0 = 0.f;
+                                        if (!(seen >> (8 * k + 4 + 2 * h + r) & 1u)) pv1 = 0.f;
+                                    }
+                                } else if (kb + kr >= u.lk) {
+                                    pv0 = 0.f;
+                                    pv1 = 0.f;
                                 }
-                                if (kb + kr >= u.lk) { pv0 = 0.f; pv1 = 0.f; }
                                 if (!kPFromTmem) {
                                     P[32 * ch + 16 * h + 4 * k + 2 * r] = kCap ? pv0 * g0 : pv0;
                                     P[32 * ch + 16 * h + 4 * k + 2 * r + 1] = kCap ? pv1 * g1 : pv1;

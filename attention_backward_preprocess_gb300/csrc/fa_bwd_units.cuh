@@ -30,6 +30,7 @@ struct Unit {
     int b, n_block, hk;
     int lq, lk;
     int q_row0, k_row0, bidx;   // TMA row offset and batch coordinate
+    int m_open = 0, m_shut = 0; // kRange: row blocks [m_open, m_shut) see the whole key block
     int m_begin, nm, iters;     // row blocks [m_begin, m_begin + nm) per head; iters = G * nm
     // Iteration order: row blocks from the last to the first, the G query
     // heads of the group innermost.  Under a causal mask every unit of a
@@ -77,9 +78,13 @@ __device__ __forceinline__ Unit decode_unit(const BwdParams &p, int t) {
         u.bidx = u.b;
     }
     if constexpr (kRange) {
+        // longest units first; the deterministic order counts on rising key blocks
+        if (!p.deterministic) u.n_block = __ldg(p.mr_order + (long long)u.b * (p.mr_rows / kBlockN) + u.n_block);
         // 64-row blocks [r.x, r.y), inside the used rows
         constexpr int F = BM / 64;
-        const int2 r = __ldg(p.mr_key + (long long)u.b * (p.mr_rows / kBlockN) + u.n_block);
+        const int4 r = __ldg(p.mr_key + (long long)u.b * (p.mr_rows / kBlockN) + u.n_block);
+        u.m_open = (r.z + F - 1) / F;
+        u.m_shut = r.w / F;
         const int lo = max(r.x, 0), hi = min(r.y, (u.lq + 63) / 64);
         u.m_begin = lo / F;
         u.nm = (lo < hi && u.n_block * kBlockN < u.lk) ? (hi + F - 1) / F - u.m_begin : 0;

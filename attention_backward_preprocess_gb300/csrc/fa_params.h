@@ -87,8 +87,9 @@ struct BwdParams {
     // block of a row block; mr_rows = Sq rounded up to 128
     const int2 *mr_row;
     const int4 *mr_block;
-    const int2 *mr_key;
+    const int4 *mr_key;
     const int *mr_first;
+    const int *mr_order;   // key blocks, the most row blocks first
     int mr_rows;
     // strides in elements (batch, row, head) of q, k, v, o and dout
     long long sq[3], sk[3], sv[3], so[3], sdo[3];

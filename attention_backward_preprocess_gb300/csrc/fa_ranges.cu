@@ -252,8 +252,50 @@ __device__ __forceinline__ int2 key_blocks(const int *first, const int *last, in
     return lo < end ? make_int2(lo, end) : make_int2(0, 0);
 }
 
+// The row blocks of [r.x, r.y) whose rows all see the whole key block n, as one
+// run [x, y): the first there is (documents, prefixes and windows leave one).  A
+// whole warp, 32 blocks at a time.
+__device__ __forceinline__ int2 open_run(const int4 *block, int n, int2 r) {
+    const int lane = threadIdx.x & 31, lo = n * kBlockN, hi = lo + kBlockN;
+    int x = -1;
+    for (int m0 = r.x; m0 < r.y; m0 += 32) {
+        const int m = m0 + lane;
+        bool open = false;
+        if (m < r.y) {
+            const int4 e = block[m];
+            open = e.z <= lo && e.w >= hi;
+        }
+        uint32_t bits = __ballot_sync(0xffffffffu, open);
+        if (x < 0) {
+            if (bits == 0u) continue;
+            const int at = __ffs((int)bits) - 1;
+            x = m0 + at;
+            bits |= (1u << at) - 1u;   // looked for: the first that is shut
+        }
+        if (bits != 0xffffffffu) return make_int2(x, m0 + __ffs((int)~bits) - 1);
+    }
+    return x < 0 ? make_int2(0, 0) : make_int2(x, r.y);
+}
+
+// Longest first: the order in which the backward takes a sequence's key blocks
+// (documents leave units of very different lengths, and a long one begun last
+// keeps the rest waiting).  The rank of a block is counted; past kRanked
+// blocks there are so many units that the order does not matter.
+constexpr int kRanked = 512;
+__device__ __forceinline__ int rank_of(const int2 *key, int nn, int n, int2 mine) {
+    const int len = mine.y - mine.x;
+    int r = 0;
+#pragma unroll 4
+    for (int i = 0; i < nn; ++i) {
+        const int l = key[i].y - key[i].x;
+        r += l > len || (l == len && i < n);
+    }
+    return r;
+}
+
 __global__ void __launch_bounds__(kTabThreads) range_tables_kernel(RangeTables t) {
     __shared__ int sh[kTabThreads / 32];
+    __shared__ int2 s_key[kRanked];
     const int b = blockIdx.x, nm = t.rows / 64, nn = t.rows / kBlockN, tid = threadIdx.x;
     const int4 *blk = t.block + (long long)b * nm;
     int *first = t.first + (long long)b * nm, *last = t.last + (long long)b * nm;
@@ -281,33 +323,94 @@ __global__ void __launch_bounds__(kTabThreads) range_tables_kernel(RangeTables t
     }
     __syncthreads();   // the block's own writes, read back below
     for (int n = tid; n < nn; n += kTabThreads) {
-        t.key[(long long)b * nn + n] = key_blocks(first, last, nm, n);
+        const int2 r = key_blocks(first, last, nm, n);
+        t.key[(long long)b * nn + n] = make_int4(r.x, r.y, 0, 0);
+        if (nn <= kRanked) s_key[n] = r;
     }
+    __syncthreads();
+    for (int n = tid; n < nn; n += kTabThreads)
+        t.order[(long long)b * nn + (nn <= kRanked ? rank_of(s_key, nn, n, s_key[n]) : n)] = n;
+}
+
+// The runs of whole row blocks, a warp per key block.
+__global__ void __launch_bounds__(256) range_runs_kernel(RangeTables t) {
+    const int b = blockIdx.y, nm = t.rows / 64, nn = t.rows / kBlockN;
+    const int n = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (n >= nn) return;
+    int4 *key = t.key + (long long)b * nn + n;
+    const int4 r = *key;
+    const int2 run = open_run(t.block + (long long)b * nm, n, make_int2(r.x, r.y));
+    if ((threadIdx.x & 31) == 0) *key = make_int4(r.x, r.y, run.x, run.y);
 }
 
 // ------------------------------------------------------- short sequences
-// Up to kShort rows: one CTA per sequence holds everything, eight rows per
-// thread, so one launch does both steps and no document end is searched for.
-// Measured (2 launches -> this): @SHORT@
+// Up to kShort rows: one CTA per sequence, eight rows per thread, so one launch
+// does both steps, no document end is searched for, and the tables are one
+// warp's work.
 constexpr int kShortThreads = 1024, kShortPer = 8, kShort = kShortThreads * kShortPer;
 constexpr int kShortBlocks = kShort / 64;
 
+// Exclusive running maximum over the block's threads, `first` before the first.
+__device__ __forceinline__ int short_scan_excl(int v, int first, int *sh) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x = max(x, y);
+    }
+    if (lane == 31) sh[w] = x;
+    __syncthreads();
+    const int before = __reduce_max_sync(0xffffffffu, lane < w ? sh[lane] : first);
+    const int up = __shfl_up_sync(0xffffffffu, x, 1);
+    return lane > 0 ? max(before, up) : before;
+}
+// The same from the other end: what lies behind a thread.
+__device__ __forceinline__ int short_scan_excl_back(int v, int first, int *sh) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_down_sync(0xffffffffu, x, o);
+        if (lane + o < 32) x = max(x, y);
+    }
+    if (lane == 0) sh[w] = x;
+    __syncthreads();
+    const int behind = __reduce_max_sync(0xffffffffu, lane > w && lane < nw ? sh[lane] : first);
+    const int dn = __shfl_down_sync(0xffffffffu, x, 1);
+    return lane < 31 ? max(behind, dn) : behind;
+}
+
 __global__ void __launch_bounds__(kShortThreads) short_ranges_kernel(MaskArgs a, RangeTables t) {
-    __shared__ int sh[kShortThreads / 32];
-    __shared__ int rev[kShortThreads];
+    __shared__ int sh[2][kShortThreads / 32];
     __shared__ int s_first[kShortBlocks], s_last[kShortBlocks];
+    __shared__ int2 s_key[kShortBlocks / 2];
+    __shared__ int4 s_block[kShortBlocks];
     const int b = blockIdx.x, S = a.S, tid = threadIdx.x, i0 = tid * kShortPer;
     const int *doc = a.doc ? a.doc + (long long)b * S : nullptr;
     int start[kShortPer], end[kShortPer];
     bool live[kShortPer];
     if (doc) {
         int id[kShortPer + 2];
+        if ((S & 3) == 0 && (reinterpret_cast<uintptr_t>(doc) & 15u) == 0) {
+            // 16-byte loads; the neighbours' ids come from the neighbour lanes
 #pragma unroll
-        for (int k = 0; k < kShortPer + 2; ++k) {
-            const int i = i0 - 1 + k;
-            id[k] = (i >= 0 && i < S) ? __ldg(doc + i) : 0;
+            for (int k = 0; k < kShortPer; k += 4) {
+                const int4 v = i0 + k < S ? __ldg(reinterpret_cast<const int4 *>(doc + i0 + k)) : make_int4(0, 0, 0, 0);
+                id[k + 1] = v.x, id[k + 2] = v.y, id[k + 3] = v.z, id[k + 4] = v.w;
+            }
+            id[0] = __shfl_up_sync(0xffffffffu, id[kShortPer], 1);
+            id[kShortPer + 1] = __shfl_down_sync(0xffffffffu, id[1], 1);
+            if ((tid & 31) == 0) id[0] = (i0 > 0 && i0 <= S) ? __ldg(doc + i0 - 1) : 0;
+            if ((tid & 31) == 31) id[kShortPer + 1] = i0 + kShortPer < S ? __ldg(doc + i0 + kShortPer) : 0;
+        } else {
+#pragma unroll
+            for (int k = 0; k < kShortPer + 2; ++k) {
+                const int i = i0 - 1 + k;
+                id[k] = (i >= 0 && i < S) ? __ldg(doc + i) : 0;
+            }
         }
-        int last = -1, next = -1, all;   // as in row_ranges_kernel
+        int last = -1, next = -1;   // as in row_ranges_kernel
 #pragma unroll
         for (int k = 0; k < kShortPer; ++k) {
             const int i = i0 + k;
@@ -321,18 +424,8 @@ __global__ void __launch_bounds__(kShortThreads) short_ranges_kernel(MaskArgs a,
             else if (i == S) next = 0;
             end[k] = next;
         }
-        // inclusive scans; a thread takes its neighbour's value
-        rev[tid] = block_scan_incl(last, true, 0, sh, &all);
-        __syncthreads();
-        const int carry = tid > 0 ? rev[tid - 1] : 0;
-        __syncthreads();
-        rev[kShortThreads - 1 - tid] = next;
-        __syncthreads();
-        const int mirrored = rev[tid];
-        const int scan = block_scan_incl(mirrored, true, 0, sh, &all);
-        rev[tid] = scan;   // every thread has read its mirrored value (the scan's barriers)
-        __syncthreads();
-        const int carry_end = tid < kShortThreads - 1 ? rev[kShortThreads - 2 - tid] : 0;
+        const int carry = short_scan_excl(last, 0, sh[0]);
+        const int carry_end = short_scan_excl_back(next, 0, sh[1]);
 #pragma unroll
         for (int k = 0; k < kShortPer; ++k) {
             start[k] = start[k] >= 0 ? start[k] : carry;
@@ -377,33 +470,57 @@ __global__ void __launch_bounds__(kShortThreads) short_ranges_kernel(MaskArgs a,
         max_lo = max(max_lo, __shfl_xor_sync(0xffffffffu, max_lo, o));
         min_hi = min(min_hi, __shfl_xor_sync(0xffffffffu, min_hi, o));
     }
-    if ((tid & 7) == 0) {
-        const int m = tid / 8;   // of kShortBlocks
-        if (m < nm) t.block[(long long)b * nm + m] = make_int4(min_lo, max_hi, max_lo, min_hi);
-        const bool some = m < nm && max_hi > min_lo;
-        s_first[m] = some ? min_lo / kBlockN : 0x7fffffff;
-        s_last[m] = some ? (max_hi - 1) / kBlockN : -1;
+    if ((tid & 7) == 0 && tid / 8 < nm) {
+        const int m = tid / 8;
+        s_block[m] = make_int4(min_lo, max_hi, max_lo, min_hi);
+        t.block[(long long)b * nm + m] = s_block[m];
+        s_first[m] = max_hi > min_lo ? min_lo / kBlockN : 0x7fffffff;
+        s_last[m] = max_hi > min_lo ? (max_hi - 1) / kBlockN : -1;
     }
-    // suffix minimum of first, prefix maximum of last, in log steps
-    for (int o = 1; o < kShortBlocks; o <<= 1) {
-        __syncthreads();
-        int f = 0, l = 0;
-        if (tid < kShortBlocks) {
-            f = tid + o < kShortBlocks ? min(s_first[tid], s_first[tid + o]) : s_first[tid];
-            l = tid >= o ? max(s_last[tid], s_last[tid - o]) : s_last[tid];
+    __syncthreads();
+    if (tid < 32) {
+        // suffix minimum of first, prefix maximum of last: four blocks per lane
+        constexpr int PER = kShortBlocks / 32;
+        int f[PER], l[PER];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int m = tid * PER + k;
+            f[k] = m < nm ? s_first[m] : 0x7fffffff;
+            l[k] = m < nm ? s_last[m] : -1;
         }
-        __syncthreads();
-        if (tid < kShortBlocks) {
-            s_first[tid] = f;
-            s_last[tid] = l;
+#pragma unroll
+        for (int k = 1; k < PER; ++k) {
+            l[k] = max(l[k], l[k - 1]);
+            f[PER - 1 - k] = min(f[PER - 1 - k], f[PER - k]);
+        }
+        int lt = l[PER - 1], ft = f[0];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, lt, o), z = __shfl_down_sync(0xffffffffu, ft, o);
+            if (tid >= o) lt = max(lt, y);
+            if (tid + o < 32) ft = min(ft, z);
+        }
+        int lb = __shfl_up_sync(0xffffffffu, lt, 1), fb = __shfl_down_sync(0xffffffffu, ft, 1);
+        if (tid == 0) lb = -1;
+        if (tid == 31) fb = 0x7fffffff;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int m = tid * PER + k;
+            if (m < nm) {
+                s_first[m] = min(f[k], fb);
+                s_last[m] = max(l[k], lb);
+                t.first[(long long)b * nm + m] = s_first[m];
+            }
         }
     }
     __syncthreads();
-    if (tid < nm) t.first[(long long)b * nm + tid] = s_first[tid];
-    if (tid < nn) {
-        const int2 r2 = key_blocks(s_first, s_last, nm, tid);
-        t.key[(long long)b * nn + tid] = r2;
+    for (int n = tid; n < nn; n += blockDim.x) s_key[n] = key_blocks(s_first, s_last, nm, n);
+    __syncthreads();
+    for (int n = tid >> 5; n < nn; n += blockDim.x >> 5) {   // a warp per key block
+        const int2 r = s_key[n], run = open_run(s_block, n, r);
+        if ((tid & 31) == 0) t.key[(long long)b * nn + n] = make_int4(r.x, r.y, run.x, run.y);
     }
+    for (int n = tid; n < nn; n += blockDim.x) t.order[(long long)b * nn + rank_of(s_key, nn, n, s_key[n])] = n;
 }
 
 }  // namespace
@@ -412,14 +529,17 @@ cudaError_t launch_mask_ranges(const int *doc, const int *prefix, int prefix_per
                                int wr, const RangeTables &t, cudaStream_t stream) {
     MaskArgs a{doc, prefix, prefix_per_token ? S : 1, prefix_per_token ? 1 : 0, B, S, wl, wr};
     if (S <= kShort) {
-        short_ranges_kernel<<<(unsigned)B, kShortThreads, 0, stream>>>(a, t);
+        const int threads = (t.rows / kShortPer + 31) / 32 * 32;
+        short_ranges_kernel<<<(unsigned)B, threads, 0, stream>>>(a, t);
         return cudaGetLastError();
     }
     const dim3 grid((unsigned)((t.rows + kTile - 1) / kTile), (unsigned)B);
     row_ranges_kernel<<<grid, kThreads, 0, stream>>>(a, t);
-    const cudaError_t e = cudaGetLastError();
+    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     range_tables_kernel<<<(unsigned)B, kTabThreads, 0, stream>>>(t);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    range_runs_kernel<<<dim3((unsigned)((t.rows / kBlockN + 7) / 8), (unsigned)B), 256, 0, stream>>>(t);
     return cudaGetLastError();
 }
 

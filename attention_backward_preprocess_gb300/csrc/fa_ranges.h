@@ -18,9 +18,12 @@ struct RangeTables {
     int4 *block;   // [B][rows / 64]   over the rows below S of a 64-row block: min lo and
                    //                  max hi of those that see a key (INT_MAX, 0: none);
                    //                  max lo and min hi of all
-    int2 *key;     // [B][rows / 128]  row blocks [x, y) the unit of a key block works on
+    int4 *key;     // [B][rows / 128]  row blocks [x, y) the unit of a key block works on, and
+                   //                  [z, w) of them whose rows all see the whole key block (a
+                   //                  run; the others are tested row by row)
     int *first;    // [B][rows / 64]   first key block whose unit works on the row block
     int *last;     // [B][rows / 64]   running maximum of the last key block (scratch)
+    int *order;    // [B][rows / 128]  key blocks, the most row blocks first
     size_t bytes;
 };
 
@@ -37,9 +40,10 @@ inline RangeTables range_tables(void *base, int B, int S) {
     };
     t.row = reinterpret_cast<int2 *>(take((size_t)B * R * sizeof(int2)));
     t.block = reinterpret_cast<int4 *>(take((size_t)B * (R / 64) * sizeof(int4)));
-    t.key = reinterpret_cast<int2 *>(take((size_t)B * (R / kBlockN) * sizeof(int2)));
+    t.key = reinterpret_cast<int4 *>(take((size_t)B * (R / kBlockN) * sizeof(int4)));
     t.first = reinterpret_cast<int *>(take((size_t)B * (R / 64) * sizeof(int)));
     t.last = reinterpret_cast<int *>(take((size_t)B * (R / 64) * sizeof(int)));
+    t.order = reinterpret_cast<int *>(take((size_t)B * (R / kBlockN) * sizeof(int)));
     t.bytes = off;
     return t;
 }

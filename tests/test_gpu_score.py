@@ -110,7 +110,13 @@ def test_mask_ranges_buffer(fa, cuda_device, c):
         at += (n + 63) // 64 * 64
         return x
     row, block = take(B * R * 2).view(B, R, 2), take(B * R // 64 * 4).view(B, R // 64, 4)
-    key, first = take(B * R // 128 * 2).view(B, R // 128, 2), take(B * R // 64).view(B, R // 64)
+    key, first = take(B * R // 128 * 4).view(B, R // 128, 4), take(B * R // 64).view(B, R // 64)
+    take(B * R // 64)
+    order = take(B * R // 128).view(B, R // 128).long()
+    for b in range(B):   # each key block once, the most row blocks first
+        assert torch.equal(order[b].sort().values, torch.arange(R // 128))
+        size = (key[b, :, 1] - key[b, :, 0])[order[b]]
+        assert (size[1:] <= size[:-1]).all()
     j = torch.arange(S)
     got = (j >= row[:, :S, :1]) & (j < row[:, :S, 1:])
     assert torch.equal(got, ok)
@@ -119,6 +125,16 @@ def test_mask_ranges_buffer(fa, cuda_device, c):
     pad[:, :S, :S] = ok
     tiles = pad.view(B, R // 64, 64, R // 128, 128).any(dim=4).any(dim=2)
     n = torch.arange(R // 128)
+    # row blocks below S that see a key block whole: the run holds none other
+    rows = torch.arange(R) < S
+    whole = (pad | ~rows[None, :, None]).view(B, R // 64, 64, R // 128, 128).all(dim=4).all(dim=2)
+    m = torch.arange(R // 64)
+    for b in range(B):
+        for i in range(R // 128):
+            run = (m >= key[b, i, 2]) & (m < key[b, i, 3])
+            assert (whole[b, run, i]).all()
+            inside = whole[b, :, i] & (m >= key[b, i, 0]) & (m < key[b, i, 1])
+            assert torch.equal(run, inside), (b, i)   # one run for every mask built here
     for b in range(B):
         for mb in range(R // 64):
             works = (key[b, :, 0] <= mb) & (mb < key[b, :, 1])
@@ -491,7 +507,7 @@ def test_mask_ranges_sizes(fa):
     n = fa.lib().fa_mask_ranges_bytes
     assert n(0, 5) == 0 and n(5, -1) == 0 and n(1 << 20, 1 << 20) == 0
     # rows of 8 bytes, blocks of 16, key blocks of 8, two words per row block
-    assert n(2, 129) == 2 * 256 * 8 + 256 + 256 + 256 + 256
+    assert n(2, 129) == 2 * 256 * 8 + 5 * 256
     assert n(1, 1 << 20) > 8 << 20
 
 
