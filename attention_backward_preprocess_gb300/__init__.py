@@ -164,15 +164,17 @@ class KvCache:
         P, H, ps, D = k.shape
         self.B = block_table.shape[0]
         self.device = k.get_device()   # index, -1: not on a GPU
-        for name, t, dt, shape in (("k", k, torch.float8_e4m3fn, (P, H, ps, D)),
-                                   ("v", v, torch.float8_e4m3fn, (P, H, D, ps)),
-                                   ("k_scale", k_scale, torch.float32, (P, H)),
-                                   ("v_scale", v_scale, torch.float32, (P, H)),
-                                   ("block_table", block_table, torch.int32, block_table.shape)):
-            self._check(name, t, dt, shape)
+        if self.device < 0 or not _binding().cache(k, v, k_scale, v_scale, block_table):
+            for name, t, dt, shape in (("k", k, torch.float8_e4m3fn, (P, H, ps, D)),
+                                       ("v", v, torch.float8_e4m3fn, (P, H, D, ps)),
+                                       ("k_scale", k_scale, torch.float32, (P, H)),
+                                       ("v_scale", v_scale, torch.float32, (P, H)),
+                                       ("block_table", block_table, torch.int32, block_table.shape)):
+                self._check(name, t, dt, shape)
         self.k, self.v, self.k_scale, self.v_scale, self.block_table = k, v, k_scale, v_scale, block_table
         self._c = _KvCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                  block_table.data_ptr(), P, ps, block_table.shape[1], H, D)
+        self._at = ctypes.addressof(self._c)
 
     def _check(self, name, t, dtype, shape):
         if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != self.device \
@@ -187,6 +189,11 @@ def kvcache_append(cache, cache_len, k_new, v_new, cu_new=None, max_new=None, st
     ``k_new`` / ``v_new``: [B, T, Hkv, D], or [total, Hkv, D] with ``cu_new``
     (int32 [B + 1] prefix sums) and ``max_new``, the most tokens of one
     sequence.  The cache's tensors are updated in place."""
+    if stream is None:
+        r = _binding().append(cache._at, cache.B, cache.device, cache_len, k_new, v_new, cu_new, max_new)
+        if r is not None:
+            _done(r, "fa_kvcache_append")
+            return
     B, c = cache.B, cache._c
     cache._check("cache_len", cache_len, torch.int32, (B,))
     if cu_new is None:
@@ -217,6 +224,10 @@ def fa_fwd_kvcache(q, cache, cache_len, softmax_scale=None, softcap=0.0, window_
     (int32 [B]) counts them.  ``workspace``: a uint8 CUDA tensor of
     ``fa_fwd_kvcache_workspace_bytes(D)`` (allocated when not given); ``out``:
     (o, lse) to write into.  See fa_fwd_kvcache in include/fa.h."""
+    if stream is None and out is None and workspace is None:
+        r = _binding().attend(cache._at, cache.B, cache.device, q, cache_len, softmax_scale, softcap, window_left)
+        if r is not None:
+            return _done(r, "fa_fwd_kvcache")
     c = cache._c
     if q.dim() != 4:
         raise ValueError("q: [B, Sq, Hq, D]")
@@ -270,6 +281,11 @@ class MaskRanges:
         self.buffer, self.B, self.S = buffer, B, S
 
 
+def _ranges(r):
+    """A MaskRanges' buffer, B and S (None, 0, 0 without one)."""
+    return (r.buffer, r.B, r.S) if isinstance(r, MaskRanges) else (r, 0, 0)
+
+
 def mask_ranges(B, S, doc_ids=None, prefix_len=None, causal=True, window=None, device=None, out=None,
                 stream=None):
     """Visible keys of every query row of a dense self-attention batch, for the
@@ -282,6 +298,10 @@ def mask_ranges(B, S, doc_ids=None, prefix_len=None, causal=True, window=None, d
     leading tokens every row of the document sees; with ``causal`` and without
     a window only.  ``window=(left, right)``, -1 = unbounded.  ``out``: a
     MaskRanges of the same B and S to fill again (a captured graph's)."""
+    if window is None and device is None and out is None and stream is None:
+        r = _binding().mask_ranges(B, S, doc_ids, prefix_len, causal)
+        if r is not None:
+            return MaskRanges(_done(r, "fa_mask_ranges"), int(B), int(S))
     at = None if device is None else torch.device(device).index   # None: the current GPU
     if out is not None:
         if not isinstance(out, MaskRanges) or (out.B, out.S) != (B, S):
@@ -378,6 +398,35 @@ def lib():
             getattr(L, name).restype = _i
         _lib = L
         return _lib
+
+
+_short = None
+
+
+def _binding():
+    """The compiled short way in (fa_torch.cpp); raises if it has not been built."""
+    global _short
+    if _short is None:
+        lib()
+        import importlib.machinery
+        import importlib.util
+        path = os.path.join(_PKG, "_fa_torch.so")
+        if not os.path.exists(path):
+            raise RuntimeError("_fa_torch.so is not built (run attention_backward_preprocess_gb300.build.build())")
+        loader = importlib.machinery.ExtensionFileLoader("_fa_torch", path)
+        spec = importlib.util.spec_from_file_location("_fa_torch", path, loader=loader)
+        mod = importlib.util.module_from_spec(spec)
+        loader.exec_module(mod)
+        _short = mod
+    return _short
+
+
+def _done(r, what):
+    """A short call's result: None for the Python path to take over, else the
+    result; a status raises."""
+    if type(r) is int:
+        _check(r, what)
+    return r
 
 
 def status_string(status: int) -> str:
@@ -493,6 +542,11 @@ def fa_fwd(q, k, v, causal=False, softmax_scale=None, cu_seqlens_q=None, cu_seql
     caps the scores, softcap * tanh(score / softcap); ``mask_ranges`` (from the
     function of that name) takes the place of ``causal`` and ``window``.
     """
+    if cu_seqlens_q is None and stream is None and window is None and alibi_slopes is None and seqused_q is None \
+            and seqused_k is None and bias is None and dropout is None and totals is None:
+        r = _binding().fwd(q, k, v, softmax_scale, causal, softcap, *_ranges(mask_ranges))
+        if r is not None:
+            return _done(r, "fa_fwd_ext")
     (q, k, v), strides = _inputs(stream, q=q, k=k, v=v)
     B, Sq, Sk, Hq, Hkv, D = _shape(q, k, cu_seqlens_q, max_seqlen_q, max_seqlen_k)
     scale = default_scale(D) if softmax_scale is None else float(softmax_scale)
@@ -528,6 +582,12 @@ def fa_bwd(q, k, v, o, dout, lse, causal=False, softmax_scale=None, cu_seqlens_q
     packed row counts, which spare the stream synchronisation of reading them
     back).  ``softcap`` and ``mask_ranges`` as the forward had them.
     """
+    if cu_seqlens_q is None and stream is None and window is None and alibi_slopes is None and seqused_q is None \
+            and seqused_k is None and bias is None and dropout is None and totals is None and not deterministic \
+            and dq is None and dk is None and dv is None and workspace is None and dbias is None:
+        r = _binding().bwd(q, k, v, softmax_scale, causal, softcap, *_ranges(mask_ranges), o, dout, lse)
+        if r is not None:
+            return _done(r, "fa_bwd_ext")
     (q, k, v, o, dout), strides = _inputs(stream, q=q, k=k, v=v, o=o, dout=dout)
     (lse,) = _dense(stream, lse=lse)
     _outputs(dq=dq, dk=dk, dv=dv)

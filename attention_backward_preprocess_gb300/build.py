@@ -17,6 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfa_gb300.so")
+BINDING = os.path.join(PKG, "_fa_torch.so")   # the short way in for torch tensors (fa_torch.cpp)
 SOURCES = ["fa_api.cu", "fa_bwd_main.cu", "fa_bwd_wide.cu", "fa_fwd_tc.cu", "fa_fwd_split.cu",
            "fa_fwd_duo.cu",
            "fa_kernels.cu", "fa_ranges.cu", "fa_kvcache.cu",
@@ -64,8 +65,28 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError("nvcc failed on %s:\n%s" % (s, r.stderr))
         return r.stderr
 
-    with ThreadPoolExecutor(max_workers=max(1, len(jobs))) as ex:
+    def compile_binding():
+        """fa_torch.cpp against the installed torch's and Python's headers."""
+        import sysconfig
+
+        import torch
+        t = os.path.dirname(torch.__file__)
+        s, o = os.path.join(CSRC, "fa_torch.cpp"), os.path.join(BUILD, "fa_torch.o")
+        if not (force or _stale(o, [s] + PUBLIC_HEADERS + [os.path.join(t, "version.py")])):
+            return
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
+        for d in (sysconfig.get_paths()["include"], os.path.join(t, "include"),
+                  os.path.join(t, "include", "torch", "csrc", "api", "include"),
+                  os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include")):
+            cmd += ["-isystem", d]
+        r = subprocess.run(cmd + ["-I" + os.path.join(ROOT, "include"), "-c", s, "-o", o], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("g++ failed on %s:\n%s" % (s, r.stderr))
+
+    with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        binding = ex.submit(compile_binding)
         logs = list(ex.map(compile_one, jobs))
+        binding.result()
     if verbose:
         for log in logs:
             sys.stderr.write(log)
@@ -80,6 +101,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError("link failed:\n%s" % r.stderr)
         os.replace(tmp, LIB)
+    o = os.path.join(BUILD, "fa_torch.o")
+    if force or _stale(BINDING, [o]):
+        import torch
+        t = os.path.join(os.path.dirname(torch.__file__), "lib")
+        tmp = BINDING + ".tmp.%d" % os.getpid()
+        cmd = ["g++", "-shared", "-o", tmp, o, "-L" + PKG, "-l:libfa_gb300.so", "-Wl,-rpath,$ORIGIN", "-L" + t,
+               "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("link failed:\n%s" % r.stderr)
+        os.replace(tmp, BINDING)
     return LIB
 
 
