@@ -867,11 +867,7 @@ fa_status fa_fwd_kvcache(const void *q, const fa_kv_cache *cache, const int *cac
     uint8_t *w = static_cast<uint8_t *>(workspace);
     p.acc = reinterpret_cast<float *>(w);
     p.stat = reinterpret_cast<float4 *>(w + n * 2 * 16 * cache->D * sizeof(float));
-    w += fa::kv_pieces_bytes(n, cache->D);
-    p.cta_acc = reinterpret_cast<float *>(w);
-    p.cta_stat = reinterpret_cast<float4 *>(w + (size_t)fa::kKvSms * 2 * 16 * cache->D * sizeof(float));
-    w += fa::kv_pieces_bytes(fa::kKvSms, cache->D);
-    p.meta = reinterpret_cast<int4 *>(w);
+    p.meta = reinterpret_cast<int4 *>(w + fa::kv_pieces_bytes(n, cache->D));
     p.budget_ns = g_budget_ns.load();
     const int ps = cache->page_size;
     p.v_block = ps % 64 == 0 ? 64 : ps % 32 == 0 ? 32 : 16;

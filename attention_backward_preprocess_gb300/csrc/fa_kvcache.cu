@@ -337,89 +337,55 @@ __device__ __forceinline__ void store_rows(const KvAttnParams &p, int b, int hk,
     }
 }
 
-// Adds a piece (fragments and statistics number `at` of a list) to a worker's
-// state of one row block.  The row sums stay with the lanes of the first key.
-template <int NR, int DM>
-__device__ __forceinline__ void add_piece(const KvAttnParams &p, const float *list, const float4 *stats, long long at,
-                                          int nr, int row0, int lane, float (&m)[2], float (&l)[2], float (&R)[2],
-                                          float (&acc)[DM][4]) {
-    const int q4 = lane & 3;
-    const float4 *src = reinterpret_cast<const float4 *>(list + (at * NR + nr) * DM * 128) + lane;
-    float4 v[DM], st[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e)   // rows past the last carry no statistics
-        st[e] = row0 + 2 * q4 + e < p.Sq * p.G ? __ldcg(stats + (at * NR + nr) * 8 + 2 * q4 + e)
-                                               : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-#pragma unroll
-    for (int dm = 0; dm < DM; ++dm) v[dm] = __ldcg(src + 32 * dm);
-    float g[2], h[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const float mn = fmaxf(m[e], st[e].x), rn = fmaxf(R[e], st[e].z);
-        const float m0 = mn == -INFINITY ? 0.f : mn, r0 = rn == -INFINITY ? 0.f : rn;
-        l[e] = l[e] * ex2(m[e] - m0) + (lane < 4 ? st[e].y * ex2(st[e].x - m0) : 0.f);
-        g[e] = ex2(R[e] - r0);
-        h[e] = ex2(st[e].z - r0);
-        m[e] = mn;
-        R[e] = rn;
-    }
-#pragma unroll
-    for (int dm = 0; dm < DM; ++dm) {
-        acc[dm][0] = fmaf(v[dm].x, h[0], acc[dm][0] * g[0]);
-        acc[dm][1] = fmaf(v[dm].y, h[1], acc[dm][1] * g[1]);
-        acc[dm][2] = fmaf(v[dm].z, h[0], acc[dm][2] * g[0]);
-        acc[dm][3] = fmaf(v[dm].w, h[1], acc[dm][3] * g[1]);
-    }
-}
-
 // Rows 2 q4 + e of one row block, one 16-dim part, over several pieces.
 struct Joined {
     float4 v;
     float m[2], l[2], r[2];
 };
-
-// The pieces of holders from .. to (piece 1 of holder `first`, piece 0 of the
-// others) summed in order against their common maxima: statistics in a first
-// pass, values in a second, whose loads do not wait for one another.
-template <int NR, int DM>
-__device__ __forceinline__ void join_pieces(const KvAttnParams &p, const float *acc, const float4 *stat, int from,
-                                            int to, int first, int nr, int dm, int row0, int lane, Joined &x) {
-    constexpr int PIECE = NR * DM * 128;
-    const int q4 = lane & 3;
-    // rows past the last carry no statistics
-    const bool live[2] = {row0 + 2 * q4 < p.Sq * p.G, row0 + 2 * q4 + 1 < p.Sq * p.G};
-    auto stat_of = [&](int w, int e) -> float4 {
-        const long long at = ((long long)w * 2 + (w == first ? 1 : 0)) * (NR * 8) + nr * 8 + 2 * q4 + e;
-        return live[e] ? __ldcg(stat + at) : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-    };
+__device__ __forceinline__ void joined_zero(Joined &x) {
+    x.v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int e = 0; e < 2; ++e) x.m[e] = x.r[e] = -INFINITY, x.l[e] = 0.f;
-#pragma unroll 4
-    for (int w = from; w <= to; ++w)
+}
+// x += a piece's values and (m, l, R) of the two rows, against the larger maxima
+__device__ __forceinline__ void joined_add(Joined &x, float4 v, const float (&m)[2], const float (&l)[2],
+                                           const float (&r)[2]) {
+    float g[2], h[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float4 st = stat_of(w, e);
-            x.m[e] = fmaxf(x.m[e], st.x);
-            x.r[e] = fmaxf(x.r[e], st.z);
-        }
-    const float m0[2] = {x.m[0] == -INFINITY ? 0.f : x.m[0], x.m[1] == -INFINITY ? 0.f : x.m[1]};
-    const float r0[2] = {x.r[0] == -INFINITY ? 0.f : x.r[0], x.r[1] == -INFINITY ? 0.f : x.r[1]};
-    x.v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int e = 0; e < 2; ++e) {
+        const float mn = fmaxf(x.m[e], m[e]), rn = fmaxf(x.r[e], r[e]);
+        const float m0 = mn == -INFINITY ? 0.f : mn, r0 = rn == -INFINITY ? 0.f : rn;
+        x.l[e] = x.l[e] * ex2(x.m[e] - m0) + l[e] * ex2(m[e] - m0);
+        g[e] = ex2(x.r[e] - r0);
+        h[e] = ex2(r[e] - r0);
+        x.m[e] = mn;
+        x.r[e] = rn;
+    }
+    x.v.x = fmaf(v.x, h[0], x.v.x * g[0]);
+    x.v.y = fmaf(v.y, h[1], x.v.y * g[1]);
+    x.v.z = fmaf(v.z, h[0], x.v.z * g[0]);
+    x.v.w = fmaf(v.w, h[1], x.v.w * g[1]);
+}
+// Every `step`-th piece of workers from .. to (piece 1 of worker `first`, piece 0
+// of the others), in order.
+template <int NR, int DM>
+__device__ __forceinline__ void join_pieces(const KvAttnParams &p, int from, int to, int step, int first, int nr,
+                                            int dm, int row0, int lane, Joined &x) {
+    constexpr int PIECE = NR * DM * 128;
+    const int q4 = lane & 3;
+    joined_zero(x);
 #pragma unroll 4
-    for (int w = from; w <= to; ++w) {
+    for (int w = from; w <= to; w += step) {
         const long long at = (long long)w * 2 + (w == first ? 1 : 0);
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(acc + at * PIECE + nr * DM * 128) + 32 * dm + lane);
-        float h[2];
+        const float4 v = *(reinterpret_cast<const float4 *>(p.acc + at * PIECE + nr * DM * 128) + 32 * dm + lane);
+        float m[2], l[2], r[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float4 st = stat_of(w, e);
-            x.l[e] = fmaf(st.y, ex2(st.x - m0[e]), x.l[e]);
-            h[e] = ex2(st.z - r0[e]);
+        for (int e = 0; e < 2; ++e) {   // rows past the last carry no statistics
+            const float4 st = row0 + 2 * q4 + e < p.Sq * p.G ? p.stat[at * (NR * 8) + nr * 8 + 2 * q4 + e]
+                                                             : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+            m[e] = st.x, l[e] = st.y, r[e] = st.z;
         }
-        x.v.x = fmaf(v.x, h[0], x.v.x);
-        x.v.y = fmaf(v.y, h[1], x.v.y);
-        x.v.z = fmaf(v.z, h[0], x.v.z);
-        x.v.w = fmaf(v.w, h[1], x.v.w);
+        joined_add(x, v, m, l, r);
     }
 }
 
@@ -453,18 +419,14 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1)
     __shared__ int s_pre[kKvMaxSeqs];   // half tiles of one head and row group of sequences 0 .. b, inclusive
     __shared__ int s_len[kKvMaxSeqs];   // their tokens, 0 where the length is outside the table
     __shared__ int s_warp[W];
-    // pieces written of the segment whose last holder in this CTA is worker w
-    // and which ends there (0) or goes on (1)
-    __shared__ int s_done[W][2];
     __shared__ __align__(8) uint64_t s_bar[W][2];   // K, V of the worker's tile landed
     __shared__ int s_abort;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int r8 = lane >> 2, q4 = lane & 3;
 
-    if (threadIdx.x == 0) p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
     if (threadIdx.x == 0) s_abort = 0;
+    if (lane == 0) p.meta[blockIdx.x * W + warp] = make_int4(-1, 0, 0, 0);
     if (lane < 2) {
-        s_done[warp][lane] = 0;
         mbar_init(smem_u32(&s_bar[warp][lane]), 1);
         fence_mbar_init();
     }
@@ -513,7 +475,7 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1)
     // shares of the workers: total / N half tiles each, one more for the first
     // total % N; a worker holds at least two tiles' worth, so that few pieces
     // are made of little work
-    const int cta0 = blockIdx.x * W, wid = cta0 + warp, N = min(p.workers, max(total / 4, 1));
+    const int wid = blockIdx.x * W + warp, N = min(p.workers, max(total / 4, 1));
     pdl_launch();
     if (wid >= N || total == 0) return;
     const int share = total / N, more = total - share * N;
@@ -876,79 +838,43 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1)
             // the rows' results, or the piece's for the join
             const int hk = cc.hk, rg = cc.rg, seg = hk * p.groups + rg;
             const bool whole = begins && ends;
-            // The holders of the segment: workers z0 .. z1, of them lo .. hi in
-            // this CTA.  One that is the CTA's only holder writes the CTA's
-            // piece, else its own; the last to write joins them.
-            const int nt = cc.t1 - cc.t0;
-            const int unit0 = (cc.b > 0 ? s_pre[cc.b - 1] : 0) * per_tile + seg * kv_units(nt);
-            const int z0 = worker_of(unit0 + 2), z1 = worker_of(unit0 + 2 * nt);
-            const int lo = max(z0, cta0), hi = min(z1, cta0 + W - 1);
-            const bool here = z0 >= cta0, over = z1 == hi, alone = lo == hi;
-            bool out = whole, mine = !whole && !alone;   // what is written next: rows, this worker's piece, the CTA's
-            while (true) {
-                const long long at = mine ? (long long)wid * 2 + (begins ? 1 : 0) : (long long)blockIdx.x * 2 + (here ? 1 : 0);
-                float *dst_acc = (mine ? p.acc : p.cta_acc) + at * C::PIECE;
-                float4 *dst_stat = (mine ? p.stat : p.cta_stat) + at * (NR * 8);
+            if (!begins && lane == 0) {
+                // piece 0, of a segment begun before: whose first tile's holder
+                const int unit0 = (cc.b > 0 ? s_pre[cc.b - 1] : 0) * per_tile + seg * kv_units(cc.t1 - cc.t0);
+                p.meta[wid] = make_int4(seg, cc.b, worker_of(unit0 + 2), ends ? 1 : 0);
+            }
+            const long long at = (long long)wid * 2 + (begins ? 1 : 0);
 #pragma unroll
-                for (int nr = 0; nr < NR; ++nr) {
-                    const int row0 = (rg * NR + nr) * 8;
-                    float f[2];
+            for (int nr = 0; nr < NR; ++nr) {
+                const int row0 = (rg * NR + nr) * 8;
+                float f[2];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float l = keys_sum(l_run[nr][e]);
-                        f[e] = out_factor(R[nr][e], m_run[nr][e], l);
-                        const int row = row0 + 2 * q4 + e;
-                        if (r8 == 0 && row < p.Sq * p.G) {
-                            if (!out)
-                                dst_stat[nr * 8 + 2 * q4 + e] = make_float4(m_run[nr][e], l, R[nr][e], 0.f);
-                            else if (p.lse)
-                                p.lse[((long long)cc.b * p.Hq + hk * p.G + row % p.G) * p.Sq + row / p.G] =
-                                    lse_of(m_run[nr][e], l);
-                        }
-                    }
-                    if (out) {
-#pragma unroll
-                        for (int dm = 0; dm < DM; ++dm) {
-                            // (a row without keys: its sums are 0, and so is the factor)
-                            float o[4] = {acc[nr][dm][0] * f[0], acc[nr][dm][1] * f[1], acc[nr][dm][2] * f[0],
-                                          acc[nr][dm][3] * f[1]};
-                            store_rows<D, T>(p, cc.b, hk, row0, lane, o, dm);
-                        }
-                    } else {
-                        float4 *dst = reinterpret_cast<float4 *>(dst_acc + nr * 8 * D) + lane;
-#pragma unroll
-                        for (int dm = 0; dm < DM; ++dm)
-                            dst[32 * dm] = make_float4(acc[nr][dm][0], acc[nr][dm][1], acc[nr][dm][2], acc[nr][dm][3]);
+                for (int e = 0; e < 2; ++e) {
+                    const float l = keys_sum(l_run[nr][e]);
+                    f[e] = out_factor(R[nr][e], m_run[nr][e], l);
+                    const int row = row0 + 2 * q4 + e;
+                    if (r8 == 0 && row < p.Sq * p.G) {
+                        if (!whole)
+                            p.stat[at * (NR * 8) + nr * 8 + 2 * q4 + e] = make_float4(m_run[nr][e], l, R[nr][e], 0.f);
+                        else if (p.lse)
+                            p.lse[((long long)cc.b * p.Hq + hk * p.G + row % p.G) * p.Sq + row / p.G] =
+                                lse_of(m_run[nr][e], l);
                     }
                 }
-                if (!mine) {
-                    if (!out && !here && lane == 0) p.meta[blockIdx.x] = make_int4(seg, cc.b, z0 / W, over ? 1 : 0);
-                    break;
-                }
-                __threadfence_block();
-                __syncwarp();
-                int n = 0;
-                if (lane == 0) n = atomicAdd(&s_done[hi - cta0][over ? 0 : 1], 1);
-                n = __shfl_sync(0xffffffffu, n, 0);
-                __threadfence_block();
-                if (n != hi - lo) break;
-                // the last of the segment's holders here: their pieces in order,
-                // each one's loads in flight together
+                if (whole) {
 #pragma unroll
-                for (int nr = 0; nr < NR; ++nr) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) m_run[nr][e] = R[nr][e] = -INFINITY, l_run[nr][e] = 0.f;
+                    for (int dm = 0; dm < DM; ++dm) {
+                        // (a row without keys: its sums are 0, and so is the factor)
+                        float o[4] = {acc[nr][dm][0] * f[0], acc[nr][dm][1] * f[1], acc[nr][dm][2] * f[0],
+                                      acc[nr][dm][3] * f[1]};
+                        store_rows<D, T>(p, cc.b, hk, row0, lane, o, dm);
+                    }
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>(p.acc + at * C::PIECE + nr * 8 * D) + lane;
 #pragma unroll
                     for (int dm = 0; dm < DM; ++dm)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) acc[nr][dm][k] = 0.f;
-#pragma unroll 1
-                    for (int w = lo; w <= hi; ++w)
-                        add_piece<NR, DM>(p, p.acc, p.stat, (long long)w * 2 + (w == z0 ? 1 : 0), nr,
-                                          (rg * NR + nr) * 8, lane, m_run[nr], l_run[nr], R[nr], acc[nr]);
+                        dst[32 * dm] = make_float4(acc[nr][dm][0], acc[nr][dm][1], acc[nr][dm][2], acc[nr][dm][3]);
                 }
-                mine = false;
-                out = here && over;
             }
             fresh = true;
         }
@@ -964,22 +890,52 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1)
 }
 
 // ------------------------------------------------------------------- join
-// One CTA per CTA of the attention kernel: if a segment begun in an earlier one
-// ends in it, the pieces of the CTAs between (piece 1 of the first, piece 0 of
-// the others) are joined and finished.  A warp per 16 dims.
+// One CTA per kJoinWorkers workers and 16 dims: for each of the workers in which
+// a segment ends that began before it, the segment's pieces are joined and
+// finished.  A warp takes a segment of few pieces by itself; of one of many the
+// kParts warps take every kParts-th piece and add their sums in order.
+// Joining in the attention kernel instead (the last holder in a CTA) kept
+// 17 to 20 thousand cycles of a worker's 115 for itself, most of them the first
+// run through code that is used once.
+constexpr int kParts = 8, kJoinWorkers = 8, kFew = 8;
+
 template <int D, int NR, typename T>
-__global__ void __launch_bounds__(D * 2) kv_join_kernel(const __grid_constant__ KvAttnParams p) {
+__global__ void __launch_bounds__(32 * kParts) kv_join_kernel(const __grid_constant__ KvAttnParams p) {
     constexpr int DM = D / 16;
+    __shared__ Joined s_x[kParts - 1][32];
+    const int part = threadIdx.x / 32, lane = threadIdx.x % 32, dm = blockIdx.y;
     pdl_wait();
-    const int4 me = p.meta[blockIdx.x];
-    if (me.x < 0 || me.w == 0) return;
-    const int dm = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int w_lane = blockIdx.x * kJoinWorkers + lane;
+    int4 mine = make_int4(-1, 0, 0, 0);
+    if (lane < kJoinWorkers && w_lane < p.workers) mine = p.meta[w_lane];
+    int turn = 0;
 #pragma unroll 1
-    for (int nr = 0; nr < NR; ++nr) {
-        const int row0 = ((me.x % p.groups) * NR + nr) * 8;
-        Joined x;
-        join_pieces<NR, DM>(p, p.cta_acc, p.cta_stat, me.z, blockIdx.x, me.z, nr, dm, row0, lane, x);
-        finish_rows<D, T>(p, x, me.y, me.x / p.groups, row0, dm, lane);
+    for (int i = 0; i < kJoinWorkers; ++i) {
+        const int seg = __shfl_sync(0xffffffffu, mine.x, i), b = __shfl_sync(0xffffffffu, mine.y, i);
+        const int first = __shfl_sync(0xffffffffu, mine.z, i), ends = __shfl_sync(0xffffffffu, mine.w, i);
+        const int w = blockIdx.x * kJoinWorkers + i;
+        if (seg < 0 || ends == 0) continue;
+        const bool few = w - first < kFew;
+        if (few && turn++ % kParts != part) continue;
+#pragma unroll 1
+        for (int nr = 0; nr < NR; ++nr) {
+            const int row0 = ((seg % p.groups) * NR + nr) * 8;
+            Joined x;
+            join_pieces<NR, DM>(p, few ? first : first + part, w, few ? 1 : kParts, first, nr, dm, row0, lane, x);
+            if (!few) {
+                if (part > 0) s_x[part - 1][lane] = x;
+                __syncthreads();   // (many pieces: every warp of the CTA is here)
+                if (part == 0)
+#pragma unroll 1
+                    for (int k = 0; k < kParts - 1; ++k) {
+                        const Joined &y = s_x[k][lane];
+                        joined_add(x, y.v, y.m, y.l, y.r);
+                    }
+                __syncthreads();
+                if (part > 0) continue;
+            }
+            finish_rows<D, T>(p, x, b, seg / p.groups, row0, dm, lane);
+        }
     }
 }
 
@@ -998,8 +954,8 @@ cudaError_t launch_attn_t(KvAttnParams p, const CUtensorMap &map_v, int sms, cud
     kern<<<grid, C::kWarps * 32, C::SMEM, stream>>>(p, map_v);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(D * 2);
+    cfg.gridDim = dim3((unsigned)((p.workers + kJoinWorkers - 1) / kJoinWorkers), D / 16);
+    cfg.blockDim = dim3(32 * kParts);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1031,9 +987,9 @@ cudaError_t launch_append_t(const KvAppendParams &p, cudaStream_t stream) {
 }  // namespace
 
 size_t kv_workspace_bytes(int D) {
-    // two pieces per worker and two per CTA: fragments and row statistics; what a CTA's piece 0 is
+    // two pieces of up to 16 rows per worker, and what its piece 0 is
     const size_t n = (size_t)kKvSms * kKvMaxWarps;
-    return kv_pieces_bytes(n, D) + kv_pieces_bytes(kKvSms, D) + (size_t)kKvSms * sizeof(int4);
+    return kv_pieces_bytes(n, D) + n * sizeof(int4);
 }
 
 cudaError_t launch_kv_append(const KvAppendParams &p, int D, int bf16, cudaStream_t stream) {

@@ -38,10 +38,10 @@ struct KvAttnParams {
     int window;            // keys a query sees before its own; < 0: all
     float scale_log2;      // c log2(e)
     float cap_log2, cap_k; // softcap log2(e) and 2 log2(e) c / softcap; 0: no cap
-    // workspace: two pieces of up to 16 rows per worker, and per CTA
-    float *acc, *cta_acc;        // [workers | CTAs][2] pieces in fragment order
-    float4 *stat, *cta_stat;     // [workers | CTAs][2][rows]  (m, l, R, -)
-    int4 *meta;                  // [CTAs]  piece 0: segment, sequence, first CTA, ends here
+    // workspace: two pieces of up to 16 rows per worker
+    float *acc;            // [workers][2] pieces in fragment order
+    float4 *stat;          // [workers][2][rows]  (m, l, R, -)
+    int4 *meta;            // [workers]  piece 0: segment, sequence, first worker, ends here
     int workers;
     uint32_t page_magic;         // divides by page / 16 (0: by 1)
     // V reaches shared memory in blocks of v_block tokens (64, 32 or 16: the
