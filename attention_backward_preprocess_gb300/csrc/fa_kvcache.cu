@@ -82,21 +82,15 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
     const int pi = len / ps + blockIdx.x % per_seq;                 // page of the sequence
     const int from = max(len, pi * ps), to = min(len + n, pi * ps + ps);
     if (from >= to) return;
+    // (read here, looked at once the tokens are on their way)
     const int page = p.c.table[(long long)b * p.c.max_pages + pi];
-    if (page < 0 || page >= p.c.num_pages) {
-        if (tid == 0) atomicOr(p.c.err, kErrBadPage);
-        return;
-    }
     const int held = from - pi * ps, T_new = to - from;   // tokens before, new tokens
-    const long long ph = (long long)page * p.c.Hkv + h;
-    float *scale = (is_v ? p.c.v_scale : p.c.k_scale) + ph;
-    uint8_t *base = (is_v ? p.c.v : p.c.k) + ph * ps * D;
-    const float old = held > 0 ? *scale : 0.f;
     // the new tokens into shared memory, rows of D 16-bit values
     constexpr int CH = D / 8;   // 16-byte pieces of a row
     const T *src = reinterpret_cast<const T *>(is_v ? p.v : p.k) + ((long long)(row0 + from - len) * p.c.Hkv + h) * D;
     uint4 *rows = reinterpret_cast<uint4 *>(smem_raw);
     float amax = 0.f;
+#pragma unroll 8
     for (int i = tid; i < T_new * CH; i += kAppendThreads) {
         const int t = i / CH, c = i % CH;
         const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + (long long)t * p.c.Hkv * D) + c);
@@ -111,6 +105,14 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
             amax = y < INFINITY ? fmaxf(amax, y) : amax;
         }
     }
+    if (page < 0 || page >= p.c.num_pages) {   // (the whole CTA)
+        if (tid == 0) atomicOr(p.c.err, kErrBadPage);
+        return;
+    }
+    const long long ph = (long long)page * p.c.Hkv + h;
+    float *scale = (is_v ? p.c.v_scale : p.c.k_scale) + ph;
+    uint8_t *base = (is_v ? p.c.v : p.c.k) + ph * ps * D;
+    const float old = held > 0 ? *scale : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if ((tid & 31) == 0) s_max[tid >> 5] = amax;
@@ -505,8 +507,19 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1)
         c.next(p, s_len);   // (a border behind a segment's last tile: the next one's first)
     };
     Cursor pc, end;   // what is loaded next, and where the worker stops
-    place(w0, pc);
-    place(w1, end);
+    {
+        Cursor c;   // even lanes place the one, odd lanes the other
+        place(lane & 1 ? w1 : w0, c);
+        auto from = [&](int src, Cursor &d) {
+            d.b = __shfl_sync(0xffffffffu, c.b, src), d.hk = __shfl_sync(0xffffffffu, c.hk, src);
+            d.rg = __shfl_sync(0xffffffffu, c.rg, src), d.t = __shfl_sync(0xffffffffu, c.t, src);
+        };
+        from(0, pc);
+        from(1, end);
+        const int t = pc.t;
+        if (pc.b < p.B) pc.open(p, s_len);
+        pc.t = t;
+    }
     auto at_end = [&](const Cursor &c) -> bool {
         return c.b == end.b && c.hk == end.hk && c.rg == end.rg && c.t == end.t;
     };

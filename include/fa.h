@@ -262,6 +262,7 @@ fa_status fa_fwd(const void *q, const void *k, const void *v, void *o, float *ls
  *   head dim itself is contiguous.  Packed varlen tensors have no batch
  *   stride (the first is not looked at).  o_stride: fa_bwd_ext only.  Outputs
  *   and lse are contiguous. */
+/* Zero the struct (window sides: -1) before setting what a call uses. */
 typedef struct {
     int window_left;
     int window_right;

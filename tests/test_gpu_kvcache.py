@@ -188,6 +188,10 @@ ATTEND = [
     ([300, 4], 2, 2, 1, 128, 48, F16, 0.0, 2 ** 31 - 1),
     ([5000], 1, 2, 1, 128, 64, BF, 0.0, -1),                # cut between many workers
     ([16] * 90 + [0] * 10, 1, 2, 2, 64, 16, BF, 0.0, -1),
+    ([250, 33], 1, 16, 1, 128, 96, F16, 0.0, -1),           # 16 rows, three parts of Q; pages of three half tiles
+    ([900, 5, 64], 2, 8, 1, 128, 128, F16, 25.0, 300),
+    ([333, 112, 113], 1, 3, 1, 64, 112, BF, 0.0, -1),
+    ([(7 * i) % 41 for i in range(700)], 1, 1, 1, 64, 16, F16, 0.0, -1),   # more sequences than threads
 ]
 
 
@@ -274,6 +278,57 @@ def test_window_leaves_old_pages_alone(fa, cuda_device):
     cache.block_table[0, :(399 - 50) // 16] = -1
     got = fa.fa_fwd_kvcache(q.cuda(), cache, n, window_left=50)
     assert torch.equal(want[0], got[0]) and fa.device_status() == fa.FA_OK
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once(fa, cuda_device):
+    """Two streams, a workspace each: what one stream alone gives."""
+    c = ([3000, 900, 17], 1, 8, 2, 128, 64, BF, 0.0, -1)
+    d = ([100, 2000], 1, 8, 1, 64, 32, F16, 30.0, -1)
+    runs = [_attend(fa, c, 14), _attend(fa, d, 15)]
+    q = [r[0].cuda() for r in runs]
+    want = [fa.fa_fwd_kvcache(q[i], runs[i][1], runs[i][2], softcap=x[7]) for i, x in enumerate((c, d))]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for i, x in enumerate((c, d)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(fa.fa_fwd_kvcache(q[i], runs[i][1], runs[i][2], softcap=x[7]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, lse in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+@pytest.mark.gpu
+def test_gpu_side_refusals(fa, cuda_device):
+    c = ([40, 50], 1, 2, 1, 64, 16, BF, 0.0, -1)
+    q, cache, n, _ = _attend(fa, c, 16)
+    with pytest.raises(ValueError):
+        fa.fa_fwd_kvcache(q, cache, n)                                  # q on the CPU
+    q = q.cuda()
+    for bad in (dict(q=q.float()), dict(q=q[:1]), dict(q=q[..., :32]), dict(n=n.long()), dict(n=n[:1]), dict(n=n.cpu())):
+        with pytest.raises(ValueError):
+            fa.fa_fwd_kvcache(bad.get("q", q), cache, bad.get("n", n))
+    with pytest.raises(fa.FaError):
+        fa.fa_fwd_kvcache(q, cache, n, softcap=-1.0)
+    with pytest.raises(ValueError):
+        fa.fa_fwd_kvcache(q, cache, n, out=(q, torch.empty(3, device="cuda")))
+    # a strided q is read as it is meant
+    wide = torch.cat([q, q], dim=3)[..., 64:]
+    a, b = fa.fa_fwd_kvcache(wide, cache, n), fa.fa_fwd_kvcache(q, cache, n)
+    assert torch.equal(a[0], b[0])
+    x = torch.zeros((2, 1, 1, 64), dtype=BF, device="cuda")
+    for k, v in ((x, x.half()), (x[:1], x[:1]), (x[..., :32], x[..., :32]), (x, x.cpu()), (x.float(), x.float())):
+        with pytest.raises(ValueError):
+            fa.kvcache_append(cache, n, k, v)
+    with pytest.raises(ValueError):
+        fa.kvcache_append(cache, n, x[:, 0], x[:, 0], cu_new=torch.tensor([0, 1, 2], dtype=torch.int32).cuda())
+    with pytest.raises(ValueError):
+        fa.KvCache(cache.k, cache.v, cache.k_scale, cache.v_scale, cache.block_table.long())
+    with pytest.raises(ValueError):
+        fa.KvCache(cache.k, cache.k, cache.k_scale, cache.v_scale, cache.block_table)
 
 
 @pytest.mark.gpu

@@ -263,6 +263,7 @@ MASKED = [
     (dict(B=1, S=700, doc="mixed", window=(40, -1)), 2, 1, 128, BF, 0.0),
     (dict(B=1, S=300, window=(9, 3), causal=False), 2, 1, 128, F16, 5.0),
     (dict(B=1, S=4200, doc="mixed"), 1, 1, 64, BF, 0.0),
+    (dict(B=1, S=8200, doc="pad"), 1, 1, 64, BF, 0.0),      # intervals of more than 8192 rows
 ]
 
 
@@ -436,6 +437,14 @@ def test_other_strides(fa, cuda_device):
     assert torch.equal(o, o4)
     with pytest.raises(ValueError):
         fa.fa_fwd(*odd, stream=torch.cuda.current_stream())
+    # head dims of the wide backward kernel, slices of a joint projection
+    w = torch.cat(_inputs(1, 140, 140, 2, 2, 192, BF, 62), dim=2).cuda()
+    parts = [w[:, :, 2 * i:2 * i + 2] for i in range(4)]
+    whole = [t.contiguous() for t in parts]
+    a, b = fa.fa_fwd(*parts[:3], causal=True), fa.fa_fwd(*whole[:3], causal=True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    ga, gb = fa.fa_bwd(*parts[:3], a[0], parts[3], a[1], causal=True), fa.fa_bwd(*whole[:3], a[0], whole[3], a[1], causal=True)
+    assert torch.equal(ga[1], gb[1]) and torch.equal(ga[2], gb[2])
     # packed varlen slices of a joint projection
     cu = torch.tensor([0, 60, 150], dtype=torch.int32).cuda()
     kw = dict(cu_seqlens_q=cu, cu_seqlens_k=cu, max_seqlen_q=90, max_seqlen_k=90, causal=True, totals=(150, 150))
