@@ -411,6 +411,120 @@ def test_nan_scores_stay_nan(fa, cuda_device, D, bad):
     assert torch.equal(dq2[0, :, 0], dq[0, :, 0]) and torch.equal(dq2[0, rest, 1], dq[0, rest, 1])
 
 
+# ------------------------------- problems of more query tiles than the GPU has SMs
+# (the forward's two CTAs per SM; tests above mostly have fewer tiles)
+MANY = [
+    # B, S (Sq, Sk), Hq, Hkv, D, dtype, mask keywords (None: the band), causal, window, cap
+    (3, (300, 300), 20, 4, 128, BF, None, True, None, 50.0),
+    (3, (300, 300), 20, 20, 64, F16, None, True, None, 30.0),
+    (2, (333, 200), 40, 8, 64, BF, None, True, None, 20.0),        # rows that see nothing
+    (80, (1, 130), 2, 1, 128, F16, None, True, None, 15.0),        # single queries
+    (2, (257, 390), 32, 8, 120, BF, None, False, (33, 70), 25.0),
+    (2, (400, 400), 24, 2, 72, F16, None, True, (60, -1), 1000.0),
+    (3, (300, 300), 20, 4, 128, F16, dict(doc="mixed"), True, None, 0.0),
+    (3, (300, 300), 20, 4, 64, BF, dict(doc="pad"), True, None, 0.0),
+    (3, (300, 300), 20, 4, 128, BF, dict(doc="pad", prefix="doc"), True, None, 50.0),
+    (160, (65, 65), 2, 1, 64, F16, dict(doc="ones"), True, None, 30.0),
+    (160, (64, 64), 1, 1, 128, BF, dict(doc="none"), True, None, 0.0),
+    (2, (420, 420), 24, 8, 96, BF, dict(doc="again", causal=False), True, None, 0.0),
+    (2, (420, 420), 24, 8, 128, F16, dict(doc="mixed", window=(40, -1)), True, None, 10.0),
+    (1, (2500, 2500), 8, 2, 64, BF, dict(doc="mixed", prefix="seq"), True, None, 0.0),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("c", MANY, ids=lambda c: "b%d_%dx%d_h%d_%d_d%d_%s_%s_c%d_w%s_cap%g" % (
+    c[0], *c[1], *c[2:5], str(c[5])[6:], "_".join("%s%s" % kv for kv in (c[6] or {"band": ""}).items()), *c[7:]))
+def test_many_tiles(fa, cuda_device, c):
+    B, (Sq, Sk), Hq, Hkv, D, dt, mask, causal, window, cap = c
+    assert B * Hq * ((Sq + 127) // 128) > torch.cuda.get_device_properties(0).multi_processor_count
+    x = _inputs(B, Sq, Sk, Hq, Hkv, D, dt, Sq + D, a=1.5 if cap else 1.0)
+    if mask is None:
+        oks, kw = [band(Sq, Sk, causal, window)] * B, dict(causal=causal, window=window)
+    else:
+        m, oks = _mask(dict(B=B, S=Sq, **mask))
+        kw = dict(mask_ranges=_build(fa, B, Sq, m))
+    _check_all(fa, x, oks, D ** -0.5, cap, kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_tiles_used_lengths(fa, cuda_device, D):
+    B, S = 4, 520
+    m, ok = _mask(dict(B=B, S=S, doc="pad"))
+    lens = [(500, 300), (130, 520), (0, 64), (520, 0)]
+    use = dict(seqused_q=torch.tensor([n for n, _ in lens], dtype=torch.int32).cuda(),
+               seqused_k=torch.tensor([n for _, n in lens], dtype=torch.int32).cuda())
+    x = _inputs(B, S, S, 12, 3, D, BF, 9)
+    _check_all(fa, x, ok, D ** -0.5, 40.0, dict(mask_ranges=_build(fa, B, S, m), **use), lens)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,dt", [(64, BF), (128, F16)])
+def test_many_tiles_varlen(fa, cuda_device, D, dt):
+    lens = [(1, 1), (200, 333), (77, 5), (64, 128), (0, 40), (129, 129)] * 8
+    x = [_inputs(1, a, b, 8, 2, D, dt, a + b + i) for i, (a, b) in enumerate(lens)]
+    cat = [torch.cat([y[i][0] for y in x]) for i in range(4)]
+    cu = [torch.tensor([sum(n[i] for n in lens[:j]) for j in range(len(lens) + 1)], dtype=torch.int32).cuda()
+          for i in (0, 1)]
+    q, k, v, g = (t.cuda() for t in cat)
+    kw = dict(causal=True, cu_seqlens_q=cu[0], cu_seqlens_k=cu[1], max_seqlen_q=200, max_seqlen_k=333,
+              totals=(q.shape[0], k.shape[0]), softcap=30.0)
+    o, lse = fa.fa_fwd(q, k, v, **kw)
+    torch.cuda.synchronize()
+    assert fa.device_status() == fa.FA_OK
+    aq = 0
+    for (nq, nk), y in zip(lens, x):
+        ro, rl, _, _, off = attend(y[0][0], y[1][0], y[2][0], band(nq, nk, True), D ** -0.5, 30.0)
+        check(o[aq:aq + nq], ro, off, "o")
+        lg, fin = lse[:, aq:aq + nq].double().cpu(), torch.isfinite(rl)
+        assert ((lg - rl)[fin].abs() <= lse_bound(30.0, rl)[fin]).all()
+        assert torch.equal(torch.isneginf(lg), torch.isneginf(rl))
+        aq += nq
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [149, 150])
+def test_many_tiles_nan_scores(fa, cuda_device, D, bad):
+    q, k, v, _ = (t.cuda() for t in _inputs(1, 200, 200, 90, 90, D, BF, 52))
+    for kw in (dict(causal=True, softcap=30.0), dict(mask_ranges=fa.mask_ranges(1, 200))):
+        want, _ = fa.fa_fwd(q, k, v, **kw)
+        q2, k2 = q.clone(), k.clone()
+        q2[0, 77, 1] = float("nan")
+        k2[0, bad, 0] = float("nan")
+        got, lse = fa.fa_fwd(q2, k2, v, **kw)
+        assert torch.isnan(got[0, 77, 1]).all() and torch.isnan(lse[0, 1, 77])
+        assert torch.isnan(got[0, bad:, 0]).all()
+        assert torch.equal(got[0, :bad, 0], want[0, :bad, 0])
+        rest = [i for i in range(200) if i != 77]
+        assert torch.equal(got[0, rest, 1], want[0, rest, 1]) and torch.equal(got[0, :, 2:], want[0, :, 2:])
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once(fa, cuda_device):
+    """Calls in flight together on two streams give what each gives alone."""
+    r = fa.mask_ranges(3, 300, doc_ids=_doc_ids(3, 300, "pad").cuda())
+    runs = [([t.cuda() for t in _inputs(3, 300, 300, 20, 4, 128, BF, 81)], dict(mask_ranges=r, softcap=30.0)),
+            ([t.cuda() for t in _inputs(2, 333, 333, 40, 8, 64, F16, 82)], dict(causal=True, softcap=20.0))]
+
+    def step(x, kw):
+        o, lse = fa.fa_fwd(*x[:3], **kw)
+        return (o, lse) + fa.fa_bwd(*x[:3], o, x[3], lse, deterministic=True, **kw)
+    want = [step(*a) for a in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in runs]
+    got = [[], []]
+    for _ in range(5):
+        for i, a in enumerate(runs):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(step(*a))
+    torch.cuda.synchronize()
+    for w, many in zip(want, got):
+        for one in many:
+            assert all(torch.equal(a, b) for a, b in zip(w, one))
+
+
 @pytest.mark.gpu
 def test_other_strides(fa, cuda_device):
     """Tensors that lie head by head, or as slices of a wider one, give what
