@@ -91,7 +91,7 @@ def _ext(Hq, window=None, alibi_slopes=None, seqused_q=None, seqused_k=None, bia
     so that the library need not read them back (no stream synchronisation).
     ``head_dim_v``: the value head dim when it differs from q's (else 0).
     ``softcap``: scores become softcap * tanh(score / softcap) (0: none).
-    ``mask_ranges``: a MaskRanges of the call's ``sizes`` (B, Sq, Sk).
+    ``mask_ranges``: a MaskRanges of the call's ``sizes`` (B, Sq, Sk, GPU).
     ``strides``: what ``_inputs`` said of inputs that are not contiguous."""
     if (window is None and alibi_slopes is None and seqused_q is None and seqused_k is None
             and bias is None and dbias is None and dropout is None and totals is None
@@ -103,8 +103,9 @@ def _ext(Hq, window=None, alibi_slopes=None, seqused_q=None, seqused_k=None, bia
             setattr(e, name + "_stride", s)
     e.softcap = float(softcap)
     if mask_ranges is not None:
-        if not isinstance(mask_ranges, MaskRanges) or sizes != (mask_ranges.B, mask_ranges.S, mask_ranges.S):
-            raise ValueError("mask_ranges: what mask_ranges(B, S, ...) returned, for this call's B and S = Sq = Sk")
+        m = mask_ranges
+        if not isinstance(m, MaskRanges) or sizes != (m.B, m.S, m.S, m.buffer.get_device()):
+            raise ValueError("mask_ranges: what mask_ranges(B, S, ...) returned, for this call's B, S = Sq = Sk and GPU")
         e.mask_ranges, e.mask_ranges_bytes = mask_ranges.buffer.data_ptr(), mask_ranges.buffer.numel()
     e.head_dim_v = int(head_dim_v)
     if totals is not None:
@@ -213,7 +214,8 @@ def kvcache_append(cache, cache_len, k_new, v_new, cu_new=None, max_new=None, st
     cache._check("v_new", v_new, k_new.dtype, shape)
     with _on(cache.device):
         _check(lib().fa_kvcache_append(ctypes.byref(c), cache_len.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
-                                       _ptr(cu_new), B, int(max_new), code, _stream(stream)), "fa_kvcache_append")
+                                       _ptr(cu_new), k_new.numel() // (c.Hkv * c.D), B, int(max_new), code,
+                                       _stream(stream)), "fa_kvcache_append")
 
 
 def fa_fwd_kvcache(q, cache, cache_len, softmax_scale=None, softcap=0.0, window_left=-1, workspace=None,
@@ -239,13 +241,14 @@ def fa_fwd_kvcache(q, cache, cache_len, softmax_scale=None, softcap=0.0, window_
     cache._check("cache_len", cache_len, torch.int32, (B,))
     scale = default_scale(D) if softmax_scale is None else float(softmax_scale)
     with _on(cache.device):
-        if out is None:
-            out = torch.empty_like(q), q.new_empty((B, Hq, Sq), dtype=torch.float32)
-        else:
-            cache._check("out[0]", out[0], q.dtype, q.shape)
-            cache._check("out[1]", out[1], torch.float32, (B, Hq, Sq))
-        if workspace is None:
-            workspace = q.new_empty(fa_fwd_kvcache_workspace_bytes(D), dtype=torch.uint8)
+        with _memory(stream):
+            if out is None:
+                out = torch.empty_like(q), q.new_empty((B, Hq, Sq), dtype=torch.float32)
+            else:
+                cache._check("out[0]", out[0], q.dtype, q.shape)
+                cache._check("out[1]", out[1], torch.float32, (B, Hq, Sq))
+            if workspace is None:
+                workspace = q.new_empty(fa_fwd_kvcache_workspace_bytes(D), dtype=torch.uint8)
         _check(lib().fa_fwd_kvcache(q.data_ptr(), ctypes.byref(c), cache_len.data_ptr(), out[0].data_ptr(),
                                     out[1].data_ptr(), B, Sq, Hq, scale, softcap, window_left, code,
                                     workspace.data_ptr(), workspace.numel(), _stream(stream)), "fa_fwd_kvcache")
@@ -271,6 +274,23 @@ _HERE = _Here()
 def _on(index):
     """A context in which GPU ``index`` (None: the current one) is current."""
     return _HERE if index is None or index == torch._C._cuda_getDevice() else torch.cuda.device(index)
+
+
+def _gpu(t):
+    """The index of the GPU a tensor lies on (None: on none)."""
+    return t.get_device() if t.is_cuda else None
+
+
+def _memory(stream):
+    """A context in which memory is allocated for work on ``stream``: a block
+    of the current stream's may still be in use there, and given back it would
+    be used there again, both without regard to the other stream."""
+    if stream is None:
+        return _HERE
+    if not isinstance(stream, torch.cuda.Stream):
+        at = int(getattr(stream, "cuda_stream", stream))
+        stream = torch.cuda.ExternalStream(at) if at else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 class MaskRanges:
@@ -322,7 +342,8 @@ def mask_ranges(B, S, doc_ids=None, prefix_len=None, causal=True, window=None, d
         raise FaError(FA_ERR_INVALID_ARG, "fa_mask_ranges")
     with _on(at):
         if out is None:
-            out = MaskRanges(torch.empty(need, dtype=torch.uint8, device="cuda"), B, S)
+            with _memory(stream):
+                out = MaskRanges(torch.empty(need, dtype=torch.uint8, device="cuda"), B, S)
         per_token = 1 if prefix_len is not None and prefix_len.dim() == 2 else 0
         _check(L.fa_mask_ranges(_ptr(doc_ids), _ptr(prefix_len), per_token, B, S, 1 if causal else 0, wl, wr,
                                 out.buffer.data_ptr(), out.buffer.numel(), _stream(stream)), "fa_mask_ranges")
@@ -380,7 +401,7 @@ def lib():
         L.fa_bwd_workspace_sync_layout.argtypes = _SHAPE + [_i, _i] + [ctypes.POINTER(_sz)] * 3
         L.fa_bwd_workspace_sync_layout.restype = _i
         _kp = ctypes.POINTER(_KvCacheStruct)
-        L.fa_kvcache_append.argtypes = [_kp] + [_vp] * 4 + [_i] * 3 + [_vp]
+        L.fa_kvcache_append.argtypes = [_kp] + [_vp] * 4 + [_i] * 4 + [_vp]
         L.fa_fwd_kvcache_workspace_bytes.argtypes = [_i]
         L.fa_fwd_kvcache_workspace_bytes.restype = _sz
         L.fa_fwd_kvcache.argtypes = [_vp, _kp, _vp, _vp, _vp] + [_i] * 3 + [_f, _f, _i, _i, _vp, _sz, _vp]
@@ -550,20 +571,21 @@ def fa_fwd(q, k, v, causal=False, softmax_scale=None, cu_seqlens_q=None, cu_seql
     (q, k, v), strides = _inputs(stream, q=q, k=k, v=v)
     B, Sq, Sk, Hq, Hkv, D = _shape(q, k, cu_seqlens_q, max_seqlen_q, max_seqlen_k)
     scale = default_scale(D) if softmax_scale is None else float(softmax_scale)
-    o = torch.empty(q.shape[:-1] + (v.shape[-1],), dtype=q.dtype, device=q.device)
-    if cu_seqlens_q is None:
-        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
-    else:
-        lse = torch.empty((Hq, q.shape[0]), dtype=torch.float32, device=q.device)
-    ext = _ext(Hq, window, alibi_slopes, seqused_q, seqused_k, bias, dropout=dropout,
-               totals=totals, head_dim_v=_value_dim(D, v), softcap=softcap, mask_ranges=mask_ranges,
-               sizes=(B, Sq, Sk), strides=strides)
-    args = [_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Sq, Sk, Hq, Hkv, D, scale,
-            int(bool(causal)), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k)]
-    if ext is None:
-        _check(lib().fa_fwd(*args, _dtype_code(q), _stream(stream)), "fa_fwd")
-    else:
-        _check(lib().fa_fwd_ext(*args, ext, _dtype_code(q), _stream(stream)), "fa_fwd_ext")
+    with _on(_gpu(q)), _memory(stream):
+        o = torch.empty(q.shape[:-1] + (v.shape[-1],), dtype=q.dtype, device=q.device)
+        if cu_seqlens_q is None:
+            lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
+        else:
+            lse = torch.empty((Hq, q.shape[0]), dtype=torch.float32, device=q.device)
+        ext = _ext(Hq, window, alibi_slopes, seqused_q, seqused_k, bias, dropout=dropout,
+                   totals=totals, head_dim_v=_value_dim(D, v), softcap=softcap, mask_ranges=mask_ranges,
+                   sizes=(B, Sq, Sk, q.get_device()), strides=strides)
+        args = [_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Sq, Sk, Hq, Hkv, D, scale,
+                int(bool(causal)), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k)]
+        if ext is None:
+            _check(lib().fa_fwd(*args, _dtype_code(q), _stream(stream)), "fa_fwd")
+        else:
+            _check(lib().fa_fwd_ext(*args, ext, _dtype_code(q), _stream(stream)), "fa_fwd_ext")
     return o, lse
 
 
@@ -593,23 +615,24 @@ def fa_bwd(q, k, v, o, dout, lse, causal=False, softmax_scale=None, cu_seqlens_q
     _outputs(dq=dq, dk=dk, dv=dv)
     B, Sq, Sk, Hq, Hkv, D = _shape(q, k, cu_seqlens_q, max_seqlen_q, max_seqlen_k)
     scale = default_scale(D) if softmax_scale is None else float(softmax_scale)
-    dq, dk, dv = (_like(t) if g is None else g for t, g in ((q, dq), (k, dk), (v, dv)))
-    args = [_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk),
-            _ptr(dv), B, Sq, Sk, Hq, Hkv, D, scale, int(bool(causal)), _ptr(cu_seqlens_q),
-            _ptr(cu_seqlens_k), int(bool(deterministic)), _dtype_code(q)]
-    ext = _ext(Hq, window, alibi_slopes, seqused_q, seqused_k, bias, dbias, dropout, totals,
-               _value_dim(D, v), softcap, mask_ranges, (B, Sq, Sk), strides)
-    if ext is not None:
-        st = lib().fa_bwd_ext(*args[:19], ext, *args[19:], _ptr(workspace),
-                              0 if workspace is None else workspace.numel(), _stream(stream))
-        _check(st, "fa_bwd_ext")
-    elif workspace is None:
-        st = lib().fa_bwd(*args, _stream(stream))
-        _check(st, "fa_bwd")
-    else:
-        st = lib().fa_bwd_with_workspace(*args, _ptr(workspace), workspace.numel(),
-                                          _stream(stream))
-        _check(st, "fa_bwd_with_workspace")
+    with _on(_gpu(q)), _memory(stream):
+        dq, dk, dv = (_like(t) if g is None else g for t, g in ((q, dq), (k, dk), (v, dv)))
+        args = [_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk),
+                _ptr(dv), B, Sq, Sk, Hq, Hkv, D, scale, int(bool(causal)), _ptr(cu_seqlens_q),
+                _ptr(cu_seqlens_k), int(bool(deterministic)), _dtype_code(q)]
+        ext = _ext(Hq, window, alibi_slopes, seqused_q, seqused_k, bias, dbias, dropout, totals,
+                   _value_dim(D, v), softcap, mask_ranges, (B, Sq, Sk, q.get_device()), strides)
+        if ext is not None:
+            st = lib().fa_bwd_ext(*args[:19], ext, *args[19:], _ptr(workspace),
+                                  0 if workspace is None else workspace.numel(), _stream(stream))
+            _check(st, "fa_bwd_ext")
+        elif workspace is None:
+            st = lib().fa_bwd(*args, _stream(stream))
+            _check(st, "fa_bwd")
+        else:
+            st = lib().fa_bwd_with_workspace(*args, _ptr(workspace), workspace.numel(),
+                                              _stream(stream))
+            _check(st, "fa_bwd_with_workspace")
     return dq, dk, dv
 
 
@@ -679,7 +702,7 @@ def fa_bwd_stages(q, k, v, o, dout, lse, workspace, causal=False, softmax_scale=
     scale = default_scale(D) if softmax_scale is None else float(softmax_scale)
     dq, dk, dv = (_like(t) if g is None else g for t, g in ((q, dq), (k, dk), (v, dv)))
     shape = [B, Sq, Sk, Hq, Hkv, D]
-    ext = _ext(Hq, window, totals=totals, softcap=softcap, mask_ranges=mask_ranges, sizes=(B, Sq, Sk))
+    ext = _ext(Hq, window, totals=totals, softcap=softcap, mask_ranges=mask_ranges, sizes=(B, Sq, Sk, q.get_device()))
     if ext is not None:
         mask = ((1 if "pre" in stages else 0) | (2 if "main" in stages else 0) |
                 (4 if "post" in stages else 0))

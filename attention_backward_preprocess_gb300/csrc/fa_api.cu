@@ -796,16 +796,18 @@ fa_status check_kv_cache(const fa_kv_cache *c, int B, fa_dtype dtype, fa::KvCach
 }  // namespace
 
 fa_status fa_kvcache_append(const fa_kv_cache *cache, const int *cache_len, const void *k_new, const void *v_new,
-                            const int *cu_new, int B, int max_new, fa_dtype dtype, cudaStream_t stream) {
+                            const int *cu_new, int rows, int B, int max_new, fa_dtype dtype,
+                            cudaStream_t stream) {
     fa::KvAppendParams p;
     std::memset(&p, 0, sizeof(p));
     fa_status st = check_kv_cache(cache, B, dtype, &p.c);
     if (st != FA_OK) return st;
-    if (!cache_len || !k_new || !v_new || max_new <= 0) return FA_ERR_INVALID_ARG;
+    if (!cache_len || !k_new || !v_new || rows <= 0 || max_new <= 0) return FA_ERR_INVALID_ARG;
     if (!aligned16(k_new) || !aligned16(v_new) || (reinterpret_cast<uintptr_t>(cache_len) & 3u) ||
         (reinterpret_cast<uintptr_t>(cu_new) & 3u))
         return FA_ERR_INVALID_ARG;
     if ((long long)B * max_new > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+    if (!cu_new && rows != B * max_new) return FA_ERR_INVALID_ARG;
     if (cache->Hkv > 65535) return FA_ERR_UNSUPPORTED;   // grid columns
     if ((st = check_device()) != FA_OK) return st;
     p.c.err = fa::fwd_error_word();
@@ -814,6 +816,7 @@ fa_status fa_kvcache_append(const fa_kv_cache *cache, const int *cache_len, cons
     p.cu = cu_new;
     p.k = k_new;
     p.v = v_new;
+    p.rows = rows;
     p.B = B;
     p.max_new = max_new;
     return cuda_status(fa::launch_kv_append(p, cache->D, dtype == FA_BF16, stream));

@@ -79,7 +79,11 @@ __device__ __forceinline__ Unit decode_unit(const BwdParams &p, int t) {
     }
     if constexpr (kRange) {
         // longest units first; the deterministic order counts on rising key blocks
-        if (!p.deterministic) u.n_block = __ldg(p.mr_order + (long long)u.b * (p.mr_rows / kBlockN) + u.n_block);
+        // (held inside the table: a buffer filled for other sizes faults nothing)
+        if (!p.deterministic) {
+            const int nb = p.mr_rows / kBlockN;
+            u.n_block = min(max(__ldg(p.mr_order + (long long)u.b * nb + u.n_block), 0), nb - 1);
+        }
         // 64-row blocks [r.x, r.y), inside the used rows
         constexpr int F = BM / 64;
         const int4 r = __ldg(p.mr_key + (long long)u.b * (p.mr_rows / kBlockN) + u.n_block);

@@ -73,9 +73,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
     const int len = p.len[b];
     const int row0 = p.cu ? p.cu[b] : b * p.max_new;
     const int n = p.cu ? p.cu[b + 1] - row0 : p.max_new;
-    // lengths outside what the call said, or tokens past the table: the
+    // lengths or rows outside what the call said, or tokens past the table: the
     // sequence is left alone and the call reports it
-    if (n < 0 || n > p.max_new || row0 < 0 || len < 0 || (long long)len + n > (long long)p.c.max_pages * ps) {
+    if (n < 0 || n > p.max_new || row0 < 0 || (long long)row0 + n > p.rows || len < 0 || (long long)len + n > (long long)p.c.max_pages * ps) {
         if (tid == 0) atomicOr(p.c.err, kErrBadLength);
         return;
     }
@@ -271,6 +271,9 @@ __device__ __forceinline__ float keys_sum(float v) {
     for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+
+// the low c bytes of a word (none below 0, all from 4 on)
+__device__ __forceinline__ uint32_t bytes_below(int c) { return c >= 4 ? 0xffffffffu : (1u << (8 * max(c, 0))) - 1u; }
 
 // First key any of the sequence's queries sees.
 __device__ __forceinline__ int kv_first(const KvAttnParams &p, int n) {
@@ -560,7 +563,7 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1)
         return page;
     };
     int pg = lookup(pc);
-    float ksc = 0.f, vsc = 0.f;   // scales of group r8 / 2 (a lane's keys) of the loaded tile
+    float ksc = -1.f, vsc = 0.f;   // scales of group r8 / 2 (a lane's keys) of the loaded tile
     bool v_ok = false;            // the lane's 16 tokens (group q4) of it are there
     // K of the tile at pc (and its scales), then V of the same tile.  Lanes 0-3
     // copy a group of 16 keys each; groups not read are masked.
@@ -568,7 +571,7 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1)
         if (!loads) return;
         const int page = __shfl_sync(0xffffffffu, pg, r8 >> 1);   // (also: every lane has read the slot)
         const long long ph = (long long)max(page, 0) * p.c.Hkv + pc.hk;
-        ksc = page >= 0 ? __ldg(p.c.k_scale + ph) : 0.f;
+        ksc = page >= 0 ? __ldg(p.c.k_scale + ph) : -1.f;   // negative: not read
         vsc = page >= 0 ? __ldg(p.c.v_scale + ph) : 0.f;
         const bool mine = lane < 4 && pg >= 0;
         const int n = __popc(__ballot_sync(0xffffffffu, mine));
@@ -722,7 +725,7 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1)
         load_k();   // this tile's K has been read
         const float ev = vs > 0.f ? lg2_approx(vs) : -INFINITY;
         // a tile inside every row's keys, all its pages read, takes no compare
-        const bool edge = __any_sync(0xffffffffu, ks == 0.f) || kTile * cc.t < lo_all || kTile * cc.t + kTile - 1 > hi_all;
+        const bool edge = __any_sync(0xffffffffu, ks < 0.f) || kTile * cc.t < lo_all || kTile * cc.t + kTile - 1 > hi_all;
         uint32_t pt[NR][4][2];   // P^T blocks, transposed: the B operand of O^T
         // scores in log2 units, masked; per block of rows
         auto scores = [&](auto edge_tag, int nr, float (&mx)[2]) __attribute__((always_inline)) {
@@ -732,8 +735,8 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1)
             for (int u = 0; u < 8; ++u) {
                 float2 x = f2_unpack(f2_mul(f2_pack(s[nr][u >> 1][2 * (u & 1)], s[nr][u >> 1][2 * (u & 1) + 1]), f2));
                 const int key = key0 + 2 * u;
-                const bool off0 = kEdge && (ks == 0.f || key < lo_r[nr][0] || key > hi_r[nr][0]);
-                const bool off1 = kEdge && (ks == 0.f || key < lo_r[nr][1] || key > hi_r[nr][1]);
+                const bool off0 = kEdge && (ks < 0.f || key < lo_r[nr][0] || key > hi_r[nr][0]);
+                const bool off1 = kEdge && (ks < 0.f || key < lo_r[nr][1] || key > hi_r[nr][1]);
                 if (kCap) {
                     // what lies behind the last token may be NaN: not into the pair
                     if (off0) x.x = 0.f;
@@ -818,9 +821,10 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1)
             break;
         }
         phase ^= 1u;
-        // tokens of the V group that exist: bytes behind them hold anything (such
-        // a tile has keys no row sees)
-        const int nv = v_here ? cc.n - (kTile * cc.t + 16 * q4) : 0;
+        // tokens of the V group that some row sees: bytes before and behind them
+        // hold anything (such a tile has keys a row does not see)
+        const int v0 = kTile * cc.t + 16 * q4;
+        const int v_from = cc.lo - v0, v_to = v_here ? cc.n - v0 : 0;
 #pragma unroll
         for (int dm = 0; dm < DM; ++dm) {
             const uint4 v = ld_shared_v4(v_at + 16 * dm * bw), u = ld_shared_v4(v_at + (16 * dm + 8) * bw);
@@ -828,8 +832,7 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1)
             if (edge) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int c = min(max(nv - 4 * k, 0), 4);
-                    const uint32_t keep = c >= 4 ? 0xffffffffu : (1u << (8 * c)) - 1u;
+                    const uint32_t keep = bytes_below(v_to - 4 * k) & ~bytes_below(v_from - 4 * k);
                     w[k] &= keep;
                     x[k] &= keep;
                 }

@@ -24,7 +24,7 @@ struct KvAppendParams {
     const int *len;        // [B] tokens held before the call
     const int *cu;         // [B + 1] rows of the new tokens; null: max_new each
     const void *k, *v;     // [rows, Hkv, D]
-    int B, max_new;
+    int rows, B, max_new;
 };
 
 struct KvAttnParams {

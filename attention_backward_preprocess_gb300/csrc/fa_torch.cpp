@@ -244,9 +244,10 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
             if (k->size(0) != B) return none();
             max_new = (long)k->size(1);
         }
-        if (max_new <= 0 || max_new > 0x7fffffffL) return none();
+        const int64_t rows = cu ? k->size(0) : (int64_t)B * max_new;
+        if (max_new <= 0 || max_new > 0x7fffffffL || rows <= 0 || rows > 0x7fffffffL) return none();
         return PyLong_FromLong(fa_kvcache_append(kc, (const int *)len->data_ptr(), k->data_ptr(), v->data_ptr(),
-                                                 cu ? (const int *)cu->data_ptr() : nullptr, (int)B, (int)max_new,
+                                                 cu ? (const int *)cu->data_ptr() : nullptr, (int)rows, (int)B, (int)max_new,
                                                  ty == at::kBFloat16 ? FA_BF16 : FA_FP16, stream((int)dev)));
     });
 }

@@ -341,7 +341,8 @@ fa_status fa_bwd_ext(const void *q, const void *k, const void *v, const void *o,
  *   k        [num_pages, Hkv, page_size, D]   16-byte aligned
  *   v        [num_pages, Hkv, D, page_size]   16-byte aligned
  *   k_scale, v_scale   fp32 [num_pages, Hkv]
- * D is 64 or 128.  The caller owns everything; both calls read block_table and
+ * D is 64 or 128.  A cache filled in another way may have any scales that are
+ * finite and not negative.  The caller owns everything; both calls read block_table and
  * the lengths on the device, need no host copy, and can be captured into a
  * CUDA graph.  Table entries past a sequence's tokens are not read.
  *
@@ -349,7 +350,7 @@ fa_status fa_bwd_ext(const void *q, const void *k, const void *v, const void *o,
  * cache_len[b] tokens (device int32 [B]) they hold.  k_new / v_new: [rows,
  * Hkv, D], 16-bit; sequence b's are rows cu_new[b] .. cu_new[b + 1] (device
  * int32 [B + 1]), at most max_new, or with cu_new NULL rows b * max_new ..
- * (b + 1) * max_new.  Per (page, head) the scale becomes 2^e, the smallest e
+ * (b + 1) * max_new (rows = B * max_new).  Per (page, head) the scale becomes 2^e, the smallest e
  * in [-120, 120] with max |new value| <= 448 * 2^e, or stays the larger one a
  * page that already held tokens of the sequence has; if it grows, those are
  * moved to it (rounded again to nearest even).  What a page held before its
@@ -362,7 +363,9 @@ fa_status fa_bwd_ext(const void *q, const void *k, const void *v, const void *o,
  * too.  Query i sits at position p = cache_len[b] - Sq + i and sees the keys
  * j <= p, with window_left >= 0 also j >= p - window_left; a query that sees
  * none gives O = 0, LSE = -inf.  softcap as in fa_ext.  Pages wholly before
- * every query's window are not read.  workspace:
+ * every query's window are not read.  Bytes of tokens that no query of the
+ * sequence sees may hold anything; a NaN among the values of a token that some
+ * of its queries see may reach all of them.  workspace:
  * fa_fwd_kvcache_workspace_bytes(D) bytes, 256-byte aligned, no
  * initialisation; calls that overlap need one each.  Results do not depend on
  * anything but the arguments and the GPU (no atomics).
@@ -372,8 +375,8 @@ fa_status fa_bwd_ext(const void *q, const void *k, const void *v, const void *o,
  * fa_fwd_kvcache more than 4096 sequences, Sq times Hq above 2^24, a cache of
  * 2^31 or more (page, head, dim) rows, or a table so wide that 64-key tiles
  * times heads times sequences reach 2^31.  A length
- * outside [0, max_pages page_size], more new tokens than max_new, or a table
- * entry that is no page is found on the device: such a sequence (or page) is
+ * outside [0, max_pages page_size], more new tokens than max_new or rows, or a
+ * table entry that is no page is found on the device: such a sequence (or page) is
  * neither read nor written, its attention output is 0 / -inf (with a bad page,
  * that over the other pages' tokens), and fa_device_status(NULL, ...) returns
  * FA_ERR_INVALID_ARG.
@@ -386,7 +389,7 @@ typedef struct {
 } fa_kv_cache;
 
 fa_status fa_kvcache_append(const fa_kv_cache *cache, const int *cache_len, const void *k_new,
-                            const void *v_new, const int *cu_new, int B, int max_new,
+                            const void *v_new, const int *cu_new, int rows, int B, int max_new,
                             fa_dtype dtype, cudaStream_t stream);
 
 size_t fa_fwd_kvcache_workspace_bytes(int D);

@@ -281,6 +281,85 @@ def test_window_leaves_old_pages_alone(fa, cuda_device):
 
 
 @pytest.mark.gpu
+def test_other_scales(fa, cuda_device):
+    """A cache filled elsewhere: scales that are no powers of two, and zeros."""
+    c = ([300, 41, 64], 1, 4, 2, 64, 32, BF, 0.0, -1)
+    q, cache, n, plain = _attend(fa, c, 21)
+    g = torch.Generator().manual_seed(22)
+    for s, on in ((plain[2], cache.k_scale), (plain[3], cache.v_scale)):
+        s.mul_(torch.rand(s.shape, generator=g) + 0.5)
+        s[torch.rand(s.shape, generator=g) < 0.3] = 0.0
+        on.copy_(s)
+    o, lse = fa.fa_fwd_kvcache(q.cuda(), cache, n)
+    ro, rl, bound = plain_attention(q, *plain, 64 ** -0.5, 0.0, -1)
+    # the V scale enters P through its logarithm, |log2| < 8 and off by 2^-22 of that: inside eps
+    check(o, ro, bound, "o")
+    assert ((lse.double().cpu() - rl).abs() <= lse_bound(0.0, rl)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,Sq", [(64, 1), (128, 3)])
+def test_nan_before_the_window(fa, cuda_device, D, Sq):
+    """Keys and values of tokens no query sees any more are not looked at."""
+    c = ([300, 41, 64], Sq, 4, 2, D, 32, F16, 0.0, 20)
+    q, cache, n, plain = _attend(fa, c, 23)
+    want = fa.fa_fwd_kvcache(q.cuda(), cache, n, window_left=20)
+    page = c[5]
+    k, v = cache.k.view(torch.uint8), cache.v.view(torch.uint8)
+    for b, tokens in enumerate(c[0]):
+        for t in range(tokens - Sq - 20):
+            at = int(plain[4][b, t // page])
+            k[at, :, t % page] = 0x7F
+            v[at, :, :, t % page] = 0x7F
+    got = fa.fa_fwd_kvcache(q.cuda(), cache, n, window_left=20)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.isfinite(got[0]).all()
+
+
+@pytest.mark.gpu
+def test_given_stream(fa, cuda_device):
+    """A call for another stream than the current one, its workspace and outputs
+    allocated by the call, while the current stream works and allocates."""
+    c = ([3000, 900, 17], 1, 8, 2, 128, 64, BF, 0.0, -1)
+    q, cache, n, _ = _attend(fa, c, 24)
+    q = q.cuda()
+    want = fa.fa_fwd_kvcache(q, cache, n)
+    full = [torch.randn((1, 300, 2, 64), device="cuda").to(BF) for _ in range(3)]
+    ranges = fa.mask_ranges(1, 300)
+    plain = fa.fa_fwd(*full, softcap=9.0, mask_ranges=ranges)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for handle in (side, side.cuda_stream):
+        for _ in range(20):
+            busy = [torch.full((1 << 20,), 3.0, device="cuda") for _ in range(8)]
+            got = fa.fa_fwd_kvcache(q, cache, n, stream=handle)
+            r = fa.mask_ranges(1, 300, stream=handle)
+            o, lse = fa.fa_fwd(*full, softcap=9.0, mask_ranges=r, stream=handle)
+            del busy
+            side.synchronize()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+            assert torch.equal(o, plain[0]) and torch.equal(lse, plain[1])
+
+
+@pytest.mark.gpu
+def test_append_rows_past_the_tensor(fa, cuda_device):
+    """Prefix sums that run past the tensors: that sequence is left alone."""
+    k, v, ks, vs = make_cache(4, 1, 16, 64, 25)
+    table = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32).cuda()
+    dev = [t.cuda() for t in (k, v, ks, vs)]
+    cache = fa.KvCache(*dev, table)
+    n = torch.tensor([3, 4], dtype=torch.int32).cuda()
+    x = torch.randn((5, 1, 64), device="cuda").to(BF)
+    fa.kvcache_append(cache, n, x, x, cu_new=torch.tensor([0, 3, 6], dtype=torch.int32).cuda(), max_new=3)
+    torch.cuda.synchronize()
+    assert fa.device_status() != fa.FA_OK
+    assert fa.device_status() == fa.FA_OK
+    assert not torch.equal(dev[0].view(torch.uint8)[0].cpu(), k.view(torch.uint8)[0])
+    assert torch.equal(dev[0].view(torch.uint8)[2:].cpu(), k.view(torch.uint8)[2:])
+    assert torch.equal(dev[1].view(torch.uint8)[2:].cpu(), v.view(torch.uint8)[2:])
+
+
+@pytest.mark.gpu
 def test_two_calls_at_once(fa, cuda_device):
     """Two streams, a workspace each: what one stream alone gives."""
     c = ([3000, 900, 17], 1, 8, 2, 128, 64, BF, 0.0, -1)
@@ -462,11 +541,11 @@ CACHE_REFUSED = [
 
 
 def _append(fa, s, **over):
-    a = dict(len=0x6000, k=0x7000, v=0x8000, cu=0, B=3, max_new=5, dtype=0)
+    a = dict(len=0x6000, k=0x7000, v=0x8000, cu=0, rows=15, B=3, max_new=5, dtype=0)
     a.update(over)
     vp = ctypes.c_void_p
-    return fa.lib().fa_kvcache_append(ctypes.byref(s), vp(a["len"]), vp(a["k"]), vp(a["v"]), vp(a["cu"]), a["B"],
-                                      a["max_new"], a["dtype"], None)
+    return fa.lib().fa_kvcache_append(ctypes.byref(s), vp(a["len"]), vp(a["k"]), vp(a["v"]), vp(a["cu"]), a["rows"],
+                                      a["B"], a["max_new"], a["dtype"], None)
 
 
 def _attn(fa, s, **over):
@@ -488,7 +567,7 @@ def test_bad_caches_refused(fa, over, status):
 @pytest.mark.parametrize("over,status", [
     (dict(len=0), 1), (dict(k=0), 1), (dict(v=0x8004), 1), (dict(k=0x7008), 1), (dict(cu=0x9002), 1),
     (dict(len=0x6001), 1), (dict(B=0), 1), (dict(max_new=0), 1), (dict(dtype=5), 2),
-    (dict(B=1 << 20, max_new=1 << 20), 1)])
+    (dict(B=1 << 20, max_new=1 << 20), 1), (dict(rows=14), 1), (dict(rows=16), 1), (dict(rows=0, cu=0x9000), 1)])
 def test_append_refused(fa, over, status):
     assert _append(fa, _struct(fa), **over) == status
 
