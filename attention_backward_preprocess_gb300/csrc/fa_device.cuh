@@ -605,4 +605,27 @@ __device__ __forceinline__ void cap_r2(float z0, float z1, float &r0, float &r1)
     r1 = r * a;
 }
 
+// tanh(y) = y q(y^2) for |y| <= 1/2, off by less than 2^-22.8: q a cubic, fitted to
+// the least largest error of tanh.  In a cap's terms y -> y cap_log2 (y in log2
+// units before the cap, softcap * tanh in log2 units after it): c[k] is q's
+// coefficient over cap_log2^(2 k).
+__device__ __forceinline__ void cap_poly(float cap_log2, float (&c)[4]) {
+    const float g = 1.f / (cap_log2 * cap_log2);
+    c[0] = 0.9999976754f;
+    c[1] = -0.3332065642f * g;
+    c[2] = 0.1314514577f * g * g;
+    c[3] = -0.0433724746f * g * g * g;
+}
+// largest of three, and of a value and two magnitudes (NaN is passed over)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+__device__ __forceinline__ float max3_abs(float a, uint32_t b, uint32_t c) {
+    float y;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "r"(b), "r"(c));
+    return y;
+}
+
 }  // namespace fa

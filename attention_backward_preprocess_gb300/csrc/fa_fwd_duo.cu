@@ -5,7 +5,7 @@
 // first, two CTAs to an SM: each has half of tensor memory, shared memory and
 // registers and works in 64-key blocks.  An interval mask leaves a tile few
 // key blocks (documents of a thousand tokens: about five of 128 keys), and a
-// capped score takes the softmax three times a plain one's time, so with one
+// capped score takes the softmax twice a plain one's time, so with one
 // CTA per SM (fa_fwd_tc.cu's shape) most of the time goes by in one warp's
 // chain of latencies at a time: a tile set up, its first K on the way, P V of
 // the last block, O written, exp2 and reciprocal behind one another.  Here the
@@ -14,11 +14,20 @@
 // and SM, 128-key blocks 204 | -; two warps per row (fa_fwd_split.cu) - | 126;
 // a persistent CTA per SM that overlaps one tile's end with the next one's
 // start 165 | 154; two CTAs of 128-key blocks with one S buffer 222 | 180;
-// this one 118 | 124, then 111 | 102 with scores taken in packed pairs.
+// this one 118 | 124, 111 | 102 with scores taken in packed pairs, 111 | 92 with
+// the cap's tanh by a polynomial where a warp's scores lie within half the cap:
+// exp2, reciprocal and exp2 again, 12 of the exponential unit's cycles per score
+// and warp, were 1 / 2 of the time (unit 45 % busy, two warps per scheduler).
+// What is left at 8192 tokens: per 64-key block 1480 cycles in each of two CTAs,
+// of which 640 are MMA (128 x 64 SS steps at 48 cycles for 32 of math), and 9000
+// of a tile's 29000 cycles from launch to first S and from last S to O.
 //
-// Per block: S = Q K^T (tcgen05 SS, 128 x 64) into one of two TMEM buffers, P =
-// exp2(S c log2e - m) written over its first half as 16-bit pairs, O += P V
-// (TS); S of block n + 1 is issued before O += P V of block n.  K and V have
+// Per block: S = Q K^T (tcgen05 SS, 128 x 64), P = exp2(S c log2e - m) as 16-bit
+// pairs into one of two TMEM buffers, O += P V (TS).  S has one buffer, free
+// once the softmax warps hold it in registers: S of block n + 1 is issued then,
+// and P of block n behind O += P V of block n - 2, which was issued before S of
+// block n and is complete with it.   (With two S buffers, P over half
+// of its own, S waited for that product: 112 | 93 us.)  K and V have
 // rings of their own (a K slot is free once its S is done).  The running
 // maximum is raised only past 2^8, as in fa_fwd_tc.cu.
 //
@@ -41,8 +50,8 @@ struct DuoCfg {
     static constexpr int kStages = (kD == 128) ? 2 : 4;   // slots of the K ring and of the V ring
     static constexpr int kThreads = 8 * 32;
     static constexpr int W_SM = 4;                         // first softmax warp
-    // TMEM: S buffer x2 (P overwrites the first half of each) | O
-    static constexpr int TM_S = 0, TM_O = 2 * BN, TM_COLS = 256;
+    // TMEM: S | P x2 (16-bit pairs) | O
+    static constexpr int TM_S = 0, TM_P = BN, TM_O = 2 * BN, TM_COLS = 256;
     static_assert(TM_O + D <= TM_COLS, "TMEM overflow");
     static constexpr int Q_BYTES = BM * D * 2, KV_BYTES = BN * D * 2;
     static constexpr int OFF_Q = 0;
@@ -65,9 +74,10 @@ struct DuoCfg {
 
 enum {
     U_Q_FULL = 0,     // (its second phase: every MMA done)
-    U_S_FULL = 1,     // +b: S of the block in S buffer b complete
-    U_P_FULL = 3,     // +b: P written back (and O rescaled) by the 4 softmax warps
-    U_PV_DONE = 5,    // +b: O += P V of the block in S buffer b complete
+    U_S_FULL = 1,     // S of the block complete
+    U_S_FREE = 2,     // S in the registers of the 4 softmax warps
+    U_P_FULL = 3,     // +b: P written (and O rescaled) by the 4 softmax warps
+    U_PV_DONE = 5,    // +b: O += P V of the block with P buffer b complete
     U_O_FINAL = 7,    // (the rings' barriers follow)
 };
 
@@ -115,8 +125,9 @@ __global__ void __launch_bounds__(DuoCfg<kD, T>::kThreads, 2)
     if (threadIdx.x == 0) {
         *abort_flag = 0;
         mbar_init(bar(U_Q_FULL), 1);
+        mbar_init(bar(U_S_FULL), 1);
+        mbar_init(bar(U_S_FREE), 4);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(U_S_FULL + i), 1);
             mbar_init(bar(U_P_FULL + i), 4);
             mbar_init(bar(U_PV_DONE + i), 1);
         }
@@ -187,26 +198,25 @@ __global__ void __launch_bounds__(DuoCfg<kD, T>::kThreads, 2)
                 const uint64_t dV_mn = sw128_desc(sbase + C::OFF_V + st * C::KV_BYTES, BN * 128, 1024);
 #pragma unroll
                 for (int kk = 0; kk < BN / 16; ++kk)
-                    mma_ts_warp(tmem + C::TM_O, tmem + C::TM_S + bb * BN + 8 * kk, desc_add(dV_mn, kk * 2048),
+                    mma_ts_warp(tmem + C::TM_O, tmem + C::TM_P + bb * (BN / 2) + 8 * kk, desc_add(dV_mn, kk * 2048),
                                 C::IDESC_PV, (n > 0 || kk > 0) ? 1u : 0u);
                 mma_commit_warp(bar(U_PV_DONE + bb));
                 mma_commit_warp(bar(C::v_empty(st)));
                 return true;
             };
             for (int n = 0; ok && n < nblk; ++n) {
-                const int bb = n & 1, st = n % S;
+                const int st = n % S;
                 if (!(ok = mbar_wait_warp(bar(C::k_full(st)), (uint32_t)(n / S) & 1u, w))) break;
-                // S buffer bb last held P of block n - 2
-                if (n >= 2 && !(ok = mbar_wait_warp(bar(U_PV_DONE + bb), (uint32_t)((n - 2) >> 1) & 1u, w))) break;
+                if (n >= 1 && !(ok = mbar_wait_warp(bar(U_S_FREE), (uint32_t)(n - 1) & 1u, w))) break;
                 tc_fence_after();
                 const uint64_t dK_k = sw128_desc(sbase + C::OFF_K + st * C::KV_BYTES, 16, 1024);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t ko = (kk / 4) * (BN * 128) + (kk % 4) * 32;
                     const uint32_t qo = (kk / 4) * (BM * 128) + (kk % 4) * 32;
-                    mma_ss_warp(tmem + C::TM_S + bb * BN, desc_add(dQ_k, qo), desc_add(dK_k, ko), C::IDESC_S, kk > 0);
+                    mma_ss_warp(tmem + C::TM_S, desc_add(dQ_k, qo), desc_add(dK_k, ko), C::IDESC_S, kk > 0);
                 }
-                mma_commit_warp(bar(U_S_FULL + bb));
+                mma_commit_warp(bar(U_S_FULL));
                 mma_commit_warp(bar(C::k_empty(st)));
                 if (n >= 1 && !(ok = issue_pv(n - 1))) break;
             }
@@ -225,25 +235,45 @@ __global__ void __launch_bounds__(DuoCfg<kD, T>::kThreads, 2)
         int kmin = (int)max(0LL, (long long)qi + diag - p.win_lo);
         int kmax = (int)min((long long)lk - 1, (long long)qi + diag + p.win_hi);
         if (kRange && p.mr_row) row_range(p, b, qi, lq, lk, &kmin, &kmax);
+        // softcap tanh(s / softcap) log2 e = y q(y^2) for y = s log2 e within half the
+        // cap (raw scores within tanh_top)
+        float tq[4] = {};
+        if (kCap) cap_poly(p.cap_log2, tq);
+        const float tanh_top = 0.5f * p.cap_log2 / p.scale_log2;
         float m_run = -INFINITY, l_run = 0.f;       // running max (log2 units), row sum
         bool ok = true;
         for (int n = 0; n < nblk; ++n) {
             const int bb = n & 1;
             const int kb = (n_begin + n) * BN;
-            if (!(ok = mbar_wait_warp(bar(U_S_FULL + bb), (uint32_t)(n >> 1) & 1u, w))) break;
+            if (!(ok = mbar_wait_warp(bar(U_S_FULL), (uint32_t)n & 1u, w))) break;
             tc_fence_after();
-            const uint32_t scol = lane_addr + C::TM_S + bb * BN;
+            const uint32_t scol = lane_addr + C::TM_S, pcol = lane_addr + C::TM_P + bb * (BN / 2);
             // element e of the block (key kb + e) is visible iff lo <= e <= hi
             const int lo = kmin - kb, hi = kmax - kb;
             const bool edge = __any_sync(0xffffffffu, lo > 0 || hi < BN - 1);
             float alpha = 1.f, m_use = m_run;
             uint64_t sumv[4] = {0ull, 0ull, 0ull, 0ull};   // row sum: pairs, four independent chains
-            auto block_pass = [&](auto mask_tag) __attribute__((always_inline)) {
-                constexpr bool kMask = decltype(mask_tag)::value;
+            // One block.  kMask: hidden keys are masked.  Under a cap the pass without
+            // masks takes the tanh by its polynomial, and gives up (false, nothing
+            // written) on a score beyond half the cap; the pass with masks takes
+            // any.  (Two bodies, not four: a body runs from the instruction cache
+            // only when it is not alone in its block.)
+            auto block_pass = [&](auto mask_tag) __attribute__((always_inline)) -> bool {
+                constexpr bool kMask = decltype(mask_tag)::value, kPoly = kCap && !kMask;
                 uint32_t sr[BN / 32][32];
 #pragma unroll
                 for (int c = 0; c < BN / 32; ++c) tmem_ld32(scol + 32 * c, sr[c]);
                 tmem_wait_ld();
+                if (kPoly) {
+                    float top[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int e = 0; e < BN; e += 2)
+                        top[e / 2 & 3] = max3_abs(top[e / 2 & 3], sr[e / 32][e % 32], sr[e / 32][e % 32 + 1]);
+                    if (!__all_sync(0xffffffffu, fmaxf(max3(top[0], top[1], top[2]), top[3]) <= tanh_top)) return false;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(U_S_FREE));
                 // hidden keys at -inf: one bit test and one select per score
                 if (kMask) {
 #pragma unroll
@@ -260,10 +290,13 @@ __global__ void __launch_bounds__(DuoCfg<kD, T>::kThreads, 2)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) mxv[i] = __uint_as_float(sr[0][i]);
 #pragma unroll
-                for (int e = 8; e < BN; ++e) mxv[e & 7] = fmaxf(mxv[e & 7], __uint_as_float(sr[e / 32][e % 32]));
-                float mx = fmaxf(fmaxf(fmaxf(mxv[0], mxv[1]), fmaxf(mxv[2], mxv[3])),
-                                 fmaxf(fmaxf(mxv[4], mxv[5]), fmaxf(mxv[6], mxv[7])));
-                if (kCap) {
+                for (int e = 8; e < BN; e += 2)
+                    mxv[e / 2 & 7] = max3(mxv[e / 2 & 7], __uint_as_float(sr[e / 32][e % 32]), __uint_as_float(sr[e / 32][e % 32 + 1]));
+                float mx = fmaxf(max3(max3(mxv[0], mxv[1], mxv[2]), mxv[3], mxv[4]), max3(mxv[5], mxv[6], mxv[7]));
+                if (kPoly) {
+                    const float y = mx * p.scale_log2, u = y * y;
+                    mx = y * fmaf(u, fmaf(u, fmaf(u, tq[3], tq[2]), tq[1]), tq[0]);
+                } else if (kCap) {
                     float r0, r1;
                     cap_r2(mx * p.cap_k, 0.f, r0, r1);
                     mx = mx == -INFINITY ? mx : fmaf(-2.f * p.cap_log2, r0, p.cap_log2);
@@ -274,9 +307,9 @@ __global__ void __launch_bounds__(DuoCfg<kD, T>::kThreads, 2)
                 m_use = (m_run == -INFINITY || m_new > m_run + kRescaleLog2) ? m_new : m_run;
                 alpha = (m_use == m_run) ? 1.f : ex2(m_run - m_use);
                 const float mref = (m_use == -INFINITY) ? 0.f : m_use;
-                const float cl = kCap ? p.cap_log2 - mref : -mref, cm = -2.f * p.cap_log2;
+                const float cl = kCap && !kPoly ? p.cap_log2 - mref : -mref, cm = -2.f * p.cap_log2;
                 const uint64_t cl2 = f2_pack(cl, cl), cm2 = f2_pack(cm, cm), one2 = f2_pack(1.f, 1.f);
-                const uint64_t k2 = kCap ? f2_pack(p.cap_k, p.cap_k) : f2_pack(p.scale_log2, p.scale_log2);
+                const uint64_t k2 = kCap && !kPoly ? f2_pack(p.cap_k, p.cap_k) : f2_pack(p.scale_log2, p.scale_log2);
                 // pass 2: P as pairs into the first BN/2 columns
 #pragma unroll
                 for (int c = 0; c < BN / 32; ++c) {
@@ -285,7 +318,13 @@ __global__ void __launch_bounds__(DuoCfg<kD, T>::kThreads, 2)
                     for (int i = 0; i < 16; ++i) {
                         const uint64_t raw = f2_pack(__uint_as_float(sr[c][2 * i]), __uint_as_float(sr[c][2 * i + 1]));
                         float2 x;
-                        if (kCap) {
+                        if (kPoly) {
+                            const uint64_t y = f2_mul(raw, k2), u = f2_mul(y, y);
+                            uint64_t t = f2_fma(u, f2_pack(tq[3], tq[3]), f2_pack(tq[2], tq[2]));
+                            t = f2_fma(u, t, f2_pack(tq[1], tq[1]));
+                            t = f2_fma(u, t, f2_pack(tq[0], tq[0]));
+                            x = f2_unpack(f2_fma(y, t, cl2));
+                        } else if (kCap) {
                             // (cap_r2 on packed pairs)
                             const float2 z = f2_unpack(f2_mul(raw, k2));
                             const float2 a = f2_unpack(f2_add(f2_pack(cap_exp(z.x), cap_exp(z.y)), one2));
@@ -302,11 +341,11 @@ __global__ void __launch_bounds__(DuoCfg<kD, T>::kThreads, 2)
                         sumv[i & 3] = f2_add(sumv[i & 3], f2_pack(p0, p1));
                         pk[i] = Cvt<T>::pack(p0, p1);
                     }
-                    tmem_st16(scol + 16 * c, pk);
+                    tmem_st16(pcol + 16 * c, pk);
                 }
+                return true;
             };
-            if (edge) block_pass(std::true_type{});
-            else block_pass(std::false_type{});
+            if (edge || !block_pass(std::false_type{})) block_pass(std::true_type{});
             const float2 sum = f2_unpack(f2_add(f2_add(sumv[0], sumv[1]), f2_add(sumv[2], sumv[3])));
             l_run = l_run * alpha + (sum.x + sum.y);
             m_run = m_use;
