@@ -609,12 +609,13 @@ __device__ __forceinline__ void cap_r2(float z0, float z1, float &r0, float &r1)
 // the least largest error of tanh.  In a cap's terms y -> y cap_log2 (y in log2
 // units before the cap, softcap * tanh in log2 units after it): c[k] is q's
 // coefficient over cap_log2^(2 k).
+constexpr float kTanh0 = 0.9999976754f, kTanh1 = -0.3332065642f, kTanh2 = 0.1314514577f, kTanh3 = -0.0433724746f;
 __device__ __forceinline__ void cap_poly(float cap_log2, float (&c)[4]) {
     const float g = 1.f / (cap_log2 * cap_log2);
-    c[0] = 0.9999976754f;
-    c[1] = -0.3332065642f * g;
-    c[2] = 0.1314514577f * g * g;
-    c[3] = -0.0433724746f * g * g * g;
+    c[0] = kTanh0;
+    c[1] = kTanh1 * g;
+    c[2] = kTanh2 * g * g;
+    c[3] = kTanh3 * g * g * g;
 }
 // largest of three, and of a value and two magnitudes (NaN is passed over)
 __device__ __forceinline__ float max3(float a, float b, float c) {
