@@ -38,10 +38,11 @@ __device__ __forceinline__ uint32_t f32_to_e4m3x2(float lo, float hi) {
 // settles the page's scale, moves tokens the page held before to it if it
 // grew, and writes the new ones.  The CTA owns the page, so bytes are merged
 // without atomics.  What bounds it: 3 bytes moved per value, and for a
-// decoding step the latency of one read, one reduction and one write (3.4 us).
-// Prompts (51 MB moved) take 11.4 us, 4.5 TB/s; with floats compared and every
-// byte of V tested 12.6, the ALU 58 % busy.
-constexpr int kAppendThreads = 128;
+// decoding step the latency of one read, one reduction and one write.
+// Prompts (51 MB moved, nothing in L2 before) take 16.5 us, 3.1 TB/s: three
+// dependent reads from memory per CTA, in two waves of CTAs.  With 128 threads
+// 18.0; with loads that the compiler was left to batch 20.4; with floats compared
+// and every byte of V tested 18.0 (but 12.6 against 10.6 with the tokens in L2).
 
 // smallest e with amax <= 448 * 2^e = 1.75 * 2^(e + 8), held in [-120, 120]
 __device__ __forceinline__ int scale_exponent(float amax) {
@@ -72,10 +73,10 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-template <int D, typename T>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ KvAppendParams p, int per_seq) {
+template <int D, typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ KvAppendParams p, int per_seq) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint32_t s_max[kAppendThreads / 32];
+    __shared__ uint32_t s_max[kThreads / 32];
     const int ps = p.c.page, tid = threadIdx.x;
     const int b = blockIdx.x / per_seq, h = blockIdx.y;
     const bool is_v = blockIdx.z != 0;
@@ -95,17 +96,25 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
     const int page = p.c.table[(long long)b * p.c.max_pages + pi];
     const int held = from - pi * ps, T_new = to - from;   // tokens before, new tokens
     // the new tokens into shared memory, rows of D 16-bit values
-    constexpr int CH = D / 8;   // 16-byte pieces of a row
+    constexpr int CH = D / 8, PER = kThreads == 128 ? 2 : 4;   // 16-byte pieces of a row, and per thread
     const T *src = reinterpret_cast<const T *>(is_v ? p.v : p.k) + ((long long)(row0 + from - len) * p.c.Hkv + h) * D;
     uint4 *rows = reinterpret_cast<uint4 *>(smem_raw);
     uint32_t top = 0u;   // largest magnitudes, as bits: of the low and of the high halves
-#pragma unroll 8
-    for (int i = tid; i < T_new * CH; i += kAppendThreads) {
-        const int t = i / CH, c = i % CH;
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + (long long)t * p.c.Hkv * D) + c);
-        rows[i] = v;
-        top = max_u16x2(max_u16x2(top, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
-        top = max_u16x2(max_u16x2(top, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
+    for (int i0 = tid; i0 < T_new * CH; i0 += PER * kThreads) {
+        uint4 v[PER];   // all on their way at once
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int i = i0 + k * kThreads, t = i / CH, c = i % CH;
+            v[k] = i < T_new * CH ? __ldg(reinterpret_cast<const uint4 *>(src + (long long)t * p.c.Hkv * D) + c)
+                                  : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int i = i0 + k * kThreads;
+            if (i < T_new * CH) rows[i] = v[k];
+            top = max_u16x2(max_u16x2(top, v[k].x & 0x7fff7fffu), v[k].y & 0x7fff7fffu);
+            top = max_u16x2(max_u16x2(top, v[k].z & 0x7fff7fffu), v[k].w & 0x7fff7fffu);
+        }
     }
     constexpr uint32_t kInf = Cvt<T>::is_bf16 ? 0x7f80u : 0x7c00u;
     top = max(top >> 16, top & 0xffffu);
@@ -113,7 +122,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
         // NaN and infinities do not set the scale (stored as NaN / saturated): the
         // thread's pieces again without them
         top = 0u;
-        for (int i = tid; i < T_new * CH; i += kAppendThreads)
+        for (int i = tid; i < T_new * CH; i += kThreads)
             for (int k = 0; k < 8; ++k) {
                 const uint32_t x = reinterpret_cast<const uint16_t *>(rows + i)[k] & 0x7fffu;
                 top = x < kInf ? max(top, x) : top;
@@ -131,7 +140,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
     if ((tid & 31) == 0) s_max[tid >> 5] = top;
     __syncthreads();   // also: every thread has read the old scale
 #pragma unroll
-    for (int i = 0; i < kAppendThreads / 32; ++i) top = max(top, s_max[i]);
+    for (int i = 0; i < kThreads / 32; ++i) top = max(top, s_max[i]);
     const float amax = Cvt<T>::unpack(top).x;
     const float now = fmaxf(old, pow2(scale_exponent(amax)));
     const float ratio = old / now, inv = 1.f / now;   // powers of two: exact
@@ -140,7 +149,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
     const T *xs = reinterpret_cast<const T *>(smem_raw);
     if (!is_v) {
         if (move) {
-            for (int i = tid; i < held * (D / 16); i += kAppendThreads) {
+            for (int i = tid; i < held * (D / 16); i += kThreads) {
                 uint4 *at = reinterpret_cast<uint4 *>(base) + i;
                 const uint4 v = *at;
                 uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -148,7 +157,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
                 *at = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
-        for (int i = tid; i < T_new * (D / 16); i += kAppendThreads) {
+        for (int i = tid; i < T_new * (D / 16); i += kThreads) {
             const uint32_t *x = reinterpret_cast<const uint32_t *>(xs) + 8 * i;
             uint32_t w[4];
 #pragma unroll
@@ -167,8 +176,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
     const int g0 = move ? 0 : held / 16;
     int g1 = (held + T_new + 15) / 16;
     const int ga = (held + 15) / 16, gw = max((held + T_new) / 16 - ga, 0);   // pieces [ga, ga + gw) are whole
-#pragma unroll 2
-    for (int i = tid; i < gw * (D / 2); i += kAppendThreads) {
+#pragma unroll 1
+    for (int i = tid; i < gw * (D / 2); i += kThreads) {
         const int g = ga + i / (D / 2), d = 2 * (i % (D / 2));
         const T *x = xs + (16 * g - held) * D + d;
         uint32_t w0[4], w1[4];
@@ -185,7 +194,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
         at[ps / 16] = make_uint4(w1[0], w1[1], w1[2], w1[3]);
     }
     g1 -= gw;
-    for (int i = tid; i < (g1 - g0) * D; i += kAppendThreads) {
+#pragma unroll 1
+    for (int i = tid; i < (g1 - g0) * D; i += kThreads) {
         int g = g0 + i / D;
         if (gw > 0 && g >= ga) g += gw;   // over the whole ones
         const int d = i % D, t0 = 16 * g - held;   // t0: new token of the piece's first byte
@@ -1033,7 +1043,9 @@ cudaError_t launch_append_t(const KvAppendParams &p, cudaStream_t stream) {
     if (per_seq * p.B > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const int smem = (p.max_new < p.c.page ? p.max_new : p.c.page) * D * 2;
     const dim3 grid((unsigned)(per_seq * p.B), (unsigned)p.c.Hkv, 2);
-    kv_append_kernel<D, T><<<grid, kAppendThreads, smem, stream>>>(p, (int)per_seq);
+    // (a decoding step's one token a page: 5.4 us a call with 128 threads, 6.2 with 256)
+    if (smem > 4096) kv_append_kernel<D, T, 256><<<grid, 256, smem, stream>>>(p, (int)per_seq);
+    else kv_append_kernel<D, T, 128><<<grid, 128, smem, stream>>>(p, (int)per_seq);
     return cudaGetLastError();
 }
 
