@@ -80,10 +80,9 @@ __device__ __forceinline__ Unit decode_unit(const BwdParams &p, int t) {
     if constexpr (kRange) {
         // longest units first; the deterministic order counts on rising key blocks
         // (held inside the table: a buffer filled for other sizes faults nothing)
-        if (!p.deterministic) {
-            const int nb = p.mr_rows / kBlockN;
-            u.n_block = min(max(__ldg(p.mr_order + (long long)u.b * nb + u.n_block), 0), nb - 1);
-        }
+        if (!p.deterministic)
+            u.n_block = (int)min((uint32_t)__ldg(p.mr_order + (long long)u.b * (p.mr_rows / kBlockN) + u.n_block),
+                                 (uint32_t)(p.mr_rows / kBlockN - 1));
         // 64-row blocks [r.x, r.y), inside the used rows
         constexpr int F = BM / 64;
         const int4 r = __ldg(p.mr_key + (long long)u.b * (p.mr_rows / kBlockN) + u.n_block);
