@@ -580,12 +580,11 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Capped scores.  With e = exp(2 y), tanh(y) = 1 - 2 r and 1 - tanh(y)^2 =
-// 4 r (1 - r) for r = 1 / (1 + e): one exp2 per score and one reciprocal per
-// two, 1 / a = b / (a b).  z = 2 y log2(e) is held at 60, where r is below
+// Capped scores.  With e = exp(2 y), tanh(y) = 1 - 2 r for r = 1 / (1 + e): one
+// exp2 per score and one reciprocal per two, 1 / a = b / (a b).  z = 2 y log2(e) is held at 60, where r is below
 // 2^-59 and tanh rounds to 1, so that the product of two 1 + e stays finite;
 // NaN passes, to both scores of a pair: the forward passes pair keys of one
-// query and zero the hidden ones first, so that only a row that is NaN anyway
+// query and take the hidden ones out first, so that only a row that is NaN anyway
 // sees it.  The error of 1 - 2 r is absolute, about 2^-22 (ex2 and rcp
 // each within 2^-22 of their result, r <= 1), which is what a capped score of
 // softcap * tanh needs: tanh.approx, one instruction, is off by 2^-11.
