@@ -23,7 +23,7 @@ SOURCES = ["fa_api.cu", "fa_bwd_main.cu", "fa_bwd_wide.cu", "fa_fwd_tc.cu", "fa_
            "fa_kernels.cu", "fa_ranges.cu", "fa_kvcache.cu",
            "fa_selftest.cu", "fa_noalloc.cu"]
 HEADERS = ["fa_device.cuh", "fa_params.h", "fa_fwd_common.h", "fa_bwd_units.cuh", "fa_ranges.h",
-           "fa_fwd_ranges.cuh", "fa_kvcache.h"]
+           "fa_fwd_ranges.cuh", "fa_kvcache.h", "fa_epilogue.h"]
 PUBLIC_HEADERS = [os.path.join(ROOT, "include", h) for h in ("fa.h", "fa_selftest.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

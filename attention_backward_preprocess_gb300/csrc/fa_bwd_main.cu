@@ -56,6 +56,7 @@
 // MMA and TMA load it issued completes before tensor memory is freed.
 #include "fa_bwd_units.cuh"
 #include "fa_device.cuh"
+#include "fa_epilogue.h"
 #include "fa_params.h"
 
 namespace fa {
@@ -143,7 +144,7 @@ struct MainCfg {
     static constexpr int OFF_LSE = OFF_STG + STG_BYTES;
     static constexpr int OFF_DV = OFF_LSE + kStages * BM * 4;
     static constexpr int OFF_BAR = OFF_DV + kStages * BM * 4;
-    static constexpr int NUM_BARS = 54;
+    static constexpr int NUM_BARS = 55;
     static_assert(40 + 2 * kStages <= 46, "barrier slots");
     // TMEM slot (+0), abort flag (+16), unit ring (+32), chunk rows (+48)
     static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
@@ -187,7 +188,8 @@ enum {
     B_FREE_A = 48,      // warp A's MMAs of a unit completed (its reads of both slots)
     B_FREE_B = 49,      // warp B's MMAs of a unit completed (its reads of the K slot)
     B_EPI_FULL = 50,    // +g: softmax group g wrote a dK / dV slice into its staging tile
-    B_EPI_FREE = 52     // +g: the tensor store of group g has read its staging tile
+    B_EPI_FREE = 52,    // +g: the tensor store of group g has read its staging tile
+    B_EPI_DONE = 54     // both groups' last stores of a unit have read their tiles
 };
 
 struct MainMaps {
@@ -377,6 +379,7 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
             mbar_init(bar(B_EPI_FULL + g), 4);
             mbar_init(bar(B_EPI_FREE + g), 1);
         }
+        mbar_init(bar(B_EPI_DONE), 2);
         for (int b = 0; b < 3; ++b) {
             mbar_init(bar(B_S_FULL + b), 1);
             mbar_init(bar(B_P_FULL + b), 8);
@@ -1007,7 +1010,7 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
         const int g4 = lane >> 2, q4 = lane & 3;     // 16-lane access shapes
         const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
         uint32_t s_ph = 0, dp_ph = 0, st_ph = 0, acc_ph = 0, dsb_ph = 0;   // s_ph, dsb_ph: bit per buffer
-        uint32_t epi_ph = 0;             // parity of this group's staging-tile barriers
+        EpiPhases epi;                   // phases of the dK / dV staging tiles
         int stage = 0, cb = 0, db = 0;   // stage, S buffer, dS^T tile of the step
         bool ok = true;
         // dBias rows take 16-byte stores when every row starts on a 16-byte boundary
@@ -1320,8 +1323,12 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
                     }
                     if (ch == 0) {
                         // the dS^T tile db may still be read by the dQ MMA of step
-                        // j-2: wait before the first write into it
-                        if (!(ok = mbar_wait(bar(B_DSB_FREE + db), bit(dsb_ph, db) ^ 1u, w))) break;
+                        // j-2, and in a unit's first step by either group's dK / dV
+                        // store of the unit before (they stage in both tiles): wait
+                        // before the first write into it
+                        if (!(ok = mbar_wait(bar(B_DSB_FREE + db), bit(dsb_ph, db) ^ 1u, w) &&
+                                   (it > 0 || mbar_wait(bar(B_EPI_DONE), epi.stored(), w))))
+                            break;
                         dsb_ph ^= 1u << db;
                     }
 #pragma unroll
@@ -1449,7 +1456,9 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
                 // of its [128 keys x D] tile in dS^T tile g (free once the last
                 // dQ^T MMA -- and, D = 128, the issuer -- finished with both
                 // tiles) in the store's 128-byte swizzle; the group's first
-                // lane issues the store and waits until it has read the tile.
+                // lane issues the store and waits until it has read the tile.  (The
+                // other group's tile: B_EPI_DONE, looked at before the next unit's
+                // first dS^T write, so that its S and P run meanwhile.)
                 bool free_ok = true;
                 for (int d = 0; d < 2; ++d)
                     free_ok = free_ok && mbar_wait(bar(B_DSB_FREE + d), bit(dsb_ph, d) ^ 1u, w);
@@ -1457,7 +1466,7 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
                 const uint32_t tile = sbase + C::OFF_DS + grp * C::DS_BYTES;
                 const CUtensorMap *omap = grp == 0 ? &maps.dk : &maps.dv;
 #pragma unroll 1
-                for (int sl = 0; sl < D / 64; ++sl) {
+                for (int sl = 0; sl < EpiPhases::slices(D); ++sl) {
 #pragma unroll
                     for (int h2 = 0; h2 < 2; ++h2) {
                         uint32_t a[32];
@@ -1474,7 +1483,7 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
                             st_shared_v4(tile + j * 128 + (((4 * h2 + c) ^ (j & 7)) << 4), pk[4 * c],
                                          pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
                     }
-                    if (sl == D / 64 - 1) {
+                    if (sl == EpiPhases::slices(D) - 1) {
                         // the accumulators are read: the next unit may use them
                         tc_fence_before();
                         __syncwarp();
@@ -1484,22 +1493,21 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_EPI_FULL + grp));
                     if (quarter == 0) {
-                        if (!(ok = mbar_wait_warp(bar(B_EPI_FULL + grp), epi_ph, w))) break;
+                        if (!(ok = mbar_wait_warp(bar(B_EPI_FULL + grp), epi.slice(), w))) break;
                         if (lane == 0) {
                             tma_store_4d(omap, tile, 64 * sl, u.hk, u.k_row0 + n0, u.bidx);
                             bulk_commit_group();
                             bulk_wait_read_all();
                             mbar_arrive(bar(B_EPI_FREE + grp));
+                            if (sl == EpiPhases::slices(D) - 1) mbar_arrive(bar(B_EPI_DONE));
                         }
                         __syncwarp();
                     }
-                    if (!(ok = mbar_wait_warp(bar(B_EPI_FREE + grp), epi_ph, w))) break;
-                    epi_ph ^= 1;
+                    if (!(ok = mbar_wait_warp(bar(B_EPI_FREE + grp), epi.slice(), w))) break;
+                    epi.next_slice();
                 }
                 if (!ok) break;
-                // the other group's store has read its tile too before the next
-                // unit's dS^T may land in either tile
-                if (!(ok = mbar_wait_warp(bar(B_EPI_FREE + (grp ^ 1)), epi_ph ^ 1u, w))) break;
+                epi.unit_stored();
                 continue;
             }
 #pragma unroll
