@@ -598,7 +598,8 @@ def fa_bwd(q, k, v, o, dout, lse, causal=False, softmax_scale=None, cu_seqlens_q
 
     Outputs are allocated when not given.  ``workspace`` (a uint8 CUDA tensor
     of at least ``workspace_bytes(...)``) selects fa_bwd_with_workspace,
-    otherwise the library's own workspace is used.  The extension keywords
+    otherwise the call takes its scratch from the library's memory pool, so
+    that calls may overlap on different streams.  The extension keywords
     (as for fa_fwd, plus ``dbias``, an output tensor filled with dBias = dS)
     select fa_bwd_ext, and so does ``totals=(total_q, total_k)`` (varlen: the
     packed row counts, which spare the stream synchronisation of reading them

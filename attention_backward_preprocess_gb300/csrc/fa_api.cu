@@ -27,6 +27,7 @@ cudaError_t launch_fwd_tc(const BwdParams &p, const CUtensorMap &q, const CUtens
 int fwd_block_m();
 int fwd_block_n(const BwdParams &p, int sms);
 int *fwd_error_word();
+cudaError_t launch_error_or(const int *from, int *word, cudaStream_t stream);
 cudaError_t launch_bwd_main(const BwdParams &p, const CUtensorMap &q, const CUtensorMap &k,
                             const CUtensorMap &v, const CUtensorMap &dout, const CUtensorMap &dk,
                             const CUtensorMap &dv, int bf16, int grid, cudaStream_t stream);
@@ -192,41 +193,64 @@ bool encode_v_map(CUtensorMap *m, const void *base, int page, long long rows, in
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// ------------------------------------------------- library-owned workspace
-struct DeviceWs {
-    void *ptr = nullptr;
-    size_t bytes = 0;
-};
-std::mutex g_ws_mutex;
-std::vector<DeviceWs> g_ws;
+// ------------------------------------------------- workspace of the library's
+// A call that brings no workspace takes one from a memory pool of the library's,
+// allocated and freed in the order of the call's stream: calls in flight together
+// never share one, and a block is given to another stream only once the work that
+// used it is over (or, captured, belongs to its graph).  The pool keeps what it
+// has, so a steady program allocates nothing from the driver; it makes no stream
+// wait for another one's block.
+std::mutex g_pool_mutex;
+std::vector<cudaMemPool_t> g_pools;   // per device, made by its first call
 
-fa_status library_workspace(size_t need, cudaStream_t stream, void **out) {
+bool library_pool(cudaMemPool_t *out) {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
-    std::lock_guard<std::mutex> lk(g_ws_mutex);
-    if ((int)g_ws.size() <= dev) g_ws.resize(dev + 1);
-    DeviceWs &w = g_ws[dev];
-    if (w.bytes < need) {
-        if (w.ptr) {
-            if (cudaFreeAsync(w.ptr, stream) != cudaSuccess) return FA_ERR_CUDA;
-            w.ptr = nullptr;
-            w.bytes = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    std::lock_guard<std::mutex> lk(g_pool_mutex);
+    if ((int)g_pools.size() <= dev) g_pools.resize(dev + 1, nullptr);
+    if (!g_pools[dev]) {
+        cudaMemPoolProps props;
+        std::memset(&props, 0, sizeof(props));
+        props.allocType = cudaMemAllocationTypePinned;
+        props.location.type = cudaMemLocationTypeDevice;
+        props.location.id = dev;
+        cudaMemPool_t pool = nullptr;
+        if (cudaMemPoolCreate(&pool, &props) != cudaSuccess) return false;
+        uint64_t keep = UINT64_MAX;
+        int off = 0;
+        if (cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep) != cudaSuccess ||
+            cudaMemPoolSetAttribute(pool, cudaMemPoolReuseAllowInternalDependencies, &off) != cudaSuccess) {
+            cudaMemPoolDestroy(pool);
+            return false;
         }
-        size_t grow = round_up(need + need / 8, 1 << 21);
-        if (cudaMallocAsync(&w.ptr, grow, stream) != cudaSuccess) return FA_ERR_CUDA;
-        w.bytes = grow;
+        g_pools[dev] = pool;
     }
-    *out = w.ptr;
-    return FA_OK;
+    *out = g_pools[dev];
+    return true;
 }
 
-void *library_workspace_peek() {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
-    std::lock_guard<std::mutex> lk(g_ws_mutex);
-    if ((int)g_ws.size() <= dev) return nullptr;
-    return g_ws[dev].ptr;
-}
+// The workspace of one call.
+struct CallWorkspace {
+    void *ptr = nullptr;
+    cudaStream_t stream = nullptr;
+
+    fa_status take(size_t bytes, cudaStream_t s) {
+        cudaMemPool_t pool;
+        if (!library_pool(&pool) || cudaMallocFromPoolAsync(&ptr, bytes, pool, s) != cudaSuccess) {
+            ptr = nullptr;
+            cudaGetLastError();   // not left for the next launch's check to find
+            return FA_ERR_CUDA;
+        }
+        stream = s;
+        return FA_OK;
+    }
+    CallWorkspace() = default;
+    CallWorkspace(const CallWorkspace &) = delete;
+    CallWorkspace &operator=(const CallWorkspace &) = delete;
+    ~CallWorkspace() {
+        if (ptr) cudaFreeAsync(ptr, stream);
+    }
+};
 
 // Totals of the packed varlen tensors (cu[B]); read back from the device.
 fa_status varlen_totals(const int *cu_q, const int *cu_k, int B, cudaStream_t stream,
@@ -687,26 +711,38 @@ fa_status fa_bwd_ext(const void *q, const void *k, const void *v, const void *o,
                      cudaStream_t stream) {
     if (!q || !k || !v || !o || !dout || !lse || !dq || !dk || !dv) return FA_ERR_INVALID_ARG;
     fa_status st;
+    CallWorkspace own;
     if (!workspace) {
-        // the library's own workspace, grown on demand
         st = check_shape(B, Sq, Sk, Hq, Hkv, D, dtype, cu_seqlens_q, cu_seqlens_k);
         if (st != FA_OK) return st;
         workspace_bytes = fa_bwd_workspace_bytes(B, Sq, Sk, Hq, Hkv, D,
                                                  cu_seqlens_q != nullptr, deterministic);
         if (workspace_bytes == 0) return FA_ERR_INVALID_ARG;
-        if ((st = library_workspace(workspace_bytes, stream, &workspace)) != FA_OK) return st;
+        if ((st = own.take(workspace_bytes, stream)) != FA_OK) return st;
+        workspace = own.ptr;
     }
     Prepared P;
     st = prepare(q, k, v, o, dout, lse, dq, dk, dv, B, Sq, Sk, Hq, Hkv, D, softmax_scale, causal,
                  cu_seqlens_q, cu_seqlens_k, deterministic, dtype, workspace, workspace_bytes,
                  stream, &P, ext);
     if (st != FA_OK) return st;
+    if (own.ptr && !deterministic) {
+        // errors go where fa_device_status finds them once the workspace is gone
+        P.p.err = fa::fwd_error_word();
+        if (!P.p.err) return FA_ERR_CUDA;
+        P.p.err_shared = 1;
+    }
     if ((st = run_preprocess(P, dtype, stream)) != FA_OK) return st;
     if (P.p.dbias && (st = zero_dbias(P, stream)) != FA_OK) return st;
     if ((st = run_main(P, dtype, stream)) != FA_OK) return st;
     if ((st = run_postprocess(P, dtype, stream)) != FA_OK) return st;
-    if (deterministic) return read_error_word(P.p.err, stream, false);
-    return FA_OK;
+    if (!deterministic) return FA_OK;
+    st = read_error_word(P.p.err, stream, false);
+    if (own.ptr && st != FA_OK && st != FA_ERR_CUDA) {
+        int *word = fa::fwd_error_word();
+        if (!word || fa::launch_error_or(P.p.err, word, stream) != cudaSuccess) return FA_ERR_CUDA;
+    }
+    return st;
 }
 
 fa_status fa_bwd_stages_ext(int stages, const void *q, const void *k, const void *v,
@@ -737,34 +773,14 @@ fa_status fa_bwd(const void *q, const void *k, const void *v, const void *o, con
                  int Hkv, int D, float softmax_scale, int causal, const int *cu_seqlens_q,
                  const int *cu_seqlens_k, int deterministic, fa_dtype dtype,
                  cudaStream_t stream) {
-    fa_status st = check_shape(B, Sq, Sk, Hq, Hkv, D, dtype, cu_seqlens_q, cu_seqlens_k);
-    if (st != FA_OK) return st;
-    const size_t need = fa_bwd_workspace_bytes(B, Sq, Sk, Hq, Hkv, D, cu_seqlens_q != nullptr,
-                                               deterministic);
-    if (need == 0) return FA_ERR_INVALID_ARG;
-    void *ws = nullptr;
-    st = library_workspace(need, stream, &ws);
-    if (st != FA_OK) return st;
-    return fa_bwd_with_workspace(q, k, v, o, dout, lse, dq, dk, dv, B, Sq, Sk, Hq, Hkv, D,
-                                 softmax_scale, causal, cu_seqlens_q, cu_seqlens_k, deterministic,
-                                 dtype, ws, need, stream);
+    return fa_bwd_ext(q, k, v, o, dout, lse, dq, dk, dv, B, Sq, Sk, Hq, Hkv, D, softmax_scale, causal,
+                      cu_seqlens_q, cu_seqlens_k, nullptr, deterministic, dtype, nullptr, 0, stream);
 }
 
 fa_status fa_device_status(void *workspace, cudaStream_t stream) {
-    void *ws = workspace ? workspace : library_workspace_peek();
-    fa_status st = FA_OK;
-    if (!workspace) {
-        // the forward pass records its timeouts in a word of its own
-        int *fwd_err = fa::fwd_error_word();
-        if (!fwd_err) return FA_ERR_CUDA;
-        st = read_error_word(fwd_err, stream, true);
-        if (st == FA_ERR_CUDA) return st;
-    }
-    if (!ws) {
-        return cudaStreamSynchronize(stream) == cudaSuccess ? st : FA_ERR_CUDA;
-    }
-    fa_status st2 = read_error_word(reinterpret_cast<int *>(ws), stream, true);
-    return st2 != FA_OK ? st2 : st;
+    int *word = workspace ? static_cast<int *>(workspace) : fa::fwd_error_word();
+    if (!word) return FA_ERR_CUDA;
+    return read_error_word(word, stream, true);
 }
 
 namespace {

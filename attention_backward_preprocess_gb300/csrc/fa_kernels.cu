@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(256) preprocess_kernel(BwdParams p) {
     static_assert(ZF % 4 == 0, "whole float4 stores");
     const int b = blockIdx.y;
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
-        *p.err = 0;            // per-call error word
+        if (!p.err_shared) *p.err = 0;   // per-call error word
         p.unit_counter[0] = 0;   // the main kernel's dynamic work-unit counter ...
         p.unit_counter[1] = 0;   // ... and its count of CTAs that ran out of units
     }
@@ -320,6 +320,14 @@ __global__ void __launch_bounds__(256) dbias_zero_kernel(BwdParams p) {
 }
 
 }  // namespace
+
+// A call's error bits added to the library's word.
+static __global__ void error_or_kernel(const int *from, int *word) { atomicOr(word, *from); }
+
+cudaError_t launch_error_or(const int *from, int *word, cudaStream_t stream) {
+    error_or_kernel<<<1, 1, 0, stream>>>(from, word);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_dbias_zero(const BwdParams &p, int bm, cudaStream_t stream) {
     const long long blocks = (long long)p.B * p.Hq * ((p.Sk + kBlockN - 1) / kBlockN);

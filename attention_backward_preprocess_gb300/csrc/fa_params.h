@@ -62,6 +62,7 @@ struct BwdParams {
     int drop_mask_w;
     // workspace
     int *err;           // device error word
+    int err_shared;     // != 0: other calls record in it too, so the preprocess leaves it alone
     int4 *tiles;        // work units (b, n_block, hk, 0)
     int *ntiles;        // varlen: number of work units written by the scheduler
     int num_units;      // dense: B * ceil(Sk / 128) * Hkv work units

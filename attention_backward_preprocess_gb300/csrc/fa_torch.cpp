@@ -139,7 +139,7 @@ PyObject *fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// bwd(q, k, v, scale, causal, softcap, ranges, B, S, o, dout, lse) -> (dq, dk, dv), the library's workspace
+// bwd(q, k, v, scale, causal, softcap, ranges, B, S, o, dout, lse) -> (dq, dk, dv), scratch from the library's pool
 PyObject *bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (n != 12) return none();
     return guarded([&]() -> PyObject * {

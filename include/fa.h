@@ -51,10 +51,11 @@
  *
  * Ownership: the caller owns every tensor and the stream.  All tensor
  * pointers are device pointers aligned to 16 bytes.  dq, dk, dv are fully
- * overwritten (key rows no query sees get zeros).  fa_bwd uses a per-device
- * workspace owned by the library (grown on demand); calls that overlap on
- * different streams of one device must use fa_bwd_with_workspace with their
- * own workspaces.
+ * overwritten (key rows no query sees get zeros).  fa_bwd, and fa_bwd_ext
+ * without a workspace, take their scratch from a memory pool the library keeps
+ * per device (cudaMallocFromPoolAsync / cudaFreeAsync on `stream`), a block of
+ * its own for every call: calls may overlap on different streams.  The pool
+ * keeps the memory it has grown to.
  *
  * Errors: arguments are validated before any launch (FA_ERR_INVALID_ARG,
  * FA_ERR_UNSUPPORTED); a failed launch returns FA_ERR_CUDA.  Otherwise the
@@ -322,7 +323,7 @@ fa_status fa_fwd_ext(const void *q, const void *k, const void *v, void *o, float
                      const int *cu_seqlens_q, const int *cu_seqlens_k, const fa_ext *ext,
                      fa_dtype dtype, cudaStream_t stream);
 
-/* fa_bwd with extensions.  workspace NULL: the library's own (as fa_bwd);
+/* fa_bwd with extensions.  workspace NULL: scratch from the library's pool (as fa_bwd);
  * otherwise a caller workspace as for fa_bwd_with_workspace (the extensions
  * do not change its size). */
 fa_status fa_bwd_ext(const void *q, const void *k, const void *v, const void *o,
@@ -401,7 +402,8 @@ fa_status fa_fwd_kvcache(const void *q, const fa_kv_cache *cache, const int *cac
 /* CUDA graphs.  A backward call that issues only launches and memsets on
  * `stream` can be captured into a CUDA graph and replayed: fa_bwd_ext /
  * fa_bwd_with_workspace with a caller workspace for dense problems, and for
- * varlen problems when ext gives the packed totals; fa_bwd_stages_ext (or
+ * varlen problems when ext gives the packed totals (without a workspace the
+ * graph gets an allocation of its own for the scratch); fa_bwd_stages_ext (or
  * the three stage calls, dense) in every mode.  A deterministic fa_bwd /
  * fa_bwd_ext reads its device status back before returning (a host wait) and
  * cannot be captured; capture its stages instead and read the status with
@@ -434,8 +436,10 @@ fa_status fa_bwd_stages_ext(int stages, const void *q, const void *k, const void
                             cudaStream_t stream);
 
 /* Synchronises `stream`, then returns and clears the device error word of
- * this device's library workspace (FA_OK or FA_ERR_TIMEOUT).  For a caller
- * workspace, pass it; NULL means the library's own. */
+ * that workspace (FA_OK, FA_ERR_TIMEOUT or FA_ERR_INVALID_ARG).  NULL: the
+ * library's word for this device, in which the forward, the cache calls and
+ * every backward without a workspace record what went wrong since it was last
+ * read. */
 fa_status fa_device_status(void *workspace, cudaStream_t stream);
 
 /* Upper limit, in nanoseconds, of every device-side wait (default 2e9).
