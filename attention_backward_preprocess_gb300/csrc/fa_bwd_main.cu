@@ -188,8 +188,8 @@ enum {
     B_FREE_A = 48,      // warp A's MMAs of a unit completed (its reads of both slots)
     B_FREE_B = 49,      // warp B's MMAs of a unit completed (its reads of the K slot)
     B_EPI_FULL = 50,    // +g: softmax group g wrote a dK / dV slice into its staging tile
-    B_EPI_FREE = 52,    // +g: the tensor store of group g has read its staging tile
-    B_EPI_DONE = 54     // both groups' last stores of a unit have read their tiles
+    B_EPI_FREE = 52,    // +g: the store of a slice of group g but the last has read its staging tile
+    B_EPI_DONE = 54     // both groups' last stores of a unit have read their tiles (fa_epilogue.h)
 };
 
 struct MainMaps {
@@ -1041,6 +1041,13 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
             // key kj is visible to query qi iff -win_lo <= kj - qi - diag <= win_hi
             const int diag = u.lk - u.lq;
             const int whi = p.win_hi, wlo = p.win_lo;
+            // both groups' dK / dV stores of the last unit have read the dS^T tiles.
+            // Waited for here, not at the first write into a tile, which would let
+            // the unit's first S and P run meanwhile: a second wait inside the step
+            // loop costs registers there (documents of 8k: main kernel 254 us
+            // against 263, capped 2k 221 against 223, B = 1, 16 heads, 32768 keys
+            // in the deterministic order 19.7 ms against 20.4)
+            if (u.iters > 0 && !(ok = mbar_wait(bar(B_EPI_DONE), epi.stored(), w))) break;
             for (int it = 0; it < u.iters; ++it) {
                 const int m = u.m_of(it, p.G);
                 const int m0 = m * BM;
@@ -1323,12 +1330,8 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
                     }
                     if (ch == 0) {
                         // the dS^T tile db may still be read by the dQ MMA of step
-                        // j-2, and in a unit's first step by either group's dK / dV
-                        // store of the unit before (they stage in both tiles): wait
-                        // before the first write into it
-                        if (!(ok = mbar_wait(bar(B_DSB_FREE + db), bit(dsb_ph, db) ^ 1u, w) &&
-                                   (it > 0 || mbar_wait(bar(B_EPI_DONE), epi.stored(), w))))
-                            break;
+                        // j-2: wait before the first write into it
+                        if (!(ok = mbar_wait(bar(B_DSB_FREE + db), bit(dsb_ph, db) ^ 1u, w))) break;
                         dsb_ph ^= 1u << db;
                     }
 #pragma unroll
@@ -1456,9 +1459,8 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
                 // of its [128 keys x D] tile in dS^T tile g (free once the last
                 // dQ^T MMA -- and, D = 128, the issuer -- finished with both
                 // tiles) in the store's 128-byte swizzle; the group's first
-                // lane issues the store and waits until it has read the tile.  (The
-                // other group's tile: B_EPI_DONE, looked at before the next unit's
-                // first dS^T write, so that its S and P run meanwhile.)
+                // lane issues the store and waits until it has read the tile (phases:
+                // fa_epilogue.h).
                 bool free_ok = true;
                 for (int d = 0; d < 2; ++d)
                     free_ok = free_ok && mbar_wait(bar(B_DSB_FREE + d), bit(dsb_ph, d) ^ 1u, w);
@@ -1493,18 +1495,20 @@ __global__ void __launch_bounds__(MainCfg<kD, T>::kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_EPI_FULL + grp));
                     if (quarter == 0) {
-                        if (!(ok = mbar_wait_warp(bar(B_EPI_FULL + grp), epi.slice(), w))) break;
+                        if (!(ok = mbar_wait_warp(bar(B_EPI_FULL + grp), epi.staged(), w))) break;
                         if (lane == 0) {
                             tma_store_4d(omap, tile, 64 * sl, u.hk, u.k_row0 + n0, u.bidx);
                             bulk_commit_group();
                             bulk_wait_read_all();
-                            mbar_arrive(bar(B_EPI_FREE + grp));
-                            if (sl == EpiPhases::slices(D) - 1) mbar_arrive(bar(B_EPI_DONE));
+                            mbar_arrive(bar(sl == EpiPhases::slices(D) - 1 ? B_EPI_DONE : B_EPI_FREE + grp));
                         }
                         __syncwarp();
                     }
-                    if (!(ok = mbar_wait_warp(bar(B_EPI_FREE + grp), epi.slice(), w))) break;
-                    epi.next_slice();
+                    epi.next_staged();
+                    if (sl < EpiPhases::slices(D) - 1) {
+                        if (!(ok = mbar_wait_warp(bar(B_EPI_FREE + grp), epi.freed(), w))) break;
+                        epi.next_freed();
+                    }
                 }
                 if (!ok) break;
                 epi.unit_stored();

@@ -3,15 +3,16 @@
 // can walk every interleaving of the warps through the very code the kernel runs.
 //
 // Softmax group g stages its dK or dV in dS^T tile g, in slices of 64 columns: two
-// at D = 128, one at D = 64.  Per slice the group's warps arrive on B_EPI_FULL + g,
-// its leader stores the tile and arrives on B_EPI_FREE + g once it has been read:
-// slices() phases a unit, waited for by the group itself.  The other group must
-// not count those (with two per unit the parity behind a unit is the same in every
-// unit, so that a wait for it holds back nothing while no slice is out yet): each
-// leader also arrives once a unit, after its last slice, on B_EPI_DONE (count 2),
-// and every softmax warp waits for that before its first dS^T write of the next
-// unit.  A phase of B_EPI_DONE thus cannot complete before every warp has looked
-// at the one before it, and one parity bit each is enough.
+// at D = 128, one at D = 64.  Per slice the group's warps arrive on B_EPI_FULL + g
+// and its leader stores the tile.  Once the store has read it, the leader arrives
+// on B_EPI_FREE + g, for which the group waits before it stages its next slice,
+// or after the last slice on B_EPI_DONE (both leaders: count 2), for which every
+// softmax warp waits before it begins its next unit with work.  No phase of
+// any of them can thus complete before every waiter has looked at the one before
+// it, and one parity bit each is enough.  (A group must not look at the other's
+// slice barriers: with two phases a unit the parity behind a unit is the same in
+// every unit, and a wait for it lets through exactly the group whose other one has
+// no slice out yet.)
 #pragma once
 
 #include <cstdint>
@@ -25,13 +26,18 @@
 namespace fa {
 
 struct EpiPhases {
-    uint32_t bits = 0;   // bit 0: slices of the own group, bit 1: units with stores (both mod 2)
+    // counts mod 2 -- bit 0: slices of the own group staged, bit 1: units with
+    // stores, bit 2: slices of the own group but a unit's last
+    uint32_t bits = 0;
     static constexpr int slices(int D) { return D / 64; }
-    // parity of B_EPI_FULL / B_EPI_FREE (own group) to wait for in the present slice
-    FA_EPI_FN uint32_t slice() const { return bits & 1u; }
-    FA_EPI_FN void next_slice() { bits ^= 1u; }
-    // parity of B_EPI_DONE to wait for before a unit's first dS^T write: the stores
-    // of the last unit that had any (before the first one the wait passes)
+    // parity of the own group's B_EPI_FULL to wait for in the present slice
+    FA_EPI_FN uint32_t staged() const { return bits & 1u; }
+    FA_EPI_FN void next_staged() { bits ^= 1u; }
+    // parity of the own group's B_EPI_FREE to wait for behind a slice but the last
+    FA_EPI_FN uint32_t freed() const { return bits >> 2 & 1u; }
+    FA_EPI_FN void next_freed() { bits ^= 4u; }
+    // parity of B_EPI_DONE to wait for before a unit with work: the stores of the
+    // last unit that had any (before the first one the wait passes)
     FA_EPI_FN uint32_t stored() const { return (bits >> 1 & 1u) ^ 1u; }
     FA_EPI_FN void unit_stored() { bits ^= 2u; }
 };

@@ -47,7 +47,7 @@ bool step(State &s, int g, int v, std::string *fault) {
     epi.bits = w.bits;
     auto next_unit = [&] { w.unit++, w.slice = 0, w.pc = 0; };
     switch (w.pc) {
-    case 0:   // before the unit's first dS^T write
+    case 0:   // before the unit
         if (protocol == 0 && !s.done.passed(epi.stored())) return false;
         w.pc = 1;
         break;
@@ -77,20 +77,25 @@ bool step(State &s, int g, int v, std::string *fault) {
         w.pc = v == 0 ? 4 : 6;
         break;
     case 4:   // the leader issues the store
-        if (!s.full[g].passed(epi.slice())) return false;
+        if (!s.full[g].passed(epi.staged())) return false;
         s.staged[g] = 2;
         w.pc = 5;
         break;
     case 5:   // the store has read the tile
         s.staged[g] = 0;
         if (w.slice == slices - 1) s.out[g]++;
-        s.free_[g].arrive();
         if (w.slice == slices - 1) s.done.arrive();
+        if (w.slice < slices - 1 || protocol == 1) s.free_[g].arrive();
         w.pc = 6;
         break;
     case 6:
-        if (!s.free_[g].passed(epi.slice())) return false;
-        epi.next_slice();
+        if (protocol == 1) {   // its slice barrier has a phase for every slice
+            if (!s.free_[g].passed(epi.staged())) return false;
+        } else if (w.slice < slices - 1) {
+            if (!s.free_[g].passed(epi.freed())) return false;
+            epi.next_freed();
+        }
+        epi.next_staged();
         if (++w.slice < slices) {
             w.pc = 3;
             break;
@@ -100,7 +105,7 @@ bool step(State &s, int g, int v, std::string *fault) {
         else next_unit();
         break;
     case 7:
-        if (!s.free_[g ^ 1].passed(epi.slice() ^ 1u)) return false;
+        if (!s.free_[g ^ 1].passed(epi.staged() ^ 1u)) return false;
         next_unit();
         break;
     }
