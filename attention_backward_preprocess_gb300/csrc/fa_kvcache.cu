@@ -5,7 +5,8 @@
 // the smallest e for which the page's largest magnitude fits 448 * 2^e.  A
 // power of two costs no precision (e4m3 is a floating type) and makes the
 // division by the scale, and moving a page to a larger scale, exact but for
-// values that become subnormal.
+// values that become subnormal.  A page filled elsewhere may keep another scale;
+// its values are rounded once all the same (div_to_odd).
 //
 // K lies token by token, V dim by dim, so that in both products the 16-byte
 // pieces a lane reads are contiguous along the axis the tensor core contracts.
@@ -52,6 +53,23 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
+// x / s and x r in 32 bits, rounded to odd: cut off, and the last bit set if
+// anything was.  Rounding that to e4m3's four bits to nearest even then gives what
+// rounding the exact value would, as a nearest 32-bit value need not (it may land on
+// a tie).  Results whose cut-off part is itself below 32 bits' range are far below
+// half of e4m3's smallest value.
+__device__ __forceinline__ float to_odd(float q, float rest) {
+    return rest < 0.f || rest > 0.f ? __uint_as_float(__float_as_uint(q) | 1u) : q;   // (NaN: as it is)
+}
+__device__ __forceinline__ float div_to_odd(float x, float s) {
+    const float q = __fdiv_rz(x, s);
+    return to_odd(q, fmaf(-q, s, x));
+}
+__device__ __forceinline__ float mul_to_odd(float x, float r) {
+    const float q = __fmul_rz(x, r);
+    return to_odd(q, fmaf(x, r, -q));
+}
+
 // 16 stored bytes moved to another scale, those from byte `n` on left alone
 __device__ __forceinline__ void requantise(uint32_t (&w)[4], float ratio, int n) {
 #pragma unroll
@@ -59,7 +77,8 @@ __device__ __forceinline__ void requantise(uint32_t (&w)[4], float ratio, int n)
         uint32_t a, b;
         e4m3x4_to_f16(w[i], a, b);
         const float2 x = Cvt<__half>::unpack(a), y = Cvt<__half>::unpack(b);
-        const uint32_t r = f32_to_e4m3x2(x.x * ratio, x.y * ratio) | f32_to_e4m3x2(y.x * ratio, y.y * ratio) << 16;
+        const uint32_t r = f32_to_e4m3x2(mul_to_odd(x.x, ratio), mul_to_odd(x.y, ratio)) |
+                           f32_to_e4m3x2(mul_to_odd(y.x, ratio), mul_to_odd(y.y, ratio)) << 16;
         const int k = min(max(n - 4 * i, 0), 4);
         const uint32_t keep = k >= 4 ? 0u : 0xffffffffu << (8 * k);
         w[i] = (w[i] & keep) | (r & ~keep);
@@ -143,85 +162,93 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     for (int i = 0; i < kThreads / 32; ++i) top = max(top, s_max[i]);
     const float amax = Cvt<T>::unpack(top).x;
     const float now = fmaxf(old, pow2(scale_exponent(amax)));
-    const float ratio = old / now, inv = 1.f / now;   // powers of two: exact
+    // exact: ratio, for now is old or a power of two; inv, where now is a power of two
+    const float ratio = old / now, inv = 1.f / now;
     if (tid == 0) *scale = now;
     const bool move = held > 0 && ratio != 1.f;
     const T *xs = reinterpret_cast<const T *>(smem_raw);
-    if (!is_v) {
-        if (move) {
-            for (int i = tid; i < held * (D / 16); i += kThreads) {
-                uint4 *at = reinterpret_cast<uint4 *>(base) + i;
-                const uint4 v = *at;
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                requantise(w, ratio, 16);
-                *at = make_uint4(w[0], w[1], w[2], w[3]);
+    // (a scale that is no power of two takes a copy of the rest that divides)
+    auto store = [&](auto exact_tag) __attribute__((always_inline)) {
+        constexpr bool kExact = decltype(exact_tag)::value;
+        auto scaled = [&](float x) __attribute__((always_inline)) -> float { return kExact ? x * inv : div_to_odd(x, now); };
+        if (!is_v) {
+            if (move) {
+                for (int i = tid; i < held * (D / 16); i += kThreads) {
+                    uint4 *at = reinterpret_cast<uint4 *>(base) + i;
+                    const uint4 v = *at;
+                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    requantise(w, ratio, 16);
+                    *at = make_uint4(w[0], w[1], w[2], w[3]);
+                }
             }
+            for (int i = tid; i < T_new * (D / 16); i += kThreads) {
+                const uint32_t *x = reinterpret_cast<const uint32_t *>(xs) + 8 * i;
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 a = Cvt<T>::unpack(x[2 * k]), c = Cvt<T>::unpack(x[2 * k + 1]);
+                    w[k] = f32_to_e4m3x2(scaled(a.x), scaled(a.y)) | f32_to_e4m3x2(scaled(c.x), scaled(c.y)) << 16;
+                }
+                reinterpret_cast<uint4 *>(base + (long long)held * D)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            return;
         }
-        for (int i = tid; i < T_new * (D / 16); i += kThreads) {
-            const uint32_t *x = reinterpret_cast<const uint32_t *>(xs) + 8 * i;
-            uint32_t w[4];
+        // V: pieces of 16 tokens of one dim; lanes go along the dims, so the reads of
+        // shared memory are rows.  Pieces all of whose tokens are new take two dims a
+        // thread and no test per byte; a piece with bytes of before, or past the last
+        // token, is read first.
+        const int g0 = move ? 0 : held / 16;
+        int g1 = (held + T_new + 15) / 16;
+        const int ga = (held + 15) / 16, gw = max((held + T_new) / 16 - ga, 0);   // pieces [ga, ga + gw) are whole
+#pragma unroll 1
+        for (int i = tid; i < gw * (D / 2); i += kThreads) {
+            const int g = ga + i / (D / 2), d = 2 * (i % (D / 2));
+            const T *x = xs + (16 * g - held) * D + d;
+            uint32_t w0[4], w1[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float2 a = Cvt<T>::unpack(x[2 * k]), c = Cvt<T>::unpack(x[2 * k + 1]);
-                w[k] = f32_to_e4m3x2(a.x * inv, a.y * inv) | f32_to_e4m3x2(c.x * inv, c.y * inv) << 16;
+                float2 f[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = Cvt<T>::unpack(*reinterpret_cast<const uint32_t *>(x + (4 * k + j) * D));
+                w0[k] = f32_to_e4m3x2(scaled(f[0].x), scaled(f[1].x)) | f32_to_e4m3x2(scaled(f[2].x), scaled(f[3].x)) << 16;
+                w1[k] = f32_to_e4m3x2(scaled(f[0].y), scaled(f[1].y)) | f32_to_e4m3x2(scaled(f[2].y), scaled(f[3].y)) << 16;
             }
-            reinterpret_cast<uint4 *>(base + (long long)held * D)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            uint4 *at = reinterpret_cast<uint4 *>(base + (long long)d * ps + 16 * g);
+            *at = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+            at[ps / 16] = make_uint4(w1[0], w1[1], w1[2], w1[3]);
         }
-        return;
-    }
-    // V: pieces of 16 tokens of one dim; lanes go along the dims, so the reads of
-    // shared memory are rows.  Pieces all of whose tokens are new take two dims a
-    // thread and no test per byte; a piece with bytes of before, or past the last
-    // token, is read first.
-    const int g0 = move ? 0 : held / 16;
-    int g1 = (held + T_new + 15) / 16;
-    const int ga = (held + 15) / 16, gw = max((held + T_new) / 16 - ga, 0);   // pieces [ga, ga + gw) are whole
+        g1 -= gw;
 #pragma unroll 1
-    for (int i = tid; i < gw * (D / 2); i += kThreads) {
-        const int g = ga + i / (D / 2), d = 2 * (i % (D / 2));
-        const T *x = xs + (16 * g - held) * D + d;
-        uint32_t w0[4], w1[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float2 f[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = Cvt<T>::unpack(*reinterpret_cast<const uint32_t *>(x + (4 * k + j) * D));
-            w0[k] = f32_to_e4m3x2(f[0].x * inv, f[1].x * inv) | f32_to_e4m3x2(f[2].x * inv, f[3].x * inv) << 16;
-            w1[k] = f32_to_e4m3x2(f[0].y * inv, f[1].y * inv) | f32_to_e4m3x2(f[2].y * inv, f[3].y * inv) << 16;
-        }
-        uint4 *at = reinterpret_cast<uint4 *>(base + (long long)d * ps + 16 * g);
-        *at = make_uint4(w0[0], w0[1], w0[2], w0[3]);
-        at[ps / 16] = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-    }
-    g1 -= gw;
-#pragma unroll 1
-    for (int i = tid; i < (g1 - g0) * D; i += kThreads) {
-        int g = g0 + i / D;
-        if (gw > 0 && g >= ga) g += gw;   // over the whole ones
-        const int d = i % D, t0 = 16 * g - held;   // t0: new token of the piece's first byte
-        uint4 *at = reinterpret_cast<uint4 *>(base + (long long)d * ps + 16 * g);
-        uint32_t w[4] = {0u, 0u, 0u, 0u};
-        if (t0 < 0 || t0 + 16 > T_new) {
-            const uint4 v = *at;
-            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-            if (move && t0 < 0) requantise(w, ratio, -t0);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float f[4];
-            uint32_t put = 0u;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = t0 + 4 * k + j;
-                const bool in = t >= 0 && t < T_new;
-                f[j] = in ? static_cast<float>(xs[t * D + d]) * inv : 0.f;
-                put |= in ? 0xffu << (8 * j) : 0u;
+        for (int i = tid; i < (g1 - g0) * D; i += kThreads) {
+            int g = g0 + i / D;
+            if (gw > 0 && g >= ga) g += gw;   // over the whole ones
+            const int d = i % D, t0 = 16 * g - held;   // t0: new token of the piece's first byte
+            uint4 *at = reinterpret_cast<uint4 *>(base + (long long)d * ps + 16 * g);
+            uint32_t w[4] = {0u, 0u, 0u, 0u};
+            if (t0 < 0 || t0 + 16 > T_new) {
+                const uint4 v = *at;
+                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+                if (move && t0 < 0) requantise(w, ratio, -t0);
             }
-            const uint32_t r = f32_to_e4m3x2(f[0], f[1]) | f32_to_e4m3x2(f[2], f[3]) << 16;
-            w[k] = (w[k] & ~put) | (r & put);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float f[4];
+                uint32_t put = 0u;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int t = t0 + 4 * k + j;
+                    const bool in = t >= 0 && t < T_new;
+                    f[j] = in ? scaled(static_cast<float>(xs[t * D + d])) : 0.f;
+                    put |= in ? 0xffu << (8 * j) : 0u;
+                }
+                const uint32_t r = f32_to_e4m3x2(f[0], f[1]) | f32_to_e4m3x2(f[2], f[3]) << 16;
+                w[k] = (w[k] & ~put) | (r & put);
+            }
+            *at = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        *at = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    };
+    if ((__float_as_uint(now) & 0x7fffffu) == 0u) store(std::true_type{});
+    else store(std::false_type{});
 }
 
 // --------------------------------------------------------------- attention

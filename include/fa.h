@@ -354,8 +354,9 @@ fa_status fa_bwd_ext(const void *q, const void *k, const void *v, const void *o,
  * (b + 1) * max_new (rows = B * max_new).  Per (page, head) the scale becomes 2^e, the smallest e
  * in [-120, 120] with max |new value| <= 448 * 2^e, or stays the larger one a
  * page that already held tokens of the sequence has; if it grows, those are
- * moved to it (rounded again to nearest even).  What a page held before its
- * first token is ignored.  NaN is stored as NaN, an infinity as +-448 scale.
+ * moved to it (rounded again to nearest even).  A value x is stored as x /
+ * scale, rounded once to nearest even whatever the scale.  What a page held
+ * before its first token is ignored.  NaN is stored as NaN, an infinity as +-448 scale.
  * A page written by the call must belong to one sequence.
  *
  * fa_fwd_kvcache: attention of the last Sq tokens of each sequence (their own
