@@ -414,8 +414,9 @@ fa_status apply_ext(fa::BwdParams &p, int causal, const fa_ext *ext) {
             if (p.varlen) return FA_ERR_UNSUPPORTED;
             if (p.Sq != p.Sk || causal || wl != -1 || wr != -1) return FA_ERR_INVALID_ARG;
             if (reinterpret_cast<uintptr_t>(ext->mask_ranges) & 255u) return FA_ERR_INVALID_ARG;
+            const size_t need = fa_mask_ranges_bytes(p.B, p.Sq);
+            if (need == 0 || ext->mask_ranges_bytes < need) return FA_ERR_INVALID_ARG;
             const fa::RangeTables t = fa::range_tables(const_cast<void *>(ext->mask_ranges), p.B, p.Sq);
-            if (ext->mask_ranges_bytes < t.bytes) return FA_ERR_INVALID_ARG;
             p.mr_row = t.row;
             p.mr_block = t.block;
             p.mr_key = t.key;
@@ -900,7 +901,7 @@ fa_status fa_fwd_kvcache(const void *q, const fa_kv_cache *cache, const int *cac
 }
 
 size_t fa_mask_ranges_bytes(int B, int S) {
-    if (B <= 0 || S <= 0 || (long long)B * S > (1LL << 31) - 1) return 0;
+    if (B <= 0 || S <= 0 || S > fa::kMaxRangeSeq || (long long)B * S > (1LL << 31) - 1) return 0;
     return fa::range_tables(nullptr, B, S).bytes;
 }
 

@@ -26,6 +26,7 @@ constexpr int kThreads = 256;
 constexpr int kPer = 4;                       // rows per thread
 constexpr int kTile = kThreads * kPer;        // rows per CTA
 constexpr int kReach = 16;                    // ids per thread and search step
+static_assert(kTile <= 4096 && kThreads * kReach <= 4096, "kMaxRangeSeq leaves two such steps");
 
 struct MaskArgs {
     const int *doc;        // [B, S], null: one document per sequence

@@ -11,6 +11,10 @@
 
 namespace fa {
 
+// Longest sequence: its rows rounded up to a CTA's, and the search for a document's
+// end one step past them (4096 ids), are counted in 32 bits.
+constexpr int kMaxRangeSeq = 0x7fffffff - 2 * 4096;
+
 // Per sequence, rows = S rounded up to 128 (rows past S see nothing):
 struct RangeTables {
     int rows;

@@ -305,7 +305,8 @@ typedef struct {
  *         sees its first n tokens.  n = prefix_len[b], or with
  *         prefix_per_token != 0 prefix_len[b * S + s], the entry of the
  *         document's first token in a [B, S] array.
- * ranges: device buffer of fa_mask_ranges_bytes(B, S) bytes (0: bad sizes),
+ * ranges: device buffer of fa_mask_ranges_bytes(B, S) bytes (0: bad sizes --
+ *   none, B times S above 2^31 - 1, or S above 2^31 - 1 - 8192),
  *   256-byte aligned, fully overwritten.  Launches on `stream` and no other
  *   call; can be captured into a CUDA graph.  Errors: FA_ERR_INVALID_ARG for
  *   sizes, alignment, a window below -1, or a prefix without causal or with a
