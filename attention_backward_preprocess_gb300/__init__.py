@@ -491,6 +491,38 @@ def _shape(q, k, cu_q, max_seqlen_q, max_seqlen_k):
     return cu_q.numel() - 1, int(max_seqlen_q), int(max_seqlen_k), q.shape[1], k.shape[1], q.shape[2]
 
 
+def _agree(q, k, v, cu_q=None, cu_k=None, o=None, dout=None, lse=None, dq=None, dk=None, dv=None, Dv=None):
+    """The tensors of a call have the shapes, types and GPU that q and k say: the
+    kernels take sizes from those two and read and write as far as they go."""
+    if (Dv is None or v.shape[-1] == Dv) and _binding().agree(q, k, v, o, dout, dq, dk, dv, lse, cu_q, cu_k):
+        return
+    at = q.get_device()   # below: the same, with its messages
+    rows, kv = q.shape[:-1], k.shape[:-1]
+    ok_k = k.dim() == q.dim() and k.shape[-1] == q.shape[-1] and (q.dim() == 3 or k.shape[0] == q.shape[0])
+    out = rows + v.shape[-1:]
+    if Dv is not None and v.shape[-1] != Dv:
+        raise ValueError("v: this call takes no head dim of its own for the values")
+    for name, t, shape in (("k", k, k.shape if ok_k else None), ("v", v, kv + v.shape[-1:]), ("o", o, out),
+                           ("dout", dout, out), ("dq", dq, q.shape), ("dk", dk, k.shape), ("dv", dv, v.shape)):
+        if t is not None and (t.shape != shape or t.dtype != q.dtype or t.get_device() != at):
+            raise ValueError("%s: %s of q's type on q's GPU, got %r" % (
+                name, "q's batch and head dim" if shape is None else list(shape), tuple(t.shape)))
+    if lse is not None:
+        # (varlen: its rows are cu_seqlens_q[B], which only the device knows)
+        n, most = lse.numel(), rows.numel()
+        if (n != most and (q.dim() == 4 or n > most or n % rows[1])) or lse.dtype != torch.float32 \
+                or lse.get_device() != at:
+            raise ValueError("lse: fp32 [B, Hq, Sq] or [Hq, total_q] on q's GPU")
+    if (cu_q is None) != (cu_k is None):
+        raise ValueError("cu_seqlens_q and cu_seqlens_k: both or neither")
+    for name, t in (("cu_seqlens_q", cu_q), ("cu_seqlens_k", cu_k)):
+        if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.shape != cu_q.shape or not t.is_contiguous()
+                              or t.get_device() != at):
+            raise ValueError(name + ": contiguous int32 [B + 1] on q's GPU")
+    if at < 0:
+        raise ValueError("q: not on a GPU")
+
+
 def _value_dim(D, v) -> int:
     """head_dim_v of fa_ext: v's last axis when it differs from the query /
     key head dim, else 0."""
@@ -541,7 +573,7 @@ def _like(t):
 def _outputs(**tensors):
     for name, t in tensors.items():
         if t is not None and not t.is_contiguous():
-            raise ValueError(name + ": a contiguous output tensor")
+            raise ValueError(name + ": must be contiguous")
 
 
 def default_scale(D: int) -> float:
@@ -568,8 +600,9 @@ def fa_fwd(q, k, v, causal=False, softmax_scale=None, cu_seqlens_q=None, cu_seql
         r = _binding().fwd(q, k, v, softmax_scale, causal, softcap, *_ranges(mask_ranges))
         if r is not None:
             return _done(r, "fa_fwd_ext")
-    (q, k, v), strides = _inputs(stream, q=q, k=k, v=v)
     B, Sq, Sk, Hq, Hkv, D = _shape(q, k, cu_seqlens_q, max_seqlen_q, max_seqlen_k)
+    _agree(q, k, v, cu_seqlens_q, cu_seqlens_k)
+    (q, k, v), strides = _inputs(stream, q=q, k=k, v=v)
     scale = default_scale(D) if softmax_scale is None else float(softmax_scale)
     with _on(_gpu(q)), _memory(stream):
         o = torch.empty(q.shape[:-1] + (v.shape[-1],), dtype=q.dtype, device=q.device)
@@ -611,10 +644,11 @@ def fa_bwd(q, k, v, o, dout, lse, causal=False, softmax_scale=None, cu_seqlens_q
         r = _binding().bwd(q, k, v, softmax_scale, causal, softcap, *_ranges(mask_ranges), o, dout, lse)
         if r is not None:
             return _done(r, "fa_bwd_ext")
+    B, Sq, Sk, Hq, Hkv, D = _shape(q, k, cu_seqlens_q, max_seqlen_q, max_seqlen_k)
+    _agree(q, k, v, cu_seqlens_q, cu_seqlens_k, o, dout, lse, dq, dk, dv)
     (q, k, v, o, dout), strides = _inputs(stream, q=q, k=k, v=v, o=o, dout=dout)
     (lse,) = _dense(stream, lse=lse)
     _outputs(dq=dq, dk=dk, dv=dv)
-    B, Sq, Sk, Hq, Hkv, D = _shape(q, k, cu_seqlens_q, max_seqlen_q, max_seqlen_k)
     scale = default_scale(D) if softmax_scale is None else float(softmax_scale)
     with _on(_gpu(q)), _memory(stream):
         dq, dk, dv = (_like(t) if g is None else g for t, g in ((q, dq), (k, dk), (v, dv)))
@@ -650,6 +684,8 @@ def fa_bwd_noalloc(q, k, v, o, dout, lse, dq, dk, dv, causal=False, softmax_scal
     library; see include/fa.h).  The outputs must be given.  Returns the
     status (FA_OK, or FA_ERR_SCRATCH_LIMIT for a problem too large)."""
     B, Sq, Sk, Hq, Hkv, D = _shape(q, k, cu_seqlens_q, max_seqlen_q, max_seqlen_k)
+    _agree(q, k, v, cu_seqlens_q, cu_seqlens_k, o, dout, lse, dq, dk, dv, D)
+    _outputs(q=q, k=k, v=v, o=o, dout=dout, lse=lse, dq=dq, dk=dk, dv=dv)
     scale = default_scale(D) if softmax_scale is None else float(softmax_scale)
     return int(lib().fa_bwd_noalloc(
         _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
@@ -698,8 +734,9 @@ def fa_bwd_stages(q, k, v, o, dout, lse, workspace, causal=False, softmax_scale=
     the packed row counts, so that no stage synchronises the stream; so do
     ``window``, ``softcap`` and ``mask_ranges`` (as for fa_bwd).  Stages in
     separate calls share no copies, so every tensor must be contiguous."""
-    _outputs(q=q, k=k, v=v, o=o, dout=dout, lse=lse, dq=dq, dk=dk, dv=dv)
     B, Sq, Sk, Hq, Hkv, D = _shape(q, k, cu_seqlens_q, max_seqlen_q, max_seqlen_k)
+    _agree(q, k, v, cu_seqlens_q, cu_seqlens_k, o, dout, lse, dq, dk, dv, D)
+    _outputs(q=q, k=k, v=v, o=o, dout=dout, lse=lse, dq=dq, dk=dk, dv=dv)
     scale = default_scale(D) if softmax_scale is None else float(softmax_scale)
     dq, dk, dv = (_like(t) if g is None else g for t, g in ((q, dq), (k, dk), (v, dv)))
     shape = [B, Sq, Sk, Hq, Hkv, D]

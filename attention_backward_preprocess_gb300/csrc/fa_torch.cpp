@@ -124,6 +124,45 @@ PyObject *guarded(F &&f) {
     return nullptr;
 }
 
+// agree(q, k, v, o, dout, dq, dk, dv, lse, cu_q, cu_k) -> True if the tensors of a
+// call (None: not of it) have the shapes, types and GPU that q and k say
+PyObject *agree(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (n != 11) return none();
+    return guarded([&]() -> PyObject * {
+        const at::Tensor *t[11];
+        for (int i = 0; i < 11; ++i) {
+            t[i] = a[i] == Py_None ? nullptr : tensor(a[i]);
+            if (!t[i] && a[i] != Py_None) return none();
+        }
+        if (!t[0] || !t[1] || !t[2]) return none();
+        const at::Tensor &q = *t[0], &k = *t[1], &v = *t[2];
+        const int64_t d = q.dim();
+        if ((d != 3 && d != 4) || k.dim() != d || v.dim() != d || !q.is_cuda() || k.size(d - 1) != q.size(d - 1) ||
+            (d == 4 && k.size(0) != q.size(0)))
+            return none();
+        const at::IntArrayRef qs = q.sizes(), ks = k.sizes();
+        auto like = [&](const at::Tensor &x, at::IntArrayRef rows, int64_t last) {
+            return x.is_cuda() && x.get_device() == q.get_device() && x.scalar_type() == q.scalar_type() &&
+                   x.dim() == d && x.size(d - 1) == last && x.sizes().slice(0, d - 1) == rows.slice(0, d - 1);
+        };
+        const int64_t D = q.size(d - 1), Dv = v.size(d - 1);
+        const at::IntArrayRef rows[8] = {qs, ks, ks, qs, qs, qs, ks, ks};
+        const int64_t last[8] = {D, D, Dv, Dv, Dv, D, D, Dv};
+        for (int i = 1; i < 8; ++i)
+            if (t[i] && !like(*t[i], rows[i], last[i])) return none();
+        if (const at::Tensor *l = t[8])
+            if (!l->is_cuda() || l->get_device() != q.get_device() || l->scalar_type() != at::kFloat ||
+                l->numel() * D != q.numel())
+                return none();
+        if (!t[9] != !t[10]) return none();
+        for (int i = 9; i < 11; ++i)
+            if (t[i] && (!plain(*t[i], at::kInt, (int)q.get_device()) || t[i]->dim() != 1 ||
+                         t[i]->sizes() != t[9]->sizes()))
+                return none();
+        Py_RETURN_TRUE;
+    });
+}
+
 // fwd(q, k, v, scale, causal, softcap, ranges, B, S) -> (o, lse)
 PyObject *fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (n != 9) return none();
@@ -283,7 +322,7 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
 }
 
 #define FN(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FN(fwd), FN(bwd), FN(mask_ranges), FN(cache), FN(append), FN(attend), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {FN(agree), FN(fwd), FN(bwd), FN(mask_ranges), FN(cache), FN(append), FN(attend), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fa_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
