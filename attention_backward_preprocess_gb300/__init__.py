@@ -157,7 +157,10 @@ class KvCache:
     float8_e4m3fn [pages, Hkv, page, D], ``v`` float8_e4m3fn [pages, Hkv, D,
     page], ``k_scale`` / ``v_scale`` float32 [pages, Hkv], ``block_table``
     int32 [B, max_pages]; see fa_kv_cache in include/fa.h.  Keeps the tensors,
-    copies nothing."""
+    copies nothing.  Their contents may change; other tensors (a wider block
+    table) make another KvCache."""
+    # read only: the library holds the addresses of these very tensors
+    k, v, k_scale, v_scale, block_table = (property(lambda self, i=i: self._tensors[i]) for i in range(5))
 
     def __init__(self, k, v, k_scale, v_scale, block_table):
         if k.dim() != 4 or block_table.dim() != 2:
@@ -172,7 +175,7 @@ class KvCache:
                                        ("v_scale", v_scale, torch.float32, (P, H)),
                                        ("block_table", block_table, torch.int32, block_table.shape)):
                 self._check(name, t, dt, shape)
-        self.k, self.v, self.k_scale, self.v_scale, self.block_table = k, v, k_scale, v_scale, block_table
+        self._tensors = k, v, k_scale, v_scale, block_table
         self._c = _KvCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                  block_table.data_ptr(), P, ps, block_table.shape[1], H, D)
         self._at = ctypes.addressof(self._c)
