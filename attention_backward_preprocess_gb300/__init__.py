@@ -30,7 +30,7 @@ EXPORTED = [
     "fa_device_status", "fa_set_wait_timeout_ns", "fa_status_string",
     "fa_selftest_umma", "fa_selftest_semaphore", "fa_selftest_tmem_layout", "fa_bwd_noalloc",
     "fa_bwd_noalloc_scratch_bytes", "fa_fwd_ext", "fa_bwd_ext", "fa_bwd_stages_ext", "fa_bwd_workspace_sync_layout",
-    "fa_bwd_noalloc_status", "fa_mask_ranges", "fa_mask_ranges_bytes",
+    "fa_bwd_noalloc_status", "fa_mask_ranges", "fa_mask_ranges_bytes", "fa_ext_bytes",
     "fa_kvcache_append", "fa_fwd_kvcache", "fa_fwd_kvcache_workspace_bytes",
 ]
 
@@ -375,6 +375,13 @@ def lib():
                 "libfa_gb300.so is not built (run attention_backward_preprocess_gb300.build."
                 "build()); there is no fallback path")
         L = ctypes.CDLL(LIB_PATH)
+        # (a library built before its header changed would read another struct)
+        size = getattr(L, "fa_ext_bytes", None)
+        if size is not None:
+            size.restype = _sz
+        if size is None or size() != ctypes.sizeof(FaExt):
+            raise RuntimeError("libfa_gb300.so was built from another include/fa.h (run "
+                               "attention_backward_preprocess_gb300.build.build()); there is no fallback path")
         L.fa_bwd.argtypes = [_vp] * 9 + _SHAPE + [_f, _i, _vp, _vp, _i, _i, _vp]
         L.fa_bwd_workspace_bytes.argtypes = _SHAPE + [_i, _i]
         L.fa_bwd_workspace_bytes.restype = _sz

@@ -900,6 +900,8 @@ fa_status fa_fwd_kvcache(const void *q, const fa_kv_cache *cache, const int *cac
     return cuda_status(fa::launch_kv_attn(p, mv, cache->D, dtype == FA_BF16, sm_count(), stream));
 }
 
+size_t fa_ext_bytes(void) { return sizeof(fa_ext); }
+
 size_t fa_mask_ranges_bytes(int B, int S) {
     if (B <= 0 || S <= 0 || S > fa::kMaxRangeSeq || (long long)B * S > (1LL << 31) - 1) return 0;
     return fa::range_tables(nullptr, B, S).bytes;

@@ -263,7 +263,11 @@ fa_status fa_fwd(const void *q, const void *k, const void *v, void *o, float *ls
  *   head dim itself is contiguous.  Packed varlen tensors have no batch
  *   stride (the first is not looked at).  o_stride: fa_bwd_ext only.  Outputs
  *   and lse are contiguous. */
-/* Zero the struct (window sides: -1) before setting what a call uses. */
+/* Zero the struct (window sides: -1) before setting what a call uses.  It has
+ * grown at its end and carries no size: the library reads all of it, so a program
+ * must be compiled with the header of the library it loads.  A program that may
+ * meet another one compares fa_ext_bytes() with its sizeof(fa_ext) first and passes
+ * no fa_ext where they differ. */
 typedef struct {
     int window_left;
     int window_right;
@@ -288,6 +292,9 @@ typedef struct {
     size_t mask_ranges_bytes;
     long long q_stride[3], k_stride[3], v_stride[3], o_stride[3], dout_stride[3];
 } fa_ext;
+
+/* sizeof(fa_ext) of the header the library was built with. */
+size_t fa_ext_bytes(void);
 
 /* Visible keys of self-attention problems (Sq = Sk = S, dense) with documents
  * and prefixes, as one interval per query row, for fa_ext.mask_ranges.  Built
