@@ -275,14 +275,18 @@ __global__ void __launch_bounds__(DuoCfg<kD, T>::kThreads, 2)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(U_S_FREE));
                 // hidden keys at -inf: one bit test and one select per score
+                uint32_t in[BN / 32];   // kMask: bit i of word c: key 32 c + i is visible
+                bool none = false;      // kMask: no key of the block is
                 if (kMask) {
 #pragma unroll
                     for (int c = 0; c < BN / 32; ++c) {
                         const uint32_t below = (uint32_t)((1ull << min(max(lo - 32 * c, 0), 32)) - 1ull);
-                        const uint32_t in = (uint32_t)((1ull << min(max(hi + 1 - 32 * c, 0), 32)) - 1ull) & ~below;
+                        in[c] = (uint32_t)((1ull << min(max(hi + 1 - 32 * c, 0), 32)) - 1ull) & ~below;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) sr[c][i] = (in >> i & 1u) ? sr[c][i] : 0xff800000u;
+                        for (int i = 0; i < 32; ++i) sr[c][i] = (in[c] >> i & 1u) ? sr[c][i] : 0xff800000u;
                     }
+                    none = (in[0] | in[BN / 32 - 1]) == 0u;
+                    static_assert(BN == 64, "two words");
                 }
                 // pass 1: maximum of the raw scores, scaled (or capped: tanh
                 // rises) once, in eight independent chains
@@ -299,7 +303,7 @@ __global__ void __launch_bounds__(DuoCfg<kD, T>::kThreads, 2)
                 } else if (kCap) {
                     float r0, r1;
                     cap_r2(mx * p.cap_k, 0.f, r0, r1);
-                    mx = mx == -INFINITY ? mx : fmaf(-2.f * p.cap_log2, r0, p.cap_log2);
+                    mx = none ? -INFINITY : fmaf(-2.f * p.cap_log2, r0, p.cap_log2);
                 } else {
                     mx *= p.scale_log2;
                 }
@@ -335,8 +339,8 @@ __global__ void __launch_bounds__(DuoCfg<kD, T>::kThreads, 2)
                         }
                         float p0 = ex2(x.x), p1 = ex2(x.y);
                         if (kCap && kMask) {   // the cap of -inf is -softcap
-                            p0 = sr[c][2 * i] == 0xff800000u ? 0.f : p0;
-                            p1 = sr[c][2 * i + 1] == 0xff800000u ? 0.f : p1;
+                            p0 = (in[c] >> (2 * i) & 1u) ? p0 : 0.f;
+                            p1 = (in[c] >> (2 * i + 1) & 1u) ? p1 : 0.f;
                         }
                         sumv[i & 3] = f2_add(sumv[i & 3], f2_pack(p0, p1));
                         pk[i] = Cvt<T>::pack(p0, p1);

@@ -486,10 +486,11 @@ __global__ void __launch_bounds__(SplitCfg<kD, T>::kThreads, 1)
                                        fmaxf(fmaxf(mxv[4], mxv[5]), fmaxf(mxv[6], mxv[7])));
                 if (kCap) {
                     // tanh rises: the cap of the largest raw score is the largest
-                    // capped one (-inf, no visible key, stays -inf)
+                    // capped one (of a visible -inf -softcap; no visible key: -inf)
                     float r0, r1;
                     cap_r2(mx * p.cap_k, 0.f, r0, r1);
-                    return mx == -INFINITY ? mx : fmaf(-2.f * p.cap_log2, r0, p.cap_log2);
+                    const bool none = kMask && max(lo, 0) > min(hi, HK - 1);
+                    return none ? -INFINITY : fmaf(-2.f * p.cap_log2, r0, p.cap_log2);
                 }
                 return kExt ? mx : mx * p.scale_log2;
             };
