@@ -883,7 +883,7 @@ fa_status fa_fwd_kvcache(const void *q, const fa_kv_cache *cache, const int *cac
     if ((st = check_device()) != FA_OK) return st;
     p.c.err = fa::fwd_error_word();
     if (!p.c.err) return FA_ERR_CUDA;
-    const size_t n = (size_t)fa::kKvSms * fa::kKvMaxWarps;
+    const size_t n = (size_t)fa::kKvSms * fa::kv_max_warps(cache->D);
     uint8_t *w = static_cast<uint8_t *>(workspace);
     p.acc = reinterpret_cast<float *>(w);
     p.stat = reinterpret_cast<float4 *>(w + n * 2 * 16 * cache->D * sizeof(float));

@@ -599,8 +599,6 @@ __global__ void __launch_bounds__(SplitCfg<kD, T>::kThreads, 1)
                 *lse_dst = l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
                 // a row of NaN scores: NaN (the other instances give -inf)
                 if ((kFlags & (kFwdCap | kFwdRange)) != 0 && l_run != l_run) *lse_dst = l_run;
-                // a row of NaN scores: NaN (the other instances give -inf)
-                if ((kFlags & (kFwdCap | kFwdRange)) != 0 && l_run != l_run) *lse_dst = l_run;
             }
             const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
             // this warp's DW columns; Dh <= D columns are stored

@@ -297,7 +297,7 @@ struct KvCfg {
     static constexpr int VB = KB + 128;                  // V's blocks lie apart (kv_block_pad)
     static constexpr int SMEM = kWarps * (KB + VB);
     static constexpr int PIECE = NR * 8 * D;             // floats of a piece
-    static_assert(kWarps <= kKvMaxWarps, "the workspace holds kKvMaxWarps workers per SM");
+    static_assert(kWarps <= kv_max_warps(D), "the workspace holds that many workers per SM");
     static_assert(SMEM + 8 * kKvMaxSeqs + 2048 <= 232448, "shared memory overflow");
 };
 
@@ -1082,7 +1082,7 @@ cudaError_t launch_append_t(const KvAppendParams &p, cudaStream_t stream) {
 
 size_t kv_workspace_bytes(int D) {
     // two pieces of up to 16 rows per worker, and what its piece 0 is
-    const size_t n = (size_t)kKvSms * kKvMaxWarps;
+    const size_t n = (size_t)kKvSms * kv_max_warps(D);
     return kv_pieces_bytes(n, D) + n * sizeof(int4);
 }
 

@@ -50,9 +50,10 @@ struct KvAttnParams {
     long long budget_ns;         // bound of every device-side wait
 };
 
-// Workers of the attention kernel at most: kKvMaxWarps warps of kKvSms CTAs.
+// Workers of the attention kernel at most: kv_max_warps(D) warps of kKvSms CTAs.
 // The grid is the device's SM count (152 on GB300), held at kKvSms.
-constexpr int kKvSms = 160, kKvMaxWarps = 16;
+constexpr int kKvSms = 160;
+constexpr int kv_max_warps(int D) { return D == 128 ? 8 : 12; }
 constexpr int kKvMaxSeqs = 4096;   // sequences whose tile counts fit shared memory
 // bytes of two pieces of 16 rows for n holders: fragments, then statistics
 inline size_t kv_pieces_bytes(size_t n, int D) { return n * 2 * 16 * (D * sizeof(float) + sizeof(float4)); }
