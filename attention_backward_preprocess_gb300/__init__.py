@@ -79,7 +79,7 @@ def dropout_mask_shape(q, k, cu_seqlens_q=None, max_seqlen_k=None):
 
 def _ext(Hq, window=None, alibi_slopes=None, seqused_q=None, seqused_k=None, bias=None,
          dbias=None, dropout=None, totals=None, head_dim_v=0, softcap=0.0, mask_ranges=None,
-         sizes=None, strides=None):
+         sizes=None, strides=None, rows=0, dtype=None):
     """A pointer to an FaExt, or None when no extension is asked for.
 
     ``bias``: [B or 1, Hq or 1, Sq, >= Sk] in the input dtype, last axis
@@ -92,13 +92,20 @@ def _ext(Hq, window=None, alibi_slopes=None, seqused_q=None, seqused_k=None, bia
     so that the library need not read them back (no stream synchronisation).
     ``head_dim_v``: the value head dim when it differs from q's (else 0).
     ``softcap``: scores become softcap * tanh(score / softcap) (0: none).
-    ``mask_ranges``: a MaskRanges of the call's ``sizes`` (B, Sq, Sk, GPU).
+    ``mask_ranges``: a MaskRanges of the call's ``sizes`` (B, Sq, Sk, GPU); ``rows``
+    query rows of type ``dtype`` in all.
     ``strides``: what ``_inputs`` said of inputs that are not contiguous."""
     if (window is None and alibi_slopes is None and seqused_q is None and seqused_k is None
             and bias is None and dbias is None and dropout is None and totals is None
             and not head_dim_v and softcap == 0.0 and mask_ranges is None and not strides):
         return None
     e = FaExt(-1, -1)   # the rest 0
+    B, Sq, Sk, at = sizes
+
+    def reaches(name, t, n, dtype=None):
+        """``t`` is on the call's GPU and holds the n elements the kernels may read or write."""
+        if t.get_device() != at or t.numel() < n or (dtype is not None and t.dtype != dtype):
+            raise ValueError("%s: at least %d elements%s on q's GPU" % (name, n, "" if dtype is None else " of %s" % dtype))
     if strides:
         for name, s in strides.items():
             setattr(e, name + "_stride", s)
@@ -118,22 +125,28 @@ def _ext(Hq, window=None, alibi_slopes=None, seqused_q=None, seqused_k=None, bia
             m = dropout[3]
             if m.dtype != torch.int32 or not m.is_contiguous():
                 raise ValueError("dropout mask: a contiguous int32 tensor of dropout_mask_shape(...)")
+            reaches("dropout mask", m, rows * Hq * ((Sk + 31) // 32))
             e.dropout_mask = m.data_ptr()
     if window is not None:
         e.window_left, e.window_right = int(window[0]), int(window[1])
     if alibi_slopes is not None:
         if alibi_slopes.dtype != torch.float32 or not alibi_slopes.is_contiguous():
             raise ValueError("alibi_slopes: contiguous fp32 [Hq] or [B, Hq]")
+        reaches("alibi_slopes", alibi_slopes, Hq * (B if alibi_slopes.dim() == 2 else 1))
         e.alibi_slopes = alibi_slopes.data_ptr()
         e.alibi_batch_stride = Hq if alibi_slopes.dim() == 2 else 0
     for name, t in (("seqused_q", seqused_q), ("seqused_k", seqused_k)):
         if t is not None:
             if t.dtype != torch.int32 or not t.is_contiguous():
                 raise ValueError(name + ": contiguous int32 [B]")
+            reaches(name, t, B)
             setattr(e, name, t.data_ptr())
     if bias is not None:
         if bias.dim() != 4 or bias.stride(3) != 1:
             raise ValueError("bias: [B or 1, Hq or 1, Sq, Sk] with a contiguous last axis")
+        reaches("bias", bias, 0, dtype)
+        if any(n != 1 and n < m for n, m in zip(bias.shape[:2], (B, Hq))) or bias.shape[2] < Sq or bias.shape[3] < Sk:
+            raise ValueError("bias: [B or 1, Hq or 1, Sq, Sk], got %r" % (tuple(bias.shape),))
         e.bias = bias.data_ptr()
         e.bias_batch_stride = 0 if bias.shape[0] == 1 else bias.stride(0)
         e.bias_head_stride = 0 if bias.shape[1] == 1 else bias.stride(1)
@@ -141,6 +154,7 @@ def _ext(Hq, window=None, alibi_slopes=None, seqused_q=None, seqused_k=None, bia
     if dbias is not None:
         if not dbias.is_contiguous():
             raise ValueError("dbias: a contiguous [B, Hq, Sq, Sk] tensor")
+        reaches("dbias", dbias, B * Hq * Sq * Sk, dtype)
         e.dbias = dbias.data_ptr()
     return ctypes.pointer(e)
 
@@ -253,6 +267,8 @@ def fa_fwd_kvcache(q, cache, cache_len, softmax_scale=None, softcap=0.0, window_
                 cache._check("out[1]", out[1], torch.float32, (B, Hq, Sq))
             if workspace is None:
                 workspace = q.new_empty(fa_fwd_kvcache_workspace_bytes(D), dtype=torch.uint8)
+            else:
+                _scratch(workspace, cache.device)
         _check(lib().fa_fwd_kvcache(q.data_ptr(), ctypes.byref(c), cache_len.data_ptr(), out[0].data_ptr(),
                                     out[1].data_ptr(), B, Sq, Hq, scale, softcap, window_left, code,
                                     workspace.data_ptr(), workspace.numel(), _stream(stream)), "fa_fwd_kvcache")
@@ -593,6 +609,13 @@ def _like(t):
     return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
+def _scratch(workspace, at):
+    """A caller's workspace lies on the call's GPU (its size is the library's to check)."""
+    if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()
+                                  or workspace.get_device() != at):
+        raise ValueError("workspace: a contiguous uint8 tensor on q's GPU")
+
+
 def _outputs(**tensors):
     for name, t in tensors.items():
         if t is not None and not t.is_contiguous():
@@ -635,7 +658,7 @@ def fa_fwd(q, k, v, causal=False, softmax_scale=None, cu_seqlens_q=None, cu_seql
             lse = torch.empty((Hq, q.shape[0]), dtype=torch.float32, device=q.device)
         ext = _ext(Hq, window, alibi_slopes, seqused_q, seqused_k, bias, dropout=dropout,
                    totals=totals, head_dim_v=_value_dim(D, v), softcap=softcap, mask_ranges=mask_ranges,
-                   sizes=(B, Sq, Sk, q.get_device()), strides=strides)
+                   sizes=(B, Sq, Sk, q.get_device()), strides=strides, rows=q.shape[:-2].numel(), dtype=q.dtype)
         args = [_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Sq, Sk, Hq, Hkv, D, scale,
                 int(bool(causal)), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k)]
         if ext is None:
@@ -672,6 +695,7 @@ def fa_bwd(q, k, v, o, dout, lse, causal=False, softmax_scale=None, cu_seqlens_q
     (q, k, v, o, dout), strides = _inputs(stream, q=q, k=k, v=v, o=o, dout=dout)
     (lse,) = _dense(stream, lse=lse)
     _outputs(dq=dq, dk=dk, dv=dv)
+    _scratch(workspace, q.get_device())
     scale = default_scale(D) if softmax_scale is None else float(softmax_scale)
     with _on(_gpu(q)), _memory(stream):
         dq, dk, dv = (_like(t) if g is None else g for t, g in ((q, dq), (k, dk), (v, dv)))
@@ -679,7 +703,8 @@ def fa_bwd(q, k, v, o, dout, lse, causal=False, softmax_scale=None, cu_seqlens_q
                 _ptr(dv), B, Sq, Sk, Hq, Hkv, D, scale, int(bool(causal)), _ptr(cu_seqlens_q),
                 _ptr(cu_seqlens_k), int(bool(deterministic)), _dtype_code(q)]
         ext = _ext(Hq, window, alibi_slopes, seqused_q, seqused_k, bias, dbias, dropout, totals,
-                   _value_dim(D, v), softcap, mask_ranges, (B, Sq, Sk, q.get_device()), strides)
+                   _value_dim(D, v), softcap, mask_ranges, (B, Sq, Sk, q.get_device()), strides,
+                   q.shape[:-2].numel(), q.dtype)
         if ext is not None:
             st = lib().fa_bwd_ext(*args[:19], ext, *args[19:], _ptr(workspace),
                                   0 if workspace is None else workspace.numel(), _stream(stream))
@@ -760,6 +785,7 @@ def fa_bwd_stages(q, k, v, o, dout, lse, workspace, causal=False, softmax_scale=
     B, Sq, Sk, Hq, Hkv, D = _shape(q, k, cu_seqlens_q, max_seqlen_q, max_seqlen_k)
     _agree(q, k, v, cu_seqlens_q, cu_seqlens_k, o, dout, lse, dq, dk, dv, D)
     _outputs(q=q, k=k, v=v, o=o, dout=dout, lse=lse, dq=dq, dk=dk, dv=dv)
+    _scratch(workspace, q.get_device())
     scale = default_scale(D) if softmax_scale is None else float(softmax_scale)
     dq, dk, dv = (_like(t) if g is None else g for t, g in ((q, dq), (k, dk), (v, dv)))
     shape = [B, Sq, Sk, Hq, Hkv, D]

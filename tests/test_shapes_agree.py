@@ -86,3 +86,46 @@ def test_value_head_dim_of_the_staged_calls(fa):
         x[n] = torch.cat([x[n], x[n]], dim=3)
     with pytest.raises(ValueError, match="^v:"):
         fa.fa_bwd_stages(workspace=torch.zeros(1 << 20, dtype=torch.uint8), **x)
+
+
+# ------------------------------------------- the tensors of the extensions
+def _more(**kw):
+    """_ext for q [2, 16, 4, D] and 24 keys, whose tensors lie on ``at`` (-1: these)."""
+    import attention_backward_preprocess_gb300 as mod
+    at = kw.pop("at", -1)
+    return mod._ext(Hq, sizes=(B, Sq, Sk, at), rows=B * Sq, dtype=BF, **kw)
+
+
+GOOD = dict(alibi_slopes=torch.zeros(Hq), seqused_q=torch.zeros(B, dtype=torch.int32),
+            seqused_k=torch.zeros(B, dtype=torch.int32), bias=torch.zeros((1, Hq, Sq, Sk), dtype=BF),
+            dbias=torch.zeros((B, Hq, Sq, Sk), dtype=BF),
+            dropout=(0.1, 1, 0, torch.zeros((B, Hq, Sq, 1), dtype=torch.int32)))
+SHORT = [("alibi_slopes", torch.zeros(Hq - 1)), ("alibi_slopes", torch.zeros((B - 1, Hq))),
+         ("seqused_q", torch.zeros(B - 1, dtype=torch.int32)), ("seqused_k", torch.zeros(0, dtype=torch.int32)),
+         ("bias", torch.zeros((B, Hq, Sq, Sk))), ("bias", torch.zeros((B, Hq - 2, Sq, Sk), dtype=BF)),
+         ("bias", torch.zeros((B, Hq, Sq - 1, Sk), dtype=BF)), ("bias", torch.zeros((1, 1, Sq, Sk - 8), dtype=BF)),
+         ("dbias", torch.zeros((B, Hq, Sq, Sk - 8), dtype=BF)), ("dbias", torch.zeros((B, Hq, Sq, Sk))),
+         ("dropout", (0.1, 1, 0, torch.zeros((B, Hq, Sq - 1, 1), dtype=torch.int32)))]
+
+
+@pytest.mark.parametrize("name", GOOD)
+def test_extension_tensors_that_reach(name):
+    assert _more(**{name: GOOD[name]}) is not None
+    with pytest.raises(ValueError, match="on q's GPU"):
+        _more(at=0, **{name: GOOD[name]})   # they lie elsewhere
+
+
+@pytest.mark.parametrize("name,t", SHORT, ids=["%s%d" % (n, i) for i, (n, _) in enumerate(SHORT)])
+def test_extension_tensors_too_short(name, t):
+    with pytest.raises(ValueError, match=name):
+        _more(**{name: t})
+
+
+def test_a_workspace_elsewhere():
+    import attention_backward_preprocess_gb300 as mod
+    ws = torch.zeros(256, dtype=torch.uint8)
+    mod._scratch(ws, -1)
+    mod._scratch(None, 0)
+    for bad, at in ((ws, 0), (ws.view(torch.float32), -1), (ws[::2], -1)):
+        with pytest.raises(ValueError, match="workspace"):
+            mod._scratch(bad, at)
