@@ -639,7 +639,8 @@ def fa_fwd(q, k, v, causal=False, softmax_scale=None, cu_seqlens_q=None, cu_seql
     (varlen: cu_seqlens_q[B], cu_seqlens_k[B]) spares the read-back of the
     packed totals, so the call does not synchronise the stream.  ``softcap``
     caps the scores, softcap * tanh(score / softcap); ``mask_ranges`` (from the
-    function of that name) takes the place of ``causal`` and ``window``.
+    function of that name) takes the place of ``causal`` and ``window``, which
+    must be off with it.
     """
     if cu_seqlens_q is None and stream is None and window is None and alibi_slopes is None and seqused_q is None \
             and seqused_k is None and bias is None and dropout is None and totals is None:

@@ -15,7 +15,8 @@
 // a persistent CTA per SM that overlaps one tile's end with the next one's
 // start 165 | 154; two CTAs of 128-key blocks with one S buffer 222 | 180;
 // this one 118 | 124, 111 | 102 with scores taken in packed pairs, 111 | 92 with
-// the cap's tanh by a polynomial where a warp's scores lie within half the cap:
+// the cap's tanh by a polynomial where a warp's scores lie within half the cap (111
+// | 93 since hidden keys are told from visible scores of -inf by their bits):
 // exp2, reciprocal and exp2 again, 12 of the exponential unit's cycles per score
 // and warp, were 1 / 2 of the time (unit 45 % busy, two warps per scheduler).
 // What is left at 8192 tokens: per 64-key block 1480 cycles in each of two CTAs,

@@ -511,9 +511,15 @@ cudaError_t launch_fwd_wide_t(const BwdParams &p, const CUtensorMap &mq, const C
 }
 
 // Capped scores and interval masks: two CTAs to an SM (fa_fwd_duo.cu), unless the
-// problem has at most a tile per SM.  Then only a tile's own
-// latency counts, and two warps per row (fa_fwd_split.cu) finish it sooner (36
-// tiles of 333 tokens, D = 64, cap and prefix: 8 against 15 us).
+// problem has at most a tile per SM.  Then only a tile's own latency counts, and
+// two warps per row (fa_fwd_split.cu) finish a capped one no later.  Kernel times,
+// split | duo, us, at D = 128 (causal cap 30 of 1024 or 333 tokens; documents of
+// 200): 36 tiles 10.5 | 10.9 capped, 9.9 | 9.0 documents; 152 tiles 19.5 | 20.8,
+// 13.9 | 11.7; 153 tiles 17.6 | 12.4, 16.1 | 11.3; 224 tiles 24.9 | 22.0, 20.4 |
+// 14.6; 300 tiles 21.5 | 15.5, 19.7 | 13.6.  At D = 64 the capped ones are within 3 %
+// of each other up to 152 tiles.  (Uncapped intervals would do better with two
+// CTAs at any number; the rule does not look at that.)  Varlen problems count every
+// sequence at the longest one's tiles: a ragged batch may pass the border early.
 bool fwd_duo(const BwdParams &p, int sms) {
     if (p.cap_log2 <= 0.f && !p.mr_row) return false;
     return (long long)p.B * p.Hq * ((p.Sq + 127) / 128) > sms;

@@ -602,7 +602,7 @@ def code_text(text):
 def source_hash(read=None):
     import hashlib
     h = hashlib.sha256()
-    for f in ("fa_bwd_main.cu", "fa_bwd_units.cuh", "fa_device.cuh", "fa_params.h"):
+    for f in ("fa_bwd_main.cu", "fa_bwd_units.cuh", "fa_device.cuh", "fa_epilogue.h", "fa_params.h"):
         path = os.path.join("attention_backward_preprocess_gb300", "csrc", f)
         text = read(path) if read else open(os.path.join(ROOT, path)).read()
         h.update(code_text(text).encode())
