@@ -243,7 +243,9 @@ fa_status fa_fwd(const void *q, const void *k, const void *v, void *o, float *ls
 /* softcap (0 = none; else in [0.001, 1000]): the score of (i, j) becomes
  *   softcap * tanh(scale * <q_i, k_j> / softcap), in natural-log units.  The
  *   backward multiplies dS by 1 - tanh^2; fa_bwd_ext must get the forward's
- *   softcap.  Computed with an absolute error of about softcap * 2^-21.  With
+ *   softcap.  Computed with an absolute error of about softcap * 2^-21; a score
+ *   beyond 32 bits is +-softcap.  A NaN query's row is NaN in O and LSE; in dQ its
+ *   neighbour (rows 2 i and 2 i + 1 of a head) may be NaN with it.  With
  *   the causal mask, windows, used lengths, varlen, deterministic mode and
  *   mask_ranges; not with ALiBi, the bias, dBias, dropout, or head dims above
  *   128 or unequal ones (FA_ERR_UNSUPPORTED).
