@@ -32,6 +32,8 @@ EXPORTED = [
     "fa_bwd_noalloc_scratch_bytes", "fa_fwd_ext", "fa_bwd_ext", "fa_bwd_stages_ext", "fa_bwd_workspace_sync_layout",
     "fa_bwd_noalloc_status", "fa_mask_ranges", "fa_mask_ranges_bytes", "fa_ext_bytes",
     "fa_kvcache_append", "fa_fwd_kvcache", "fa_fwd_kvcache_workspace_bytes",
+    "fa_kvcache4_append", "fa_kvcache4_read", "fa_fwd_kvcache4", "fa_fwd_kvcache4_workspace_bytes",
+    "fa_rope", "fa_rope_frequencies", "fa_rope_steps",
 ]
 
 
@@ -160,22 +162,43 @@ def _ext(Hq, window=None, alibi_slopes=None, seqused_q=None, seqused_k=None, bia
 
 
 class _KvCacheStruct(ctypes.Structure):
-    """fa_kv_cache of include/fa.h."""
+    """fa_kv_cache of include/fa.h, and fa_kv_cache4, whose fields are the same."""
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("num_pages", ctypes.c_int),
                 ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("Hkv", ctypes.c_int),
                 ("D", ctypes.c_int)]
 
 
-class KvCache:
+class _PagedCache:
+    """What the two kinds of cache share: the tensors, held, and their struct."""
+    # read only: the library holds the addresses of these very tensors
+    k, v, k_scale, v_scale, block_table = (property(lambda self, i=i: self._tensors[i]) for i in range(5))
+
+    def _hold(self, k, v, k_scale, v_scale, block_table, P, ps, H, D):
+        self._tensors = k, v, k_scale, v_scale, block_table
+        self._c = _KvCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                 block_table.data_ptr(), P, ps, block_table.shape[1], H, D)
+        self._at = ctypes.addressof(self._c)
+
+    def _check(self, name, t, dtype, shape):
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != self.device \
+                or self.device < 0:
+            raise ValueError("%s: contiguous %s %r on the cache's GPU" % (name, dtype, tuple(shape)))
+
+
+def _kind(cache, cls):
+    """The library reads a cache of another kind, or none, past its end."""
+    if not isinstance(cache, cls):
+        raise ValueError("cache: a %s" % cls.__name__)
+
+
+class KvCache(_PagedCache):
     """An 8-bit paged key / value cache over the caller's tensors: ``k``
     float8_e4m3fn [pages, Hkv, page, D], ``v`` float8_e4m3fn [pages, Hkv, D,
     page], ``k_scale`` / ``v_scale`` float32 [pages, Hkv], ``block_table``
     int32 [B, max_pages]; see fa_kv_cache in include/fa.h.  Keeps the tensors,
     copies nothing.  Their contents may change; other tensors (a wider block
     table) make another KvCache."""
-    # read only: the library holds the addresses of these very tensors
-    k, v, k_scale, v_scale, block_table = (property(lambda self, i=i: self._tensors[i]) for i in range(5))
 
     def __init__(self, k, v, k_scale, v_scale, block_table):
         if k.dim() != 4 or block_table.dim() != 2:
@@ -190,15 +213,7 @@ class KvCache:
                                        ("v_scale", v_scale, torch.float32, (P, H)),
                                        ("block_table", block_table, torch.int32, block_table.shape)):
                 self._check(name, t, dt, shape)
-        self._tensors = k, v, k_scale, v_scale, block_table
-        self._c = _KvCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                                 block_table.data_ptr(), P, ps, block_table.shape[1], H, D)
-        self._at = ctypes.addressof(self._c)
-
-    def _check(self, name, t, dtype, shape):
-        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != self.device \
-                or self.device < 0:
-            raise ValueError("%s: contiguous %s %r on the cache's GPU" % (name, dtype, tuple(shape)))
+        self._hold(k, v, k_scale, v_scale, block_table, P, ps, H, D)
 
 
 def kvcache_append(cache, cache_len, k_new, v_new, cu_new=None, max_new=None, stream=None):
@@ -208,11 +223,17 @@ def kvcache_append(cache, cache_len, k_new, v_new, cu_new=None, max_new=None, st
     ``k_new`` / ``v_new``: [B, T, Hkv, D], or [total, Hkv, D] with ``cu_new``
     (int32 [B + 1] prefix sums) and ``max_new``, the most tokens of one
     sequence.  The cache's tensors are updated in place."""
+    _kind(cache, KvCache)
     if stream is None:
         r = _binding().append(cache._at, cache.B, cache.device, cache_len, k_new, v_new, cu_new, max_new)
         if r is not None:
             _done(r, "fa_kvcache_append")
             return
+    _append("fa_kvcache_append", cache, cache_len, k_new, v_new, cu_new, max_new, stream)
+
+
+def _append(what, cache, cache_len, k_new, v_new, cu_new, max_new, stream):
+    """An append through ctypes, to either kind of cache."""
     B, c = cache.B, cache._c
     cache._check("cache_len", cache_len, torch.int32, (B,))
     if cu_new is None:
@@ -231,9 +252,9 @@ def kvcache_append(cache, cache_len, k_new, v_new, cu_new=None, max_new=None, st
     cache._check("k_new", k_new, k_new.dtype, shape)
     cache._check("v_new", v_new, k_new.dtype, shape)
     with _on(cache.device):
-        _check(lib().fa_kvcache_append(ctypes.byref(c), cache_len.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
-                                       _ptr(cu_new), k_new.numel() // (c.Hkv * c.D), B, int(max_new), code,
-                                       _stream(stream)), "fa_kvcache_append")
+        _check(getattr(lib(), what)(ctypes.byref(c), cache_len.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+                                    _ptr(cu_new), k_new.numel() // (c.Hkv * c.D), B, int(max_new), code,
+                                    _stream(stream)), what)
 
 
 def fa_fwd_kvcache(q, cache, cache_len, softmax_scale=None, softcap=0.0, window_left=-1, workspace=None,
@@ -244,10 +265,16 @@ def fa_fwd_kvcache(q, cache, cache_len, softmax_scale=None, softcap=0.0, window_
     (int32 [B]) counts them.  ``workspace``: a uint8 CUDA tensor of
     ``fa_fwd_kvcache_workspace_bytes(D)`` (allocated when not given); ``out``:
     (o, lse) to write into.  See fa_fwd_kvcache in include/fa.h."""
+    _kind(cache, KvCache)
     if stream is None and out is None and workspace is None:
         r = _binding().attend(cache._at, cache.B, cache.device, q, cache_len, softmax_scale, softcap, window_left)
         if r is not None:
             return _done(r, "fa_fwd_kvcache")
+    return _attend("fa_fwd_kvcache", q, cache, cache_len, softmax_scale, softcap, window_left, workspace, out, stream)
+
+
+def _attend(what, q, cache, cache_len, softmax_scale, softcap, window_left, workspace, out, stream):
+    """An attention over either kind of cache through ctypes."""
     c = cache._c
     if q.dim() != 4:
         raise ValueError("q: [B, Sq, Hq, D]")
@@ -266,18 +293,245 @@ def fa_fwd_kvcache(q, cache, cache_len, softmax_scale=None, softcap=0.0, window_
                 cache._check("out[0]", out[0], q.dtype, q.shape)
                 cache._check("out[1]", out[1], torch.float32, (B, Hq, Sq))
             if workspace is None:
-                workspace = q.new_empty(fa_fwd_kvcache_workspace_bytes(D), dtype=torch.uint8)
+                workspace = q.new_empty(getattr(lib(), what + "_workspace_bytes")(int(D)), dtype=torch.uint8)
             else:
                 _scratch(workspace, cache.device)
-        _check(lib().fa_fwd_kvcache(q.data_ptr(), ctypes.byref(c), cache_len.data_ptr(), out[0].data_ptr(),
+        _check(getattr(lib(), what)(q.data_ptr(), ctypes.byref(c), cache_len.data_ptr(), out[0].data_ptr(),
                                     out[1].data_ptr(), B, Sq, Hq, scale, softcap, window_left, code,
-                                    workspace.data_ptr(), workspace.numel(), _stream(stream)), "fa_fwd_kvcache")
+                                    workspace.data_ptr(), workspace.numel(), _stream(stream)), what)
     return out
 
 
 def fa_fwd_kvcache_workspace_bytes(D) -> int:
     """Bytes of workspace fa_fwd_kvcache needs (0: a head dim it does not take)."""
     return int(lib().fa_fwd_kvcache_workspace_bytes(int(D)))
+
+
+class KvCache4(_PagedCache):
+    """A 4-bit paged key / value cache over the caller's tensors: ``k`` and
+    ``v`` uint8 [pages, Hkv, page, D / 2], ``k_scale`` and ``v_scale`` bfloat16
+    [pages, Hkv, page, D / 64, 2] (scale, middle), ``block_table`` int32 [B,
+    max_pages]; see fa_kv_cache4 in include/fa.h.  Otherwise as KvCache."""
+
+    def __init__(self, k, v, k_scale, v_scale, block_table):
+        if k.dim() != 4 or block_table.dim() != 2:
+            raise ValueError("k: [pages, Hkv, page, D / 2], block_table: [B, max_pages]")
+        P, H, ps, D = k.shape[0], k.shape[1], k.shape[2], 2 * k.shape[3]
+        self.B = block_table.shape[0]
+        self.device = k.get_device()   # index, -1: not on a GPU
+        if self.device < 0 or not _binding().cache4(k, v, k_scale, v_scale, block_table):
+            for name, t, dt, shape in (("k", k, torch.uint8, (P, H, ps, D // 2)),
+                                       ("v", v, torch.uint8, (P, H, ps, D // 2)),
+                                       ("k_scale", k_scale, torch.bfloat16, (P, H, ps, D // 64, 2)),
+                                       ("v_scale", v_scale, torch.bfloat16, (P, H, ps, D // 64, 2)),
+                                       ("block_table", block_table, torch.int32, block_table.shape)):
+                self._check(name, t, dt, shape)
+        self._hold(k, v, k_scale, v_scale, block_table, P, ps, H, D)
+
+
+def kvcache4_append(cache, cache_len, k_new, v_new, cu_new=None, max_new=None, stream=None):
+    """Quantises new keys and values into ``cache`` (a KvCache4) behind the
+    ``cache_len`` tokens each sequence holds: fa_kvcache4_append.  Arguments as
+    for kvcache_append."""
+    _kind(cache, KvCache4)
+    if stream is None:
+        r = _binding().append4(cache._at, cache.B, cache.device, cache_len, k_new, v_new, cu_new, max_new)
+        if r is not None:
+            _done(r, "fa_kvcache4_append")
+            return
+    _append("fa_kvcache4_append", cache, cache_len, k_new, v_new, cu_new, max_new, stream)
+
+
+def fa_fwd_kvcache4(q, cache, cache_len, softmax_scale=None, softcap=0.0, window_left=-1, workspace=None,
+                    out=None, stream=None):
+    """Attention of each sequence's last tokens over a 4-bit paged cache (a
+    KvCache4): returns (o, lse).  Arguments as for fa_fwd_kvcache, ``workspace``
+    of ``fa_fwd_kvcache4_workspace_bytes(D)``."""
+    _kind(cache, KvCache4)
+    if stream is None and out is None and workspace is None:
+        r = _binding().attend4(cache._at, cache.B, cache.device, q, cache_len, softmax_scale, softcap, window_left)
+        if r is not None:
+            return _done(r, "fa_fwd_kvcache4")
+    return _attend("fa_fwd_kvcache4", q, cache, cache_len, softmax_scale, softcap, window_left, workspace, out, stream)
+
+
+def fa_fwd_kvcache4_workspace_bytes(D) -> int:
+    """Bytes of workspace fa_fwd_kvcache4 needs (0: a head dim it does not take)."""
+    return int(lib().fa_fwd_kvcache4_workspace_bytes(int(D)))
+
+
+def kvcache4_read(cache, cache_len, cu_rows, rows, dtype=torch.bfloat16, first=None, out=None, stream=None):
+    """Tokens of a 4-bit cache (a KvCache4) as 16-bit tensors (k, v), each [rows,
+    Hkv, D]: rows ``cu_rows[b] .. cu_rows[b + 1]`` (int32 [B + 1] prefix sums, in
+    all ``rows``) are sequence b's tokens from ``first[b]`` (int32 [B]; None: 0)
+    on, of the ``cache_len[b]`` held.  They are what fa_fwd takes with
+    ``cu_seqlens_k``.  ``out``: (k, v) to write into; rows behind the last
+    sequence's are left as they are.  See fa_kvcache4_read in include/fa.h."""
+    _kind(cache, KvCache4)
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("dtype: bf16 or fp16, got %s" % dtype)
+    if stream is None and out is None:
+        r = _binding().read4(cache._at, cache.B, cache.device, cache_len, cu_rows, rows, dtype == torch.bfloat16, first)
+        if r is not None:
+            return _done(r, "fa_kvcache4_read")
+    c, B, rows = cache._c, cache.B, int(rows)
+    cache._check("cache_len", cache_len, torch.int32, (B,))
+    cache._check("cu_rows", cu_rows, torch.int32, (B + 1,))
+    if first is not None:
+        cache._check("first", first, torch.int32, (B,))
+    if rows <= 0:
+        raise ValueError("rows: the rows of k and v, at least one")
+    with _on(cache.device):
+        with _memory(stream):
+            if out is None:
+                out = tuple(torch.empty((rows, c.Hkv, c.D), dtype=dtype, device=cache.k.device) for _ in range(2))
+            else:
+                for i in range(2):
+                    cache._check("out[%d]" % i, out[i], dtype, (rows, c.Hkv, c.D))
+        _check(lib().fa_kvcache4_read(ctypes.byref(c), cache_len.data_ptr(), _ptr(first), cu_rows.data_ptr(), rows, B,
+                                      out[0].data_ptr(), out[1].data_ptr(), FA_BF16 if dtype == torch.bfloat16 else FA_FP16,
+                                      _stream(stream)), "fa_kvcache4_read")
+    return out
+
+
+# ------------------------------------------------------------ rotary positions
+class _RopeTensor(ctypes.Structure):
+    """fa_rope_tensor of include/fa.h."""
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int),
+                ("in_stride", ctypes.c_longlong * 3), ("out_stride", ctypes.c_longlong * 3)]
+
+
+class RopeTable:
+    """What turns a head's pairs of dims: ``steps``, int64 CUDA tensor
+    [rotary_dim / 2], the part of a turn that pair i makes per position in
+    2^-64ths (as unsigned numbers), and the ``factor`` that the turned dims are
+    multiplied by.  Made by rope_table or RopeTable.of; see fa_rope in
+    include/fa.h."""
+
+    def __init__(self, steps, factor=1.0):
+        self.steps, self.factor = steps, float(factor)
+
+    @property
+    def rotary_dim(self):
+        return 2 * self.steps.numel()
+
+    @staticmethod
+    def of(frequencies, factor=1.0, device="cuda"):
+        """From radians per position (numbers or a tensor, one per pair)."""
+        w = torch.as_tensor(frequencies, dtype=torch.float64).cpu().contiguous()
+        if w.dim() != 1 or w.numel() == 0:
+            raise ValueError("frequencies: one per pair of dims")
+        steps = torch.empty(w.numel(), dtype=torch.int64)
+        _check(lib().fa_rope_steps(w.data_ptr(), w.numel(), steps.data_ptr()), "fa_rope_steps")
+        return RopeTable(steps.to(device), factor)
+
+
+_SCALINGS = {"linear": 1, "ntk": 2, "yarn": 3}
+
+
+def rope_frequencies(rotary_dim, base=10000.0, scaling=None):
+    """(radians per position of every pair, a float64 CPU tensor; factor).
+    ``scaling``: None, ("linear", scale), ("ntk", scale) or ("yarn", scale,
+    trained_len[, beta_fast, beta_slow]); see fa_rope_frequencies in include/fa.h."""
+    kind, args = 0, ()
+    if scaling is not None:
+        if scaling[0] not in _SCALINGS:
+            raise ValueError("scaling: one of %s, got %r" % (", ".join(sorted(_SCALINGS)), scaling[0]))
+        kind, args = _SCALINGS[scaling[0]], tuple(float(x) for x in scaling[1:])
+        if len(args) not in ((2, 4) if kind == 3 else (1,)):
+            raise ValueError("scaling: (kind, scale), for yarn (kind, scale, trained_len[, beta_fast, beta_slow])")
+    args += (1.0, 1.0, 32.0, 1.0)[len(args):]
+    w, factor = torch.empty(max(int(rotary_dim) // 2, 0), dtype=torch.float64), ctypes.c_double()
+    _check(lib().fa_rope_frequencies(int(rotary_dim), float(base), kind, *args, w.data_ptr(), ctypes.byref(factor)),
+           "fa_rope_frequencies")
+    return w, factor.value
+
+
+def rope_table(rotary_dim, base=10000.0, scaling=None, device="cuda"):
+    """The RopeTable of rope_frequencies(rotary_dim, base, scaling)."""
+    return RopeTable.of(*rope_frequencies(rotary_dim, base, scaling), device=device)
+
+
+def rope(q, k, table, positions=None, offsets=None, interleaved=False, out=None, stream=None):
+    """q and k (or None) turned by their rows' positions: (q, k), new tensors or
+    ``out``, which may be the inputs themselves (in place).
+
+    ``q`` / ``k``: [B, S, heads, D] or packed [total, heads, D]; slices of a
+    joint projection are read (and with ``out`` written) where they lie.  The
+    first ``table.rotary_dim`` dims of a head are turned, as pairs of its halves
+    or ``interleaved``; the rest is copied.  A row's position is
+    ``positions[b, s]`` (int32 [B, S]; packed: [total]), or ``offsets[b] + s``
+    (int32 [B]), or s.  See fa_rope in include/fa.h."""
+    return _rope(q, k, table, positions, offsets, interleaved, False, out, stream)
+
+
+def rope_bwd(dq, dk, table, positions=None, offsets=None, interleaved=False, out=None, stream=None):
+    """The gradients of rope's inputs from those of its results: (dq, dk).
+    Arguments as for rope, of which it is the transpose."""
+    return _rope(dq, dk, table, positions, offsets, interleaved, True, out, stream)
+
+
+def _rope(q, k, table, positions, offsets, interleaved, inverse, out, stream):
+    if out is None and stream is None:
+        r = _binding().rope(q, k, table.steps, table.factor, positions, offsets, interleaved, inverse)
+        if r is not None:
+            return _done(r, "fa_rope")
+    at = q.get_device()
+    if at < 0:
+        raise ValueError("q: not on a GPU")
+    if q.dim() not in (3, 4):
+        raise ValueError("q: [B, S, heads, D] or [total, heads, D]")
+    code, D = _dtype_code(q), q.shape[-1]
+    rows = tuple(q.shape[:-2])
+    B, S = rows if len(rows) == 2 else (1, rows[0])
+    if out is not None and (len(out) != 2 or (out[1] is None) != (k is None)):
+        raise ValueError("out: (q, k) as the inputs are")
+    given = [("q", q), ("k", k)] + ([] if out is None else [("out[0]", out[0]), ("out[1]", out[1])])
+    for i, (name, t) in enumerate(given):
+        if t is not None and (t.dim() != q.dim() or t.shape[:-2] != rows or t.shape[-1] != D or t.dtype != q.dtype
+                              or t.get_device() != at or (i > 1 and t.shape != given[i - 2][1].shape)):
+            raise ValueError("%s: %r of q's type on q's GPU" % (name, rows + ("heads", D)))
+    for name, t, shape in (("positions", positions, rows), ("offsets", offsets, (B,))):
+        if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.get_device() != at):
+            raise ValueError("%s: contiguous int32 %r on q's GPU" % (name, shape))
+    steps = table.steps
+    if steps.dtype != torch.int64 or steps.dim() != 1 or not steps.is_contiguous() or steps.get_device() != at:
+        raise ValueError("table: its steps, contiguous int64, on q's GPU")
+    heads = [t.shape[-2] for t in (q, k) if t is not None]
+    if B * S == 0 or 0 in heads:
+        raise ValueError("q: empty")
+
+    def lies(name, t, must):
+        """(batch, row, head) strides as the library takes them; None where it cannot."""
+        st = ((t.shape[0] * t.stride(0),) if t.dim() == 3 else ()) + t.stride()
+        use = [8 if n == 1 else x for n, x in zip(((1,) if t.dim() == 3 else ()) + tuple(t.shape[:-1]), st[:3])]
+        if st[3] == 1 and t.data_ptr() % 16 == 0 and all(0 < x < 1 << 39 and x % 8 == 0 for x in use):
+            return use
+        if must:
+            raise ValueError(name + ": D contiguous, other strides multiples of 8, 16-byte aligned")
+        return None
+    with _on(at), _memory(stream):
+        made, args = [], []
+        for i, (name, t) in enumerate((("q", q), ("k", k))):
+            if t is None:
+                made.append(None)
+                args.append(None)
+                continue
+            into = _like(t) if out is None else out[i]
+            st = lies(name, t, False)
+            if st is None:
+                if out is not None and into.data_ptr() == t.data_ptr():
+                    raise ValueError(name + ": cannot be turned in place as it lies")
+                (t,) = _dense(stream, **{name: t})
+                st = lies(name, t, True)
+            r = _RopeTensor(t.data_ptr(), into.data_ptr(), t.shape[-2])
+            r.in_stride[:], r.out_stride[:] = st, lies("out", into, True)
+            made.append((into, t))   # (a copy lives until the call is made)
+            args.append(ctypes.pointer(r))
+        _check(lib().fa_rope(args[0], args[1], B, S, D, table.rotary_dim, steps.data_ptr(), table.factor,
+                             int(bool(interleaved)), int(bool(inverse)), _ptr(positions), _ptr(offsets), code,
+                             _stream(stream)), "fa_rope")
+    return tuple(None if m is None else m[0] for m in made)
 
 
 class _Here:
@@ -432,6 +686,15 @@ def lib():
         L.fa_fwd_kvcache_workspace_bytes.argtypes = [_i]
         L.fa_fwd_kvcache_workspace_bytes.restype = _sz
         L.fa_fwd_kvcache.argtypes = [_vp, _kp, _vp, _vp, _vp] + [_i] * 3 + [_f, _f, _i, _i, _vp, _sz, _vp]
+        L.fa_kvcache4_append.argtypes = L.fa_kvcache_append.argtypes
+        L.fa_kvcache4_read.argtypes = [_kp] + [_vp] * 3 + [_i] * 2 + [_vp, _vp, _i, _vp]
+        L.fa_fwd_kvcache4_workspace_bytes.argtypes = [_i]
+        L.fa_fwd_kvcache4_workspace_bytes.restype = _sz
+        L.fa_fwd_kvcache4.argtypes = L.fa_fwd_kvcache.argtypes
+        _d, _rp = ctypes.c_double, ctypes.POINTER(_RopeTensor)
+        L.fa_rope_frequencies.argtypes = [_i, _d, _i] + [_d] * 4 + [_vp, _vp]
+        L.fa_rope_steps.argtypes = [_vp, _i, _vp]
+        L.fa_rope.argtypes = [_rp, _rp] + [_i] * 4 + [_vp, _f, _i, _i, _vp, _vp, _i, _vp]
         L.fa_mask_ranges_bytes.argtypes = [_i, _i]
         L.fa_mask_ranges_bytes.restype = _sz
         L.fa_mask_ranges.argtypes = [_vp, _vp] + [_i] * 6 + [_vp, _sz, _vp]
@@ -441,6 +704,8 @@ def lib():
         for name in ("fa_bwd", "fa_bwd_with_workspace", "fa_bwd_preprocess", "fa_bwd_main",
                      "fa_bwd_postprocess", "fa_bwd_workspace_layout", "fa_fwd", "fa_fwd_ext",
                      "fa_bwd_ext", "fa_mask_ranges", "fa_kvcache_append", "fa_fwd_kvcache",
+                     "fa_kvcache4_append", "fa_kvcache4_read", "fa_fwd_kvcache4", "fa_rope",
+                     "fa_rope_frequencies", "fa_rope_steps",
                      "fa_device_status", "fa_selftest_umma", "fa_selftest_semaphore",
                      "fa_selftest_tmem_layout"):
             getattr(L, name).restype = _i

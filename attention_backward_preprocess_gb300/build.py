@@ -20,10 +20,10 @@ LIB = os.path.join(PKG, "libfa_gb300.so")
 BINDING = os.path.join(PKG, "_fa_torch.so")   # the short way in for torch tensors (fa_torch.cpp)
 SOURCES = ["fa_api.cu", "fa_bwd_main.cu", "fa_bwd_wide.cu", "fa_fwd_tc.cu", "fa_fwd_split.cu",
            "fa_fwd_duo.cu",
-           "fa_kernels.cu", "fa_ranges.cu", "fa_kvcache.cu",
+           "fa_kernels.cu", "fa_ranges.cu", "fa_kvcache.cu", "fa_kvcache4.cu", "fa_rope.cu",
            "fa_selftest.cu", "fa_noalloc.cu"]
 HEADERS = ["fa_device.cuh", "fa_params.h", "fa_fwd_common.h", "fa_bwd_units.cuh", "fa_ranges.h",
-           "fa_fwd_ranges.cuh", "fa_kvcache.h", "fa_epilogue.h"]
+           "fa_fwd_ranges.cuh", "fa_kvcache.h", "fa_kvwork.cuh", "fa_epilogue.h", "fa_rope.h"]
 PUBLIC_HEADERS = [os.path.join(ROOT, "include", h) for h in ("fa.h", "fa_selftest.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -15,6 +15,7 @@
 #include "fa_kvcache.h"
 #include "fa_params.h"
 #include "fa_ranges.h"
+#include "fa_rope.h"
 
 namespace fa {
 cudaError_t launch_schedule(const BwdParams &p, cudaStream_t stream);
@@ -191,6 +192,20 @@ bool encode_v_map(CUtensorMap *m, const void *base, int page, long long rows, in
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The 4-bit cache's codes of K or V: rows of D / 2 bytes, `block` of them a copy,
+// swizzled over their own width so that eight rows' 16-byte chunks lie in all banks.
+bool encode_codes_map(CUtensorMap *m, const void *base, int D, long long rows, int block) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)(D / 2), (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(D / 2)};
+    const cuuint32_t box[2] = {(cuuint32_t)(D / 2), (cuuint32_t)block};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // ------------------------------------------------- workspace of the library's
@@ -812,6 +827,81 @@ fa_status check_kv_cache(const fa_kv_cache *c, int B, fa_dtype dtype, fa::KvCach
 
 }  // namespace
 
+namespace {
+
+// The new rows of an append, into the kernels' parameter block.
+fa_status check_kv_append(const int *cache_len, const void *k_new, const void *v_new, const int *cu_new, int rows, int B,
+                          int max_new, fa::KvAppendParams *p) {
+    if (!cache_len || !k_new || !v_new || rows <= 0 || max_new <= 0) return FA_ERR_INVALID_ARG;
+    if (!aligned16(k_new) || !aligned16(v_new) || (reinterpret_cast<uintptr_t>(cache_len) & 3u) ||
+        (reinterpret_cast<uintptr_t>(cu_new) & 3u))
+        return FA_ERR_INVALID_ARG;
+    if ((long long)B * max_new > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+    if (!cu_new && rows != B * max_new) return FA_ERR_INVALID_ARG;
+    p->len = cache_len;
+    p->cu = cu_new;
+    p->k = k_new;
+    p->v = v_new;
+    p->rows = rows;
+    p->B = B;
+    p->max_new = max_new;
+    return FA_OK;
+}
+
+// An attention over a cache of `value_rows` rows a tensor load counts: the arguments
+// that do not depend on how the values are held.
+fa_status check_kv_attn(const void *q, const int *cache_len, void *o, float *lse, int B, int Sq, int Hq, int page_size,
+                        int D, float softmax_scale, float softcap, int window_left, const void *workspace,
+                        size_t workspace_bytes, size_t need, long long value_rows, fa::KvAttnParams *p) {
+    const int Hkv = p->c.Hkv;
+    if (!q || !o || !cache_len || !workspace || Sq <= 0 || Hq <= 0 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
+        (reinterpret_cast<uintptr_t>(cache_len) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return FA_ERR_INVALID_ARG;
+    if (!(std::isfinite(softmax_scale) && softmax_scale > 0.f) || window_left < -1) return FA_ERR_INVALID_ARG;
+    if (softcap != 0.f && !(softcap >= kMinSoftcap && softcap <= kMaxSoftcap)) return FA_ERR_INVALID_ARG;
+    if (B > fa::kKvMaxSeqs) return FA_ERR_UNSUPPORTED;
+    if ((long long)Sq * Hq > (1 << 24)) return FA_ERR_UNSUPPORTED;
+    p->scale_log2 = softmax_scale * kLog2e;
+    if (softcap != 0.f) {
+        p->cap_log2 = softcap * kLog2e;
+        p->cap_k = 2.f * p->scale_log2 / softcap;
+        if (!std::isfinite(p->cap_k)) return FA_ERR_INVALID_ARG;
+    }
+    if (workspace_bytes < need) return FA_ERR_INVALID_ARG;
+    p->len = cache_len;
+    p->q = q;
+    p->o = o;
+    p->lse = lse;
+    p->B = B;
+    p->Sq = Sq;
+    p->Hq = Hq;
+    p->G = Hq / Hkv;
+    // tiles of all sequences, heads and row groups are counted in 32 bits
+    const long long groups = ((long long)p->G * Sq + 7) / 8;
+    const long long tiles = 2 * ((long long)p->c.max_pages * page_size / 64 + 3);   // in halves
+    if (tiles * B > 0x7fffffffLL / ((long long)Hkv * groups)) return FA_ERR_UNSUPPORTED;
+    if (value_rows > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    p->window = std::min(window_left, 1 << 30);   // positions stay inside 32 bits
+    return FA_OK;
+}
+
+// The workspace of n workers, the error word and the wait budget.
+fa_status place_kv_attn(void *workspace, size_t n, int D, fa::KvAttnParams *p) {
+    const fa_status st = check_device();
+    if (st != FA_OK) return st;
+    p->c.err = fa::fwd_error_word();
+    if (!p->c.err) return FA_ERR_CUDA;
+    uint8_t *w = static_cast<uint8_t *>(workspace);
+    p->acc = reinterpret_cast<float *>(w);
+    p->stat = reinterpret_cast<float4 *>(w + n * 2 * 16 * D * sizeof(float));
+    p->meta = reinterpret_cast<int4 *>(w + fa::kv_pieces_bytes(n, D));
+    p->budget_ns = g_budget_ns.load();
+    return FA_OK;
+}
+
+}  // namespace
+
 fa_status fa_kvcache_append(const fa_kv_cache *cache, const int *cache_len, const void *k_new, const void *v_new,
                             const int *cu_new, int rows, int B, int max_new, fa_dtype dtype,
                             cudaStream_t stream) {
@@ -819,23 +909,11 @@ fa_status fa_kvcache_append(const fa_kv_cache *cache, const int *cache_len, cons
     std::memset(&p, 0, sizeof(p));
     fa_status st = check_kv_cache(cache, B, dtype, &p.c);
     if (st != FA_OK) return st;
-    if (!cache_len || !k_new || !v_new || rows <= 0 || max_new <= 0) return FA_ERR_INVALID_ARG;
-    if (!aligned16(k_new) || !aligned16(v_new) || (reinterpret_cast<uintptr_t>(cache_len) & 3u) ||
-        (reinterpret_cast<uintptr_t>(cu_new) & 3u))
-        return FA_ERR_INVALID_ARG;
-    if ((long long)B * max_new > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
-    if (!cu_new && rows != B * max_new) return FA_ERR_INVALID_ARG;
+    if ((st = check_kv_append(cache_len, k_new, v_new, cu_new, rows, B, max_new, &p)) != FA_OK) return st;
     if (cache->Hkv > 65535) return FA_ERR_UNSUPPORTED;   // grid columns
     if ((st = check_device()) != FA_OK) return st;
     p.c.err = fa::fwd_error_word();
     if (!p.c.err) return FA_ERR_CUDA;
-    p.len = cache_len;
-    p.cu = cu_new;
-    p.k = k_new;
-    p.v = v_new;
-    p.rows = rows;
-    p.B = B;
-    p.max_new = max_new;
     return cuda_status(fa::launch_kv_append(p, cache->D, dtype == FA_BF16, stream));
 }
 
@@ -848,56 +926,195 @@ fa_status fa_fwd_kvcache(const void *q, const fa_kv_cache *cache, const int *cac
     std::memset(&p, 0, sizeof(p));
     fa_status st = check_kv_cache(cache, B, dtype, &p.c);
     if (st != FA_OK) return st;
-    if (!q || !o || !cache_len || !workspace || Sq <= 0 || Hq <= 0 || Hq % cache->Hkv != 0)
-        return FA_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
-        (reinterpret_cast<uintptr_t>(cache_len) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
-        return FA_ERR_INVALID_ARG;
-    if (!(std::isfinite(softmax_scale) && softmax_scale > 0.f) || window_left < -1) return FA_ERR_INVALID_ARG;
-    if (softcap != 0.f && !(softcap >= kMinSoftcap && softcap <= kMaxSoftcap)) return FA_ERR_INVALID_ARG;
-    if (B > fa::kKvMaxSeqs) return FA_ERR_UNSUPPORTED;
-    if ((long long)Sq * Hq > (1 << 24)) return FA_ERR_UNSUPPORTED;
-    p.scale_log2 = softmax_scale * kLog2e;
-    if (softcap != 0.f) {
-        p.cap_log2 = softcap * kLog2e;
-        p.cap_k = 2.f * p.scale_log2 / softcap;
-        if (!std::isfinite(p.cap_k)) return FA_ERR_INVALID_ARG;
-    }
-    const size_t need = fa_fwd_kvcache_workspace_bytes(cache->D);
-    if (workspace_bytes < need) return FA_ERR_INVALID_ARG;
-    p.len = cache_len;
-    p.q = q;
-    p.o = o;
-    p.lse = lse;
-    p.B = B;
-    p.Sq = Sq;
-    p.Hq = Hq;
-    p.G = Hq / cache->Hkv;
-    // tiles of all sequences, heads and row groups are counted in 32 bits
-    const long long groups = ((long long)p.G * Sq + 7) / 8;
-    const long long tiles = 2 * ((long long)cache->max_pages * cache->page_size / 64 + 3);   // in halves
-    if (tiles * B > 0x7fffffffLL / ((long long)cache->Hkv * groups)) return FA_ERR_UNSUPPORTED;
-    // rows of V as the tensor loads see it
-    if ((long long)cache->num_pages * cache->Hkv * cache->D > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
-    p.window = std::min(window_left, 1 << 30);   // positions stay inside 32 bits
-    if ((st = check_device()) != FA_OK) return st;
-    p.c.err = fa::fwd_error_word();
-    if (!p.c.err) return FA_ERR_CUDA;
-    const size_t n = (size_t)fa::kKvSms * fa::kv_max_warps(cache->D);
-    uint8_t *w = static_cast<uint8_t *>(workspace);
-    p.acc = reinterpret_cast<float *>(w);
-    p.stat = reinterpret_cast<float4 *>(w + n * 2 * 16 * cache->D * sizeof(float));
-    p.meta = reinterpret_cast<int4 *>(w + fa::kv_pieces_bytes(n, cache->D));
-    p.budget_ns = g_budget_ns.load();
-    const int ps = cache->page_size;
+    const int ps = cache->page_size, D = cache->D;
+    const long long v_rows = (long long)cache->num_pages * cache->Hkv * D;   // as the tensor loads see V
+    if ((st = check_kv_attn(q, cache_len, o, lse, B, Sq, Hq, ps, D, softmax_scale, softcap, window_left, workspace,
+                            workspace_bytes, fa_fwd_kvcache_workspace_bytes(D), v_rows, &p)) != FA_OK)
+        return st;
+    if ((st = place_kv_attn(workspace, (size_t)fa::kKvSms * fa::kv_max_warps(D), D, &p)) != FA_OK) return st;
     p.v_block = ps % 64 == 0 ? 64 : ps % 32 == 0 ? 32 : 16;
     // pads that spread the blocks of a lane's four rows over the banks; tensor
     // loads (a block narrower than its page) need 128-byte destinations
     p.v_pad = p.v_block != ps || ps == 64 ? 0 : ps == 32 ? 64 : 32;
     CUtensorMap mv;
-    if (!encode_v_map(&mv, cache->v, ps, (long long)cache->num_pages * cache->Hkv * cache->D, p.v_block, cache->D))
+    if (!encode_v_map(&mv, cache->v, ps, v_rows, p.v_block, D)) return FA_ERR_CUDA;
+    return cuda_status(fa::launch_kv_attn(p, mv, D, dtype == FA_BF16, sm_count(), stream));
+}
+
+namespace {
+
+// The 4-bit cache's fields: the 8-bit one's checks, with scales copied 16 bytes at a time.
+fa_status check_kv_cache4(const fa_kv_cache4 *c, int B, fa_dtype dtype, fa::KvCacheParams *p) {
+    if (!c || !c->k_scale || !c->v_scale) return FA_ERR_INVALID_ARG;
+    const fa_kv_cache same = {c->k, c->v, static_cast<float *>(c->k_scale), static_cast<float *>(c->v_scale),
+                              c->block_table, c->num_pages, c->page_size, c->max_pages, c->Hkv, c->D};
+    if (!aligned16(c->k_scale) || !aligned16(c->v_scale)) return FA_ERR_INVALID_ARG;
+    return check_kv_cache(&same, B, dtype, p);
+}
+// Items of a row of the append and of the read, counted in 32 bits over eight rows.
+constexpr int kKv4MaxHeads = 1 << 20;
+
+}  // namespace
+
+fa_status fa_kvcache4_append(const fa_kv_cache4 *cache, const int *cache_len, const void *k_new, const void *v_new,
+                             const int *cu_new, int rows, int B, int max_new, fa_dtype dtype, cudaStream_t stream) {
+    fa::KvAppendParams p;
+    std::memset(&p, 0, sizeof(p));
+    fa_status st = check_kv_cache4(cache, B, dtype, &p.c);
+    if (st != FA_OK) return st;
+    if ((st = check_kv_append(cache_len, k_new, v_new, cu_new, rows, B, max_new, &p)) != FA_OK) return st;
+    if (cache->Hkv > kKv4MaxHeads) return FA_ERR_UNSUPPORTED;
+    if ((st = check_device()) != FA_OK) return st;
+    p.c.err = fa::fwd_error_word();
+    if (!p.c.err) return FA_ERR_CUDA;
+    return cuda_status(fa::launch_kv4_append(p, cache->D, dtype == FA_BF16, stream));
+}
+
+fa_status fa_kvcache4_read(const fa_kv_cache4 *cache, const int *cache_len, const int *first, const int *cu_rows, int rows,
+                           int B, void *k_out, void *v_out, fa_dtype dtype, cudaStream_t stream) {
+    fa::KvReadParams p;
+    std::memset(&p, 0, sizeof(p));
+    fa_status st = check_kv_cache4(cache, B, dtype, &p.c);
+    if (st != FA_OK) return st;
+    if (!cache_len || !cu_rows || !k_out || !v_out || rows <= 0) return FA_ERR_INVALID_ARG;
+    if (!aligned16(k_out) || !aligned16(v_out)) return FA_ERR_INVALID_ARG;
+    const int *ints[] = {cache_len, first, cu_rows};
+    for (const int *x : ints)
+        if (reinterpret_cast<uintptr_t>(x) & 3u) return FA_ERR_INVALID_ARG;
+    if (cache->Hkv > kKv4MaxHeads) return FA_ERR_UNSUPPORTED;
+    if ((st = check_device()) != FA_OK) return st;
+    p.c.err = fa::fwd_error_word();
+    if (!p.c.err) return FA_ERR_CUDA;
+    p.len = cache_len;
+    p.first = first;
+    p.cu = cu_rows;
+    p.k = k_out;
+    p.v = v_out;
+    p.rows = rows;
+    p.B = B;
+    return cuda_status(fa::launch_kv4_read(p, cache->D, dtype == FA_BF16, stream));
+}
+
+size_t fa_fwd_kvcache4_workspace_bytes(int D) {
+    const size_t n = fa::kv4_workers();
+    return (D == 64 || D == 128) ? fa::kv_pieces_bytes(n, D) + n * sizeof(int4) : 0;
+}
+
+fa_status fa_fwd_kvcache4(const void *q, const fa_kv_cache4 *cache, const int *cache_len, void *o, float *lse, int B,
+                          int Sq, int Hq, float softmax_scale, float softcap, int window_left, fa_dtype dtype,
+                          void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    fa::KvAttnParams p;
+    std::memset(&p, 0, sizeof(p));
+    fa_status st = check_kv_cache4(cache, B, dtype, &p.c);
+    if (st != FA_OK) return st;
+    const int ps = cache->page_size, D = cache->D;
+    const long long rows = (long long)cache->num_pages * cache->Hkv * ps;   // as the tensor loads see them
+    if ((st = check_kv_attn(q, cache_len, o, lse, B, Sq, Hq, ps, D, softmax_scale, softcap, window_left, workspace,
+                            workspace_bytes, fa_fwd_kvcache4_workspace_bytes(D), rows, &p)) != FA_OK)
+        return st;
+    if ((st = place_kv_attn(workspace, fa::kv4_workers(), D, &p)) != FA_OK) return st;
+    p.bf16 = dtype == FA_BF16;
+    p.v_block = ps % 64 == 0 ? 64 : ps % 32 == 0 ? 32 : 16;   // tokens of a copy, all of one page
+    CUtensorMap mk, mv;
+    if (!encode_codes_map(&mk, cache->k, D, rows, p.v_block) || !encode_codes_map(&mv, cache->v, D, rows, p.v_block))
         return FA_ERR_CUDA;
-    return cuda_status(fa::launch_kv_attn(p, mv, cache->D, dtype == FA_BF16, sm_count(), stream));
+    return cuda_status(fa::launch_kv4_attn(p, mk, mv, D, sm_count(), stream));
+}
+
+// ------------------------------------------------------------ rotary positions
+fa_status fa_rope_frequencies(int rotary_dim, double base, int scaling, double scale, double trained_len,
+                              double beta_fast, double beta_slow, double *w, double *factor) {
+    if (rotary_dim <= 0 || rotary_dim % 2 != 0 || rotary_dim > 256 || !w || !factor) return FA_ERR_INVALID_ARG;
+    if (!(std::isfinite(base) && base > 1.0)) return FA_ERR_INVALID_ARG;
+    if (scaling < FA_ROPE_NONE || scaling > FA_ROPE_YARN) return FA_ERR_INVALID_ARG;
+    if (scaling != FA_ROPE_NONE && !(std::isfinite(scale) && scale >= 1.0)) return FA_ERR_INVALID_ARG;
+    if (scaling == FA_ROPE_NTK) {
+        if (rotary_dim == 2) return FA_ERR_INVALID_ARG;   // its exponent has no value
+        base *= std::pow(scale, (double)rotary_dim / (rotary_dim - 2));
+        if (!std::isfinite(base)) return FA_ERR_INVALID_ARG;
+    }
+    if (scaling == FA_ROPE_YARN && !(std::isfinite(trained_len) && trained_len > 0.0 && std::isfinite(beta_fast) &&
+                                     std::isfinite(beta_slow) && beta_fast > beta_slow))
+        return FA_ERR_INVALID_ARG;
+    *factor = scaling == FA_ROPE_YARN ? 0.1 * std::log(scale) + 1.0 : 1.0;
+    for (int i = 0; i < rotary_dim / 2; ++i) {
+        w[i] = std::pow(base, -2.0 * i / rotary_dim);
+        if (scaling == FA_ROPE_LINEAR) w[i] /= scale;
+        if (scaling == FA_ROPE_YARN) {
+            const double r = trained_len * w[i] / 6.283185307179586;
+            const double g = std::min(1.0, std::max(0.0, (r - beta_slow) / (beta_fast - beta_slow)));
+            w[i] = w[i] / scale * (1.0 - g) + w[i] * g;
+        }
+    }
+    return FA_OK;
+}
+
+fa_status fa_rope_steps(const double *w, int n, unsigned long long *steps) {
+    if (!w || !steps || n <= 0) return FA_ERR_INVALID_ARG;
+    // 2^128 / (2 pi), to the nearest whole number: w = m 2^e (m of 53 bits) is m times it, shifted
+    constexpr unsigned long long hi = 0x28be60db9391054aull, lo = 0x7f09d5f47d4d3770ull;
+    for (int i = 0; i < n; ++i) {
+        if (!(std::isfinite(w[i]) && w[i] >= 0.0 && w[i] < 1024.0)) return FA_ERR_INVALID_ARG;
+        int e = 0;
+        const unsigned long long m = (unsigned long long)std::ldexp(std::frexp(w[i], &e), 53);
+        const unsigned __int128 a = (unsigned __int128)m * hi, b = (unsigned __int128)m * lo;
+        const unsigned __int128 top = a + (b >> 64);   // m 2^128 / (2 pi), in 2^64ths; below 2^117
+        // times 2^(e - 53) 2^64 / 2^128: shifted right by 53 - e more, rounded
+        const int shift = 53 - e;                      // 43 or more
+        steps[i] = shift > 126 ? 0ull : (unsigned long long)(((top >> (shift - 1)) + 1) >> 1);
+    }
+    return FA_OK;
+}
+
+fa_status fa_rope(const fa_rope_tensor *q, const fa_rope_tensor *k, int B, int S, int D, int rotary_dim,
+                  const unsigned long long *steps, float factor, int interleaved, int inverse, const int *positions,
+                  const int *offsets, fa_dtype dtype, cudaStream_t stream) {
+    if (!q || !steps || B <= 0 || S <= 0 || D <= 0 || rotary_dim <= 0 || rotary_dim > D || rotary_dim % 2 != 0)
+        return FA_ERR_INVALID_ARG;
+    if (!std::isfinite(factor) || (positions && offsets)) return FA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(steps) & 7u) || (reinterpret_cast<uintptr_t>(positions) & 3u) ||
+        (reinterpret_cast<uintptr_t>(offsets) & 3u))
+        return FA_ERR_INVALID_ARG;
+    if (D % 8 != 0 || D > 256 || (dtype != FA_BF16 && dtype != FA_FP16)) return FA_ERR_UNSUPPORTED;
+    if ((long long)B * S > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    fa::RopeParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.in_place = 1;
+    const fa_rope_tensor *both[] = {q, k};
+    for (int i = 0; i < 2 && both[i]; ++i) {
+        const fa_rope_tensor &x = *both[i];
+        fa::RopeTensor &t = p.t[i];
+        if (!x.in || !x.out || !aligned16(x.in) || !aligned16(x.out) || x.heads <= 0) return FA_ERR_INVALID_ARG;
+        if (x.heads > 32767) return FA_ERR_UNSUPPORTED;   // items of a row
+        const long long dense[3] = {(long long)S * x.heads * D, (long long)x.heads * D, D};
+        const long long *in[] = {x.in_stride, x.out_stride};
+        long long *out[] = {t.is, t.os};
+        for (int j = 0; j < 2; ++j) {
+            const bool none = in[j][0] == 0 && in[j][1] == 0 && in[j][2] == 0;
+            for (int a = 0; a < 3; ++a) {
+                const long long st = none ? dense[a] : in[j][a];
+                if (st <= 0 || st % 8 != 0 || st >= 1LL << 39) return FA_ERR_INVALID_ARG;
+                out[j][a] = st;
+            }
+        }
+        t.in = x.in;
+        t.out = x.out;
+        p.heads[i] = x.heads;
+        if (x.in != x.out) p.in_place = 0;
+        else if (std::memcmp(t.is, t.os, sizeof(t.is)) != 0) return FA_ERR_INVALID_ARG;
+    }
+    fa_status st = check_device();
+    if (st != FA_OK) return st;
+    p.B = B;
+    p.S = S;
+    p.D = D;
+    p.R = rotary_dim;
+    p.steps = steps;
+    p.positions = positions;
+    p.offsets = offsets;
+    p.factor = factor;
+    p.inverse = inverse ? 1 : 0;
+    return cuda_status(fa::launch_rope(p, interleaved ? 1 : 0, dtype == FA_BF16, sm_count(), stream));
 }
 
 size_t fa_ext_bytes(void) { return sizeof(fa_ext); }

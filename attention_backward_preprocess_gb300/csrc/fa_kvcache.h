@@ -1,4 +1,4 @@
-// fa_kvcache.h -- parameter blocks of the 8-bit paged key / value cache.
+// fa_kvcache.h -- parameter blocks of the paged key / value caches.
 #pragma once
 
 #include <cstddef>
@@ -9,8 +9,10 @@
 
 namespace fa {
 
-// The cache: e4m3 values, K as [page][kv head][token][d], V as [page][kv
+// The 8-bit cache: e4m3 values, K as [page][kv head][token][d], V as [page][kv
 // head][d][token], one power-of-two scale per (page, kv head).
+// The 4-bit cache: codes as [page][kv head][token][d / 2] for both, and in place of
+// the scales [page][kv head][token][d / 64] words of bf16 (scale, middle).
 struct KvCacheParams {
     uint8_t *k, *v;
     float *k_scale, *v_scale;
@@ -25,6 +27,13 @@ struct KvAppendParams {
     const int *cu;         // [B + 1] rows of the new tokens; null: max_new each
     const void *k, *v;     // [rows, Hkv, D]
     int rows, B, max_new;
+};
+
+struct KvReadParams {
+    KvCacheParams c;
+    const int *len, *first, *cu;   // [B] tokens held, [B] first token read (null: 0), [B + 1] rows
+    void *k, *v;           // [rows, Hkv, D]
+    int rows, B;
 };
 
 struct KvAttnParams {
@@ -48,6 +57,8 @@ struct KvAttnParams {
     // widest that divides a page's tokens), v_pad bytes apart
     int v_block, v_pad;
     long long budget_ns;         // bound of every device-side wait
+    int bf16;                    // 4-bit cache: q's and o's type
+    int stages;                  // and the tiles a worker has in shared memory
 };
 
 // Workers of the attention kernel at most: kv_max_warps(D) warps of kKvSms CTAs.
@@ -58,9 +69,16 @@ constexpr int kKvMaxSeqs = 4096;   // sequences whose tile counts fit shared mem
 // bytes of two pieces of 16 rows for n holders: fragments, then statistics
 inline size_t kv_pieces_bytes(size_t n, int D) { return n * 2 * 16 * (D * sizeof(float) + sizeof(float4)); }
 size_t kv_workspace_bytes(int D);
+// The 4-bit cache's attention has workers of its own number.
+constexpr int kKv4MaxWarps = 12;
+inline size_t kv4_workers() { return (size_t)kKvSms * kKv4MaxWarps; }
 
 cudaError_t launch_kv_append(const KvAppendParams &p, int D, int bf16, cudaStream_t stream);
 cudaError_t launch_kv_attn(const KvAttnParams &p, const CUtensorMap &map_v, int D, int bf16, int sms,
                            cudaStream_t stream);
+cudaError_t launch_kv4_append(const KvAppendParams &p, int D, int bf16, cudaStream_t stream);
+cudaError_t launch_kv4_read(const KvReadParams &p, int D, int bf16, cudaStream_t stream);
+cudaError_t launch_kv4_attn(const KvAttnParams &p, const CUtensorMap &map_k, const CUtensorMap &map_v, int D, int sms,
+                            cudaStream_t stream);
 
 }  // namespace fa

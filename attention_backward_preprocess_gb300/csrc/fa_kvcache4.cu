@@ -1,0 +1,808 @@
+// fa_kvcache4.cu -- the 4-bit paged key / value cache: appending to it, reading
+// it back, and the attention of a sequence's last tokens over it.
+//
+// A value is middle + scale (c - 8) for a code c in 0 .. 15, with a bf16 (scale,
+// middle) pair per 64 dims of a token.  Unsigned codes, because they reach the
+// tensor core at one logical operation per two of them: below 2^11 the bits of an
+// f16 number are that number in units of 2^-24, so masking a word of eight codes
+// with 0x000f000f leaves two f16 operands c 2^-24, and with 0x00f000f0 two of 16 c
+// 2^-24.  What the units and the 16 do is undone on the other operand or the result.
+#include <type_traits>
+
+#include "fa_device.cuh"
+#include "fa_kvcache.h"
+#include "fa_kvwork.cuh"
+#include "fa_params.h"
+
+namespace fa {
+namespace {
+
+// ------------------------------------------------------- rows of a ragged call
+// The sequence whose rows hold `row`: the number of b with cu[b + 1] <= row.  For
+// the whole CTA (kThreads wide) at once: one round of loads for up to kThreads
+// sequences, where a search would take one after the other.
+template <int kThreads>
+__device__ __forceinline__ int first_sequence(const int *cu, int B, int row) {
+    int n = 0;
+    for (int b = threadIdx.x; b < B; b += kThreads) n += __ldg(cu + b + 1) <= row ? 1 : 0;
+    __shared__ int s_n[kThreads / 32];
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (threadIdx.x % 32 == 0) s_n[threadIdx.x / 32] = n;
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) all += s_n[i];
+    return all;
+}
+// ... of a later row, from that one on
+__device__ __forceinline__ int next_sequence(const int *cu, int B, int b, int row) {
+    int hi = B;
+    if (b < B && __ldg(cu + b + 1) > row) return b;
+    while (b < hi) {
+        const int mid = (b + hi) >> 1;
+        if (__ldg(cu + mid + 1) <= row) b = mid + 1;
+        else hi = mid;
+    }
+    return b;
+}
+
+// Place of token `at` of sequence b, in tokens of one head: (page Hkv) page_size +
+// slot, so that head h's row is h page_size further; -1 (reported) on a bad page.
+__device__ __forceinline__ long long token_row(const KvCacheParams &c, int b, int at) {
+    const int i = at / c.page;
+    const int page = __ldg(c.table + (long long)b * c.max_pages + i);
+    if (page < 0 || page >= c.num_pages) {
+        atomicOr(c.err, kErrBadPage);
+        return -1;
+    }
+    return (long long)page * c.Hkv * c.page + (at - i * c.page);
+}
+
+constexpr float kLeastScale = 0x1p-60f, kFifteenths = 8947849.f * 0x1p-26f;   // 2 / 15
+
+__device__ __forceinline__ float lanes8_min(float v) {
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) v = fminf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float lanes8_max(float v) {
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// ------------------------------------------------------------------ append
+// A thread takes eight dims of one new token (K or V, one head); the eight
+// threads of a group of 64 share its least and largest value by shuffles.  Every
+// token is written by itself, so nothing of the cache is read.
+constexpr int kAppend = 256;   // threads
+constexpr int kMaxRows = 8;    // tokens of a CTA
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kAppend) kv4_append_kernel(const __grid_constant__ KvAppendParams p, int per_cta) {
+    __shared__ long long s_at[kMaxRows];
+    constexpr int CH = D / 8;
+    const int tid = threadIdx.x, row0 = blockIdx.x * per_cta, rows = min(per_cta, p.rows - row0);
+    const int side = p.c.Hkv * CH, per_row = 2 * side, items = rows * per_row;   // (side: a multiple of 8)
+    auto load = [&](int i) -> uint4 {
+        const int r = i / per_row, in = i - r * per_row, is_v = in >= side;
+        const T *src = reinterpret_cast<const T *>(is_v ? p.v : p.k);
+        return __ldcs(reinterpret_cast<const uint4 *>(src) + (long long)(row0 + r) * side + (in - (is_v ? side : 0)));
+    };
+    uint4 x = tid < items ? load(tid) : make_uint4(0u, 0u, 0u, 0u);   // on its way while the rows are looked up
+    // every sequence's rows and length, once
+    if (blockIdx.x == 0)
+        for (int b = tid; b < p.B; b += kAppend) {
+            const int at = p.cu ? p.cu[b] : b * p.max_new, n = p.cu ? p.cu[b + 1] - at : p.max_new, len = p.len[b];
+            if (n < 0 || n > p.max_new || at < 0 || (long long)at + n > p.rows || len < 0 ||
+                (long long)len + n > (long long)p.c.max_pages * p.c.page)
+                atomicOr(p.c.err, kErrBadLength);
+        }
+    const int b0 = p.cu ? first_sequence<kAppend>(p.cu, p.B, row0) : 0;
+    if (tid < rows) {
+        const int row = row0 + tid;
+        const int b = p.cu ? next_sequence(p.cu, p.B, b0, row) : row / p.max_new;
+        long long at = -1;
+        if (b < p.B) {
+            const int from = p.cu ? __ldg(p.cu + b) : b * p.max_new, n = p.cu ? __ldg(p.cu + b + 1) - from : p.max_new;
+            const int len = __ldg(p.len + b);
+            // (a row of no sequence, or of one that the call said otherwise of: left alone)
+            if (row >= from && from >= 0 && n <= p.max_new && (long long)from + n <= p.rows && len >= 0 &&
+                (long long)len + n <= (long long)p.c.max_pages * p.c.page)
+                at = token_row(p.c, b, len + (row - from));
+        }
+        s_at[tid] = at;
+    }
+    __syncthreads();
+    for (int i0 = 0; i0 < items; i0 += kAppend) {   // (items: a multiple of 8, so groups are whole)
+        const int i = i0 + tid;
+        uint4 nx = make_uint4(0u, 0u, 0u, 0u);
+        if (i + kAppend < items) nx = load(i + kAppend);
+        float f[8];
+        {
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 y = Cvt<T>::unpack(w[k]);
+                f[2 * k] = y.x, f[2 * k + 1] = y.y;
+            }
+        }
+        float lo = f[0], hi = f[0], sum = 0.f;   // sum: NaN if any value is NaN or infinite
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            lo = fminf(lo, f[k]), hi = fmaxf(hi, f[k]);
+            sum += f[k] * 0.f;
+        }
+        lo = lanes8_min(lo), hi = lanes8_max(hi);
+        const bool bad = (__ballot_sync(0xffffffffu, sum != 0.f) >> (tid & 24) & 255u) != 0u;   // (NaN != 0)
+        const float mid = __bfloat162float(__float2bfloat16_rn(__fadd_rn(0.5f * lo, 0.5f * hi)));
+        const float far = fmaxf(__fsub_rn(hi, mid), __fsub_rn(mid, lo)) * kFifteenths;
+        const float scale = fmaxf(__uint_as_float((__float_as_uint(far) + 0xffffu) & 0xffff0000u), kLeastScale);
+        const float inv = __frcp_rn(scale);
+        uint32_t codes = 0u;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float c = fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(f[k], mid), inv)), -8.f), 7.f);
+            codes |= (uint32_t)((int)c + 8) << (4 * k);
+        }
+        if (i < items) {
+            const int r = i / per_row, in = i - r * per_row, is_v = in >= side, rest = in - (is_v ? side : 0);
+            const int h = rest / CH, ch = rest % CH;
+            if (s_at[r] >= 0) {
+                const long long at = s_at[r] + (long long)h * p.c.page;
+                reinterpret_cast<uint32_t *>(is_v ? p.c.v : p.c.k)[at * CH + ch] = bad ? 0x88888888u : codes;
+                if (ch % 8 == 0)
+                    reinterpret_cast<uint32_t *>(is_v ? p.c.v_scale : p.c.k_scale)[at * (D / 64) + ch / 8] =
+                        bad ? 0x7fc00000u | __float_as_uint(kLeastScale) >> 16
+                            : __float_as_uint(scale) >> 16 | (__float_as_uint(mid) & 0xffff0000u);
+            }
+        }
+        x = nx;
+    }
+}
+
+// -------------------------------------------------------------------- read
+// A thread takes 16 dims of one token: eight bytes of codes and a word of scale
+// and middle in, two 16-byte pieces out.
+constexpr int kRead = 256;
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kRead) kv4_read_kernel(const __grid_constant__ KvReadParams p, int per_cta) {
+    __shared__ long long s_at[kMaxRows];
+    constexpr int CH = D / 16;
+    const int tid = threadIdx.x, row0 = blockIdx.x * per_cta, rows = min(per_cta, p.rows - row0);
+    if (blockIdx.x == 0)
+        for (int b = tid; b < p.B; b += kRead) {
+            const int at = p.cu[b], n = p.cu[b + 1] - at, from = p.first ? p.first[b] : 0, len = p.len[b];
+            if (n < 0 || at < 0 || (long long)at + n > p.rows || from < 0 || len < 0 || (long long)from + n > len ||
+                (long long)len > (long long)p.c.max_pages * p.c.page)
+                atomicOr(p.c.err, kErrBadLength);
+        }
+    const int b0 = first_sequence<kRead>(p.cu, p.B, row0);
+    if (tid < rows) {
+        const int row = row0 + tid, b = next_sequence(p.cu, p.B, b0, row);
+        long long at = -1;
+        if (b < p.B) {
+            const int r0 = __ldg(p.cu + b), n = __ldg(p.cu + b + 1) - r0, from = p.first ? __ldg(p.first + b) : 0;
+            const int len = __ldg(p.len + b);
+            if (row >= r0 && r0 >= 0 && (long long)r0 + n <= p.rows && from >= 0 && len >= 0 && (long long)from + n <= len &&
+                (long long)len <= (long long)p.c.max_pages * p.c.page)
+                at = token_row(p.c, b, from + (row - r0));
+        }
+        s_at[tid] = at;
+    }
+    __syncthreads();
+    const int side = p.c.Hkv * CH, per_row = 2 * side, items = rows * per_row;
+#pragma unroll 2
+    for (int i = tid; i < items; i += kRead) {
+        const int r = i / per_row, in = i - r * per_row, is_v = in >= side, rest = in - (is_v ? side : 0);
+        if (s_at[r] < 0) continue;
+        const int h = rest / CH, ch = rest % CH;
+        const long long at = s_at[r] + (long long)h * p.c.page;
+        const uint2 c = __ldg(reinterpret_cast<const uint2 *>(is_v ? p.c.v : p.c.k) + at * CH + ch);
+        const uint32_t sm = __ldg(reinterpret_cast<const uint32_t *>(is_v ? p.c.v_scale : p.c.k_scale) + at * (D / 64) + ch / 4);
+        const float scale = __uint_as_float(sm << 16), mid = __uint_as_float(sm & 0xffff0000u);
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t two = (k < 4 ? c.x : c.y) >> (8 * (k & 3));
+            w[k] = Cvt<T>::pack(fmaf(scale, (float)((int)(two & 15u) - 8), mid),
+                                fmaf(scale, (float)((int)(two >> 4 & 15u) - 8), mid));
+        }
+        uint4 *dst = reinterpret_cast<uint4 *>(is_v ? p.v : p.k) + ((long long)(row0 + r) * side + rest) * 2;
+        __stcs(dst, make_uint4(w[0], w[1], w[2], w[3]));
+        __stcs(dst + 1, make_uint4(w[4], w[5], w[6], w[7]));
+    }
+}
+
+// --------------------------------------------------------------- attention
+// The rows of a kv head's query group times Sq tokens lie along N of m16n8k16
+// products, keys (then dims) along M, as in the 8-bit kernel, and the work is
+// shared out as there: every warp a worker with a contiguous share of all 64-key
+// tiles.  Bytes bound it (D + D / 8 per key against 4 D flops per row and key), so
+// each worker keeps a ring of kStages tiles (codes of K and V, their scales) in
+// shared memory and has all but one of them under way.
+//
+// S^T.  A key's row of codes is D / 2 bytes; ldmatrix hands lane (r8, q4) the word
+// of dims 32 j + 8 q4 .. + 7 of key r8: masked, the operands (d0, d4), 16 (d1, d5),
+// (d2, d6), 16 (d3, d7).  The contracted axis may be permuted and scaled as long as
+// Q's side agrees: Q lies as f16 under a power of two per row that brings its largest
+// value to [2^14, 2^15), the odd dims at a sixteenth.  (bf16's 8 bits and f16's 11 fit
+// but for values 2^29 below the row's largest.)  With per-group sums Q_g of what the
+// tensor core sees, scale a - 8 scale Q_g + middle Q_g is the group's part of the
+// score: the product starts at -8 Q_g, the rest is two fused operations a group.
+//
+// O^T.  ldmatrix.trans hands lane (r8, q4) 16-bit pieces of tokens 2 q4, + 1: dims 32
+// j + 4 r8 .. + 3 of both, which masked are operands of one dim (or 16 times it) of
+// two neighbouring tokens, so P^T is needed in the keys' own order and the 16 falls
+// on whole rows of the result.  V's scales go into P: P_g = p scale_g in f16, at most
+// about 2^8 against a running maximum R of score + log2(largest scale of the key); the middles' part,
+// sum p middle_g, is kept in 32 bits per row and group, and so is 8 sum P_g, by a
+// product with a constant operand, from the rounded P_g that the codes were
+// multiplied with: the two cancel as exactly as the codes demand.
+//
+// Codes are finite whatever their bits, so only scores and scales of hidden keys
+// are masked.
+constexpr uint32_t kLoMask = 0x000f000fu, kHiMask = 0x00f000f0u;
+
+template <int D, int NR>
+struct Kv4Cfg {
+    static constexpr int kWarps = NR == 1 ? 12 : 8;
+    static constexpr int KB = kTile * D / 2;             // codes of a K (or V) tile
+    static constexpr int SB = kTile * (D / 64) * 4;      // its scales
+    static constexpr int STAGE = 2 * (KB + SB);
+    static constexpr int kStages = D == 64 ? 4 : NR == 1 ? 2 : 3;   // at most
+    // shared memory of a CTA with `stages`, for B sequences (1008: to a whole pattern)
+    static constexpr int smem(int stages, int B) { return 1008 + kWarps * stages * STAGE + 8 * B; }
+    // One stage less where the sequences' tables want the room.
+    static constexpr int stages(int B) { return smem(kStages, B) <= 232448 - 1024 ? kStages : kStages - 1; }
+    static_assert(smem(kStages - 1, kKvMaxSeqs) <= 232448 - 1024, "shared memory overflow");
+    static_assert(kWarps <= kKv4MaxWarps, "the workspace holds that many workers per SM");
+    static_assert(STAGE % 512 == 0 && KB % 512 == 0, "swizzled tiles start on whole patterns");
+};
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t row_addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(row_addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared_b32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float scale_of(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float middle_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Q's words of the row: eight dims as four pairs; out: the two registers each of the
+// two products of a chunk, and the sum of what they hold.
+template <typename T>
+__device__ __forceinline__ void q_operands(uint4 raw, float up, uint32_t (&b)[4], float &sum) {
+    const float2 a = Cvt<T>::unpack(raw.x), c = Cvt<T>::unpack(raw.y), d = Cvt<T>::unpack(raw.z), e = Cvt<T>::unpack(raw.w);
+    const float od = up * 0.0625f;
+    b[0] = Cvt<__half>::pack(a.x * up, d.x * up);   // dims 0, 4
+    b[1] = Cvt<__half>::pack(a.y * od, d.y * od);   // dims 1, 5
+    b[2] = Cvt<__half>::pack(c.x * up, e.x * up);   // dims 2, 6
+    b[3] = Cvt<__half>::pack(c.y * od, e.y * od);   // dims 3, 7
+    const float2 s0 = Cvt<__half>::unpack(b[0]), s1 = Cvt<__half>::unpack(b[1]), s2 = Cvt<__half>::unpack(b[2]),
+                 s3 = Cvt<__half>::unpack(b[3]);
+    sum += (s0.x + s0.y) + (s2.x + s2.y) + 16.f * ((s1.x + s1.y) + (s3.x + s3.y));
+}
+template <typename T>
+__device__ __forceinline__ float largest(uint4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float m = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 f = Cvt<T>::unpack(w[k]);
+        m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+        if (f.x != f.x || f.y != f.y) m = INFINITY;   // (fmaxf passes NaN over)
+    }
+    return m;
+}
+
+template <int D, int NR, bool kCap>
+__global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
+    kv4_attn_kernel(const __grid_constant__ KvAttnParams p, const __grid_constant__ CUtensorMap map_k,
+                    const __grid_constant__ CUtensorMap map_v) {
+    using C = Kv4Cfg<D, NR>;
+    constexpr int W = C::kWarps, J = D / 32, GR = D / 64, DM = D / 16;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    __shared__ int s_warp[W];
+    __shared__ __align__(8) uint64_t s_bar[W][C::kStages];   // a stage's tile landed
+    __shared__ int s_abort;
+    const int ST = p.stages;
+    const uint32_t tiles = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    int *s_pre = reinterpret_cast<int *>(smem_raw + (tiles - smem_u32(smem_raw)) + W * ST * C::STAGE), *s_len = s_pre + p.B;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int r8 = lane >> 2, q4 = lane & 3;
+
+    if (threadIdx.x == 0) s_abort = 0;
+    if (lane == 0) p.meta[blockIdx.x * W + warp] = make_int4(-1, 0, 0, 0);
+    if (lane < ST) {
+        mbar_init(smem_u32(&s_bar[warp][lane]), 1);
+        fence_mbar_init();
+    }
+    const int per_tile = p.c.Hkv * p.groups;
+    const int total = kv_count<W, D>(p, s_pre, s_len, s_warp, warp, lane) * per_tile;   // (the host keeps it below 2^31)
+    const int wid = blockIdx.x * W + warp;
+    pdl_launch();
+    const KvShare sh(p, wid, total);
+    if (wid >= sh.N || total == 0) return;
+    Cursor pc, end;   // what is loaded next, and where the worker stops
+    {
+        Cursor c;   // even lanes place the one, odd lanes the other
+        kv_place(p, s_pre, s_len, per_tile, lane & 1 ? sh.w1 : sh.w0, c);
+        auto from = [&](int src, Cursor &d) {
+            d.b = __shfl_sync(0xffffffffu, c.b, src), d.hk = __shfl_sync(0xffffffffu, c.hk, src);
+            d.rg = __shfl_sync(0xffffffffu, c.rg, src), d.t = __shfl_sync(0xffffffffu, c.t, src);
+        };
+        from(0, pc);
+        from(1, end);
+        const int t = pc.t;
+        if (pc.b < p.B) pc.open(p, s_len);
+        pc.t = t;
+    }
+    auto at_end = [&](const Cursor &c) -> bool {
+        return c.b == end.b && c.hk == end.hk && c.rg == end.rg && c.t == end.t;
+    };
+    if (at_end(pc)) return;
+    Cursor cc = pc;   // what is computed next
+
+    const uint32_t ring = tiles + warp * (ST * C::STAGE), bars = smem_u32(&s_bar[warp][0]);
+    const WaitCtl wctl{&s_abort, p.c.err, p.budget_ns};
+    const int bw = p.v_block, page16 = p.c.page / 16;
+    auto page_of = [&](int x) -> int { return p.page_magic ? __umulhi((uint32_t)x, p.page_magic) : x; };
+    // page of group (lane % 4) of a tile
+    auto lookup = [&](const Cursor &c) -> int {
+        const int x = 4 * c.t + q4;
+        if (16 * x >= c.n || 16 * x + 16 <= c.lo) return -1;    // a group nobody sees: not read
+        const int page = __ldg(p.c.table + (long long)c.b * p.c.max_pages + page_of(x));
+        if (page < 0 || page >= p.c.num_pages) {
+            atomicOr(p.c.err, kErrBadPage);
+            return -1;
+        }
+        return page;
+    };
+    bool loads = true;      // pc is a tile of this worker's
+    int pg = lookup(pc);
+    uint32_t read = 0u;     // four bits per stage: its 16-key groups that are read
+    int under_way = 0;      // tiles loaded and not yet computed
+    // The tile at pc into stage s: lane 4 i + k copies block i (bw tokens of one page) of
+    // part k (K's codes, V's codes, K's scales, V's), if one of its groups is read.
+    auto load = [&](int s) __attribute__((always_inline)) {
+        if (!loads) return;
+        const uint32_t ok = __ballot_sync(0xffffffffu, pg >= 0) & 15u;   // (also: every lane has read the stage)
+        const int per = bw / 16, blk = lane >> 2, part = lane & 3, first = blk * per;
+        int page = -1, n = 0;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int pgg = __shfl_sync(0xffffffffu, pg, g);
+            if (g >= first && g < first + per) page = max(page, pgg);
+            if (g % per == 0) n += (ok >> g & ((1u << per) - 1u)) != 0u ? 1 : 0;
+        }
+        const uint32_t bar = bars + 8 * s;
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * bw) * (D + 8 * GR));
+        __syncwarp();
+        if (blk < 64 / bw && page >= 0) {
+            const int x = 4 * pc.t + first;
+            const long long row = ((long long)page * p.c.Hkv + pc.hk) * p.c.page + 16 * (x - page_of(x) * page16);
+            const uint32_t st = ring + s * C::STAGE + (part & 1) * C::KB;
+            if (part < 2)
+                tma_load_2d(st + blk * bw * (D / 2), part ? &map_v : &map_k, bar, 0, (int)row);
+            else
+                bulk_load(ring + s * C::STAGE + 2 * C::KB + (part & 1) * C::SB + blk * bw * (4 * GR),
+                          reinterpret_cast<const uint32_t *>(part & 1 ? p.c.v_scale : p.c.k_scale) + row * GR, bw * 4 * GR, bar);
+        }
+        read = (read & ~(15u << (4 * s))) | ok << (4 * s);
+        ++under_way;
+        pc.next(p, s_len);
+        loads = !at_end(pc);
+        if (loads) pg = lookup(pc);
+    };
+#pragma unroll 1
+    for (int s = 0; s < ST; ++s) load(s);
+
+    // ldmatrix: lane l gives the address of row l % 8 of matrix l / 8, matrices being the
+    // 16-byte chunks of eight keys (D = 64: of sixteen).  Chunks lie as the tensor loads
+    // swizzle them: chunk c of row r at c ^ (r / 2 % 4) (64-byte rows), c ^ (r / 4 % 2) (32).
+    const int lr = lane & 7, lm = lane >> 3;
+    const uint32_t lm_at = D == 128 ? lr * 64 + ((lm ^ (lr >> 1)) << 4)
+                                    : ((lm >> 1) * 8 + lr) * 32 + (((lm & 1) ^ (lr >> 2)) << 4);
+
+    // ---- state of the segment being computed: row block nr, row 2 q4 + e of it
+    uint32_t qb[NR][J][4];       // Q's operands
+    float qs[NR][GR][2];         // its sums per group, times 2^-24
+    float fr[NR][2];             // undoes the units and Q's power of two, times c log2(e) (or the cap's factor)
+    int lo_r[NR][2], hi_r[NR][2];   // visible keys
+    int lo_all = 0, hi_all = 0;     // keys every row of the worker sees
+    float acc[NR][DM][4];        // 2^-24 O^T against R: dims 32 (dm / 2) + 4 r8 + 2 (dm % 2), and 16 times the next
+    float eight[NR][GR][4];      // 2^-24 8 sum P_g against R
+    float zc[NR][GR][2];         // the lane's part of sum p middle_g against m_run
+    float m_run[NR][2], l_run[NR][2], R[NR][2];
+    bool fresh = true, begins = false;
+    int s_at = 0;
+    uint32_t phase = 0;   // of stage s_at's barrier
+    while (true) {
+        if (fresh) {
+            lo_all = 0, hi_all = 0x7fffffff;
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) {
+                const int row = (cc.rg * NR + nr) * 8 + r8;
+                const bool live = row < p.Sq * p.G;
+                const int i = live ? row / p.G : p.Sq - 1, g = live ? row % p.G : 0;
+                const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) +
+                                      (((long long)cc.b * p.Sq + i) * p.Hq + cc.hk * p.G + g) * D + 8 * q4;
+                uint4 raw[J];
+                float amax = 0.f;
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    raw[j] = live ? __ldg(reinterpret_cast<const uint4 *>(src + 32 * j)) : make_uint4(0, 0, 0, 0);
+                    amax = fmaxf(amax, p.bf16 ? largest<__nv_bfloat16>(raw[j]) : largest<__half>(raw[j]));
+                }
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 126);
+                const float up = pow2(14 - e), down = pow2(e - 14) * 0x1p24f * (kCap ? p.cap_k : p.scale_log2);
+                float sum[GR];
+#pragma unroll
+                for (int g2 = 0; g2 < GR; ++g2) sum[g2] = 0.f;
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    if (p.bf16) q_operands<__nv_bfloat16>(raw[j], up, qb[nr][j], sum[j / 2]);
+                    else q_operands<__half>(raw[j], up, qb[nr][j], sum[j / 2]);
+                }
+                // a NaN or infinite query: what is left of it is NaN, for its own row only
+                const float dn = amax < INFINITY ? down : NAN;
+                const int hi = cc.n - p.Sq + i;
+#pragma unroll
+                for (int g2 = 0; g2 < GR; ++g2) {
+                    sum[g2] += __shfl_xor_sync(0xffffffffu, sum[g2], 1);
+                    sum[g2] += __shfl_xor_sync(0xffffffffu, sum[g2], 2);
+                }
+#pragma unroll
+                for (int e2 = 0; e2 < 2; ++e2) {   // the rows a lane's scores belong to
+                    const int src_lane = 4 * (2 * q4 + e2);
+                    fr[nr][e2] = __shfl_sync(0xffffffffu, dn, src_lane);
+                    hi_r[nr][e2] = __shfl_sync(0xffffffffu, hi, src_lane);
+                    lo_r[nr][e2] = p.window < 0 ? 0 : max(0, hi_r[nr][e2] - p.window);
+                    lo_all = max(lo_all, lo_r[nr][e2]);
+                    hi_all = min(hi_all, hi_r[nr][e2]);
+                    m_run[nr][e2] = R[nr][e2] = -INFINITY;
+                    l_run[nr][e2] = 0.f;
+#pragma unroll
+                    for (int g2 = 0; g2 < GR; ++g2) {
+                        qs[nr][g2][e2] = __shfl_sync(0xffffffffu, sum[g2], src_lane) * 0x1p-24f;
+                        zc[nr][g2][e2] = 0.f;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                    for (int dm = 0; dm < DM; ++dm) acc[nr][dm][k] = 0.f;
+#pragma unroll
+                    for (int g2 = 0; g2 < GR; ++g2) eight[nr][g2][k] = 0.f;
+                }
+            }
+            lo_all = __reduce_max_sync(0xffffffffu, lo_all);
+            hi_all = __reduce_min_sync(0xffffffffu, hi_all);
+            begins = cc.t == cc.t0;
+            fresh = false;
+        }
+        if (!mbar_wait_warp(bars + 8 * s_at, phase, wctl)) break;
+        const uint32_t kt = ring + s_at * C::STAGE, vt = kt + C::KB;
+        const uint32_t ks_at = kt + 2 * C::KB + r8 * (4 * GR), vs_at = ks_at + C::SB;
+        const uint32_t ok = read >> (4 * s_at) & 15u;
+        // ---- S^T = K Q^T, per 16 keys: scores of keys 16 t + r8 (+ 8), rows 2 q4, + 1
+        float x[NR][4][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            uint32_t w[2][J];   // key r8, key r8 + 8: the words of chunk j
+            if constexpr (D == 128) {
+                ldmatrix_x4(kt + (2 * t) * 512 + lm_at, w[0]);
+                ldmatrix_x4(kt + (2 * t + 1) * 512 + lm_at, w[1]);
+            } else {
+                uint32_t r[4];
+                ldmatrix_x4(kt + t * 512 + lm_at, r);
+                w[0][0] = r[0], w[0][1] = r[1], w[1][0] = r[2], w[1][1] = r[3];
+            }
+            float a[NR][GR][4];
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                for (int g = 0; g < GR; ++g)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) a[nr][g][k] = -8.f * qs[nr][g][k & 1];
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t u = w[0][j] >> (8 * h), v = w[1][j] >> (8 * h);
+                    const uint32_t A[4] = {u & kLoMask, v & kLoMask, u & kHiMask, v & kHiMask};
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr) mma_f16(a[nr][j / 2], A, qb[nr][j][2 * h], qb[nr][j][2 * h + 1]);
+                }
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                uint32_t sm[GR];
+#pragma unroll
+                for (int g = 0; g < GR; ++g) sm[g] = ld_shared_b32(ks_at + (16 * t + 8 * hh) * (4 * GR) + 4 * g);
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float y = middle_of(sm[0]) * qs[nr][0][e];
+                        y = fmaf(scale_of(sm[0]), a[nr][0][2 * hh + e], y);
+#pragma unroll
+                        for (int g = 1; g < GR; ++g) {
+                            y = fmaf(middle_of(sm[g]), qs[nr][g][e], y);
+                            y = fmaf(scale_of(sm[g]), a[nr][g][2 * hh + e], y);
+                        }
+                        x[nr][t][2 * hh + e] = y * fr[nr][e];
+                    }
+            }
+        }
+        // ---- softmax, and V's scales
+        const int key0 = kTile * cc.t + r8;   // the lane's keys: key0 + 8 u
+        const bool ends = cc.t + 1 == cc.t1;
+        // a tile inside every row's keys, all its pages read, takes no compare
+        const bool edge = ok != 15u || kTile * cc.t < lo_all || kTile * cc.t + kTile - 1 > hi_all;
+        uint32_t vsm[8][GR];   // (scale, middle) of V, 0 for keys nobody sees
+        float ev[8];           // log2 of the larger scale
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const bool off = edge && (!(ok >> (u >> 1) & 1u) || key0 + 8 * u >= cc.n || key0 + 8 * u < cc.lo);
+            float top = 0.f;
+#pragma unroll
+            for (int g = 0; g < GR; ++g) {
+                vsm[u][g] = ld_shared_b32(vs_at + 8 * u * (4 * GR) + 4 * g);
+                if (off) vsm[u][g] = 0u;
+                top = fmaxf(top, scale_of(vsm[u][g]));
+            }
+            ev[u] = lg2_approx(top);
+        }
+        auto scores = [&](auto edge_tag, int nr, float (&mx)[2], float (&my)[2]) __attribute__((always_inline)) {
+            constexpr bool kEdge = decltype(edge_tag)::value;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                float *y = &x[nr][u >> 1][2 * (u & 1)];
+                const int key = key0 + 8 * u;
+                const bool gone = kEdge && !(ok >> (u >> 1) & 1u);
+                const bool off0 = kEdge && (gone || key < lo_r[nr][0] || key > hi_r[nr][0]);
+                const bool off1 = kEdge && (gone || key < lo_r[nr][1] || key > hi_r[nr][1]);
+                if (kCap) {
+                    // what lies behind the last token may be NaN: not into the pair
+                    if (off0) y[0] = 0.f;
+                    if (off1) y[1] = 0.f;
+                    float r0, r1;
+                    cap_r2(y[0], y[1], r0, r1);
+                    y[0] = fmaf(-2.f * p.cap_log2, r0, p.cap_log2);
+                    y[1] = fmaf(-2.f * p.cap_log2, r1, p.cap_log2);
+                }
+                if (off0) y[0] = -INFINITY;
+                if (off1) y[1] = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mx[e] = fmaxf(mx[e], y[e]);
+                    my[e] = fmaxf(my[e], y[e] + ev[u]);
+                }
+            }
+        };
+        uint32_t pt[NR][GR][8];   // P_g^T blocks, transposed: the B operands of O^T
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+            float mx[2] = {-INFINITY, -INFINITY}, my[2] = {-INFINITY, -INFINITY};
+            if (edge) scores(std::true_type{}, nr, mx, my);
+            else scores(std::false_type{}, nr, mx, my);
+            float mref[2], fv[2], grow[2];
+            bool any_grow = false;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float m = fmaxf(m_run[nr][e], keys_max(mx[e])), y = keys_max(my[e]);
+                mref[e] = m == -INFINITY ? 0.f : m;
+                const float shrink = ex2(m_run[nr][e] - mref[e]);   // -inf before the first key: 0
+                l_run[nr][e] *= shrink;
+#pragma unroll
+                for (int g = 0; g < GR; ++g) zc[nr][g][e] *= shrink;
+                m_run[nr][e] = m;
+                grow[e] = 1.f;
+                if (y > R[nr][e] + kLazy || (R[nr][e] == -INFINITY && y > R[nr][e])) {
+                    grow[e] = ex2(R[nr][e] - y);
+                    R[nr][e] = y;
+                    any_grow = true;
+                }
+                fv[e] = R[nr][e] == -INFINITY ? 0.f : ex2(mref[e] - R[nr][e]);   // no weight yet: P = 0
+            }
+            if (__any_sync(0xffffffffu, any_grow)) {
+                const uint64_t g2 = f2_pack(grow[0], grow[1]);
+                auto times = [&](float (&v)[4]) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int k = 0; k < 4; k += 2) {
+                        const float2 y = f2_unpack(f2_mul(f2_pack(v[k], v[k + 1]), g2));
+                        v[k] = y.x, v[k + 1] = y.y;
+                    }
+                };
+#pragma unroll
+                for (int dm = 0; dm < DM; ++dm) times(acc[nr][dm]);
+#pragma unroll
+                for (int g = 0; g < GR; ++g) times(eight[nr][g]);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                float pp[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    pp[e] = ex2(x[nr][u >> 1][2 * (u & 1) + e] - mref[e]);
+                    l_run[nr][e] += pp[e];
+#pragma unroll
+                    for (int g = 0; g < GR; ++g) zc[nr][g][e] = fmaf(pp[e], middle_of(vsm[u][g]), zc[nr][g][e]);
+                    pp[e] *= fv[e];
+                }
+#pragma unroll
+                for (int g = 0; g < GR; ++g) {
+                    const float s = scale_of(vsm[u][g]);
+                    pt[nr][g][u] = transpose8(Cvt<__half>::pack(pp[0] * s, pp[1] * s));
+                }
+            }
+        }
+        // ---- O^T += V^T P^T, per 16 tokens
+        constexpr uint32_t kEight[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            uint32_t w[2][J];   // tokens 2 q4, + 1 and 8 further: dims 32 j + 4 r8 ..
+            if constexpr (D == 128) {
+                ldmatrix_x4_trans(vt + (2 * t) * 512 + lm_at, w[0][0], w[0][1], w[0][2], w[0][3]);
+                ldmatrix_x4_trans(vt + (2 * t + 1) * 512 + lm_at, w[1][0], w[1][1], w[1][2], w[1][3]);
+            } else {
+                ldmatrix_x4_trans(vt + t * 512 + lm_at, w[0][0], w[0][1], w[1][0], w[1][1]);
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t u = w[0][j] >> (8 * h), v = w[1][j] >> (8 * h);
+                    const uint32_t A[4] = {u & kLoMask, u & kHiMask, v & kLoMask, v & kHiMask};
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr)
+                        mma_f16(acc[nr][2 * j + h], A, pt[nr][j / 2][2 * t], pt[nr][j / 2][2 * t + 1]);
+                }
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                for (int g = 0; g < GR; ++g) mma_f16(eight[nr][g], kEight, pt[nr][g][2 * t], pt[nr][g][2 * t + 1]);
+        }
+        --under_way;
+        load(s_at);
+        if (++s_at == ST) s_at = 0, phase ^= 1u;
+        Cursor nx = cc;
+        nx.next(p, s_len);
+        const bool done = at_end(nx);
+        if (ends || done) {
+            // the rows' results, or the piece's for the join
+            const int hk = cc.hk, rg = cc.rg, seg = hk * p.groups + rg;
+            const bool whole = begins && ends;
+            if (!begins && lane == 0) {
+                // piece 0, of a segment begun before: whose first tile's holder
+                const int unit0 = (cc.b > 0 ? s_pre[cc.b - 1] : 0) * per_tile + seg * kv_units(cc.t1 - cc.t0);
+                p.meta[wid] = make_int4(seg, cc.b, sh.worker_of(unit0 + 2), ends ? 1 : 0);
+            }
+            const long long at = (long long)wid * 2 + (begins ? 1 : 0);
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) {
+                const int row0 = (rg * NR + nr) * 8;
+                float f[2], z[GR][2], out[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float l = keys_sum(l_run[nr][e]);
+                    // what brings acc from R to m
+                    f[e] = R[nr][e] == -INFINITY ? 0.f : ex2(R[nr][e] - m_run[nr][e]);
+                    out[e] = whole ? out_factor(0.f, 0.f, l) : 1.f;
+#pragma unroll
+                    for (int g = 0; g < GR; ++g) z[g][e] = keys_sum(zc[nr][g][e]) * out[e];
+                    f[e] *= out[e];
+                    const int row = row0 + 2 * q4 + e;
+                    if (r8 == 0 && row < p.Sq * p.G) {
+                        if (!whole)
+                            p.stat[at * (NR * 8) + nr * 8 + 2 * q4 + e] = make_float4(m_run[nr][e], l, m_run[nr][e], 0.f);
+                        else if (p.lse)
+                            p.lse[((long long)cc.b * p.Hq + hk * p.G + row % p.G) * p.Sq + row / p.G] =
+                                lse_of(m_run[nr][e], l);
+                    }
+                }
+#pragma unroll
+                for (int dm = 0; dm < DM; ++dm) {
+                    float o[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float a = (k < 2 ? acc[nr][dm][k] : acc[nr][dm][k] * 0.0625f) - eight[nr][dm / 4][k & 1];
+                        o[k] = fmaf(a * 0x1p24f, f[k & 1], z[dm / 4][k & 1]);
+                    }
+                    if (whole) {
+                        if (p.bf16) store_rows<D, __nv_bfloat16, true>(p, cc.b, hk, row0, lane, o, dm);
+                        else store_rows<D, __half, true>(p, cc.b, hk, row0, lane, o, dm);
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(p.acc + at * (NR * 8 * D) + nr * 8 * D) + lane;
+                        dst[32 * dm] = make_float4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+            }
+            fresh = true;
+        }
+        if (done) return;
+        cc = nx;
+    }
+    // a wait ran out: the copies in flight land before the CTA's memory goes
+    for (int i = 0; i < under_way; ++i) {
+        mbar_wait_drain_warp(bars + 8 * s_at, phase, p.c.err, p.budget_ns);
+        if (++s_at == ST) s_at = 0, phase ^= 1u;
+    }
+}
+
+template <int D, int NR, bool kCap>
+cudaError_t launch_attn(KvAttnParams p, const CUtensorMap &mk, const CUtensorMap &mv, int sms, cudaStream_t stream) {
+    using C = Kv4Cfg<D, NR>;
+    auto kern = kv4_attn_kernel<D, NR, kCap>;
+    p.stages = C::stages(p.B);
+    const int smem = C::smem(p.stages, p.B);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int grid = sms < kKvSms ? sms : kKvSms;
+    p.workers = grid * C::kWarps;
+    p.groups = (p.G * p.Sq + 8 * NR - 1) / (8 * NR);
+    // x / (page / 16) as a product: exact for x below 2^29 and divisors up to 8
+    const uint32_t d = (uint32_t)p.c.page / 16;
+    p.page_magic = d > 1 ? (uint32_t)((1ull << 32) / d + 1) : 0u;
+    kern<<<grid, C::kWarps * 32, smem, stream>>>(p, mk, mv);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return p.bf16 ? launch_join<D, NR, __nv_bfloat16, true>(p, stream) : launch_join<D, NR, __half, true>(p, stream);
+}
+
+template <int D>
+cudaError_t launch_attn_d(const KvAttnParams &p, const CUtensorMap &mk, const CUtensorMap &mv, int sms, cudaStream_t stream) {
+    const bool cap = p.cap_log2 > 0.f;
+    if (p.G * p.Sq <= 8)
+        return cap ? launch_attn<D, 1, true>(p, mk, mv, sms, stream) : launch_attn<D, 1, false>(p, mk, mv, sms, stream);
+    return cap ? launch_attn<D, 2, true>(p, mk, mv, sms, stream) : launch_attn<D, 2, false>(p, mk, mv, sms, stream);
+}
+
+// Rows of a CTA whose rows have `per_row` items: about four a thread, one row where
+// there are few.
+int rows_per_cta(int rows, long long per_row, int threads) {
+    const long long n = 4 * threads / per_row, most = rows / 608;
+    const long long m = n < most ? n : most;
+    return (int)(m < 1 ? 1 : m > kMaxRows ? kMaxRows : m);
+}
+
+template <int D, typename T>
+cudaError_t launch_append_t(const KvAppendParams &p, cudaStream_t stream) {
+    const int per = rows_per_cta(p.rows, 2LL * p.c.Hkv * (D / 8), kAppend);
+    kv4_append_kernel<D, T><<<(p.rows + per - 1) / per, kAppend, 0, stream>>>(p, per);
+    return cudaGetLastError();
+}
+template <int D, typename T>
+cudaError_t launch_read_t(const KvReadParams &p, cudaStream_t stream) {
+    const int per = rows_per_cta(p.rows, 2LL * p.c.Hkv * (D / 16), kRead);
+    kv4_read_kernel<D, T><<<(p.rows + per - 1) / per, kRead, 0, stream>>>(p, per);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_append(const KvAppendParams &p, int D, int bf16, cudaStream_t stream) {
+    if (D == 128)
+        return bf16 ? launch_append_t<128, __nv_bfloat16>(p, stream) : launch_append_t<128, __half>(p, stream);
+    return bf16 ? launch_append_t<64, __nv_bfloat16>(p, stream) : launch_append_t<64, __half>(p, stream);
+}
+
+cudaError_t launch_kv4_read(const KvReadParams &p, int D, int bf16, cudaStream_t stream) {
+    if (D == 128) return bf16 ? launch_read_t<128, __nv_bfloat16>(p, stream) : launch_read_t<128, __half>(p, stream);
+    return bf16 ? launch_read_t<64, __nv_bfloat16>(p, stream) : launch_read_t<64, __half>(p, stream);
+}
+
+cudaError_t launch_kv4_attn(const KvAttnParams &p, const CUtensorMap &mk, const CUtensorMap &mv, int D, int sms,
+                            cudaStream_t stream) {
+    return D == 128 ? launch_attn_d<128>(p, mk, mv, sms, stream) : launch_attn_d<64>(p, mk, mv, sms, stream);
+}
+
+}  // namespace fa

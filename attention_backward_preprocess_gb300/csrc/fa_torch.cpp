@@ -254,15 +254,54 @@ PyObject *cache(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-const fa_kv_cache *cache_struct(PyObject *o) {
-    return reinterpret_cast<const fa_kv_cache *>(PyLong_AsUnsignedLongLong(o));
+// cache4(k, v, k_scale, v_scale, block_table) -> True if they make a 4-bit cache on the current device
+PyObject *cache4(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (n != 5) return none();
+    return guarded([&]() -> PyObject * {
+        const at::Tensor *t[5];
+        for (int i = 0; i < 5; ++i)
+            if (!(t[i] = tensor(a[i]))) return none();
+        const int dev = current();
+        if (t[0]->dim() != 4 || t[4]->dim() != 2) return none();
+        const int64_t P = t[0]->size(0), H = t[0]->size(1), ps = t[0]->size(2), D = 2 * t[0]->size(3);
+        if (D % 64 != 0 || !plain(*t[0], at::kByte, dev) || !plain(*t[1], at::kByte, dev) ||
+            !plain(*t[2], at::kBFloat16, dev) || !plain(*t[3], at::kBFloat16, dev) || !plain(*t[4], at::kInt, dev))
+            return none();
+        if (t[1]->sizes() != t[0]->sizes() || t[2]->sizes() != at::IntArrayRef({P, H, ps, D / 64, 2}) ||
+            t[3]->sizes() != t[2]->sizes())
+            return none();
+        Py_RETURN_TRUE;
+    });
 }
 
-// append(cache struct's address, B, device, cache_len, k_new, v_new, cu_new, max_new) -> status
-PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
+// A cache's struct by its address (both caches' structs begin alike; Cache says which).
+template <typename Cache> const Cache *cache_struct(PyObject *o) {
+    return reinterpret_cast<const Cache *>(PyLong_AsUnsignedLongLong(o));
+}
+fa_status call_append(const fa_kv_cache *c, const int *len, const void *k, const void *v, const int *cu, int rows, int B,
+                      int max_new, fa_dtype t, cudaStream_t s) {
+    return fa_kvcache_append(c, len, k, v, cu, rows, B, max_new, t, s);
+}
+fa_status call_append(const fa_kv_cache4 *c, const int *len, const void *k, const void *v, const int *cu, int rows, int B,
+                      int max_new, fa_dtype t, cudaStream_t s) {
+    return fa_kvcache4_append(c, len, k, v, cu, rows, B, max_new, t, s);
+}
+size_t attend_bytes(const fa_kv_cache *c) { return fa_fwd_kvcache_workspace_bytes(c->D); }
+size_t attend_bytes(const fa_kv_cache4 *c) { return fa_fwd_kvcache4_workspace_bytes(c->D); }
+fa_status call_attend(const void *q, const fa_kv_cache *c, const int *len, void *o, float *lse, int B, int Sq, int Hq,
+                      float scale, float cap, int window, fa_dtype t, void *ws, size_t bytes, cudaStream_t s) {
+    return fa_fwd_kvcache(q, c, len, o, lse, B, Sq, Hq, scale, cap, window, t, ws, bytes, s);
+}
+fa_status call_attend(const void *q, const fa_kv_cache4 *c, const int *len, void *o, float *lse, int B, int Sq, int Hq,
+                      float scale, float cap, int window, fa_dtype t, void *ws, size_t bytes, cudaStream_t s) {
+    return fa_fwd_kvcache4(q, c, len, o, lse, B, Sq, Hq, scale, cap, window, t, ws, bytes, s);
+}
+
+// (cache struct's address, B, device, cache_len, k_new, v_new, cu_new, max_new) -> status
+template <typename Cache> PyObject *append_to(PyObject *const *a, Py_ssize_t n) {
     if (n != 8) return none();
     return guarded([&]() -> PyObject * {
-        const fa_kv_cache *kc = cache_struct(a[0]);
+        const Cache *kc = cache_struct<Cache>(a[0]);
         const long B = PyLong_AsLong(a[1]), dev = PyLong_AsLong(a[2]);
         const at::Tensor *len = tensor(a[3]), *k = tensor(a[4]), *v = tensor(a[5]);
         const at::Tensor *cu = a[6] == Py_None ? nullptr : tensor(a[6]);
@@ -285,17 +324,19 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         }
         const int64_t rows = cu ? k->size(0) : (int64_t)B * max_new;
         if (max_new <= 0 || max_new > 0x7fffffffL || rows <= 0 || rows > 0x7fffffffL) return none();
-        return PyLong_FromLong(fa_kvcache_append(kc, (const int *)len->data_ptr(), k->data_ptr(), v->data_ptr(),
-                                                 cu ? (const int *)cu->data_ptr() : nullptr, (int)rows, (int)B, (int)max_new,
-                                                 ty == at::kBFloat16 ? FA_BF16 : FA_FP16, stream((int)dev)));
+        return PyLong_FromLong(call_append(kc, (const int *)len->data_ptr(), k->data_ptr(), v->data_ptr(),
+                                           cu ? (const int *)cu->data_ptr() : nullptr, (int)rows, (int)B, (int)max_new,
+                                           ty == at::kBFloat16 ? FA_BF16 : FA_FP16, stream((int)dev)));
     });
 }
+PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) { return append_to<fa_kv_cache>(a, n); }
+PyObject *append4(PyObject *, PyObject *const *a, Py_ssize_t n) { return append_to<fa_kv_cache4>(a, n); }
 
-// attend(cache struct's address, B, device, q, cache_len, scale, softcap, window_left) -> (o, lse)
-PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
+// (cache struct's address, B, device, q, cache_len, scale, softcap, window_left) -> (o, lse)
+template <typename Cache> PyObject *attend_over(PyObject *const *a, Py_ssize_t n) {
     if (n != 8) return none();
     return guarded([&]() -> PyObject * {
-        const fa_kv_cache *kc = cache_struct(a[0]);
+        const Cache *kc = cache_struct<Cache>(a[0]);
         const long B = PyLong_AsLong(a[1]), dev = PyLong_AsLong(a[2]);
         const at::Tensor *q = tensor(a[3]), *len = tensor(a[4]);
         if (PyErr_Occurred() || !q || !len || dev != current()) return none();
@@ -308,21 +349,95 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const float cap = (float)PyFloat_AsDouble(a[6]);
         const long window = PyLong_AsLong(a[7]);
         if (PyErr_Occurred() || window > 0x7fffffffL || window < -0x7fffffffL) return none();
-        const size_t bytes = fa_fwd_kvcache_workspace_bytes(kc->D);
+        const size_t bytes = attend_bytes(kc);
         if (bytes == 0) return none();
         at::Tensor o = at::empty(q->sizes(), q->options());
         at::Tensor lse = at::empty({q->size(0), q->size(2), q->size(1)}, q->options().dtype(at::kFloat));
         at::Tensor ws = at::empty({(int64_t)bytes}, q->options().dtype(at::kByte));
         const fa_status st =
-            fa_fwd_kvcache(q->data_ptr(), kc, (const int *)len->data_ptr(), o.data_ptr(), (float *)lse.data_ptr(),
-                           (int)B, (int)q->size(1), (int)q->size(2), scale, cap, (int)window,
-                           ty == at::kBFloat16 ? FA_BF16 : FA_FP16, ws.data_ptr(), bytes, stream((int)dev));
+            call_attend(q->data_ptr(), kc, (const int *)len->data_ptr(), o.data_ptr(), (float *)lse.data_ptr(), (int)B,
+                        (int)q->size(1), (int)q->size(2), scale, cap, (int)window,
+                        ty == at::kBFloat16 ? FA_BF16 : FA_FP16, ws.data_ptr(), bytes, stream((int)dev));
         return st == FA_OK ? pair(std::move(o), std::move(lse)) : PyLong_FromLong(st);
     });
 }
+PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) { return attend_over<fa_kv_cache>(a, n); }
+PyObject *attend4(PyObject *, PyObject *const *a, Py_ssize_t n) { return attend_over<fa_kv_cache4>(a, n); }
+
+// read4(cache struct's address, B, device, cache_len, cu_rows, rows, bf16, first) -> (k, v)
+PyObject *read4(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (n != 8) return none();
+    return guarded([&]() -> PyObject * {
+        const fa_kv_cache4 *kc = cache_struct<fa_kv_cache4>(a[0]);
+        const long B = PyLong_AsLong(a[1]), dev = PyLong_AsLong(a[2]), rows = PyLong_AsLong(a[5]);
+        const at::Tensor *len = tensor(a[3]), *cu = tensor(a[4]), *first = a[7] == Py_None ? nullptr : tensor(a[7]);
+        if (PyErr_Occurred() || !len || !cu || (!first && a[7] != Py_None) || dev != current()) return none();
+        auto fits = [&](const at::Tensor *t, int64_t n) {
+            return !t || (plain(*t, at::kInt, (int)dev) && t->dim() == 1 && t->size(0) == n);
+        };
+        if (!fits(len, B) || !fits(cu, B + 1) || !fits(first, B)) return none();
+        if (rows <= 0 || rows > 0x7fffffffL) return none();
+        const bool bf16 = a[6] == Py_True;
+        const auto opt = at::TensorOptions().dtype(bf16 ? at::kBFloat16 : at::kHalf).device(at::kCUDA, (int)dev);
+        at::Tensor k = at::empty({rows, kc->Hkv, kc->D}, opt), v = at::empty({rows, kc->Hkv, kc->D}, opt);
+        const fa_status st = fa_kvcache4_read(kc, (const int *)len->data_ptr(), first ? (const int *)first->data_ptr() : nullptr,
+                                              (const int *)cu->data_ptr(), (int)rows, (int)B, k.data_ptr(), v.data_ptr(),
+                                              bf16 ? FA_BF16 : FA_FP16, stream((int)dev));
+        return st == FA_OK ? pair(std::move(k), std::move(v)) : PyLong_FromLong(st);
+    });
+}
+
+// rope(q, k or None, steps, factor, positions, offsets, interleaved, inverse) -> (q, k) turned, k None without one
+PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (n != 8) return none();
+    return guarded([&]() -> PyObject * {
+        const at::Tensor *x[2] = {tensor(a[0]), a[1] == Py_None ? nullptr : tensor(a[1])}, *steps = tensor(a[2]);
+        const at::Tensor *pos = a[4] == Py_None ? nullptr : tensor(a[4]), *off = a[5] == Py_None ? nullptr : tensor(a[5]);
+        if (!x[0] || (!x[1] && a[1] != Py_None) || !steps || (!pos && a[4] != Py_None) || (!off && a[5] != Py_None))
+            return none();
+        const float factor = (float)PyFloat_AsDouble(a[3]);
+        if (PyErr_Occurred() || !x[0]->is_cuda() || x[0]->dim() != 4) return none();
+        const int dev = x[0]->get_device();
+        const at::ScalarType ty = x[0]->scalar_type();
+        const int64_t B = x[0]->size(0), S = x[0]->size(1), D = x[0]->size(3);
+        if (dev != current() || (ty != at::kBFloat16 && ty != at::kHalf) || B > 0x7fffffff || S > 0x7fffffff ||
+            !plain(*steps, at::kLong, dev) || steps->dim() != 1 || steps->size(0) > 0x3fffffff)
+            return none();
+        if (pos && (!plain(*pos, at::kInt, dev) || pos->sizes() != at::IntArrayRef({B, S}))) return none();
+        if (off && (!plain(*off, at::kInt, dev) || off->sizes() != at::IntArrayRef({B}))) return none();
+        fa_rope_tensor t[2];
+        std::memset(t, 0, sizeof(t));
+        at::Tensor out[2];
+        for (int i = 0; i < 2 && x[i]; ++i) {
+            if (!x[i]->is_cuda() || x[i]->get_device() != dev || x[i]->scalar_type() != ty || x[i]->dim() != 4 ||
+                x[i]->size(0) != B || x[i]->size(1) != S || x[i]->size(3) != D || x[i]->numel() == 0 ||
+                x[i]->size(2) > 0x7fffffff || !strides(*x[i], t[i].in_stride))
+                return none();
+            out[i] = at::empty(x[i]->sizes(), x[i]->options());
+            t[i].in = x[i]->data_ptr();
+            t[i].out = out[i].data_ptr();
+            t[i].heads = (int)x[i]->size(2);
+        }
+        const fa_status st = fa_rope(&t[0], x[1] ? &t[1] : nullptr, (int)B, (int)S, (int)D, 2 * (int)steps->size(0),
+                                     (const unsigned long long *)steps->data_ptr(), factor, PyObject_IsTrue(a[6]),
+                                     PyObject_IsTrue(a[7]), pos ? (const int *)pos->data_ptr() : nullptr,
+                                     off ? (const int *)off->data_ptr() : nullptr,
+                                     ty == at::kBFloat16 ? FA_BF16 : FA_FP16, stream(dev));
+        if (st != FA_OK) return PyLong_FromLong(st);
+        if (x[1]) return pair(std::move(out[0]), std::move(out[1]));
+        PyObject *r = PyTuple_New(2);
+        if (!r) return nullptr;
+        PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(out[0])));
+        Py_INCREF(Py_None);
+        PyTuple_SET_ITEM(r, 1, Py_None);
+        return r;
+    });
+}
+
 
 #define FN(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FN(agree), FN(fwd), FN(bwd), FN(mask_ranges), FN(cache), FN(append), FN(attend), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {FN(agree), FN(fwd), FN(bwd), FN(mask_ranges), FN(cache), FN(append), FN(attend),
+                         FN(cache4), FN(append4), FN(attend4), FN(read4), FN(rope), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fa_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -410,6 +410,115 @@ fa_status fa_fwd_kvcache(const void *q, const fa_kv_cache *cache, const int *cac
                          int window_left, fa_dtype dtype, void *workspace, size_t workspace_bytes,
                          cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The 4-bit paged cache: the same pages and block table with values in four
+ * bits, for contexts that 8 bits would not let fit.  Both K and V lie token by
+ * token:
+ *   k, v               [num_pages, Hkv, page_size, D / 2]   16-byte aligned; dim 2i
+ *                      of a token in the low four bits of byte i, dim 2i + 1 in the high
+ *   k_scale, v_scale   bf16 [num_pages, Hkv, page_size, D / 64, 2]   16-byte aligned:
+ *                      (scale, middle) of 64 neighbouring dims of a token
+ * A code c in 0 .. 15 stands for middle + scale (c - 8): 4.5 bits a value.  A cache
+ * filled in another way may have any middles and any scales that are 0 or between
+ * 2^-100 and 2^100.  page_size, D, the table, ownership, capture into CUDA graphs,
+ * what is found on the device and how it is reported: as for the 8-bit cache, but
+ * that every token is written by itself, so that a page's other tokens, and rows
+ * behind the last sequence's, are left as they were.
+ *
+ * fa_kvcache4_append: arguments as fa_kvcache_append.  Of the 64 values x of a group,
+ * in 32-bit operations each rounded to nearest,
+ *   middle = lo / 2 + hi / 2, rounded to bf16, for the least and largest x;
+ *   scale  = max(hi - middle, middle - lo) * (2 / 15), rounded up to bf16, at least 2^-60;
+ *   code   = clamp(nearest even whole number of (x - middle) * (1 / scale), -8, 7) + 8,
+ * so that a value is off by at most half a scale, but for what those roundings add.  A group with a
+ * NaN or an infinity has the middle NaN, the scale 2^-60 and all codes 8: it reads as NaN.
+ *
+ * fa_fwd_kvcache4: arguments and results as fa_fwd_kvcache.
+ *
+ * fa_kvcache4_read writes tokens of the cache out as 16-bit values, for the dense
+ * attention of a prompt's next chunk (fa_fwd with cu_seqlens) or for another cache.
+ * Rows cu_rows[b] .. cu_rows[b + 1] (device int32 [B + 1]) of k_out and v_out [rows,
+ * Hkv, D] become sequence b's tokens first[b], first[b] + 1, .. (first: device int32
+ * [B], NULL: 0).  Tokens must be held: a sequence with first[b] < 0 or more rows than
+ * cache_len[b] - first[b] is left alone and reported, as are rows on a bad page.
+ * Values are rounded to the output's type once from 32 bits.
+ *
+ * Errors: as the 8-bit calls; fa_fwd_kvcache4 counts a cache's (page, head, token)
+ * rows, which must stay below 2^31.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    void *k, *v;
+    void *k_scale, *v_scale;
+    const int *block_table;
+    int num_pages, page_size, max_pages, Hkv, D;
+} fa_kv_cache4;
+
+fa_status fa_kvcache4_append(const fa_kv_cache4 *cache, const int *cache_len, const void *k_new,
+                             const void *v_new, const int *cu_new, int rows, int B, int max_new,
+                             fa_dtype dtype, cudaStream_t stream);
+
+fa_status fa_kvcache4_read(const fa_kv_cache4 *cache, const int *cache_len, const int *first,
+                           const int *cu_rows, int rows, int B, void *k_out, void *v_out,
+                           fa_dtype dtype, cudaStream_t stream);
+
+size_t fa_fwd_kvcache4_workspace_bytes(int D);
+fa_status fa_fwd_kvcache4(const void *q, const fa_kv_cache4 *cache, const int *cache_len, void *o,
+                          float *lse, int B, int Sq, int Hq, float softmax_scale, float softcap,
+                          int window_left, fa_dtype dtype, void *workspace, size_t workspace_bytes,
+                          cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions: what turns q and k before attention, or before k enters a cache.
+ * The first rotary_dim dims of every head (even, at most D) are rotary_dim / 2 pairs,
+ * dims i and i + rotary_dim / 2, or with interleaved != 0 dims 2i and 2i + 1.  Pair i
+ * of the row at position p is turned by the angle p w_i:
+ *   a' = factor (a cos - b sin),  b' = factor (b cos + a sin);
+ * the other dims are copied.  inverse != 0 turns by -p w_i, times the same factor: the
+ * gradient of the call with inverse = 0.
+ *
+ * Frequencies.  steps (device, rotary_dim / 2 of them) are w_i / (2 pi), parts of a
+ * turn per position, in 2^-64ths: p steps[i] modulo 2^64 is the angle, to 2^-32 of a
+ * turn however far the position.  fa_rope_steps makes them on the host from radians
+ * per position (finite, 0 <= w < 1024).  fa_rope_frequencies makes those: base^(-2i /
+ * rotary_dim), scaled for contexts of `scale` times the trained length by
+ *   FA_ROPE_LINEAR  w / scale (position interpolation);
+ *   FA_ROPE_NTK     base scale^(rotary_dim / (rotary_dim - 2)) for base;
+ *   FA_ROPE_YARN    (YaRN, Peng et al. 2023) w (1 - g) / scale + w g with g = (r - beta_slow) /
+ *                   (beta_fast - beta_slow) held in [0, 1], r = trained_len w / (2 pi);
+ *                   *factor = 0.1 ln(scale) + 1 (1 for the others).
+ *
+ * fa_rope works on q, and on k where it is not NULL, in one launch.  A tensor is
+ * [B, S, heads, D] with D contiguous and (batch, row, head) strides in elements (all
+ * three zero: contiguous; otherwise positive multiples of 8 below 2^39), 16-byte
+ * aligned; out may be in with the same strides, and must not overlap it otherwise.
+ * Packed rows are B = 1, S = rows.  The position of row s of sequence b is
+ * positions[b S + s] (device int32), or offsets[b] + s (device int32 [B]), or s, with
+ * both NULL; giving both is an error.  Positions may be negative.
+ *
+ * Errors: FA_ERR_INVALID_ARG for null or misaligned pointers, sizes, strides, factor
+ * (finite), an odd rotary_dim or one above D; FA_ERR_UNSUPPORTED for D that is no multiple of 8
+ * or above 256, for dtype, for 2^31 rows or more and 2^15 heads or more.
+ * ------------------------------------------------------------------------- */
+#define FA_ROPE_NONE 0
+#define FA_ROPE_LINEAR 1
+#define FA_ROPE_NTK 2
+#define FA_ROPE_YARN 3
+
+typedef struct {
+    const void *in;
+    void *out;
+    int heads;
+    long long in_stride[3], out_stride[3];
+} fa_rope_tensor;
+
+fa_status fa_rope_frequencies(int rotary_dim, double base, int scaling, double scale, double trained_len,
+                              double beta_fast, double beta_slow, double *w, double *factor);
+fa_status fa_rope_steps(const double *w, int n, unsigned long long *steps);
+
+fa_status fa_rope(const fa_rope_tensor *q, const fa_rope_tensor *k, int B, int S, int D, int rotary_dim,
+                  const unsigned long long *steps, float factor, int interleaved, int inverse,
+                  const int *positions, const int *offsets, fa_dtype dtype, cudaStream_t stream);
+
 /* CUDA graphs.  A backward call that issues only launches and memsets on
  * `stream` can be captured into a CUDA graph and replayed: fa_bwd_ext /
  * fa_bwd_with_workspace with a caller workspace for dense problems, and for
