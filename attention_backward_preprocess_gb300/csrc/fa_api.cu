@@ -848,11 +848,11 @@ fa_status check_kv_append(const int *cache_len, const void *k_new, const void *v
     return FA_OK;
 }
 
-// An attention over a cache of `value_rows` rows a tensor load counts: the arguments
-// that do not depend on how the values are held.
+// An attention over a cache of `value_rows` rows a tensor load counts, a segment's opening
+// counted as `open` half tiles: the arguments that do not depend on how the values are held.
 fa_status check_kv_attn(const void *q, const int *cache_len, void *o, float *lse, int B, int Sq, int Hq, int page_size,
                         int D, float softmax_scale, float softcap, int window_left, const void *workspace,
-                        size_t workspace_bytes, size_t need, long long value_rows, fa::KvAttnParams *p) {
+                        size_t workspace_bytes, size_t need, long long value_rows, int open, fa::KvAttnParams *p) {
     const int Hkv = p->c.Hkv;
     if (!q || !o || !cache_len || !workspace || Sq <= 0 || Hq <= 0 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
@@ -879,7 +879,7 @@ fa_status check_kv_attn(const void *q, const int *cache_len, void *o, float *lse
     p->G = Hq / Hkv;
     // tiles of all sequences, heads and row groups are counted in 32 bits
     const long long groups = ((long long)p->G * Sq + 7) / 8;
-    const long long tiles = 2 * ((long long)p->c.max_pages * page_size / 64 + 3);   // in halves
+    const long long tiles = 2 * ((long long)p->c.max_pages * page_size / 64 + 2) + open;   // in halves
     if (tiles * B > 0x7fffffffLL / ((long long)Hkv * groups)) return FA_ERR_UNSUPPORTED;
     if (value_rows > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
     p->window = std::min(window_left, 1 << 30);   // positions stay inside 32 bits
@@ -929,7 +929,7 @@ fa_status fa_fwd_kvcache(const void *q, const fa_kv_cache *cache, const int *cac
     const int ps = cache->page_size, D = cache->D;
     const long long v_rows = (long long)cache->num_pages * cache->Hkv * D;   // as the tensor loads see V
     if ((st = check_kv_attn(q, cache_len, o, lse, B, Sq, Hq, ps, D, softmax_scale, softcap, window_left, workspace,
-                            workspace_bytes, fa_fwd_kvcache_workspace_bytes(D), v_rows, &p)) != FA_OK)
+                            workspace_bytes, fa_fwd_kvcache_workspace_bytes(D), v_rows, fa::kKvOpen, &p)) != FA_OK)
         return st;
     if ((st = place_kv_attn(workspace, (size_t)fa::kKvSms * fa::kv_max_warps(D), D, &p)) != FA_OK) return st;
     p.v_block = ps % 64 == 0 ? 64 : ps % 32 == 0 ? 32 : 16;
@@ -1010,7 +1010,7 @@ fa_status fa_fwd_kvcache4(const void *q, const fa_kv_cache4 *cache, const int *c
     const int ps = cache->page_size, D = cache->D;
     const long long rows = (long long)cache->num_pages * cache->Hkv * ps;   // as the tensor loads see them
     if ((st = check_kv_attn(q, cache_len, o, lse, B, Sq, Hq, ps, D, softmax_scale, softcap, window_left, workspace,
-                            workspace_bytes, fa_fwd_kvcache4_workspace_bytes(D), rows, &p)) != FA_OK)
+                            workspace_bytes, fa_fwd_kvcache4_workspace_bytes(D), rows, fa::kKv4Open, &p)) != FA_OK)
         return st;
     if ((st = place_kv_attn(workspace, fa::kv4_workers(), D, &p)) != FA_OK) return st;
     p.bf16 = dtype == FA_BF16;

@@ -312,6 +312,92 @@ __device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], 
 // the low c bytes of a word (none below 0, all from 4 on)
 __device__ __forceinline__ uint32_t bytes_below(int c) { return c >= 4 ? 0xffffffffu : (1u << (8 * max(c, 0))) - 1u; }
 
+// Output rows of a piece in fragment order: acc[dm] holds dims 16 dm + r8 (and
+// + 8) of rows row0 + 2 q4, + 1, already scaled.
+template <int D, typename T>
+__device__ __forceinline__ void store_rows(const KvAttnParams &p, int b, int hk, int row0, int lane,
+                                           float (&acc)[4], int dm) {
+    const int r8 = lane >> 2, q4 = lane & 3;
+    // two 8x8 blocks (dims x rows), transposed: lane gets row r8, dims 2 q4, + 1
+    const uint32_t lo = transpose8(Cvt<T>::pack(acc[0], acc[1]));
+    const uint32_t hi = transpose8(Cvt<T>::pack(acc[2], acc[3]));
+    const int row = row0 + r8;
+    if (row < p.Sq * p.G) {
+        const int i = row / p.G, hq = hk * p.G + row % p.G;
+        T *dst = reinterpret_cast<T *>(p.o) + (((long long)b * p.Sq + i) * p.Hq + hq) * D + 16 * dm + 2 * q4;
+        *reinterpret_cast<uint32_t *>(dst) = lo;
+        *reinterpret_cast<uint32_t *>(dst + 8) = hi;
+    }
+}
+
+// Rows 2 q4 + e of one row block, one 16-dim part, over several pieces.
+struct Joined {
+    float4 v;
+    float m[2], l[2], r[2];
+};
+__device__ __forceinline__ void joined_zero(Joined &x) {
+    x.v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) x.m[e] = x.r[e] = -INFINITY, x.l[e] = 0.f;
+}
+// x += a piece's values and (m, l, R) of the two rows, against the larger maxima
+__device__ __forceinline__ void joined_add(Joined &x, float4 v, const float (&m)[2], const float (&l)[2],
+                                           const float (&r)[2]) {
+    float g[2], h[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const float mn = fmaxf(x.m[e], m[e]), rn = fmaxf(x.r[e], r[e]);
+        const float m0 = mn == -INFINITY ? 0.f : mn, r0 = rn == -INFINITY ? 0.f : rn;
+        x.l[e] = x.l[e] * ex2(x.m[e] - m0) + l[e] * ex2(m[e] - m0);
+        g[e] = ex2(x.r[e] - r0);
+        h[e] = ex2(r[e] - r0);
+        x.m[e] = mn;
+        x.r[e] = rn;
+    }
+    x.v.x = fmaf(v.x, h[0], x.v.x * g[0]);
+    x.v.y = fmaf(v.y, h[1], x.v.y * g[1]);
+    x.v.z = fmaf(v.z, h[0], x.v.z * g[0]);
+    x.v.w = fmaf(v.w, h[1], x.v.w * g[1]);
+}
+// Every `step`-th piece of workers from .. to (piece 1 of worker `first`, piece 0
+// of the others), in order.
+template <int NR, int DM>
+__device__ __forceinline__ void join_pieces(const KvAttnParams &p, int from, int to, int step, int first, int nr,
+                                            int dm, int row0, int lane, Joined &x) {
+    constexpr int PIECE = NR * DM * 128;
+    const int q4 = lane & 3;
+    joined_zero(x);
+#pragma unroll 4
+    for (int w = from; w <= to; w += step) {
+        const long long at = (long long)w * 2 + (w == first ? 1 : 0);
+        const float4 v = *(reinterpret_cast<const float4 *>(p.acc + at * PIECE + nr * DM * 128) + 32 * dm + lane);
+        float m[2], l[2], r[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {   // rows past the last carry no statistics
+            const float4 st = row0 + 2 * q4 + e < p.Sq * p.G ? p.stat[at * (NR * 8) + nr * 8 + 2 * q4 + e]
+                                                             : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+            m[e] = st.x, l[e] = st.y, r[e] = st.z;
+        }
+        joined_add(x, v, m, l, r);
+    }
+}
+
+template <int D, typename T>
+__device__ __forceinline__ void finish_rows(const KvAttnParams &p, const Joined &x, int b, int hk, int row0, int dm,
+                                            int lane) {
+    const float f0 = out_factor(x.r[0], x.m[0], x.l[0]), f1 = out_factor(x.r[1], x.m[1], x.l[1]);
+    float o[4] = {x.v.x * f0, x.v.y * f1, x.v.z * f0, x.v.w * f1};
+    store_rows<D, T>(p, b, hk, row0, lane, o, dm);
+    if (p.lse && dm == 0 && lane < 4) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int row = row0 + 2 * lane + e;
+            if (row < p.Sq * p.G)
+                p.lse[((long long)b * p.Hq + hk * p.G + row % p.G) * p.Sq + row / p.G] = lse_of(x.m[e], x.l[e]);
+        }
+    }
+}
+
 template <int D, int NR, typename T, bool kCap>
 __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1)
     kv_attn_kernel(const __grid_constant__ KvAttnParams p, const __grid_constant__ CUtensorMap map_v) {
@@ -333,7 +419,7 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1)
         fence_mbar_init();
     }
     const int per_tile = p.c.Hkv * p.groups;
-    const int total = kv_count<W, D>(p, s_pre, s_len, s_warp, warp, lane) * per_tile;   // (the host keeps it below 2^31)
+    const int total = kv_count<W, D, kKvOpen>(p, s_pre, s_len, s_warp, warp, lane) * per_tile;   // (the host keeps it below 2^31)
     const int wid = blockIdx.x * W + warp;
     pdl_launch();
     const KvShare sh(p, wid, total);
@@ -341,7 +427,7 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1)
     Cursor pc, end;   // what is loaded next, and where the worker stops
     {
         Cursor c;   // even lanes place the one, odd lanes the other
-        kv_place(p, s_pre, s_len, per_tile, lane & 1 ? sh.w1 : sh.w0, c);
+        kv_place<kKvOpen>(p, s_pre, s_len, per_tile, lane & 1 ? sh.w1 : sh.w0, c);
         auto from = [&](int src, Cursor &d) {
             d.b = __shfl_sync(0xffffffffu, c.b, src), d.hk = __shfl_sync(0xffffffffu, c.hk, src);
             d.rg = __shfl_sync(0xffffffffu, c.rg, src), d.t = __shfl_sync(0xffffffffu, c.t, src);
@@ -685,8 +771,8 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1)
             const bool whole = begins && ends;
             if (!begins && lane == 0) {
                 // piece 0, of a segment begun before: whose first tile's holder
-                const int unit0 = (cc.b > 0 ? s_pre[cc.b - 1] : 0) * per_tile + seg * kv_units(cc.t1 - cc.t0);
-                p.meta[wid] = make_int4(seg, cc.b, sh.worker_of(unit0 + 2), ends ? 1 : 0);
+                const int unit0 = (cc.b > 0 ? s_pre[cc.b - 1] : 0) * per_tile + seg * kv_units<kKvOpen>(cc.t1 - cc.t0);
+                p.meta[wid] = make_int4(seg, cc.b, sh.worker_of(unit0 + kKvOpen), ends ? 1 : 0);
             }
             const long long at = (long long)wid * 2 + (begins ? 1 : 0);
 #pragma unroll
@@ -712,7 +798,7 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1)
                         // (a row without keys: its sums are 0, and so is the factor)
                         float o[4] = {acc[nr][dm][0] * f[0], acc[nr][dm][1] * f[1], acc[nr][dm][2] * f[0],
                                       acc[nr][dm][3] * f[1]};
-                        store_rows<D, T, false>(p, cc.b, hk, row0, lane, o, dm);
+                        store_rows<D, T>(p, cc.b, hk, row0, lane, o, dm);
                     }
                 } else {
                     float4 *dst = reinterpret_cast<float4 *>(p.acc + at * C::PIECE + nr * 8 * D) + lane;
@@ -734,6 +820,73 @@ __global__ void __launch_bounds__(KvCfg<D, NR>::kWarps * 32, 1)
     }
 }
 
+// ------------------------------------------------------------------- join
+// One CTA per kJoinWorkers workers and 16 dims: for each of the workers in which
+// a segment ends that began before it, the segment's pieces are joined and
+// finished.  A warp takes a segment of few pieces by itself; of one of many the
+// kParts warps take every kParts-th piece and add their sums in order.
+// Joining in the attention kernel instead (the last holder in a CTA) kept
+// 17 to 20 thousand cycles of a worker's 115 for itself, most of them the first
+// run through code that is used once.  Eight workers and eight warps a CTA: 67 us
+// for 64 requests of 256 to 8192 tokens, 48 for two of up to 64k (calls); 16
+// workers 68 and 48, 32 workers 73 and 49, four of each 65 and 52.
+constexpr int kParts = 8, kJoinWorkers = 8, kFew = 8;
+
+template <int D, int NR, typename T>
+__global__ void __launch_bounds__(32 * kParts) kv_join_kernel(const __grid_constant__ KvAttnParams p) {
+    constexpr int DM = D / 16;
+    __shared__ Joined s_x[kParts - 1][32];
+    const int part = threadIdx.x / 32, lane = threadIdx.x % 32, dm = blockIdx.y;
+    pdl_wait();
+    const int w_lane = blockIdx.x * kJoinWorkers + lane;
+    int4 mine = make_int4(-1, 0, 0, 0);
+    if (lane < kJoinWorkers && w_lane < p.workers) mine = p.meta[w_lane];
+    int turn = 0;
+#pragma unroll 1
+    for (int i = 0; i < kJoinWorkers; ++i) {
+        const int seg = __shfl_sync(0xffffffffu, mine.x, i), b = __shfl_sync(0xffffffffu, mine.y, i);
+        const int first = __shfl_sync(0xffffffffu, mine.z, i), ends = __shfl_sync(0xffffffffu, mine.w, i);
+        const int w = blockIdx.x * kJoinWorkers + i;
+        if (seg < 0 || ends == 0) continue;
+        const bool few = w - first < kFew;
+        if (few && turn++ % kParts != part) continue;
+#pragma unroll 1
+        for (int nr = 0; nr < NR; ++nr) {
+            const int row0 = ((seg % p.groups) * NR + nr) * 8;
+            Joined x;
+            join_pieces<NR, DM>(p, few ? first : first + part, w, few ? 1 : kParts, first, nr, dm, row0, lane, x);
+            if (!few) {
+                if (part > 0) s_x[part - 1][lane] = x;
+                __syncthreads();   // (many pieces: every warp of the CTA is here)
+                if (part == 0)
+#pragma unroll 1
+                    for (int k = 0; k < kParts - 1; ++k) {
+                        const Joined &y = s_x[k][lane];
+                        joined_add(x, y.v, y.m, y.l, y.r);
+                    }
+                __syncthreads();
+                if (part > 0) continue;
+            }
+            finish_rows<D, T>(p, x, b, seg / p.groups, row0, dm, lane);
+        }
+    }
+}
+
+// The join behind an attention kernel on the same stream, set up while that one runs.
+template <int D, int NR, typename T>
+cudaError_t launch_join(const KvAttnParams &p, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.workers + kJoinWorkers - 1) / kJoinWorkers), D / 16);
+    cfg.blockDim = dim3(32 * kParts);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NR, T>, p);
+}
+
 template <int D, int NR, typename T, bool kCap>
 cudaError_t launch_attn_t(KvAttnParams p, const CUtensorMap &map_v, int sms, cudaStream_t stream) {
     using C = KvCfg<D, NR>;
@@ -748,7 +901,7 @@ cudaError_t launch_attn_t(KvAttnParams p, const CUtensorMap &map_v, int sms, cud
     p.page_magic = d > 1 ? (uint32_t)((1ull << 32) / d + 1) : 0u;
     kern<<<grid, C::kWarps * 32, C::SMEM, stream>>>(p, map_v);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return launch_join<D, NR, T, false>(p, stream);
+    return launch_join<D, NR, T>(p, stream);
 }
 
 template <int D, typename T>

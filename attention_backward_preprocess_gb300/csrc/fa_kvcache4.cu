@@ -247,11 +247,11 @@ constexpr uint32_t kLoMask = 0x000f000fu, kHiMask = 0x00f000f0u;
 
 template <int D, int NR>
 struct Kv4Cfg {
-    static constexpr int kWarps = NR == 1 ? 12 : 8;
+    static constexpr int kWarps = 8;
     static constexpr int KB = kTile * D / 2;             // codes of a K (or V) tile
     static constexpr int SB = kTile * (D / 64) * 4;      // its scales
     static constexpr int STAGE = 2 * (KB + SB);
-    static constexpr int kStages = D == 64 ? 4 : NR == 1 ? 2 : 3;   // at most
+    static constexpr int kStages = D == 64 ? 4 : 2;   // at most
     // shared memory of a CTA with `stages`, for B sequences (1008: to a whole pattern)
     static constexpr int smem(int stages, int B) { return 1008 + kWarps * stages * STAGE + 8 * B; }
     // One stage less where the sequences' tables want the room.
@@ -267,10 +267,21 @@ __device__ __forceinline__ void ldmatrix_x4(uint32_t row_addr, uint32_t (&r)[4])
                  : "r"(row_addr)
                  : "memory");
 }
-__device__ __forceinline__ uint32_t ld_shared_b32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void ld_shared_words(uint32_t addr, uint32_t (&v)[1]) {
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ld_shared_words(uint32_t addr, uint32_t (&v)[2]) {
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ float log2_scale(float x) {   // (below 2^-126: -inf)
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ float scale_of(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float middle_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -302,6 +313,20 @@ __device__ __forceinline__ float largest(uint4 v) {
     return m;
 }
 
+// Two dims of two rows: v is (row 2 q4, dim d), (row + 1, d), (row, d + 1), (row + 1, d + 1)
+// with d = 32 (dm / 2) + 4 r8 + 2 (dm % 2).
+template <int D, typename T>
+__device__ __forceinline__ void store_pairs(const KvAttnParams &p, int b, int hk, int row0, int lane, float4 v, int dm) {
+    const int row = row0 + 2 * (lane & 3), d = 32 * (dm >> 1) + 4 * (lane >> 2) + 2 * (dm & 1);
+    const uint32_t w[2] = {Cvt<T>::pack(v.x, v.z), Cvt<T>::pack(v.y, v.w)};
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        if (row + e < p.Sq * p.G) {
+            const int i = (row + e) / p.G, hq = hk * p.G + (row + e) % p.G;
+            *reinterpret_cast<uint32_t *>(reinterpret_cast<T *>(p.o) + (((long long)b * p.Sq + i) * p.Hq + hq) * D + d) = w[e];
+        }
+}
+
 template <int D, int NR, bool kCap>
 __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
     kv4_attn_kernel(const __grid_constant__ KvAttnParams p, const __grid_constant__ CUtensorMap map_k,
@@ -325,7 +350,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
         fence_mbar_init();
     }
     const int per_tile = p.c.Hkv * p.groups;
-    const int total = kv_count<W, D>(p, s_pre, s_len, s_warp, warp, lane) * per_tile;   // (the host keeps it below 2^31)
+    const int total = kv_count<W, D, kKv4Open>(p, s_pre, s_len, s_warp, warp, lane) * per_tile;   // (the host keeps it below 2^31)
     const int wid = blockIdx.x * W + warp;
     pdl_launch();
     const KvShare sh(p, wid, total);
@@ -333,7 +358,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
     Cursor pc, end;   // what is loaded next, and where the worker stops
     {
         Cursor c;   // even lanes place the one, odd lanes the other
-        kv_place(p, s_pre, s_len, per_tile, lane & 1 ? sh.w1 : sh.w0, c);
+        kv_place<kKv4Open>(p, s_pre, s_len, per_tile, lane & 1 ? sh.w1 : sh.w0, c);
         auto from = [&](int src, Cursor &d) {
             d.b = __shfl_sync(0xffffffffu, c.b, src), d.hk = __shfl_sync(0xffffffffu, c.hk, src);
             d.rg = __shfl_sync(0xffffffffu, c.rg, src), d.t = __shfl_sync(0xffffffffu, c.t, src);
@@ -351,13 +376,16 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
     Cursor cc = pc;   // what is computed next
 
     const uint32_t ring = tiles + warp * (ST * C::STAGE), bars = smem_u32(&s_bar[warp][0]);
+    float2 *const stat = reinterpret_cast<float2 *>(p.stat);   // (m, l) of a piece's rows
     const WaitCtl wctl{&s_abort, p.c.err, p.budget_ns};
     const int bw = p.v_block, page16 = p.c.page / 16;
     auto page_of = [&](int x) -> int { return p.page_magic ? __umulhi((uint32_t)x, p.page_magic) : x; };
-    // page of group (lane % 4) of a tile
+    // Lane 4 i + k copies block i (bw tokens of one page) of part k: K's codes, V's codes,
+    // K's scales, V's.  The page of its block of a tile, -1 if no query sees it.
+    const int blk = lane >> 2, part = lane & 3, blocks = 64 / bw;
     auto lookup = [&](const Cursor &c) -> int {
-        const int x = 4 * c.t + q4;
-        if (16 * x >= c.n || 16 * x + 16 <= c.lo) return -1;    // a group nobody sees: not read
+        const int x = 4 * c.t + blk * (bw / 16);
+        if (blk >= blocks || 16 * x >= c.n || 16 * x + bw <= c.lo) return -1;
         const int page = __ldg(p.c.table + (long long)c.b * p.c.max_pages + page_of(x));
         if (page < 0 || page >= p.c.num_pages) {
             atomicOr(p.c.err, kErrBadPage);
@@ -365,42 +393,50 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
         }
         return page;
     };
+    const uint32_t whole_tile = (1u << blocks) - 1u;
+    // where the lane's copies land in a stage, and its part's codes or scales
+    const uint32_t copy_at = part < 2 ? part * C::KB + blk * bw * (D / 2)
+                                      : 2 * C::KB + (part & 1) * C::SB + blk * bw * (4 * GR);
+    const uint32_t *const scales = reinterpret_cast<const uint32_t *>(part & 1 ? p.c.v_scale : p.c.k_scale);
     bool loads = true;      // pc is a tile of this worker's
     int pg = lookup(pc);
-    uint32_t read = 0u;     // four bits per stage: its 16-key groups that are read
+    uint32_t read = 0u;     // four bits per stage: its blocks that are read
     int under_way = 0;      // tiles loaded and not yet computed
-    // The tile at pc into stage s: lane 4 i + k copies block i (bw tokens of one page) of
-    // part k (K's codes, V's codes, K's scales, V's), if one of its groups is read.
-    auto load = [&](int s) __attribute__((always_inline)) {
-        if (!loads) return;
-        const uint32_t ok = __ballot_sync(0xffffffffu, pg >= 0) & 15u;   // (also: every lane has read the stage)
-        const int per = bw / 16, blk = lane >> 2, part = lane & 3, first = blk * per;
-        int page = -1, n = 0;
+    // Q's rows of a segment whose tiles are about to be loaded, on their way to this SM: lane
+    // (r8, q4) a quarter of row r8
+    auto prefetch_q = [&](const Cursor &c) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int pgg = __shfl_sync(0xffffffffu, pg, g);
-            if (g >= first && g < first + per) page = max(page, pgg);
-            if (g % per == 0) n += (ok >> g & ((1u << per) - 1u)) != 0u ? 1 : 0;
+        for (int nr = 0; nr < NR; ++nr) {
+            const int row = (c.rg * NR + nr) * 8 + r8;
+            if (row < p.Sq * p.G) {
+                const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) +
+                                      (((long long)c.b * p.Sq + row / p.G) * p.Hq + c.hk * p.G + row % p.G) * D + q4 * (D / 4);
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(src));
+            }
         }
+    };
+    auto load = [&](int s) __attribute__((always_inline)) {   // the tile at pc, into stage s
+        if (!loads) return;
+        const uint32_t b = __ballot_sync(0xffffffffu, pg >= 0 && part == 0);   // (also: every lane has read the stage)
         const uint32_t bar = bars + 8 * s;
-        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * bw) * (D + 8 * GR));
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(b) * bw) * (D + 8 * GR));
         __syncwarp();
-        if (blk < 64 / bw && page >= 0) {
-            const int x = 4 * pc.t + first;
-            const long long row = ((long long)page * p.c.Hkv + pc.hk) * p.c.page + 16 * (x - page_of(x) * page16);
-            const uint32_t st = ring + s * C::STAGE + (part & 1) * C::KB;
-            if (part < 2)
-                tma_load_2d(st + blk * bw * (D / 2), part ? &map_v : &map_k, bar, 0, (int)row);
-            else
-                bulk_load(ring + s * C::STAGE + 2 * C::KB + (part & 1) * C::SB + blk * bw * (4 * GR),
-                          reinterpret_cast<const uint32_t *>(part & 1 ? p.c.v_scale : p.c.k_scale) + row * GR, bw * 4 * GR, bar);
+        if (pg >= 0) {
+            const int x = 4 * pc.t + blk * (bw / 16);
+            const int row = (pg * p.c.Hkv + pc.hk) * p.c.page + 16 * (x - page_of(x) * page16);   // (below 2^31)
+            const uint32_t dst = ring + s * C::STAGE + copy_at;
+            if (part < 2) tma_load_2d(dst, part ? &map_v : &map_k, bar, 0, row);
+            else bulk_load(dst, scales + (long long)row * GR, bw * 4 * GR, bar);
         }
-        read = (read & ~(15u << (4 * s))) | ok << (4 * s);
+        read = (read & ~(15u << (4 * s))) | ((b & 1u) | (b >> 3 & 2u) | (b >> 6 & 4u) | (b >> 9 & 8u)) << (4 * s);
         ++under_way;
+        const bool last = pc.t + 1 == pc.t1;
         pc.next(p, s_len);
         loads = !at_end(pc);
         if (loads) pg = lookup(pc);
+        if (last && loads) prefetch_q(pc);
     };
+    prefetch_q(pc);
 #pragma unroll 1
     for (int s = 0; s < ST; ++s) load(s);
 
@@ -413,14 +449,16 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
 
     // ---- state of the segment being computed: row block nr, row 2 q4 + e of it
     uint32_t qb[NR][J][4];       // Q's operands
-    float qs[NR][GR][2];         // its sums per group, times 2^-24
-    float fr[NR][2];             // undoes the units and Q's power of two, times c log2(e) (or the cap's factor)
+    uint32_t qz[NR][2];          // its sums per group, as the operand of scales and middles
+    float fr[NR][2];             // undoes the units and Q's power of two, times c log2(e) (or the cap's factor); > 0
     int lo_r[NR][2], hi_r[NR][2];   // visible keys
     int lo_all = 0, hi_all = 0;     // keys every row of the worker sees
-    float acc[NR][DM][4];        // 2^-24 O^T against R: dims 32 (dm / 2) + 4 r8 + 2 (dm % 2), and 16 times the next
-    float eight[NR][GR][4];      // 2^-24 8 sum P_g against R
-    float zc[NR][GR][2];         // the lane's part of sum p middle_g against m_run
-    float m_run[NR][2], l_run[NR][2], R[NR][2];
+    float acc[NR][DM][4];        // 2^-24 sum P_g c: dims 32 (dm / 2) + 4 r8 + 2 (dm % 2), and 16 times the next
+    float eight[NR][GR][4];      // 2^-24 8 sum P_g
+    float zc[NR][GR][2];         // the lane's part of sum p middle_g
+    float m[NR][2], R[NR][2];    // what p = 2^(score - m) and P_g = 2^(score - R + 6) scale_g refer to
+    float mr[NR][2], fv[NR][2];  // m (0 before the first key), 2^(m - R + 6) (0 before the first scale)
+    float l_run[NR][2];          // the lane's part of sum p
     bool fresh = true, begins = false;
     int s_at = 0;
     uint32_t phase = 0;   // of stage s_at's barrier
@@ -445,9 +483,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                 const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 126);
                 const float up = pow2(14 - e), down = pow2(e - 14) * 0x1p24f * (kCap ? p.cap_k : p.scale_log2);
-                float sum[GR];
-#pragma unroll
-                for (int g2 = 0; g2 < GR; ++g2) sum[g2] = 0.f;
+                float sum[2] = {0.f, 0.f};
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
                     if (p.bf16) q_operands<__nv_bfloat16>(raw[j], up, qb[nr][j], sum[j / 2]);
@@ -461,6 +497,18 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
                     sum[g2] += __shfl_xor_sync(0xffffffffu, sum[g2], 1);
                     sum[g2] += __shfl_xor_sync(0xffffffffu, sum[g2], 2);
                 }
+                // (-8 Q_g, Q_g) against a key's (scale, middle) pairs: Q_g as three bf16 parts, lane q4
+                // the first or second part of group q4 % 2 and (below) the third (one group: part q4)
+                {
+                    const float z0 = sum[GR == 2 ? q4 & 1 : 0] * 0x1p-24f;
+                    const float p0 = Cvt<__nv_bfloat16>::unpack(Cvt<__nv_bfloat16>::pack(z0, 0.f)).x;
+                    const float p1 = Cvt<__nv_bfloat16>::unpack(Cvt<__nv_bfloat16>::pack(z0 - p0, 0.f)).x;
+                    const float p2 = Cvt<__nv_bfloat16>::unpack(Cvt<__nv_bfloat16>::pack(z0 - p0 - p1, 0.f)).x;
+                    const int part = GR == 2 ? q4 >> 1 : q4;
+                    const float a = part == 0 ? p0 : part == 1 ? p1 : part == 2 ? p2 : 0.f, b = GR == 2 && q4 < 2 ? p2 : 0.f;
+                    qz[nr][0] = Cvt<__nv_bfloat16>::pack(-8.f * a, a);
+                    qz[nr][1] = Cvt<__nv_bfloat16>::pack(-8.f * b, b);
+                }
 #pragma unroll
                 for (int e2 = 0; e2 < 2; ++e2) {   // the rows a lane's scores belong to
                     const int src_lane = 4 * (2 * q4 + e2);
@@ -469,13 +517,10 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
                     lo_r[nr][e2] = p.window < 0 ? 0 : max(0, hi_r[nr][e2] - p.window);
                     lo_all = max(lo_all, lo_r[nr][e2]);
                     hi_all = min(hi_all, hi_r[nr][e2]);
-                    m_run[nr][e2] = R[nr][e2] = -INFINITY;
-                    l_run[nr][e2] = 0.f;
+                    m[nr][e2] = R[nr][e2] = -INFINITY;
+                    mr[nr][e2] = fv[nr][e2] = l_run[nr][e2] = 0.f;
 #pragma unroll
-                    for (int g2 = 0; g2 < GR; ++g2) {
-                        qs[nr][g2][e2] = __shfl_sync(0xffffffffu, sum[g2], src_lane) * 0x1p-24f;
-                        zc[nr][g2][e2] = 0.f;
-                    }
+                    for (int g2 = 0; g2 < GR; ++g2) zc[nr][g2][e2] = 0.f;
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -513,7 +558,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
 #pragma unroll
                 for (int g = 0; g < GR; ++g)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) a[nr][g][k] = -8.f * qs[nr][g][k & 1];
+                    for (int k = 0; k < 4; ++k) a[nr][g][k] = 0.f;
 #pragma unroll
             for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -523,128 +568,144 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
 #pragma unroll
                     for (int nr = 0; nr < NR; ++nr) mma_f16(a[nr][j / 2], A, qb[nr][j][2 * h], qb[nr][j][2 * h + 1]);
                 }
+            uint32_t sm[2][GR];   // (scale, middle) of keys r8, r8 + 8
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                uint32_t sm[GR];
+            for (int hh = 0; hh < 2; ++hh) ld_shared_words(ks_at + (16 * t + 8 * hh) * (4 * GR), sm[hh]);
+            const uint32_t w0 = GR == 2 && (q4 & 1) ? sm[0][GR - 1] : sm[0][0], w1 = GR == 2 && (q4 & 1) ? sm[1][GR - 1] : sm[1][0];
+            const uint32_t Z[4] = {w0, w1, w0, w1};
 #pragma unroll
-                for (int g = 0; g < GR; ++g) sm[g] = ld_shared_b32(ks_at + (16 * t + 8 * hh) * (4 * GR) + 4 * g);
+            for (int nr = 0; nr < NR; ++nr) {
+                float y[4] = {0.f, 0.f, 0.f, 0.f};   // sum over the groups of (middle - 8 scale) Q_g
+                mma_bf16(y, Z, qz[nr][0], qz[nr][1]);
 #pragma unroll
-                for (int nr = 0; nr < NR; ++nr)
+                for (int k = 0; k < 4; ++k) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float y = middle_of(sm[0]) * qs[nr][0][e];
-                        y = fmaf(scale_of(sm[0]), a[nr][0][2 * hh + e], y);
-#pragma unroll
-                        for (int g = 1; g < GR; ++g) {
-                            y = fmaf(middle_of(sm[g]), qs[nr][g][e], y);
-                            y = fmaf(scale_of(sm[g]), a[nr][g][2 * hh + e], y);
-                        }
-                        x[nr][t][2 * hh + e] = y * fr[nr][e];
-                    }
+                    for (int g = 0; g < GR; ++g) y[k] = fmaf(scale_of(sm[k >> 1][g]), a[nr][g][k], y[k]);
+                    x[nr][t][k] = y[k];
+                }
             }
         }
         // ---- softmax, and V's scales
         const int key0 = kTile * cc.t + r8;   // the lane's keys: key0 + 8 u
         const bool ends = cc.t + 1 == cc.t1;
         // a tile inside every row's keys, all its pages read, takes no compare
-        const bool edge = ok != 15u || kTile * cc.t < lo_all || kTile * cc.t + kTile - 1 > hi_all;
+        const bool edge = ok != whole_tile || kTile * cc.t < lo_all || kTile * cc.t + kTile - 1 > hi_all;
         uint32_t vsm[8][GR];   // (scale, middle) of V, 0 for keys nobody sees
-        float ev[8];           // log2 of the larger scale
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const bool off = edge && (!(ok >> (u >> 1) & 1u) || key0 + 8 * u >= cc.n || key0 + 8 * u < cc.lo);
-            float top = 0.f;
-#pragma unroll
-            for (int g = 0; g < GR; ++g) {
-                vsm[u][g] = ld_shared_b32(vs_at + 8 * u * (4 * GR) + 4 * g);
-                if (off) vsm[u][g] = 0u;
-                top = fmaxf(top, scale_of(vsm[u][g]));
-            }
-            ev[u] = lg2_approx(top);
-        }
-        auto scores = [&](auto edge_tag, int nr, float (&mx)[2], float (&my)[2]) __attribute__((always_inline)) {
-            constexpr bool kEdge = decltype(edge_tag)::value;
+        for (int u = 0; u < 8; ++u) ld_shared_words(vs_at + 8 * u * (4 * GR), vsm[u]);
+        if (edge) {
+            const int per = bw / 16;
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                float *y = &x[nr][u >> 1][2 * (u & 1)];
                 const int key = key0 + 8 * u;
-                const bool gone = kEdge && !(ok >> (u >> 1) & 1u);
-                const bool off0 = kEdge && (gone || key < lo_r[nr][0] || key > hi_r[nr][0]);
-                const bool off1 = kEdge && (gone || key < lo_r[nr][1] || key > hi_r[nr][1]);
-                if (kCap) {
-                    // what lies behind the last token may be NaN: not into the pair
-                    if (off0) y[0] = 0.f;
-                    if (off1) y[1] = 0.f;
-                    float r0, r1;
-                    cap_r2(y[0], y[1], r0, r1);
-                    y[0] = fmaf(-2.f * p.cap_log2, r0, p.cap_log2);
-                    y[1] = fmaf(-2.f * p.cap_log2, r1, p.cap_log2);
-                }
-                if (off0) y[0] = -INFINITY;
-                if (off1) y[1] = -INFINITY;
+                const bool gone = !(ok >> (per == 4 ? 0 : per == 2 ? u >> 2 : u >> 1) & 1u) || key >= cc.n || key < cc.lo;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    mx[e] = fmaxf(mx[e], y[e]);
-                    my[e] = fmaxf(my[e], y[e] + ev[u]);
-                }
+                for (int g = 0; g < GR; ++g) vsm[u][g] = gone ? 0u : vsm[u][g];
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        // (under a cap: what lies behind the last token may be NaN, not into the pair)
+                        const bool off = gone || key < lo_r[nr][e] || key > hi_r[nr][e];
+                        if (off) x[nr][u >> 1][2 * (u & 1) + e] = kCap ? 0.f : -INFINITY;
+                    }
             }
-        };
+        }
+        float top = 0.f;   // largest scale of the lane's keys
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            top = GR == 2 ? max3(top, scale_of(vsm[u][0]), scale_of(vsm[u][GR - 1])) : fmaxf(top, scale_of(vsm[u][0]));
+        const float ev = log2_scale(top);
         uint32_t pt[NR][GR][8];   // P_g^T blocks, transposed: the B operands of O^T
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
-            float mx[2] = {-INFINITY, -INFINITY}, my[2] = {-INFINITY, -INFINITY};
-            if (edge) scores(std::true_type{}, nr, mx, my);
-            else scores(std::false_type{}, nr, mx, my);
-            float mref[2], fv[2], grow[2];
-            bool any_grow = false;
+            if (kCap) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    float *y = &x[nr][u >> 1][2 * (u & 1)], r0, r1;
+                    cap_r2(y[0] * fr[nr][0], y[1] * fr[nr][1], r0, r1);
+                    y[0] = fmaf(-2.f * p.cap_log2, r0, p.cap_log2);
+                    y[1] = fmaf(-2.f * p.cap_log2, r1, p.cap_log2);
+                    if (edge) {
+                        const int key = key0 + 8 * u, per = bw / 16;
+                        const bool gone = !(ok >> (per == 4 ? 0 : per == 2 ? u >> 2 : u >> 1) & 1u);
+                        if (gone || key < lo_r[nr][0] || key > hi_r[nr][0]) y[0] = -INFINITY;
+                        if (gone || key < lo_r[nr][1] || key > hi_r[nr][1]) y[1] = -INFINITY;
+                    }
+                }
+            }
+            // The references move only where a lane's largest score, or that plus its
+            // largest log2 scale, is 8 above them: mostly in a segment's first tile.
+            // (R then to the largest sum of a key's own two.)
+            float mx[2];
+            bool moves = false;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float m = fmaxf(m_run[nr][e], keys_max(mx[e])), y = keys_max(my[e]);
-                mref[e] = m == -INFINITY ? 0.f : m;
-                const float shrink = ex2(m_run[nr][e] - mref[e]);   // -inf before the first key: 0
-                l_run[nr][e] *= shrink;
+                float y = x[nr][0][e];
 #pragma unroll
-                for (int g = 0; g < GR; ++g) zc[nr][g][e] *= shrink;
-                m_run[nr][e] = m;
-                grow[e] = 1.f;
-                if (y > R[nr][e] + kLazy || (R[nr][e] == -INFINITY && y > R[nr][e])) {
-                    grow[e] = ex2(R[nr][e] - y);
-                    R[nr][e] = y;
-                    any_grow = true;
-                }
-                fv[e] = R[nr][e] == -INFINITY ? 0.f : ex2(mref[e] - R[nr][e]);   // no weight yet: P = 0
+                for (int u = 1; u < 7; u += 2)
+                    y = max3(y, x[nr][u >> 1][2 * (u & 1) + e], x[nr][(u + 1) >> 1][2 * ((u + 1) & 1) + e]);
+                y = fmaxf(y, x[nr][3][2 + e]);
+                mx[e] = kCap ? y : y * fr[nr][e];
+                moves |= mx[e] > m[nr][e] + kLazy || mx[e] + ev > R[nr][e] + kLazy;
             }
-            if (__any_sync(0xffffffffu, any_grow)) {
-                const uint64_t g2 = f2_pack(grow[0], grow[1]);
+            if (__any_sync(0xffffffffu, moves)) {
+                float grow[2], my[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const float lg = log2_scale(fmaxf(scale_of(vsm[u][0]), scale_of(vsm[u][GR - 1])));
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float y = x[nr][u >> 1][2 * (u & 1) + e];
+                        my[e] = fmaxf(my[e], kCap ? y + lg : fmaf(y, fr[nr][e], lg));
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float mn = fmaxf(m[nr][e], keys_max(mx[e])), y = keys_max(my[e]);
+                    mr[nr][e] = mn == -INFINITY ? 0.f : mn;
+                    const float shrink = ex2(m[nr][e] - mr[nr][e]);   // -inf before the first key: 0
+                    m[nr][e] = mn;
+                    l_run[nr][e] *= shrink;
+#pragma unroll
+                    for (int g = 0; g < GR; ++g) zc[nr][g][e] *= shrink;
+                    grow[e] = 1.f;
+                    if (y > R[nr][e] + kLazy || (R[nr][e] == -INFINITY && y > R[nr][e])) {
+                        grow[e] = ex2(R[nr][e] - y);
+                        R[nr][e] = y;
+                    }
+                    fv[nr][e] = R[nr][e] == -INFINITY ? 0.f : ex2(mr[nr][e] - R[nr][e] + 6.f);
+                }
                 auto times = [&](float (&v)[4]) __attribute__((always_inline)) {
 #pragma unroll
-                    for (int k = 0; k < 4; k += 2) {
-                        const float2 y = f2_unpack(f2_mul(f2_pack(v[k], v[k + 1]), g2));
-                        v[k] = y.x, v[k + 1] = y.y;
-                    }
+                    for (int k = 0; k < 4; ++k) v[k] *= grow[k & 1];
                 };
 #pragma unroll
                 for (int dm = 0; dm < DM; ++dm) times(acc[nr][dm]);
 #pragma unroll
                 for (int g = 0; g < GR; ++g) times(eight[nr][g]);
             }
+            const uint64_t fr2 = f2_pack(fr[nr][0], fr[nr][1]), nm = f2_pack(-mr[nr][0], -mr[nr][1]);
+            const uint64_t fv2 = f2_pack(fv[nr][0], fv[nr][1]);
+            uint64_t sum = f2_pack(l_run[nr][0], l_run[nr][1]);
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                float pp[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    pp[e] = ex2(x[nr][u >> 1][2 * (u & 1) + e] - mref[e]);
-                    l_run[nr][e] += pp[e];
-#pragma unroll
-                    for (int g = 0; g < GR; ++g) zc[nr][g][e] = fmaf(pp[e], middle_of(vsm[u][g]), zc[nr][g][e]);
-                    pp[e] *= fv[e];
-                }
+                const uint64_t x2 = f2_pack(x[nr][u >> 1][2 * (u & 1)], x[nr][u >> 1][2 * (u & 1) + 1]);
+                const float2 y = f2_unpack(kCap ? f2_add(x2, nm) : f2_fma(x2, fr2, nm));
+                const float2 pp = make_float2(ex2(y.x), ex2(y.y));
+                const uint64_t p2 = f2_pack(pp.x, pp.y);
+                sum = f2_add(sum, p2);
+                const float2 w = f2_unpack(f2_mul(p2, fv2));
 #pragma unroll
                 for (int g = 0; g < GR; ++g) {
-                    const float s = scale_of(vsm[u][g]);
-                    pt[nr][g][u] = transpose8(Cvt<__half>::pack(pp[0] * s, pp[1] * s));
+                    const float mid = middle_of(vsm[u][g]), sc = scale_of(vsm[u][g]);
+                    zc[nr][g][0] = fmaf(pp.x, mid, zc[nr][g][0]);
+                    zc[nr][g][1] = fmaf(pp.y, mid, zc[nr][g][1]);
+                    pt[nr][g][u] = transpose8(Cvt<__half>::pack(w.x * sc, w.y * sc));
                 }
             }
+            const float2 l2 = f2_unpack(sum);
+            l_run[nr][0] = l2.x, l_run[nr][1] = l2.y;
         }
         // ---- O^T += V^T P^T, per 16 tokens
         constexpr uint32_t kEight[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
@@ -683,31 +744,28 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
             const int hk = cc.hk, rg = cc.rg, seg = hk * p.groups + rg;
             const bool whole = begins && ends;
             if (!begins && lane == 0) {
-                // piece 0, of a segment begun before: whose first tile's holder
-                const int unit0 = (cc.b > 0 ? s_pre[cc.b - 1] : 0) * per_tile + seg * kv_units(cc.t1 - cc.t0);
-                p.meta[wid] = make_int4(seg, cc.b, sh.worker_of(unit0 + 2), ends ? 1 : 0);
+                // piece 0, of a segment begun before: the holders of its first and last tiles
+                const int units = kv_units<kKv4Open>(cc.t1 - cc.t0), unit0 = (cc.b > 0 ? s_pre[cc.b - 1] : 0) * per_tile + seg * units;
+                p.meta[wid] = make_int4(seg, cc.b, sh.worker_of(unit0 + kKv4Open), sh.worker_of(unit0 + units - 2));
             }
             const long long at = (long long)wid * 2 + (begins ? 1 : 0);
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr) {
                 const int row0 = (rg * NR + nr) * 8;
-                float f[2], z[GR][2], out[2];
+                float f[2], z[GR][2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float l = keys_sum(l_run[nr][e]);
-                    // what brings acc from R to m
-                    f[e] = R[nr][e] == -INFINITY ? 0.f : ex2(R[nr][e] - m_run[nr][e]);
-                    out[e] = whole ? out_factor(0.f, 0.f, l) : 1.f;
+                    const float l = keys_sum(l_run[nr][e]), out = whole ? out_factor(0.f, 0.f, l) : 1.f;
 #pragma unroll
-                    for (int g = 0; g < GR; ++g) z[g][e] = keys_sum(zc[nr][g][e]) * out[e];
-                    f[e] *= out[e];
+                    for (int g = 0; g < GR; ++g) z[g][e] = keys_sum(zc[nr][g][e]) * out;
+                    // what brings acc from R to m
+                    f[e] = R[nr][e] == -INFINITY ? 0.f : ex2(R[nr][e] - mr[nr][e]) * out;
                     const int row = row0 + 2 * q4 + e;
                     if (r8 == 0 && row < p.Sq * p.G) {
                         if (!whole)
-                            p.stat[at * (NR * 8) + nr * 8 + 2 * q4 + e] = make_float4(m_run[nr][e], l, m_run[nr][e], 0.f);
+                            stat[at * (NR * 8) + nr * 8 + 2 * q4 + e] = make_float2(m[nr][e], l);
                         else if (p.lse)
-                            p.lse[((long long)cc.b * p.Hq + hk * p.G + row % p.G) * p.Sq + row / p.G] =
-                                lse_of(m_run[nr][e], l);
+                            p.lse[((long long)cc.b * p.Hq + hk * p.G + row % p.G) * p.Sq + row / p.G] = lse_of(m[nr][e], l);
                     }
                 }
 #pragma unroll
@@ -716,15 +774,12 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float a = (k < 2 ? acc[nr][dm][k] : acc[nr][dm][k] * 0.0625f) - eight[nr][dm / 4][k & 1];
-                        o[k] = fmaf(a * 0x1p24f, f[k & 1], z[dm / 4][k & 1]);
+                        o[k] = fmaf(a * 0x1p18f, f[k & 1], z[dm / 4][k & 1]);
                     }
-                    if (whole) {
-                        if (p.bf16) store_rows<D, __nv_bfloat16, true>(p, cc.b, hk, row0, lane, o, dm);
-                        else store_rows<D, __half, true>(p, cc.b, hk, row0, lane, o, dm);
-                    } else {
-                        float4 *dst = reinterpret_cast<float4 *>(p.acc + at * (NR * 8 * D) + nr * 8 * D) + lane;
-                        dst[32 * dm] = make_float4(o[0], o[1], o[2], o[3]);
-                    }
+                    const float4 v = make_float4(o[0], o[1], o[2], o[3]);
+                    if (!whole) reinterpret_cast<float4 *>(p.acc + at * (NR * 8 * D) + nr * 8 * D)[32 * dm + lane] = v;
+                    else if (p.bf16) store_pairs<D, __nv_bfloat16>(p, cc.b, hk, row0, lane, v, dm);
+                    else store_pairs<D, __half>(p, cc.b, hk, row0, lane, v, dm);
                 }
             }
             fresh = true;
@@ -736,6 +791,70 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
     for (int i = 0; i < under_way; ++i) {
         mbar_wait_drain_warp(bars + 8 * s_at, phase, p.c.err, p.budget_ns);
         if (++s_at == ST) s_at = 0, phase ^= 1u;
+    }
+}
+
+// ------------------------------------------------------------------- join
+// One CTA per worker.  The workers first .. last that held a segment have a piece of it
+// each (piece 1 of the first, piece 0 of the others); the CTAs of the others put them
+// together, H of them (a power of two, as many as there are up to kHelpers) a 1 / H of
+// the segment's values each, with H sets of threads that take every H-th piece and are
+// added in a tree.  So every thread has a few pieces to read at once, two
+// pieces or two hundred.  Latency bounds it: three dependent reads.
+constexpr int kHelpers = 32;
+
+template <int D, int NR>
+__global__ void __launch_bounds__(2 * D) kv4_join_kernel(const __grid_constant__ KvAttnParams p) {
+    constexpr int N = 2 * D;   // threads, and float4s of eight rows of a piece
+    __shared__ float4 s_v[N], s_s[N];
+    const int tid = threadIdx.x, w = blockIdx.x;
+    pdl_wait();
+    const int4 meta = p.meta[w];   // segment, sequence, first and last worker
+    const int first = meta.z, last = meta.w, others = last - first;
+    if (meta.x < 0) return;
+    const int H = 1 << (31 - __clz(min(others, kHelpers))), h = w - first - 1;
+    if (h >= H) return;
+    const int F = N / H, set = tid / F, q = h * F + tid % F, dm = q / 32, lane = q % 32;
+    const int hk = meta.x / p.groups, rg = meta.x - hk * p.groups;
+#pragma unroll 1
+    for (int nr = 0; nr < NR; ++nr) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), t = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);   // t: m, l of the two rows
+        auto add = [&](float4 v, float4 s) __attribute__((always_inline)) {
+            const float m0 = fmaxf(t.x, s.x), m1 = fmaxf(t.z, s.z);
+            const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
+            const float a0 = ex2(t.x - r0), a1 = ex2(t.z - r1), b0 = ex2(s.x - r0), b1 = ex2(s.z - r1);
+            t = make_float4(m0, fmaf(s.y, b0, t.y * a0), m1, fmaf(s.w, b1, t.w * a1));
+            x = make_float4(fmaf(v.x, b0, x.x * a0), fmaf(v.y, b1, x.y * a1), fmaf(v.z, b0, x.z * a0), fmaf(v.w, b1, x.w * a1));
+        };
+#pragma unroll 2
+        for (int i = first + set; i <= last; i += H) {
+            const long long at = ((long long)i * 2 + (i == first ? 1 : 0)) * NR + nr;
+            add(reinterpret_cast<const float4 *>(p.acc + at * (8 * D))[q],
+                reinterpret_cast<const float4 *>(p.stat)[at * 4 + (lane & 3)]);
+        }
+#pragma unroll 1
+        for (int o = H / 2; o > 0; o >>= 1) {
+            if (set >= o && set < 2 * o) s_v[tid] = x, s_s[tid] = t;
+            __syncthreads();
+            if (set < o) add(s_v[tid + o * F], s_s[tid + o * F]);
+        }
+        if (set == 0) {
+            const float f0 = t.y == 0.f ? 0.f : 1.f / t.y, f1 = t.w == 0.f ? 0.f : 1.f / t.w;
+            const float4 o = make_float4(x.x * f0, x.y * f1, x.z * f0, x.w * f1);
+            const int row0 = (rg * NR + nr) * 8;
+            if (p.bf16) store_pairs<D, __nv_bfloat16>(p, meta.y, hk, row0, lane, o, dm);
+            else store_pairs<D, __half>(p, meta.y, hk, row0, lane, o, dm);
+            if (p.lse && q < 4) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = row0 + 2 * q + e;
+                    if (row < p.Sq * p.G)
+                        p.lse[((long long)meta.y * p.Hq + hk * p.G + row % p.G) * p.Sq + row / p.G] =
+                            e ? lse_of(t.z, t.w) : lse_of(t.x, t.y);
+                }
+            }
+        }
+        if (NR > 1) __syncthreads();
     }
 }
 
@@ -755,7 +874,16 @@ cudaError_t launch_attn(KvAttnParams p, const CUtensorMap &mk, const CUtensorMap
     p.page_magic = d > 1 ? (uint32_t)((1ull << 32) / d + 1) : 0u;
     kern<<<grid, C::kWarps * 32, smem, stream>>>(p, mk, mv);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return p.bf16 ? launch_join<D, NR, __nv_bfloat16, true>(p, stream) : launch_join<D, NR, __half, true>(p, stream);
+    cudaLaunchConfig_t cfg = {};   // set up while the attention runs
+    cfg.gridDim = dim3((unsigned)p.workers);
+    cfg.blockDim = dim3(2 * D);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NR>, p);
 }
 
 template <int D>

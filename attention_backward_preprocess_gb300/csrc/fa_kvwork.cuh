@@ -1,11 +1,7 @@
 // fa_kvwork.cuh -- what the attention kernels over a paged cache share, whatever
 // their values are held in: how the work is counted and split over the workers
-// (warps), and how the pieces of a segment that several of them held are joined.
-//
-// Fragments.  A worker's accumulator of 16-dim part dm holds two dims of two rows
-// a lane (r8 = lane / 4, q4 = lane % 4): rows 2 q4, + 1 of its 8, and dims
-// 16 dm + r8, + 8 (kPairs false) or two neighbours, 32 (dm / 2) + 4 r8 +
-// 2 (dm % 2), + 1 (kPairs true).
+// (warps), and the fragments' small operations.  A lane of a worker: r8 = lane / 4,
+// q4 = lane % 4.
 #pragma once
 
 #include "fa_device.cuh"
@@ -62,13 +58,13 @@ __device__ __forceinline__ int kv_first(const KvAttnParams &p, int n) {
 __device__ __forceinline__ int kv_tiles(const KvAttnParams &p, int n) {
     return (n + kTile - 1) / kTile - kv_first(p, n) / kTile;
 }
-// Work is shared out in half tiles: a segment of nt tiles counts 2 nt + 2, for
-// opening and closing it takes about as long as a tile.  A border x half tiles
-// into a segment lies before tile kv_border(x); tile t belongs to the worker
-// that holds half tile 2 t + 2.  (Shared out by tiles alone, workers with short
-// sequences took 145 k cycles where the mean was 118 k.)
-__device__ __forceinline__ int kv_units(int nt) { return nt > 0 ? 2 * nt + 2 : 0; }
-__device__ __forceinline__ int kv_border(int x) { return max(x - 1, 0) / 2; }
+// Work is shared out in half tiles: a segment of nt tiles counts 2 nt + kOpen, for
+// opening and closing it takes time as well.  A border x half tiles into a segment
+// lies before tile kv_border(x); tile t belongs to the worker that holds half tile
+// 2 t + kOpen.  (8-bit, shared out by tiles alone: workers with short sequences took
+// 145 k cycles where the mean was 118 k.)
+template <int kOpen> __device__ __forceinline__ int kv_units(int nt) { return nt > 0 ? 2 * nt + kOpen : 0; }
+template <int kOpen> __device__ __forceinline__ int kv_border(int x) { return max(x - kOpen + 1, 0) / 2; }
 
 // A worker's place in the work: tile t of [t0, t1) of sequence b, kv head hk and
 // row group rg.
@@ -101,7 +97,7 @@ struct Cursor {
 // their tokens into s_len (0 where the length is outside the table), and the sum
 // back, to every thread of the CTA of W warps.  Rows of sequences without a key
 // are written here.
-template <int W, int D>
+template <int W, int D, int kOpen>
 __device__ __forceinline__ int kv_count(const KvAttnParams &p, int *s_pre, int *s_len, int *s_warp, int warp, int lane) {
     int carry = 0;
     for (int b0 = 0; b0 < p.B; b0 += W * 32) {
@@ -113,7 +109,7 @@ __device__ __forceinline__ int kv_count(const KvAttnParams &p, int *s_pre, int *
                 if (blockIdx.x == 0) atomicOr(p.c.err, kErrBadLength);
                 n = 0;
             }
-            x = kv_units(kv_tiles(p, n));
+            x = kv_units<kOpen>(kv_tiles(p, n));
             s_len[b] = n;
         }
 #pragma unroll
@@ -166,6 +162,7 @@ struct KvShare {
 };
 
 // The tile behind a border (past the last one: b == B).
+template <int kOpen>
 __device__ __forceinline__ void kv_place(const KvAttnParams &p, const int *s_pre, const int *s_len, int per_tile, int w,
                                          Cursor &c) {
     const int u = w / per_tile;   // the border over the sequences, if every half tile came once
@@ -179,11 +176,11 @@ __device__ __forceinline__ void kv_place(const KvAttnParams &p, const int *s_pre
     c.hk = c.rg = c.t = 0;
     if (lo == p.B) return;
     c.open(p, s_len);
-    const int in = w - (lo > 0 ? s_pre[lo - 1] : 0) * per_tile, units = kv_units(c.t1 - c.t0);
+    const int in = w - (lo > 0 ? s_pre[lo - 1] : 0) * per_tile, units = kv_units<kOpen>(c.t1 - c.t0);
     const int seg = in / units;
     c.hk = seg / p.groups;
     c.rg = seg - c.hk * p.groups;
-    c.t = c.t0 + kv_border(in - seg * units) - 1;
+    c.t = c.t0 + kv_border<kOpen>(in - seg * units) - 1;
     c.next(p, s_len);   // (a border behind a segment's last tile: the next one's first)
 }
 
@@ -194,172 +191,10 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 // that saw nothing).
 __device__ __forceinline__ float out_factor(float R, float m, float l) { return l == 0.f ? 0.f : ex2(R - m) / l; }
 
-// Output rows of a piece: acc is one 16-dim part dm of them, already scaled.
-template <int D, typename T, bool kPairs>
-__device__ __forceinline__ void store_rows(const KvAttnParams &p, int b, int hk, int row0, int lane,
-                                           float (&acc)[4], int dm) {
-    const int r8 = lane >> 2, q4 = lane & 3;
-    auto at = [&](int row) __attribute__((always_inline)) -> T * {
-        const int i = row / p.G, hq = hk * p.G + row % p.G;
-        return reinterpret_cast<T *>(p.o) + (((long long)b * p.Sq + i) * p.Hq + hq) * D;
-    };
-    if (kPairs) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (row0 + 2 * q4 + e < p.Sq * p.G)
-                *reinterpret_cast<uint32_t *>(at(row0 + 2 * q4 + e) + 32 * (dm >> 1) + 4 * r8 + 2 * (dm & 1)) =
-                    Cvt<T>::pack(acc[e], acc[2 + e]);
-        return;
-    }
-    // two 8x8 blocks (dims x rows), transposed: lane gets row r8, dims 2 q4, + 1
-    const uint32_t lo = transpose8(Cvt<T>::pack(acc[0], acc[1]));
-    const uint32_t hi = transpose8(Cvt<T>::pack(acc[2], acc[3]));
-    if (row0 + r8 < p.Sq * p.G) {
-        T *dst = at(row0 + r8) + 16 * dm + 2 * q4;
-        *reinterpret_cast<uint32_t *>(dst) = lo;
-        *reinterpret_cast<uint32_t *>(dst + 8) = hi;
-    }
-}
-
-// Rows 2 q4 + e of one row block, one 16-dim part, over several pieces.
-struct Joined {
-    float4 v;
-    float m[2], l[2], r[2];
-};
-__device__ __forceinline__ void joined_zero(Joined &x) {
-    x.v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) x.m[e] = x.r[e] = -INFINITY, x.l[e] = 0.f;
-}
-// x += a piece's values and (m, l, R) of the two rows, against the larger maxima
-__device__ __forceinline__ void joined_add(Joined &x, float4 v, const float (&m)[2], const float (&l)[2],
-                                           const float (&r)[2]) {
-    float g[2], h[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const float mn = fmaxf(x.m[e], m[e]), rn = fmaxf(x.r[e], r[e]);
-        const float m0 = mn == -INFINITY ? 0.f : mn, r0 = rn == -INFINITY ? 0.f : rn;
-        x.l[e] = x.l[e] * ex2(x.m[e] - m0) + l[e] * ex2(m[e] - m0);
-        g[e] = ex2(x.r[e] - r0);
-        h[e] = ex2(r[e] - r0);
-        x.m[e] = mn;
-        x.r[e] = rn;
-    }
-    x.v.x = fmaf(v.x, h[0], x.v.x * g[0]);
-    x.v.y = fmaf(v.y, h[1], x.v.y * g[1]);
-    x.v.z = fmaf(v.z, h[0], x.v.z * g[0]);
-    x.v.w = fmaf(v.w, h[1], x.v.w * g[1]);
-}
-// Every `step`-th piece of workers from .. to (piece 1 of worker `first`, piece 0
-// of the others), in order.
-template <int NR, int DM>
-__device__ __forceinline__ void join_pieces(const KvAttnParams &p, int from, int to, int step, int first, int nr,
-                                            int dm, int row0, int lane, Joined &x) {
-    constexpr int PIECE = NR * DM * 128;
-    const int q4 = lane & 3;
-    joined_zero(x);
-#pragma unroll 4
-    for (int w = from; w <= to; w += step) {
-        const long long at = (long long)w * 2 + (w == first ? 1 : 0);
-        const float4 v = *(reinterpret_cast<const float4 *>(p.acc + at * PIECE + nr * DM * 128) + 32 * dm + lane);
-        float m[2], l[2], r[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {   // rows past the last carry no statistics
-            const float4 st = row0 + 2 * q4 + e < p.Sq * p.G ? p.stat[at * (NR * 8) + nr * 8 + 2 * q4 + e]
-                                                             : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-            m[e] = st.x, l[e] = st.y, r[e] = st.z;
-        }
-        joined_add(x, v, m, l, r);
-    }
-}
-
-template <int D, typename T, bool kPairs>
-__device__ __forceinline__ void finish_rows(const KvAttnParams &p, const Joined &x, int b, int hk, int row0, int dm,
-                                            int lane) {
-    const float f0 = out_factor(x.r[0], x.m[0], x.l[0]), f1 = out_factor(x.r[1], x.m[1], x.l[1]);
-    float o[4] = {x.v.x * f0, x.v.y * f1, x.v.z * f0, x.v.w * f1};
-    store_rows<D, T, kPairs>(p, b, hk, row0, lane, o, dm);
-    if (p.lse && dm == 0 && lane < 4) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int row = row0 + 2 * lane + e;
-            if (row < p.Sq * p.G)
-                p.lse[((long long)b * p.Hq + hk * p.G + row % p.G) * p.Sq + row / p.G] = lse_of(x.m[e], x.l[e]);
-        }
-    }
-}
-
 // Programmatic dependent launch: the second kernel's CTAs may be set up while
 // the first still runs, and wait here for its results.
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-// ------------------------------------------------------------------- join
-// One CTA per kJoinWorkers workers and 16 dims: for each of the workers in which
-// a segment ends that began before it, the segment's pieces are joined and
-// finished.  A warp takes a segment of few pieces by itself; of one of many the
-// kParts warps take every kParts-th piece and add their sums in order.
-// Joining in the attention kernel instead (the last holder in a CTA) kept
-// 17 to 20 thousand cycles of a worker's 115 for itself, most of them the first
-// run through code that is used once.  Eight workers and eight warps a CTA: 67 us
-// for 64 requests of 256 to 8192 tokens, 48 for two of up to 64k (calls); 16
-// workers 68 and 48, 32 workers 73 and 49, four of each 65 and 52.
-constexpr int kParts = 8, kJoinWorkers = 8, kFew = 8;
-
-template <int D, int NR, typename T, bool kPairs>
-__global__ void __launch_bounds__(32 * kParts) kv_join_kernel(const __grid_constant__ KvAttnParams p) {
-    constexpr int DM = D / 16;
-    __shared__ Joined s_x[kParts - 1][32];
-    const int part = threadIdx.x / 32, lane = threadIdx.x % 32, dm = blockIdx.y;
-    pdl_wait();
-    const int w_lane = blockIdx.x * kJoinWorkers + lane;
-    int4 mine = make_int4(-1, 0, 0, 0);
-    if (lane < kJoinWorkers && w_lane < p.workers) mine = p.meta[w_lane];
-    int turn = 0;
-#pragma unroll 1
-    for (int i = 0; i < kJoinWorkers; ++i) {
-        const int seg = __shfl_sync(0xffffffffu, mine.x, i), b = __shfl_sync(0xffffffffu, mine.y, i);
-        const int first = __shfl_sync(0xffffffffu, mine.z, i), ends = __shfl_sync(0xffffffffu, mine.w, i);
-        const int w = blockIdx.x * kJoinWorkers + i;
-        if (seg < 0 || ends == 0) continue;
-        const bool few = w - first < kFew;
-        if (few && turn++ % kParts != part) continue;
-#pragma unroll 1
-        for (int nr = 0; nr < NR; ++nr) {
-            const int row0 = ((seg % p.groups) * NR + nr) * 8;
-            Joined x;
-            join_pieces<NR, DM>(p, few ? first : first + part, w, few ? 1 : kParts, first, nr, dm, row0, lane, x);
-            if (!few) {
-                if (part > 0) s_x[part - 1][lane] = x;
-                __syncthreads();   // (many pieces: every warp of the CTA is here)
-                if (part == 0)
-#pragma unroll 1
-                    for (int k = 0; k < kParts - 1; ++k) {
-                        const Joined &y = s_x[k][lane];
-                        joined_add(x, y.v, y.m, y.l, y.r);
-                    }
-                __syncthreads();
-                if (part > 0) continue;
-            }
-            finish_rows<D, T, kPairs>(p, x, b, seg / p.groups, row0, dm, lane);
-        }
-    }
-}
-
-// The join behind an attention kernel on the same stream, set up while that one runs.
-template <int D, int NR, typename T, bool kPairs>
-cudaError_t launch_join(const KvAttnParams &p, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.workers + kJoinWorkers - 1) / kJoinWorkers), D / 16);
-    cfg.blockDim = dim3(32 * kParts);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NR, T, kPairs>, p);
-}
 
 }  // namespace
 }  // namespace fa
