@@ -20,20 +20,6 @@
 namespace fa {
 namespace {
 
-// four e4m3 bytes -> two f16 pairs (exact), low bytes first
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-}
-// two fp32 -> two e4m3 bytes, lo in the low byte (nearest even, saturating)
-__device__ __forceinline__ uint32_t f32_to_e4m3x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // ------------------------------------------------------------------ append
 // One CTA per (page a sequence's new tokens touch, kv head, K or V).  It reads
 // the tokens once (into shared memory, their largest magnitude on the way),
@@ -83,13 +69,6 @@ __device__ __forceinline__ void requantise(uint32_t (&w)[4], float ratio, int n)
         const uint32_t keep = k >= 4 ? 0u : 0xffffffffu << (8 * k);
         w[i] = (w[i] & keep) | (r & ~keep);
     }
-}
-
-// magnitudes of two 16-bit floats compare as their bits do
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
 }
 
 template <int D, typename T, int kThreads>
@@ -303,11 +282,6 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
-}
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // the low c bytes of a word (none below 0, all from 4 on)
 __device__ __forceinline__ uint32_t bytes_below(int c) { return c >= 4 ? 0xffffffffu : (1u << (8 * max(c, 0))) - 1u; }

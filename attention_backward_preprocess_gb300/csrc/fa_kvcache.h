@@ -58,6 +58,7 @@ struct KvAttnParams {
     int v_block, v_pad;
     long long budget_ns;         // bound of every device-side wait
     int bf16;                    // 4-bit cache: q's and o's type
+
     int stages;                  // and the tiles a worker has in shared memory
 };
 
@@ -72,7 +73,7 @@ size_t kv_workspace_bytes(int D);
 // Half tiles that opening and closing a segment counts as where work is shared out.
 constexpr int kKvOpen = 2, kKv4Open = 6;
 // The 4-bit cache's attention has workers of its own number.
-constexpr int kKv4MaxWarps = 8;
+constexpr int kKv4MaxWarps = 12;
 inline size_t kv4_workers() { return (size_t)kKvSms * kKv4MaxWarps; }
 
 cudaError_t launch_kv_append(const KvAppendParams &p, int D, int bf16, cudaStream_t stream);

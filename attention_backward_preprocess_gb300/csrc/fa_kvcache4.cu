@@ -247,7 +247,8 @@ constexpr uint32_t kLoMask = 0x000f000fu, kHiMask = 0x00f000f0u;
 
 template <int D, int NR>
 struct Kv4Cfg {
-    static constexpr int kWarps = 8;
+    static constexpr int kWarps = NR == 1 ? 12 : 8;
+    static constexpr int kStep = 2;   // 16-key products at a time
     static constexpr int KB = kTile * D / 2;             // codes of a K (or V) tile
     static constexpr int SB = kTile * (D / 64) * 4;      // its scales
     static constexpr int STAGE = 2 * (KB + SB);
@@ -286,8 +287,8 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ float scale_of(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float middle_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Q's words of the row: eight dims as four pairs; out: the two registers each of the
-// two products of a chunk, and the sum of what they hold.
+// Q's operands from a row's dims 32 j + 8 q4 .. + 7, `up` its power of two: the two
+// registers each of the two products of a chunk; what they sum to is added to `sum`.
 template <typename T>
 __device__ __forceinline__ void q_operands(uint4 raw, float up, uint32_t (&b)[4], float &sum) {
     const float2 a = Cvt<T>::unpack(raw.x), c = Cvt<T>::unpack(raw.y), d = Cvt<T>::unpack(raw.z), e = Cvt<T>::unpack(raw.w);
@@ -296,21 +297,7 @@ __device__ __forceinline__ void q_operands(uint4 raw, float up, uint32_t (&b)[4]
     b[1] = Cvt<__half>::pack(a.y * od, d.y * od);   // dims 1, 5
     b[2] = Cvt<__half>::pack(c.x * up, e.x * up);   // dims 2, 6
     b[3] = Cvt<__half>::pack(c.y * od, e.y * od);   // dims 3, 7
-    const float2 s0 = Cvt<__half>::unpack(b[0]), s1 = Cvt<__half>::unpack(b[1]), s2 = Cvt<__half>::unpack(b[2]),
-                 s3 = Cvt<__half>::unpack(b[3]);
-    sum += (s0.x + s0.y) + (s2.x + s2.y) + 16.f * ((s1.x + s1.y) + (s3.x + s3.y));
-}
-template <typename T>
-__device__ __forceinline__ float largest(uint4 v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float m = 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float2 f = Cvt<T>::unpack(w[k]);
-        m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
-        if (f.x != f.x || f.y != f.y) m = INFINITY;   // (fmaxf passes NaN over)
-    }
-    return m;
+    sum += up * (((a.x + a.y) + (c.x + c.y)) + ((d.x + d.y) + (e.x + e.y)));
 }
 
 // Two dims of two rows: v is (row 2 q4, dim d), (row + 1, d), (row, d + 1), (row + 1, d + 1)
@@ -327,12 +314,12 @@ __device__ __forceinline__ void store_pairs(const KvAttnParams &p, int b, int hk
         }
 }
 
-template <int D, int NR, bool kCap>
+template <int D, int NR, typename T, bool kCap>
 __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
     kv4_attn_kernel(const __grid_constant__ KvAttnParams p, const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v) {
     using C = Kv4Cfg<D, NR>;
-    constexpr int W = C::kWarps, J = D / 32, GR = D / 64, DM = D / 16;
+    constexpr int W = C::kWarps, KS = C::kStep, J = D / 32, GR = D / 64, DM = D / 16;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     __shared__ int s_warp[W];
     __shared__ __align__(8) uint64_t s_bar[W][C::kStages];   // a stage's tile landed
@@ -401,7 +388,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
     bool loads = true;      // pc is a tile of this worker's
     int pg = lookup(pc);
     uint32_t read = 0u;     // four bits per stage: its blocks that are read
-    int under_way = 0;      // tiles loaded and not yet computed
+    int under_way = 0, s_ld = 0;   // tiles loaded and not yet computed; the next one's stage
     // Q's rows of a segment whose tiles are about to be loaded, on their way to this SM: lane
     // (r8, q4) a quarter of row r8
     auto prefetch_q = [&](const Cursor &c) {
@@ -415,8 +402,8 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
             }
         }
     };
-    auto load = [&](int s) __attribute__((always_inline)) {   // the tile at pc, into stage s
-        if (!loads) return;
+    auto load = [&]() __attribute__((always_inline)) {   // the tile at pc
+        const int s = s_ld;
         const uint32_t b = __ballot_sync(0xffffffffu, pg >= 0 && part == 0);   // (also: every lane has read the stage)
         const uint32_t bar = bars + 8 * s;
         if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(b) * bw) * (D + 8 * GR));
@@ -430,6 +417,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
         }
         read = (read & ~(15u << (4 * s))) | ((b & 1u) | (b >> 3 & 2u) | (b >> 6 & 4u) | (b >> 9 & 8u)) << (4 * s);
         ++under_way;
+        if (++s_ld == ST) s_ld = 0;
         const bool last = pc.t + 1 == pc.t1;
         pc.next(p, s_len);
         loads = !at_end(pc);
@@ -437,8 +425,6 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
         if (last && loads) prefetch_q(pc);
     };
     prefetch_q(pc);
-#pragma unroll 1
-    for (int s = 0; s < ST; ++s) load(s);
 
     // ldmatrix: lane l gives the address of row l % 8 of matrix l / 8, matrices being the
     // 16-byte chunks of eight keys (D = 64: of sixteen).  Chunks lie as the tensor loads
@@ -463,6 +449,10 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
     int s_at = 0;
     uint32_t phase = 0;   // of stage s_at's barrier
     while (true) {
+        // (in one place, and so are the other parts that run seldom: a launch fetches them cold)
+        // A segment's Q is made ready behind one tile's loads, the other stages' come after.
+#pragma unroll 1
+        while (loads && under_way < (fresh ? 1 : ST)) load();
         if (fresh) {
             lo_all = 0, hi_all = 0x7fffffff;
 #pragma unroll
@@ -470,25 +460,24 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
                 const int row = (cc.rg * NR + nr) * 8 + r8;
                 const bool live = row < p.Sq * p.G;
                 const int i = live ? row / p.G : p.Sq - 1, g = live ? row % p.G : 0;
-                const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) +
-                                      (((long long)cc.b * p.Sq + i) * p.Hq + cc.hk * p.G + g) * D + 8 * q4;
+                const T *src = reinterpret_cast<const T *>(p.q) + (((long long)cc.b * p.Sq + i) * p.Hq + cc.hk * p.G + g) * D + 8 * q4;
                 uint4 raw[J];
-                float amax = 0.f;
+                uint32_t top = 0u;   // largest magnitudes as bits
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
                     raw[j] = live ? __ldg(reinterpret_cast<const uint4 *>(src + 32 * j)) : make_uint4(0, 0, 0, 0);
-                    amax = fmaxf(amax, p.bf16 ? largest<__nv_bfloat16>(raw[j]) : largest<__half>(raw[j]));
+                    top = max_u16x2(max_u16x2(top, raw[j].x & 0x7fff7fffu), raw[j].y & 0x7fff7fffu);
+                    top = max_u16x2(max_u16x2(top, raw[j].z & 0x7fff7fffu), raw[j].w & 0x7fff7fffu);
                 }
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                top = max(top >> 16, top & 0xffffu);
+                const float amax = Cvt<T>::unpack(top).x;
                 const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 126);
                 const float up = pow2(14 - e), down = pow2(e - 14) * 0x1p24f * (kCap ? p.cap_k : p.scale_log2);
                 float sum[2] = {0.f, 0.f};
 #pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    if (p.bf16) q_operands<__nv_bfloat16>(raw[j], up, qb[nr][j], sum[j / 2]);
-                    else q_operands<__half>(raw[j], up, qb[nr][j], sum[j / 2]);
-                }
+                for (int j = 0; j < J; ++j) q_operands<T>(raw[j], up, qb[nr][j], sum[j / 2]);
                 // a NaN or infinite query: what is left of it is NaN, for its own row only
                 const float dn = amax < INFINITY ? down : NAN;
                 const int hi = cc.n - p.Sq + i;
@@ -534,207 +523,206 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
             hi_all = __reduce_min_sync(0xffffffffu, hi_all);
             begins = cc.t == cc.t0;
             fresh = false;
+            continue;   // (to the loads)
         }
         if (!mbar_wait_warp(bars + 8 * s_at, phase, wctl)) break;
         const uint32_t kt = ring + s_at * C::STAGE, vt = kt + C::KB;
         const uint32_t ks_at = kt + 2 * C::KB + r8 * (4 * GR), vs_at = ks_at + C::SB;
         const uint32_t ok = read >> (4 * s_at) & 15u;
-        // ---- S^T = K Q^T, per 16 keys: scores of keys 16 t + r8 (+ 8), rows 2 q4, + 1
-        float x[NR][4][4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            uint32_t w[2][J];   // key r8, key r8 + 8: the words of chunk j
-            if constexpr (D == 128) {
-                ldmatrix_x4(kt + (2 * t) * 512 + lm_at, w[0]);
-                ldmatrix_x4(kt + (2 * t + 1) * 512 + lm_at, w[1]);
-            } else {
-                uint32_t r[4];
-                ldmatrix_x4(kt + t * 512 + lm_at, r);
-                w[0][0] = r[0], w[0][1] = r[1], w[1][0] = r[2], w[1][1] = r[3];
-            }
-            float a[NR][GR][4];
-#pragma unroll
-            for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-                for (int g = 0; g < GR; ++g)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) a[nr][g][k] = 0.f;
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t u = w[0][j] >> (8 * h), v = w[1][j] >> (8 * h);
-                    const uint32_t A[4] = {u & kLoMask, v & kLoMask, u & kHiMask, v & kHiMask};
-#pragma unroll
-                    for (int nr = 0; nr < NR; ++nr) mma_f16(a[nr][j / 2], A, qb[nr][j][2 * h], qb[nr][j][2 * h + 1]);
-                }
-            uint32_t sm[2][GR];   // (scale, middle) of keys r8, r8 + 8
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) ld_shared_words(ks_at + (16 * t + 8 * hh) * (4 * GR), sm[hh]);
-            const uint32_t w0 = GR == 2 && (q4 & 1) ? sm[0][GR - 1] : sm[0][0], w1 = GR == 2 && (q4 & 1) ? sm[1][GR - 1] : sm[1][0];
-            const uint32_t Z[4] = {w0, w1, w0, w1};
-#pragma unroll
-            for (int nr = 0; nr < NR; ++nr) {
-                float y[4] = {0.f, 0.f, 0.f, 0.f};   // sum over the groups of (middle - 8 scale) Q_g
-                mma_bf16(y, Z, qz[nr][0], qz[nr][1]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-#pragma unroll
-                    for (int g = 0; g < GR; ++g) y[k] = fmaf(scale_of(sm[k >> 1][g]), a[nr][g][k], y[k]);
-                    x[nr][t][k] = y[k];
-                }
-            }
-        }
-        // ---- softmax, and V's scales
-        const int key0 = kTile * cc.t + r8;   // the lane's keys: key0 + 8 u
         const bool ends = cc.t + 1 == cc.t1;
         // a tile inside every row's keys, all its pages read, takes no compare
         const bool edge = ok != whole_tile || kTile * cc.t < lo_all || kTile * cc.t + kTile - 1 > hi_all;
-        uint32_t vsm[8][GR];   // (scale, middle) of V, 0 for keys nobody sees
+#pragma unroll 1
+        for (int t0 = 0; t0 < 4; t0 += KS) {
+            // ---- S^T = K Q^T: scores of keys 16 t + r8 (+ 8), rows 2 q4, + 1
+            float x[NR][KS][4];
+            uint32_t vsm[2 * KS][GR];   // V's (scale, middle) of keys r8 + 8 u, 0 for keys nobody sees
 #pragma unroll
-        for (int u = 0; u < 8; ++u) ld_shared_words(vs_at + 8 * u * (4 * GR), vsm[u]);
-        if (edge) {
-            const int per = bw / 16;
+            for (int u = 0; u < 2 * KS; ++u) ld_shared_words(vs_at + (16 * t0 + 8 * u) * (4 * GR), vsm[u]);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int key = key0 + 8 * u;
-                const bool gone = !(ok >> (per == 4 ? 0 : per == 2 ? u >> 2 : u >> 1) & 1u) || key >= cc.n || key < cc.lo;
+            for (int tt = 0; tt < KS; ++tt) {
+                const uint32_t at = kt + (t0 + tt) * (16 * D / 2) + lm_at;
+                uint32_t w[2][J];   // key r8, key r8 + 8: the words of chunk j
+                if constexpr (D == 128) {
+                    ldmatrix_x4(at, w[0]);
+                    ldmatrix_x4(at + 512, w[1]);
+                } else {
+                    uint32_t r[4];
+                    ldmatrix_x4(at, r);
+                    w[0][0] = r[0], w[0][1] = r[1], w[1][0] = r[2], w[1][1] = r[3];
+                }
+                uint32_t sm[2][GR];   // (scale, middle) of keys r8, r8 + 8
 #pragma unroll
-                for (int g = 0; g < GR; ++g) vsm[u][g] = gone ? 0u : vsm[u][g];
+                for (int hh = 0; hh < 2; ++hh) ld_shared_words(ks_at + (16 * (t0 + tt) + 8 * hh) * (4 * GR), sm[hh]);
+                float a[NR][GR][4];
 #pragma unroll
                 for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        // (under a cap: what lies behind the last token may be NaN, not into the pair)
-                        const bool off = gone || key < lo_r[nr][e] || key > hi_r[nr][e];
-                        if (off) x[nr][u >> 1][2 * (u & 1) + e] = kCap ? 0.f : -INFINITY;
+                    for (int g = 0; g < GR; ++g)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) a[nr][g][k] = 0.f;
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t u = w[0][j] >> (8 * h), v = w[1][j] >> (8 * h);
+                        const uint32_t A[4] = {u & kLoMask, v & kLoMask, u & kHiMask, v & kHiMask};
+#pragma unroll
+                        for (int nr = 0; nr < NR; ++nr) mma_f16(a[nr][j / 2], A, qb[nr][j][2 * h], qb[nr][j][2 * h + 1]);
                     }
-            }
-        }
-        float top = 0.f;   // largest scale of the lane's keys
+                const uint32_t w0 = GR == 2 && (q4 & 1) ? sm[0][GR - 1] : sm[0][0], w1 = GR == 2 && (q4 & 1) ? sm[1][GR - 1] : sm[1][0];
+                const uint32_t Z[4] = {w0, w1, w0, w1};
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            top = GR == 2 ? max3(top, scale_of(vsm[u][0]), scale_of(vsm[u][GR - 1])) : fmaxf(top, scale_of(vsm[u][0]));
-        const float ev = log2_scale(top);
-        uint32_t pt[NR][GR][8];   // P_g^T blocks, transposed: the B operands of O^T
+                for (int nr = 0; nr < NR; ++nr) {
+                    float y[4] = {0.f, 0.f, 0.f, 0.f};   // sum over the groups of (middle - 8 scale) Q_g
+                    mma_bf16(y, Z, qz[nr][0], qz[nr][1]);
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-            if (kCap) {
+                    for (int k = 0; k < 4; ++k) {
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    float *y = &x[nr][u >> 1][2 * (u & 1)], r0, r1;
-                    cap_r2(y[0] * fr[nr][0], y[1] * fr[nr][1], r0, r1);
-                    y[0] = fmaf(-2.f * p.cap_log2, r0, p.cap_log2);
-                    y[1] = fmaf(-2.f * p.cap_log2, r1, p.cap_log2);
-                    if (edge) {
-                        const int key = key0 + 8 * u, per = bw / 16;
-                        const bool gone = !(ok >> (per == 4 ? 0 : per == 2 ? u >> 2 : u >> 1) & 1u);
-                        if (gone || key < lo_r[nr][0] || key > hi_r[nr][0]) y[0] = -INFINITY;
-                        if (gone || key < lo_r[nr][1] || key > hi_r[nr][1]) y[1] = -INFINITY;
+                        for (int g = 0; g < GR; ++g) y[k] = fmaf(scale_of(sm[k >> 1][g]), a[nr][g][k], y[k]);
+                        x[nr][tt][k] = y[k];
                     }
                 }
             }
-            // The references move only where a lane's largest score, or that plus its
-            // largest log2 scale, is 8 above them: mostly in a segment's first tile.
-            // (R then to the largest sum of a key's own two.)
-            float mx[2];
-            bool moves = false;
+            // ---- softmax, and V's scales
+            uint32_t hidden = 0u;   // (under a cap) a bit per score
+            if (edge) {
+                const int per = bw / 16;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float y = x[nr][0][e];
+                for (int u = 0; u < 2 * KS; ++u) {
+                    const int t = t0 + (u >> 1), key = kTile * cc.t + 16 * t0 + 8 * u + r8;
+                    const bool gone = !(ok >> (per == 4 ? 0 : per == 2 ? t >> 1 : t) & 1u) || key >= cc.n || key < cc.lo;
 #pragma unroll
-                for (int u = 1; u < 7; u += 2)
-                    y = max3(y, x[nr][u >> 1][2 * (u & 1) + e], x[nr][(u + 1) >> 1][2 * ((u + 1) & 1) + e]);
-                y = fmaxf(y, x[nr][3][2 + e]);
-                mx[e] = kCap ? y : y * fr[nr][e];
-                moves |= mx[e] > m[nr][e] + kLazy || mx[e] + ev > R[nr][e] + kLazy;
-            }
-            if (__any_sync(0xffffffffu, moves)) {
-                float grow[2], my[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const float lg = log2_scale(fmaxf(scale_of(vsm[u][0]), scale_of(vsm[u][GR - 1])));
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float y = x[nr][u >> 1][2 * (u & 1) + e];
-                        my[e] = fmaxf(my[e], kCap ? y + lg : fmaf(y, fr[nr][e], lg));
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float mn = fmaxf(m[nr][e], keys_max(mx[e])), y = keys_max(my[e]);
-                    mr[nr][e] = mn == -INFINITY ? 0.f : mn;
-                    const float shrink = ex2(m[nr][e] - mr[nr][e]);   // -inf before the first key: 0
-                    m[nr][e] = mn;
-                    l_run[nr][e] *= shrink;
-#pragma unroll
-                    for (int g = 0; g < GR; ++g) zc[nr][g][e] *= shrink;
-                    grow[e] = 1.f;
-                    if (y > R[nr][e] + kLazy || (R[nr][e] == -INFINITY && y > R[nr][e])) {
-                        grow[e] = ex2(R[nr][e] - y);
-                        R[nr][e] = y;
-                    }
-                    fv[nr][e] = R[nr][e] == -INFINITY ? 0.f : ex2(mr[nr][e] - R[nr][e] + 6.f);
-                }
-                auto times = [&](float (&v)[4]) __attribute__((always_inline)) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) v[k] *= grow[k & 1];
-                };
-#pragma unroll
-                for (int dm = 0; dm < DM; ++dm) times(acc[nr][dm]);
-#pragma unroll
-                for (int g = 0; g < GR; ++g) times(eight[nr][g]);
-            }
-            const uint64_t fr2 = f2_pack(fr[nr][0], fr[nr][1]), nm = f2_pack(-mr[nr][0], -mr[nr][1]);
-            const uint64_t fv2 = f2_pack(fv[nr][0], fv[nr][1]);
-            uint64_t sum = f2_pack(l_run[nr][0], l_run[nr][1]);
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const uint64_t x2 = f2_pack(x[nr][u >> 1][2 * (u & 1)], x[nr][u >> 1][2 * (u & 1) + 1]);
-                const float2 y = f2_unpack(kCap ? f2_add(x2, nm) : f2_fma(x2, fr2, nm));
-                const float2 pp = make_float2(ex2(y.x), ex2(y.y));
-                const uint64_t p2 = f2_pack(pp.x, pp.y);
-                sum = f2_add(sum, p2);
-                const float2 w = f2_unpack(f2_mul(p2, fv2));
-#pragma unroll
-                for (int g = 0; g < GR; ++g) {
-                    const float mid = middle_of(vsm[u][g]), sc = scale_of(vsm[u][g]);
-                    zc[nr][g][0] = fmaf(pp.x, mid, zc[nr][g][0]);
-                    zc[nr][g][1] = fmaf(pp.y, mid, zc[nr][g][1]);
-                    pt[nr][g][u] = transpose8(Cvt<__half>::pack(w.x * sc, w.y * sc));
-                }
-            }
-            const float2 l2 = f2_unpack(sum);
-            l_run[nr][0] = l2.x, l_run[nr][1] = l2.y;
-        }
-        // ---- O^T += V^T P^T, per 16 tokens
-        constexpr uint32_t kEight[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            uint32_t w[2][J];   // tokens 2 q4, + 1 and 8 further: dims 32 j + 4 r8 ..
-            if constexpr (D == 128) {
-                ldmatrix_x4_trans(vt + (2 * t) * 512 + lm_at, w[0][0], w[0][1], w[0][2], w[0][3]);
-                ldmatrix_x4_trans(vt + (2 * t + 1) * 512 + lm_at, w[1][0], w[1][1], w[1][2], w[1][3]);
-            } else {
-                ldmatrix_x4_trans(vt + t * 512 + lm_at, w[0][0], w[0][1], w[1][0], w[1][1]);
-            }
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t u = w[0][j] >> (8 * h), v = w[1][j] >> (8 * h);
-                    const uint32_t A[4] = {u & kLoMask, u & kHiMask, v & kLoMask, v & kHiMask};
+                    for (int g = 0; g < GR; ++g) vsm[u][g] = gone ? 0u : vsm[u][g];
 #pragma unroll
                     for (int nr = 0; nr < NR; ++nr)
-                        mma_f16(acc[nr][2 * j + h], A, pt[nr][j / 2][2 * t], pt[nr][j / 2][2 * t + 1]);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (gone || key < lo_r[nr][e] || key > hi_r[nr][e]) {
+                                // (what lies behind the last token may be NaN: not into the cap's pair)
+                                x[nr][u >> 1][2 * (u & 1) + e] = kCap ? 0.f : -INFINITY;
+                                if (kCap) hidden |= 1u << ((nr * 2 * KS + u) * 2 + e);
+                            }
+                }
+            }
+            float top = 0.f;   // largest scale of the lane's keys
+#pragma unroll
+            for (int u = 0; u < 2 * KS; ++u)
+                top = GR == 2 ? max3(top, scale_of(vsm[u][0]), scale_of(vsm[u][GR - 1])) : fmaxf(top, scale_of(vsm[u][0]));
+            const float ev = log2_scale(top);
+            uint32_t pt[NR][GR][2 * KS];   // P_g^T blocks, transposed: the B operands of O^T
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) {
+                if (kCap) {
+#pragma unroll
+                    for (int u = 0; u < 2 * KS; ++u) {
+                        float *y = &x[nr][u >> 1][2 * (u & 1)], r0, r1;
+                        cap_r2(y[0] * fr[nr][0], y[1] * fr[nr][1], r0, r1);
+                        y[0] = fmaf(-2.f * p.cap_log2, r0, p.cap_log2);
+                        y[1] = fmaf(-2.f * p.cap_log2, r1, p.cap_log2);
+                        if (edge && (hidden >> ((nr * 2 * KS + u) * 2) & 1u)) y[0] = -INFINITY;
+                        if (edge && (hidden >> ((nr * 2 * KS + u) * 2) & 2u)) y[1] = -INFINITY;
+                    }
+                }
+                // The references move only where a lane's largest score, or that plus its
+                // largest log2 scale, is 8 above them: mostly in a segment's first tile.
+                // (R then to the largest sum of a key's own two.)
+                float mx[2];
+                bool moves = false;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float y = fmaxf(x[nr][0][e], x[nr][0][2 + e]);
+#pragma unroll
+                    for (int tt = 1; tt < KS; ++tt) y = max3(y, x[nr][tt][e], x[nr][tt][2 + e]);
+                    mx[e] = kCap ? y : y * fr[nr][e];
+                    moves |= mx[e] > m[nr][e] + kLazy || mx[e] + ev > R[nr][e] + kLazy;
+                }
+                if (__any_sync(0xffffffffu, moves)) {
+                    float grow[2], my[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int u = 0; u < 2 * KS; ++u) {
+                        const float lg = log2_scale(fmaxf(scale_of(vsm[u][0]), scale_of(vsm[u][GR - 1])));
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float y = x[nr][u >> 1][2 * (u & 1) + e];
+                            my[e] = fmaxf(my[e], kCap ? y + lg : fmaf(y, fr[nr][e], lg));
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float mn = fmaxf(m[nr][e], keys_max(mx[e])), y = keys_max(my[e]);
+                        mr[nr][e] = mn == -INFINITY ? 0.f : mn;
+                        const float shrink = ex2(m[nr][e] - mr[nr][e]);   // -inf before the first key: 0
+                        m[nr][e] = mn;
+                        l_run[nr][e] *= shrink;
+#pragma unroll
+                        for (int g = 0; g < GR; ++g) zc[nr][g][e] *= shrink;
+                        grow[e] = 1.f;
+                        if (y > R[nr][e] + kLazy || (R[nr][e] == -INFINITY && y > R[nr][e])) {
+                            grow[e] = ex2(R[nr][e] - y);
+                            R[nr][e] = y;
+                        }
+                        fv[nr][e] = R[nr][e] == -INFINITY ? 0.f : ex2(mr[nr][e] - R[nr][e] + 6.f);
+                    }
+                    auto times = [&](float (&v)[4]) __attribute__((always_inline)) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[k] *= grow[k & 1];
+                    };
+#pragma unroll
+                    for (int dm = 0; dm < DM; ++dm) times(acc[nr][dm]);
+#pragma unroll
+                    for (int g = 0; g < GR; ++g) times(eight[nr][g]);
+                }
+                const uint64_t fr2 = f2_pack(fr[nr][0], fr[nr][1]), nm = f2_pack(-mr[nr][0], -mr[nr][1]);
+                const uint64_t fv2 = f2_pack(fv[nr][0], fv[nr][1]);
+                uint64_t sum = f2_pack(l_run[nr][0], l_run[nr][1]);
+#pragma unroll
+                for (int u = 0; u < 2 * KS; ++u) {
+                    const uint64_t x2 = f2_pack(x[nr][u >> 1][2 * (u & 1)], x[nr][u >> 1][2 * (u & 1) + 1]);
+                    const float2 y = f2_unpack(kCap ? f2_add(x2, nm) : f2_fma(x2, fr2, nm));
+                    const float2 pp = make_float2(ex2(y.x), ex2(y.y));
+                    const uint64_t p2 = f2_pack(pp.x, pp.y);
+                    sum = f2_add(sum, p2);
+                    const float2 w = f2_unpack(f2_mul(p2, fv2));
+#pragma unroll
+                    for (int g = 0; g < GR; ++g) {
+                        const float mid = middle_of(vsm[u][g]), sc = scale_of(vsm[u][g]);
+                        zc[nr][g][0] = fmaf(pp.x, mid, zc[nr][g][0]);
+                        zc[nr][g][1] = fmaf(pp.y, mid, zc[nr][g][1]);
+                        pt[nr][g][u] = transpose8(Cvt<__half>::pack(w.x * sc, w.y * sc));
+                    }
+                }
+                const float2 l2 = f2_unpack(sum);
+                l_run[nr][0] = l2.x, l_run[nr][1] = l2.y;
+            }
+            // ---- O^T += V^T P^T
+            constexpr uint32_t kEight[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
+#pragma unroll
+            for (int tt = 0; tt < KS; ++tt) {
+                const uint32_t at = vt + (t0 + tt) * (16 * D / 2) + lm_at;
+                uint32_t w[2][J];   // tokens 2 q4, + 1 and 8 further: dims 32 j + 4 r8 ..
+                if constexpr (D == 128) {
+                    ldmatrix_x4_trans(at, w[0][0], w[0][1], w[0][2], w[0][3]);
+                    ldmatrix_x4_trans(at + 512, w[1][0], w[1][1], w[1][2], w[1][3]);
+                } else {
+                    ldmatrix_x4_trans(at, w[0][0], w[0][1], w[1][0], w[1][1]);
                 }
 #pragma unroll
-            for (int nr = 0; nr < NR; ++nr)
+                for (int j = 0; j < J; ++j)
 #pragma unroll
-                for (int g = 0; g < GR; ++g) mma_f16(eight[nr][g], kEight, pt[nr][g][2 * t], pt[nr][g][2 * t + 1]);
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t u = w[0][j] >> (8 * h), v = w[1][j] >> (8 * h);
+                        const uint32_t A[4] = {u & kLoMask, u & kHiMask, v & kLoMask, v & kHiMask};
+#pragma unroll
+                        for (int nr = 0; nr < NR; ++nr)
+                            mma_f16(acc[nr][2 * j + h], A, pt[nr][j / 2][2 * tt], pt[nr][j / 2][2 * tt + 1]);
+                    }
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                    for (int g = 0; g < GR; ++g) mma_f16(eight[nr][g], kEight, pt[nr][g][2 * tt], pt[nr][g][2 * tt + 1]);
+            }
         }
         --under_way;
-        load(s_at);
         if (++s_at == ST) s_at = 0, phase ^= 1u;
         Cursor nx = cc;
         nx.next(p, s_len);
@@ -768,18 +756,35 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
                             p.lse[((long long)cc.b * p.Hq + hk * p.G + row % p.G) * p.Sq + row / p.G] = lse_of(m[nr][e], l);
                     }
                 }
+                T *dst[2] = {nullptr, nullptr};   // rows 2 q4, + 1 of the output, dim 4 r8
+                if (whole)
 #pragma unroll
-                for (int dm = 0; dm < DM; ++dm) {
-                    float o[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float a = (k < 2 ? acc[nr][dm][k] : acc[nr][dm][k] * 0.0625f) - eight[nr][dm / 4][k & 1];
-                        o[k] = fmaf(a * 0x1p18f, f[k & 1], z[dm / 4][k & 1]);
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = row0 + 2 * q4 + e;
+                        if (row < p.Sq * p.G)
+                            dst[e] = reinterpret_cast<T *>(p.o) + (((long long)cc.b * p.Sq + row / p.G) * p.Hq + hk * p.G + row % p.G) * D + 4 * r8;
                     }
-                    const float4 v = make_float4(o[0], o[1], o[2], o[3]);
-                    if (!whole) reinterpret_cast<float4 *>(p.acc + at * (NR * 8 * D) + nr * 8 * D)[32 * dm + lane] = v;
-                    else if (p.bf16) store_pairs<D, __nv_bfloat16>(p, cc.b, hk, row0, lane, v, dm);
-                    else store_pairs<D, __half>(p, cc.b, hk, row0, lane, v, dm);
+                float4 *const piece = reinterpret_cast<float4 *>(p.acc + at * (NR * 8 * D) + nr * 8 * D) + lane;
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    float o[2][4];   // dims 32 j + 4 r8 + 2 h, + 1 of the two rows
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float a = fmaf(acc[nr][2 * j + h][k], k < 2 ? 1.f : 0.0625f, -eight[nr][j / 2][k & 1]);
+                            o[h][k] = fmaf(a * 0x1p18f, f[k & 1], z[j / 2][k & 1]);
+                        }
+                    if (!whole) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) piece[32 * (2 * j + h)] = make_float4(o[h][0], o[h][1], o[h][2], o[h][3]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (dst[e])
+                                *reinterpret_cast<uint2 *>(dst[e] + 32 * j) =
+                                    make_uint2(Cvt<T>::pack(o[0][e], o[0][2 + e]), Cvt<T>::pack(o[1][e], o[1][2 + e]));
+                    }
                 }
             }
             fresh = true;
@@ -858,10 +863,10 @@ __global__ void __launch_bounds__(2 * D) kv4_join_kernel(const __grid_constant__
     }
 }
 
-template <int D, int NR, bool kCap>
+template <int D, int NR, typename T, bool kCap>
 cudaError_t launch_attn(KvAttnParams p, const CUtensorMap &mk, const CUtensorMap &mv, int sms, cudaStream_t stream) {
     using C = Kv4Cfg<D, NR>;
-    auto kern = kv4_attn_kernel<D, NR, kCap>;
+    auto kern = kv4_attn_kernel<D, NR, T, kCap>;
     p.stages = C::stages(p.B);
     const int smem = C::smem(p.stages, p.B);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -886,12 +891,12 @@ cudaError_t launch_attn(KvAttnParams p, const CUtensorMap &mk, const CUtensorMap
     return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NR>, p);
 }
 
-template <int D>
+template <int D, typename T>
 cudaError_t launch_attn_d(const KvAttnParams &p, const CUtensorMap &mk, const CUtensorMap &mv, int sms, cudaStream_t stream) {
     const bool cap = p.cap_log2 > 0.f;
     if (p.G * p.Sq <= 8)
-        return cap ? launch_attn<D, 1, true>(p, mk, mv, sms, stream) : launch_attn<D, 1, false>(p, mk, mv, sms, stream);
-    return cap ? launch_attn<D, 2, true>(p, mk, mv, sms, stream) : launch_attn<D, 2, false>(p, mk, mv, sms, stream);
+        return cap ? launch_attn<D, 1, T, true>(p, mk, mv, sms, stream) : launch_attn<D, 1, T, false>(p, mk, mv, sms, stream);
+    return cap ? launch_attn<D, 2, T, true>(p, mk, mv, sms, stream) : launch_attn<D, 2, T, false>(p, mk, mv, sms, stream);
 }
 
 // Rows of a CTA whose rows have `per_row` items: about four a thread, one row where
@@ -930,7 +935,9 @@ cudaError_t launch_kv4_read(const KvReadParams &p, int D, int bf16, cudaStream_t
 
 cudaError_t launch_kv4_attn(const KvAttnParams &p, const CUtensorMap &mk, const CUtensorMap &mv, int D, int sms,
                             cudaStream_t stream) {
-    return D == 128 ? launch_attn_d<128>(p, mk, mv, sms, stream) : launch_attn_d<64>(p, mk, mv, sms, stream);
+    if (D == 128)
+        return p.bf16 ? launch_attn_d<128, __nv_bfloat16>(p, mk, mv, sms, stream) : launch_attn_d<128, __half>(p, mk, mv, sms, stream);
+    return p.bf16 ? launch_attn_d<64, __nv_bfloat16>(p, mk, mv, sms, stream) : launch_attn_d<64, __half>(p, mk, mv, sms, stream);
 }
 
 }  // namespace fa
