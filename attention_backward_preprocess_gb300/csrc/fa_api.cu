@@ -951,8 +951,7 @@ fa_status check_kv_cache4(const fa_kv_cache4 *c, int B, fa_dtype dtype, fa::KvCa
     if (!aligned16(c->k_scale) || !aligned16(c->v_scale)) return FA_ERR_INVALID_ARG;
     return check_kv_cache(&same, B, dtype, p);
 }
-// Items of a row of the append and of the read, counted in 32 bits over eight rows.
-constexpr int kKv4MaxHeads = 1 << 20;
+constexpr int kKv4MaxHeads = 1 << 18;   // grid rows of the append and of the read
 
 }  // namespace
 
