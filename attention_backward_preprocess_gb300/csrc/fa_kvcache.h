@@ -71,9 +71,9 @@ constexpr int kKvMaxSeqs = 4096;   // sequences whose tile counts fit shared mem
 inline size_t kv_pieces_bytes(size_t n, int D) { return n * 2 * 16 * (D * sizeof(float) + sizeof(float4)); }
 size_t kv_workspace_bytes(int D);
 // Half tiles that opening and closing a segment counts as where work is shared out.
-constexpr int kKvOpen = 2, kKv4Open = 6;
+constexpr int kKvOpen = 2, kKv4Open = 4;
 // The 4-bit cache's attention has workers of its own number.
-constexpr int kKv4MaxWarps = 12;
+constexpr int kKv4MaxWarps = 8;
 inline size_t kv4_workers() { return (size_t)kKvSms * kKv4MaxWarps; }
 
 cudaError_t launch_kv_append(const KvAppendParams &p, int D, int bf16, cudaStream_t stream);

@@ -281,38 +281,54 @@ __global__ void __launch_bounds__(kRagged) kv4_read_kernel(const __grid_constant
 
 // --------------------------------------------------------------- attention
 // The rows of a kv head's query group times Sq tokens lie along N of m16n8k16
-// products, keys (then dims) along M, as in the 8-bit kernel, and the work is
-// shared out as there: every warp a worker with a contiguous share of all 64-key
-// tiles.  Bytes bound it (D + D / 8 per key against 4 D flops per row and key), so
-// each worker keeps a ring of kStages tiles (codes of K and V, their scales) in
-// shared memory and has all but one of them under way.
+// products, keys (then dims) along M, and the work is shared out as in the 8-bit kernel:
+// every warp a worker with a contiguous share of all 64-key tiles.  Bytes should bound
+// it (D + D / 8 per key against 4 D flops per row and key); a key's codes take about as
+// many instructions to multiply as the memory takes cycles to bring them, so the design
+// spares instructions, and each worker has a ring of tiles (codes of K and V, their scales)
+// in shared memory, all but one under way.
 //
 // S^T.  A key's row of codes is D / 2 bytes; ldmatrix hands lane (r8, q4) the word
 // of dims 32 j + 8 q4 .. + 7 of key r8: masked, the operands (d0, d4), 16 (d1, d5),
 // (d2, d6), 16 (d3, d7).  The contracted axis may be permuted and scaled as long as
 // Q's side agrees: Q lies as f16 under a power of two per row that brings its largest
 // value to [2^14, 2^15), the odd dims at a sixteenth.  (bf16's 8 bits and f16's 11 fit
-// but for values 2^29 below the row's largest.)  With per-group sums Q_g of what the
-// tensor core sees, scale a - 8 scale Q_g + middle Q_g is the group's part of the
-// score: the product starts at -8 Q_g, the rest is two fused operations a group.
+// but for values 2^29 below the row's largest.)  A group's part of the score is scale a +
+// (middle - 8 scale) Q_g, a from the product and Q_g the sum of Q over the group.  The second
+// term is a product of its own: the keys' (scale, middle) words as they lie, two bf16 operands,
+// against (-8 Q_g, Q_g) in three bf16 parts.
 //
 // O^T.  ldmatrix.trans hands lane (r8, q4) 16-bit pieces of tokens 2 q4, + 1: dims 32
 // j + 4 r8 .. + 3 of both, which masked are operands of one dim (or 16 times it) of
 // two neighbouring tokens, so P^T is needed in the keys' own order and the 16 falls
 // on whole rows of the result.  V's scales go into P: P_g = p scale_g in f16, at most
-// about 2^8 against a running maximum R of score + log2(largest scale of the key); the middles' part,
-// sum p middle_g, is kept in 32 bits per row and group, and so is 8 sum P_g, by a
-// product with a constant operand, from the rounded P_g that the codes were
-// multiplied with: the two cancel as exactly as the codes demand.
+// 2^14 against a running reference R of score + log2(largest scale of the key); p's own
+// reference, for sums and middles, is the score alone.  The middles' part, sum p middle_g,
+// is kept in 32 bits per row and group, and so is 8 sum P_g, by a product with a
+// constant operand, from the rounded P_g that the codes were multiplied with: the two
+// cancel as exactly as the codes demand.
 //
 // Codes are finite whatever their bits, so only scores and scales of hidden keys
 // are masked.
+//
+// Measured (64 requests of 256 to 8192 tokens, 32 / 8 heads of 128; two of 64 k capped),
+// the call with its join: 42.4 and 32.8 us, 3.95 TB/s and 3.28.  Of a worker's 74 k cycles
+// the first 12 k pass before its first tile is there (lengths, table, copy: three
+// dependent reads; Q), 5 k at a segment's end; a tile takes 2.9 k, eight at a time on
+// an SM, which is 26 bytes per cycle where the memory gives 23.  What else was measured:
+//   scores by e4m3 products (Q in parts, three operations a word of codes where f16
+//   takes five): 57 us where f16 took 47;
+//   12 warps an SM (16 or 32 keys at a time fit 168 registers): 44.9 and 34.6; 10: 50.4 and
+//   37.4; 6: 54 and 39; three tiles a worker: as two; one: 50.9 and 39;
+//   rows 4 .. 7 left idle where there are four (kSplit): 45.1 and 34.8.
 constexpr uint32_t kLoMask = 0x000f000fu, kHiMask = 0x00f000f0u;
+
+constexpr int kKv4Smem = 232448 - 1024;   // of a CTA, what is not dynamic set aside
 
 template <int D, int NR>
 struct Kv4Cfg {
-    static constexpr int kWarps = NR == 1 ? 12 : 8;
-    static constexpr int kStep = 2;   // 16-key products at a time
+    static constexpr int kWarps = 8;
+    static constexpr int kStep = NR == 1 ? 4 : 2;   // 16-key products at a time
     static constexpr int KB = kTile * D / 2;             // codes of a K (or V) tile
     static constexpr int SB = kTile * (D / 64) * 4;      // its scales
     static constexpr int STAGE = 2 * (KB + SB);
@@ -320,8 +336,8 @@ struct Kv4Cfg {
     // shared memory of a CTA with `stages`, for B sequences (1008: to a whole pattern)
     static constexpr int smem(int stages, int B) { return 1008 + kWarps * stages * STAGE + 8 * B; }
     // One stage less where the sequences' tables want the room.
-    static constexpr int stages(int B) { return smem(kStages, B) <= 232448 - 1024 ? kStages : kStages - 1; }
-    static_assert(smem(kStages - 1, kKvMaxSeqs) <= 232448 - 1024, "shared memory overflow");
+    static constexpr int stages(int B) { return smem(kStages, B) <= kKv4Smem ? kStages : kStages - 1; }
+    static_assert(smem(kStages - 1, kKvMaxSeqs) <= kKv4Smem, "shared memory overflow");
     static_assert(kWarps <= kKv4MaxWarps, "the workspace holds that many workers per SM");
     static_assert(STAGE % 512 == 0 && KB % 512 == 0, "swizzled tiles start on whole patterns");
 };
@@ -378,7 +394,9 @@ __device__ __forceinline__ void store_pairs(const KvAttnParams &p, int b, int hk
         }
 }
 
-template <int D, int NR, typename T, bool kCap>
+// kSplit: at most four rows (NR is 1).  Lanes q4 >= 2, whose rows 4 .. 7 there are not, take
+// the softmax of every second 16 keys off their neighbours q4 - 2.
+template <int D, int NR, typename T, bool kCap, bool kSplit>
 __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
     kv4_attn_kernel(const __grid_constant__ KvAttnParams p, const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v) {
@@ -393,7 +411,21 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
     int *s_pre = reinterpret_cast<int *>(smem_raw + (tiles - smem_u32(smem_raw)) + W * ST * C::STAGE), *s_len = s_pre + p.B;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int r8 = lane >> 2, q4 = lane & 3;
+    // the rows a lane's scores belong to: 2 qr, + 1; which of two 16-key products it takes (kSplit)
+    const int qr = kSplit ? q4 & 1 : q4, odd = kSplit ? q4 >> 1 : 0;
+    static_assert(!kSplit || (NR == 1 && KS % 2 == 0), "pairs of products");
+    constexpr int KU = kSplit ? KS / 2 : KS;   // 16-key products whose softmax a lane takes part in
 
+    // The block table and Q on their way from memory while the lengths are read: a line a
+    // thread (what lies further comes when it is wanted).
+    {
+        const long long line = (long long)(blockIdx.x * W * 32 + threadIdx.x) * 128;
+        if (line < (long long)p.B * p.c.max_pages * 4)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(p.c.table) + line));
+        if (line < (long long)p.B * p.Sq * p.Hq * D * 2)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(p.q) + line));
+    }
+    if (threadIdx.x == 32) prefetch_tmap(&map_k), prefetch_tmap(&map_v);
     if (threadIdx.x == 0) s_abort = 0;
     if (lane == 0) p.meta[blockIdx.x * W + warp] = make_int4(-1, 0, 0, 0);
     if (lane < ST) {
@@ -497,7 +529,16 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
     const uint32_t lm_at = D == 128 ? lr * 64 + ((lm ^ (lr >> 1)) << 4)
                                     : ((lm >> 1) * 8 + lr) * 32 + (((lm & 1) ^ (lr >> 2)) << 4);
 
-    // ---- state of the segment being computed: row block nr, row 2 q4 + e of it
+    // over the lanes that hold a row's keys
+    auto row_max = [&](float v) __attribute__((always_inline)) -> float {
+        v = keys_max(v);
+        return kSplit ? fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2)) : v;
+    };
+    auto row_sum = [&](float v) __attribute__((always_inline)) -> float {
+        v = keys_sum(v);
+        return kSplit ? v + __shfl_xor_sync(0xffffffffu, v, 2) : v;
+    };
+    // ---- state of the segment being computed: row block nr, row 2 qr + e of it
     uint32_t qb[NR][J][4];       // Q's operands
     uint32_t qz[NR][2];          // its sums per group, as the operand of scales and middles
     float fr[NR][2];             // undoes the units and Q's power of two, times c log2(e) (or the cap's factor); > 0
@@ -564,7 +605,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
                 }
 #pragma unroll
                 for (int e2 = 0; e2 < 2; ++e2) {   // the rows a lane's scores belong to
-                    const int src_lane = 4 * (2 * q4 + e2);
+                    const int src_lane = 4 * (2 * qr + e2);
                     fr[nr][e2] = __shfl_sync(0xffffffffu, dn, src_lane);
                     hi_r[nr][e2] = __shfl_sync(0xffffffffu, hi, src_lane);
                     lo_r[nr][e2] = p.window < 0 ? 0 : max(0, hi_r[nr][e2] - p.window);
@@ -600,9 +641,11 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
         for (int t0 = 0; t0 < 4; t0 += KS) {
             // ---- S^T = K Q^T: scores of keys 16 t + r8 (+ 8), rows 2 q4, + 1
             float x[NR][KS][4];
-            uint32_t vsm[2 * KS][GR];   // V's (scale, middle) of keys r8 + 8 u, 0 for keys nobody sees
+            uint32_t vsm[2 * KU][GR];   // V's (scale, middle) of the lane's keys, 0 for keys nobody sees
+            // product of its keys u (two each): rows r8 (+ 8) of it
+            auto tile_of = [&](int u) __attribute__((always_inline)) -> int { return t0 + (kSplit ? (u & ~1) + odd : u >> 1); };
 #pragma unroll
-            for (int u = 0; u < 2 * KS; ++u) ld_shared_words(vs_at + (16 * t0 + 8 * u) * (4 * GR), vsm[u]);
+            for (int u = 0; u < 2 * KU; ++u) ld_shared_words(vs_at + (16 * tile_of(u) + 8 * (u & 1)) * (4 * GR), vsm[u]);
 #pragma unroll
             for (int tt = 0; tt < KS; ++tt) {
                 const uint32_t at = kt + (t0 + tt) * (16 * D / 2) + lm_at;
@@ -647,13 +690,23 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
                     }
                 }
             }
+            if (kSplit) {
+#pragma unroll
+                for (int i = 0; i < KU; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float own = x[0][2 * i][k], other = x[0][2 * i + 1][k];
+                        const float got = __shfl_xor_sync(0xffffffffu, other, 2);   // (of lanes q4 < 2; they ignore theirs)
+                        x[0][i][k] = odd ? got : own;
+                    }
+            }
             // ---- softmax, and V's scales
             uint32_t hidden = 0u;   // (under a cap) a bit per score
             if (edge) {
                 const int per = bw / 16;
 #pragma unroll
-                for (int u = 0; u < 2 * KS; ++u) {
-                    const int t = t0 + (u >> 1), key = kTile * cc.t + 16 * t0 + 8 * u + r8;
+                for (int u = 0; u < 2 * KU; ++u) {
+                    const int t = tile_of(u), key = kTile * cc.t + 16 * t + 8 * (u & 1) + r8;
                     const bool gone = !(ok >> (per == 4 ? 0 : per == 2 ? t >> 1 : t) & 1u) || key >= cc.n || key < cc.lo;
 #pragma unroll
                     for (int g = 0; g < GR; ++g) vsm[u][g] = gone ? 0u : vsm[u][g];
@@ -664,27 +717,27 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
                             if (gone || key < lo_r[nr][e] || key > hi_r[nr][e]) {
                                 // (what lies behind the last token may be NaN: not into the cap's pair)
                                 x[nr][u >> 1][2 * (u & 1) + e] = kCap ? 0.f : -INFINITY;
-                                if (kCap) hidden |= 1u << ((nr * 2 * KS + u) * 2 + e);
+                                if (kCap) hidden |= 1u << ((nr * 2 * KU + u) * 2 + e);
                             }
                 }
             }
             float top = 0.f;   // largest scale of the lane's keys
 #pragma unroll
-            for (int u = 0; u < 2 * KS; ++u)
+            for (int u = 0; u < 2 * KU; ++u)
                 top = GR == 2 ? max3(top, scale_of(vsm[u][0]), scale_of(vsm[u][GR - 1])) : fmaxf(top, scale_of(vsm[u][0]));
             const float ev = log2_scale(top);
-            uint32_t pt[NR][GR][2 * KS];   // P_g^T blocks, transposed: the B operands of O^T
+            uint32_t pt[NR][GR][2 * KU];   // P_g^T blocks, transposed: the B operands of O^T
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr) {
                 if (kCap) {
 #pragma unroll
-                    for (int u = 0; u < 2 * KS; ++u) {
+                    for (int u = 0; u < 2 * KU; ++u) {
                         float *y = &x[nr][u >> 1][2 * (u & 1)], r0, r1;
                         cap_r2(y[0] * fr[nr][0], y[1] * fr[nr][1], r0, r1);
                         y[0] = fmaf(-2.f * p.cap_log2, r0, p.cap_log2);
                         y[1] = fmaf(-2.f * p.cap_log2, r1, p.cap_log2);
-                        if (edge && (hidden >> ((nr * 2 * KS + u) * 2) & 1u)) y[0] = -INFINITY;
-                        if (edge && (hidden >> ((nr * 2 * KS + u) * 2) & 2u)) y[1] = -INFINITY;
+                        if (edge && (hidden >> ((nr * 2 * KU + u) * 2) & 1u)) y[0] = -INFINITY;
+                        if (edge && (hidden >> ((nr * 2 * KU + u) * 2) & 2u)) y[1] = -INFINITY;
                     }
                 }
                 // The references move only where a lane's largest score, or that plus its
@@ -696,14 +749,14 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
                 for (int e = 0; e < 2; ++e) {
                     float y = fmaxf(x[nr][0][e], x[nr][0][2 + e]);
 #pragma unroll
-                    for (int tt = 1; tt < KS; ++tt) y = max3(y, x[nr][tt][e], x[nr][tt][2 + e]);
+                    for (int tt = 1; tt < KU; ++tt) y = max3(y, x[nr][tt][e], x[nr][tt][2 + e]);
                     mx[e] = kCap ? y : y * fr[nr][e];
                     moves |= mx[e] > m[nr][e] + kLazy || mx[e] + ev > R[nr][e] + kLazy;
                 }
                 if (__any_sync(0xffffffffu, moves)) {
                     float grow[2], my[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int u = 0; u < 2 * KS; ++u) {
+                    for (int u = 0; u < 2 * KU; ++u) {
                         const float lg = log2_scale(fmaxf(scale_of(vsm[u][0]), scale_of(vsm[u][GR - 1])));
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
@@ -713,7 +766,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
                     }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float mn = fmaxf(m[nr][e], keys_max(mx[e])), y = keys_max(my[e]);
+                        const float mn = fmaxf(m[nr][e], row_max(mx[e])), y = row_max(my[e]);
                         mr[nr][e] = mn == -INFINITY ? 0.f : mn;
                         const float shrink = ex2(m[nr][e] - mr[nr][e]);   // -inf before the first key: 0
                         m[nr][e] = mn;
@@ -740,7 +793,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
                 const uint64_t fv2 = f2_pack(fv[nr][0], fv[nr][1]);
                 uint64_t sum = f2_pack(l_run[nr][0], l_run[nr][1]);
 #pragma unroll
-                for (int u = 0; u < 2 * KS; ++u) {
+                for (int u = 0; u < 2 * KU; ++u) {
                     const uint64_t x2 = f2_pack(x[nr][u >> 1][2 * (u & 1)], x[nr][u >> 1][2 * (u & 1) + 1]);
                     const float2 y = f2_unpack(kCap ? f2_add(x2, nm) : f2_fma(x2, fr2, nm));
                     const float2 pp = make_float2(ex2(y.x), ex2(y.y));
@@ -762,6 +815,18 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
             constexpr uint32_t kEight[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
 #pragma unroll
             for (int tt = 0; tt < KS; ++tt) {
+                // (kSplit: rows 4 .. 7 of P are rows 0 .. 3 of the pair's second product, and what they
+                // sum to, of this one's V, goes unread)
+                uint32_t P[NR][GR][2];
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                    for (int g = 0; g < GR; ++g)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            P[nr][g][k] = pt[nr][g][2 * (kSplit ? tt / 2 : tt) + k];
+                            if (kSplit && (tt & 1)) P[nr][g][k] = __shfl_xor_sync(0xffffffffu, P[nr][g][k], 16);
+                        }
                 const uint32_t at = vt + (t0 + tt) * (16 * D / 2) + lm_at;
                 uint32_t w[2][J];   // tokens 2 q4, + 1 and 8 further: dims 32 j + 4 r8 ..
                 if constexpr (D == 128) {
@@ -777,13 +842,12 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
                         const uint32_t u = w[0][j] >> (8 * h), v = w[1][j] >> (8 * h);
                         const uint32_t A[4] = {u & kLoMask, u & kHiMask, v & kLoMask, v & kHiMask};
 #pragma unroll
-                        for (int nr = 0; nr < NR; ++nr)
-                            mma_f16(acc[nr][2 * j + h], A, pt[nr][j / 2][2 * tt], pt[nr][j / 2][2 * tt + 1]);
+                        for (int nr = 0; nr < NR; ++nr) mma_f16(acc[nr][2 * j + h], A, P[nr][j / 2][0], P[nr][j / 2][1]);
                     }
 #pragma unroll
                 for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                    for (int g = 0; g < GR; ++g) mma_f16(eight[nr][g], kEight, pt[nr][g][2 * tt], pt[nr][g][2 * tt + 1]);
+                    for (int g = 0; g < GR; ++g) mma_f16(eight[nr][g], kEight, P[nr][g][0], P[nr][g][1]);
             }
         }
         --under_way;
@@ -807,9 +871,9 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
                 float f[2], z[GR][2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float l = keys_sum(l_run[nr][e]), out = whole ? out_factor(0.f, 0.f, l) : 1.f;
+                    const float l = row_sum(l_run[nr][e]), out = whole ? out_factor(0.f, 0.f, l) : 1.f;
 #pragma unroll
-                    for (int g = 0; g < GR; ++g) z[g][e] = keys_sum(zc[nr][g][e]) * out;
+                    for (int g = 0; g < GR; ++g) z[g][e] = row_sum(zc[nr][g][e]) * out;
                     // what brings acc from R to m
                     f[e] = R[nr][e] == -INFINITY ? 0.f : ex2(R[nr][e] - mr[nr][e]) * out;
                     const int row = row0 + 2 * q4 + e;
@@ -927,10 +991,10 @@ __global__ void __launch_bounds__(2 * D) kv4_join_kernel(const __grid_constant__
     }
 }
 
-template <int D, int NR, typename T, bool kCap>
+template <int D, int NR, typename T, bool kCap, bool kSplit>
 cudaError_t launch_attn(KvAttnParams p, const CUtensorMap &mk, const CUtensorMap &mv, int sms, cudaStream_t stream) {
     using C = Kv4Cfg<D, NR>;
-    auto kern = kv4_attn_kernel<D, NR, T, kCap>;
+    auto kern = kv4_attn_kernel<D, NR, T, kCap, kSplit>;
     p.stages = C::stages(p.B);
     const int smem = C::smem(p.stages, p.B);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -958,9 +1022,12 @@ cudaError_t launch_attn(KvAttnParams p, const CUtensorMap &mk, const CUtensorMap
 template <int D, typename T>
 cudaError_t launch_attn_d(const KvAttnParams &p, const CUtensorMap &mk, const CUtensorMap &mv, int sms, cudaStream_t stream) {
     const bool cap = p.cap_log2 > 0.f;
-    if (p.G * p.Sq <= 8)
-        return cap ? launch_attn<D, 1, T, true>(p, mk, mv, sms, stream) : launch_attn<D, 1, T, false>(p, mk, mv, sms, stream);
-    return cap ? launch_attn<D, 2, T, true>(p, mk, mv, sms, stream) : launch_attn<D, 2, T, false>(p, mk, mv, sms, stream);
+    const int rows = p.G * p.Sq;
+    if (rows <= 4)
+        return cap ? launch_attn<D, 1, T, true, true>(p, mk, mv, sms, stream) : launch_attn<D, 1, T, false, true>(p, mk, mv, sms, stream);
+    if (rows <= 8)
+        return cap ? launch_attn<D, 1, T, true, false>(p, mk, mv, sms, stream) : launch_attn<D, 1, T, false, false>(p, mk, mv, sms, stream);
+    return cap ? launch_attn<D, 2, T, true, false>(p, mk, mv, sms, stream) : launch_attn<D, 2, T, false, false>(p, mk, mv, sms, stream);
 }
 
 // CTAs of a ragged call: about `each` parts a thread, fewer rows where that would

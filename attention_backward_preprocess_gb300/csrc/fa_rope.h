@@ -25,8 +25,11 @@ struct RopeParams {
     int in_place;             // out is in: the dims behind R stay
     // filled by launch_rope
     int units;                // pieces of a head a thread takes at a time
+    int heads_at_once;        // heads whose pieces a CTA's threads cover, in rows
+    int step_rows, step_heads;   // and heads beyond them
     int rows_per_cta;
-    uint32_t by_units, by_row; // divide by units, and by units of a row: x * m >> 32, exact for what is divided
+    uint32_t by_units;        // divides a thread's number by units
+    int batches;              // sequences with rows apart from each other (1: all rows evenly spaced)
 };
 
 cudaError_t launch_rope(RopeParams p, int interleaved, int bf16, int sms, cudaStream_t stream);
