@@ -316,7 +316,8 @@ class KvCache4(_PagedCache):
     def __init__(self, k, v, k_scale, v_scale, block_table):
         if k.dim() != 4 or block_table.dim() != 2:
             raise ValueError("k: [pages, Hkv, page, D / 2], block_table: [B, max_pages]")
-        P, H, ps, D = k.shape[0], k.shape[1], k.shape[2], 2 * k.shape[3]
+        P, H, ps, D = k.shape
+        D *= 2
         self.B = block_table.shape[0]
         self.device = k.get_device()   # index, -1: not on a GPU
         if self.device < 0 or not _binding().cache4(k, v, k_scale, v_scale, block_table):

@@ -12,6 +12,8 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -49,6 +51,13 @@ PyObject *none() { Py_RETURN_NONE; }
 int current() {
     c10::DeviceIndex d = -1;
     return c10::cuda::GetDevice(&d) == cudaSuccess ? d : -1;
+}
+
+// A new contiguous tensor on the current device: at::empty without the dispatcher's
+// rounds, a microsecond each of a small call's five.
+at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type) {
+    return at::detail::empty_generic(sizes, c10::cuda::CUDACachingAllocator::get(),
+                                     c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt);
 }
 
 struct Call {   // what the forward and the backward share
@@ -351,9 +360,9 @@ template <typename Cache> PyObject *attend_over(PyObject *const *a, Py_ssize_t n
         if (PyErr_Occurred() || window > 0x7fffffffL || window < -0x7fffffffL) return none();
         const size_t bytes = attend_bytes(kc);
         if (bytes == 0) return none();
-        at::Tensor o = at::empty(q->sizes(), q->options());
-        at::Tensor lse = at::empty({q->size(0), q->size(2), q->size(1)}, q->options().dtype(at::kFloat));
-        at::Tensor ws = at::empty({(int64_t)bytes}, q->options().dtype(at::kByte));
+        at::Tensor o = fresh(q->sizes(), ty);
+        at::Tensor lse = fresh({q->size(0), q->size(2), q->size(1)}, at::kFloat);
+        at::Tensor ws = fresh({(int64_t)bytes}, at::kByte);
         const fa_status st =
             call_attend(q->data_ptr(), kc, (const int *)len->data_ptr(), o.data_ptr(), (float *)lse.data_ptr(), (int)B,
                         (int)q->size(1), (int)q->size(2), scale, cap, (int)window,
@@ -378,8 +387,8 @@ PyObject *read4(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (!fits(len, B) || !fits(cu, B + 1) || !fits(first, B)) return none();
         if (rows <= 0 || rows > 0x7fffffffL) return none();
         const bool bf16 = a[6] == Py_True;
-        const auto opt = at::TensorOptions().dtype(bf16 ? at::kBFloat16 : at::kHalf).device(at::kCUDA, (int)dev);
-        at::Tensor k = at::empty({rows, kc->Hkv, kc->D}, opt), v = at::empty({rows, kc->Hkv, kc->D}, opt);
+        const at::ScalarType ty = bf16 ? at::kBFloat16 : at::kHalf;
+        at::Tensor k = fresh({rows, kc->Hkv, kc->D}, ty), v = fresh({rows, kc->Hkv, kc->D}, ty);
         const fa_status st = fa_kvcache4_read(kc, (const int *)len->data_ptr(), first ? (const int *)first->data_ptr() : nullptr,
                                               (const int *)cu->data_ptr(), (int)rows, (int)B, k.data_ptr(), v.data_ptr(),
                                               bf16 ? FA_BF16 : FA_FP16, stream((int)dev));
@@ -413,7 +422,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
                 x[i]->size(0) != B || x[i]->size(1) != S || x[i]->size(3) != D || x[i]->numel() == 0 ||
                 x[i]->size(2) > 0x7fffffff || !strides(*x[i], t[i].in_stride))
                 return none();
-            out[i] = at::empty(x[i]->sizes(), x[i]->options());
+            out[i] = fresh(x[i]->sizes(), ty);
             t[i].in = x[i]->data_ptr();
             t[i].out = out[i].data_ptr();
             t[i].heads = (int)x[i]->size(2);
