@@ -38,11 +38,11 @@ template <typename T> __device__ __forceinline__ void turn_pair(uint32_t &a, flo
 
 // A thread keeps its piece u of a head and goes from head to head (and row to row) of
 // the CTA: a piece then costs no division and its cosines' place is known.  2 x 8192
-// rows of 40 heads of 128: 55.3 us (6.06 TB/s, 89 % of a copy's rate) at six CTAs an SM, 57.4
-// at five, 68 at eight (registers in memory), 65.8 with half the rows a CTA, whose
-// cosines then come too often.
+// rows of 40 heads of 128: 52.5 us (6.39 TB/s, 94 % of a copy's rate) at five CTAs an SM, 53
+// at six (registers in memory), 57.4 at seven; 55.4 with twice the rows a CTA, 55.3 with the
+// cosines in the pairs' order, 57.4 with two divisions a piece besides.
 template <typename T, RopeKind kKind>
-__global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 5) rope_kernel(const __grid_constant__ RopeParams p) {
     __shared__ __align__(16) float2 s_cs[kMaxRows][kMaxPairs];   // factor (cos, sin)
     const int row0 = blockIdx.x * p.rows_per_cta;   // (rows are below 2^31)
     const int rows = min(p.rows_per_cta, p.B * p.S - row0);
@@ -52,6 +52,8 @@ __global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant
     // a piece's first dim, and (halves) the other one's
     const int d0 = kKind == kHalves ? (8 * u < half ? 8 * u : p.R + 8 * u - half)
                    : kKind == kInterleaved ? 8 * u : (u < half ? u : u + half);
+    constexpr int kPairs = kKind == kHalves ? 8 : 4;   // of a piece
+    const int pieces = (half + kPairs - 1) / kPairs;   // that turn
     const bool turns = kKind == kInterleaved || (kKind == kHalves ? 8 * u < half : u < half);
     struct At {
         int r, h;   // row of the CTA, head of q and k together
@@ -91,7 +93,10 @@ __global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant
         const unsigned long long turns_at = (unsigned long long)pos * p.steps[j];
         float sn, cs;
         sincospif((float)(int)(turns_at >> 32) * 0x1p-31f, &sn, &cs);
-        s_cs[r][j] = make_float2(cs * p.factor, sn * (p.inverse ? -p.factor : p.factor));
+        // pairs in twos: the first two of every piece, then the next two of every piece ..., so that
+        // neighbouring pieces' reads lie side by side (in the pairs' order, four times the wavefronts)
+        const int at = kKind == kScalar ? j : ((j % kPairs / 2) * pieces + j / kPairs) * 2 + j % 2;
+        s_cs[r][at] = make_float2(cs * p.factor, sn * (p.inverse ? -p.factor : p.factor));
     }
     __syncthreads();
     auto store = [&](const At &x, uint4 a, uint4 c) __attribute__((always_inline)) {
@@ -100,17 +105,17 @@ __global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant
         const float2 *cs = s_cs[x.r];
         if (kKind == kHalves) {
             if (turns) {
-                const float4 *q = reinterpret_cast<const float4 *>(cs + 8 * u);
+                const float4 *q = reinterpret_cast<const float4 *>(cs) + u;
                 turn<T>(a.x, c.x, q[0]);
-                turn<T>(a.y, c.y, q[1]);
-                turn<T>(a.z, c.z, q[2]);
-                turn<T>(a.w, c.w, q[3]);
+                turn<T>(a.y, c.y, q[pieces]);
+                turn<T>(a.z, c.z, q[2 * pieces]);
+                turn<T>(a.w, c.w, q[3 * pieces]);
                 __stcs(reinterpret_cast<uint4 *>(out + half), c);
             }
             __stcs(reinterpret_cast<uint4 *>(out), a);
         } else if (kKind == kInterleaved) {
-            const float4 *q = reinterpret_cast<const float4 *>(cs + 4 * u);   // (beyond R: not looked at)
-            const float4 v0 = q[0], v1 = q[1];
+            const float4 *q = reinterpret_cast<const float4 *>(cs) + min(u, pieces - 1);   // (beyond R: not looked at)
+            const float4 v0 = q[0], v1 = q[pieces];
             if (4 * u < half) turn_pair<T>(a.x, v0.x, v0.y);
             if (4 * u + 1 < half) turn_pair<T>(a.y, v0.z, v0.w);
             if (4 * u + 2 < half) turn_pair<T>(a.z, v1.x, v1.y);
