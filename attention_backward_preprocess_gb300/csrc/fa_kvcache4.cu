@@ -34,6 +34,9 @@ struct Ragged {
     }
 };
 
+// (borders may be anything: the difference as 32 bits hold it)
+__device__ __forceinline__ int rows_between(int at, int end) { return (int)((unsigned)end - (unsigned)at); }
+
 constexpr int kRagged = 256;   // threads of a CTA
 constexpr int kMaxRows = 16;   // rows of it
 
@@ -78,7 +81,7 @@ __device__ __forceinline__ void place_rows(const Ragged &r, int row0, int n_rows
         long long place = -1;
         if (b < r.B) {
             at = !r.cu ? b * r.max_new : staged ? s_cu[b] : __ldg(r.cu + b);
-            n = !r.cu ? r.max_new : end(b) - at;
+            n = !r.cu ? r.max_new : rows_between(at, end(b));
             held = r.cu && staged ? s_len[b] : __ldg(r.len + b);
             from = !r.first ? 0 : staged ? s_first[b] : __ldg(r.first + b);
             if (row >= at && r.fits(at, n, held, from)) {
@@ -96,7 +99,7 @@ __device__ __forceinline__ void place_rows(const Ragged &r, int row0, int n_rows
 __device__ __forceinline__ void check_ragged(const Ragged &r) {
     if (blockIdx.x != 0 || blockIdx.y != 0) return;
     for (int b = threadIdx.x; b < r.B; b += kRagged) {
-        const int at = r.cu ? r.cu[b] : b * r.max_new, n = r.cu ? r.cu[b + 1] - at : r.max_new;
+        const int at = r.cu ? r.cu[b] : b * r.max_new, n = r.cu ? rows_between(at, r.cu[b + 1]) : r.max_new;
         if (!r.fits(at, n, r.len[b], r.first ? r.first[b] : 0)) atomicOr(r.c.err, kErrBadLength);
     }
 }
@@ -1036,7 +1039,7 @@ template <int D> dim3 ragged_grid(int rows, int Hkv, int each, int *per_cta) {
     const long long parts = 2LL * Hkv * (D / 16), n = each * kRagged / parts, most = rows / 608;
     const long long m = n < most ? n : most;
     *per_cta = (int)(m < 1 ? 1 : m > kMaxRows ? kMaxRows : m);
-    return dim3((unsigned)((rows + *per_cta - 1) / *per_cta), (unsigned)((parts + kRagged - 1) / kRagged));
+    return dim3((unsigned)(((long long)rows + *per_cta - 1) / *per_cta), (unsigned)((parts + kRagged - 1) / kRagged));
 }
 
 template <int D, typename T>

@@ -405,27 +405,28 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (!x[0] || (!x[1] && a[1] != Py_None) || !steps || (!pos && a[4] != Py_None) || (!off && a[5] != Py_None))
             return none();
         const float factor = (float)PyFloat_AsDouble(a[3]);
-        if (PyErr_Occurred() || !x[0]->is_cuda() || x[0]->dim() != 4) return none();
+        if (PyErr_Occurred() || !x[0]->is_cuda() || (x[0]->dim() != 4 && x[0]->dim() != 3)) return none();
         const int dev = x[0]->get_device();
         const at::ScalarType ty = x[0]->scalar_type();
-        const int64_t B = x[0]->size(0), S = x[0]->size(1), D = x[0]->size(3);
+        const int64_t nd = x[0]->dim(), B = nd == 4 ? x[0]->size(0) : 1, S = x[0]->size(nd - 3), D = x[0]->size(nd - 1);
         if (dev != current() || (ty != at::kBFloat16 && ty != at::kHalf) || B > 0x7fffffff || S > 0x7fffffff ||
             !plain(*steps, at::kLong, dev) || steps->dim() != 1 || steps->size(0) > 0x3fffffff)
             return none();
-        if (pos && (!plain(*pos, at::kInt, dev) || pos->sizes() != at::IntArrayRef({B, S}))) return none();
+        if (pos && (!plain(*pos, at::kInt, dev) || pos->sizes() != x[0]->sizes().slice(0, nd - 2))) return none();
         if (off && (!plain(*off, at::kInt, dev) || off->sizes() != at::IntArrayRef({B}))) return none();
         fa_rope_tensor t[2];
         std::memset(t, 0, sizeof(t));
         at::Tensor out[2];
         for (int i = 0; i < 2 && x[i]; ++i) {
-            if (!x[i]->is_cuda() || x[i]->get_device() != dev || x[i]->scalar_type() != ty || x[i]->dim() != 4 ||
-                x[i]->size(0) != B || x[i]->size(1) != S || x[i]->size(3) != D || x[i]->numel() == 0 ||
-                x[i]->size(2) > 0x7fffffff || !strides(*x[i], t[i].in_stride))
+            if (!x[i]->is_cuda() || x[i]->get_device() != dev || x[i]->scalar_type() != ty || x[i]->dim() != nd ||
+                x[i]->sizes().slice(0, nd - 2) != x[0]->sizes().slice(0, nd - 2) || x[i]->size(nd - 1) != D ||
+                x[i]->numel() == 0 || x[i]->size(nd - 2) > 0x7fffffff ||
+                !(nd == 4 ? strides(*x[i], t[i].in_stride) : x[i]->is_contiguous()))
                 return none();
             out[i] = fresh(x[i]->sizes(), ty);
             t[i].in = x[i]->data_ptr();
             t[i].out = out[i].data_ptr();
-            t[i].heads = (int)x[i]->size(2);
+            t[i].heads = (int)x[i]->size(nd - 2);
         }
         const fa_status st = fa_rope(&t[0], x[1] ? &t[1] : nullptr, (int)B, (int)S, (int)D, 2 * (int)steps->size(0),
                                      (const unsigned long long *)steps->data_ptr(), factor, PyObject_IsTrue(a[6]),

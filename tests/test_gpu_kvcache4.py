@@ -278,6 +278,10 @@ ATTEND = [
     ([333, 112, 113], 1, 3, 1, 64, 112, BF, 0.0, -1),
     ([(7 * i) % 41 for i in range(700)], 1, 1, 1, 64, 16, F16, 0.0, -1),   # more sequences than threads
     ([(5 * i) % 23 for i in range(1300)], 1, 1, 1, 128, 16, BF, 0.0, -1),  # so many that a stage of the ring makes room
+    ([(5 * i) % 67 for i in range(3000)], 1, 2, 1, 64, 64, F16, 0.0, -1),  # more still
+    ([400, 31, 9], 2, 4, 2, 128, 16, F16, 20.0, 70),        # four rows: capped, in a window, small pages
+    ([400, 31, 9], 1, 4, 1, 64, 32, BF, 50.0, -1),
+    ([77, 300], 4, 2, 2, 64, 128, F16, 0.0, 33),
 ]
 
 
@@ -308,6 +312,84 @@ def test_attention_over_the_cache(fa, cuda_device, c):
     check(o, ro, off, "o")
     check_lse(lse, rl, lse_off)
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seed", range(40))
+def test_attention_of_any_sizes(fa, cuda_device, seed):
+    """Sizes, pages, masks and types drawn at random."""
+    r = torch.Generator().manual_seed(100 + seed)
+    pick = lambda *x: x[int(torch.randint(0, len(x), (), generator=r))]   # noqa: E731
+    Hkv, cap = pick(1, 2, 3), pick(0.0, 0.0, 15.0)
+    lens = [int(n) for n in torch.randint(0, pick(20, 200, 900), (pick(1, 2, 5),), generator=r)]
+    c = (lens, pick(1, 1, 2, 3, 5), Hkv * pick(1, 2, 3, 4, 8), Hkv, pick(64, 128), pick(16, 32, 48, 64, 80, 128), pick(BF, F16),
+         cap, pick(-1, -1, 0, 15, 100))
+    q, cache, n, plain = _attend(fa, c, seed, a=2.0 if cap else 1.0)
+    o, lse = fa.fa_fwd_kvcache4(q.cuda(), cache, n, softcap=cap, window_left=c[8])
+    assert fa.device_status() == fa.FA_OK
+    ro, rl, off, lse_off = plain_attention(q, *plain, c[4] ** -0.5, cap, c[8])
+    check(o, ro, off, "o of %r" % (c,))
+    check_lse(lse, rl, lse_off)
+
+
+@pytest.mark.gpu
+def test_a_heavy_scale_nobody_looks_at(fa, cuda_device):
+    """Tokens with V scales 2^40 above the others' and scores far below: their weight
+    is nothing, and the others keep theirs."""
+    c = ([500, 64], 1, 4, 1, 128, 16, BF, 0.0, -1)
+    q, cache, n, plain = _attend(fa, c, 31, 3.0)
+    ks, vs, table = plain[2], plain[3], plain[4]
+    for b, tokens in enumerate(c[0]):
+        for t in range(0, tokens, 7):   # a key that is a large multiple of -q: its score is about -2 |q|^2 c < -150
+            at, slot = int(table[b, t // 16]), t % 16
+            x = -q[b, 0].double().mean(dim=0) * 2
+            code, s = _keys_like(x)
+            plain[0][at, 0, slot], ks[at, 0, slot] = code, s
+            vs[at, 0, slot, :, 0] *= 2.0 ** 40
+    cache.k.copy_(plain[0])
+    cache.k_scale.copy_(ks)
+    cache.v_scale.copy_(vs)
+    o, lse = fa.fa_fwd_kvcache4(q.cuda(), cache, n)
+    ro, rl, off, lse_off = plain_attention(q, *plain, 128 ** -0.5, 0.0, -1)
+    check(o, ro, off, "o")
+    check_lse(lse, rl, lse_off)
+
+
+def _keys_like(x):
+    c, s = quantise(x.float()[None])
+    return c[0], s[0]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seed", range(20))
+def test_append_and_read_of_any_sizes(fa, cuda_device, seed):
+    """Appends of random sizes behind each other, then everything read back."""
+    r = torch.Generator().manual_seed(200 + seed)
+    pick = lambda *x: x[int(torch.randint(0, len(x), (), generator=r))]   # noqa: E731
+    B, H, D, page, dt = pick(1, 3, 40, 270), pick(1, 2, 5, 8), pick(64, 128), pick(16, 48, 64, 128), pick(BF, F16)
+    steps = [[int(n) for n in torch.randint(0, pick(2, 9, 60), (B,), generator=r)] for _ in range(3)]
+    total = [sum(x) for x in zip(*steps)]
+    table, pages = block_table(total, page, extra=1, seed=seed)
+    cache = fa.KvCache4(*(t.cuda() for t in make_cache(pages, H, page, D, seed)), table.cuda())
+    held, want = [0] * B, [([], []) for _ in range(B)]
+    for new in steps:
+        if sum(new) == 0:
+            continue
+        kv = [torch.randn((sum(new), H, D), generator=r).to(dt) for _ in range(2)]
+        fa.kvcache4_append(cache, ints(held), kv[0].cuda(), kv[1].cuda(), cu_new=sums(new), max_new=max(new))
+        at = 0
+        for b, n in enumerate(new):
+            for i in range(2):
+                want[b][i].append(kv[i][at:at + n])
+            at += n
+        held = [a + n for a, n in zip(held, new)]
+    if sum(held) == 0:
+        return
+    got = fa.kvcache4_read(cache, ints(held), sums(held), sum(held), dt)
+    assert fa.device_status() == fa.FA_OK
+    for i in range(2):
+        x = torch.cat([t for b in range(B) for t in want[b][i]])
+        assert torch.equal(got[i].cpu(), values(*quantise(x)).float().to(dt))
 
 
 @pytest.mark.gpu

@@ -100,6 +100,28 @@ def test_turned(fa, cuda_device, c):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("seed", range(30))
+def test_any_sizes(fa, cuda_device, seed):
+    """Sizes, layouts and positions drawn at random."""
+    r = torch.Generator().manual_seed(300 + seed)
+    pick = lambda *x: x[int(torch.randint(0, len(x), (), generator=r))]   # noqa: E731
+    D = 8 * int(torch.randint(1, 33, (), generator=r))
+    R = pick(D, 2 * int(torch.randint(1, D // 2 + 1, (), generator=r)))
+    B, S, Hq, Hkv, dt = pick(1, 2, 7), pick(1, 3, 50, 900), pick(1, 2, 6, 20), pick(0, 1, 3), pick(BF, F16)
+    inter, kind = pick(True, False), pick("rows", "given", "offsets", "far")
+    q, k = (torch.randn((B, S, h, D), generator=r).to(dt) if h else None for h in (Hq, Hkv))
+    positions, offsets, pos = _positions(kind, B, S, r)
+    w, factor = fa.rope_frequencies(R, 500.0)
+    got = fa.rope(q.cuda(), None if k is None else k.cuda(), fa.rope_table(R, 500.0), positions=positions, offsets=offsets,
+                  interleaved=inter)
+    for x, y in ((q, got[0]), (k, got[1])):
+        if x is not None:
+            want, bound = plain(x, w, factor, pos, inter)
+            check(y, want, bound, "%r" % ((B, S, Hq, Hkv, D, R, inter, kind),))
+            assert torch.equal(y[..., R:].cpu(), x[..., R:])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("inter", [False, True])
 def test_gradient_against_differences(fa, cuda_device, inter):
     """<g, rope(x + h) - rope(x - h)> against <rope_bwd(g), 2 h>: rope is linear, so the
