@@ -316,17 +316,22 @@ class KvCache4(_PagedCache):
     def __init__(self, k, v, k_scale, v_scale, block_table):
         if k.dim() != 4 or block_table.dim() != 2:
             raise ValueError("k: [pages, Hkv, page, D / 2], block_table: [B, max_pages]")
-        P, H, ps, D = k.shape
-        D *= 2
         self.B = block_table.shape[0]
         self.device = k.get_device()   # index, -1: not on a GPU
-        if self.device < 0 or not _binding().cache4(k, v, k_scale, v_scale, block_table):
-            for name, t, dt, shape in (("k", k, torch.uint8, (P, H, ps, D // 2)),
-                                       ("v", v, torch.uint8, (P, H, ps, D // 2)),
-                                       ("k_scale", k_scale, torch.bfloat16, (P, H, ps, D // 64, 2)),
-                                       ("v_scale", v_scale, torch.bfloat16, (P, H, ps, D // 64, 2)),
-                                       ("block_table", block_table, torch.int32, block_table.shape)):
-                self._check(name, t, dt, shape)
+        raw = _binding().cache4(k, v, k_scale, v_scale, block_table) if self.device >= 0 else None
+        if raw is not None:
+            self._tensors = k, v, k_scale, v_scale, block_table
+            self._c = _KvCacheStruct.from_buffer_copy(raw)
+            self._at = ctypes.addressof(self._c)
+            return
+        P, H, ps, D = k.shape
+        D *= 2
+        for name, t, dt, shape in (("k", k, torch.uint8, (P, H, ps, D // 2)),
+                                   ("v", v, torch.uint8, (P, H, ps, D // 2)),
+                                   ("k_scale", k_scale, torch.bfloat16, (P, H, ps, D // 64, 2)),
+                                   ("v_scale", v_scale, torch.bfloat16, (P, H, ps, D // 64, 2)),
+                                   ("block_table", block_table, torch.int32, block_table.shape)):
+            self._check(name, t, dt, shape)
         self._hold(k, v, k_scale, v_scale, block_table, P, ps, H, D)
 
 

@@ -263,7 +263,7 @@ PyObject *cache(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// cache4(k, v, k_scale, v_scale, block_table) -> True if they make a 4-bit cache on the current device
+// cache4(k, v, k_scale, v_scale, block_table) -> the bytes of their fa_kv_cache4 if they make one on the current device
 PyObject *cache4(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (n != 5) return none();
     return guarded([&]() -> PyObject * {
@@ -279,7 +279,10 @@ PyObject *cache4(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (t[1]->sizes() != t[0]->sizes() || t[2]->sizes() != at::IntArrayRef({P, H, ps, D / 64, 2}) ||
             t[3]->sizes() != t[2]->sizes())
             return none();
-        Py_RETURN_TRUE;
+        if (P > 0x7fffffff || H > 0x7fffffff || ps > 0x7fffffff || D > 0x7fffffff || t[4]->size(1) > 0x7fffffff) return none();
+        const fa_kv_cache4 c = {t[0]->data_ptr(), t[1]->data_ptr(), t[2]->data_ptr(), t[3]->data_ptr(),
+                                (const int *)t[4]->data_ptr(), (int)P, (int)ps, (int)t[4]->size(1), (int)H, (int)D};
+        return PyBytes_FromStringAndSize(reinterpret_cast<const char *>(&c), sizeof(c));
     });
 }
 
