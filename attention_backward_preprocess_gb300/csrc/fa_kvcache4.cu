@@ -104,11 +104,13 @@ __device__ __forceinline__ void check_ragged(const Ragged &r) {
     }
 }
 
-// A thread's part of a CTA's rows: 16 dims of K or V of one head, the 16-byte pieces l
-// and l + 4 of a group of 64 dims for the group's l-th of four threads (so that these
-// read and write whole 64 bytes), of every step-th row: a row costs no division.  CTAs
-// go over the rows along x, over rows of more than kRagged parts along y.
-template <int D> struct Part {
+// A thread's part of a CTA's rows: 16 dims of K or V of one head, two 16-byte pieces of a
+// group of 64 dims, of every step-th row: a row costs no division.  The group's l-th of
+// four threads has pieces 2 l and 2 l + 1 (kNext 1: the codes are stored in whole sectors,
+// the pieces' second load meets the first one's) or l and l + 4 (kNext 4: the pieces are
+// stored in whole sectors).  CTAs go over the rows along x, over rows of more than kRagged
+// parts along y.
+template <int D, int kNext> struct Part {
     static constexpr int CH = D / 8, N = D / 16;   // pieces and parts of a head
     int row, step, side, at;     // first row, rows from one to the next; pieces of K's (or V's) row, and the first one's place
     bool is_v, live;
@@ -121,7 +123,7 @@ template <int D> struct Part {
         const int col = blockIdx.y * kRagged + tid - row * width;
         live = row < step && col < all;
         is_v = 2 * col >= all;
-        const int part = col - (is_v ? all / 2 : 0), head = part / N, in = part % N / 4 * 8 + part % 4;
+        const int part = col - (is_v ? all / 2 : 0), head = part / N, in = part % N / 4 * 8 + part % 4 * (kNext == 1 ? 2 : 1);
         at = head * CH + in;
         in_cache = (long long)head * c.page * CH + in;
     }
@@ -129,16 +131,22 @@ template <int D> struct Part {
 
 constexpr float kLeastScale = 0x1p-60f, kFifteenths = 8947849.f * 0x1p-26f;   // 2 / 15
 
-// The smaller of two pairs of 16-bit floats, NaN if either is.
-template <typename T> __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b);
-template <> __device__ __forceinline__ uint32_t min2_nan<__nv_bfloat16>(uint32_t a, uint32_t b) {
+// The smaller, the larger of two pairs of 16-bit floats, NaN if either is.
+template <typename T> __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    if constexpr (std::is_same_v<T, __half>) asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-template <> __device__ __forceinline__ uint32_t min2_nan<__half>(uint32_t a, uint32_t b) {
+template <typename T> __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    if constexpr (std::is_same_v<T, __half>) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t min_s16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.s16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
@@ -146,14 +154,16 @@ template <> __device__ __forceinline__ uint32_t min2_nan<__half>(uint32_t a, uin
 // A thread takes 16 dims of one new token; the four threads of a group of 64 share its
 // least and largest value by shuffles.  Every token is written by itself, so nothing of
 // the cache is read.  A thread's first loads (two tokens' parts) go out before the rows'
-// places are looked up.
+// places are looked up.  Prompts of 8256 tokens (8 heads of 128): 14.2 us, 43 MB.  Neither
+// instructions nor occupancy bound it: 4 to 8 operations a value, four to six CTAs an
+// SM and all of a thread's rows under way by asynchronous copies came out at 14.2 to 14.5.
 template <int D, typename T>
 __global__ void __launch_bounds__(kRagged) kv4_append_kernel(const __grid_constant__ KvAppendParams p, int per_cta) {
     __shared__ long long s_at[kMaxRows];
     constexpr int CH = D / 8, PER = 2;
     const Ragged ragged{p.c, p.cu, p.len, nullptr, p.B, p.rows, p.max_new};
     const int row0 = blockIdx.x * per_cta, rows = min(per_cta, p.rows - row0);
-    const Part<D> me(p.c);
+    const Part<D, 1> me(p.c);
     const uint4 *src = reinterpret_cast<const uint4 *>(me.is_v ? p.v : p.k) + (long long)row0 * me.side + me.at;
     uint32_t *const codes_at = reinterpret_cast<uint32_t *>(me.is_v ? p.c.v : p.c.k);
     uint32_t *const scales_at = reinterpret_cast<uint32_t *>(me.is_v ? p.c.v_scale : p.c.k_scale);
@@ -165,7 +175,7 @@ __global__ void __launch_bounds__(kRagged) kv4_append_kernel(const __grid_consta
             x[k][0] = x[k][1] = make_uint4(0u, 0u, 0u, 0u);
             if (me.live && r < rows) {
                 const uint4 *from = src + (long long)r * me.side;
-                x[k][0] = __ldcs(from), x[k][1] = __ldcs(from + 4);
+                x[k][0] = __ldcs(from), x[k][1] = __ldcs(from + 1);
             }
         }
     };
@@ -179,11 +189,12 @@ __global__ void __launch_bounds__(kRagged) kv4_append_kernel(const __grid_consta
             const int r = r0 + me.row + k * me.step;
             if (r0 + k * me.step >= rows) break;
             const uint32_t w[8] = {x[k][0].x, x[k][0].y, x[k][0].z, x[k][0].w, x[k][1].x, x[k][1].y, x[k][1].z, x[k][1].w};
-            // least values of the pairs' halves, and of the negated ones; then (least, -largest) of
-            // the group: NaN or infinite exactly where the group has such a value
-            uint32_t a = w[0], b = w[0] ^ 0x80008000u;
+            // least and largest values of the pairs' halves; then (least, -largest) of the group: NaN
+            // or infinite exactly where the group has such a value
+            uint32_t a = w[0], b = w[0];
 #pragma unroll
-            for (int j = 1; j < 8; ++j) a = min2_nan<T>(a, w[j]), b = min2_nan<T>(b, w[j] ^ 0x80008000u);
+            for (int j = 1; j < 8; ++j) a = min2_nan<T>(a, w[j]), b = max2_nan<T>(b, w[j]);
+            b ^= 0x80008000u;
             uint32_t ends = min2_nan<T>(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
 #pragma unroll
             for (int o = 1; o < 4; o <<= 1) ends = min2_nan<T>(ends, __shfl_xor_sync(0xffffffffu, ends, o));
@@ -194,26 +205,32 @@ __global__ void __launch_bounds__(kRagged) kv4_append_kernel(const __grid_consta
             const float far = fmaxf(__fsub_rn(hi, mid), __fsub_rn(mid, lo)) * kFifteenths;
             const float scale = fmaxf(__uint_as_float((__float_as_uint(far) + 0xffffu) & 0xffff0000u), kLeastScale);
             const float inv = __frcp_rn(scale);
-            // Distances are at most 7.5 scales and a hair, so only 8 needs clamping (its bound is whole, so
-            // it may come first).  Rounded to nearest even by adding 1.5 2^23, codes then put together by
-            // exact products and sums: conversions run at a quarter of the rate.
-            float c[16];
+            // Rounded to nearest even by adding 1.5 2^23 (and 8): the sum's low 16 bits are the code.
+            // Distances are at most 7.5 scales and a hair, so only 16 needs clamping.  (Conversions
+            // run at a quarter of the rate.  Single products: a packed one and the sum behind it came out
+            // rounded once.)
+            const uint64_t mid2 = f2_pack(-mid, -mid), whole2 = f2_pack(12582920.f, 12582920.f);
+            uint32_t c[8][2];   // of dims 2 i, + 1
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const float2 y = Cvt<T>::unpack(w[j >> 1]);
-                const float t = fminf(__fmul_rn(__fsub_rn(j & 1 ? y.y : y.x, mid), inv), 7.f);
-                c[j] = __fadd_rn(__fadd_rn(t, 12582912.f), -12582904.f);   // its code
+            for (int i = 0; i < 8; ++i) {
+                const float2 y = Cvt<T>::unpack(w[i]);
+                const float2 d = f2_unpack(f2_add(f2_pack(y.x, y.y), mid2));
+                const float2 t = f2_unpack(f2_add(f2_pack(__fmul_rn(d.x, inv), __fmul_rn(d.y, inv)), whole2));
+                c[i][0] = __float_as_uint(t.x), c[i][1] = __float_as_uint(t.y);
             }
-            uint32_t h[4];   // four codes each
+            uint32_t h[2];   // eight codes each
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                h[j] = __float_as_uint(fmaf(fmaf(c[4 * j + 3], 16.f, c[4 * j + 2]), 256.f, fmaf(c[4 * j + 1], 16.f, c[4 * j])) + 8388608.f);
+            for (int i = 0; i < 2; ++i) {
+                h[i] = 0u;
+#pragma unroll
+                for (int j = 3; j >= 0; --j)   // codes j and j + 4: 16 bits apart
+                    h[i] = h[i] * 16u + min_s16x2(__byte_perm(c[4 * i + j / 2][j & 1], c[4 * i + 2 + j / 2][j & 1], 0x5410), 0x000f000fu);
+            }
             if (!me.live || r >= rows) continue;
             const long long place = s_at[r];
             if (place >= 0) {
                 const long long at = place * CH + me.in_cache;
-                codes_at[at] = bad ? 0x88888888u : __byte_perm(h[0], h[1], 0x5410);
-                codes_at[at + 4] = bad ? 0x88888888u : __byte_perm(h[2], h[3], 0x5410);
+                *reinterpret_cast<uint2 *>(codes_at + at) = bad ? make_uint2(0x88888888u, 0x88888888u) : make_uint2(h[0], h[1]);
                 if ((me.at & 7) == 0)
                     scales_at[at >> 3] = bad ? 0x7fc00000u | __float_as_uint(kLeastScale) >> 16
                                              : __float_as_uint(scale) >> 16 | (__float_as_uint(mid) & 0xffff0000u);
@@ -235,7 +252,7 @@ __global__ void __launch_bounds__(kRagged) kv4_read_kernel(const __grid_constant
     constexpr int CH = D / 8, PER = 4;
     const Ragged ragged{p.c, p.cu, p.len, p.first, p.B, p.rows, -1};
     const int row0 = blockIdx.x * per_cta, rows = min(per_cta, p.rows - row0);
-    const Part<D> me(p.c);
+    const Part<D, 4> me(p.c);
     const uint32_t *const codes_at = reinterpret_cast<const uint32_t *>(me.is_v ? p.c.v : p.c.k);
     const uint32_t *const scales_at = reinterpret_cast<const uint32_t *>(me.is_v ? p.c.v_scale : p.c.k_scale);
     uint4 *const dst = reinterpret_cast<uint4 *>(me.is_v ? p.v : p.k) + (long long)row0 * me.side + me.at;
@@ -270,8 +287,8 @@ __global__ void __launch_bounds__(kRagged) kv4_read_kernel(const __grid_constant
                         const __half2 n = *reinterpret_cast<const __half2 *>(&v);
                         const float2 y = __half22float2(j & 1 ? __hfma2(n, __half2half2(__ushort_as_half(0x2c00)), __half2half2(__ushort_as_half(0xd480)))
                                                               : __hadd2(n, __half2half2(__ushort_as_half(0xe408))));
-                        f[j] = fmaf(scale, y.x, mid);
-                        f[j + 4] = fmaf(scale, y.y, mid);
+                        const float2 x = f2_unpack(f2_fma(f2_pack(scale, scale), f2_pack(y.x, y.y), f2_pack(mid, mid)));
+                        f[j] = x.x, f[j + 4] = x.y;
                     }
                     __stcs(to + 4 * i, make_uint4(Cvt<T>::pack(f[0], f[1]), Cvt<T>::pack(f[2], f[3]), Cvt<T>::pack(f[4], f[5]),
                                                   Cvt<T>::pack(f[6], f[7])));
