@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kRagged) kv4_read_kernel(const __grid_constant
 // are masked.
 //
 // Measured (64 requests of 256 to 8192 tokens, 32 / 8 heads of 128; two of 64 k capped),
-// the call with its join: 42.4 and 32.8 us, 3.95 TB/s and 3.28.  Of a worker's 74 k cycles
+// the call with its join: 41.0 and 32.8 us, 4.08 TB/s and 3.28.  Of a worker's 74 k cycles
 // the first 12 k pass before its first tile is there (lengths, table, copy: three
 // dependent reads; Q), 5 k at a segment's end; a tile takes 2.9 k, eight at a time on
 // an SM, which is 26 bytes per cycle where the memory gives 23.  What else was measured:
@@ -956,47 +956,70 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
 // pieces or two hundred.  Latency bounds it: three dependent reads.
 constexpr int kHelpers = 32;
 
+// Two float4s a thread: with one the call over 64 requests takes 43.0 us, with two 41.0,
+// with four 42.7 (two contexts of 64 k: 32.8, 32.8, 34.8).
 template <int D, int NR>
-__global__ void __launch_bounds__(2 * D) kv4_join_kernel(const __grid_constant__ KvAttnParams p) {
-    constexpr int N = 2 * D;   // threads, and float4s of eight rows of a piece
-    __shared__ float4 s_v[N], s_s[N];
+__global__ void __launch_bounds__(D) kv4_join_kernel(const __grid_constant__ KvAttnParams p) {
+    constexpr int V = 2, N = 2 * D / V;   // threads; float4s of eight rows of a piece: V times that
+    constexpr int kMost = N / 4 < kHelpers ? N / 4 : kHelpers;   // (a thread's float4s are of the same two rows)
+    __shared__ float4 s_v[V][N], s_s[N];
     const int tid = threadIdx.x, w = blockIdx.x;
     pdl_wait();
     const int4 meta = p.meta[w];   // segment, sequence, first and last worker
     const int first = meta.z, last = meta.w, others = last - first;
     if (meta.x < 0) return;
-    const int H = 1 << (31 - __clz(min(others, kHelpers))), h = w - first - 1;
+    const int H = 1 << (31 - __clz(min(others, kMost))), h = w - first - 1;
     if (h >= H) return;
-    const int F = N / H, set = tid / F, q = h * F + tid % F, dm = q / 32, lane = q % 32;
+    const int F = N / H, set = tid / F, q = h * F * V + tid % F;   // float4s q + v F
     const int hk = meta.x / p.groups, rg = meta.x - hk * p.groups;
 #pragma unroll 1
     for (int nr = 0; nr < NR; ++nr) {
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), t = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);   // t: m, l of the two rows
-        auto add = [&](float4 v, float4 s) __attribute__((always_inline)) {
+        float4 x[V], t = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);   // t: m, l of the two rows
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](const float4 (&y)[V], float4 s) __attribute__((always_inline)) {
             const float m0 = fmaxf(t.x, s.x), m1 = fmaxf(t.z, s.z);
             const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
             const float a0 = ex2(t.x - r0), a1 = ex2(t.z - r1), b0 = ex2(s.x - r0), b1 = ex2(s.z - r1);
             t = make_float4(m0, fmaf(s.y, b0, t.y * a0), m1, fmaf(s.w, b1, t.w * a1));
-            x = make_float4(fmaf(v.x, b0, x.x * a0), fmaf(v.y, b1, x.y * a1), fmaf(v.z, b0, x.z * a0), fmaf(v.w, b1, x.w * a1));
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                x[v] = make_float4(fmaf(y[v].x, b0, x[v].x * a0), fmaf(y[v].y, b1, x[v].y * a1), fmaf(y[v].z, b0, x[v].z * a0),
+                                   fmaf(y[v].w, b1, x[v].w * a1));
         };
 #pragma unroll 2
         for (int i = first + set; i <= last; i += H) {
             const long long at = ((long long)i * 2 + (i == first ? 1 : 0)) * NR + nr;
-            add(reinterpret_cast<const float4 *>(p.acc + at * (8 * D))[q],
-                reinterpret_cast<const float4 *>(p.stat)[at * 4 + (lane & 3)]);
+            float4 y[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) y[v] = reinterpret_cast<const float4 *>(p.acc + at * (8 * D))[q + v * F];
+            add(y, reinterpret_cast<const float4 *>(p.stat)[at * 4 + (q & 3)]);
         }
 #pragma unroll 1
         for (int o = H / 2; o > 0; o >>= 1) {
-            if (set >= o && set < 2 * o) s_v[tid] = x, s_s[tid] = t;
+            if (set >= o && set < 2 * o) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) s_v[v][tid] = x[v];
+                s_s[tid] = t;
+            }
             __syncthreads();
-            if (set < o) add(s_v[tid + o * F], s_s[tid + o * F]);
+            if (set < o) {
+                float4 y[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) y[v] = s_v[v][tid + o * F];
+                add(y, s_s[tid + o * F]);
+            }
         }
         if (set == 0) {
             const float f0 = t.y == 0.f ? 0.f : 1.f / t.y, f1 = t.w == 0.f ? 0.f : 1.f / t.w;
-            const float4 o = make_float4(x.x * f0, x.y * f1, x.z * f0, x.w * f1);
             const int row0 = (rg * NR + nr) * 8;
-            if (p.bf16) store_pairs<D, __nv_bfloat16>(p, meta.y, hk, row0, lane, o, dm);
-            else store_pairs<D, __half>(p, meta.y, hk, row0, lane, o, dm);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float4 o = make_float4(x[v].x * f0, x[v].y * f1, x[v].z * f0, x[v].w * f1);
+                const int at = q + v * F;
+                if (p.bf16) store_pairs<D, __nv_bfloat16>(p, meta.y, hk, row0, at % 32, o, at / 32);
+                else store_pairs<D, __half>(p, meta.y, hk, row0, at % 32, o, at / 32);
+            }
             if (p.lse && q < 4) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -1029,7 +1052,7 @@ cudaError_t launch_attn(KvAttnParams p, const CUtensorMap &mk, const CUtensorMap
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};   // set up while the attention runs
     cfg.gridDim = dim3((unsigned)p.workers);
-    cfg.blockDim = dim3(2 * D);
+    cfg.blockDim = dim3(D);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
