@@ -306,7 +306,8 @@ __global__ void __launch_bounds__(kRagged) kv4_read_kernel(const __grid_constant
 // it (D + D / 8 per key against 4 D flops per row and key); a key's codes take about as
 // many instructions to multiply as the memory takes cycles to bring them, so the design
 // spares instructions, and each worker has a ring of tiles (codes of K and V, their scales)
-// in shared memory, all but one under way.
+// in shared memory, all but one under way.  Four more warps look up the pages and start the
+// copies, two workers' each; the workers take over most of their registers.
 //
 // S^T.  A key's row of codes is D / 2 bytes; ldmatrix hands lane (r8, q4) the word
 // of dims 32 j + 8 q4 .. + 7 of key r8: masked, the operands (d0, d4), 16 (d1, d5),
@@ -332,22 +333,25 @@ __global__ void __launch_bounds__(kRagged) kv4_read_kernel(const __grid_constant
 // are masked.
 //
 // Measured (64 requests of 256 to 8192 tokens, 32 / 8 heads of 128; two of 64 k capped),
-// the call with its join: 41.0 and 32.8 us, 4.08 TB/s and 3.28.  Of a worker's 74 k cycles
-// the first 12 k pass before its first tile is there (lengths, table, copy: three
-// dependent reads; Q), 5 k at a segment's end; a tile takes 2.9 k, eight at a time on
-// an SM, which is 26 bytes per cycle where the memory gives 23.  What else was measured:
-//   scores by e4m3 products (Q in parts, three operations a word of codes where f16
-//   takes five): 57 us where f16 took 47;
-//   12 warps an SM (16 or 32 keys at a time fit 168 registers): 44.9 and 34.6; 10: 50.4 and
-//   37.4; 6: 54 and 39; three tiles a worker: as two; one: 50.9 and 39;
+// the call with its join: 41.0 and 31.0 us, 4.08 TB/s and 3.46; three rows of 8 / 2 heads of
+// 64 over 200 tokens 12.3.  What else was measured:
+//   each worker starting its own copies: 41.6, 32.8 and 14.3;
+//   and with that: scores by e4m3 products (Q in parts, three operations a word of codes
+//   where f16 takes five): 57 us where f16 took 47;
+//   12 workers an SM (16 or 32 keys at a time fit 168 registers): 44.9 and 34.6; 10: 50.4 and
+//   37.4; 6: 54 and 39; one tile a worker: 50.9 and 39;
 //   rows 4 .. 7 left idle where there are four (kSplit): 45.1 and 34.8.
+// Three tiles a worker: 43.3 and 31.9.
 constexpr uint32_t kLoMask = 0x000f000fu, kHiMask = 0x00f000f0u;
 
 constexpr int kKv4Smem = 232448 - 1024;   // of a CTA, what is not dynamic set aside
 
 template <int D, int NR>
 struct Kv4Cfg {
-    static constexpr int kWarps = 8;
+    static constexpr int kWarps = 8, kThreads = (kWarps + 4) * 32;   // workers; and the four warps that load
+    // Registers of a thread: as launched (what three warps a scheduler may have), a worker's, a loading warp's.
+    static constexpr int kRegs = 168, kWorkRegs = 224, kLoadRegs = 56;
+    static_assert(kWarps * kWorkRegs + 4 * kLoadRegs <= (kWarps + 4) * kRegs, "the launch's registers are shared out");
     static constexpr int kStep = NR == 1 ? 4 : 2;   // 16-key products at a time
     static constexpr int KB = kTile * D / 2;             // codes of a K (or V) tile
     static constexpr int SB = kTile * (D / 64) * 4;      // its scales
@@ -414,17 +418,148 @@ __device__ __forceinline__ void store_pairs(const KvAttnParams &p, int b, int hk
         }
 }
 
+// Does the phase of that parity lie behind?  (Without waiting.)
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+
+// Waits for a phase, within the budget and, if it heeds an abort, until there is one.
+// (Inline: no calls where warps have registers of their own number.)
+template <bool kHeeds>
+__device__ __forceinline__ bool kv4_wait(uint32_t bar, uint32_t parity, const WaitCtl &w) {
+    uint64_t since = 0;
+#pragma unroll 1
+    for (int i = 1; !mbar_try_wait(bar, parity); ++i) {
+        if (i & 31) continue;
+        if (kHeeds && *w.abort_flag) return false;
+        const uint64_t now = globaltimer_ns();
+        if (since == 0) since = now;
+        if ((long long)(now - since) > w.budget_ns) {
+            raise_error(w, kErrWaitTimeout);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool kv4_wait_warp(uint32_t bar, uint32_t parity, const WaitCtl &w) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    int ok = 1;
+    if ((threadIdx.x & 31) == 0) ok = kv4_wait<true>(bar, parity, w);
+    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// The warps that load the workers' tiles, two workers each: lane 16 j + 4 i + k copies part k
+// (K's codes, V's codes, K's scales, V's) of block i (bw tokens of one page) of worker 2 warp + j's.
+template <int D, int NR>
+__device__ __forceinline__ void kv4_loads(const KvAttnParams &p, const CUtensorMap &map_k, const CUtensorMap &map_v,
+                                          const int *s_pre, const int *s_len, int per_tile, int total, uint32_t tiles,
+                                          uint32_t full, uint32_t empty, uint32_t *s_ok, int warp, int lane, const WaitCtl &wctl) {
+    using C = Kv4Cfg<D, NR>;
+    constexpr int GR = D / 64;
+    static_assert(C::kWarps == 8, "two workers a loading warp");
+    const int half = lane & 16, worker = 2 * warp + (lane >> 4), blk = lane >> 2 & 3, part = lane & 3, ST = p.stages;
+    const bool leads = (lane & 15) == 0;
+    Cursor pc, end;   // what is loaded next, and where the worker stops
+    bool left;
+    {
+        const KvShare sh(p, blockIdx.x * C::kWarps + worker, total);
+        left = sh.wid < sh.N && total > 0;
+        Cursor c;   // even lanes place the one, odd lanes the other
+        c.b = c.hk = c.rg = c.t = 0;
+        if (left) kv_place<kKv4Open>(p, s_pre, s_len, per_tile, lane & 1 ? sh.w1 : sh.w0, c);
+        __syncwarp();
+        auto from = [&](int src, Cursor &d) {
+            d.b = __shfl_sync(0xffffffffu, c.b, src), d.hk = __shfl_sync(0xffffffffu, c.hk, src);
+            d.rg = __shfl_sync(0xffffffffu, c.rg, src), d.t = __shfl_sync(0xffffffffu, c.t, src);
+        };
+        from(half, pc);
+        from(half + 1, end);
+        const int t = pc.t;
+        if (left && pc.b < p.B) pc.open(p, s_len);
+        pc.t = t;
+    }
+    auto at_end = [&]() -> bool { return pc.b == end.b && pc.hk == end.hk && pc.rg == end.rg && pc.t == end.t; };
+    left = left && !at_end();
+    const int bw = p.v_block, page16 = p.c.page / 16;
+    auto page_of = [&](int x) -> int { return p.page_magic ? __umulhi((uint32_t)x, p.page_magic) : x; };
+    // The page of the lane's block of the tile at pc, -1 if no query sees it.
+    auto lookup = [&]() __attribute__((always_inline)) -> int {
+        const int x = 4 * pc.t + blk * (bw / 16);
+        if (blk * bw >= 64 || 16 * x >= pc.n || 16 * x + bw <= pc.lo) return -1;
+        const int page = __ldg(p.c.table + (long long)pc.b * p.c.max_pages + page_of(x));
+        if (page < 0 || page >= p.c.num_pages) {
+            atomicOr(p.c.err, kErrBadPage);
+            return -1;
+        }
+        return page;
+    };
+    // where the lane's copies land in a stage, and its part's scales
+    const uint32_t ring = tiles + worker * (ST * C::STAGE) + (part < 2 ? part * C::KB + blk * bw * (D / 2)
+                                                                       : 2 * C::KB + (part & 1) * C::SB + blk * bw * (4 * GR));
+    const uint32_t *const scales = reinterpret_cast<const uint32_t *>(part & 1 ? p.c.v_scale : p.c.k_scale);
+    full += worker * (8 * C::kStages), empty += worker * (8 * C::kStages), s_ok += worker * C::kStages;
+    int pg = left ? lookup() : -1, s = 0, loaded = 0, idle = 0;
+    uint32_t phase = 0;
+    uint64_t since = 0;
+    while (__any_sync(0xffffffffu, left)) {
+        bool go = left && leads && mbar_test(empty + 8 * s, phase ^ 1u);
+        go = __shfl_sync(0xffffffffu, go, half);
+        if (!__any_sync(0xffffffffu, go)) {
+            if ((++idle & 255) == 0) {   // (the workers' own waits are bounded: a second bound)
+                const uint64_t now = globaltimer_ns();
+                if (since == 0) since = now;
+                if ((long long)(now - since) > 2 * p.budget_ns) raise_error(wctl, kErrWaitTimeout);
+                __syncwarp();
+            }
+            if (__any_sync(0xffffffffu, *wctl.abort_flag != 0)) break;
+            __nanosleep(40);
+            continue;
+        }
+        idle = 0, since = 0;
+        const uint32_t b = __ballot_sync(0xffffffffu, pg >= 0 && part == 0) >> half;
+        if (go && leads) {
+            s_ok[s] = (b & 1u) | (b >> 3 & 2u) | (b >> 6 & 4u) | (b >> 9 & 8u);
+            mbar_arrive_expect_tx(full + 8 * s, (uint32_t)(__popc(b & 0xffffu) * bw) * (D + 8 * GR));
+        }
+        __syncwarp();
+        if (go) {
+            if (pg >= 0) {
+                const int x = 4 * pc.t + blk * (bw / 16);
+                const int row = (pg * p.c.Hkv + pc.hk) * p.c.page + 16 * (x - page_of(x) * page16);   // (below 2^31)
+                const uint32_t dst = ring + s * C::STAGE;
+                if (part < 2) tma_load_2d(dst, part ? &map_v : &map_k, full + 8 * s, 0, row);
+                else bulk_load(dst, scales + (long long)row * GR, bw * 4 * GR, full + 8 * s);
+            }
+            ++loaded;
+            if (++s == ST) s = 0, phase ^= 1u;
+            pc.next(p, s_len);
+            left = !at_end();
+            if (left) pg = lookup();
+        }
+        __syncwarp();
+    }
+    if (leads)   // the copies in flight land before the CTA's memory goes, whatever the workers do
+        for (int k = max(loaded - ST, 0); k < loaded; ++k)
+            kv4_wait<false>(full + 8 * (k % ST), k / ST & 1, wctl);
+}
+
 // kSplit: at most four rows (NR is 1).  Lanes q4 >= 2, whose rows 4 .. 7 there are not, take
 // the softmax of every second 16 keys off their neighbours q4 - 2.
 template <int D, int NR, typename T, bool kCap, bool kSplit>
-__global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
+__global__ void __launch_bounds__(Kv4Cfg<D, NR>::kThreads, 1)
     kv4_attn_kernel(const __grid_constant__ KvAttnParams p, const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v) {
     using C = Kv4Cfg<D, NR>;
     constexpr int W = C::kWarps, KS = C::kStep, J = D / 32, GR = D / 64, DM = D / 16;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    __shared__ int s_warp[W];
-    __shared__ __align__(8) uint64_t s_bar[W][C::kStages];   // a stage's tile landed
+    __shared__ int s_warp[W + 4];
+    __shared__ __align__(8) uint64_t s_full[W][C::kStages], s_empty[W][C::kStages];   // a stage's tile landed, was used
+    __shared__ uint32_t s_ok[W][C::kStages];   // its blocks that were read
     __shared__ int s_abort;
     const int ST = p.stages;
     const uint32_t tiles = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -439,7 +574,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
     // The block table and Q on their way from memory while the lengths are read: a line a
     // thread (what lies further comes when it is wanted).
     {
-        const long long line = (long long)(blockIdx.x * W * 32 + threadIdx.x) * 128;
+        const long long line = (long long)(blockIdx.x * C::kThreads + threadIdx.x) * 128;
         if (line < (long long)p.B * p.c.max_pages * 4)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(p.c.table) + line));
         if (line < (long long)p.B * p.Sq * p.Hq * D * 2)
@@ -447,18 +582,29 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
     }
     if (threadIdx.x == 32) prefetch_tmap(&map_k), prefetch_tmap(&map_v);
     if (threadIdx.x == 0) s_abort = 0;
-    if (lane == 0) p.meta[blockIdx.x * W + warp] = make_int4(-1, 0, 0, 0);
-    if (lane < ST) {
-        mbar_init(smem_u32(&s_bar[warp][lane]), 1);
-        fence_mbar_init();
+    if (warp < W) {
+        if (lane == 0) p.meta[blockIdx.x * W + warp] = make_int4(-1, 0, 0, 0);
+        if (lane < ST) {
+            mbar_init(smem_u32(&s_full[warp][lane]), 1);
+            mbar_init(smem_u32(&s_empty[warp][lane]), 1);
+            fence_mbar_init();
+        }
     }
     const int per_tile = p.c.Hkv * p.groups;
-    const int total = kv_count<W, D, kKv4Open>(p, s_pre, s_len, s_warp, warp, lane) * per_tile;   // (the host keeps it below 2^31)
-    const int wid = blockIdx.x * W + warp;
+    const int total = kv_count<W + 4, D, kKv4Open>(p, s_pre, s_len, s_warp, warp, lane) * per_tile;   // (the host keeps it below 2^31)
     pdl_launch();
+    const WaitCtl wctl{&s_abort, p.c.err, p.budget_ns};
+    if (warp >= W) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLoadRegs));
+        kv4_loads<D, NR>(p, map_k, map_v, s_pre, s_len, per_tile, total, tiles, smem_u32(&s_full[0][0]), smem_u32(&s_empty[0][0]),
+                         &s_ok[0][0], warp - W, lane, wctl);
+        return;
+    }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kWorkRegs));
+    const int wid = blockIdx.x * W + warp;
     const KvShare sh(p, wid, total);
     if (wid >= sh.N || total == 0) return;
-    Cursor pc, end;   // what is loaded next, and where the worker stops
+    Cursor cc, end;   // what is computed next, and where the worker stops
     {
         Cursor c;   // even lanes place the one, odd lanes the other
         kv_place<kKv4Open>(p, s_pre, s_len, per_tile, lane & 1 ? sh.w1 : sh.w0, c);
@@ -466,47 +612,24 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
             d.b = __shfl_sync(0xffffffffu, c.b, src), d.hk = __shfl_sync(0xffffffffu, c.hk, src);
             d.rg = __shfl_sync(0xffffffffu, c.rg, src), d.t = __shfl_sync(0xffffffffu, c.t, src);
         };
-        from(0, pc);
+        from(0, cc);
         from(1, end);
-        const int t = pc.t;
-        if (pc.b < p.B) pc.open(p, s_len);
-        pc.t = t;
+        const int t = cc.t;
+        if (cc.b < p.B) cc.open(p, s_len);
+        cc.t = t;
     }
     auto at_end = [&](const Cursor &c) -> bool {
         return c.b == end.b && c.hk == end.hk && c.rg == end.rg && c.t == end.t;
     };
-    if (at_end(pc)) return;
-    Cursor cc = pc;   // what is computed next
+    if (at_end(cc)) return;
 
-    const uint32_t ring = tiles + warp * (ST * C::STAGE), bars = smem_u32(&s_bar[warp][0]);
+    const uint32_t ring = tiles + warp * (ST * C::STAGE);
+    const uint32_t full = smem_u32(&s_full[warp][0]), empty = smem_u32(&s_empty[warp][0]);
     float2 *const stat = reinterpret_cast<float2 *>(p.stat);   // (m, l) of a piece's rows
-    const WaitCtl wctl{&s_abort, p.c.err, p.budget_ns};
-    const int bw = p.v_block, page16 = p.c.page / 16;
-    auto page_of = [&](int x) -> int { return p.page_magic ? __umulhi((uint32_t)x, p.page_magic) : x; };
-    // Lane 4 i + k copies block i (bw tokens of one page) of part k: K's codes, V's codes,
-    // K's scales, V's.  The page of its block of a tile, -1 if no query sees it.
-    const int blk = lane >> 2, part = lane & 3, blocks = 64 / bw;
-    auto lookup = [&](const Cursor &c) -> int {
-        const int x = 4 * c.t + blk * (bw / 16);
-        if (blk >= blocks || 16 * x >= c.n || 16 * x + bw <= c.lo) return -1;
-        const int page = __ldg(p.c.table + (long long)c.b * p.c.max_pages + page_of(x));
-        if (page < 0 || page >= p.c.num_pages) {
-            atomicOr(p.c.err, kErrBadPage);
-            return -1;
-        }
-        return page;
-    };
-    const uint32_t whole_tile = (1u << blocks) - 1u;
-    // where the lane's copies land in a stage, and its part's codes or scales
-    const uint32_t copy_at = part < 2 ? part * C::KB + blk * bw * (D / 2)
-                                      : 2 * C::KB + (part & 1) * C::SB + blk * bw * (4 * GR);
-    const uint32_t *const scales = reinterpret_cast<const uint32_t *>(part & 1 ? p.c.v_scale : p.c.k_scale);
-    bool loads = true;      // pc is a tile of this worker's
-    int pg = lookup(pc);
-    uint32_t read = 0u;     // four bits per stage: its blocks that are read
-    int under_way = 0, s_ld = 0;   // tiles loaded and not yet computed; the next one's stage
-    // Q's rows of a segment whose tiles are about to be loaded, on their way to this SM: lane
-    // (r8, q4) a quarter of row r8
+    const int bw = p.v_block;
+    const uint32_t whole_tile = (1u << (64 / bw)) - 1u;
+    // Q's rows of the segment that comes next, on their way to this SM: lane (r8, q4) a quarter
+    // of row r8
     auto prefetch_q = [&](const Cursor &c) {
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
@@ -518,30 +641,6 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
             }
         }
     };
-    auto load = [&]() __attribute__((always_inline)) {   // the tile at pc
-        const int s = s_ld;
-        const uint32_t b = __ballot_sync(0xffffffffu, pg >= 0 && part == 0);   // (also: every lane has read the stage)
-        const uint32_t bar = bars + 8 * s;
-        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(b) * bw) * (D + 8 * GR));
-        __syncwarp();
-        if (pg >= 0) {
-            const int x = 4 * pc.t + blk * (bw / 16);
-            const int row = (pg * p.c.Hkv + pc.hk) * p.c.page + 16 * (x - page_of(x) * page16);   // (below 2^31)
-            const uint32_t dst = ring + s * C::STAGE + copy_at;
-            if (part < 2) tma_load_2d(dst, part ? &map_v : &map_k, bar, 0, row);
-            else bulk_load(dst, scales + (long long)row * GR, bw * 4 * GR, bar);
-        }
-        read = (read & ~(15u << (4 * s))) | ((b & 1u) | (b >> 3 & 2u) | (b >> 6 & 4u) | (b >> 9 & 8u)) << (4 * s);
-        ++under_way;
-        if (++s_ld == ST) s_ld = 0;
-        const bool last = pc.t + 1 == pc.t1;
-        pc.next(p, s_len);
-        loads = !at_end(pc);
-        if (loads) pg = lookup(pc);
-        if (last && loads) prefetch_q(pc);
-    };
-    prefetch_q(pc);
-
     // ldmatrix: lane l gives the address of row l % 8 of matrix l / 8, matrices being the
     // 16-byte chunks of eight keys (D = 64: of sixteen).  Chunks lie as the tensor loads
     // swizzle them: chunk c of row r at c ^ (r / 2 % 4) (64-byte rows), c ^ (r / 4 % 2) (32).
@@ -574,10 +673,6 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
     int s_at = 0;
     uint32_t phase = 0;   // of stage s_at's barrier
     while (true) {
-        // (in one place, and so are the other parts that run seldom: a launch fetches them cold)
-        // A segment's Q is made ready behind one tile's loads, the other stages' come after.
-#pragma unroll 1
-        while (loads && under_way < (fresh ? 1 : ST)) load();
         if (fresh) {
             lo_all = 0, hi_all = 0x7fffffff;
 #pragma unroll
@@ -648,13 +743,15 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
             hi_all = __reduce_min_sync(0xffffffffu, hi_all);
             begins = cc.t == cc.t0;
             fresh = false;
-            continue;   // (to the loads)
         }
-        if (!mbar_wait_warp(bars + 8 * s_at, phase, wctl)) break;
+        Cursor nx = cc;
+        nx.next(p, s_len);
+        const bool done = at_end(nx), ends = cc.t + 1 == cc.t1;
+        if (ends && !done) prefetch_q(nx);
+        if (!kv4_wait_warp(full + 8 * s_at, phase, wctl)) return;   // (the copies in flight: the loading warp waits for them)
         const uint32_t kt = ring + s_at * C::STAGE, vt = kt + C::KB;
         const uint32_t ks_at = kt + 2 * C::KB + r8 * (4 * GR), vs_at = ks_at + C::SB;
-        const uint32_t ok = read >> (4 * s_at) & 15u;
-        const bool ends = cc.t + 1 == cc.t1;
+        const uint32_t ok = *reinterpret_cast<volatile uint32_t *>(&s_ok[warp][s_at]);
         // a tile inside every row's keys, all its pages read, takes no compare
         const bool edge = ok != whole_tile || kTile * cc.t < lo_all || kTile * cc.t + kTile - 1 > hi_all;
 #pragma unroll 1
@@ -870,11 +967,9 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
                     for (int g = 0; g < GR; ++g) mma_f16(eight[nr][g], kEight, P[nr][g][0], P[nr][g][1]);
             }
         }
-        --under_way;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + 8 * s_at);
         if (++s_at == ST) s_at = 0, phase ^= 1u;
-        Cursor nx = cc;
-        nx.next(p, s_len);
-        const bool done = at_end(nx);
         if (ends || done) {
             // the rows' results, or the piece's for the join
             const int hk = cc.hk, rg = cc.rg, seg = hk * p.groups + rg;
@@ -939,11 +1034,6 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kWarps * 32, 1)
         }
         if (done) return;
         cc = nx;
-    }
-    // a wait ran out: the copies in flight land before the CTA's memory goes
-    for (int i = 0; i < under_way; ++i) {
-        mbar_wait_drain_warp(bars + 8 * s_at, phase, p.c.err, p.budget_ns);
-        if (++s_at == ST) s_at = 0, phase ^= 1u;
     }
 }
 
@@ -1040,6 +1130,12 @@ cudaError_t launch_attn(KvAttnParams p, const CUtensorMap &mk, const CUtensorMap
     auto kern = kv4_attn_kernel<D, NR, T, kCap, kSplit>;
     p.stages = C::stages(p.B);
     const int smem = C::smem(p.stages, p.B);
+    // (a property of the code: workers would wait for registers that a smaller launch has not got)
+    static const bool fits = [&] {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, kern) == cudaSuccess && a.numRegs >= C::kRegs;
+    }();
+    if (!fits) return cudaErrorInvalidConfiguration;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int grid = sms < kKvSms ? sms : kKvSms;
@@ -1048,7 +1144,7 @@ cudaError_t launch_attn(KvAttnParams p, const CUtensorMap &mk, const CUtensorMap
     // x / (page / 16) as a product: exact for x below 2^29 and divisors up to 8
     const uint32_t d = (uint32_t)p.c.page / 16;
     p.page_magic = d > 1 ? (uint32_t)((1ull << 32) / d + 1) : 0u;
-    kern<<<grid, C::kWarps * 32, smem, stream>>>(p, mk, mv);
+    kern<<<grid, C::kThreads, smem, stream>>>(p, mk, mv);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};   // set up while the attention runs
     cfg.gridDim = dim3((unsigned)p.workers);
