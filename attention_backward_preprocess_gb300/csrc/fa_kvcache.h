@@ -58,8 +58,6 @@ struct KvAttnParams {
     int v_block, v_pad;
     long long budget_ns;         // bound of every device-side wait
     int bf16;                    // 4-bit cache: q's and o's type
-
-    int stages;                  // and the tiles a worker has in shared memory
 };
 
 // Workers of the attention kernel at most: kv_max_warps(D) warps of kKvSms CTAs.

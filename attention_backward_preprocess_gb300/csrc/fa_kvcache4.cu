@@ -356,12 +356,10 @@ struct Kv4Cfg {
     static constexpr int KB = kTile * D / 2;             // codes of a K (or V) tile
     static constexpr int SB = kTile * (D / 64) * 4;      // its scales
     static constexpr int STAGE = 2 * (KB + SB);
-    static constexpr int kStages = D == 64 ? 4 : 2;   // at most
-    // shared memory of a CTA with `stages`, for B sequences (1008: to a whole pattern)
-    static constexpr int smem(int stages, int B) { return 1008 + kWarps * stages * STAGE + 8 * B; }
-    // One stage less where the sequences' tables want the room.
-    static constexpr int stages(int B) { return smem(kStages, B) <= kKv4Smem ? kStages : kStages - 1; }
-    static_assert(smem(kStages - 1, kKvMaxSeqs) <= kKv4Smem, "shared memory overflow");
+    static constexpr int kStages = D == 64 ? 4 : 2;
+    // shared memory of a CTA for B sequences (1008: to a whole pattern)
+    static constexpr int smem(int B) { return 1008 + kWarps * kStages * STAGE + 8 * B; }
+    static_assert(smem(kKvMaxSeqs) <= kKv4Smem, "shared memory overflow");
     static_assert(kWarps <= kKv4MaxWarps, "the workspace holds that many workers per SM");
     static_assert(STAGE % 512 == 0 && KB % 512 == 0, "swizzled tiles start on whole patterns");
 };
@@ -460,9 +458,9 @@ __device__ __forceinline__ void kv4_loads(const KvAttnParams &p, const CUtensorM
                                           const int *s_pre, const int *s_len, int per_tile, int total, uint32_t tiles,
                                           uint32_t full, uint32_t empty, uint32_t *s_ok, int warp, int lane, const WaitCtl &wctl) {
     using C = Kv4Cfg<D, NR>;
-    constexpr int GR = D / 64;
+    constexpr int GR = D / 64, ST = C::kStages;
     static_assert(C::kWarps == 8, "two workers a loading warp");
-    const int half = lane & 16, worker = 2 * warp + (lane >> 4), blk = lane >> 2 & 3, part = lane & 3, ST = p.stages;
+    const int half = lane & 16, worker = 2 * warp + (lane >> 4), blk = lane >> 2 & 3, part = lane & 3;
     const bool leads = (lane & 15) == 0;
     Cursor pc, end;   // what is loaded next, and where the worker stops
     bool left;
@@ -555,13 +553,12 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kThreads, 1)
     kv4_attn_kernel(const __grid_constant__ KvAttnParams p, const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v) {
     using C = Kv4Cfg<D, NR>;
-    constexpr int W = C::kWarps, KS = C::kStep, J = D / 32, GR = D / 64, DM = D / 16;
+    constexpr int W = C::kWarps, KS = C::kStep, J = D / 32, GR = D / 64, DM = D / 16, ST = C::kStages;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     __shared__ int s_warp[W + 4];
     __shared__ __align__(8) uint64_t s_full[W][C::kStages], s_empty[W][C::kStages];   // a stage's tile landed, was used
     __shared__ uint32_t s_ok[W][C::kStages];   // its blocks that were read
     __shared__ int s_abort;
-    const int ST = p.stages;
     const uint32_t tiles = (smem_u32(smem_raw) + 1023u) & ~1023u;
     int *s_pre = reinterpret_cast<int *>(smem_raw + (tiles - smem_u32(smem_raw)) + W * ST * C::STAGE), *s_len = s_pre + p.B;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -1128,8 +1125,7 @@ template <int D, int NR, typename T, bool kCap, bool kSplit>
 cudaError_t launch_attn(KvAttnParams p, const CUtensorMap &mk, const CUtensorMap &mv, int sms, cudaStream_t stream) {
     using C = Kv4Cfg<D, NR>;
     auto kern = kv4_attn_kernel<D, NR, T, kCap, kSplit>;
-    p.stages = C::stages(p.B);
-    const int smem = C::smem(p.stages, p.B);
+    const int smem = C::smem(p.B);
     // (a property of the code: workers would wait for registers that a smaller launch has not got)
     static const bool fits = [&] {
         cudaFuncAttributes a;

@@ -277,7 +277,7 @@ ATTEND = [
     ([900, 5, 64], 2, 8, 1, 128, 128, F16, 25.0, 300),
     ([333, 112, 113], 1, 3, 1, 64, 112, BF, 0.0, -1),
     ([(7 * i) % 41 for i in range(700)], 1, 1, 1, 64, 16, F16, 0.0, -1),   # more sequences than threads
-    ([(5 * i) % 23 for i in range(1300)], 1, 1, 1, 128, 16, BF, 0.0, -1),  # so many that a stage of the ring makes room
+    ([(5 * i) % 23 for i in range(1300)], 1, 1, 1, 128, 16, BF, 0.0, -1),  # with tables in shared memory for all
     ([(5 * i) % 67 for i in range(3000)], 1, 2, 1, 64, 64, F16, 0.0, -1),  # more still
     ([400, 31, 9], 2, 4, 2, 128, 16, F16, 20.0, 70),        # four rows: capped, in a window, small pages
     ([400, 31, 9], 1, 4, 1, 64, 32, BF, 50.0, -1),
