@@ -7,6 +7,7 @@
 // f16 number are that number in units of 2^-24, so masking a word of eight codes
 // with 0x000f000f leaves two f16 operands c 2^-24, and with 0x00f000f0 two of 16 c
 // 2^-24.  What the units and the 16 do is undone on the other operand or the result.
+#include <atomic>
 #include <type_traits>
 
 #include "fa_device.cuh"
@@ -1126,14 +1127,16 @@ cudaError_t launch_attn(KvAttnParams p, const CUtensorMap &mk, const CUtensorMap
     using C = Kv4Cfg<D, NR>;
     auto kern = kv4_attn_kernel<D, NR, T, kCap, kSplit>;
     const int smem = C::smem(p.B);
-    // (a property of the code: workers would wait for registers that a smaller launch has not got)
-    static const bool fits = [&] {
+    // Registers of the code as built: workers would wait for those that a smaller launch has not got.
+    static std::atomic<int> regs{0};
+    cudaError_t e;
+    if (regs.load(std::memory_order_relaxed) == 0) {
         cudaFuncAttributes a;
-        return cudaFuncGetAttributes(&a, kern) == cudaSuccess && a.numRegs >= C::kRegs;
-    }();
-    if (!fits) return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+        if ((e = cudaFuncGetAttributes(&a, kern)) != cudaSuccess) return e;
+        regs.store(a.numRegs, std::memory_order_relaxed);
+    }
+    if (regs.load(std::memory_order_relaxed) < C::kRegs) return cudaErrorInvalidConfiguration;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
     const int grid = sms < kKvSms ? sms : kKvSms;
     p.workers = grid * C::kWarps;
     p.groups = (p.G * p.Sq + 8 * NR - 1) / (8 * NR);
