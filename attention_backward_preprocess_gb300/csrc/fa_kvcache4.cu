@@ -344,6 +344,9 @@ __global__ void __launch_bounds__(kRagged) kv4_read_kernel(const __grid_constant
 //   rows 4 .. 7 left idle where there are four (kSplit): 45.1 and 34.8.
 // Three tiles a worker: 43.3 and 31.9.
 constexpr uint32_t kLoMask = 0x000f000fu, kHiMask = 0x00f000f0u;
+// R is at most this far below m, so that 2^(m - R + 6) p stays in 32 bits where the top keys' V scales
+// are 0: what scales of 2^-100 reach, and the references' slack.  What P_g loses to it weighs below 2^-130.
+constexpr float kFarBelow = 108.f;
 
 constexpr int kKv4Smem = 232448 - 1024;   // of a CTA, what is not dynamic set aside
 
@@ -889,9 +892,11 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kThreads, 1)
 #pragma unroll
                         for (int g = 0; g < GR; ++g) zc[nr][g][e] *= shrink;
                         grow[e] = 1.f;
-                        if (y > R[nr][e] + kLazy || (R[nr][e] == -INFINITY && y > R[nr][e])) {
-                            grow[e] = ex2(R[nr][e] - y);
-                            R[nr][e] = y;
+                        float r = y > R[nr][e] + kLazy || R[nr][e] == -INFINITY ? y : R[nr][e];
+                        if (r > -INFINITY) r = fmaxf(r, mn - kFarBelow);
+                        if (r > R[nr][e]) {
+                            grow[e] = ex2(R[nr][e] - r);
+                            R[nr][e] = r;
                         }
                         fv[nr][e] = R[nr][e] == -INFINITY ? 0.f : ex2(mr[nr][e] - R[nr][e] + 6.f);
                     }
