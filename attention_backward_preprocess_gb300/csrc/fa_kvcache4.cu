@@ -1141,7 +1141,9 @@ cudaError_t launch_attn(KvAttnParams p, const CUtensorMap &mk, const CUtensorMap
         regs.store(a.numRegs, std::memory_order_relaxed);
     }
     if (regs.load(std::memory_order_relaxed) < C::kRegs) return cudaErrorInvalidConfiguration;
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    // (the limit is the kernel's, not the call's: the same for all of them, or a call of fewer sequences
+    // could lower it under another thread's launch)
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(kKvMaxSeqs))) != cudaSuccess) return e;
     const int grid = sms < kKvSms ? sms : kKvSms;
     p.workers = grid * C::kWarps;
     p.groups = (p.G * p.Sq + 8 * NR - 1) / (8 * NR);

@@ -49,3 +49,40 @@ def test_no_scale_under_the_top_score(fa, cuda_device, D, lens, high, cap):
         ro, rl, off, lse_off = plain_attention(q, *host, table, lens, 16, D ** -0.5, cap, -1)
         check(o, ro, off, "o")
         check_lse(lse, rl, lse_off)
+
+
+class _Call(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("cache", ctypes.c_void_p), ("len", ctypes.c_void_p), ("o", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("B", ctypes.c_int), ("Hq", ctypes.c_int), ("workspace", ctypes.c_void_p),
+                ("bytes", ctypes.c_size_t), ("stream", ctypes.c_void_p)]
+
+
+@pytest.mark.gpu
+def test_two_threads(fa, cuda_device, tmp_path):
+    """Calls of one and of 4000 sequences from two threads at a time, each on its stream with its workspace:
+    none is refused for what the other one needs."""
+    cxx, cuda = shutil.which("g++") or shutil.which("c++"), os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    if cxx is None:
+        pytest.skip("no C++ compiler")
+    so = str(tmp_path / "two_callers.so")
+    subprocess.run([cxx, "-O1", "-std=c++17", "-shared", "-fPIC", "-pthread", "-I", os.path.join(ROOT, "include"), "-I",
+                    os.path.join(cuda, "include"), os.path.join(ROOT, "tests", "two_callers.cpp"), "-o", so,
+                    "-L", os.path.join(cuda, "lib64"), "-lcudart"], check=True)
+    held, calls = [], (_Call * 2)()
+    for i, B in enumerate((1, 4000)):
+        lens = [20] + [0] * (B - 1)
+        table, pages = block_table(lens, 16)
+        cache = fa.KvCache4(*(t.cuda() for t in make_cache(pages, 1, 16, 64, 1)), table.cuda())
+        q = torch.ones((B, 1, 1, 64), dtype=BF, device="cuda")
+        n, stream = ints(lens), torch.cuda.Stream()
+        ws = torch.empty(fa.fa_fwd_kvcache4_workspace_bytes(64), dtype=torch.uint8, device="cuda")
+        o, lse = torch.empty_like(q), torch.empty((B, 1, 1), device="cuda")
+        held.append((cache, q, n, stream, ws, o, lse))
+        calls[i] = _Call(q.data_ptr(), ctypes.addressof(cache._c), n.data_ptr(), o.data_ptr(), lse.data_ptr(), B, 1,
+                         ws.data_ptr(), ws.numel(), stream.cuda_stream)
+    torch.cuda.synchronize()
+    entry = ctypes.cast(fa.lib().fa_fwd_kvcache4, ctypes.c_void_p)
+    failed = ctypes.CDLL(so).two_callers(entry, calls, torch.cuda.current_device(), 5000)
+    torch.cuda.synchronize()
+    assert failed == 0 and fa.device_status() == fa.FA_OK
+    assert torch.equal(held[0][5][0], held[1][5][0]) and not held[1][5][1:].any()
