@@ -695,7 +695,10 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kThreads, 1)
                 top = max(top >> 16, top & 0xffffu);
                 const float amax = Cvt<T>::unpack(top).x;
                 const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 126);
-                const float up = pow2(14 - e), down = pow2(e - 14) * 0x1p24f * (kCap ? p.cap_k : p.scale_log2);
+                // (down: the smaller products first, and held within the finite numbers above 0: a row of next to
+                // nothing scores 0, and a hidden key's -inf stays what it is)
+                const float up = pow2(14 - e), c = kCap ? p.cap_k : p.scale_log2;
+                const float down = fminf(fmaxf(e < 14 ? pow2(e - 14) * 0x1p24f * c : pow2(e - 14) * c * 0x1p24f, 0x1p-126f), 0x1.fffffep127f);
                 float sum[2] = {0.f, 0.f};
 #pragma unroll
                 for (int j = 0; j < J; ++j) q_operands<T>(raw[j], up, qb[nr][j], sum[j / 2]);

@@ -86,3 +86,25 @@ def test_two_threads(fa, cuda_device, tmp_path):
     torch.cuda.synchronize()
     assert failed == 0 and fa.device_status() == fa.FA_OK
     assert torch.equal(held[0][5][0], held[1][5][0]) and not held[1][5][1:].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+@pytest.mark.parametrize("Hq,D", [(2, 64), (8, 128), (16, 64)])
+def test_small_queries_and_softmax_scales(fa, cuda_device, Hq, D, cap):
+    """Rows of zeros and of next to nothing under softmax scales down to the least: the mean of the values
+    they see.  And large queries under scales that make up for them."""
+    c = ([100, 7, 16], 2, Hq, 1, D, 16, BF, cap, 40)
+    q, cache, n, plain = _attend(fa, c, 17)
+    q[:, :, 0] = 0.0
+    q[:, 1, 1] = (q[:, 1, 1].float() * 1e-37).to(BF)
+    for scale in (1e-20, 1e-38):
+        o, lse = fa.fa_fwd_kvcache4(q.cuda(), cache, n, softmax_scale=scale, softcap=cap, window_left=40)
+        ro, rl, off, lse_off = plain_attention(q, *plain, scale, cap, 40)
+        check(o, ro, off, "o")
+        check_lse(lse, rl, lse_off)
+    big = (q.float() * 2.0 ** 100).to(BF)
+    o, lse = fa.fa_fwd_kvcache4(big.cuda(), cache, n, softmax_scale=2.0 ** -103, softcap=cap, window_left=40)
+    ro, rl, off, lse_off = plain_attention(big, *plain, 2.0 ** -103, cap, 40)
+    check(o, ro, off, "o")
+    check_lse(lse, rl, lse_off)
