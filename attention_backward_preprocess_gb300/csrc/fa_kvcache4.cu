@@ -852,14 +852,16 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kThreads, 1)
             for (int nr = 0; nr < NR; ++nr) {
                 if (kCap) {
 #pragma unroll
-                    for (int u = 0; u < 2 * KU; ++u) {
-                        float *y = &x[nr][u >> 1][2 * (u & 1)], r0, r1;
-                        cap_r2(y[0] * fr[nr][0], y[1] * fr[nr][1], r0, r1);
-                        y[0] = fmaf(-2.f * p.cap_log2, r0, p.cap_log2);
-                        y[1] = fmaf(-2.f * p.cap_log2, r1, p.cap_log2);
-                        if (edge && (hidden >> ((nr * 2 * KU + u) * 2) & 1u)) y[0] = -INFINITY;
-                        if (edge && (hidden >> ((nr * 2 * KU + u) * 2) & 2u)) y[1] = -INFINITY;
-                    }
+                    for (int i = 0; i < KU; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {   // (a pair is of two keys, so that a NaN query stays in its row)
+                            float &a = x[nr][i][e], &b = x[nr][i][2 + e], ra, rb;
+                            cap_r2(a * fr[nr][e], b * fr[nr][e], ra, rb);
+                            a = fmaf(-2.f * p.cap_log2, ra, p.cap_log2);
+                            b = fmaf(-2.f * p.cap_log2, rb, p.cap_log2);
+                            if (edge && (hidden >> ((nr * KU + i) * 4 + e) & 1u)) a = -INFINITY;
+                            if (edge && (hidden >> ((nr * KU + i) * 4 + e) & 4u)) b = -INFINITY;
+                        }
                 }
                 // The references move only where a lane's largest score, or that plus its
                 // largest log2 scale, is 8 above them: mostly in a segment's first tile.

@@ -108,3 +108,20 @@ def test_small_queries_and_softmax_scales(fa, cuda_device, Hq, D, cap):
     ro, rl, off, lse_off = plain_attention(big, *plain, 2.0 ** -103, cap, 40)
     check(o, ro, off, "o")
     check_lse(lse, rl, lse_off)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+@pytest.mark.parametrize("Hq,Sq,D", [(4, 1, 128), (2, 1, 64), (8, 1, 128), (8, 3, 64)])
+def test_a_nan_query_stays_in_its_row(fa, cuda_device, Hq, Sq, D, cap):
+    c = ([300, 40], Sq, Hq, 1, D, 16, BF, cap, -1)
+    q, cache, n, _ = _attend(fa, c, 18)
+    want, want_lse = fa.fa_fwd_kvcache4(q.cuda(), cache, n, softcap=cap)
+    for bad in (math.nan, math.inf):
+        for i, h in ((0, 0), (Sq - 1, 1), (0, Hq - 1)):
+            y = q.clone()
+            y[0, i, h, 5] = bad
+            o, lse = fa.fa_fwd_kvcache4(y.cuda(), cache, n, softcap=cap)
+            assert torch.isnan(o[0, i, h]).all() and torch.isnan(lse[0, h, i])
+            o[0, i, h], lse[0, h, i] = want[0, i, h], want_lse[0, h, i]
+            assert torch.equal(o, want) and torch.equal(lse, want_lse)
