@@ -928,8 +928,9 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kThreads, 1)
 #pragma unroll
                     for (int g = 0; g < GR; ++g) {
                         const float mid = middle_of(vsm[u][g]), sc = scale_of(vsm[u][g]);
-                        zc[nr][g][0] = fmaf(pp.x, mid, zc[nr][g][0]);
-                        zc[nr][g][1] = fmaf(pp.y, mid, zc[nr][g][1]);
+                        // (a row that does not see the key: nothing, whatever the middle)
+                        zc[nr][g][0] = fmaf(pp.x, edge && y.x == -INFINITY ? 0.f : mid, zc[nr][g][0]);
+                        zc[nr][g][1] = fmaf(pp.y, edge && y.y == -INFINITY ? 0.f : mid, zc[nr][g][1]);
                         pt[nr][g][u] = transpose8(Cvt<__half>::pack(w.x * sc, w.y * sc));
                     }
                 }

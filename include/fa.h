@@ -433,8 +433,9 @@ fa_status fa_fwd_kvcache(const void *q, const fa_kv_cache *cache, const int *cac
  * so that a value is off by at most half a scale, but for what those roundings add.  A group with a
  * NaN or an infinity has the middle NaN, the scale 2^-60 and all codes 8: it reads as NaN.
  *
- * fa_fwd_kvcache4: arguments and results as fa_fwd_kvcache; queries of 2^110 and
- * above in size may give NaN.
+ * fa_fwd_kvcache4: arguments and results as fa_fwd_kvcache, but that a NaN or an
+ * infinity among a token's keys or values reaches no query that does not see the
+ * token; queries of 2^110 and above in size may give NaN.
  *
  * fa_kvcache4_read writes tokens of the cache out as 16-bit values, for the dense
  * attention of a prompt's next chunk (fa_fwd with cu_seqlens) or for another cache.

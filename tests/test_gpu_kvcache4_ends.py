@@ -125,3 +125,27 @@ def test_a_nan_query_stays_in_its_row(fa, cuda_device, Hq, Sq, D, cap):
             assert torch.isnan(o[0, i, h]).all() and torch.isnan(lse[0, h, i])
             o[0, i, h], lse[0, h, i] = want[0, i, h], want_lse[0, h, i]
             assert torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+@pytest.mark.parametrize("Sq,Hq,D", [(2, 2, 64), (3, 1, 128), (4, 2, 128), (5, 4, 128), (5, 4, 64)])
+def test_values_that_some_rows_do_not_see(fa, cuda_device, Sq, Hq, D, cap, bad):
+    """A V middle of NaN or infinity reaches the rows that see its token, in its 64 dims, and no other row: of the
+    last token (seen by the last query alone) and of the first in the first query's window."""
+    for lens in ([150, 41], [5000, 41]):
+        c = (lens, Sq, Hq, 1, D, 16, BF, cap, 30)
+        q, cache, n, plain = _attend(fa, c, 19)
+        want, want_lse = fa.fa_fwd_kvcache4(q.cuda(), cache, n, softcap=cap, window_left=30)
+        vs = cache.v_scale.clone()
+        for token, sees in ((lens[0] - 1, [Sq - 1]), (lens[0] - Sq - 30, [0])):
+            group = (D // 64 - 1)
+            cache.v_scale[int(plain[4][0, token // 16]), 0, token % 16, group, 1] = bad
+            o, lse = fa.fa_fwd_kvcache4(q.cuda(), cache, n, softcap=cap, window_left=30)
+            cache.v_scale.copy_(vs)
+            dims = slice(64 * group, 64 * group + 64)
+            for i in sees:
+                assert not torch.isfinite(o[0, i, :, dims]).any()
+                o[0, i, :, dims] = want[0, i, :, dims]
+            assert torch.equal(o, want) and torch.equal(lse, want_lse)
