@@ -132,6 +132,7 @@ template <int D, int kNext> struct Part {
 
 constexpr float kLeastScale = 0x1p-60f, kFifteenths = 8947849.f * 0x1p-26f;   // 2 / 15
 
+template <typename T> __device__ __forceinline__ constexpr float largest() { return std::is_same_v<T, __half> ? 65504.f : 0x1.fep127f; }
 // The smaller, the larger of two pairs of 16-bit floats, NaN if either is.
 template <typename T> __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -226,6 +227,12 @@ __global__ void __launch_bounds__(kRagged) kv4_append_kernel(const __grid_consta
 #pragma unroll
                 for (int j = 3; j >= 0; --j)   // codes j and j + 4: 16 bits apart
                     h[i] = h[i] * 16u + min_s16x2(__byte_perm(c[4 * i + j / 2][j & 1], c[4 * i + 2 + j / 2][j & 1], 0x5410), 0x000f000fu);
+            }
+            // The least value may be half a scale from codes 0 and 1 and rounded to 0; where the type has no such
+            // value, codes 0 become 1.
+            if (fmaf(-8.f, scale, mid) < -largest<T>()) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) h[i] |= ~(h[i] | h[i] >> 1 | h[i] >> 2 | h[i] >> 3) & 0x11111111u;
             }
             if (!me.live || r >= rows) continue;
             const long long place = s_at[r];

@@ -430,7 +430,9 @@ fa_status fa_fwd_kvcache(const void *q, const fa_kv_cache *cache, const int *cac
  *   middle = lo / 2 + hi / 2, rounded to bf16, for the least and largest x;
  *   scale  = max(hi - middle, middle - lo) * (2 / 15), rounded up to bf16, at least 2^-60;
  *   code   = clamp(nearest even whole number of (x - middle) * (1 / scale), -8, 7) + 8,
- * so that a value is off by at most half a scale, but for what those roundings add.  A group with a
+ * so that a value is off by at most half a scale, but for what those roundings add.  Where middle -
+ * 8 scale lies below the type's least finite value, the least code is 1, so that finite tokens stay
+ * finite (the rounding, half a scale from both, could have gone either way).  A group with a
  * NaN or an infinity has the middle NaN, the scale 2^-60 and all codes 8: it reads as NaN.
  *
  * fa_fwd_kvcache4: arguments and results as fa_fwd_kvcache, but that a NaN or an

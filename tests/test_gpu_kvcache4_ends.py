@@ -149,3 +149,46 @@ def test_values_that_some_rows_do_not_see(fa, cuda_device, Sq, Hq, D, cap, bad):
                 assert not torch.isfinite(o[0, i, :, dims]).any()
                 o[0, i, :, dims] = want[0, i, :, dims]
             assert torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
+def _near_the_largest(dt, D):
+    """Rows whose groups reach down to the type's largest value and end at steps that make the least value a tie."""
+    top, unit = (65280.0, 2.0 ** 7) if dt == F16 else (255 * 2.0 ** 120, 2.0 ** 120 / 2)
+    ends = [3840.0] if dt == F16 else [15 * 2.0 ** 120]
+    g = torch.Generator().manual_seed(5)
+    rows = []
+    for i in range(40):
+        hi = ends[0] if i < 2 else float(torch.randint(1, 400, (), generator=g)) * unit
+        lo = top if i < 2 else top - float(torch.randint(0, 40, (), generator=g)) * unit
+        x = -(torch.rand((D,), generator=g, dtype=torch.float64) * (lo - hi) + hi)
+        x[0::64], x[1::64] = -lo, -hi
+        rows.append((x if i != 1 else -x).to(dt))
+    return torch.stack(rows)[:, None]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF, F16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_next_to_the_largest_stay_finite(fa, cuda_device, D, dt):
+    """A group's least value is half a scale from codes 0 and 1 where rounding leaves it there; code 0 lies below it,
+    and must not be taken where the type has no such value."""
+    x = _near_the_largest(dt, D)
+    n, largest = x.shape[0], torch.finfo(dt).max
+    assert torch.isfinite(x).all()
+    table, pages = block_table([n], 16)
+    cache = fa.KvCache4(*(t.cuda() for t in make_cache(pages, 1, 16, D, 1)), table.cuda())
+    fa.kvcache4_append(cache, ints([0]), x.cuda(), x.cuda(), cu_new=sums([n]), max_new=n)
+    codes, scales = quantise(x)
+    c, s, m = unpack(codes, scales)
+    beyond = m - 8 * s < -largest
+    assert beyond[0].all() and int((beyond & (c == -8)).sum()) > 0
+    want = m + s * torch.where(beyond, c.clamp_min(-7), c)
+    assert ((want - x.double()).abs() <= s * (0.5 + 2.0 ** -19)).all()
+    for got in fa.kvcache4_read(cache, ints([n]), sums([n]), n, dt):
+        assert torch.isfinite(got).all()
+        assert torch.equal(got.cpu(), want.to(dt))   # (from 64 bits at once: the sums are exact in 32)
+    for i in (0, 1):   # a token by itself: its own values
+        one = fa.KvCache4(cache.k, cache.v, cache.k_scale, cache.v_scale, ints([[int(table[0, 0])]]))
+        o, _ = fa.fa_fwd_kvcache4(torch.zeros((1, 1, 1, D), dtype=dt, device="cuda"), one, ints([i + 1]),
+                                  window_left=0)
+        assert torch.isfinite(o).all()
