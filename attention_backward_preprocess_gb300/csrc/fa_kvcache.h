@@ -60,6 +60,12 @@ struct KvAttnParams {
     int bf16;                    // 4-bit cache: q's and o's type
 };
 
+// Has a wait taken more than twice its budget (up to the largest, whose double is out of range)?
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline bool twice_over(uint64_t waited, long long budget) { return waited / 2 > (uint64_t)budget; }
+
 // Workers of the attention kernel at most: kv_max_warps(D) warps of kKvSms CTAs.
 // The grid is the device's SM count (152 on GB300), held at kKvSms.
 constexpr int kKvSms = 160;

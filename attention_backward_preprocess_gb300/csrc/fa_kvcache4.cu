@@ -522,7 +522,7 @@ __device__ __forceinline__ void kv4_loads(const KvAttnParams &p, const CUtensorM
             if ((++idle & 255) == 0) {   // (the workers' own waits are bounded: a second bound)
                 const uint64_t now = globaltimer_ns();
                 if (since == 0) since = now;
-                if ((long long)(now - since) > 2 * p.budget_ns) raise_error(wctl, kErrWaitTimeout);
+                if (twice_over(now - since, p.budget_ns)) raise_error(wctl, kErrWaitTimeout);
                 __syncwarp();
             }
             if (__any_sync(0xffffffffu, *wctl.abort_flag != 0)) break;

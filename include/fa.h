@@ -566,8 +566,9 @@ fa_status fa_bwd_stages_ext(int stages, const void *q, const void *k, const void
  * read. */
 fa_status fa_device_status(void *workspace, cudaStream_t stream);
 
-/* Upper limit, in nanoseconds, of every device-side wait (default 2e9).
- * Returns the previous value; 0 leaves it unchanged. */
+/* Upper limit, in nanoseconds, of every device-side wait (default 2e9); the
+ * warps that load tiles for others in fa_fwd_kvcache4 wait up to twice that for
+ * them.  Returns the previous value; 0 leaves it unchanged. */
 long long fa_set_wait_timeout_ns(long long ns);
 
 const char *fa_status_string(fa_status s);
