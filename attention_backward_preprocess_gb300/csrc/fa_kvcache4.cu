@@ -459,7 +459,9 @@ __device__ __forceinline__ bool kv4_wait_warp(uint32_t bar, uint32_t parity, con
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     int ok = 1;
     if ((threadIdx.x & 31) == 0) ok = kv4_wait<true>(bar, parity, w);
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    __syncwarp();   // (what lane 0 has waited for is there for all lanes: a shuffle alone orders no memory)
+    return ok != 0;
 }
 
 // The warps that load the workers' tiles, two workers each: lane 16 j + 4 i + k copies part k
