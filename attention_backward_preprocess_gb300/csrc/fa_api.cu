@@ -981,6 +981,9 @@ fa_status fa_kvcache4_read(const fa_kv_cache4 *cache, const int *cache_len, cons
     for (const int *x : ints)
         if (reinterpret_cast<uintptr_t>(x) & 3u) return FA_ERR_INVALID_ARG;
     if (cache->Hkv > kKv4MaxHeads) return FA_ERR_UNSUPPORTED;
+    const uintptr_t k_at = reinterpret_cast<uintptr_t>(k_out), v_at = reinterpret_cast<uintptr_t>(v_out);
+    if ((k_at > v_at ? k_at - v_at : v_at - k_at) < 2 * (uintptr_t)rows * cache->Hkv * cache->D)
+        return FA_ERR_INVALID_ARG;   // k over v
     if ((st = check_device()) != FA_OK) return st;
     p.c.err = fa::fwd_error_word();
     if (!p.c.err) return FA_ERR_CUDA;
@@ -1065,6 +1068,22 @@ fa_status fa_rope_steps(const double *w, int n, unsigned long long *steps) {
     return FA_OK;
 }
 
+namespace {
+
+// Where a tensor of a call lies: bytes [at, end), end 0 for one whose strides leave gaps.
+struct Extent {
+    uintptr_t at, end;
+    bool meets(const Extent &o) const { return at == o.at || (end && o.end && at < o.end && o.at < end); }
+};
+Extent rope_extent(const fa::RopeParams &p, int i, bool out) {
+    const long long *st = out ? p.t[i].os : p.t[i].is;
+    const bool dense = st[2] == p.D && st[1] == (long long)p.heads[i] * p.D && (p.B == 1 || st[0] == p.S * st[1]);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(out ? p.t[i].out : p.t[i].in);
+    return {at, dense ? at + 2 * (uintptr_t)p.B * p.S * p.heads[i] * p.D : 0};
+}
+
+}  // namespace
+
 fa_status fa_rope(const fa_rope_tensor *q, const fa_rope_tensor *k, int B, int S, int D, int rotary_dim,
                   const unsigned long long *steps, float factor, int interleaved, int inverse, const int *positions,
                   const int *offsets, fa_dtype dtype, cudaStream_t stream) {
@@ -1078,6 +1097,9 @@ fa_status fa_rope(const fa_rope_tensor *q, const fa_rope_tensor *k, int B, int S
     if ((long long)B * S > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
     fa::RopeParams p;
     std::memset(&p, 0, sizeof(p));
+    p.B = B;
+    p.S = S;
+    p.D = D;
     p.in_place = 1;
     const fa_rope_tensor *both[] = {q, k};
     for (int i = 0; i < 2 && both[i]; ++i) {
@@ -1102,11 +1124,16 @@ fa_status fa_rope(const fa_rope_tensor *q, const fa_rope_tensor *k, int B, int S
         if (x.in != x.out) p.in_place = 0;
         else if (std::memcmp(t.is, t.os, sizeof(t.is)) != 0) return FA_ERR_INVALID_ARG;
     }
+    // What is written twice, or read by one thread and written by another, would be turned or not as it
+    // happens.  (Of tensors with strides, slices of one projection say, only equal starts tell.)
+    for (int i = 0; i < 2 && both[i]; ++i)
+        for (int j = 0; j < 2 && both[j]; ++j) {
+            const Extent out = rope_extent(p, i, true);
+            if (both[j]->in != both[i]->out && out.meets(rope_extent(p, j, false))) return FA_ERR_INVALID_ARG;
+            if (i != j && (both[j]->in == both[i]->out || out.meets(rope_extent(p, j, true)))) return FA_ERR_INVALID_ARG;
+        }
     fa_status st = check_device();
     if (st != FA_OK) return st;
-    p.B = B;
-    p.S = S;
-    p.D = D;
     p.R = rotary_dim;
     p.steps = steps;
     p.positions = positions;

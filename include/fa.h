@@ -445,7 +445,8 @@ fa_status fa_fwd_kvcache(const void *q, const fa_kv_cache *cache, const int *cac
  * Hkv, D] become sequence b's tokens first[b], first[b] + 1, .. (first: device int32
  * [B], NULL: 0).  Tokens must be held: a sequence with first[b] < 0 or more rows than
  * cache_len[b] - first[b] is left alone and reported, as are rows on a bad page.
- * Values are rounded to the output's type once from 32 bits.
+ * Values are rounded to the output's type once from 32 bits.  k_out and v_out must not
+ * overlap (FA_ERR_INVALID_ARG).
  *
  * Errors: as the 8-bit calls; fa_fwd_kvcache4 counts a cache's (page, head, token)
  * rows, which must stay below 2^31.
@@ -494,7 +495,9 @@ fa_status fa_fwd_kvcache4(const void *q, const fa_kv_cache4 *cache, const int *c
  * fa_rope works on q, and on k where it is not NULL, in one launch.  A tensor is
  * [B, S, heads, D] with D contiguous and (batch, row, head) strides in elements (all
  * three zero: contiguous; otherwise positive multiples of 8 below 2^39), 16-byte
- * aligned; out may be in with the same strides, and must not overlap it otherwise.
+ * aligned; out may be in with the same strides.  Otherwise what is written must overlap
+ * nothing else of the call, and no two of its elements each other: contiguous tensors that
+ * do, and any that start at the same place, are refused.
  * Packed rows are B = 1, S = rows.  The position of row s of sequence b is
  * positions[b S + s] (device int32), or offsets[b] + s (device int32 [B]), or s, with
  * both NULL; giving both is an error.  Positions may be negative.
