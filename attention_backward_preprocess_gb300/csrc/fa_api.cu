@@ -966,7 +966,7 @@ fa_status fa_kvcache4_append(const fa_kv_cache4 *cache, const int *cache_len, co
     if ((st = check_device()) != FA_OK) return st;
     p.c.err = fa::fwd_error_word();
     if (!p.c.err) return FA_ERR_CUDA;
-    return cuda_status(fa::launch_kv4_append(p, cache->D, dtype == FA_BF16, stream));
+    return cuda_status(fa::launch_kv4_append(p, cache->D, dtype == FA_BF16, sm_count(), stream));
 }
 
 fa_status fa_kvcache4_read(const fa_kv_cache4 *cache, const int *cache_len, const int *first, const int *cu_rows, int rows,
@@ -994,7 +994,7 @@ fa_status fa_kvcache4_read(const fa_kv_cache4 *cache, const int *cache_len, cons
     p.v = v_out;
     p.rows = rows;
     p.B = B;
-    return cuda_status(fa::launch_kv4_read(p, cache->D, dtype == FA_BF16, stream));
+    return cuda_status(fa::launch_kv4_read(p, cache->D, dtype == FA_BF16, sm_count(), stream));
 }
 
 size_t fa_fwd_kvcache4_workspace_bytes(int D) {

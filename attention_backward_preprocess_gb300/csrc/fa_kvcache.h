@@ -83,8 +83,8 @@ inline size_t kv4_workers() { return (size_t)kKvSms * kKv4MaxWarps; }
 cudaError_t launch_kv_append(const KvAppendParams &p, int D, int bf16, cudaStream_t stream);
 cudaError_t launch_kv_attn(const KvAttnParams &p, const CUtensorMap &map_v, int D, int bf16, int sms,
                            cudaStream_t stream);
-cudaError_t launch_kv4_append(const KvAppendParams &p, int D, int bf16, cudaStream_t stream);
-cudaError_t launch_kv4_read(const KvReadParams &p, int D, int bf16, cudaStream_t stream);
+cudaError_t launch_kv4_append(const KvAppendParams &p, int D, int bf16, int sms, cudaStream_t stream);
+cudaError_t launch_kv4_read(const KvReadParams &p, int D, int bf16, int sms, cudaStream_t stream);
 cudaError_t launch_kv4_attn(const KvAttnParams &p, const CUtensorMap &map_k, const CUtensorMap &map_v, int D, int sms,
                             cudaStream_t stream);
 

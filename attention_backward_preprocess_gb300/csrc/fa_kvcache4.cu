@@ -1192,39 +1192,39 @@ cudaError_t launch_attn_d(const KvAttnParams &p, const CUtensorMap &mk, const CU
 
 // CTAs of a ragged call: about `each` parts a thread, fewer rows where that would
 // leave SMs idle.
-template <int D> dim3 ragged_grid(int rows, int Hkv, int each, int *per_cta) {
-    const long long parts = 2LL * Hkv * (D / 16), n = each * kRagged / parts, most = rows / 608;
+template <int D> dim3 ragged_grid(int rows, int Hkv, int each, int sms, int *per_cta) {
+    const long long parts = 2LL * Hkv * (D / 16), n = each * kRagged / parts, most = rows / (4 * sms);
     const long long m = n < most ? n : most;
     *per_cta = (int)(m < 1 ? 1 : m > kMaxRows ? kMaxRows : m);
     return dim3((unsigned)(((long long)rows + *per_cta - 1) / *per_cta), (unsigned)((parts + kRagged - 1) / kRagged));
 }
 
 template <int D, typename T>
-cudaError_t launch_append_t(const KvAppendParams &p, cudaStream_t stream) {
+cudaError_t launch_append_t(const KvAppendParams &p, int sms, cudaStream_t stream) {
     int per;
-    const dim3 grid = ragged_grid<D>(p.rows, p.c.Hkv, 4, &per);
+    const dim3 grid = ragged_grid<D>(p.rows, p.c.Hkv, 4, sms, &per);
     kv4_append_kernel<D, T><<<grid, kRagged, 0, stream>>>(p, per);
     return cudaGetLastError();
 }
 template <int D, typename T>
-cudaError_t launch_read_t(const KvReadParams &p, cudaStream_t stream) {
+cudaError_t launch_read_t(const KvReadParams &p, int sms, cudaStream_t stream) {
     int per;
-    const dim3 grid = ragged_grid<D>(p.rows, p.c.Hkv, 4, &per);
+    const dim3 grid = ragged_grid<D>(p.rows, p.c.Hkv, 4, sms, &per);
     kv4_read_kernel<D, T><<<grid, kRagged, 0, stream>>>(p, per);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_kv4_append(const KvAppendParams &p, int D, int bf16, cudaStream_t stream) {
+cudaError_t launch_kv4_append(const KvAppendParams &p, int D, int bf16, int sms, cudaStream_t stream) {
     if (D == 128)
-        return bf16 ? launch_append_t<128, __nv_bfloat16>(p, stream) : launch_append_t<128, __half>(p, stream);
-    return bf16 ? launch_append_t<64, __nv_bfloat16>(p, stream) : launch_append_t<64, __half>(p, stream);
+        return bf16 ? launch_append_t<128, __nv_bfloat16>(p, sms, stream) : launch_append_t<128, __half>(p, sms, stream);
+    return bf16 ? launch_append_t<64, __nv_bfloat16>(p, sms, stream) : launch_append_t<64, __half>(p, sms, stream);
 }
 
-cudaError_t launch_kv4_read(const KvReadParams &p, int D, int bf16, cudaStream_t stream) {
-    if (D == 128) return bf16 ? launch_read_t<128, __nv_bfloat16>(p, stream) : launch_read_t<128, __half>(p, stream);
-    return bf16 ? launch_read_t<64, __nv_bfloat16>(p, stream) : launch_read_t<64, __half>(p, stream);
+cudaError_t launch_kv4_read(const KvReadParams &p, int D, int bf16, int sms, cudaStream_t stream) {
+    if (D == 128) return bf16 ? launch_read_t<128, __nv_bfloat16>(p, sms, stream) : launch_read_t<128, __half>(p, sms, stream);
+    return bf16 ? launch_read_t<64, __nv_bfloat16>(p, sms, stream) : launch_read_t<64, __half>(p, sms, stream);
 }
 
 cudaError_t launch_kv4_attn(const KvAttnParams &p, const CUtensorMap &mk, const CUtensorMap &mv, int D, int sms,
