@@ -440,7 +440,10 @@ _SCALINGS = {"linear": 1, "ntk": 2, "yarn": 3}
 def rope_frequencies(rotary_dim, base=10000.0, scaling=None):
     """(radians per position of every pair, a float64 CPU tensor; factor).
     ``scaling``: None, ("linear", scale), ("ntk", scale) or ("yarn", scale,
-    trained_len[, beta_fast, beta_slow]); see fa_rope_frequencies in include/fa.h."""
+    trained_len[, beta_fast, beta_slow]); see fa_rope_frequencies in include/fa.h.
+    YaRN's ramp is its paper's, linear in a pair's turns over ``trained_len``.  For
+    a model that was stretched with another one (linear between two pairs' numbers,
+    as some are), make the frequencies that way and hand them to RopeTable.of."""
     kind, args = 0, ()
     if scaling is not None:
         if scaling[0] not in _SCALINGS:

@@ -156,7 +156,7 @@ __device__ __forceinline__ uint32_t min_s16x2(uint32_t a, uint32_t b) {
 // A thread takes 16 dims of one new token; the four threads of a group of 64 share its
 // least and largest value by shuffles.  Every token is written by itself, so nothing of
 // the cache is read.  A thread's first loads (two tokens' parts) go out before the rows'
-// places are looked up.  Prompts of 8256 tokens (8 heads of 128): 14.2 us, 43 MB.  Neither
+// places are looked up.  Prompts of 8256 tokens (8 heads of 128): 14.3 us, 43 MB.  Neither
 // instructions nor occupancy bound it: 4 to 8 operations a value, four to six CTAs an
 // SM and all of a thread's rows under way by asynchronous copies came out at 14.2 to 14.5.
 template <int D, typename T>
@@ -341,8 +341,10 @@ __global__ void __launch_bounds__(kRagged) kv4_read_kernel(const __grid_constant
 // are masked.
 //
 // Measured (64 requests of 256 to 8192 tokens, 32 / 8 heads of 128; two of 64 k capped),
-// the call with its join: 41.0 and 31.0 us, 4.08 TB/s and 3.46; three rows of 8 / 2 heads of
-// 64 over 200 tokens 12.3.  What else was measured:
+// the call with its join: 41.2 and 31.1 us, 4.07 TB/s and 3.45; three rows of 8 / 2 heads of
+// 64 over 200 tokens 12.3.  By events around the call, which add 9 us, over 140 k tokens in 64
+// requests: 32, 64 and 128 heads on 8 (4, 8, 16 rows) 50.2, 50.2 and 66.8 us (capped 50.2, 52.2, 75.8).
+// What else was measured (against 41.0, 31.0 and 12.3):
 //   each worker starting its own copies: 41.6, 32.8 and 14.3;
 //   and with that: scores by e4m3 products (Q in parts, three operations a word of codes
 //   where f16 takes five): 57 us where f16 took 47;

@@ -2,10 +2,12 @@
 // that goes with the row's position, forward and (the other way round) backward.
 //
 // a' = f (a cos - b sin), b' = f (b cos + a sin), in 32 bits and rounded once.  Each
-// element is read and written once, so bytes bound it.  The angles: p w / (2 pi)
+// element is read and written once, so bytes bound it where it moves in 16-byte pieces;
+// single pairs (kScalar) are bound by their instructions, one per two bytes, and by reads
+// that wait for each other.  The angles: p w / (2 pi)
 // turns, as a 64-bit fixed-point product whose overflow drops the whole turns, so
 // that no position is too far for its angle; its upper 32 bits, as a signed part of
-// half a turn, go to sincospif.  A CTA works out the cosines and sines of its few
+// half a turn (24 bits of them, in f32), go to sincospif.  A CTA works out the cosines and sines of its few
 // rows once, in shared memory, while its first loads are under way; all heads of
 // q and k use them.
 #include "fa_device.cuh"
@@ -37,10 +39,14 @@ template <typename T> __device__ __forceinline__ void turn_pair(uint32_t &a, flo
 }
 
 // A thread keeps its piece u of a head and goes from head to head (and row to row) of
-// the CTA: a piece then costs no division and its cosines' place is known.  2 x 8192
+// the CTA: a piece then costs no division (but for sequences that do not follow each other
+// as rows do, where each address has one: 57.3 us where evenly spaced ones take 56.4, by
+// events around the call) and its cosines' place is known.  2 x 8192
 // rows of 40 heads of 128: 52.5 us (6.39 TB/s, 94 % of a copy's rate) at five CTAs an SM, 53
 // at six (registers in memory), 57.4 at seven; 55.4 with twice the rows a CTA, 55.3 with the
-// cosines in the pairs' order, 57.4 with two divisions a piece besides.
+// cosines in the pairs' order, 57.4 with two divisions a piece besides.  By events around a call,
+// which add 5 us: whole heads in halves 57.3, interleaved 70.3; half of a head turned, 67.6 and
+// 69.6; kScalar, 24 of 96 dims 235 us (1.07 TB/s), 20 of 80 dims 215 (0.98; interleaved 47.1).
 template <typename T, RopeKind kKind>
 __global__ void __launch_bounds__(kThreads, 5) rope_kernel(const __grid_constant__ RopeParams p) {
     __shared__ __align__(16) float2 s_cs[kMaxRows][kMaxPairs];   // factor (cos, sin)

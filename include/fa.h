@@ -377,7 +377,8 @@ fa_status fa_bwd_ext(const void *q, const void *k, const void *v, const void *o,
  * none gives O = 0, LSE = -inf.  softcap as in fa_ext.  Pages wholly before
  * every query's window are not read.  Bytes of tokens that no query of the
  * sequence sees may hold anything; a NaN among the values of a token that some
- * of its queries see may reach all of them.  workspace:
+ * of its queries see may reach all of them, and under a cap a NaN query its
+ * neighbour's row (of the rows of a kv head, 2 i and 2 i + 1).  workspace:
  * fa_fwd_kvcache_workspace_bytes(D) bytes, 256-byte aligned, no
  * initialisation; calls that overlap need one each.  Results do not depend on
  * anything but the arguments and the GPU (no atomics).
@@ -437,7 +438,8 @@ fa_status fa_fwd_kvcache(const void *q, const fa_kv_cache *cache, const int *cac
  *
  * fa_fwd_kvcache4: arguments and results as fa_fwd_kvcache, but that a NaN or an
  * infinity among a token's keys or values reaches no query that does not see the
- * token; queries of 2^110 and above in size may give NaN.
+ * token; queries of 2^110 and above in size may give NaN, and
+ * values of that size infinities (their weighted sums are 32-bit).
  *
  * fa_kvcache4_read writes tokens of the cache out as 16-bit values, for the dense
  * attention of a prompt's next chunk (fa_fwd with cu_seqlens) or for another cache.
@@ -483,12 +485,15 @@ fa_status fa_fwd_kvcache4(const void *q, const fa_kv_cache4 *cache, const int *c
  *
  * Frequencies.  steps (device, rotary_dim / 2 of them) are w_i / (2 pi), parts of a
  * turn per position, in 2^-64ths: p steps[i] modulo 2^64 is the angle, to 2^-32 of a
- * turn however far the position.  fa_rope_steps makes them on the host from radians
+ * turn however far the position; the cosine and sine are taken of its 24 leading bits
+ * (2^-26 of a turn).  fa_rope_steps makes them on the host from radians
  * per position (finite, 0 <= w < 1024).  fa_rope_frequencies makes those: base^(-2i /
  * rotary_dim), scaled for contexts of `scale` times the trained length by
  *   FA_ROPE_LINEAR  w / scale (position interpolation);
  *   FA_ROPE_NTK     base scale^(rotary_dim / (rotary_dim - 2)) for base;
- *   FA_ROPE_YARN    (YaRN, Peng et al. 2023) w (1 - g) / scale + w g with g = (r - beta_slow) /
+ *   FA_ROPE_YARN    (YaRN, Peng et al. 2023, the ramp as its paper has it: over turns.  Other
+ *                   ramps, over the pairs' numbers say, come in as w to fa_rope_steps)
+ *                   w (1 - g) / scale + w g with g = (r - beta_slow) /
  *                   (beta_fast - beta_slow) held in [0, 1], r = trained_len w / (2 pi);
  *                   *factor = 0.1 ln(scale) + 1 (1 for the others).
  *
