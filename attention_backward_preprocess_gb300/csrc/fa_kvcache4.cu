@@ -711,11 +711,15 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kThreads, 1)
                 const float up = pow2(14 - e), c = kCap ? p.cap_k : p.scale_log2;
                 const float down = fminf(fmaxf(e < 14 ? pow2(e - 14) * 0x1p24f * c : pow2(e - 14) * c * 0x1p24f, 0x1p-126f), 0x1.fffffep127f);
                 float sum[2] = {0.f, 0.f};
+                // A NaN or infinite query goes on as zeros (a NaN would get past the -inf of keys that it does not
+                // see); its row sum is NaN where it sees a key.
+                const bool fine = amax < INFINITY;
 #pragma unroll
-                for (int j = 0; j < J; ++j) q_operands<T>(raw[j], up, qb[nr][j], sum[j / 2]);
-                // a NaN or infinite query: what is left of it is NaN, for its own row only
-                const float dn = amax < INFINITY ? down : NAN;
+                for (int j = 0; j < J; ++j)
+                    q_operands<T>(fine ? raw[j] : make_uint4(0u, 0u, 0u, 0u), fine ? up : 1.f, qb[nr][j], sum[j / 2]);
+                const float dn = fine ? down : 1.f;
                 const int hi = cc.n - p.Sq + i;
+                const float l0 = fine || hi < 0 ? 0.f : NAN;
 #pragma unroll
                 for (int g2 = 0; g2 < GR; ++g2) {
                     sum[g2] += __shfl_xor_sync(0xffffffffu, sum[g2], 1);
@@ -742,7 +746,8 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kThreads, 1)
                     lo_all = max(lo_all, lo_r[nr][e2]);
                     hi_all = min(hi_all, hi_r[nr][e2]);
                     m[nr][e2] = R[nr][e2] = -INFINITY;
-                    mr[nr][e2] = fv[nr][e2] = l_run[nr][e2] = 0.f;
+                    mr[nr][e2] = fv[nr][e2] = 0.f;
+                    l_run[nr][e2] = __shfl_sync(0xffffffffu, l0, src_lane);
 #pragma unroll
                     for (int g2 = 0; g2 < GR; ++g2) zc[nr][g2][e2] = 0.f;
                 }
@@ -865,7 +870,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NR>::kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < KU; ++i)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {   // (a pair is of two keys, so that a NaN query stays in its row)
+                        for (int e = 0; e < 2; ++e) {   // (a pair is of two keys: a row's scores are its own affair)
                             float &a = x[nr][i][e], &b = x[nr][i][2 + e], ra, rb;
                             cap_r2(a * fr[nr][e], b * fr[nr][e], ra, rb);
                             a = fmaf(-2.f * p.cap_log2, ra, p.cap_log2);

@@ -128,6 +128,19 @@ def test_a_nan_query_stays_in_its_row(fa, cuda_device, Hq, Sq, D, cap):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_a_nan_query_that_sees_nothing(fa, cuda_device, cap):
+    """More queries than tokens: the first ones see no key, whatever they are."""
+    c = ([2, 100], 4, 2, 1, 64, 16, BF, cap, -1)
+    q, cache, n, _ = _attend(fa, c, 20)
+    want, want_lse = fa.fa_fwd_kvcache4(q.cuda(), cache, n, softcap=cap)
+    q[0, 1, 0, 7] = math.nan
+    o, lse = fa.fa_fwd_kvcache4(q.cuda(), cache, n, softcap=cap)
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    assert not o[0, :2].any() and torch.isneginf(lse[0, :, :2]).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
 @pytest.mark.parametrize("cap", [0.0, 30.0])
 @pytest.mark.parametrize("Sq,Hq,D", [(2, 2, 64), (3, 1, 128), (4, 2, 128), (5, 4, 128), (5, 4, 64)])
